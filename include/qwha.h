@@ -27,7 +27,8 @@
  *     the library reads them on `stream` and never frees or keeps them.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream). Every call
  *     only enqueues work on it and returns without synchronising, except
- *     qwha_validate_plan and qwha_check_stream_status, which synchronise it.
+ *     qwha_validate_plan, qwha_validate_slots and qwha_check_stream_status,
+ *     which synchronise it.
  *   - Device buffers must be 16-byte aligned (QWHA_ERR_MISALIGNED otherwise).
  *   - The caller owns all memory. Calls that need scratch take `ws` (device,
  *     256-byte aligned) and `ws_bytes`; qwha_workspace_size gives the need.
@@ -143,7 +144,9 @@ typedef enum {
   QWHA_OP_SELECT_GLOBAL = 6, /* qwha_init_select_global */
   QWHA_OP_REFINE = 7,        /* qwha_refine_values */
   QWHA_OP_ENERGY = 8,        /* qwha_energy_stats */
-  QWHA_OP_PATTERN = 9        /* qwha_pattern_stats */
+  QWHA_OP_PATTERN = 9,       /* qwha_pattern_stats */
+  QWHA_OP_DECODE = 10,       /* qwha_adapter_decode */
+  QWHA_OP_SLOTS = 11         /* qwha_validate_slots; p = slots of the cache, other sizes 1 */
 } qwha_op;
 
 /* Z = X H row by row: x and z are [rows, n] of dtype dt (device), each row
@@ -186,6 +189,97 @@ qwha_status qwha_adapter_fwd(const qwha_adapter *a, const qwha_qweight *wq, qwha
 qwha_status qwha_adapter_bwd(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtype dt,
                              const void *dY, const void *Z, int64_t T, float alpha, float *dc,
                              void *dX, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------- serving
+ * The layer on the few tokens of a decode step, and the cache its keys and
+ * values go to. There is no counterpart on the pages (they train the adapter
+ * and merge nothing); the formulas are the layer's own. */
+
+/* Most tokens of a qwha_qgemv or qwha_adapter_decode call. Above it the
+ * weight is better dequantized once for the GEMM (qwha_adapter_fwd). */
+#define QWHA_DECODE_MAX_T 64
+
+/* Y = X W_Q^T for 0 <= T <= QWHA_DECODE_MAX_T tokens, straight from the packed
+ * codes: X [T, d_in], Y [T, d_out] of dtype dt (fp32 or bf16). Unlike the base
+ * GEMM, which rounds W_Q to bf16, the products of q - zeros (an exact integer)
+ * and X are summed in fp32 per group and scaled in fp32; Y is rounded once.
+ * d_out >= 1; d_in a multiple of wq->group (a multiple of 8). Deterministic.
+ * QWHA_ERR_UNSUPPORTED above QWHA_DECODE_MAX_T. */
+qwha_status qwha_qgemv(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha_dtype dt, const void *X,
+                       int64_t T, void *Y, void *stream);
+
+/* Forward of the adapted layer on 0 <= T <= QWHA_DECODE_MAX_T tokens:
+ *   Y = X W_Q^T + alpha Z F^T,  Z = X H,
+ * with the weight read packed as in qwha_qgemv and Z kept in fp32 (dt fp32 or
+ * bf16; wq == NULL computes the adapter alone). a->row_ptr/col_idx/coef are
+ * read; a->algo, a->weff and the backward's views are not; a->z_given must be
+ * 0 (QWHA_ERR_UNSUPPORTED). Z_out [T, d_in] of dtype dt, if not NULL, receives
+ * Z for qwha_adapter_bwd, which is the backward of these tokens too. ws:
+ * qwha_workspace_size(QWHA_OP_DECODE, d_out, d_in, p, T, 0) bytes (Z in fp32;
+ * 0 when p = 0). Columns of E outside [0, d_in) are skipped. Deterministic. */
+qwha_status qwha_adapter_decode(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtype dt, const void *X,
+                                int64_t T, float alpha, void *Z_out, void *Y, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/* A paged cache of quantized rows: the keys (or values) of one attention
+ * layer. Slot = page * page_size + offset holds one token, each of its `heads`
+ * rows head_dim codes in the format of qwha_qweight:
+ *   codes  u8   [n_pages, page_size, heads, head_dim * bits / 8]
+ *   scales fp32 [n_pages, page_size, heads, head_dim / group]
+ *   zeros  u8   [n_pages, page_size, heads, head_dim / group]
+ * bits in {2, 3, 4, 8}; head_dim a multiple of 8 up to 256; group a multiple
+ * of 8 dividing head_dim. had_block: 0, or a power of two dividing head_dim:
+ * rows are rotated by the block-diagonal orthonormal H before they are
+ * quantized and rotated back when read, which spreads the few large channels
+ * of keys over a block. The caller owns the memory and the page numbers. */
+typedef struct {
+  int32_t bits, group, had_block, heads, head_dim, page_size;
+  int64_t n_pages;
+  uint8_t *codes;
+  float *scales;
+  uint8_t *zeros;
+} qwha_cache;
+
+/* Quantize rows[c] [n, heads, head_dim] (device, dtype dt) into the slots
+ * slots[i] (device int64 [n]) of caches[c], c < n_caches (1 or 2: keys and
+ * values in one launch). caches and rows are host arrays. slots[i] = -1 skips
+ * row i (padding); slots outside [-1, n_pages * page_size) are skipped and
+ * reported by qwha_check_stream_status (QWHA_ERR_INVALID_ARG). The slots of a
+ * call must be distinct apart from -1: of rows sent to one slot it is not
+ * defined which codes and which scales stay (qwha_validate_slots checks).
+ * Slots not named keep their contents.
+ * Per group of the rotated row v (bf16 rows: fp32 arithmetic; fp32 rows: fp64;
+ * butterflies 1, 2, 4, ..., then times 1/sqrt(had_block)), with qmax =
+ * 2^bits - 1 and half = 0.5 + 2^-12:
+ *   lo = min(0, min v), hi = max(0, max v), s = fp32((hi - lo) * (1 / qmax)),
+ *   s below 2^-126 counts as 1; inv = 1 / s;
+ *   z = min(floor(-lo * inv + half), qmax);
+ *   q = clamp(floor(v * inv + (z + half)), 0, qmax),
+ * and s (q - z) is what the row reads as. A group whose s is not finite (it
+ * holds an infinity or a NaN, or overflows) reads back as NaN. */
+qwha_status qwha_cache_write(const qwha_cache *caches, int32_t n_caches, qwha_dtype dt, const void *const *rows,
+                             const int64_t *slots, int64_t n, void *stream);
+
+/* Read sequences back as dense rows of dtype dt: row i of rows[c] [n, heads,
+ * head_dim], row_start[b] <= i < row_start[b + 1], is token first[b] + i -
+ * row_start[b] of sequence b (first NULL: 0). row_start int64 [n_seqs + 1]
+ * (non-decreasing from 0) and first int64 [n_seqs] are device arrays; token t
+ * of sequence b lies in page pages[b * max_pages + t / page_size] (device
+ * int32 [n_seqs, max_pages]) at offset t % page_size. Rows from
+ * row_start[n_seqs] on are left as they were, and so are rows whose page is
+ * outside [0, n_pages) or whose token lies outside the page table; those are
+ * reported by qwha_check_stream_status (QWHA_ERR_INVALID_ARG). fp32
+ * arithmetic, one rounding to dt. */
+qwha_status qwha_cache_read(const qwha_cache *caches, int32_t n_caches, qwha_dtype dt, const int32_t *pages,
+                            int32_t max_pages, const int64_t *row_start, const int64_t *first, int32_t n_seqs,
+                            void *const *rows, int64_t n, void *stream);
+
+/* Check on the device that slots [n] are -1 or within the cache and distinct.
+ * Synchronises the stream. QWHA_ERR_INVALID_ARG names the first failure in
+ * qwha_last_error(). ws: qwha_workspace_size(QWHA_OP_SLOTS, 1, 1, n_pages *
+ * page_size, 0, 0) bytes. */
+qwha_status qwha_validate_slots(const qwha_cache *cache, const int64_t *slots, int64_t n, void *ws,
+                                size_t ws_bytes, void *stream);
 
 /* AdaAlloc initialisation from the quantization error dW_Q = W0 - W_Q
  * (papernotes.org 关键设计 2 and 3; gist.science 2.2). dWq fp32 [d_out, d_in]
@@ -374,7 +468,8 @@ size_t qwha_workspace_size(qwha_op op, int32_t d_out, int32_t d_in, int64_t p, i
 qwha_status qwha_validate_plan(const qwha_adapter *a, void *stream);
 
 /* Synchronise `stream` and report a device-side error word set by a bounded
- * wait (QWHA_ERR_TIMEOUT) or a CUDA error (QWHA_ERR_CUDA); clears the word. */
+ * wait (QWHA_ERR_TIMEOUT) or by a slot or page outside its cache
+ * (QWHA_ERR_INVALID_ARG), or a CUDA error (QWHA_ERR_CUDA); clears the word. */
 qwha_status qwha_check_stream_status(void *stream);
 
 /* Tracing aid: per-stage device time of the library's own kernels. While

@@ -7,10 +7,16 @@ of include/qwha.h. Import fails if the library is not built.
 
 from ._lib import QwhaError, lib  # noqa: F401
 from .api import (  # noqa: F401
+    DECODE_MAX_T,
     Adapter,
+    QCache,
     QWeight,
     adapter_bwd,
+    adapter_decode,
     adapter_fwd,
+    cache_alloc,
+    cache_read,
+    cache_write,
     calib_hessian,
     dp_backward,
     dp_step,
@@ -25,11 +31,13 @@ from .api import (  # noqa: F401
     pattern_stats,
     plan_build,
     plan_tiles,
+    qgemv,
     refine_values,
     shard_rows,
     stage_report,
     stage_timing,
     validate_plan,
+    validate_slots,
     workspace_size,
 )
 

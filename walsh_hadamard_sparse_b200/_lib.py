@@ -41,6 +41,11 @@ class QwhaQweight(ctypes.Structure):
     _fields_ = [("bits", i32), ("group", i32), ("qweight", P), ("scales", P), ("zeros", P)]
 
 
+class QwhaCache(ctypes.Structure):
+    _fields_ = [("bits", i32), ("group", i32), ("had_block", i32), ("heads", i32), ("head_dim", i32),
+                ("page_size", i32), ("n_pages", i64), ("codes", P), ("scales", P), ("zeros", P)]
+
+
 _SIGNATURES = {
     "qwha_fwht": (ctypes.c_int, [ctypes.c_int, P, P, i64, i32, i32, P]),
     "qwha_adapter_fwd": (
@@ -51,6 +56,15 @@ _SIGNATURES = {
         ctypes.c_int,
         [ctypes.POINTER(QwhaAdapter), ctypes.POINTER(QwhaQweight), ctypes.c_int, P, P, i64, f32, P, P, P, sz, P],
     ),
+    "qwha_qgemv": (ctypes.c_int, [ctypes.POINTER(QwhaQweight), i32, i32, ctypes.c_int, P, i64, P, P]),
+    "qwha_adapter_decode": (
+        ctypes.c_int,
+        [ctypes.POINTER(QwhaAdapter), ctypes.POINTER(QwhaQweight), ctypes.c_int, P, i64, f32, P, P, P, sz, P],
+    ),
+    "qwha_cache_write": (ctypes.c_int, [ctypes.POINTER(QwhaCache), i32, ctypes.c_int, ctypes.POINTER(P), P, i64, P]),
+    "qwha_cache_read": (ctypes.c_int, [ctypes.POINTER(QwhaCache), i32, ctypes.c_int, P, i32, P, P, i32,
+                                       ctypes.POINTER(P), i64, P]),
+    "qwha_validate_slots": (ctypes.c_int, [ctypes.POINTER(QwhaCache), P, i64, P, sz, P]),
     "qwha_coef_grad_noalloc": (ctypes.c_int, [ctypes.POINTER(QwhaAdapter), ctypes.c_int, P, P, i64, f32, P, P]),
     "qwha_init_alloc": (ctypes.c_int, [P, i32, i32, i32, i64, i32, ctypes.c_int, P, P, P, P, P, sz, P]),
     "qwha_init_norms": (ctypes.c_int, [P, i32, i32, P, P]),

@@ -12,11 +12,12 @@ from dataclasses import dataclass, fields
 
 import torch
 
-from ._lib import QwhaAdapter, QwhaQweight, check, lib
+from ._lib import P, QwhaAdapter, QwhaCache, QwhaQweight, check, lib
 
 F32, BF16 = 0, 1
 OP_FWD, OP_BWD, OP_INIT, OP_PLAN, OP_FWD_DENSE, OP_BWD_DENSE, OP_SELECT_GLOBAL, OP_REFINE = 0, 1, 2, 3, 4, 5, 6, 7
-OP_ENERGY, OP_PATTERN = 8, 9
+OP_ENERGY, OP_PATTERN, OP_DECODE, OP_SLOTS = 8, 9, 10, 11
+DECODE_MAX_T = 64  # most tokens of a qgemv or adapter_decode call
 PATTERN_STATS = ("empty_rows", "empty_cols", "min_row", "max_row", "min_col", "max_col", "rank_bound", "half_rows")
 SELECTION = {"magnitude": 0, "random": 1}
 ALGO = {"sparse": 0, "dense": 1}
@@ -158,6 +159,191 @@ def adapter_bwd(a: Adapter, dY: torch.Tensor, Z: torch.Tensor, alpha: float = 1.
                                 _ptr(dX) if want_dx else None, _ptr(ws), 0 if ws is None else ws.numel(), _stream())
     check(rc, "qwha_adapter_bwd")
     return (dc if want_dc else None), (dX if want_dx else None)
+
+
+def _same_device(*tensors) -> None:
+    """Work goes to the current device's current stream: every tensor of the call has to live there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _check_weight(wq: QWeight, d_out: int, d_in: int) -> None:
+    groups = d_in // wq.group if wq.group > 0 else 0
+    for name, t, dtype, shape in (("qweight", wq.qweight, torch.uint8, (d_out, d_in * wq.bits // 8)),
+                                  ("scales", wq.scales, torch.float32, (d_out, groups)),
+                                  ("zeros", wq.zeros, torch.uint8, (d_out, groups))):
+        if t.dtype != dtype or tuple(t.shape) != shape:
+            raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _check_out(name: str, t: torch.Tensor, like: torch.Tensor, shape: tuple) -> None:
+    if t.dtype != like.dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {like.dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def qgemv(wq: QWeight, X: torch.Tensor, Y: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = X W_Q^T for up to DECODE_MAX_T tokens X [T, d_in] (fp32 or bf16), straight from the packed weight; products
+    of the exact q - zeros, fp32 sums, one rounding."""
+    T, d_in = X.shape
+    d_out = wq.scales.shape[0]
+    _check_weight(wq, d_out, d_in)
+    if Y is None:
+        Y = torch.empty((T, d_out), dtype=X.dtype, device=X.device)
+    else:
+        _check_out("Y", Y, X, (T, d_out))
+    _same_device(X, Y, wq.qweight, wq.scales, wq.zeros)
+    cw = wq.c_struct()
+    check(lib().qwha_qgemv(ctypes.byref(cw), d_out, d_in, _dt(X), _ptr(X), T, _ptr(Y), _stream()), "qwha_qgemv")
+    return Y
+
+
+def adapter_decode(a: Adapter, X: torch.Tensor, alpha: float = 1.0, wq: QWeight | None = None,
+                   Z_out: torch.Tensor | None = None, Y: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = X W_Q^T + alpha (X H) F^T for up to DECODE_MAX_T tokens X [T, d_in] (fp32 or bf16; W_Q term only with wq):
+    the forward of a decode step, straight from the packed weight. Only the CSR arrays of `a` are read. Z_out, if
+    given, receives X H in X's dtype for adapter_bwd."""
+    T, d_in = X.shape
+    if d_in != a.d_in:
+        raise ValueError(f"X has {d_in} columns, the adapter {a.d_in}")
+    if Y is None:
+        Y = torch.empty((T, a.d_out), dtype=X.dtype, device=X.device)
+    else:
+        _check_out("Y", Y, X, (T, a.d_out))
+    if Z_out is not None:
+        _check_out("Z_out", Z_out, X, (T, d_in))
+    _same_device(X, Y, Z_out, ws, a.row_ptr, a.col_idx, a.coef)
+    cw = None
+    if wq is not None:
+        _check_weight(wq, a.d_out, d_in)
+        _same_device(wq.qweight, wq.scales, wq.zeros)
+        cw = wq.c_struct()
+    if ws is None:
+        ws = _ws(workspace_size(OP_DECODE, a.d_out, a.d_in, a.p, T, False), X.device)
+    cs = a.c_struct()
+    rc = lib().qwha_adapter_decode(ctypes.byref(cs), ctypes.byref(cw) if cw is not None else None, _dt(X), _ptr(X), T,
+                                   float(alpha), _ptr(Z_out), _ptr(Y), _ptr(ws), 0 if ws is None else ws.numel(),
+                                   _stream())
+    check(rc, "qwha_adapter_decode")
+    return Y
+
+
+@dataclass
+class QCache:
+    """A paged cache of quantized rows (the keys or the values of one attention layer), in the format of QWeight:
+    codes u8 [n_pages, page_size, heads, head_dim*bits/8], scales f32 and zeros u8 [n_pages, page_size, heads,
+    head_dim/group]. had_block: rows are rotated by H (blocks of had_block) before they are quantized; 0: they are
+    not."""
+
+    bits: int
+    group: int
+    had_block: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+    zeros: torch.Tensor
+
+    @property
+    def heads(self) -> int:
+        return self.scales.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return self.scales.shape[3] * self.group
+
+    @property
+    def n_slots(self) -> int:
+        return self.scales.shape[0] * self.scales.shape[1]
+
+    def c_struct(self) -> QwhaCache:
+        if self.scales.dim() != 4:
+            raise ValueError(f"scales: expected 4 dimensions, got {tuple(self.scales.shape)}")
+        n_pages, page_size, heads, groups = self.scales.shape
+        head_dim = groups * self.group
+        for name, t, dtype, width in (("codes", self.codes, torch.uint8, head_dim * self.bits // 8),
+                                      ("scales", self.scales, torch.float32, groups),
+                                      ("zeros", self.zeros, torch.uint8, groups)):
+            if t.dtype != dtype or tuple(t.shape) != (n_pages, page_size, heads, width):
+                raise ValueError(f"{name}: expected {dtype} {(n_pages, page_size, heads, width)}, got {t.dtype} "
+                                 f"{tuple(t.shape)}")
+        return QwhaCache(self.bits, self.group, self.had_block, heads, head_dim, page_size, n_pages,
+                         _ptr(self.codes), _ptr(self.scales), _ptr(self.zeros))
+
+
+def cache_alloc(n_pages: int, page_size: int, heads: int, head_dim: int, bits: int = 4, group: int | None = None,
+                had_block: int = 0, device="cuda") -> QCache:
+    """An empty cache (every slot reads as zero); group defaults to the whole head."""
+    group = group or head_dim
+    rows = (n_pages, page_size, heads)
+    return QCache(bits, group, had_block,
+                  torch.zeros(rows + (head_dim * bits // 8,), dtype=torch.uint8, device=device),
+                  torch.ones(rows + (head_dim // group,), dtype=torch.float32, device=device),
+                  torch.zeros(rows + (head_dim // group,), dtype=torch.uint8, device=device))
+
+
+def _caches(caches) -> tuple:
+    return (caches,) if isinstance(caches, QCache) else tuple(caches)
+
+
+def cache_write(caches, rows, slots: torch.Tensor) -> None:
+    """Quantize rows [n, heads, head_dim] (fp32 or bf16) into the slots [n] (int64, distinct; -1 skips a row) of a
+    cache; with a pair of caches and a pair of rows (keys and values) both in one launch."""
+    cs = _caches(caches)
+    rs = (rows,) if isinstance(rows, torch.Tensor) else tuple(rows)
+    n = slots.shape[0]
+    if len(cs) != len(rs) or not 1 <= len(cs) <= 2:
+        raise ValueError(f"{len(cs)} caches and {len(rs)} row tensors: one or two of each")
+    if slots.dtype != torch.int64 or slots.dim() != 1:
+        raise ValueError("slots: expected an int64 vector")
+    for c, r in zip(cs, rs):
+        _check_out("rows", r, rs[0], (n, c.heads, c.head_dim))
+        _same_device(r, slots, c.codes, c.scales, c.zeros)
+    rc = lib().qwha_cache_write((QwhaCache * len(cs))(*(c.c_struct() for c in cs)), len(cs), _dt(rs[0]),
+                                (P * len(rs))(*(_ptr(r) for r in rs)), _ptr(slots), n, _stream())
+    check(rc, "qwha_cache_write")
+
+
+def cache_read(caches, pages: torch.Tensor, row_start: torch.Tensor, n: int, first: torch.Tensor | None = None,
+               dtype: torch.dtype = torch.bfloat16, out=None):
+    """Sequences of a cache as dense rows [n, heads, head_dim] (a pair of caches: a pair of tensors, in one launch).
+    Rows row_start[b] .. row_start[b+1] (int64 [n_seqs+1]) are the tokens first[b], first[b]+1, ... (int64 [n_seqs];
+    None: 0) of sequence b, whose token t lies in page pages[b, t // page_size] (int32 [n_seqs, max_pages]). Rows from
+    row_start[-1] on are left as they were (they are not initialised without `out`)."""
+    cs = _caches(caches)
+    if not 1 <= len(cs) <= 2:
+        raise ValueError(f"{len(cs)} caches: one or two")
+    n_seqs, max_pages = pages.shape
+    for name, t, want, shape in (("pages", pages, torch.int32, (n_seqs, max_pages)),
+                                 ("row_start", row_start, torch.int64, (n_seqs + 1,)),
+                                 ("first", first, torch.int64, (n_seqs,))):
+        if t is not None and (t.dtype != want or tuple(t.shape) != shape):
+            raise ValueError(f"{name}: expected {want} {shape}, got {t.dtype} {tuple(t.shape)}")
+    if out is None:
+        outs = tuple(torch.empty((n, c.heads, c.head_dim), dtype=dtype, device=pages.device) for c in cs)
+    else:
+        outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(outs) != len(cs):
+            raise ValueError(f"{len(cs)} caches and {len(outs)} outputs")
+    for c, o in zip(cs, outs):
+        _check_out("out", o, outs[0], (n, c.heads, c.head_dim))
+        _same_device(o, pages, row_start, first, c.codes, c.scales, c.zeros)
+    rc = lib().qwha_cache_read((QwhaCache * len(cs))(*(c.c_struct() for c in cs)), len(cs), _dt(outs[0]), _ptr(pages),
+                               max_pages, _ptr(row_start), _ptr(first), n_seqs, (P * len(outs))(*(_ptr(o) for o in outs)),
+                               n, _stream())
+    check(rc, "qwha_cache_read")
+    return outs[0] if isinstance(caches, QCache) else outs
+
+
+def validate_slots(cache: QCache, slots: torch.Tensor, ws: torch.Tensor | None = None) -> None:
+    """Raise QwhaError unless every slot is -1 or within the cache and no slot is named twice (synchronises)."""
+    if slots.dtype != torch.int64 or slots.dim() != 1:
+        raise ValueError("slots: expected an int64 vector")
+    _same_device(slots, cache.codes)
+    ws = _ws(workspace_size(OP_SLOTS, 1, 1, cache.n_slots, 0, False), slots.device) if ws is None else ws
+    cs = cache.c_struct()
+    check(lib().qwha_validate_slots(ctypes.byref(cs), _ptr(slots), slots.shape[0], _ptr(ws),
+                                    0 if ws is None else ws.numel(), _stream()), "qwha_validate_slots")
 
 
 def dp_backward(a: Adapter, dY: torch.Tensor, Z: torch.Tensor, alpha: float = 1.0, wq: QWeight | None = None,

@@ -137,11 +137,16 @@ enum Stage {
   ST_FWHT,
   ST_WEFF,
   ST_GEMM_DC,
+  ST_DECODE_FWHT,
+  ST_GEMV,
+  ST_CACHE_WRITE,
+  ST_CACHE_READ,
   ST_COUNT
 };
 const char *kStageNames[ST_COUNT] = {"fwht_fwd",   "spmm_fwd",   "dequant",  "gemm_fwd",  "sddmm_dc",
                                      "gather_bwd", "fwht_bwd",   "gemm_bwd", "init_alloc",
-                                     "plan_build", "fwht",       "weff",      "gemm_dc"};
+                                     "plan_build", "fwht",       "weff",      "gemm_dc",
+                                     "decode_fwht", "gemv",      "cache_write", "cache_read"};
 
 struct StageRec {
   int stage, kernels;
@@ -324,17 +329,21 @@ qwha_status check_views(const qwha_adapter *a) {
   return QWHA_OK;
 }
 
-qwha_status check_qweight(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha_dtype dt) {
-  if (!wq) return QWHA_OK;
-  if (dt != QWHA_BF16) return fail(QWHA_ERR_UNSUPPORTED, "the base GEMM needs dtype bf16");
+qwha_status check_codes(const qwha_qweight *wq, int32_t d_in) {
   if (wq->bits < 2 || wq->bits > 4) return fail(QWHA_ERR_INVALID_ARG, "bits %d not in {2,3,4}", wq->bits);
   if (wq->group <= 0 || wq->group % 8 || d_in % wq->group)
     return fail(QWHA_ERR_INVALID_ARG, "group %d must be a multiple of 8 dividing d_in %d", wq->group, d_in);
   QWHA_CHECK_PTR(wq->qweight, "qweight");
   QWHA_CHECK_PTR(wq->scales, "scales");
   QWHA_CHECK_PTR(wq->zeros, "zeros");
-  (void)d_out;
   return QWHA_OK;
+}
+
+qwha_status check_qweight(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha_dtype dt) {
+  if (!wq) return QWHA_OK;
+  if (dt != QWHA_BF16) return fail(QWHA_ERR_UNSUPPORTED, "the base GEMM needs dtype bf16");
+  (void)d_out;
+  return check_codes(wq, d_in);
 }
 
 qwha_status check_ws(void *ws, size_t ws_bytes, size_t need) {
@@ -378,6 +387,12 @@ size_t bwd_ws(int32_t d_out, int32_t d_in, int64_t p, int64_t T, bool base) {
   n += ent_bytes(p, d_out, d_in);  // CSC entries in gather order
   if (base) n += align_up((size_t)T * d_in * 4, 256) + align_up(wdeq_bytes(d_out, d_in), 256);
   return n;
+}
+
+// Z of a decode call, fp32 with the tokens side by side.
+size_t decode_ws(int32_t d_in, int64_t p, int64_t T) {
+  if (p == 0 || T == 0) return 0;
+  return align_up((size_t)decode_tokens_padded(std::min<int64_t>(T, QWHA_DECODE_MAX_T)) * d_in * 4, 256);
 }
 
 // Dense backward: W_eff, dX = dY W_eff (W_eff read MN-major), and dc = alpha *
@@ -432,6 +447,8 @@ size_t qwha_workspace_size(qwha_op op, int32_t d_out, int32_t d_in, int64_t p, i
     case QWHA_OP_REFINE: return refine_workspace(d_out, d_in);
     case QWHA_OP_ENERGY: return energy_stats_workspace(d_out, d_in);
     case QWHA_OP_PATTERN: return pattern_stats_workspace(d_in);
+    case QWHA_OP_DECODE: return decode_ws(d_in, p, T);
+    case QWHA_OP_SLOTS: return check_slots_bytes(p);
   }
   return 0;
 }
@@ -646,6 +663,10 @@ qwha_status qwha_check_stream_status(void *stream) {
   unsigned int word = 0;
   e = read_and_clear_error_word(&word, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e, "error word");
+  if (word && !(word & ~(kErrSlot | kErrPage)))
+    return fail(QWHA_ERR_INVALID_ARG, "cache: %s%s%s", word & kErrSlot ? "a slot outside the cache" : "",
+                word == (kErrSlot | kErrPage) ? ", " : "",
+                word & kErrPage ? "a page outside the cache or its page table" : "");
   if (word) return fail(QWHA_ERR_TIMEOUT, "device wait gave up (code 0x%x)", word);
   return QWHA_OK;
 }
@@ -812,6 +833,173 @@ qwha_status qwha_init_select(const float *dWq, int32_t rows, int32_t d_in, int32
   return cuda_status(launch_init_select(dWq, rows, d_in, had_block, budgets, row_ptr, p_local, col_idx, coef,
                                         (cudaStream_t)stream),
                      "init_select");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- serving
+
+namespace {
+
+qwha_status check_tokens(int64_t T) {
+  if (T < 0) return fail(QWHA_ERR_INVALID_ARG, "T %lld < 0", (long long)T);
+  if (T > QWHA_DECODE_MAX_T)
+    return fail(QWHA_ERR_UNSUPPORTED, "T %lld above %d: use qwha_adapter_fwd", (long long)T, QWHA_DECODE_MAX_T);
+  return QWHA_OK;
+}
+
+qwha_status check_cache(const qwha_cache *c) {
+  if (c->bits != 2 && c->bits != 3 && c->bits != 4 && c->bits != 8)
+    return fail(QWHA_ERR_INVALID_ARG, "cache bits %d not in {2,3,4,8}", c->bits);
+  if (c->heads < 1 || c->heads > 65535) return fail(QWHA_ERR_INVALID_ARG, "cache heads %d", c->heads);
+  if (c->head_dim < 8 || c->head_dim % 8)
+    return fail(QWHA_ERR_INVALID_ARG, "cache head_dim %d must be a positive multiple of 8", c->head_dim);
+  if (c->head_dim > cache_max_head_dim())
+    return fail(QWHA_ERR_UNSUPPORTED, "cache head_dim %d above %d", c->head_dim, cache_max_head_dim());
+  if (c->group <= 0 || c->group % 8 || c->head_dim % c->group)
+    return fail(QWHA_ERR_INVALID_ARG, "cache group %d must be a multiple of 8 dividing head_dim %d", c->group,
+                c->head_dim);
+  if (c->had_block) {
+    qwha_status st = check_hadamard(c->head_dim, c->had_block);
+    if (st != QWHA_OK) return st;
+  }
+  if (c->page_size < 1 || c->n_pages < 0 || c->n_pages > 2147483647LL)
+    return fail(QWHA_ERR_INVALID_ARG, "cache page_size %d, n_pages %lld", c->page_size, (long long)c->n_pages);
+  if (c->n_pages > 0) {
+    QWHA_CHECK_PTR(c->codes, "cache codes");
+    QWHA_CHECK_PTR(c->scales, "cache scales");
+    QWHA_CHECK_PTR(c->zeros, "cache zeros");
+  }
+  return QWHA_OK;
+}
+
+qwha_status check_caches(const qwha_cache *caches, int32_t n_caches, qwha_dtype dt, const void *const *rows,
+                         int64_t n) {
+  if (!valid_dtype(dt)) return fail(QWHA_ERR_INVALID_ARG, "dtype %d", (int)dt);
+  if (n_caches < 1 || n_caches > 2) return fail(QWHA_ERR_INVALID_ARG, "n_caches %d not 1 or 2", n_caches);
+  if (!caches || !rows) return fail(QWHA_ERR_INVALID_ARG, "%s is NULL", caches ? "rows" : "caches");
+  if (n < 0 || n > (1LL << 40)) return fail(QWHA_ERR_INVALID_ARG, "n %lld out of range", (long long)n);
+  for (int i = 0; i < n_caches; ++i) {
+    qwha_status st = check_cache(caches + i);
+    if (st != QWHA_OK) return st;
+    if (n > 0) QWHA_CHECK_PTR(rows[i], "rows");
+  }
+  return QWHA_OK;
+}
+
+CachePair cache_pair(const qwha_cache *caches, int32_t n_caches, const void *const *rows) {
+  CachePair c = {};
+  for (int i = 0; i < n_caches; ++i) {
+    c.cache[i] = caches[i];
+    c.rows[i] = rows[i];
+    c.unit[i] = caches[i].had_block ? 1.0 / sqrt((double)caches[i].had_block) : 1.0;
+  }
+  return c;
+}
+
+}  // namespace
+
+extern "C" {
+
+qwha_status qwha_qgemv(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha_dtype dt, const void *X, int64_t T,
+                       void *Y, void *stream) {
+  if (!wq) return fail(QWHA_ERR_INVALID_ARG, "wq is NULL");
+  if (!valid_dtype(dt)) return fail(QWHA_ERR_INVALID_ARG, "dtype %d", (int)dt);
+  if (d_out <= 0 || d_in <= 0) return fail(QWHA_ERR_INVALID_ARG, "d_out %d, d_in %d", d_out, d_in);
+  qwha_status st = check_codes(wq, d_in);
+  if (st != QWHA_OK || (st = check_tokens(T)) != QWHA_OK) return st;
+  if (T == 0) return QWHA_OK;
+  QWHA_CHECK_PTR(X, "X");
+  QWHA_CHECK_PTR(Y, "Y");
+  GemvArgs g = {};
+  g.qw = wq->qweight, g.scales = wq->scales, g.zeros = wq->zeros;
+  g.bits = wq->bits, g.group = wq->group, g.d_out = d_out, g.d_in = d_in;
+  g.x = X, g.T = (int)T, g.y = Y;
+  StageScope sc(ST_GEMV, 1, (cudaStream_t)stream);
+  return cuda_status(launch_gemv(dt, g, (cudaStream_t)stream), "qgemv");
+}
+
+qwha_status qwha_adapter_decode(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtype dt, const void *X,
+                                int64_t T, float alpha, void *Z_out, void *Y, void *ws, size_t ws_bytes,
+                                void *stream) {
+  qwha_status st = check_adapter_shape(a);
+  if (st != QWHA_OK) return st;
+  if (!valid_dtype(dt)) return fail(QWHA_ERR_INVALID_ARG, "dtype %d", (int)dt);
+  if (wq && (st = check_codes(wq, a->d_in)) != QWHA_OK) return st;
+  if ((st = check_tokens(T)) != QWHA_OK) return st;
+  if (a->z_given) return fail(QWHA_ERR_UNSUPPORTED, "a decode call computes its own transform (z_given must be 0)");
+  if (T == 0) return QWHA_OK;
+  QWHA_CHECK_PTR(X, "X");
+  QWHA_CHECK_PTR(Y, "Y");
+  if (Z_out) QWHA_CHECK_PTR(Z_out, "Z_out");
+  if ((st = check_ws(ws, ws_bytes, decode_ws(a->d_in, a->p, T))) != QWHA_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  GemvArgs g = {};
+  if (wq) {
+    g.qw = wq->qweight, g.scales = wq->scales, g.zeros = wq->zeros;
+    g.bits = wq->bits, g.group = wq->group;
+  }
+  g.d_out = a->d_out, g.d_in = a->d_in, g.x = X, g.T = (int)T, g.y = Y;
+  if (a->p > 0) {
+    g.row_ptr = a->row_ptr, g.col_idx = a->col_idx, g.coef = a->coef, g.p = a->p, g.alpha = alpha;
+    g.zt = static_cast<float *>(ws), g.tp = decode_tokens_padded(T);
+  }
+  if (a->p > 0 || Z_out) {
+    StageScope sc(ST_DECODE_FWHT, 1, s);
+    st = cuda_status(launch_decode_fwht(dt, X, (int)T, a->d_in, ilog2(a->had_block),
+                                        a->p > 0 ? static_cast<float *>(ws) : nullptr, g.tp, Z_out, s),
+                     "decode transform");
+    if (st != QWHA_OK) return st;
+  }
+  StageScope sc(ST_GEMV, 1, s);
+  return cuda_status(launch_gemv(dt, g, s), "decode");
+}
+
+qwha_status qwha_cache_write(const qwha_cache *caches, int32_t n_caches, qwha_dtype dt, const void *const *rows,
+                             const int64_t *slots, int64_t n, void *stream) {
+  qwha_status st = check_caches(caches, n_caches, dt, rows, n);
+  if (st != QWHA_OK) return st;
+  if (n == 0) return QWHA_OK;
+  QWHA_CHECK_PTR(slots, "slots");
+  StageScope sc(ST_CACHE_WRITE, 1, (cudaStream_t)stream);
+  return cuda_status(launch_cache_write(dt, cache_pair(caches, n_caches, rows), n_caches, slots, n,
+                                        (cudaStream_t)stream),
+                     "cache_write");
+}
+
+qwha_status qwha_cache_read(const qwha_cache *caches, int32_t n_caches, qwha_dtype dt, const int32_t *pages,
+                            int32_t max_pages, const int64_t *row_start, const int64_t *first, int32_t n_seqs,
+                            void *const *rows, int64_t n, void *stream) {
+  qwha_status st = check_caches(caches, n_caches, dt, rows, n);
+  if (st != QWHA_OK) return st;
+  if (n_seqs < 0 || max_pages < 0) return fail(QWHA_ERR_INVALID_ARG, "n_seqs %d, max_pages %d", n_seqs, max_pages);
+  if (n == 0 || n_seqs == 0) return QWHA_OK;
+  if (max_pages > 0) QWHA_CHECK_PTR(pages, "pages");
+  QWHA_CHECK_PTR(row_start, "row_start");
+  if (first) QWHA_CHECK_PTR(first, "first");
+  StageScope sc(ST_CACHE_READ, 1, (cudaStream_t)stream);
+  return cuda_status(launch_cache_read(dt, cache_pair(caches, n_caches, rows), n_caches, pages, max_pages, row_start,
+                                       first, n_seqs, n, (cudaStream_t)stream),
+                     "cache_read");
+}
+
+qwha_status qwha_validate_slots(const qwha_cache *cache, const int64_t *slots, int64_t n, void *ws, size_t ws_bytes,
+                                void *stream) {
+  if (!cache) return fail(QWHA_ERR_INVALID_ARG, "cache is NULL");
+  qwha_status st = check_cache(cache);
+  if (st != QWHA_OK) return st;
+  if (n < 0 || n > (1LL << 40)) return fail(QWHA_ERR_INVALID_ARG, "n %lld out of range", (long long)n);
+  if (n == 0) return QWHA_OK;
+  QWHA_CHECK_PTR(slots, "slots");
+  const int64_t n_slots = cache->n_pages * cache->page_size;
+  if ((st = check_ws(ws, ws_bytes, check_slots_bytes(n_slots))) != QWHA_OK) return st;
+  unsigned long long bad = 0;
+  cudaError_t e = launch_check_slots(slots, n, n_slots, ws, &bad, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_status(e, "validate_slots");
+  if (bad != ~0ull)
+    return fail(QWHA_ERR_INVALID_ARG, "%s (at %llu)", bad & 1 ? "a slot named twice" : "a slot outside the cache",
+                bad >> 1);
+  return QWHA_OK;
 }
 
 }  // extern "C"

@@ -145,3 +145,48 @@ size_t weff_smem(int32_t d_in);
 cudaError_t launch_weff(const qwha_adapter *a, const qwha_qweight *wq, float alpha, void *out, cudaStream_t s);
 
 }  // namespace qwha
+
+namespace qwha {
+
+// Products with the packed weight for a few tokens (gemv.cu). qw NULL: no base
+// term; row_ptr NULL: no adapter term. zt: fp32 [d_in][tp], the transformed
+// tokens of launch_decode_fwht.
+struct GemvArgs {
+  const uint8_t *qw;
+  const float *scales;
+  const uint8_t *zeros;
+  int bits, group, d_out, d_in;
+  const void *x;
+  int T;
+  void *y;
+  const int32_t *row_ptr, *col_idx;
+  const float *coef;
+  int64_t p;
+  float alpha;
+  const float *zt;
+  int tp;
+};
+int decode_tokens_padded(int64_t T);  // tp: the next power of two
+cudaError_t launch_decode_fwht(qwha_dtype dt, const void *x, int T, int d_in, int logn, float *zt, int tp,
+                               void *z_out, cudaStream_t s);
+cudaError_t launch_gemv(qwha_dtype dt, const GemvArgs &a, cudaStream_t s);
+
+// The quantized cache (cache.cu): up to two caches (keys and values) whose rows
+// move in one launch. unit = 1/sqrt(had_block).
+struct CachePair {
+  qwha_cache cache[2];
+  const void *rows[2];
+  double unit[2];
+};
+// Bits of the device error word.
+constexpr unsigned int kErrSlot = 0x1000u, kErrPage = 0x2000u;
+int cache_max_head_dim();
+cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, const int64_t *slots, int64_t n,
+                               cudaStream_t s);
+cudaError_t launch_cache_read(qwha_dtype dt, const CachePair &c, int n_caches, const int32_t *pages, int max_pages,
+                              const int64_t *row_start, const int64_t *first, int n_seqs, int64_t n, cudaStream_t s);
+size_t check_slots_bytes(int64_t n_slots);
+cudaError_t launch_check_slots(const int64_t *slots, int64_t n, int64_t n_slots, void *ws, unsigned long long *bad,
+                               cudaStream_t s);
+
+}  // namespace qwha
