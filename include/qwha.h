@@ -145,8 +145,9 @@ typedef enum {
   QWHA_OP_REFINE = 7,        /* qwha_refine_values */
   QWHA_OP_ENERGY = 8,        /* qwha_energy_stats */
   QWHA_OP_PATTERN = 9,       /* qwha_pattern_stats */
-  QWHA_OP_DECODE = 10,       /* qwha_adapter_decode */
-  QWHA_OP_SLOTS = 11         /* qwha_validate_slots; p = slots of the cache, other sizes 1 */
+  QWHA_OP_DECODE = 10,       /* qwha_adapter_decode; with_base: 0 without a base weight, else as below */
+  QWHA_OP_SLOTS = 11,        /* qwha_validate_slots; p = slots of the cache, other sizes 1 */
+  QWHA_OP_QGEMV = 12         /* qwha_qgemv; with_base: 1 for bf16 tokens, 2 for fp32 */
 } qwha_op;
 
 /* Z = X H row by row: x and z are [rows, n] of dtype dt (device), each row
@@ -204,9 +205,12 @@ qwha_status qwha_adapter_bwd(const qwha_adapter *a, const qwha_qweight *wq, qwha
  * GEMM, which rounds W_Q to bf16, the products of q - zeros (an exact integer)
  * and X are summed in fp32 per group and scaled in fp32; Y is rounded once.
  * d_out >= 1; d_in a multiple of wq->group (a multiple of 8). Deterministic.
- * QWHA_ERR_UNSUPPORTED above QWHA_DECODE_MAX_T. */
+ * QWHA_ERR_UNSUPPORTED above QWHA_DECODE_MAX_T. ws:
+ * qwha_workspace_size(QWHA_OP_QGEMV, d_out, d_in, 0, T, with_base) bytes,
+ * with_base 1 for bf16 and 2 for fp32 (the tokens as operands of the tensor
+ * cores). */
 qwha_status qwha_qgemv(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha_dtype dt, const void *X,
-                       int64_t T, void *Y, void *stream);
+                       int64_t T, void *Y, void *ws, size_t ws_bytes, void *stream);
 
 /* Forward of the adapted layer on 0 <= T <= QWHA_DECODE_MAX_T tokens:
  *   Y = X W_Q^T + alpha Z F^T,  Z = X H,
@@ -215,8 +219,9 @@ qwha_status qwha_qgemv(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha
  * read; a->algo, a->weff and the backward's views are not; a->z_given must be
  * 0 (QWHA_ERR_UNSUPPORTED). Z_out [T, d_in] of dtype dt, if not NULL, receives
  * Z for qwha_adapter_bwd, which is the backward of these tokens too. ws:
- * qwha_workspace_size(QWHA_OP_DECODE, d_out, d_in, p, T, 0) bytes (Z in fp32;
- * 0 when p = 0). Columns of E outside [0, d_in) are skipped. Deterministic. */
+ * qwha_workspace_size(QWHA_OP_DECODE, d_out, d_in, p, T, with_base) bytes,
+ * with_base 0 without wq, else as for qwha_qgemv (its operands, and Z in fp32
+ * when p > 0). Columns of E outside [0, d_in) are skipped. Deterministic. */
 qwha_status qwha_adapter_decode(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtype dt, const void *X,
                                 int64_t T, float alpha, void *Z_out, void *Y, void *ws, size_t ws_bytes,
                                 void *stream);

@@ -27,8 +27,8 @@ def _wq(L, bits=4, group=64, **kw):
     return L.QwhaQweight(bits, group, f["qweight"], f["scales"], f["zeros"])
 
 
-def _qgemv(L, wq, d_out=64, d_in=256, dt=1, x=BUF, T=1, y=BUF):
-    return L.lib().qwha_qgemv(ctypes.byref(wq) if wq is not None else None, d_out, d_in, dt, x, T, y, None)
+def _qgemv(L, wq, d_out=64, d_in=256, dt=1, x=BUF, T=1, y=BUF, ws=None, nbytes=0):
+    return L.lib().qwha_qgemv(ctypes.byref(wq) if wq is not None else None, d_out, d_in, dt, x, T, y, ws, nbytes, None)
 
 
 def test_qgemv_refusals():
@@ -49,6 +49,12 @@ def test_qgemv_refusals():
     assert _qgemv(L, _wq(L, scales=4)) == MISALIGNED
     assert _qgemv(L, _wq(L, zeros=None)) == INVALID
     assert _qgemv(L, _wq(L), T=0, x=None, y=None) == OK  # nothing to do
+    for dt, base, pieces in ((1, 1, 1), (0, 2, 3)):  # two bytes a value and piece, and the sums
+        need = L.lib().qwha_workspace_size(12, 64, 256, 0, 3, base)
+        assert need > 3 * 256 * 2 * pieces
+        assert _qgemv(L, _wq(L), dt=dt, T=3) == WORKSPACE
+        assert _qgemv(L, _wq(L), dt=dt, T=3, ws=BUF, nbytes=need - 1) == WORKSPACE
+        assert _qgemv(L, _wq(L), dt=dt, T=3, ws=P(4096 + 16), nbytes=need) == MISALIGNED
 
 
 def test_decode_refusals():
@@ -79,6 +85,8 @@ def test_decode_refusals():
     assert call(T=3, ws=P(4096 + 16), nbytes=need) == MISALIGNED
     assert call(T=0) == OK
     assert h.qwha_workspace_size(10, 64, 256, 0, 3, 0) == 0  # no entries: no transform to hold
+    for base in (1, 2):  # with a base weight, its operands too
+        assert h.qwha_workspace_size(10, 64, 256, 10, 3, base) == need + h.qwha_workspace_size(12, 64, 256, 0, 3, base)
 
 
 def _cache(L, **kw):

@@ -237,7 +237,7 @@ def test_products_repeat_bit_for_bit_on_other_streams_and_in_graphs():
     for k, y, b in outs:
         assert torch.equal(y, want[k]) and torch.equal(b, base[k])
     xin = xs[0].clone()
-    ws = torch.empty(W.workspace_size(10, d_out, d_in, a.p, T, False), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(W.workspace_size(10, d_out, d_in, a.p, T, 1), dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         y = W.adapter_decode(a, xin, 1.0, wq, ws=ws)

@@ -56,7 +56,7 @@ _SIGNATURES = {
         ctypes.c_int,
         [ctypes.POINTER(QwhaAdapter), ctypes.POINTER(QwhaQweight), ctypes.c_int, P, P, i64, f32, P, P, P, sz, P],
     ),
-    "qwha_qgemv": (ctypes.c_int, [ctypes.POINTER(QwhaQweight), i32, i32, ctypes.c_int, P, i64, P, P]),
+    "qwha_qgemv": (ctypes.c_int, [ctypes.POINTER(QwhaQweight), i32, i32, ctypes.c_int, P, i64, P, P, sz, P]),
     "qwha_adapter_decode": (
         ctypes.c_int,
         [ctypes.POINTER(QwhaAdapter), ctypes.POINTER(QwhaQweight), ctypes.c_int, P, i64, f32, P, P, P, sz, P],

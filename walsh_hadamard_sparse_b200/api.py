@@ -16,7 +16,7 @@ from ._lib import P, QwhaAdapter, QwhaCache, QwhaQweight, check, lib
 
 F32, BF16 = 0, 1
 OP_FWD, OP_BWD, OP_INIT, OP_PLAN, OP_FWD_DENSE, OP_BWD_DENSE, OP_SELECT_GLOBAL, OP_REFINE = 0, 1, 2, 3, 4, 5, 6, 7
-OP_ENERGY, OP_PATTERN, OP_DECODE, OP_SLOTS = 8, 9, 10, 11
+OP_ENERGY, OP_PATTERN, OP_DECODE, OP_SLOTS, OP_QGEMV = 8, 9, 10, 11, 12
 DECODE_MAX_T = 64  # most tokens of a qgemv or adapter_decode call
 PATTERN_STATS = ("empty_rows", "empty_cols", "min_row", "max_row", "min_col", "max_col", "rank_bound", "half_rows")
 SELECTION = {"magnitude": 0, "random": 1}
@@ -99,8 +99,8 @@ class QWeight:
         return s
 
 
-def workspace_size(op: int, d_out: int, d_in: int, p: int, T: int, with_base: bool) -> int:
-    return int(lib().qwha_workspace_size(op, d_out, d_in, p, T, int(bool(with_base))))
+def workspace_size(op: int, d_out: int, d_in: int, p: int, T: int, with_base: bool | int) -> int:
+    return int(lib().qwha_workspace_size(op, d_out, d_in, p, T, int(with_base)))
 
 
 def plan_tiles(d_out: int, d_in: int) -> int:
@@ -169,6 +169,11 @@ def _same_device(*tensors) -> None:
             raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{dev}")
 
 
+def _base(X: torch.Tensor) -> int:
+    """with_base of a decode workspace: the operands of fp32 tokens are larger."""
+    return 2 if X.dtype == torch.float32 else 1
+
+
 def _check_weight(wq: QWeight, d_out: int, d_in: int) -> None:
     groups = d_in // wq.group if wq.group > 0 else 0
     for name, t, dtype, shape in (("qweight", wq.qweight, torch.uint8, (d_out, d_in * wq.bits // 8)),
@@ -183,7 +188,8 @@ def _check_out(name: str, t: torch.Tensor, like: torch.Tensor, shape: tuple) -> 
         raise ValueError(f"{name}: expected {like.dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
 
 
-def qgemv(wq: QWeight, X: torch.Tensor, Y: torch.Tensor | None = None) -> torch.Tensor:
+def qgemv(wq: QWeight, X: torch.Tensor, Y: torch.Tensor | None = None,
+          ws: torch.Tensor | None = None) -> torch.Tensor:
     """Y = X W_Q^T for up to DECODE_MAX_T tokens X [T, d_in] (fp32 or bf16), straight from the packed weight; products
     of the exact q - zeros, fp32 sums, one rounding."""
     T, d_in = X.shape
@@ -193,9 +199,12 @@ def qgemv(wq: QWeight, X: torch.Tensor, Y: torch.Tensor | None = None) -> torch.
         Y = torch.empty((T, d_out), dtype=X.dtype, device=X.device)
     else:
         _check_out("Y", Y, X, (T, d_out))
-    _same_device(X, Y, wq.qweight, wq.scales, wq.zeros)
+    _same_device(X, Y, ws, wq.qweight, wq.scales, wq.zeros)
+    if ws is None:
+        ws = _ws(workspace_size(OP_QGEMV, d_out, d_in, 0, T, _base(X)), X.device)
     cw = wq.c_struct()
-    check(lib().qwha_qgemv(ctypes.byref(cw), d_out, d_in, _dt(X), _ptr(X), T, _ptr(Y), _stream()), "qwha_qgemv")
+    check(lib().qwha_qgemv(ctypes.byref(cw), d_out, d_in, _dt(X), _ptr(X), T, _ptr(Y), _ptr(ws),
+                           0 if ws is None else ws.numel(), _stream()), "qwha_qgemv")
     return Y
 
 
@@ -221,7 +230,8 @@ def adapter_decode(a: Adapter, X: torch.Tensor, alpha: float = 1.0, wq: QWeight 
         _same_device(wq.qweight, wq.scales, wq.zeros)
         cw = wq.c_struct()
     if ws is None:
-        ws = _ws(workspace_size(OP_DECODE, a.d_out, a.d_in, a.p, T, False), X.device)
+        need = workspace_size(OP_DECODE, a.d_out, a.d_in, a.p, T, 0 if wq is None else _base(X))
+        ws = _ws(need, X.device)
     cs = a.c_struct()
     rc = lib().qwha_adapter_decode(ctypes.byref(cs), ctypes.byref(cw) if cw is not None else None, _dt(X), _ptr(X), T,
                                    float(alpha), _ptr(Z_out), _ptr(Y), _ptr(ws), 0 if ws is None else ws.numel(),

@@ -137,7 +137,7 @@ enum Stage {
   ST_FWHT,
   ST_WEFF,
   ST_GEMM_DC,
-  ST_DECODE_FWHT,
+  ST_DECODE_PREPARE,
   ST_GEMV,
   ST_CACHE_WRITE,
   ST_CACHE_READ,
@@ -146,7 +146,7 @@ enum Stage {
 const char *kStageNames[ST_COUNT] = {"fwht_fwd",   "spmm_fwd",   "dequant",  "gemm_fwd",  "sddmm_dc",
                                      "gather_bwd", "fwht_bwd",   "gemm_bwd", "init_alloc",
                                      "plan_build", "fwht",       "weff",      "gemm_dc",
-                                     "decode_fwht", "gemv",      "cache_write", "cache_read"};
+                                     "decode_prepare", "gemv",      "cache_write", "cache_read"};
 
 struct StageRec {
   int stage, kernels;
@@ -389,10 +389,17 @@ size_t bwd_ws(int32_t d_out, int32_t d_in, int64_t p, int64_t T, bool base) {
   return n;
 }
 
-// Z of a decode call, fp32 with the tokens side by side.
-size_t decode_ws(int32_t d_in, int64_t p, int64_t T) {
-  if (p == 0 || T == 0) return 0;
-  return align_up((size_t)decode_tokens_padded(std::min<int64_t>(T, QWHA_DECODE_MAX_T)) * d_in * 4, 256);
+// The tokens as the tensor-core product reads them, then Z in fp32 with the
+// tokens of a column side by side.
+size_t qgemv_ws(int32_t d_in, int64_t T, bool f32) {
+  return gemv_x_bytes(d_in, std::min<int64_t>(T, QWHA_DECODE_MAX_T), f32);
+}
+size_t decode_ws(int32_t d_in, int64_t p, int64_t T, bool base, bool f32) {
+  const size_t z =
+      p > 0 && T > 0
+          ? align_up((size_t)decode_tokens_padded(std::min<int64_t>(T, QWHA_DECODE_MAX_T)) * d_in * 4, 256)
+          : 0;
+  return (base ? qgemv_ws(d_in, T, f32) : 0) + z;
 }
 
 // Dense backward: W_eff, dX = dY W_eff (W_eff read MN-major), and dc = alpha *
@@ -447,7 +454,8 @@ size_t qwha_workspace_size(qwha_op op, int32_t d_out, int32_t d_in, int64_t p, i
     case QWHA_OP_REFINE: return refine_workspace(d_out, d_in);
     case QWHA_OP_ENERGY: return energy_stats_workspace(d_out, d_in);
     case QWHA_OP_PATTERN: return pattern_stats_workspace(d_in);
-    case QWHA_OP_DECODE: return decode_ws(d_in, p, T);
+    case QWHA_OP_DECODE: return decode_ws(d_in, p, T, with_base != 0, with_base == 2);
+    case QWHA_OP_QGEMV: return qgemv_ws(d_in, T, with_base == 2);
     case QWHA_OP_SLOTS: return check_slots_bytes(p);
   }
   return 0;
@@ -848,6 +856,32 @@ qwha_status check_tokens(int64_t T) {
   return QWHA_OK;
 }
 
+// The launches of a checked qwha_qgemv (a NULL) or qwha_adapter_decode call.
+qwha_status decode_call(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtype dt, const void *X, int64_t T,
+                        int32_t d_out, int32_t d_in, float alpha, void *Z_out, void *Y, void *ws, cudaStream_t s) {
+  GemvArgs g = {};
+  if (wq) {
+    g.qw = wq->qweight, g.scales = wq->scales, g.zeros = wq->zeros;
+    g.bits = wq->bits, g.group = wq->group;
+  }
+  g.d_out = d_out, g.d_in = d_in, g.x = X, g.T = (int)T, g.f32 = dt == QWHA_F32, g.y = Y;
+  const bool tensor = gemv_on_tensor_cores(g.qw, g.group);
+  if (tensor) gemv_place_x(&g, ws);
+  if (a && a->p > 0) {
+    g.row_ptr = a->row_ptr, g.col_idx = a->col_idx, g.coef = a->coef, g.p = a->p, g.alpha = alpha;
+    g.zt = reinterpret_cast<float *>(static_cast<char *>(ws) + (wq ? qgemv_ws(d_in, T, g.f32) : 0));
+    g.tp = decode_tokens_padded(T);
+  }
+  if (gemv_prepares_x(g) || g.zt || Z_out) {
+    g.prepared = 1;
+    StageScope sc(ST_DECODE_PREPARE, 1, s);
+    qwha_status st = cuda_status(launch_decode_prepare(g, a ? ilog2(a->had_block) : 0, Z_out, s), "decode preparation");
+    if (st != QWHA_OK) return st;
+  }
+  StageScope sc(ST_GEMV, 1, s);
+  return cuda_status(launch_gemv(g, s), "matrix-vector product");
+}
+
 qwha_status check_cache(const qwha_cache *c) {
   if (c->bits != 2 && c->bits != 3 && c->bits != 4 && c->bits != 8)
     return fail(QWHA_ERR_INVALID_ARG, "cache bits %d not in {2,3,4,8}", c->bits);
@@ -902,7 +936,7 @@ CachePair cache_pair(const qwha_cache *caches, int32_t n_caches, const void *con
 extern "C" {
 
 qwha_status qwha_qgemv(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha_dtype dt, const void *X, int64_t T,
-                       void *Y, void *stream) {
+                       void *Y, void *ws, size_t ws_bytes, void *stream) {
   if (!wq) return fail(QWHA_ERR_INVALID_ARG, "wq is NULL");
   if (!valid_dtype(dt)) return fail(QWHA_ERR_INVALID_ARG, "dtype %d", (int)dt);
   if (d_out <= 0 || d_in <= 0) return fail(QWHA_ERR_INVALID_ARG, "d_out %d, d_in %d", d_out, d_in);
@@ -911,12 +945,8 @@ qwha_status qwha_qgemv(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha
   if (T == 0) return QWHA_OK;
   QWHA_CHECK_PTR(X, "X");
   QWHA_CHECK_PTR(Y, "Y");
-  GemvArgs g = {};
-  g.qw = wq->qweight, g.scales = wq->scales, g.zeros = wq->zeros;
-  g.bits = wq->bits, g.group = wq->group, g.d_out = d_out, g.d_in = d_in;
-  g.x = X, g.T = (int)T, g.y = Y;
-  StageScope sc(ST_GEMV, 1, (cudaStream_t)stream);
-  return cuda_status(launch_gemv(dt, g, (cudaStream_t)stream), "qgemv");
+  if ((st = check_ws(ws, ws_bytes, qgemv_ws(d_in, T, dt == QWHA_F32))) != QWHA_OK) return st;
+  return decode_call(nullptr, wq, dt, X, T, d_out, d_in, 0.f, nullptr, Y, ws, (cudaStream_t)stream);
 }
 
 qwha_status qwha_adapter_decode(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtype dt, const void *X,
@@ -932,27 +962,8 @@ qwha_status qwha_adapter_decode(const qwha_adapter *a, const qwha_qweight *wq, q
   QWHA_CHECK_PTR(X, "X");
   QWHA_CHECK_PTR(Y, "Y");
   if (Z_out) QWHA_CHECK_PTR(Z_out, "Z_out");
-  if ((st = check_ws(ws, ws_bytes, decode_ws(a->d_in, a->p, T))) != QWHA_OK) return st;
-  cudaStream_t s = (cudaStream_t)stream;
-  GemvArgs g = {};
-  if (wq) {
-    g.qw = wq->qweight, g.scales = wq->scales, g.zeros = wq->zeros;
-    g.bits = wq->bits, g.group = wq->group;
-  }
-  g.d_out = a->d_out, g.d_in = a->d_in, g.x = X, g.T = (int)T, g.y = Y;
-  if (a->p > 0) {
-    g.row_ptr = a->row_ptr, g.col_idx = a->col_idx, g.coef = a->coef, g.p = a->p, g.alpha = alpha;
-    g.zt = static_cast<float *>(ws), g.tp = decode_tokens_padded(T);
-  }
-  if (a->p > 0 || Z_out) {
-    StageScope sc(ST_DECODE_FWHT, 1, s);
-    st = cuda_status(launch_decode_fwht(dt, X, (int)T, a->d_in, ilog2(a->had_block),
-                                        a->p > 0 ? static_cast<float *>(ws) : nullptr, g.tp, Z_out, s),
-                     "decode transform");
-    if (st != QWHA_OK) return st;
-  }
-  StageScope sc(ST_GEMV, 1, s);
-  return cuda_status(launch_gemv(dt, g, s), "decode");
+  if ((st = check_ws(ws, ws_bytes, decode_ws(a->d_in, a->p, T, wq != nullptr, dt == QWHA_F32))) != QWHA_OK) return st;
+  return decode_call(a, wq, dt, X, T, a->d_out, a->d_in, alpha, Z_out, Y, ws, (cudaStream_t)stream);
 }
 
 qwha_status qwha_cache_write(const qwha_cache *caches, int32_t n_caches, qwha_dtype dt, const void *const *rows,

@@ -11,10 +11,13 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "gemv_mma.cuh"
 #include "kernels.h"
 
 namespace qwha {
 namespace {
+
+using gemv::load8;
 
 constexpr int kRowThreads = 256;
 constexpr int kRowTokens = 8;  // tokens a row kernel's CTA takes (the rest are further grid rows)
@@ -24,12 +27,6 @@ __device__ __forceinline__ uint32_t run_word(const uint8_t *p, int bits) {
   if (bits == 4) return *reinterpret_cast<const uint32_t *>(p);
   if (bits == 2) return *reinterpret_cast<const uint16_t *>(p);
   return (uint32_t)p[0] | (uint32_t)p[1] << 8 | (uint32_t)p[2] << 16;
-}
-
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, float *v) {
-#pragma unroll
-  for (int u = 0; u < 8; u += io<T>::kVec) io<T>::unpack(*reinterpret_cast<const uint4 *>(p + u), v + u);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -96,38 +93,50 @@ __global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const GemvArgs a
   }
 }
 
-// Z = X H for the few tokens of a decode call, in fp32 with the tokens of one
-// column side by side (zt[k * tp + t]), so that an entry of E finds its column
-// of every token in one place; and, on request, z_out [T, d_in] in X's type
-// for the backward. One CTA per token and span of whole Hadamard blocks.
-template <typename T>
-__global__ void __launch_bounds__(512) decode_fwht_kernel(const T *__restrict__ x, int d_in, int logn, int span,
-                                                          float scale, float *zt, int tp, T *z_out) {
+constexpr int kPrepThreads = 256;
+
+// What a product needs of its tokens beforehand: the operands above (CTAs from
+// `spans` on), and Z = X H, one CTA per token and span of whole Hadamard
+// blocks: zt in fp32 with the tokens of one column side by side (zt[k * tp +
+// t]), so that an entry of E finds its column of every token in one place, and
+// z_out [T, d_in] in X's type for the backward, on request.
+template <int BITS, typename T>
+__global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const GemvArgs a, int logn, int span, int spans,
+                                                                      float scale, T *z_out) {
   extern __shared__ __align__(16) float row[];
-  const int t = blockIdx.y, k0 = blockIdx.x * span;
-  const int d = d_in - k0 < span ? d_in - k0 : span;
-  const T *src = x + (int64_t)t * d_in + k0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may start on the weight
+  if ((int)blockIdx.x >= spans) {
+    const int parts = (a.d_in + 127) / 128 * 16, i = (blockIdx.x - spans) * kPrepThreads + threadIdx.x;
+    gemv::prepare_piece<BITS, T>(a, i / parts, i % parts, i < a.T * parts, a.T * a.pieces, a.xpieces, a.xsums);
+    return;
+  }
+  const int per = (a.d_in + span - 1) / span;
+  const int t = blockIdx.x / per, k0 = blockIdx.x % per * span;
+  const int d = a.d_in - k0 < span ? a.d_in - k0 : span;
+  const T *src = static_cast<const T *>(a.x) + (int64_t)t * a.d_in + k0;
   for (int k = threadIdx.x; k < d; k += blockDim.x) row[k] = io<T>::load1(src + k);
   __syncthreads();
   butterflies_smem_f32(row, d, logn);
   for (int k = threadIdx.x; k < d; k += blockDim.x) {
     const float v = row[k] * scale;
-    if (zt) zt[(int64_t)(k0 + k) * tp + t] = v;
-    if (z_out) io<T>::store1(z_out + (int64_t)t * d_in + k0 + k, v);
+    if (a.zt) a.zt[(int64_t)(k0 + k) * a.tp + t] = v;
+    if (z_out) io<T>::store1(z_out + (int64_t)t * a.d_in + k0 + k, v);
   }
 }
 
-template <typename T>
-cudaError_t transform(const void *x, int T_, int d_in, int logn, float *zt, int tp, void *z_out, cudaStream_t s) {
+template <int BITS, typename T>
+cudaError_t prepare(const GemvArgs &a, int logn, void *z_out, cudaStream_t s) {
   const int n = 1 << logn;
   // spans of whole blocks, about 2048 columns where the blocks are shorter
   const int span = n >= 2048 ? n : 2048;
-  const size_t smem = (size_t)span * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(decode_fwht_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int spans = a.zt || z_out ? a.T * (int)cdiv(a.d_in, span) : 0;
+  const int parts = gemv_prepares_x(a) ? a.T * (int)cdiv(a.d_in, 128) * 16 : 0;
+  const size_t smem = spans ? (size_t)span * sizeof(float) : 0;
+  auto kernel = decode_prepare_kernel<BITS, T>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32768 * 4);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)cdiv(d_in, span), (unsigned)T_);
-  decode_fwht_kernel<T><<<grid, 512, smem, s>>>(static_cast<const T *>(x), d_in, logn, span,
-                                                (float)(1.0 / sqrt((double)n)), zt, tp, static_cast<T *>(z_out));
+  kernel<<<(unsigned)(spans + cdiv(parts, kPrepThreads)), kPrepThreads, smem, s>>>(
+      a, logn, span, spans, (float)(1.0 / sqrt((double)n)), static_cast<T *>(z_out));
   return cudaGetLastError();
 }
 
@@ -139,15 +148,42 @@ int decode_tokens_padded(int64_t T) {
   return tp;
 }
 
-cudaError_t launch_decode_fwht(qwha_dtype dt, const void *x, int T, int d_in, int logn, float *zt, int tp,
-                               void *z_out, cudaStream_t s) {
-  return dt == QWHA_F32 ? transform<float>(x, T, d_in, logn, zt, tp, z_out, s)
-                        : transform<__nv_bfloat16>(x, T, d_in, logn, zt, tp, z_out, s);
+bool gemv_on_tensor_cores(const uint8_t *qw, int group) { return qw && group % 32 == 0; }
+
+bool gemv_prepares_x(const GemvArgs &a) { return a.xpieces; }
+
+namespace {
+int pieces_of(bool f32) { return f32 ? 3 : 1; }
+// The last n-tile of a chunk is whole, whatever the group: up to seven columns more than there are.
+size_t xpieces_bytes(int32_t d_in, int64_t T, bool f32) {
+  return align_up((size_t)cdiv(d_in, 128) * 256 * (T * pieces_of(f32) + 7), 256);
+}
+}  // namespace
+
+size_t gemv_x_bytes(int32_t d_in, int64_t T, bool f32) {
+  if (T <= 0) return 0;
+  return xpieces_bytes(d_in, T, f32) + align_up((size_t)cdiv(d_in, 128) * 64 * x_tiles((int)T * pieces_of(f32), 4), 256);
 }
 
-cudaError_t launch_gemv(qwha_dtype dt, const GemvArgs &a, cudaStream_t s) {
+void gemv_place_x(GemvArgs *a, void *ws) {
+  a->pieces = pieces_of(a->f32);
+  a->xpieces = static_cast<uint4 *>(ws);
+  a->xsums = reinterpret_cast<float2 *>(static_cast<char *>(ws) + xpieces_bytes(a->d_in, a->T, a->f32));
+}
+
+cudaError_t launch_decode_prepare(const GemvArgs &a, int logn, void *z_out, cudaStream_t s) {
+  if (a.bits == 2)
+    return a.f32 ? prepare<2, float>(a, logn, z_out, s) : prepare<2, __nv_bfloat16>(a, logn, z_out, s);
+  if (a.bits == 3)
+    return a.f32 ? prepare<3, float>(a, logn, z_out, s) : prepare<3, __nv_bfloat16>(a, logn, z_out, s);
+  return a.f32 ? prepare<4, float>(a, logn, z_out, s) : prepare<4, __nv_bfloat16>(a, logn, z_out, s);
+}
+
+cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s) {
+  if (gemv_on_tensor_cores(a.qw, a.group))
+    return a.bits == 4 ? launch_gemv_b4(a, s) : a.bits == 3 ? launch_gemv_b3(a, s) : launch_gemv_b2(a, s);
   const dim3 grid((unsigned)cdiv(a.d_out, kRowThreads / 32), (unsigned)cdiv(a.T, kRowTokens));
-  if (dt == QWHA_F32) gemv_rows_kernel<float><<<grid, kRowThreads, 0, s>>>(a);
+  if (a.f32) gemv_rows_kernel<float><<<grid, kRowThreads, 0, s>>>(a);
   else gemv_rows_kernel<__nv_bfloat16><<<grid, kRowThreads, 0, s>>>(a);
   return cudaGetLastError();
 }

@@ -1,0 +1,545 @@
+// The packed matrix-vector product on tensor cores (see gemv.cu): one
+// definition for the three code widths, instantiated by gemv_b2/3/4.cu.
+//
+// Unpacking bounds this kernel as much as memory does: at 6.5 TB/s a 4-bit
+// code leaves about three instruction slots, and half as many on the integer
+// pipe. Two exact representations keep the count below one slot a code:
+//   * a code masked out of a 16-bit half at bit o (o + bits <= 10) IS the f16
+//     denormal q * 2^(o - 24): most codes need one mask and no shift;
+//   * the tokens' values, scaled by a power of two per chunk of 128 columns so
+//     that the largest lies in [2^14, 2^15), are f16 numbers too: a bf16 value
+//     in one piece, an fp32 value in three (exact down to 2^-31 of the chunk's
+//     largest or less); 2^-o is folded into the values
+//     (decode_prepare_kernel). Each piece is a column of the instruction.
+// The matrix unit (m16n8k16, 8.3 clocks measured for f16 and bf16 alike) adds
+// the exact products in fp32 over one quantization group; then, in fp32,
+//   acc += scale * 2^k * (sum_k q x - zero * sum_k x),
+// with 2^k and sum_k x per (group, piece) prepared beside the values. No
+// weight is rounded.
+//
+// Layout. A warp takes 16 MT rows and a slice of the columns; the warps of a
+// CTA are KS slices of kWarps / KS tiles. The four lanes of a row take a run of
+// 32 columns each of a 128-column chunk. The order of the columns inside the
+// sum is free: a lane's fragment holds codes of its own run in the order the
+// masks yield, and the values are stored in that order. Where a group is
+// shorter than the chunk (G = 2 or 4 groups in it), the eight columns of the
+// instruction are G groups times 8 / G pieces: a column holds its piece on the
+// lanes of its group and zeros elsewhere, so no sum crosses a group.
+//
+// Memory. Codes, scales and zero points go straight to the registers of the
+// lane that uses them, DEPTH chunks ahead, past L1; the values stay in L1. No
+// shared memory and no barrier until the slices are added.
+
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace qwha {
+namespace gemv {
+
+constexpr int kWarps = 8;
+
+// Pair p (0 <= p < 16) of a run of 32 codes: codes first(p) and first(p) +
+// gap() in the halves of a register, at bit `unit(p)` of their half.
+template <int BITS>
+__host__ __device__ constexpr int first(int p) {
+  return BITS == 4 ? 8 * (p / 4) + p % 4 : BITS == 2 ? 16 * (p / 8) + p % 8 : p;
+}
+template <int BITS>
+__host__ __device__ constexpr int gap() {
+  return BITS == 4 ? 4 : BITS == 2 ? 8 : 16;
+}
+template <int BITS>
+__host__ __device__ constexpr int unit(int p) {
+  if (BITS == 4) return p % 2 * 4;
+  if (BITS == 2) return p % 8 < 5 ? 2 * (p % 8) : 2 * (p % 8 - 5);
+  constexpr int u[16] = {0, 3, 6, 0, 3, 6, 2, 5, 0, 3, 6, 1, 4, 7, 0, 3};
+  return u[p];
+}
+
+// The sixteen pairs of a run.
+template <int BITS>
+__device__ __forceinline__ void unpack(const uint32_t *w, uint32_t *q) {
+  if constexpr (BITS == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = w[i] >> 8;
+      q[4 * i] = w[i] & 0x000f000fu, q[4 * i + 1] = w[i] & 0x00f000f0u;
+      q[4 * i + 2] = h & 0x000f000fu, q[4 * i + 3] = h & 0x00f000f0u;
+    }
+  } else if constexpr (BITS == 2) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t h = w[i] >> 10;
+#pragma unroll
+      for (int j = 0; j < 5; ++j) q[8 * i + j] = w[i] & (0x00030003u << (2 * j));
+#pragma unroll
+      for (int j = 0; j < 3; ++j) q[8 * i + 5 + j] = h & (0x00030003u << (2 * j));
+    }
+  } else {
+    // the 96 bits as halves h0..h5: codes 0..15 are h0..h2, codes 16..31 are h3..h5; side by side, halves i and
+    // i + 3 hold codes p and p + 16 at the same place. Codes 5 and 10 straddle two halves.
+    const uint32_t a = __byte_perm(w[0], w[1], 0x7610), b = __byte_perm(w[0], w[2], 0x5432),
+                   c = __byte_perm(w[1], w[2], 0x7610);
+    const uint32_t ah = a >> 9, bh = b >> 8, ch = c >> 10;
+    q[0] = a & 0x00070007u, q[1] = a & 0x00380038u, q[2] = a & 0x01c001c0u;
+    q[3] = ah & 0x00070007u, q[4] = ah & 0x00380038u;
+    q[5] = (ah & 0x00400040u) | ((b << 7) & 0x01800180u);
+    q[6] = b & 0x001c001cu, q[7] = b & 0x00e000e0u;
+    q[8] = bh & 0x00070007u, q[9] = bh & 0x00380038u;
+    q[10] = (bh & 0x00c000c0u) | ((c << 8) & 0x01000100u);
+    q[11] = c & 0x000e000eu, q[12] = c & 0x00700070u, q[13] = c & 0x03800380u;
+    q[14] = ch & 0x00070007u, q[15] = ch & 0x00380038u;
+  }
+}
+
+// d = A B
+__device__ __forceinline__ void mma0(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// c += A B
+__device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Entries of one row of E against the transformed tokens t0 .. t0 + np - 1:
+// VW tokens to a lane, lpe lanes to an entry; the sums of the row land in
+// sp[0 .. np). The order of the additions depends on the sizes alone.
+template <int VW>
+__device__ __forceinline__ void sparse_row(const GemvArgs &a, const float *z, int row, int t0, int np, int lpe,
+                                           int lane, float *sp) {
+  const int e0 = lane / lpe, tq = (lane % lpe) * VW;
+  const bool on = tq < np;
+  float acc[VW];
+#pragma unroll
+  for (int i = 0; i < VW; ++i) acc[i] = 0.f;
+  int64_t b = a.row_ptr[row], e = a.row_ptr[row + 1];
+  if (b < 0) b = 0;
+  if (e > a.p) e = a.p;
+  const int step = 32 / lpe;
+  if (on) {
+#pragma unroll 4
+    for (int64_t j = b + e0; j < e; j += step) {
+      const int k = a.col_idx[j];
+      const float c = a.coef[j];
+      if ((unsigned)k >= (unsigned)a.d_in) continue;
+      const float *src = z + (int64_t)k * a.tp + t0 + tq;
+      if constexpr (VW == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(src);
+        acc[0] = fmaf(c, v.x, acc[0]), acc[1] = fmaf(c, v.y, acc[1]);
+        acc[2] = fmaf(c, v.z, acc[2]), acc[3] = fmaf(c, v.w, acc[3]);
+      } else if constexpr (VW == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(src);
+        acc[0] = fmaf(c, v.x, acc[0]), acc[1] = fmaf(c, v.y, acc[1]);
+      } else {
+        acc[0] = fmaf(c, *src, acc[0]);
+      }
+    }
+  }
+  for (int o = lpe; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < VW; ++i) acc[i] += __shfl_xor_sync(~0u, acc[i], o);
+  if (e0 == 0 && on)
+#pragma unroll
+    for (int i = 0; i < VW; ++i) sp[tq + i] = acc[i];
+}
+
+// One row and token by the definition, for results the fast path leaves NaN: a
+// chunk with an infinity or a NaN has no pieces (its factor is NaN).
+static __device__ __noinline__ float plain_dot(const GemvArgs &a, int row, int tok) {
+  const int ng = a.d_in / a.group;
+  const uint8_t *qw = a.qw + (int64_t)row * (a.d_in / 8) * a.bits;
+  const uint32_t mask = (1u << a.bits) - 1u;
+  float sum = 0.f;
+  for (int r = 0; r < a.d_in / 8; ++r) {
+    uint32_t w = 0;
+    for (int b = 0; b < a.bits; ++b) w |= (uint32_t)qw[(int64_t)r * a.bits + b] << (8 * b);
+    const int64_t g = (int64_t)row * ng + r * 8 / a.group;
+    const float z = (float)a.zeros[g];
+    float part = 0.f;
+    for (int i = 0; i < 8; ++i) {
+      const int64_t at = (int64_t)tok * a.d_in + r * 8 + i;
+      const float v = a.f32 ? static_cast<const float *>(a.x)[at]
+                            : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.x)[at]);
+      part = fmaf((float)((w >> (a.bits * i)) & mask) - z, v, part);
+    }
+    sum = fmaf(a.scales[g], part, sum);
+  }
+  return sum;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float *v) {
+#pragma unroll
+  for (int u = 0; u < 8; u += io<T>::kVec) io<T>::unpack(*reinterpret_cast<const uint4 *>(p + u), v + u);
+}
+
+__host__ __device__ constexpr int even(int n) { return (n + 1) & ~1; }
+
+// Four consecutive values.
+__device__ __forceinline__ void load4(const float *p, float *v) { io<float>::unpack(*reinterpret_cast<const uint4 *>(p), v); }
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *v) {
+  const uint2 q = *reinterpret_cast<const uint2 *>(p);
+  v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
+}
+
+__device__ __forceinline__ float exp2i(int k) { return __int_as_float((k + 127) << 23); }  // -126 <= k <= 127
+
+// The tokens as operands: one thread per token, run of 32 columns and quarter
+// of its pairs, the sixteen of a chunk on neighbouring lanes (i = run * 4 + j).
+// The chunk's values are scaled by the power of two that brings the largest
+// into [2^14, 2^15), then split into f16 pieces by rounding and subtracting
+// (exact in fp32: each piece takes the leading eleven bits, so a bf16 value is
+// one piece and an fp32 value three). A pair's unit divides its values. sums
+// gets, per group, the sum of the scaled values (times 2^-24, the unit of the
+// codes) beside the first piece's column and 0 beside the others, and the
+// factor that undoes the scaling, times 2^12 (the other 2^12 of the unit is
+// applied at the end, so that neither leaves fp32's range). A chunk with an
+// infinity or a NaN gets the factor NaN, which sends its rows' sums to the
+// plain path.
+template <int BITS, typename T>
+__device__ __forceinline__ void prepare_piece(const GemvArgs &a, int tok, int i, bool live, int cols, uint4 *pieces,
+                                              float2 *sums) {
+  const int run = i >> 2, j = i & 3, chunk = run >> 2, t = run & 3, k0 = run * 32;
+  // the pairs' first halves and second halves are four consecutive values each
+  const int at = first<BITS>(0) + (BITS == 4 ? 8 * j : BITS == 2 ? 16 * (j >> 1) + 4 * (j & 1) : 4 * j);
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (live && k0 < a.d_in) {
+    const T *src = static_cast<const T *>(a.x) + (int64_t)tok * a.d_in + k0 + at;
+    load4(src, v);
+    load4(src + gap<BITS>(), v + 4);
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) top = max(top, __float_as_uint(v[u]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = 1; o < 16; o *= 2) top = max(top, __shfl_xor_sync(~0u, top, o));
+  const bool finite = top < 0x7f800000u;
+  const int e = max(1, (int)(top >> 23)), up = top && finite ? 141 - e : 0;  // top < 2^(e - 126)
+  const float f0 = exp2i(up >> 1), f1 = exp2i(up - (up >> 1));
+  float sum = 0.f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    v[u] = finite ? v[u] * f0 * f1 : 0.f;
+    sum += v[u];
+  }
+  const int G = a.group % 128 == 0 ? 1 : a.group % 64 == 0 ? 2 : 4;
+  sum += __shfl_xor_sync(~0u, sum, 1);
+  sum += __shfl_xor_sync(~0u, sum, 2);
+  const float sum2 = sum + __shfl_xor_sync(~0u, sum, 4);
+  const float sum4 = sum2 + __shfl_xor_sync(~0u, sum2, 8);
+  if (!live) return;
+  sum = G == 1 ? sum4 : G == 2 ? sum2 : sum;
+  for (int p = 0; p < a.pieces; ++p) {
+    const int col = tok * a.pieces + p, TPN = 8 / G;
+    const int64_t tile = (int64_t)chunk * x_tiles(cols, G) + col / TPN;
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // 2^-unit of pair 4 j + k
+      float by;
+      if (BITS == 4) by = k % 2 ? 0x1p-4f : 1.f;
+      else {
+        constexpr int A[4] = {unit<BITS>(0), unit<BITS>(1), unit<BITS>(2), unit<BITS>(3)},
+                      B[4] = {unit<BITS>(4), unit<BITS>(5), unit<BITS>(6), unit<BITS>(7)},
+                      C[4] = {unit<BITS>(8), unit<BITS>(9), unit<BITS>(10), unit<BITS>(11)},
+                      D[4] = {unit<BITS>(12), unit<BITS>(13), unit<BITS>(14), unit<BITS>(15)};
+        by = exp2i(-(j == 0 ? A[k] : j == 1 ? B[k] : j == 2 ? C[k] : D[k]));
+      }
+      const __half2 h = __floats2half2_rn(v[k], v[4 + k]), d = __floats2half2_rn(v[k] * by, v[4 + k] * by);
+      r[k] = *reinterpret_cast<const uint32_t *>(&d);
+      v[k] -= __low2float(h), v[4 + k] -= __high2float(h);
+    }
+    pieces[tile * (16 * TPN) + j * (4 * TPN) + col % TPN * 4 + t] = make_uint4(r[0], r[1], r[2], r[3]);
+    if (j == 0 && t % (4 / G) == 0)
+      sums[tile * 8 + t * G / 4 * TPN + col % TPN] =
+          make_float2(p == 0 ? sum * 0x1p-24f : 0.f, finite ? exp2i(12 - up) : __int_as_float(0x7fc00000));
+  }
+}
+
+// What a lane holds of a chunk: its runs of 2 MT rows, their scales and zero points.
+template <int BITS, int MT>
+struct Chunk {
+  uint32_t w[2 * MT][BITS];
+  float s[2 * MT];
+  uint32_t z[2 * MT];
+};
+
+template <int BITS>
+__device__ __forceinline__ void f_zero(uint32_t *w) {
+#pragma unroll
+  for (int i = 0; i < BITS; ++i) w[i] = 0;
+}
+
+// f(0), f(1), ..., f(N - 1) with compile-time arguments.
+template <int N, typename F>
+__device__ __forceinline__ void each(F &&f) {
+  if constexpr (N > 0) {
+    each<N - 1>(f);
+    f(std::integral_constant<int, N - 1>());
+  }
+}
+
+template <int BITS, int OFF>
+__device__ __forceinline__ void load_run(const uint8_t *p, uint32_t *w) {
+  if constexpr (BITS == 4)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4+%5];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p), "n"(OFF));
+  else if constexpr (BITS == 2)
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2+%3];" : "=r"(w[0]), "=r"(w[1]) : "l"(p), "n"(OFF));
+  else
+    asm volatile(
+        "ld.global.nc.u32 %0, [%3+%4];\n\tld.global.nc.u32 %1, [%3+%5];\n\tld.global.nc.u32 %2, [%3+%6];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2])
+        : "l"(p), "n"(OFF), "n"(OFF + 4), "n"(OFF + 8));
+}
+
+// EXACT: the group is 128 / G columns, so a chunk's groups follow the chunk.
+template <int BITS, int G, int NT, int MT, int DEPTH, bool EXACT>
+__global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
+    gemv_mma_kernel(const GemvArgs a, int tokens_per_pass, int slices, int z_floats) {
+  constexpr int TPN = 8 / G, ROWS = 16 * MT, ROW_CHUNK = 16 * BITS;
+  extern __shared__ __align__(16) float smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int t0 = blockIdx.y * tokens_per_pass;
+  const int np = a.T - t0 < tokens_per_pass ? a.T - t0 : tokens_per_pass;
+  const int ng = a.d_in / a.group, chunks = (a.d_in + 127) / 128;
+  const int tiles_here = kWarps / slices;
+  const int row_first = blockIdx.x * tiles_here * ROWS;  // of the CTA
+  const int row0 = row_first + warp / slices * ROWS;     // of the warp
+  const int per = (chunks + slices - 1) / slices;
+  const int c_begin = warp % slices * per;
+  const int c_end = row0 < a.d_out ? (c_begin + per < chunks ? c_begin + per : chunks) : c_begin;
+
+  const uint8_t *pw[2 * MT], *pz[2 * MT];
+  const float *ps[2 * MT];
+  {
+    const int64_t row_bytes = (int64_t)(a.d_in / 32) * (4 * BITS);
+#pragma unroll
+    for (int h = 0; h < 2 * MT; ++h) {
+      int r = row0 + h * 8 + g;
+      r = r < a.d_out ? r : a.d_out - 1;  // rows behind the last one repeat it and are not stored
+      const int64_t grp = (int64_t)r * ng + (EXACT ? c_begin * G + t * G / 4 : 0);
+      pw[h] = a.qw + r * row_bytes + (int64_t)c_begin * ROW_CHUNK + t * (4 * BITS);
+      ps[h] = a.scales + grp;
+      pz[h] = a.zeros + grp;
+    }
+  }
+  // chunk c + I, I chunks behind the pointers
+  auto fetch = [&](Chunk<BITS, MT> &f, int c, auto I) {
+    constexpr int i = decltype(I)::value;
+    const int k0 = c * 128 + t * 32;
+    const bool on = c < c_end && (G == 1 || k0 < a.d_in);
+#pragma unroll
+    for (int h = 0; h < 2 * MT; ++h) {
+      f.s[h] = 0.f;
+      if (on) {
+        load_run<BITS, i * ROW_CHUNK>(pw[h], f.w[h]);
+        const int gi = EXACT ? i * G : k0 / a.group;
+        f.s[h] = __ldg(ps[h] + gi);
+        f.z[h] = __ldg(pz[h] + gi);
+      }
+    }
+  };
+  Chunk<BITS, MT> buf[DEPTH];
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i)
+#pragma unroll
+    for (int h = 0; h < 2 * MT; ++h) {
+      f_zero<BITS>(buf[i].w[h]);
+      buf[i].z[h] = 0;
+    }
+  each<DEPTH>([&](auto I) { fetch(buf[decltype(I)::value], c_begin + decltype(I)::value, I); });
+
+  // the values and Z are the preparing launch's outputs: wait for it only here
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int pieces = a.pieces, v_end = np * pieces, v_most = tokens_per_pass * pieces;
+  const int n_tiles = x_tiles(a.T * pieces, G), nt0 = t0 * pieces / TPN;
+  // this lane's column of an n-tile: a piece, live where the column's group is the lane's own
+  const bool mine = g / TPN == t * G / 4;
+  const uint4 *xp = a.xpieces + ((int64_t)c_begin * n_tiles + nt0) * (16 * TPN) + g % TPN * 4 + t;
+  const float4 *xs = reinterpret_cast<const float4 *>(a.xsums) + ((int64_t)c_begin * n_tiles + nt0) * 4 + t;
+
+  float acc[MT][NT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+
+  for (int c = c_begin; c < c_end; c += DEPTH) {
+#pragma unroll
+    for (int h = 0; h < 2 * MT; ++h) {
+      pw[h] += DEPTH * ROW_CHUNK;
+      if (EXACT) ps[h] += DEPTH * G, pz[h] += DEPTH * G;
+    }
+    each<DEPTH>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      if (c + i < c_end) {
+        Chunk<BITS, MT> &f = buf[i];
+        const bool in = G == 1 || (c + i) * 128 + t * 32 < a.d_in;
+        uint32_t q[2 * MT][16];
+        float s[2 * MT], zp[2 * MT];
+#pragma unroll
+        for (int h = 0; h < 2 * MT; ++h) {
+          unpack<BITS>(f.w[h], q[h]);
+          s[h] = f.s[h];
+          zp[h] = (float)f.z[h];
+        }
+        fetch(f, c + i + DEPTH, I);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (NT > 1 && n * TPN >= v_end) break;
+          uint4 x[4];
+          const bool on = in && mine && n * TPN + g % TPN < v_end;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j] = make_uint4(0, 0, 0, 0);
+            if (on) x[j] = xp[n * (16 * TPN) + j * (4 * TPN)];
+          }
+          const float4 fx = xs[n * 4];
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t *q0 = q[2 * m], *q1 = q[2 * m + 1];
+            float d[4];
+            mma0(d, q0[0], q1[0], q0[1], q1[1], x[0].x, x[0].y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (j) mma(d, q0[4 * j], q1[4 * j], q0[4 * j + 1], q1[4 * j + 1], x[j].x, x[j].y);
+              mma(d, q0[4 * j + 2], q1[4 * j + 2], q0[4 * j + 3], q1[4 * j + 3], x[j].z, x[j].w);
+            }
+            // d[0], d[1]: row g, columns 2t and 2t + 1, whose group is this lane's; d[2], d[3]: row g + 8
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              acc[m][n][2 * h] = fmaf(s[2 * m + h] * fx.y, fmaf(-zp[2 * m + h], fx.x, d[2 * h]), acc[m][n][2 * h]);
+              acc[m][n][2 * h + 1] =
+                  fmaf(s[2 * m + h] * fx.w, fmaf(-zp[2 * m + h], fx.z, d[2 * h + 1]), acc[m][n][2 * h + 1]);
+            }
+          }
+        }
+        xp += (int64_t)n_tiles * (16 * TPN);
+        xs += n_tiles * 4;
+      }
+    });
+  }
+
+  const int spw = (tokens_per_pass + 3) & ~3;
+  float *red = smem;                                // [kWarps][G][v_most][ROWS]: the warps' sums
+  float *sp = red + kWarps * G * v_most * ROWS;     // [tiles_here * ROWS][spw]: the entries' sums
+  float *zs = sp + kWarps * ROWS * spw;             // [z_floats]
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (NT > 1 && n * TPN >= v_end) break;
+    const int v = n * TPN + 2 * t % TPN;
+    float *dst = red + ((warp * G + 2 * t / TPN) * v_most + v) * ROWS + g;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (v + j < v_end) dst[j * ROWS + m * 16] = acc[m][n][j], dst[j * ROWS + m * 16 + 8] = acc[m][n][2 + j];
+  }
+  const int rows_here = tiles_here * ROWS < a.d_out - row_first ? tiles_here * ROWS : a.d_out - row_first;
+  if (a.row_ptr) {
+    const float *z = a.zt;
+    if (z_floats) {
+      for (int i = threadIdx.x * 4; i < z_floats; i += blockDim.x * 4)
+        *reinterpret_cast<float4 *>(zs + i) = *reinterpret_cast<const float4 *>(a.zt + i);
+      __syncthreads();
+      z = zs;
+    }
+    const int al = gridDim.y == 1 ? 0 : tokens_per_pass;  // passes start at its multiples
+    int vw = a.tp < 4 ? a.tp : 4, lpe = 1;
+    while (al % vw) vw /= 2;
+    while (lpe * vw < np) lpe *= 2;
+    for (int r = warp; r < rows_here; r += kWarps) {
+      if (vw == 4) sparse_row<4>(a, z, row_first + r, t0, np, lpe, lane, sp + r * spw);
+      else if (vw == 2) sparse_row<2>(a, z, row_first + r, t0, np, lpe, lane, sp + r * spw);
+      else sparse_row<1>(a, z, row_first + r, t0, np, lpe, lane, sp + r * spw);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < tiles_here * ROWS * np; i += blockDim.x) {
+    const int r = i % (tiles_here * ROWS), tok = i / (tiles_here * ROWS);
+    if (r >= rows_here) continue;
+    const float *src = red + (r / ROWS) * slices * G * v_most * ROWS + r % ROWS;
+    float sum = 0.f;
+    for (int v = tok * pieces; v < (tok + 1) * pieces; ++v)
+      for (int w = 0; w < slices * G; ++w) sum += src[(w * v_most + v) * ROWS];
+    sum *= 0x1p12f;  // the rest of the codes' unit
+    if (sum != sum) sum = plain_dot(a, row_first + r, t0 + tok);
+    if (a.row_ptr) sum += a.alpha * sp[r * spw + tok];
+    const int64_t at = (int64_t)(t0 + tok) * a.d_out + row_first + r;
+    if (a.f32) static_cast<float *>(a.y)[at] = sum;
+    else static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(sum);
+  }
+}
+
+template <int BITS, int G, int NT, int MT, int DEPTH, bool EXACT>
+cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
+  constexpr int TPN = 8 / G, cols = NT * TPN, ROWS = 16 * MT;
+  int tpp = cols / a.pieces;
+  // a further pass starts with an n-tile, and where a vector of the entries' tokens does
+  if (tpp < a.T) tpp = std::max(tpp & ~(TPN - 1) & ~3, tpp & ~(TPN - 1) & ~1);
+  else tpp = a.T;
+  // slices of the columns: as many as it takes to give every SM sixteen warps, two chunks a warp at least
+  const int64_t tiles = cdiv(a.d_out, ROWS), chunks = cdiv(a.d_in, 128);
+  int slices = 1;
+  while (slices < kWarps && tiles * slices < (int64_t)sm_count() * 12 && chunks >= 2 * slices) slices *= 2;
+  size_t smem = sizeof(float) * ((size_t)kWarps * G * tpp * a.pieces * ROWS + kWarps * ROWS * ((tpp + 3) & ~3));
+  const int64_t z_all = a.row_ptr ? (int64_t)a.d_in * a.tp : 0;
+  const int z_floats = smem + z_all * 4 <= 96 * 1024 ? (int)z_all : 0;
+  smem += (size_t)z_floats * 4;
+  auto kernel = gemv_mma_kernel<BITS, G, NT, MT, DEPTH, EXACT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cdiv(tiles, kWarps / slices), (unsigned)cdiv(a.T, tpp));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.prepared ? 1 : 0;  // overlaps the preparing launch
+  return cudaLaunchKernelEx(&cfg, kernel, a, tpp, slices, z_floats);
+}
+
+template <int BITS, int G, bool EXACT>
+cudaError_t launch_cols(const GemvArgs &a, cudaStream_t s) {
+  const int tiles = x_tiles(a.T * a.pieces, G);
+  if (tiles <= 1) return launch_one<BITS, G, 1, 1, 4, EXACT>(a, s);
+  if (tiles <= 2) return launch_one<BITS, G, 2, 1, 3, EXACT>(a, s);
+  if (tiles <= 4) return launch_one<BITS, G, 4, 1, 2, EXACT>(a, s);
+  return launch_one<BITS, G, 8, 2, 2, EXACT>(a, s);
+}
+
+template <int BITS>
+cudaError_t launch_bits(const GemvArgs &a, cudaStream_t s) {
+  if (a.group == 128) return launch_cols<BITS, 1, true>(a, s);
+  if (a.group == 64) return launch_cols<BITS, 2, true>(a, s);
+  if (a.group == 32) return launch_cols<BITS, 4, true>(a, s);
+  if (a.group % 128 == 0) return launch_cols<BITS, 1, false>(a, s);
+  if (a.group % 64 == 0) return launch_cols<BITS, 2, false>(a, s);
+  return launch_cols<BITS, 4, false>(a, s);
+}
+
+}  // namespace gemv
+}  // namespace qwha

@@ -149,27 +149,45 @@ cudaError_t launch_weff(const qwha_adapter *a, const qwha_qweight *wq, float alp
 namespace qwha {
 
 // Products with the packed weight for a few tokens (gemv.cu). qw NULL: no base
-// term; row_ptr NULL: no adapter term. zt: fp32 [d_in][tp], the transformed
-// tokens of launch_decode_fwht.
+// term; row_ptr NULL: no adapter term. zt: fp32 [d_in][tp]; xpieces, xsums: the
+// tokens for the tensor cores (gemv_on_tensor_cores); all three written by the
+// launch_decode_prepare that precedes the product on its stream.
 struct GemvArgs {
   const uint8_t *qw;
   const float *scales;
   const uint8_t *zeros;
   int bits, group, d_out, d_in;
   const void *x;
-  int T;
+  int T, f32;  // tokens, and whether x and y are fp32 (else bf16)
   void *y;
   const int32_t *row_ptr, *col_idx;
   const float *coef;
   int64_t p;
   float alpha;
-  const float *zt;
+  float *zt;
   int tp;
+  // The values as operands, `pieces` columns a token, C = T * pieces rounded up to even: xpieces [chunk of 128
+  // columns][C][4 runs][4] of 16 bytes, xsums [chunk][groups in it][C] (sum, factor) pairs. Where each CTA of the
+  // product makes them itself (gemv_prepares_x false) they are not read.
+  int pieces;
+  uint4 *xpieces;
+  float2 *xsums;
+  int prepared;  // a launch_decode_prepare precedes the product
 };
+__host__ __device__ constexpr int x_tiles(int cols, int G) { return (cols * G + 7) / 8; }
+bool gemv_prepares_x(const GemvArgs &a);
 int decode_tokens_padded(int64_t T);  // tp: the next power of two
-cudaError_t launch_decode_fwht(qwha_dtype dt, const void *x, int T, int d_in, int logn, float *zt, int tp,
-                               void *z_out, cudaStream_t s);
-cudaError_t launch_gemv(qwha_dtype dt, const GemvArgs &a, cudaStream_t s);
+bool gemv_on_tensor_cores(const uint8_t *qw, int group);
+// Workspace of the operands of T tokens, and where in it they lie.
+size_t gemv_x_bytes(int32_t d_in, int64_t T, bool f32);
+void gemv_place_x(GemvArgs *a, void *ws);
+// Fills a.zt (if set), a.xpieces and a.xsums (if set) and z_out (if not NULL) from a.x.
+cudaError_t launch_decode_prepare(const GemvArgs &a, int logn, void *z_out, cudaStream_t s);
+cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s);
+// Its tensor-core kernels (gemv_mma.cuh).
+cudaError_t launch_gemv_b2(const GemvArgs &a, cudaStream_t s);
+cudaError_t launch_gemv_b3(const GemvArgs &a, cudaStream_t s);
+cudaError_t launch_gemv_b4(const GemvArgs &a, cudaStream_t s);
 
 // The quantized cache (cache.cu): up to two caches (keys and values) whose rows
 // move in one launch. unit = 1/sqrt(had_block).
