@@ -220,8 +220,8 @@ qwha_status qwha_qgemv(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha
  * 0 (QWHA_ERR_UNSUPPORTED). Z_out [T, d_in] of dtype dt, if not NULL, receives
  * Z for qwha_adapter_bwd, which is the backward of these tokens too. ws:
  * qwha_workspace_size(QWHA_OP_DECODE, d_out, d_in, p, T, with_base) bytes,
- * with_base 0 without wq, else as for qwha_qgemv (its operands, and Z in fp32
- * when p > 0). Columns of E outside [0, d_in) are skipped. Deterministic. */
+ * with_base 0 without wq, else as for qwha_qgemv (its operands, and when p > 0
+ * Z and the entries' sums in fp32). Columns of E outside [0, d_in) are skipped. Deterministic. */
 qwha_status qwha_adapter_decode(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtype dt, const void *X,
                                 int64_t T, float alpha, void *Z_out, void *Y, void *ws, size_t ws_bytes,
                                 void *stream);

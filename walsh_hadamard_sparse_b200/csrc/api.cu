@@ -138,6 +138,7 @@ enum Stage {
   ST_WEFF,
   ST_GEMM_DC,
   ST_DECODE_PREPARE,
+  ST_DECODE_ENTRIES,
   ST_GEMV,
   ST_CACHE_WRITE,
   ST_CACHE_READ,
@@ -146,7 +147,7 @@ enum Stage {
 const char *kStageNames[ST_COUNT] = {"fwht_fwd",   "spmm_fwd",   "dequant",  "gemm_fwd",  "sddmm_dc",
                                      "gather_bwd", "fwht_bwd",   "gemm_bwd", "init_alloc",
                                      "plan_build", "fwht",       "weff",      "gemm_dc",
-                                     "decode_prepare", "gemv",      "cache_write", "cache_read"};
+                                     "decode_prepare", "decode_entries", "gemv",      "cache_write", "cache_read"};
 
 struct StageRec {
   int stage, kernels;
@@ -389,17 +390,14 @@ size_t bwd_ws(int32_t d_out, int32_t d_in, int64_t p, int64_t T, bool base) {
   return n;
 }
 
-// The tokens as the tensor-core product reads them, then Z in fp32 with the
-// tokens of a column side by side.
+// The tokens as the tensor-core product reads them, then Z in fp32 and the
+// entries' sums.
 size_t qgemv_ws(int32_t d_in, int64_t T, bool f32) {
   return gemv_x_bytes(d_in, std::min<int64_t>(T, QWHA_DECODE_MAX_T), f32);
 }
-size_t decode_ws(int32_t d_in, int64_t p, int64_t T, bool base, bool f32) {
-  const size_t z =
-      p > 0 && T > 0
-          ? align_up((size_t)decode_tokens_padded(std::min<int64_t>(T, QWHA_DECODE_MAX_T)) * d_in * 4, 256)
-          : 0;
-  return (base ? qgemv_ws(d_in, T, f32) : 0) + z;
+size_t decode_ws(int32_t d_out, int32_t d_in, int64_t p, int64_t T, bool base, bool f32) {
+  const int64_t n = std::min<int64_t>(T, QWHA_DECODE_MAX_T);
+  return (base ? qgemv_ws(d_in, T, f32) : 0) + (p > 0 ? gemv_z_bytes(d_out, d_in, n) : 0);
 }
 
 // Dense backward: W_eff, dX = dY W_eff (W_eff read MN-major), and dc = alpha *
@@ -454,7 +452,7 @@ size_t qwha_workspace_size(qwha_op op, int32_t d_out, int32_t d_in, int64_t p, i
     case QWHA_OP_REFINE: return refine_workspace(d_out, d_in);
     case QWHA_OP_ENERGY: return energy_stats_workspace(d_out, d_in);
     case QWHA_OP_PATTERN: return pattern_stats_workspace(d_in);
-    case QWHA_OP_DECODE: return decode_ws(d_in, p, T, with_base != 0, with_base == 2);
+    case QWHA_OP_DECODE: return decode_ws(d_out, d_in, p, T, with_base != 0, with_base == 2);
     case QWHA_OP_QGEMV: return qgemv_ws(d_in, T, with_base == 2);
     case QWHA_OP_SLOTS: return check_slots_bytes(p);
   }
@@ -869,13 +867,17 @@ qwha_status decode_call(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtyp
   if (tensor) gemv_place_x(&g, ws);
   if (a && a->p > 0) {
     g.row_ptr = a->row_ptr, g.col_idx = a->col_idx, g.coef = a->coef, g.p = a->p, g.alpha = alpha;
-    g.zt = reinterpret_cast<float *>(static_cast<char *>(ws) + (wq ? qgemv_ws(d_in, T, g.f32) : 0));
-    g.tp = decode_tokens_padded(T);
+    gemv_place_z(&g, static_cast<char *>(ws) + (wq ? qgemv_ws(d_in, T, g.f32) : 0));
   }
-  if (gemv_prepares_x(g) || g.zt || Z_out) {
-    g.prepared = 1;
+  g.prepared = tensor || g.zt || Z_out;
+  if (g.prepared) {
     StageScope sc(ST_DECODE_PREPARE, 1, s);
     qwha_status st = cuda_status(launch_decode_prepare(g, a ? ilog2(a->had_block) : 0, Z_out, s), "decode preparation");
+    if (st != QWHA_OK) return st;
+  }
+  if (g.zt) {
+    StageScope sc(ST_DECODE_ENTRIES, 1, s);
+    qwha_status st = cuda_status(launch_decode_entries(g, s), "decode entries");
     if (st != QWHA_OK) return st;
   }
   StageScope sc(ST_GEMV, 1, s);
@@ -957,12 +959,13 @@ qwha_status qwha_adapter_decode(const qwha_adapter *a, const qwha_qweight *wq, q
   if (!valid_dtype(dt)) return fail(QWHA_ERR_INVALID_ARG, "dtype %d", (int)dt);
   if (wq && (st = check_codes(wq, a->d_in)) != QWHA_OK) return st;
   if ((st = check_tokens(T)) != QWHA_OK) return st;
+  if (a->p > 2147483647LL - 4096) return fail(QWHA_ERR_UNSUPPORTED, "decode: p = %lld", (long long)a->p);
   if (a->z_given) return fail(QWHA_ERR_UNSUPPORTED, "a decode call computes its own transform (z_given must be 0)");
   if (T == 0) return QWHA_OK;
   QWHA_CHECK_PTR(X, "X");
   QWHA_CHECK_PTR(Y, "Y");
   if (Z_out) QWHA_CHECK_PTR(Z_out, "Z_out");
-  if ((st = check_ws(ws, ws_bytes, decode_ws(a->d_in, a->p, T, wq != nullptr, dt == QWHA_F32))) != QWHA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, decode_ws(a->d_out, a->d_in, a->p, T, wq != nullptr, dt == QWHA_F32))) != QWHA_OK) return st;
   return decode_call(a, wq, dt, X, T, a->d_out, a->d_in, alpha, Z_out, Y, ws, (cudaStream_t)stream);
 }
 

@@ -10,6 +10,7 @@
 
 #include <algorithm>
 
+#include "bulk.cuh"
 #include "common.cuh"
 #include "gemv_mma.cuh"
 #include "kernels.h"
@@ -36,17 +37,17 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // One warp per output row: lanes stride over the row's runs of eight codes (a
-// run lies in one group, as groups are multiples of 8), then over the row's
-// entries of E. Takes every group the format has.
+// run lies in one group, as groups are multiples of 8). Takes every group the
+// format has, and calls without a base term.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const GemvArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
   const int t0 = blockIdx.y * kRowTokens;
   const int nt = a.T - t0 < kRowTokens ? a.T - t0 : kRowTokens;
-  float base[kRowTokens], ad[kRowTokens];
+  float base[kRowTokens];
 #pragma unroll
-  for (int u = 0; u < kRowTokens; ++u) base[u] = ad[u] = 0.f;
+  for (int u = 0; u < kRowTokens; ++u) base[u] = 0.f;
   if (row < a.d_out && a.qw) {
     const T *x = static_cast<const T *>(a.x) + (int64_t)t0 * a.d_in;
     const int runs = a.d_in / 8, ng = a.d_in / a.group;
@@ -70,36 +71,54 @@ __global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const GemvArgs a
       }
     }
   }
-  if (row < a.d_out && a.row_ptr) {
-    int64_t b = a.row_ptr[row], e = a.row_ptr[row + 1];
-    if (b < 0) b = 0;
-    if (e > a.p) e = a.p;
-    for (int64_t j = b + lane; j < e; j += 32) {
-      const int k = a.col_idx[j];
-      if ((unsigned)k >= (unsigned)a.d_in) continue;
-      const float c = a.coef[j];
-      const float *z = a.zt + (int64_t)k * a.tp + t0;
-#pragma unroll
-      for (int u = 0; u < kRowTokens; ++u)
-        if (u < nt) ad[u] = fmaf(c, z[u], ad[u]);
-    }
-  }
 #pragma unroll
   for (int u = 0; u < kRowTokens; ++u) {
     if (u >= nt) break;
-    const float v = warp_sum(base[u]) + a.alpha * warp_sum(ad[u]);
-    if (lane == 0 && row < a.d_out)
+    float v = warp_sum(base[u]);
+    if (lane == 0 && row < a.d_out) {
+      if (a.y_ad) v += a.alpha * a.y_ad[row * a.tp + t0 + u];
       io<T>::store1(static_cast<T *>(a.y) + (int64_t)(t0 + u) * a.d_out + row, v);
+    }
   }
 }
 
 constexpr int kPrepThreads = 256;
 
-// What a product needs of its tokens beforehand: the operands above (CTAs from
+// Shared-memory place of element i of a span: four floats of padding every
+// sixteen, so that sixteen consecutive elements a thread and elements sixteen
+// apart are both free of bank conflicts (two ways at most).
+__host__ __device__ constexpr int span_at(int i) { return i + (i >> 4) * 4; }
+
+// NB butterfly stages from stage s on over d elements, sixteen or fewer to a
+// thread and turn, in registers.
+template <int NB>
+__device__ __forceinline__ void span_pass(float *row, int d, int s) {
+  constexpr int N = 1 << NB;
+  for (int q = threadIdx.x; q < (d >> NB); q += kPrepThreads) {
+    const int base = ((q >> s) << (s + NB)) | (q & ((1 << s) - 1));
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = row[span_at(base + (i << s))];
+#pragma unroll
+    for (int h = 1; h < N; h *= 2)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!(i & h)) {
+          const float x = v[i], y = v[i + h];
+          v[i] = x + y, v[i + h] = x - y;
+        }
+#pragma unroll
+    for (int i = 0; i < N; ++i) row[span_at(base + (i << s))] = v[i];
+  }
+  __syncthreads();
+}
+
+// What a product needs of its tokens beforehand: the operands (CTAs from
 // `spans` on), and Z = X H, one CTA per token and span of whole Hadamard
-// blocks: zt in fp32 with the tokens of one column side by side (zt[k * tp +
-// t]), so that an entry of E finds its column of every token in one place, and
-// z_out [T, d_in] in X's type for the backward, on request.
+// blocks: zt in fp32 with the tg tokens of a group side by side, so that an
+// entry of E finds its column of all of them in one place, and z_out [T, d_in]
+// in X's type for the backward, on request. Latency bounds it:
+// four stages a pass, so 4096 columns take three turns through shared memory.
 template <int BITS, typename T>
 __global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const GemvArgs a, int logn, int span, int spans,
                                                                       float scale, T *z_out) {
@@ -112,16 +131,229 @@ __global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const Gemv
   }
   const int per = (a.d_in + span - 1) / span;
   const int t = blockIdx.x / per, k0 = blockIdx.x % per * span;
-  const int d = a.d_in - k0 < span ? a.d_in - k0 : span;
+  const int d = a.d_in - k0 < span ? a.d_in - k0 : span;  // a multiple of 8
   const T *src = static_cast<const T *>(a.x) + (int64_t)t * a.d_in + k0;
-  for (int k = threadIdx.x; k < d; k += blockDim.x) row[k] = io<T>::load1(src + k);
+  for (int k = threadIdx.x * 4; k < d; k += kPrepThreads * 4) {
+    float v[4];
+    gemv::load4(src + k, v);
+    *reinterpret_cast<float4 *>(row + span_at(k)) = make_float4(v[0], v[1], v[2], v[3]);
+  }
   __syncthreads();
-  butterflies_smem_f32(row, d, logn);
-  for (int k = threadIdx.x; k < d; k += blockDim.x) {
-    const float v = row[k] * scale;
-    if (a.zt) a.zt[(int64_t)(k0 + k) * a.tp + t] = v;
+  for (int s = 0; s < logn; s += 4) {
+    if (logn - s >= 4) span_pass<4>(row, d, s);
+    else if (logn - s == 3) span_pass<3>(row, d, s);
+    else if (logn - s == 2) span_pass<2>(row, d, s);
+    else span_pass<1>(row, d, s);
+  }
+  for (int k = threadIdx.x; k < d; k += kPrepThreads) {
+    const float v = row[span_at(k)] * scale;
+    if (a.zt) a.zt[((int64_t)(t / a.tg) * a.d_in + k0 + k) * a.tg + t % a.tg] = v;
     if (z_out) io<T>::store1(z_out + (int64_t)t * a.d_in + k0 + k, v);
   }
+}
+
+constexpr int kEntThreads = 1024, kEntWarps = kEntThreads / 32;
+constexpr int kEntRows = 1024;  // rows of a CTA whose borders are kept in shared memory
+constexpr int kLongRow = 256, kHugeRow = 1024;
+constexpr size_t kEntSmem = 200 * 1024;
+constexpr unsigned kErrEntries = 0x8000u;  // a wait for a copy gave up
+
+// Sum over n entries by 1 << LANES_LOG2 lanes, four entries a lane in flight.
+template <int TG, int LANES_LOG2>
+__device__ __forceinline__ void row_sum(const int32_t *cols, const float *coefs, int n, const float *zs, int d_in, int lane,
+                                        float *acc) {
+  constexpr int L = 1 << LANES_LOG2;
+#pragma unroll
+  for (int i = 0; i < TG; ++i) acc[i] = 0.f;
+  for (int j = lane; j < n; j += 4 * L) {
+    int k[4];
+    float c[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool in = j + u * L < n;
+      k[u] = in ? __ldg(cols + j + u * L) : -1;
+      c[u] = in ? __ldg(coefs + j + u * L) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if ((unsigned)k[u] >= (unsigned)d_in) k[u] = 0, c[u] = 0.f;
+      const float *z = zs + (int64_t)k[u] * TG;
+      if constexpr (TG >= 4) {
+#pragma unroll
+        for (int i = 0; i < TG; i += 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(z + i);
+          acc[i] = fmaf(c[u], v.x, acc[i]), acc[i + 1] = fmaf(c[u], v.y, acc[i + 1]);
+          acc[i + 2] = fmaf(c[u], v.z, acc[i + 2]), acc[i + 3] = fmaf(c[u], v.w, acc[i + 3]);
+        }
+      } else if constexpr (TG == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(z);
+        acc[0] = fmaf(c[u], v.x, acc[0]), acc[1] = fmaf(c[u], v.y, acc[1]);
+      } else {
+        acc[0] = fmaf(c[u], *z, acc[0]);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < L; o *= 2)
+#pragma unroll
+    for (int i = 0; i < TG; ++i) acc[i] += __shfl_xor_sync(~0u, acc[i], o);
+}
+
+// The entries of E against the transformed tokens: y_ad[i][t] = sum_{j in row i}
+// c_j Z[t][k_j], fp32. Gathering Z from L2 costs a sector an entry and waits
+// for each (measured on the gate layer, sixteen tokens: 47 us inside the
+// product's kernel), so the columns of a group of TG tokens are brought into
+// shared memory where they fit, and an entry a lane gathers there; the entries
+// themselves stream from L2 once a group. Wider layers gather from L2 (three
+// turns of the entries with a third of the columns each cost more: 70 against
+// 54 us a pass on the down layer, five tokens).
+//
+// Rows differ in length by orders of magnitude (the budget follows the row's
+// quantization error): a CTA takes whole rows that hold its even share of the
+// entries; 8 to 32 lanes, as the CTA's rows are many or few, take a row of up
+// to kLongRow entries, a warp a longer one, the CTA one above kHugeRow. Every sum has one place and one order.
+template <int TG>
+__global__ void __launch_bounds__(kEntThreads, 1)
+    decode_entries_kernel(const GemvArgs a, int buffers, unsigned int *err) {
+  extern __shared__ __align__(16) float zs_all[];  // [buffers][d_in][TG]
+  __shared__ int rp_s[kEntRows + 1], counts[2];
+  __shared__ float part[kEntWarps][TG];
+  __shared__ uint64_t s_bar[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may start on the weight
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < 2) {
+    bulk::init(bulk::saddr(s_bar + threadIdx.x), 1);
+    bulk::fence_init();
+    counts[threadIdx.x] = 0;
+  }
+  __syncthreads();
+  auto border = [&](int r) {
+    const int b = a.row_ptr[r];
+    return b < 0 ? 0 : b > a.p ? (int)a.p : b;
+  };
+  // the CTA's rows: those whose entries start at or behind its share's first entry, before the next share's
+  const int64_t share = (a.p + gridDim.x - 1) / gridDim.x, s0 = blockIdx.x * share, s1 = s0 + share;
+  {
+    int n0 = 0, n1 = 0;
+#pragma unroll 4
+    for (int r = threadIdx.x; r < a.d_out; r += kEntThreads) {
+      const int b = border(r);
+      n0 += b < s0, n1 += b < s1;
+    }
+    n0 = __reduce_add_sync(~0u, n0), n1 = __reduce_add_sync(~0u, n1);
+    if (lane == 0) atomicAdd(counts, n0), atomicAdd(counts + 1, n1);
+  }
+  __syncthreads();
+  const int r0 = blockIdx.x == 0 ? 0 : counts[0], r1 = blockIdx.x == gridDim.x - 1 ? a.d_out : counts[1];
+  const bool near = r1 - r0 <= kEntRows;
+  for (int i = threadIdx.x; near && i <= r1 - r0; i += kEntThreads) rp_s[i] = border(r0 + i);
+  auto row_at = [&](int r) { return near ? rp_s[r - r0] : border(r); };
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // Z is the preparing launch's output
+  // turn n: the tokens of group n; with two buffers the next turn's Z is on its way
+  const int turns = a.tp / TG;
+  const uint32_t bytes = a.d_in * TG * 4;
+  auto copy_z = [&](int n) {
+    const uint32_t bar = bulk::saddr(s_bar + n % 2);
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+    bulk::fence_proxy();
+    bulk::copy(bulk::saddr(zs_all) + (buffers == 2 ? n % 2 * bytes : 0), a.zt + (int64_t)n * a.d_in * TG, bytes, bar);
+  };
+  if (buffers && threadIdx.x == 0) copy_z(0);
+  for (int n = 0; n < turns; ++n) {
+    const int t0 = n * TG;
+    const float *zs = !buffers ? a.zt + (int64_t)n * a.d_in * TG : zs_all + (buffers == 2 ? n % 2 * (a.d_in * TG) : 0);
+    __syncthreads();  // the last turn's gathers are done (and the rows' borders are there)
+    if (buffers) {
+      if (threadIdx.x == 0 && (buffers == 2 ? n + 1 < turns : n > 0)) copy_z(buffers == 2 ? n + 1 : n);
+      // incomplete if it gives up, reported through the error word
+      if (!bulk::wait(bulk::saddr(s_bar + n % 2), (uint32_t)(n / 2 & 1))) atomicOr(err, kErrEntries);
+      __syncwarp();
+    }
+    auto put = [&](int r, const float *acc) {
+      float *out = a.y_ad + (int64_t)r * a.tp + t0;
+      if constexpr (TG >= 4) {
+#pragma unroll
+        for (int i = 0; i < TG; i += 4)
+          *reinterpret_cast<float4 *>(out + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < TG; ++i) out[i] = acc[i];
+      }
+    };
+    float acc[TG];
+    // the short rows, `1 << LL` lanes each
+    auto short_rows = [&](auto LL) {
+      constexpr int ll = decltype(LL)::value, rows = 32 >> ll;
+      for (int q = r0 + warp * rows; q < r1; q += kEntWarps * rows) {
+        const int r = q + (lane >> ll);
+        int b = 0, len = -1;
+        if (r < r1) {
+          b = row_at(r);
+          len = row_at(r + 1) - b;
+          if (len < 0) len = 0;
+        }
+        row_sum<TG, ll>(a.col_idx + b, a.coef + b, len > kLongRow ? 0 : len, zs, a.d_in, lane & ((1 << ll) - 1), acc);
+        if ((lane & ((1 << ll) - 1)) == 0 && len >= 0 && len <= kLongRow) put(r, acc);
+      }
+    };
+    if (r1 - r0 <= kEntWarps) short_rows(std::integral_constant<int, 5>());
+    else if (r1 - r0 <= 2 * kEntWarps) short_rows(std::integral_constant<int, 4>());
+    else short_rows(std::integral_constant<int, 3>());
+    // a warp a long row, the CTA a huge one (the longest row would otherwise be the kernel's time)
+    for (int q = r0; q < r1; q += 32) {
+      const int r = q + lane;
+      const int mine = r < r1 ? row_at(r + 1) - row_at(r) : 0;
+      unsigned some = __ballot_sync(~0u, mine > kLongRow && mine <= kHugeRow), huge = __ballot_sync(~0u, mine > kHugeRow);
+      while (some) {
+        const int at = __ffs(some) - 1, b = row_at(q + at), len = row_at(q + at + 1) - b;
+        some &= some - 1;
+        if (((q - r0) + at) % kEntWarps != warp) continue;
+        row_sum<TG, 5>(a.col_idx + b, a.coef + b, len, zs, a.d_in, lane, acc);
+        if (lane == 0) put(q + at, acc);
+      }
+      while (huge) {
+        const int at = __ffs(huge) - 1, b = row_at(q + at), len = row_at(q + at + 1) - b;
+        huge &= huge - 1;
+        const int per = (len + kEntWarps - 1) / kEntWarps, lo = warp * per < len ? warp * per : len;
+        const int n_here = len - lo < per ? len - lo : per;
+        row_sum<TG, 5>(a.col_idx + b + lo, a.coef + b + lo, n_here, zs, a.d_in, lane, acc);
+        if (lane == 0)
+#pragma unroll
+          for (int i = 0; i < TG; ++i) part[warp][i] = acc[i];
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+          for (int i = 0; i < TG; ++i) acc[i] = warp_sum(part[lane][i]);
+          if (lane == 0) put(q + at, acc);
+        }
+        __syncthreads();
+      }
+    }
+  }
+}
+
+template <int TG>
+cudaError_t entries(const GemvArgs &a, cudaStream_t s) {
+  const size_t group_bytes = (size_t)a.d_in * TG * sizeof(float);
+  const int buffers = 2 * group_bytes <= kEntSmem && a.tp > TG ? 2 : group_bytes <= kEntSmem ? 1 : 0;
+  auto kernel = decode_entries_kernel<TG>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kEntSmem);
+  if (e != cudaSuccess) return e;
+  unsigned int *err = device_error_word();
+  if (!err) return cudaErrorInvalidDevicePointer;
+  cudaLaunchConfig_t cfg = {};
+  // a CTA an SM, with 256 entries at least
+  cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(sm_count(), a.p / 256)));
+  cfg.blockDim = dim3(kEntThreads);
+  cfg.dynamicSmemBytes = buffers * group_bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;  // overlaps the preparing launch, which is the one before
+  return cudaLaunchKernelEx(&cfg, kernel, a, buffers, err);
 }
 
 template <int BITS, typename T>
@@ -130,10 +362,10 @@ cudaError_t prepare(const GemvArgs &a, int logn, void *z_out, cudaStream_t s) {
   // spans of whole blocks, about 2048 columns where the blocks are shorter
   const int span = n >= 2048 ? n : 2048;
   const int spans = a.zt || z_out ? a.T * (int)cdiv(a.d_in, span) : 0;
-  const int parts = gemv_prepares_x(a) ? a.T * (int)cdiv(a.d_in, 128) * 16 : 0;
-  const size_t smem = spans ? (size_t)span * sizeof(float) : 0;
+  const int parts = a.xpieces ? a.T * (int)cdiv(a.d_in, 128) * 16 : 0;
+  const size_t smem = spans ? (size_t)span_at(span) * sizeof(float) : 0;
   auto kernel = decode_prepare_kernel<BITS, T>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 32768 * 4);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, span_at(32768) * 4);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)(spans + cdiv(parts, kPrepThreads)), kPrepThreads, smem, s>>>(
       a, logn, span, spans, (float)(1.0 / sqrt((double)n)), static_cast<T *>(z_out));
@@ -142,15 +374,7 @@ cudaError_t prepare(const GemvArgs &a, int logn, void *z_out, cudaStream_t s) {
 
 }  // namespace
 
-int decode_tokens_padded(int64_t T) {
-  int tp = 1;
-  while (tp < T) tp *= 2;
-  return tp;
-}
-
 bool gemv_on_tensor_cores(const uint8_t *qw, int group) { return qw && group % 32 == 0; }
-
-bool gemv_prepares_x(const GemvArgs &a) { return a.xpieces; }
 
 namespace {
 int pieces_of(bool f32) { return f32 ? 3 : 1; }
@@ -169,6 +393,28 @@ void gemv_place_x(GemvArgs *a, void *ws) {
   a->pieces = pieces_of(a->f32);
   a->xpieces = static_cast<uint4 *>(ws);
   a->xsums = reinterpret_cast<float2 *>(static_cast<char *>(ws) + xpieces_bytes(a->d_in, a->T, a->f32));
+}
+
+namespace {
+// Tokens of a group: as many as there are up to two, then four (a 16-byte gather) or eight.
+int group_tokens(int64_t T) { return T <= 2 ? (int)T : T <= 4 ? 4 : 8; }
+}  // namespace
+
+size_t gemv_z_bytes(int32_t d_out, int32_t d_in, int64_t T) {
+  if (T <= 0) return 0;
+  const size_t tp = cdiv(T, group_tokens(T)) * group_tokens(T);
+  return align_up(tp * d_in * 4, 256) + align_up(tp * d_out * 4, 256);
+}
+
+void gemv_place_z(GemvArgs *a, void *ws) {
+  a->tg = group_tokens(a->T);
+  a->tp = (a->T + a->tg - 1) / a->tg * a->tg;
+  a->zt = static_cast<float *>(ws);
+  a->y_ad = reinterpret_cast<float *>(static_cast<char *>(ws) + align_up((size_t)a->tp * a->d_in * 4, 256));
+}
+
+cudaError_t launch_decode_entries(const GemvArgs &a, cudaStream_t s) {
+  return a.tg == 1 ? entries<1>(a, s) : a.tg == 2 ? entries<2>(a, s) : a.tg == 4 ? entries<4>(a, s) : entries<8>(a, s);
 }
 
 cudaError_t launch_decode_prepare(const GemvArgs &a, int logn, void *z_out, cudaStream_t s) {

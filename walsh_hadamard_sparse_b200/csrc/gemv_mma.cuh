@@ -116,48 +116,6 @@ __device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Entries of one row of E against the transformed tokens t0 .. t0 + np - 1:
-// VW tokens to a lane, lpe lanes to an entry; the sums of the row land in
-// sp[0 .. np). The order of the additions depends on the sizes alone.
-template <int VW>
-__device__ __forceinline__ void sparse_row(const GemvArgs &a, const float *z, int row, int t0, int np, int lpe,
-                                           int lane, float *sp) {
-  const int e0 = lane / lpe, tq = (lane % lpe) * VW;
-  const bool on = tq < np;
-  float acc[VW];
-#pragma unroll
-  for (int i = 0; i < VW; ++i) acc[i] = 0.f;
-  int64_t b = a.row_ptr[row], e = a.row_ptr[row + 1];
-  if (b < 0) b = 0;
-  if (e > a.p) e = a.p;
-  const int step = 32 / lpe;
-  if (on) {
-#pragma unroll 4
-    for (int64_t j = b + e0; j < e; j += step) {
-      const int k = a.col_idx[j];
-      const float c = a.coef[j];
-      if ((unsigned)k >= (unsigned)a.d_in) continue;
-      const float *src = z + (int64_t)k * a.tp + t0 + tq;
-      if constexpr (VW == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(src);
-        acc[0] = fmaf(c, v.x, acc[0]), acc[1] = fmaf(c, v.y, acc[1]);
-        acc[2] = fmaf(c, v.z, acc[2]), acc[3] = fmaf(c, v.w, acc[3]);
-      } else if constexpr (VW == 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(src);
-        acc[0] = fmaf(c, v.x, acc[0]), acc[1] = fmaf(c, v.y, acc[1]);
-      } else {
-        acc[0] = fmaf(c, *src, acc[0]);
-      }
-    }
-  }
-  for (int o = lpe; o < 32; o <<= 1)
-#pragma unroll
-    for (int i = 0; i < VW; ++i) acc[i] += __shfl_xor_sync(~0u, acc[i], o);
-  if (e0 == 0 && on)
-#pragma unroll
-    for (int i = 0; i < VW; ++i) sp[tq + i] = acc[i];
-}
-
 // One row and token by the definition, for results the fast path leaves NaN: a
 // chunk with an infinity or a NaN has no pieces (its factor is NaN).
 static __device__ __noinline__ float plain_dot(const GemvArgs &a, int row, int tok) {
@@ -312,7 +270,7 @@ __device__ __forceinline__ void load_run(const uint8_t *p, uint32_t *w) {
 // EXACT: the group is 128 / G columns, so a chunk's groups follow the chunk.
 template <int BITS, int G, int NT, int MT, int DEPTH, bool EXACT>
 __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
-    gemv_mma_kernel(const GemvArgs a, int tokens_per_pass, int slices, int z_floats) {
+    gemv_mma_kernel(const GemvArgs a, int tokens_per_pass, int slices) {
   constexpr int TPN = 8 / G, ROWS = 16 * MT, ROW_CHUNK = 16 * BITS;
   extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -367,7 +325,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
     }
   each<DEPTH>([&](auto I) { fetch(buf[decltype(I)::value], c_begin + decltype(I)::value, I); });
 
-  // the values and Z are the preparing launch's outputs: wait for it only here
+  // the values (and the entries' sums) are outputs of the launches before: wait for them only here
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int pieces = a.pieces, v_end = np * pieces, v_most = tokens_per_pass * pieces;
   const int n_tiles = x_tiles(a.T * pieces, G), nt0 = t0 * pieces / TPN;
@@ -440,10 +398,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
     });
   }
 
-  const int spw = (tokens_per_pass + 3) & ~3;
-  float *red = smem;                                // [kWarps][G][v_most][ROWS]: the warps' sums
-  float *sp = red + kWarps * G * v_most * ROWS;     // [tiles_here * ROWS][spw]: the entries' sums
-  float *zs = sp + kWarps * ROWS * spw;             // [z_floats]
+  float *red = smem;  // [kWarps][G][v_most][ROWS]: the warps' sums
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     if (NT > 1 && n * TPN >= v_end) break;
@@ -456,24 +411,6 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
         if (v + j < v_end) dst[j * ROWS + m * 16] = acc[m][n][j], dst[j * ROWS + m * 16 + 8] = acc[m][n][2 + j];
   }
   const int rows_here = tiles_here * ROWS < a.d_out - row_first ? tiles_here * ROWS : a.d_out - row_first;
-  if (a.row_ptr) {
-    const float *z = a.zt;
-    if (z_floats) {
-      for (int i = threadIdx.x * 4; i < z_floats; i += blockDim.x * 4)
-        *reinterpret_cast<float4 *>(zs + i) = *reinterpret_cast<const float4 *>(a.zt + i);
-      __syncthreads();
-      z = zs;
-    }
-    const int al = gridDim.y == 1 ? 0 : tokens_per_pass;  // passes start at its multiples
-    int vw = a.tp < 4 ? a.tp : 4, lpe = 1;
-    while (al % vw) vw /= 2;
-    while (lpe * vw < np) lpe *= 2;
-    for (int r = warp; r < rows_here; r += kWarps) {
-      if (vw == 4) sparse_row<4>(a, z, row_first + r, t0, np, lpe, lane, sp + r * spw);
-      else if (vw == 2) sparse_row<2>(a, z, row_first + r, t0, np, lpe, lane, sp + r * spw);
-      else sparse_row<1>(a, z, row_first + r, t0, np, lpe, lane, sp + r * spw);
-    }
-  }
   __syncthreads();
   for (int i = threadIdx.x; i < tiles_here * ROWS * np; i += blockDim.x) {
     const int r = i % (tiles_here * ROWS), tok = i / (tiles_here * ROWS);
@@ -484,7 +421,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
       for (int w = 0; w < slices * G; ++w) sum += src[(w * v_most + v) * ROWS];
     sum *= 0x1p12f;  // the rest of the codes' unit
     if (sum != sum) sum = plain_dot(a, row_first + r, t0 + tok);
-    if (a.row_ptr) sum += a.alpha * sp[r * spw + tok];
+    if (a.y_ad) sum += a.alpha * a.y_ad[(int64_t)(row_first + r) * a.tp + t0 + tok];
     const int64_t at = (int64_t)(t0 + tok) * a.d_out + row_first + r;
     if (a.f32) static_cast<float *>(a.y)[at] = sum;
     else static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(sum);
@@ -495,17 +432,13 @@ template <int BITS, int G, int NT, int MT, int DEPTH, bool EXACT>
 cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   constexpr int TPN = 8 / G, cols = NT * TPN, ROWS = 16 * MT;
   int tpp = cols / a.pieces;
-  // a further pass starts with an n-tile, and where a vector of the entries' tokens does
-  if (tpp < a.T) tpp = std::max(tpp & ~(TPN - 1) & ~3, tpp & ~(TPN - 1) & ~1);
+  if (tpp < a.T) tpp &= ~(TPN - 1);  // a further pass starts with an n-tile
   else tpp = a.T;
   // slices of the columns: as many as it takes to give every SM sixteen warps, two chunks a warp at least
   const int64_t tiles = cdiv(a.d_out, ROWS), chunks = cdiv(a.d_in, 128);
   int slices = 1;
   while (slices < kWarps && tiles * slices < (int64_t)sm_count() * 12 && chunks >= 2 * slices) slices *= 2;
-  size_t smem = sizeof(float) * ((size_t)kWarps * G * tpp * a.pieces * ROWS + kWarps * ROWS * ((tpp + 3) & ~3));
-  const int64_t z_all = a.row_ptr ? (int64_t)a.d_in * a.tp : 0;
-  const int z_floats = smem + z_all * 4 <= 96 * 1024 ? (int)z_all : 0;
-  smem += (size_t)z_floats * 4;
+  size_t smem = sizeof(float) * (size_t)kWarps * G * tpp * a.pieces * ROWS;
   auto kernel = gemv_mma_kernel<BITS, G, NT, MT, DEPTH, EXACT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -519,7 +452,7 @@ cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = a.prepared ? 1 : 0;  // overlaps the preparing launch
-  return cudaLaunchKernelEx(&cfg, kernel, a, tpp, slices, z_floats);
+  return cudaLaunchKernelEx(&cfg, kernel, a, tpp, slices);
 }
 
 template <int BITS, int G, bool EXACT>

@@ -148,10 +148,11 @@ cudaError_t launch_weff(const qwha_adapter *a, const qwha_qweight *wq, float alp
 
 namespace qwha {
 
-// Products with the packed weight for a few tokens (gemv.cu). qw NULL: no base
-// term; row_ptr NULL: no adapter term. zt: fp32 [d_in][tp]; xpieces, xsums: the
-// tokens for the tensor cores (gemv_on_tensor_cores); all three written by the
-// launch_decode_prepare that precedes the product on its stream.
+// Products with the packed weight for a few tokens (gemv.cu). A call is up to
+// three launches on one stream, each overlapping the one before: the tokens'
+// operands and transform (launch_decode_prepare), the entries of E
+// (launch_decode_entries), the product (launch_gemv). qw NULL: no base term;
+// row_ptr NULL: no adapter term.
 struct GemvArgs {
   const uint8_t *qw;
   const float *scales;
@@ -164,25 +165,26 @@ struct GemvArgs {
   const float *coef;
   int64_t p;
   float alpha;
-  float *zt;
-  int tp;
-  // The values as operands, `pieces` columns a token, C = T * pieces rounded up to even: xpieces [chunk of 128
-  // columns][C][4 runs][4] of 16 bytes, xsums [chunk][groups in it][C] (sum, factor) pairs. Where each CTA of the
-  // product makes them itself (gemv_prepares_x false) they are not read.
+  // Z = X H in fp32 by groups of tg tokens: zt [tp / tg][d_in][tg]; the entries' sums y_ad [d_out][tp].
+  float *zt, *y_ad;
+  int tg, tp;
+  // The values as operands, `pieces` columns a token, TPN = 8 / G columns to an n-tile (G groups in a chunk of 128
+  // columns): xpieces [chunk][n-tile][4][TPN][4 runs] of 16 bytes, xsums [chunk][n-tile][8] (sum, factor) pairs.
   int pieces;
   uint4 *xpieces;
   float2 *xsums;
-  int prepared;  // a launch_decode_prepare precedes the product
+  int prepared;  // another launch of the call precedes the product
 };
 __host__ __device__ constexpr int x_tiles(int cols, int G) { return (cols * G + 7) / 8; }
-bool gemv_prepares_x(const GemvArgs &a);
-int decode_tokens_padded(int64_t T);  // tp: the next power of two
 bool gemv_on_tensor_cores(const uint8_t *qw, int group);
-// Workspace of the operands of T tokens, and where in it they lie.
+// Workspaces, and where in them the arrays lie.
 size_t gemv_x_bytes(int32_t d_in, int64_t T, bool f32);
 void gemv_place_x(GemvArgs *a, void *ws);
+size_t gemv_z_bytes(int32_t d_out, int32_t d_in, int64_t T);
+void gemv_place_z(GemvArgs *a, void *ws);
 // Fills a.zt (if set), a.xpieces and a.xsums (if set) and z_out (if not NULL) from a.x.
 cudaError_t launch_decode_prepare(const GemvArgs &a, int logn, void *z_out, cudaStream_t s);
+cudaError_t launch_decode_entries(const GemvArgs &a, cudaStream_t s);
 cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s);
 // Its tensor-core kernels (gemv_mma.cuh).
 cudaError_t launch_gemv_b2(const GemvArgs &a, cudaStream_t s);
