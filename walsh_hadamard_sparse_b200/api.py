@@ -8,7 +8,7 @@ allocator and is passed to the library as the `ws` argument.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass, fields
+from dataclasses import dataclass
 
 import torch
 
@@ -38,6 +38,10 @@ def _ptr(t) -> ctypes.c_void_p | None:
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("expected a contiguous CUDA tensor")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _addr(t) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _stream() -> ctypes.c_void_p:
@@ -71,15 +75,10 @@ class Adapter:
     weff: torch.Tensor | None = None  # dense: W_eff kept from the forward for the backward
 
     def c_struct(self) -> QwhaAdapter:
-        s = QwhaAdapter()
-        s.d_in, s.d_out, s.had_block, s.p = self.d_in, self.d_out, self.had_block, self.p
-        s.algo = ALGO[self.algo]
-        for f in fields(self):
-            if f.name in ("d_in", "d_out", "had_block", "p", "algo"):
-                continue
-            v = getattr(self, f.name)
-            setattr(s, f.name, None if v is None else v.data_ptr())
-        return s
+        return QwhaAdapter(self.d_in, self.d_out, self.had_block, ALGO[self.algo], self.p, _addr(self.row_ptr),
+                           _addr(self.col_idx), _addr(self.coef), _addr(self.col_ptr), _addr(self.row_idx),
+                           _addr(self.perm), _addr(self.tile_ptr), _addr(self.tile_pos), _addr(self.tile_rk),
+                           _addr(self.weff))
 
 
 @dataclass
@@ -93,10 +92,8 @@ class QWeight:
     zeros: torch.Tensor
 
     def c_struct(self) -> QwhaQweight:
-        s = QwhaQweight()
-        s.bits, s.group = self.bits, self.group
-        s.qweight, s.scales, s.zeros = self.qweight.data_ptr(), self.scales.data_ptr(), self.zeros.data_ptr()
-        return s
+        return QwhaQweight(self.bits, self.group, self.qweight.data_ptr(), self.scales.data_ptr(),
+                           self.zeros.data_ptr())
 
 
 def workspace_size(op: int, d_out: int, d_in: int, p: int, T: int, with_base: bool | int) -> int:
@@ -161,50 +158,55 @@ def adapter_bwd(a: Adapter, dY: torch.Tensor, Z: torch.Tensor, alpha: float = 1.
     return (dc if want_dc else None), (dX if want_dx else None)
 
 
-def _same_device(*tensors) -> None:
-    """Work goes to the current device's current stream: every tensor of the call has to live there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{dev}")
+# The serving calls take microseconds on the GPU, so their checks build no message, tuple or wrapper they do not need.
 
 
-def _base(X: torch.Tensor) -> int:
-    """with_base of a decode workspace: the operands of fp32 tokens are larger."""
-    return 2 if X.dtype == torch.float32 else 1
+def _fit(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    """The address of a tensor of a serving call: of this type and shape, contiguous, on the current device (whose
+    current stream the work goes to)."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    return t.data_ptr()
 
 
-def _check_weight(wq: QWeight, d_out: int, d_in: int) -> None:
+def _fit_ws(ws: torch.Tensor, dev: int) -> int:
+    if not ws.is_cuda or not ws.is_contiguous() or ws.get_device() != dev:
+        raise ValueError(f"ws: expected a contiguous tensor on cuda:{dev}")
+    return ws.data_ptr()
+
+
+def _fit_weight(wq: QWeight, d_out: int, d_in: int, dev: int) -> QwhaQweight:
     groups = d_in // wq.group if wq.group > 0 else 0
-    for name, t, dtype, shape in (("qweight", wq.qweight, torch.uint8, (d_out, d_in * wq.bits // 8)),
-                                  ("scales", wq.scales, torch.float32, (d_out, groups)),
-                                  ("zeros", wq.zeros, torch.uint8, (d_out, groups))):
-        if t.dtype != dtype or tuple(t.shape) != shape:
-            raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    return QwhaQweight(wq.bits, wq.group, _fit("qweight", wq.qweight, torch.uint8, (d_out, d_in * wq.bits // 8), dev),
+                       _fit("scales", wq.scales, torch.float32, (d_out, groups), dev),
+                       _fit("zeros", wq.zeros, torch.uint8, (d_out, groups), dev))
 
 
-def _check_out(name: str, t: torch.Tensor, like: torch.Tensor, shape: tuple) -> None:
-    if t.dtype != like.dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected {like.dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+def _raw_stream(dev: int) -> int:
+    """The current stream's handle, without the wrapper object where this torch hands it out."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(dev) if get is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def qgemv(wq: QWeight, X: torch.Tensor, Y: torch.Tensor | None = None,
           ws: torch.Tensor | None = None) -> torch.Tensor:
     """Y = X W_Q^T for up to DECODE_MAX_T tokens X [T, d_in] (fp32 or bf16), straight from the packed weight; products
     of the exact q - zeros, fp32 sums, one rounding."""
+    h, dev, dt = lib(), torch.cuda.current_device(), _dt(X)
     T, d_in = X.shape
     d_out = wq.scales.shape[0]
-    _check_weight(wq, d_out, d_in)
+    x = _fit("X", X, X.dtype, (T, d_in), dev)
+    cw = _fit_weight(wq, d_out, d_in, dev)
     if Y is None:
-        Y = torch.empty((T, d_out), dtype=X.dtype, device=X.device)
-    else:
-        _check_out("Y", Y, X, (T, d_out))
-    _same_device(X, Y, ws, wq.qweight, wq.scales, wq.zeros)
+        Y = X.new_empty((T, d_out))
     if ws is None:
-        ws = _ws(workspace_size(OP_QGEMV, d_out, d_in, 0, T, _base(X)), X.device)
-    cw = wq.c_struct()
-    check(lib().qwha_qgemv(ctypes.byref(cw), d_out, d_in, _dt(X), _ptr(X), T, _ptr(Y), _ptr(ws),
-                           0 if ws is None else ws.numel(), _stream()), "qwha_qgemv")
+        ws = X.new_empty(h.qwha_workspace_size(OP_QGEMV, d_out, d_in, 0, T, 2 - dt), dtype=torch.uint8)
+    check(h.qwha_qgemv(cw, d_out, d_in, dt, x, T, _fit("Y", Y, X.dtype, (T, d_out), dev), _fit_ws(ws, dev), ws.numel(),
+                       _raw_stream(dev)), "qwha_qgemv")
     return Y
 
 
@@ -214,29 +216,24 @@ def adapter_decode(a: Adapter, X: torch.Tensor, alpha: float = 1.0, wq: QWeight 
     """Y = X W_Q^T + alpha (X H) F^T for up to DECODE_MAX_T tokens X [T, d_in] (fp32 or bf16; W_Q term only with wq):
     the forward of a decode step, straight from the packed weight. Only the CSR arrays of `a` are read. Z_out, if
     given, receives X H in X's dtype for adapter_bwd."""
-    T, d_in = X.shape
-    if d_in != a.d_in:
-        raise ValueError(f"X has {d_in} columns, the adapter {a.d_in}")
+    h, dev, dt = lib(), torch.cuda.current_device(), _dt(X)
+    T, d_out, d_in = X.shape[0], a.d_out, a.d_in
+    x = _fit("X", X, X.dtype, (T, d_in), dev)
+    if a.col_idx.shape[0] < a.p or a.coef.shape[0] < a.p:
+        raise ValueError(f"col_idx and coef hold {a.col_idx.shape[0]} and {a.coef.shape[0]} entries, p is {a.p}")
+    cs = QwhaAdapter(d_in, d_out, a.had_block, 0, a.p, _fit("row_ptr", a.row_ptr, torch.int32, (d_out + 1,), dev),
+                     _fit("col_idx", a.col_idx, torch.int32, a.col_idx.shape, dev),
+                     _fit("coef", a.coef, torch.float32, a.coef.shape, dev))
+    cw = None if wq is None else _fit_weight(wq, d_out, d_in, dev)
     if Y is None:
-        Y = torch.empty((T, a.d_out), dtype=X.dtype, device=X.device)
-    else:
-        _check_out("Y", Y, X, (T, a.d_out))
-    if Z_out is not None:
-        _check_out("Z_out", Z_out, X, (T, d_in))
-    _same_device(X, Y, Z_out, ws, a.row_ptr, a.col_idx, a.coef)
-    cw = None
-    if wq is not None:
-        _check_weight(wq, a.d_out, d_in)
-        _same_device(wq.qweight, wq.scales, wq.zeros)
-        cw = wq.c_struct()
+        Y = X.new_empty((T, d_out))
     if ws is None:
-        need = workspace_size(OP_DECODE, a.d_out, a.d_in, a.p, T, 0 if wq is None else _base(X))
-        ws = _ws(need, X.device)
-    cs = a.c_struct()
-    rc = lib().qwha_adapter_decode(ctypes.byref(cs), ctypes.byref(cw) if cw is not None else None, _dt(X), _ptr(X), T,
-                                   float(alpha), _ptr(Z_out), _ptr(Y), _ptr(ws), 0 if ws is None else ws.numel(),
-                                   _stream())
-    check(rc, "qwha_adapter_decode")
+        ws = X.new_empty(h.qwha_workspace_size(OP_DECODE, d_out, d_in, a.p, T, 0 if cw is None else 2 - dt),
+                         dtype=torch.uint8)
+    check(h.qwha_adapter_decode(cs, cw, dt, x, T, alpha,
+                                None if Z_out is None else _fit("Z_out", Z_out, X.dtype, (T, d_in), dev),
+                                _fit("Y", Y, X.dtype, (T, d_out), dev), _fit_ws(ws, dev), ws.numel(), _raw_stream(dev)),
+          "qwha_adapter_decode")
     return Y
 
 
@@ -266,19 +263,16 @@ class QCache:
     def n_slots(self) -> int:
         return self.scales.shape[0] * self.scales.shape[1]
 
-    def c_struct(self) -> QwhaCache:
+    def c_struct(self, dev: int | None = None) -> QwhaCache:
+        dev = torch.cuda.current_device() if dev is None else dev
         if self.scales.dim() != 4:
             raise ValueError(f"scales: expected 4 dimensions, got {tuple(self.scales.shape)}")
         n_pages, page_size, heads, groups = self.scales.shape
         head_dim = groups * self.group
-        for name, t, dtype, width in (("codes", self.codes, torch.uint8, head_dim * self.bits // 8),
-                                      ("scales", self.scales, torch.float32, groups),
-                                      ("zeros", self.zeros, torch.uint8, groups)):
-            if t.dtype != dtype or tuple(t.shape) != (n_pages, page_size, heads, width):
-                raise ValueError(f"{name}: expected {dtype} {(n_pages, page_size, heads, width)}, got {t.dtype} "
-                                 f"{tuple(t.shape)}")
         return QwhaCache(self.bits, self.group, self.had_block, heads, head_dim, page_size, n_pages,
-                         _ptr(self.codes), _ptr(self.scales), _ptr(self.zeros))
+                         _fit("codes", self.codes, torch.uint8, (n_pages, page_size, heads, head_dim * self.bits // 8), dev),
+                         _fit("scales", self.scales, torch.float32, self.scales.shape, dev),
+                         _fit("zeros", self.zeros, torch.uint8, self.scales.shape, dev))
 
 
 def cache_alloc(n_pages: int, page_size: int, heads: int, head_dim: int, bits: int = 4, group: int | None = None,
@@ -292,26 +286,30 @@ def cache_alloc(n_pages: int, page_size: int, heads: int, head_dim: int, bits: i
                   torch.zeros(rows + (head_dim // group,), dtype=torch.uint8, device=device))
 
 
+_CACHES = (None, QwhaCache * 1, QwhaCache * 2)
+_ROWS = (None, P * 1, P * 2)
+
+
 def _caches(caches) -> tuple:
-    return (caches,) if isinstance(caches, QCache) else tuple(caches)
+    cs = (caches,) if isinstance(caches, QCache) else tuple(caches)
+    if not 1 <= len(cs) <= 2:
+        raise ValueError(f"{len(cs)} caches: one or two")
+    return cs
 
 
 def cache_write(caches, rows, slots: torch.Tensor) -> None:
     """Quantize rows [n, heads, head_dim] (fp32 or bf16) into the slots [n] (int64, distinct; -1 skips a row) of a
     cache; with a pair of caches and a pair of rows (keys and values) both in one launch."""
-    cs = _caches(caches)
+    cs, dev, m = _caches(caches), torch.cuda.current_device(), slots.shape[0]
     rs = (rows,) if isinstance(rows, torch.Tensor) else tuple(rows)
-    n = slots.shape[0]
-    if len(cs) != len(rs) or not 1 <= len(cs) <= 2:
-        raise ValueError(f"{len(cs)} caches and {len(rs)} row tensors: one or two of each")
-    if slots.dtype != torch.int64 or slots.dim() != 1:
-        raise ValueError("slots: expected an int64 vector")
-    for c, r in zip(cs, rs):
-        _check_out("rows", r, rs[0], (n, c.heads, c.head_dim))
-        _same_device(r, slots, c.codes, c.scales, c.zeros)
-    rc = lib().qwha_cache_write((QwhaCache * len(cs))(*(c.c_struct() for c in cs)), len(cs), _dt(rs[0]),
-                                (P * len(rs))(*(_ptr(r) for r in rs)), _ptr(slots), n, _stream())
-    check(rc, "qwha_cache_write")
+    k = len(cs)
+    if k != len(rs):
+        raise ValueError(f"{k} caches and {len(rs)} row tensors: one or two of each")
+    dtype = rs[0].dtype
+    structs = _CACHES[k](*(c.c_struct(dev) for c in cs))
+    ptrs = _ROWS[k](*(_fit("rows", r, dtype, (m, c.heads, c.head_dim), dev) for c, r in zip(structs, rs)))
+    check(lib().qwha_cache_write(structs, k, _dt(rs[0]), ptrs, _fit("slots", slots, torch.int64, (m,), dev), m,
+                                 _raw_stream(dev)), "qwha_cache_write")
 
 
 def cache_read(caches, pages: torch.Tensor, row_start: torch.Tensor, n: int, first: torch.Tensor | None = None,
@@ -320,40 +318,33 @@ def cache_read(caches, pages: torch.Tensor, row_start: torch.Tensor, n: int, fir
     Rows row_start[b] .. row_start[b+1] (int64 [n_seqs+1]) are the tokens first[b], first[b]+1, ... (int64 [n_seqs];
     None: 0) of sequence b, whose token t lies in page pages[b, t // page_size] (int32 [n_seqs, max_pages]). Rows from
     row_start[-1] on are left as they were (they are not initialised without `out`)."""
-    cs = _caches(caches)
-    if not 1 <= len(cs) <= 2:
-        raise ValueError(f"{len(cs)} caches: one or two")
+    cs, dev = _caches(caches), torch.cuda.current_device()
     n_seqs, max_pages = pages.shape
-    for name, t, want, shape in (("pages", pages, torch.int32, (n_seqs, max_pages)),
-                                 ("row_start", row_start, torch.int64, (n_seqs + 1,)),
-                                 ("first", first, torch.int64, (n_seqs,))):
-        if t is not None and (t.dtype != want or tuple(t.shape) != shape):
-            raise ValueError(f"{name}: expected {want} {shape}, got {t.dtype} {tuple(t.shape)}")
+    k = len(cs)
+    structs = _CACHES[k](*(c.c_struct(dev) for c in cs))
     if out is None:
-        outs = tuple(torch.empty((n, c.heads, c.head_dim), dtype=dtype, device=pages.device) for c in cs)
+        outs = tuple(torch.empty((n, c.heads, c.head_dim), dtype=dtype, device=pages.device) for c in structs)
     else:
         outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
-        if len(outs) != len(cs):
-            raise ValueError(f"{len(cs)} caches and {len(outs)} outputs")
-    for c, o in zip(cs, outs):
-        _check_out("out", o, outs[0], (n, c.heads, c.head_dim))
-        _same_device(o, pages, row_start, first, c.codes, c.scales, c.zeros)
-    rc = lib().qwha_cache_read((QwhaCache * len(cs))(*(c.c_struct() for c in cs)), len(cs), _dt(outs[0]), _ptr(pages),
-                               max_pages, _ptr(row_start), _ptr(first), n_seqs, (P * len(outs))(*(_ptr(o) for o in outs)),
-                               n, _stream())
-    check(rc, "qwha_cache_read")
+        if len(outs) != k:
+            raise ValueError(f"{k} caches and {len(outs)} outputs")
+        dtype = outs[0].dtype
+    ptrs = _ROWS[k](*(_fit("out", o, dtype, (n, c.heads, c.head_dim), dev) for c, o in zip(structs, outs)))
+    check(lib().qwha_cache_read(structs, k, _dt(outs[0]), _fit("pages", pages, torch.int32, (n_seqs, max_pages), dev),
+                                max_pages, _fit("row_start", row_start, torch.int64, (n_seqs + 1,), dev),
+                                None if first is None else _fit("first", first, torch.int64, (n_seqs,), dev), n_seqs,
+                                ptrs, n, _raw_stream(dev)), "qwha_cache_read")
     return outs[0] if isinstance(caches, QCache) else outs
 
 
 def validate_slots(cache: QCache, slots: torch.Tensor, ws: torch.Tensor | None = None) -> None:
     """Raise QwhaError unless every slot is -1 or within the cache and no slot is named twice (synchronises)."""
-    if slots.dtype != torch.int64 or slots.dim() != 1:
-        raise ValueError("slots: expected an int64 vector")
-    _same_device(slots, cache.codes)
+    dev = torch.cuda.current_device()
+    p = _fit("slots", slots, torch.int64, (slots.shape[0],), dev)
+    cs = cache.c_struct(dev)
     ws = _ws(workspace_size(OP_SLOTS, 1, 1, cache.n_slots, 0, False), slots.device) if ws is None else ws
-    cs = cache.c_struct()
-    check(lib().qwha_validate_slots(ctypes.byref(cs), _ptr(slots), slots.shape[0], _ptr(ws),
-                                    0 if ws is None else ws.numel(), _stream()), "qwha_validate_slots")
+    check(lib().qwha_validate_slots(cs, p, slots.shape[0], _fit_ws(ws, dev), ws.numel(), _raw_stream(dev)),
+          "qwha_validate_slots")
 
 
 def dp_backward(a: Adapter, dY: torch.Tensor, Z: torch.Tensor, alpha: float = 1.0, wq: QWeight | None = None,

@@ -58,6 +58,15 @@ int sm_count() {
   return counts[dev];
 }
 
+cudaError_t allow_smem(const void *kernel, size_t bytes, std::atomic<size_t> (&allowed)[64]) {
+  std::atomic<size_t> &most = allowed[device_slot()];
+  if (bytes <= 48 * 1024 || bytes <= most.load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  // a smaller size set by another thread afterwards would only make this one ask again, so keep the smaller record
+  if (e == cudaSuccess) most.store(bytes, std::memory_order_relaxed);
+  return e;
+}
+
 int device_slot() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qwha.h"
 
 namespace qwha {
@@ -27,6 +29,10 @@ inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 int sm_count();  // multiprocessors of the current device
 int device_slot();  // index of the current device in [0, 64) (0 if unreadable), for per-device caches
+
+// Let `kernel` have `bytes` of dynamic shared memory on the current device: asked for once per kernel, size and device
+// (a launch of at most 48 KB needs no asking). `allowed` is the kernel's own record, one per device slot.
+cudaError_t allow_smem(const void *kernel, size_t bytes, std::atomic<size_t> (&allowed)[64]);
 
 // Device error word for bounded waits (set by kernels, read by
 // qwha_check_stream_status). One per device, in __device__ memory.

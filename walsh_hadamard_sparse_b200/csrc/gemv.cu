@@ -338,7 +338,8 @@ cudaError_t entries(const GemvArgs &a, cudaStream_t s) {
   const size_t group_bytes = (size_t)a.d_in * TG * sizeof(float);
   const int buffers = 2 * group_bytes <= kEntSmem && a.tp > TG ? 2 : group_bytes <= kEntSmem ? 1 : 0;
   auto kernel = decode_entries_kernel<TG>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kEntSmem);
+  static std::atomic<size_t> allowed[64];
+  const cudaError_t e = allow_smem((const void *)kernel, buffers * group_bytes, allowed);
   if (e != cudaSuccess) return e;
   unsigned int *err = device_error_word();
   if (!err) return cudaErrorInvalidDevicePointer;
@@ -365,7 +366,8 @@ cudaError_t prepare(const GemvArgs &a, int logn, void *z_out, cudaStream_t s) {
   const int parts = a.xpieces ? a.T * (int)cdiv(a.d_in, 128) * 16 : 0;
   const size_t smem = spans ? (size_t)span_at(span) * sizeof(float) : 0;
   auto kernel = decode_prepare_kernel<BITS, T>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, span_at(32768) * 4);
+  static std::atomic<size_t> allowed[64];
+  const cudaError_t e = allow_smem((const void *)kernel, smem, allowed);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)(spans + cdiv(parts, kPrepThreads)), kPrepThreads, smem, s>>>(
       a, logn, span, spans, (float)(1.0 / sqrt((double)n)), static_cast<T *>(z_out));

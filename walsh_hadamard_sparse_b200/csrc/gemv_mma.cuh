@@ -440,7 +440,8 @@ cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   while (slices < kWarps && tiles * slices < (int64_t)sm_count() * 12 && chunks >= 2 * slices) slices *= 2;
   size_t smem = sizeof(float) * (size_t)kWarps * G * tpp * a.pieces * ROWS;
   auto kernel = gemv_mma_kernel<BITS, G, NT, MT, DEPTH, EXACT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<size_t> allowed[64];
+  const cudaError_t e = allow_smem((const void *)kernel, smem, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cdiv(tiles, kWarps / slices), (unsigned)cdiv(a.T, tpp));
