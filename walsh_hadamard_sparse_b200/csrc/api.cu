@@ -1001,8 +1001,8 @@ qwha_status qwha_cache_read(const qwha_cache *caches, int32_t n_caches, qwha_dty
   QWHA_CHECK_PTR(row_start, "row_start");
   if (first) QWHA_CHECK_PTR(first, "first");
   StageScope sc(ST_CACHE_READ, 1, (cudaStream_t)stream);
-  return cuda_status(launch_cache_read(dt, cache_pair(caches, n_caches, rows), n_caches, pages, max_pages, row_start,
-                                       first, n_seqs, n, (cudaStream_t)stream),
+  const ReadArgs r = {pages, max_pages, n_seqs, row_start, first};
+  return cuda_status(launch_cache_read(dt, cache_pair(caches, n_caches, rows), n_caches, r, n, (cudaStream_t)stream),
                      "cache_read");
 }
 

@@ -147,123 +147,422 @@ __device__ __forceinline__ void load_run(const uint8_t *p, float *q, int bits) {
   for (int i = 0; i < 8; ++i) q[i] = (float)((w >> (bits * i)) & mask);
 }
 
-// Rows of up to 256 elements, eight to a lane: 1 << ll lanes hold a row.
+constexpr int kTileTokens = 32;  // tokens of a CTA's tile, at most
+
+// The (token, head) pairs of a tile, `step` apart: no division per pair.
+struct Walk {
+  int token, head, heads, step_tokens, step_heads;
+  __device__ __forceinline__ Walk(int first, int step, int heads_) : heads(heads_) {
+    token = first / heads, head = first - token * heads;
+    step_tokens = step / heads, step_heads = step - step_tokens * heads;
+  }
+  __device__ __forceinline__ void next() {
+    token += step_tokens, head += step_heads;
+    if (head >= heads) head -= heads, ++token;
+  }
+};
+
+// Slots of a tile of written rows: -1 where the row is skipped.
+__device__ __forceinline__ void write_slots(int64_t *slot, const qwha_cache &a, const int64_t *slots, int64_t t0, int n,
+                                            unsigned int *err) {
+  if (threadIdx.x < n) {
+    int64_t s = slots[t0 + threadIdx.x];
+    if (s < -1 || s >= a.n_pages * a.page_size) {
+      atomicOr(err, kErrSlot);
+      s = -1;
+    }
+    slot[threadIdx.x] = s;
+  }
+  __syncthreads();
+}
+
+// Slots of a tile of rows to read: output row i belongs to the sequence b with
+// row_start[b] <= i < row_start[b + 1] and is its token first[b] + i -
+// row_start[b]; -1 where the page table or the cache ends.
+__device__ __forceinline__ void read_slots(int64_t *slot, const qwha_cache &a, const ReadArgs &r, int64_t t0, int n,
+                                           unsigned int *err) {
+  if (threadIdx.x < n) {
+    const int64_t i = t0 + threadIdx.x;
+    int lo = 0, hi = r.n_seqs;  // row_start[lo] <= i < row_start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (r.row_start[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    const int64_t pos = i - r.row_start[lo] + (r.first ? r.first[lo] : 0), pg = pos / a.page_size;
+    int64_t page = -1;
+    if (pos >= 0 && pg < r.max_pages) page = r.pages[(int64_t)lo * r.max_pages + pg];
+    int64_t s = -1;
+    if (page < 0 || page >= a.n_pages) atomicOr(err, kErrPage);
+    else s = page * a.page_size + (pos - pg * a.page_size);
+    slot[threadIdx.x] = s;
+  }
+  __syncthreads();
+}
+
+// Scale, zero point and the factor of the codes of a group with range [lo, hi].
+template <typename A>
+struct Step {
+  float s;
+  A inv, z;
+  bool bad;
+  __device__ __forceinline__ Step(A lo, A hi, A qmax, A step, A half) {
+    s = (float)mul(add(hi, -lo), step);
+    bad = !(s <= 3.402823466e38f);
+    if (s < 1.1754943508e-38f) s = 1.f;
+    inv = (A)1 / (A)s;
+    z = floor(add(mul(-lo, inv), half));
+    z = z < qmax ? z : qmax;
+  }
+};
+
+// Any row of up to 256 elements, eight to a lane: 1 << ll lanes hold a row.
 template <typename T>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CachePair c, int ll,
                                                                     const int64_t *__restrict__ slots, int64_t n,
-                                                                    unsigned int *err) {
+                                                                    int tile, unsigned int *err) {
   using A = typename wide<T>::type;
+  __shared__ int64_t slot_s[kTileTokens];
   const qwha_cache &a = c.cache[blockIdx.y];
   const T *rows = static_cast<const T *>(c.rows[blockIdx.y]);
   const int lane = threadIdx.x & ((1 << ll) - 1);
   const bool has = lane * 8 < a.head_dim;
-  const int gl = a.group / 8, ng = a.head_dim / a.group;
+  const int gl = a.group / 8, ng = a.head_dim / a.group, group_at = lane / gl;
   const A qmax = (A)((1 << a.bits) - 1), step = (A)1 / qmax, unit = (A)c.unit[blockIdx.y], half = (A)(0.5 + 1.0 / 4096);
-  const int64_t items = n * a.heads, n_slots = a.n_pages * a.page_size;
-  const int64_t per = kCacheThreads >> ll;
-  for (int64_t base = (int64_t)blockIdx.x * per; base < items; base += (int64_t)gridDim.x * per) {
-    const int64_t it = base + (threadIdx.x >> ll);
-    bool live = it < items;
-    int64_t slot = -1;
-    if (live) slot = slots[it / a.heads];
-    if (slot < -1 || slot >= n_slots) {
-      if (lane == 0) atomicOr(err, kErrSlot);
-      slot = -1;
-    }
-    live = slot >= 0 && has;
-    A v[8];
+  for (int64_t t0 = (int64_t)blockIdx.x * tile; t0 < n; t0 += (int64_t)gridDim.x * tile) {
+    const int tokens = n - t0 < tile ? (int)(n - t0) : tile;
+    __syncthreads();  // the last tile's slots are read
+    write_slots(slot_s, a, slots, t0, tokens, err);
+    Walk w(threadIdx.x >> ll, kCacheThreads >> ll, a.heads);
+    // whole warps stay together: their pairs differ by less than the tile's last ones
+    for (int base = 0; base < tokens * a.heads; base += kCacheThreads >> ll, w.next()) {
+      const int64_t slot = w.token < tokens ? slot_s[w.token] : -1;
+      const bool live = slot >= 0 && has;
+      A v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0;
-    if (live) {
-      const T *src = rows + it * a.head_dim + lane * 8;
-      float f[8];
+      for (int i = 0; i < 8; ++i) v[i] = 0;
+      if (live) {
+        const T *src = rows + ((t0 + w.token) * a.heads + w.head) * a.head_dim + lane * 8;
+        float f[8];
 #pragma unroll
-      for (int u = 0; u < 8; u += io<T>::kVec) io<T>::unpack(*reinterpret_cast<const uint4 *>(src + u), f + u);
+        for (int u = 0; u < 8; u += io<T>::kVec) io<T>::unpack(*reinterpret_cast<const uint4 *>(src + u), f + u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = f[i];
-    }
-    rotate8(v, a.had_block, unit, lane);
-    A lo = 0, hi = 0;
+        for (int i = 0; i < 8; ++i) v[i] = f[i];
+      }
+      rotate8(v, a.had_block, unit, lane);
+      A lo = 0, hi = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lo = min_nan(lo, v[i]), hi = max_nan(hi, v[i]);
-    group_range(lo, hi, gl, lane);
-    float s = (float)mul(add(hi, -lo), step);
-    const bool bad = !(s <= 3.402823466e38f);
-    if (s < 1.1754943508e-38f) s = 1.f;
-    const A inv = (A)1 / (A)s;
-    const A zf = floor(add(mul(-lo, inv), half)), z = zf < qmax ? zf : qmax;
-    uint32_t q[8];
+      for (int i = 0; i < 8; ++i) lo = min_nan(lo, v[i]), hi = max_nan(hi, v[i]);
+      group_range(lo, hi, gl, lane);
+      const Step<A> g(lo, hi, qmax, step, half);
+      uint32_t q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const A r = add(mul(v[i], inv), z + half);
-      q[i] = bad || !(r > (A)0) ? 0u : r < qmax ? (uint32_t)r : (uint32_t)qmax;
-    }
-    if (live) {
-      const int64_t row = slot * a.heads + it % a.heads;
-      store_run(a.codes + row * (a.head_dim / 8 * a.bits) + lane * a.bits, q, a.bits);
-      if (lane % gl == 0) {
-        a.scales[row * ng + lane / gl] = bad ? __int_as_float(0x7fc00000) : s;
-        a.zeros[row * ng + lane / gl] = bad ? 0 : (uint8_t)z;
+      for (int i = 0; i < 8; ++i) {
+        const A r = add(mul(v[i], g.inv), g.z + half);
+        q[i] = g.bad || !(r > (A)0) ? 0u : r < qmax ? (uint32_t)r : (uint32_t)qmax;
+      }
+      if (live) {
+        const int64_t row = slot * a.heads + w.head;
+        store_run(a.codes + row * (a.head_dim / 8 * a.bits) + lane * a.bits, q, a.bits);
+        if (lane == group_at * gl) {
+          a.scales[row * ng + group_at] = g.bad ? __int_as_float(0x7fc00000) : g.s;
+          a.zeros[row * ng + group_at] = g.bad ? 0 : (uint8_t)g.z;
+        }
       }
     }
   }
 }
 
-// Output row i belongs to the sequence b with row_start[b] <= i <
-// row_start[b + 1] and is its token first[b] + i - row_start[b].
 template <typename T>
 __global__ void __launch_bounds__(kCacheThreads)
-    cache_read_kernel(const CachePair c, int ll, const int32_t *__restrict__ pages, int max_pages,
-                      const int64_t *__restrict__ row_start, const int64_t *__restrict__ first, int n_seqs, int64_t n,
-                      unsigned int *err) {
+    cache_read_kernel(const CachePair c, int ll, const ReadArgs r, int64_t n, int tile, unsigned int *err) {
+  __shared__ int64_t slot_s[kTileTokens];
   const qwha_cache &a = c.cache[blockIdx.y];
   T *rows = static_cast<T *>(const_cast<void *>(c.rows[blockIdx.y]));
   const int lane = threadIdx.x & ((1 << ll) - 1);
   const bool has = lane * 8 < a.head_dim;
-  const int ng = a.head_dim / a.group;
+  const int ng = a.head_dim / a.group, group_at = lane * 8 / a.group;
   const float unit = (float)c.unit[blockIdx.y];
-  const int64_t end = row_start[n_seqs];
-  const int64_t items = (end < n ? end : n) * a.heads;
-  const int64_t per = kCacheThreads >> ll;
-  for (int64_t base = (int64_t)blockIdx.x * per; base < items; base += (int64_t)gridDim.x * per) {
-    const int64_t it = base + (threadIdx.x >> ll);
-    const int64_t i = it / a.heads;
-    bool live = it < items;
-    int64_t slot = 0;
-    if (live) {
-      int lo = 0, hi = n_seqs;  // row_start[lo] <= i < row_start[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (row_start[mid] <= i) lo = mid;
-        else hi = mid;
+  const int64_t end = r.row_start[r.n_seqs], rows_n = end < n ? end : n;
+  for (int64_t t0 = (int64_t)blockIdx.x * tile; t0 < rows_n; t0 += (int64_t)gridDim.x * tile) {
+    const int tokens = rows_n - t0 < tile ? (int)(rows_n - t0) : tile;
+    __syncthreads();
+    read_slots(slot_s, a, r, t0, tokens, err);
+    Walk w(threadIdx.x >> ll, kCacheThreads >> ll, a.heads);
+    for (int base = 0; base < tokens * a.heads; base += kCacheThreads >> ll, w.next()) {
+      const int64_t slot = w.token < tokens ? slot_s[w.token] : -1;
+      const bool live = slot >= 0 && has;
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = 0.f;
+      if (live) {
+        const int64_t row = slot * a.heads + w.head;
+        load_run(a.codes + row * (a.head_dim / 8 * a.bits) + lane * a.bits, v, a.bits);
+        const float s = a.scales[row * ng + group_at], z = (float)a.zeros[row * ng + group_at];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = __fmul_rn(s, v[u] - z);
       }
-      const int64_t pos = i - row_start[lo] + (first ? first[lo] : 0);
-      const int64_t pg = pos / a.page_size;
-      int64_t page = -1;
-      if (pos >= 0 && pg < max_pages) page = pages[(int64_t)lo * max_pages + pg];
-      if (page < 0 || page >= a.n_pages) {
-        if (lane == 0) atomicOr(err, kErrPage);
-        live = false;
+      rotate8(v, a.had_block, unit, lane);
+      if (live) {
+        T *dst = rows + ((t0 + w.token) * a.heads + w.head) * a.head_dim + lane * 8;
+#pragma unroll
+        for (int u = 0; u < 8; u += io<T>::kVec) *reinterpret_cast<uint4 *>(dst + u) = io<T>::pack(v + u);
       }
-      slot = page * a.page_size + (pos - pg * a.page_size);
     }
-    live = live && has;
-    float v[8];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// bf16 rows of 64, 128 or 256 elements with power-of-two groups, the shapes that
+// move much data. Arithmetic and shuffles bound these kernels, not memory: at
+// 6.5 TB/s 2.6 bytes a value leave 14 instruction slots. So a lane holds
+// sixteen elements in two runs of eight, a row's halves apart (element = half
+// * hd / 2 + lane * 8 + i): five of the seven stages of 128 elements stay in
+// registers or between lanes with one shuffle a value, in the order 1, 2, 4
+// (registers), 8, 16, 32 (lanes), 64 (registers); adds, products and the
+// butterflies between lanes (p + sign * v, exact) run two to an instruction,
+// and codes become floats, and floats codes, by the exponent of 2^23.
+
+using f2 = unsigned long long;  // two fp32 values
+__device__ __forceinline__ f2 pack2(float a, float b) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(f2 v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 sub2(f2 a, f2 b) {
+  f2 d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// v[p], p = 0..7: elements (2p, 2p + 1) of the lane's sixteen (p < 4: first half).
+template <int LPH>
+__device__ __forceinline__ void rotate16(f2 *v, int had_block, int lane) {
+  if (had_block < 2) return;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = 0.f;
-    const int64_t row = slot * a.heads + it % a.heads;
-    if (live) {
-      load_run(a.codes + row * (a.head_dim / 8 * a.bits) + lane * a.bits, v, a.bits);
-      const int64_t g = row * ng + lane * 8 / a.group;
-      const float s = a.scales[g], z = (float)a.zeros[g];
+  for (int p = 0; p < 8; ++p) {  // stage 1, inside a pair
+    float a, b;
+    unpack2(v[p], a, b);
+    v[p] = pack2(a + b, a - b);
+  }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = __fmul_rn(s, v[u] - z);
+  for (int h = 1; h < 4; h *= 2)  // stages 2 and 4
+    if (had_block >= 4 * h)
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (!(p & h)) {
+          const f2 a = v[p], b = v[p + h];
+          v[p] = add2(a, b), v[p + h] = sub2(a, b);
+        }
+#pragma unroll
+  for (int o = 1; o < (1 << LPH); o *= 2)
+    if (had_block >= 16 * o) {
+      const float sign = lane & o ? -1.f : 1.f;
+      const f2 sg = pack2(sign, sign);
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        float a, b;
+        unpack2(v[p], a, b);
+        v[p] = fma2(v[p], sg, pack2(__shfl_xor_sync(~0u, a, o), __shfl_xor_sync(~0u, b, o)));
+      }
     }
-    rotate8(v, a.had_block, unit, lane);
-    if (live) {
-      T *dst = rows + it * a.head_dim + lane * 8;
+  if (had_block == (16 << LPH))
 #pragma unroll
-      for (int u = 0; u < 8; u += io<T>::kVec) *reinterpret_cast<uint4 *>(dst + u) = io<T>::pack(v + u);
+    for (int p = 0; p < 4; ++p) {
+      const f2 a = v[p], b = v[p + 4];
+      v[p] = add2(a, b), v[p + 4] = sub2(a, b);
+    }
+}
+
+// Eight codes as floats 2^23 + q (the codes' place in the mantissa), in pairs.
+template <int BITS>
+__device__ __forceinline__ void load_run16(const uint8_t *p, f2 *v) {
+  uint32_t q[8];
+  if constexpr (BITS == 8) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q[i] = __byte_perm(w.x, 0x4b000000u, 0x7440 + i), q[i + 4] = __byte_perm(w.y, 0x4b000000u, 0x7440 + i);
+  } else {
+    uint32_t w;
+    if constexpr (BITS == 4) w = *reinterpret_cast<const uint32_t *>(p);
+    else if constexpr (BITS == 2) w = *reinterpret_cast<const uint16_t *>(p);
+    else w = (uint32_t)p[0] | (uint32_t)p[1] << 8 | (uint32_t)p[2] << 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = ((w >> (BITS * i)) & ((1u << BITS) - 1u)) | 0x4b000000u;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pack2(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1]));
+}
+
+template <int BITS, int LPH>
+__global__ void __launch_bounds__(kCacheThreads)
+    cache_read16_kernel(const CachePair c, const ReadArgs r, int64_t n, int tile, unsigned int *err) {
+  constexpr int HD = 16 << LPH, LANES = 1 << LPH, PER = kCacheThreads >> LPH;
+  __shared__ int64_t slot_s[kTileTokens];
+  const qwha_cache &a = c.cache[blockIdx.y];
+  __nv_bfloat16 *rows = static_cast<__nv_bfloat16 *>(const_cast<void *>(c.rows[blockIdx.y]));
+  const int lane = threadIdx.x & (LANES - 1);
+  const int ng = HD / a.group, g0 = lane * 8 / a.group, g1 = (HD / 2 + lane * 8) / a.group;
+  const float unit = (float)c.unit[blockIdx.y];
+  const int64_t end = r.row_start[r.n_seqs], rows_n = end < n ? end : n;
+  for (int64_t t0 = (int64_t)blockIdx.x * tile; t0 < rows_n; t0 += (int64_t)gridDim.x * tile) {
+    const int tokens = rows_n - t0 < tile ? (int)(rows_n - t0) : tile;
+    __syncthreads();
+    read_slots(slot_s, a, r, t0, tokens, err);
+    Walk w(threadIdx.x >> LPH, PER, a.heads);
+    for (int base = 0; base < tokens * a.heads; base += PER, w.next()) {
+      const int64_t slot = w.token < tokens ? slot_s[w.token] : -1;
+      f2 v[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) v[p] = 0;
+      if (slot >= 0) {
+        const int64_t row = slot * a.heads + w.head;
+        const uint8_t *src = a.codes + row * (HD / 8 * BITS) + lane * BITS;
+        load_run16<BITS>(src, v);
+        load_run16<BITS>(src + HD / 16 * BITS, v + 4);
+        const float s0 = a.scales[row * ng + g0], s1 = a.scales[row * ng + g1];
+        // 2^23 + zero: the difference to 2^23 + q is exact
+        const float z0 = 8388608.f + (float)a.zeros[row * ng + g0], z1 = 8388608.f + (float)a.zeros[row * ng + g1];
+        const f2 zz0 = pack2(z0, z0), zz1 = pack2(z1, z1), ss0 = pack2(s0, s0), ss1 = pack2(s1, s1);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          v[p] = mul2(sub2(v[p], zz0), ss0);
+          v[p + 4] = mul2(sub2(v[p + 4], zz1), ss1);
+        }
+      }
+      rotate16<LPH>(v, a.had_block, lane);
+      if (slot >= 0) {
+        const f2 u2 = pack2(unit, unit);
+        __nv_bfloat16 *dst = rows + ((t0 + w.token) * a.heads + w.head) * HD + lane * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            float x, y;
+            unpack2(mul2(v[4 * h + p], u2), x, y);
+            o[p] = pack_bf16x2(x, y);
+          }
+          *reinterpret_cast<uint4 *>(dst + h * (HD / 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    }
+  }
+}
+
+template <int BITS, int LPH>
+__global__ void __launch_bounds__(kCacheThreads)
+    cache_write16_kernel(const CachePair c, const int64_t *__restrict__ slots, int64_t n, int tile, unsigned int *err) {
+  constexpr int HD = 16 << LPH, LANES = 1 << LPH, PER = kCacheThreads >> LPH;
+  constexpr float qmax = (float)((1 << BITS) - 1);
+  __shared__ int64_t slot_s[kTileTokens];
+  const qwha_cache &a = c.cache[blockIdx.y];
+  const __nv_bfloat16 *rows = static_cast<const __nv_bfloat16 *>(c.rows[blockIdx.y]);
+  const int lane = threadIdx.x & (LANES - 1);
+  const int gl = a.group / 8, ng = HD / a.group;  // lanes of a group, groups of a row
+  const bool whole = a.group == HD;
+  const float unit = (float)c.unit[blockIdx.y], step = 1.0f / qmax, half = (float)(0.5 + 1.0 / 4096);
+  for (int64_t t0 = (int64_t)blockIdx.x * tile; t0 < n; t0 += (int64_t)gridDim.x * tile) {
+    const int tokens = n - t0 < tile ? (int)(n - t0) : tile;
+    __syncthreads();
+    write_slots(slot_s, a, slots, t0, tokens, err);
+    Walk w(threadIdx.x >> LPH, PER, a.heads);
+    for (int base = 0; base < tokens * a.heads; base += PER, w.next()) {
+      const int64_t slot = w.token < tokens ? slot_s[w.token] : -1;
+      f2 v[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) v[p] = 0;
+      if (slot >= 0) {
+        const __nv_bfloat16 *src = rows + ((t0 + w.token) * a.heads + w.head) * HD + lane * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 q = ld_stream(src + h * (HD / 2));
+          v[4 * h] = pack2(bf16_lo(q.x), bf16_hi(q.x)), v[4 * h + 1] = pack2(bf16_lo(q.y), bf16_hi(q.y));
+          v[4 * h + 2] = pack2(bf16_lo(q.z), bf16_hi(q.z)), v[4 * h + 3] = pack2(bf16_lo(q.w), bf16_hi(q.w));
+        }
+      }
+      rotate16<LPH>(v, a.had_block, lane);
+      if (a.had_block) {
+        const f2 u2 = pack2(unit, unit);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) v[p] = mul2(v[p], u2);
+      }
+      float lo[2] = {0.f, 0.f}, hi[2] = {0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          float x, y;
+          unpack2(v[4 * h + p], x, y);
+          lo[h] = min_nan(lo[h], min_nan(x, y)), hi[h] = max_nan(hi[h], max_nan(x, y));
+        }
+      if (whole) lo[0] = lo[1] = min_nan(lo[0], lo[1]), hi[0] = hi[1] = max_nan(hi[0], hi[1]);
+#pragma unroll
+      for (int o = 1; o < LANES; o *= 2)
+        if (o < gl) {  // a whole row's group has more lanes than there are; half a row's exactly as many
+          lo[0] = min_nan(lo[0], __shfl_xor_sync(~0u, lo[0], o)), hi[0] = max_nan(hi[0], __shfl_xor_sync(~0u, hi[0], o));
+          if (!whole)
+            lo[1] = min_nan(lo[1], __shfl_xor_sync(~0u, lo[1], o)), hi[1] = max_nan(hi[1], __shfl_xor_sync(~0u, hi[1], o));
+        }
+      if (whole) lo[1] = lo[0], hi[1] = hi[0];
+      const int64_t row = slot * a.heads + w.head;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const Step<float> g(lo[h], hi[h], qmax, step, half);
+        const float up = g.z + half;
+        const f2 inv2 = pack2(g.inv, g.inv), up2 = pack2(up, up);
+        uint32_t q[8];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          float x, y;
+          unpack2(add2(mul2(v[4 * h + p], inv2), up2), x, y);
+          // within [0, qmax], then rounded down into the low bits of 2^23 + q
+          q[2 * p] = __float_as_uint(__fadd_rz(fminf(fmaxf(x, 0.f), qmax), 8388608.f));
+          q[2 * p + 1] = __float_as_uint(__fadd_rz(fminf(fmaxf(y, 0.f), qmax), 8388608.f));
+        }
+        if (slot >= 0) {
+          uint8_t *dst = a.codes + row * (HD / 8 * BITS) + h * (HD / 16 * BITS) + lane * BITS;
+          if constexpr (BITS == 8) {
+            uint2 o;
+            o.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+            o.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+            if (g.bad) o = make_uint2(0, 0);
+            *reinterpret_cast<uint2 *>(dst) = o;
+          } else {
+            uint32_t o = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o |= (q[i] & ((1u << BITS) - 1u)) << (BITS * i);
+            if (g.bad) o = 0;
+            if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(dst) = o;
+            else if constexpr (BITS == 2) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)o;
+            else dst[0] = (uint8_t)o, dst[1] = (uint8_t)(o >> 8), dst[2] = (uint8_t)(o >> 16);
+          }
+          const int gi = (h * (HD / 2) + lane * 8) / a.group;
+          if ((whole ? lane + h : lane % gl) == 0) {
+            a.scales[row * ng + gi] = g.bad ? __int_as_float(0x7fc00000) : g.s;
+            a.zeros[row * ng + gi] = g.bad ? 0 : (uint8_t)g.z;
+          }
+        }
+      }
     }
   }
 }
@@ -281,10 +580,43 @@ __global__ void __launch_bounds__(256) check_slots_kernel(const int64_t *__restr
   }
 }
 
-int lanes_log2(int head_dim) { return ilog2(cdiv(head_dim, 8)); }
+// Tokens of a tile: as many as leave eight CTAs to an SM, so that few rows
+// spread over the GPU and many share the look-up of their slots.
+int tile_tokens(int64_t n, int n_caches) {
+  return (int)std::clamp<int64_t>(n * n_caches / ((int64_t)sm_count() * 8), 1, kTileTokens);
+}
+dim3 tile_grid(int64_t n, int tile, int n_caches) {
+  return dim3((unsigned)std::min<int64_t>(cdiv(n, tile), (int64_t)sm_count() * 128), (unsigned)n_caches);
+}
 
-unsigned row_grid(int64_t items, int ll) {
-  return (unsigned)std::min<int64_t>(cdiv(items, kCacheThreads >> ll), (int64_t)sm_count() * 16);
+// lanes of the widest row, eight elements each
+int lanes_log2(const CachePair &c, int n_caches) {
+  int ll = 0;
+  for (int i = 0; i < n_caches; ++i) ll = std::max(ll, ilog2(cdiv(c.cache[i].head_dim, 8)));
+  return ll;
+}
+
+// Whether the sixteen-element kernels take the call: caches alike in shape, rows
+// of 64 to 256 elements, power-of-two groups.
+bool takes16(qwha_dtype dt, const CachePair &c, int n_caches) {
+  const qwha_cache &a = c.cache[0], &b = c.cache[n_caches - 1];
+  return dt == QWHA_BF16 && a.bits == b.bits && a.head_dim == b.head_dim && is_pow2(a.head_dim) && a.head_dim >= 64 &&
+         is_pow2(a.group) && is_pow2(b.group);
+}
+
+template <int BITS>
+void write16(const CachePair &c, dim3 grid, int tile, const int64_t *slots, int64_t n, unsigned int *err, cudaStream_t s) {
+  const int hd = c.cache[0].head_dim;
+  if (hd == 64) cache_write16_kernel<BITS, 2><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err);
+  else if (hd == 128) cache_write16_kernel<BITS, 3><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err);
+  else cache_write16_kernel<BITS, 4><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err);
+}
+template <int BITS>
+void read16(const CachePair &c, dim3 grid, int tile, const ReadArgs &r, int64_t n, unsigned int *err, cudaStream_t s) {
+  const int hd = c.cache[0].head_dim;
+  if (hd == 64) cache_read16_kernel<BITS, 2><<<grid, kCacheThreads, 0, s>>>(c, r, n, tile, err);
+  else if (hd == 128) cache_read16_kernel<BITS, 3><<<grid, kCacheThreads, 0, s>>>(c, r, n, tile, err);
+  else cache_read16_kernel<BITS, 4><<<grid, kCacheThreads, 0, s>>>(c, r, n, tile, err);
 }
 
 }  // namespace
@@ -293,32 +625,43 @@ int cache_max_head_dim() { return 256; }
 
 cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, const int64_t *slots, int64_t n,
                                cudaStream_t s) {
-  int ll = 0, heads = 0;
-  for (int i = 0; i < n_caches; ++i) {
-    ll = std::max(ll, lanes_log2(c.cache[i].head_dim));
-    heads = std::max(heads, c.cache[i].heads);
-  }
-  const dim3 grid(row_grid(n * heads, ll), (unsigned)n_caches);
+  const int tile = tile_tokens(n, n_caches);
+  const dim3 grid = tile_grid(n, tile, n_caches);
   unsigned int *err = device_error_word();
-  if (dt == QWHA_F32) cache_write_kernel<float><<<grid, kCacheThreads, 0, s>>>(c, ll, slots, n, err);
-  else cache_write_kernel<__nv_bfloat16><<<grid, kCacheThreads, 0, s>>>(c, ll, slots, n, err);
+  if (!err) return cudaErrorInvalidDevicePointer;
+  if (takes16(dt, c, n_caches)) {
+    switch (c.cache[0].bits) {
+      case 2: write16<2>(c, grid, tile, slots, n, err, s); break;
+      case 3: write16<3>(c, grid, tile, slots, n, err, s); break;
+      case 4: write16<4>(c, grid, tile, slots, n, err, s); break;
+      default: write16<8>(c, grid, tile, slots, n, err, s);
+    }
+    return cudaGetLastError();
+  }
+  const int ll = lanes_log2(c, n_caches);
+  if (dt == QWHA_F32) cache_write_kernel<float><<<grid, kCacheThreads, 0, s>>>(c, ll, slots, n, tile, err);
+  else cache_write_kernel<__nv_bfloat16><<<grid, kCacheThreads, 0, s>>>(c, ll, slots, n, tile, err);
   return cudaGetLastError();
 }
 
-cudaError_t launch_cache_read(qwha_dtype dt, const CachePair &c, int n_caches, const int32_t *pages, int max_pages,
-                              const int64_t *row_start, const int64_t *first, int n_seqs, int64_t n, cudaStream_t s) {
-  int ll = 0, heads = 0;
-  for (int i = 0; i < n_caches; ++i) {
-    ll = std::max(ll, lanes_log2(c.cache[i].head_dim));
-    heads = std::max(heads, c.cache[i].heads);
-  }
-  const dim3 grid(row_grid(n * heads, ll), (unsigned)n_caches);
+cudaError_t launch_cache_read(qwha_dtype dt, const CachePair &c, int n_caches, const ReadArgs &r, int64_t n,
+                              cudaStream_t s) {
+  const int tile = tile_tokens(n, n_caches);
+  const dim3 grid = tile_grid(n, tile, n_caches);
   unsigned int *err = device_error_word();
-  if (dt == QWHA_F32)
-    cache_read_kernel<float><<<grid, kCacheThreads, 0, s>>>(c, ll, pages, max_pages, row_start, first, n_seqs, n, err);
-  else
-    cache_read_kernel<__nv_bfloat16>
-        <<<grid, kCacheThreads, 0, s>>>(c, ll, pages, max_pages, row_start, first, n_seqs, n, err);
+  if (!err) return cudaErrorInvalidDevicePointer;
+  if (takes16(dt, c, n_caches)) {
+    switch (c.cache[0].bits) {
+      case 2: read16<2>(c, grid, tile, r, n, err, s); break;
+      case 3: read16<3>(c, grid, tile, r, n, err, s); break;
+      case 4: read16<4>(c, grid, tile, r, n, err, s); break;
+      default: read16<8>(c, grid, tile, r, n, err, s);
+    }
+    return cudaGetLastError();
+  }
+  const int ll = lanes_log2(c, n_caches);
+  if (dt == QWHA_F32) cache_read_kernel<float><<<grid, kCacheThreads, 0, s>>>(c, ll, r, n, tile, err);
+  else cache_read_kernel<__nv_bfloat16><<<grid, kCacheThreads, 0, s>>>(c, ll, r, n, tile, err);
   return cudaGetLastError();
 }
 

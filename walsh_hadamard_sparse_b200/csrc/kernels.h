@@ -203,8 +203,14 @@ constexpr unsigned int kErrSlot = 0x1000u, kErrPage = 0x2000u;
 int cache_max_head_dim();
 cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, const int64_t *slots, int64_t n,
                                cudaStream_t s);
-cudaError_t launch_cache_read(qwha_dtype dt, const CachePair &c, int n_caches, const int32_t *pages, int max_pages,
-                              const int64_t *row_start, const int64_t *first, int n_seqs, int64_t n, cudaStream_t s);
+// Where the rows of a read come from (qwha_cache_read).
+struct ReadArgs {
+  const int32_t *pages;
+  int max_pages, n_seqs;
+  const int64_t *row_start, *first;
+};
+cudaError_t launch_cache_read(qwha_dtype dt, const CachePair &c, int n_caches, const ReadArgs &r, int64_t n,
+                              cudaStream_t s);
 size_t check_slots_bytes(int64_t n_slots);
 cudaError_t launch_check_slots(const int64_t *slots, int64_t n, int64_t n_slots, void *ws, unsigned long long *bad,
                                cudaStream_t s);
