@@ -147,7 +147,7 @@ __device__ __forceinline__ void load_run(const uint8_t *p, float *q, int bits) {
   for (int i = 0; i < 8; ++i) q[i] = (float)((w >> (bits * i)) & mask);
 }
 
-constexpr int kTileTokens = 32;  // tokens of a CTA's tile, at most
+constexpr int kTileTokens = 64;  // tokens of a CTA's tile, at most
 
 // The (token, head) pairs of a tile, `step` apart: no division per pair.
 struct Walk {
@@ -162,42 +162,30 @@ struct Walk {
   }
 };
 
-// Slots of a tile of written rows: -1 where the row is skipped.
-__device__ __forceinline__ void write_slots(int64_t *slot, const qwha_cache &a, const int64_t *slots, int64_t t0, int n,
-                                            unsigned int *err) {
-  if (threadIdx.x < n) {
-    int64_t s = slots[t0 + threadIdx.x];
-    if (s < -1 || s >= a.n_pages * a.page_size) {
-      atomicOr(err, kErrSlot);
-      s = -1;
-    }
-    slot[threadIdx.x] = s;
-  }
-  __syncthreads();
+// Slot of written row i: -1 where the row is skipped.
+__device__ __forceinline__ int64_t write_slot(const qwha_cache &a, const int64_t *slots, int64_t i, unsigned int *err) {
+  const int64_t s = slots[i];
+  if (s >= -1 && s < a.n_pages * a.page_size) return s;
+  atomicOr(err, kErrSlot);
+  return -1;
 }
 
-// Slots of a tile of rows to read: output row i belongs to the sequence b with
-// row_start[b] <= i < row_start[b + 1] and is its token first[b] + i -
-// row_start[b]; -1 where the page table or the cache ends.
-__device__ __forceinline__ void read_slots(int64_t *slot, const qwha_cache &a, const ReadArgs &r, int64_t t0, int n,
-                                           unsigned int *err) {
-  if (threadIdx.x < n) {
-    const int64_t i = t0 + threadIdx.x;
-    int lo = 0, hi = r.n_seqs;  // row_start[lo] <= i < row_start[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (r.row_start[mid] <= i) lo = mid;
-      else hi = mid;
-    }
-    const int64_t pos = i - r.row_start[lo] + (r.first ? r.first[lo] : 0), pg = pos / a.page_size;
-    int64_t page = -1;
-    if (pos >= 0 && pg < r.max_pages) page = r.pages[(int64_t)lo * r.max_pages + pg];
-    int64_t s = -1;
-    if (page < 0 || page >= a.n_pages) atomicOr(err, kErrPage);
-    else s = page * a.page_size + (pos - pg * a.page_size);
-    slot[threadIdx.x] = s;
+// Slot of output row i, which belongs to the sequence b with row_start[b] <= i <
+// row_start[b + 1] and is its token first[b] + i - row_start[b]; -1 where the
+// page table or the cache ends.
+__device__ __forceinline__ int64_t read_slot(const qwha_cache &a, const ReadArgs &r, int64_t i, unsigned int *err) {
+  int lo = 0, hi = r.n_seqs;  // row_start[lo] <= i < row_start[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (r.row_start[mid] <= i) lo = mid;
+    else hi = mid;
   }
-  __syncthreads();
+  const int64_t pos = i - r.row_start[lo] + (r.first ? r.first[lo] : 0), pg = pos / a.page_size;
+  int64_t page = -1;
+  if (pos >= 0 && pg < r.max_pages) page = r.pages[(int64_t)lo * r.max_pages + pg];
+  if (page >= 0 && page < a.n_pages) return page * a.page_size + (pos - pg * a.page_size);
+  atomicOr(err, kErrPage);
+  return -1;
 }
 
 // Scale, zero point and the factor of the codes of a group with range [lo, hi].
@@ -232,7 +220,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheP
   for (int64_t t0 = (int64_t)blockIdx.x * tile; t0 < n; t0 += (int64_t)gridDim.x * tile) {
     const int tokens = n - t0 < tile ? (int)(n - t0) : tile;
     __syncthreads();  // the last tile's slots are read
-    write_slots(slot_s, a, slots, t0, tokens, err);
+    if (threadIdx.x < tokens) slot_s[threadIdx.x] = write_slot(a, slots, t0 + threadIdx.x, err);
+    __syncthreads();
     Walk w(threadIdx.x >> ll, kCacheThreads >> ll, a.heads);
     // whole warps stay together: their pairs differ by less than the tile's last ones
     for (int base = 0; base < tokens * a.heads; base += kCacheThreads >> ll, w.next()) {
@@ -287,7 +276,8 @@ __global__ void __launch_bounds__(kCacheThreads)
   for (int64_t t0 = (int64_t)blockIdx.x * tile; t0 < rows_n; t0 += (int64_t)gridDim.x * tile) {
     const int tokens = rows_n - t0 < tile ? (int)(rows_n - t0) : tile;
     __syncthreads();
-    read_slots(slot_s, a, r, t0, tokens, err);
+    if (threadIdx.x < tokens) slot_s[threadIdx.x] = read_slot(a, r, t0 + threadIdx.x, err);
+    __syncthreads();
     Walk w(threadIdx.x >> ll, kCacheThreads >> ll, a.heads);
     for (int base = 0; base < tokens * a.heads; base += kCacheThreads >> ll, w.next()) {
       const int64_t slot = w.token < tokens ? slot_s[w.token] : -1;
@@ -307,6 +297,185 @@ __global__ void __launch_bounds__(kCacheThreads)
         T *dst = rows + ((t0 + w.token) * a.heads + w.head) * a.head_dim + lane * 8;
 #pragma unroll
         for (int u = 0; u < 8; u += io<T>::kVec) *reinterpret_cast<uint4 *>(dst + u) = io<T>::pack(v + u);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Reading on tensor cores. q - zero is an integer of at most 8 bits and a sign,
+// so H (q - zero) is exact in matrix instructions of f16 with fp32 sums, and one
+// multiplication by scale / sqrt(n) is left per value. A unit is 128 elements in
+// a row of a token's heads; the bits e0..e6 of an element's place are split over
+// the operands of two products,
+//   D[m][n]  = sum_k A[m][k] (q - zero)[k][n],  k = (e2, e3, e4, e0), n = (e1, e5, e6)
+//   E[m][n'] = sum_n D[m][n] B[n][n'],
+// A and B the Hadamard matrices of those bits (the identity in bits at or above
+// had_block), D in the layout of the second product's operand as it stands. A
+// lane reads the eight codes that differ in e0..e2, takes the four with its own
+// e1, and ends with four neighbours of the row. Bits e5 and e6 that lie between
+// two groups of a block are left to fp32 butterflies after the scales.
+// D is at most 16 (2^bits - 1): exact in f16 up to 2048, so for 8 bits it is
+// split into two f16 (D - f16(D) is at most 1).
+//
+// Memory bounds this: 2 bytes written and 0.53 read a value of 4 bits. A CTA
+// fetches 256 units of a tile with all its threads and computes from shared
+// memory; eight CTAs on an SM overlap each other's phases. Two caches, 8 heads
+// of 128, 4 bits, 192526 tokens, bf16: 182 us, 84 % of the copy rate. Loads
+// straight to the registers of the lane that uses them, four units in flight a
+// warp, took 285 us (waiting for memory), butterflies in registers and between
+// lanes 309 us (issue slots).
+
+__device__ __forceinline__ void mma_16816(float *d, const uint32_t *a, const uint32_t *b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
+}
+__device__ __forceinline__ void mma_1688(float *d, uint32_t a0, uint32_t a1, uint32_t b) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+__device__ __forceinline__ void cp_async16(void *smem, const void *p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Entry (i, j) of the Kronecker product of [1 1; 1 -1] in the bits of `on` and
+// the identity in the others, in f16.
+__device__ __forceinline__ uint32_t sign_entry(int i, int j, int on) {
+  return (i ^ j) & ~on ? 0u : __popc(i & j & on) & 1 ? 0xbc00u : 0x3c00u;
+}
+
+// The lane's eight codes as the register (or two) that hold them.
+template <int BITS>
+__device__ __forceinline__ uint2 load_codes(const uint8_t *unit, int word) {
+  if constexpr (BITS == 8) return *reinterpret_cast<const uint2 *>(unit + 8 * word);
+  if constexpr (BITS == 4) return make_uint2(*reinterpret_cast<const uint32_t *>(unit + 4 * word), 0);
+  if constexpr (BITS == 2) return make_uint2(*reinterpret_cast<const uint16_t *>(unit + 2 * word), 0);
+  const uint32_t *w = reinterpret_cast<const uint32_t *>(unit);  // bytes 3 word .. 3 word + 2
+  return make_uint2(w[3 * word / 4], w[(3 * word + 2) / 4]);
+}
+// b[i]: 1024 + q of the codes e0 = i, e1, e2 = 0 and 1, two f16.
+template <int BITS>
+__device__ __forceinline__ void spread_codes(uint2 c, int word, int e1, uint32_t *b) {
+  if constexpr (BITS == 8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) b[i] = __byte_perm(c.x, c.y, e1 ? 0x0602 + 0x101 * i : 0x0400 + 0x101 * i) & 0x00ff00ffu;
+  } else {
+    uint32_t w = c.x;
+    if constexpr (BITS == 2) w = __byte_perm(w, 0, 0x4140);
+    if constexpr (BITS == 3) {
+      w = __funnelshift_r(c.x, c.y, 8 * (3 * word % 4));
+      w = (w & 0xfffu) | (w << 4 & 0x0fff0000u);
+    }
+    w >>= 2 * BITS * e1;
+    b[0] = w, b[1] = w >> BITS;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) b[i] = (b[i] & (0x00010001u * ((1u << BITS) - 1u))) | 0x64006400u;
+}
+
+constexpr int kTileUnits = 256;
+constexpr uint32_t kNoSlot = ~0u;  // in place of a zero point
+
+template <typename T, int BITS>
+__global__ void __launch_bounds__(kCacheThreads)
+    cache_read_mma_kernel(const CachePair c, const ReadArgs r, int64_t n, int tile, unsigned int *err) {
+  constexpr int kWarps = kCacheThreads / 32;
+  __shared__ int64_t slot_s[kTileTokens];
+  __shared__ __align__(16) uint8_t code_s[kTileUnits * 16 * BITS];
+  __shared__ float scale_s[kTileUnits * 4];
+  __shared__ uint32_t zero_s[kTileUnits * 4];  // 1024 + zero, two f16
+  const qwha_cache &a = c.cache[blockIdx.y];
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
+  const int lg = 31 - __clz(a.group), had = a.had_block > 1 ? a.had_block : 1;
+  const int units = a.heads * a.head_dim / 128;  // of a token
+  const int word = t + 4 * (g >> 1), e1 = g & 1;
+  // the bits of A's and B's indices that are in the block, and for B in the group
+  const int on_k = (had > 4) | (had > 8) << 1 | (had > 16) << 2 | (had > 1) << 3;
+  const int on_n = (had > 2) | (had > 32 && lg > 5) << 1 | (had > 64 && lg > 6) << 2;
+  const bool cross5 = had > 32 && lg <= 5, cross6 = had > 64 && lg <= 6;
+  uint32_t ha[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = g + 8 * (i & 1), k = 2 * t + 8 * (i >> 1);
+    ha[i] = sign_entry(m, k, on_k) | sign_entry(m, k + 1, on_k) << 16;
+  }
+  const uint32_t hb = sign_entry(2 * t, g, on_n) | sign_entry(2 * t + 1, g, on_n) << 16;
+  const float scale = (float)c.unit[blockIdx.y];
+  const int up = lg < 7 ? lg - 5 : 2;  // the lane's group of a unit is its (e5, e6) >> up
+  const int pieces = units * BITS, groups = units * 128 >> lg;  // 16-byte pieces of codes and groups of a token
+  T *rows = static_cast<T *>(const_cast<void *>(c.rows[blockIdx.y])) + 4 * g + 32 * t;
+  const int64_t end = r.row_start[r.n_seqs], rows_n = end < n ? end : n;
+  for (int64_t t0 = (int64_t)blockIdx.x * tile; t0 < rows_n; t0 += (int64_t)gridDim.x * tile) {
+    const int tokens = rows_n - t0 < tile ? (int)(rows_n - t0) : tile;
+    __syncthreads();
+    if (threadIdx.x < tokens) slot_s[threadIdx.x] = read_slot(a, r, t0 + threadIdx.x, err);
+    const int total = tokens * units;
+    for (int u0 = 0; u0 < total; u0 += kTileUnits) {
+      __syncthreads();
+      const int here = total - u0 < kTileUnits ? total - u0 : kTileUnits;
+      for (int i = threadIdx.x; i < here * BITS; i += kCacheThreads) {
+        const int at = u0 * BITS + i, token = at / pieces;
+        const int64_t slot = slot_s[token];
+        if (slot >= 0) cp_async16(code_s + 16 * i, a.codes + (slot * pieces + (at - token * pieces)) * 16);
+      }
+      const int g0 = u0 * 128 >> lg;
+      for (int i = threadIdx.x; i < here * 128 >> lg; i += kCacheThreads) {
+        const int token = (g0 + i) / groups;
+        const int64_t slot = slot_s[token], group = slot * groups + (g0 + i - token * groups);
+        if (slot >= 0) scale_s[i] = a.scales[group] * scale, zero_s[i] = (a.zeros[group] | 0x6400u) * 0x10001u;
+        else zero_s[i] = kNoSlot;
+      }
+      cp_async_wait_all();
+      __syncthreads();
+      T *out = rows + (t0 * units + u0 + warp) * 128;
+#pragma unroll 4
+      for (int u = warp; u < here; u += kWarps, out += kWarps * 128) {
+        const int group = u * 128 >> lg;
+        const uint32_t zz = zero_s[group + (g >> 1 >> up)];
+        const float f = scale_s[group + (t >> up)];
+        const bool live = zz != kNoSlot;
+        const uint2 code = load_codes<BITS>(code_s + u * (16 * BITS), word);
+        uint32_t b[2];
+        spread_codes<BITS>(code, word, e1, b);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const __half2 d = __hsub2(reinterpret_cast<const __half2 &>(b[i]), reinterpret_cast<const __half2 &>(zz));
+          b[i] = reinterpret_cast<const uint32_t &>(d);
+        }
+        float d[4], e[4];
+        mma_16816(d, ha, b);
+        const uint32_t d0 = f16x2(d[0], d[1]), d1 = f16x2(d[2], d[3]);
+        mma_1688(e, d0, d1, hb);
+        if constexpr (BITS == 8) {
+          const float2 f0 = __half22float2(reinterpret_cast<const __half2 &>(d0)),
+                       f1 = __half22float2(reinterpret_cast<const __half2 &>(d1));
+          float lo[4];
+          mma_1688(lo, f16x2(d[0] - f0.x, d[1] - f0.y), f16x2(d[2] - f1.x, d[3] - f1.y), hb);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] += lo[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] *= f;
+        if (cross5)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = fmaf(e[i], t & 1 ? -1.f : 1.f, __shfl_xor_sync(~0u, e[i], 1));
+        if (cross6)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = fmaf(e[i], t & 2 ? -1.f : 1.f, __shfl_xor_sync(~0u, e[i], 2));
+        // e0 is the bit of m above g, e1 the lower bit of n'
+        if (!live) continue;
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(out) = make_float4(e[0], e[2], e[1], e[3]);
+        else *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(e[0], e[2]), pack_bf16x2(e[1], e[3]));
       }
     }
   }
@@ -392,83 +561,6 @@ __device__ __forceinline__ void rotate16(f2 *v, int had_block, int lane) {
     }
 }
 
-// Eight codes as floats 2^23 + q (the codes' place in the mantissa), in pairs.
-template <int BITS>
-__device__ __forceinline__ void load_run16(const uint8_t *p, f2 *v) {
-  uint32_t q[8];
-  if constexpr (BITS == 8) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      q[i] = __byte_perm(w.x, 0x4b000000u, 0x7440 + i), q[i + 4] = __byte_perm(w.y, 0x4b000000u, 0x7440 + i);
-  } else {
-    uint32_t w;
-    if constexpr (BITS == 4) w = *reinterpret_cast<const uint32_t *>(p);
-    else if constexpr (BITS == 2) w = *reinterpret_cast<const uint16_t *>(p);
-    else w = (uint32_t)p[0] | (uint32_t)p[1] << 8 | (uint32_t)p[2] << 16;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = ((w >> (BITS * i)) & ((1u << BITS) - 1u)) | 0x4b000000u;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = pack2(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1]));
-}
-
-template <int BITS, int LPH>
-__global__ void __launch_bounds__(kCacheThreads)
-    cache_read16_kernel(const CachePair c, const ReadArgs r, int64_t n, int tile, unsigned int *err) {
-  constexpr int HD = 16 << LPH, LANES = 1 << LPH, PER = kCacheThreads >> LPH;
-  __shared__ int64_t slot_s[kTileTokens];
-  const qwha_cache &a = c.cache[blockIdx.y];
-  __nv_bfloat16 *rows = static_cast<__nv_bfloat16 *>(const_cast<void *>(c.rows[blockIdx.y]));
-  const int lane = threadIdx.x & (LANES - 1);
-  const int ng = HD / a.group, g0 = lane * 8 / a.group, g1 = (HD / 2 + lane * 8) / a.group;
-  const float unit = (float)c.unit[blockIdx.y];
-  const int64_t end = r.row_start[r.n_seqs], rows_n = end < n ? end : n;
-  for (int64_t t0 = (int64_t)blockIdx.x * tile; t0 < rows_n; t0 += (int64_t)gridDim.x * tile) {
-    const int tokens = rows_n - t0 < tile ? (int)(rows_n - t0) : tile;
-    __syncthreads();
-    read_slots(slot_s, a, r, t0, tokens, err);
-    Walk w(threadIdx.x >> LPH, PER, a.heads);
-    for (int base = 0; base < tokens * a.heads; base += PER, w.next()) {
-      const int64_t slot = w.token < tokens ? slot_s[w.token] : -1;
-      f2 v[8];
-#pragma unroll
-      for (int p = 0; p < 8; ++p) v[p] = 0;
-      if (slot >= 0) {
-        const int64_t row = slot * a.heads + w.head;
-        const uint8_t *src = a.codes + row * (HD / 8 * BITS) + lane * BITS;
-        load_run16<BITS>(src, v);
-        load_run16<BITS>(src + HD / 16 * BITS, v + 4);
-        const float s0 = a.scales[row * ng + g0], s1 = a.scales[row * ng + g1];
-        // 2^23 + zero: the difference to 2^23 + q is exact
-        const float z0 = 8388608.f + (float)a.zeros[row * ng + g0], z1 = 8388608.f + (float)a.zeros[row * ng + g1];
-        const f2 zz0 = pack2(z0, z0), zz1 = pack2(z1, z1), ss0 = pack2(s0, s0), ss1 = pack2(s1, s1);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          v[p] = mul2(sub2(v[p], zz0), ss0);
-          v[p + 4] = mul2(sub2(v[p + 4], zz1), ss1);
-        }
-      }
-      rotate16<LPH>(v, a.had_block, lane);
-      if (slot >= 0) {
-        const f2 u2 = pack2(unit, unit);
-        __nv_bfloat16 *dst = rows + ((t0 + w.token) * a.heads + w.head) * HD + lane * 8;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t o[4];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            float x, y;
-            unpack2(mul2(v[4 * h + p], u2), x, y);
-            o[p] = pack_bf16x2(x, y);
-          }
-          *reinterpret_cast<uint4 *>(dst + h * (HD / 2)) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
-    }
-  }
-}
-
 template <int BITS, int LPH>
 __global__ void __launch_bounds__(kCacheThreads)
     cache_write16_kernel(const CachePair c, const int64_t *__restrict__ slots, int64_t n, int tile, unsigned int *err) {
@@ -484,7 +576,8 @@ __global__ void __launch_bounds__(kCacheThreads)
   for (int64_t t0 = (int64_t)blockIdx.x * tile; t0 < n; t0 += (int64_t)gridDim.x * tile) {
     const int tokens = n - t0 < tile ? (int)(n - t0) : tile;
     __syncthreads();
-    write_slots(slot_s, a, slots, t0, tokens, err);
+    if (threadIdx.x < tokens) slot_s[threadIdx.x] = write_slot(a, slots, t0 + threadIdx.x, err);
+    __syncthreads();
     Walk w(threadIdx.x >> LPH, PER, a.heads);
     for (int base = 0; base < tokens * a.heads; base += PER, w.next()) {
       const int64_t slot = w.token < tokens ? slot_s[w.token] : -1;
@@ -589,6 +682,14 @@ dim3 tile_grid(int64_t n, int tile, int n_caches) {
   return dim3((unsigned)std::min<int64_t>(cdiv(n, tile), (int64_t)sm_count() * 128), (unsigned)n_caches);
 }
 
+// The second cache by itself: a pair whose caches need different kernels takes a
+// launch for each, so that a cache's rows do not depend on its partner.
+CachePair second(const CachePair &c) {
+  CachePair d = c;
+  d.cache[0] = c.cache[1], d.rows[0] = c.rows[1], d.unit[0] = c.unit[1];
+  return d;
+}
+
 // lanes of the widest row, eight elements each
 int lanes_log2(const CachePair &c, int n_caches) {
   int ll = 0;
@@ -611,12 +712,26 @@ void write16(const CachePair &c, dim3 grid, int tile, const int64_t *slots, int6
   else if (hd == 128) cache_write16_kernel<BITS, 3><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err);
   else cache_write16_kernel<BITS, 4><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err);
 }
-template <int BITS>
-void read16(const CachePair &c, dim3 grid, int tile, const ReadArgs &r, int64_t n, unsigned int *err, cudaStream_t s) {
-  const int hd = c.cache[0].head_dim;
-  if (hd == 64) cache_read16_kernel<BITS, 2><<<grid, kCacheThreads, 0, s>>>(c, r, n, tile, err);
-  else if (hd == 128) cache_read16_kernel<BITS, 3><<<grid, kCacheThreads, 0, s>>>(c, r, n, tile, err);
-  else cache_read16_kernel<BITS, 4><<<grid, kCacheThreads, 0, s>>>(c, r, n, tile, err);
+// Whether the tensor cores read the caches: units of 128 elements, groups that
+// hold whole columns of the first product, blocks inside a unit.
+bool takes_mma(const CachePair &c, int n_caches) {
+  for (int i = 0; i < n_caches; ++i) {
+    const qwha_cache &a = c.cache[i];
+    if (a.bits != c.cache[0].bits || (int64_t)a.heads * a.head_dim % 128 || !is_pow2(a.group) || a.group < 32 ||
+        a.had_block > 128)
+      return false;
+  }
+  return true;
+}
+template <typename T>
+void read_mma(const CachePair &c, dim3 grid, int tile, const ReadArgs &r, int64_t n, unsigned int *err,
+              cudaStream_t s) {
+  switch (c.cache[0].bits) {
+    case 2: cache_read_mma_kernel<T, 2><<<grid, kCacheThreads, 0, s>>>(c, r, n, tile, err); break;
+    case 3: cache_read_mma_kernel<T, 3><<<grid, kCacheThreads, 0, s>>>(c, r, n, tile, err); break;
+    case 4: cache_read_mma_kernel<T, 4><<<grid, kCacheThreads, 0, s>>>(c, r, n, tile, err); break;
+    default: cache_read_mma_kernel<T, 8><<<grid, kCacheThreads, 0, s>>>(c, r, n, tile, err);
+  }
 }
 
 }  // namespace
@@ -625,6 +740,10 @@ int cache_max_head_dim() { return 256; }
 
 cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, const int64_t *slots, int64_t n,
                                cudaStream_t s) {
+  if (n_caches == 2 && !takes16(dt, c, 2) && (takes16(dt, c, 1) || takes16(dt, second(c), 1))) {
+    const cudaError_t e = launch_cache_write(dt, c, 1, slots, n, s);
+    return e != cudaSuccess ? e : launch_cache_write(dt, second(c), 1, slots, n, s);
+  }
   const int tile = tile_tokens(n, n_caches);
   const dim3 grid = tile_grid(n, tile, n_caches);
   unsigned int *err = device_error_word();
@@ -646,17 +765,17 @@ cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, 
 
 cudaError_t launch_cache_read(qwha_dtype dt, const CachePair &c, int n_caches, const ReadArgs &r, int64_t n,
                               cudaStream_t s) {
+  if (n_caches == 2 && !takes_mma(c, 2) && (takes_mma(c, 1) || takes_mma(second(c), 1))) {
+    const cudaError_t e = launch_cache_read(dt, c, 1, r, n, s);
+    return e != cudaSuccess ? e : launch_cache_read(dt, second(c), 1, r, n, s);
+  }
   const int tile = tile_tokens(n, n_caches);
   const dim3 grid = tile_grid(n, tile, n_caches);
   unsigned int *err = device_error_word();
   if (!err) return cudaErrorInvalidDevicePointer;
-  if (takes16(dt, c, n_caches)) {
-    switch (c.cache[0].bits) {
-      case 2: read16<2>(c, grid, tile, r, n, err, s); break;
-      case 3: read16<3>(c, grid, tile, r, n, err, s); break;
-      case 4: read16<4>(c, grid, tile, r, n, err, s); break;
-      default: read16<8>(c, grid, tile, r, n, err, s);
-    }
+  if (takes_mma(c, n_caches)) {
+    if (dt == QWHA_F32) read_mma<float>(c, grid, tile, r, n, err, s);
+    else read_mma<__nv_bfloat16>(c, grid, tile, r, n, err, s);
     return cudaGetLastError();
   }
   const int ll = lanes_log2(c, n_caches);
