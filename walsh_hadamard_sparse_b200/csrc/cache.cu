@@ -482,15 +482,16 @@ __global__ void __launch_bounds__(kCacheThreads)
 }
 
 // ---------------------------------------------------------------------------
-// bf16 rows of 64, 128 or 256 elements with power-of-two groups, the shapes that
-// move much data. Arithmetic and shuffles bound these kernels, not memory: at
-// 6.5 TB/s 2.6 bytes a value leave 14 instruction slots. So a lane holds
-// sixteen elements in two runs of eight, a row's halves apart (element = half
-// * hd / 2 + lane * 8 + i): five of the seven stages of 128 elements stay in
-// registers or between lanes with one shuffle a value, in the order 1, 2, 4
-// (registers), 8, 16, 32 (lanes), 64 (registers); adds, products and the
-// butterflies between lanes (p + sign * v, exact) run two to an instruction,
-// and codes become floats, and floats codes, by the exponent of 2^23.
+// Writing bf16 rows in units of 128 elements. The fp32 butterflies and the
+// quantizer bound this, not memory: at the copy rate 2.5 bytes a value leave
+// about 12 instructions, so every step counts. Eight lanes hold two units, one
+// in each half of packed fp32 pairs. A lane begins with sixteen neighbours
+// (stages 1, 2, 4, 8), the units turn in shared memory, and it ends with the
+// elements l + 8 j (stages 16, 32, 64; l its place among the eight lanes): no
+// stage crosses lanes. Ranges of the groups are reduced so that each lane ends
+// with one group, computes its step and hands it round. Codes become nibbles
+// (8 bits: bytes) by one shifted addition each, and an eight by eight transpose
+// in registers brings each lane sixteen neighbours to store.
 
 using f2 = unsigned long long;  // two fp32 values
 __device__ __forceinline__ f2 pack2(float a, float b) {
@@ -516,146 +517,207 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
+
+// Butterflies between v[i] and v[i + H].
+template <int H>
+__device__ __forceinline__ void stage16(f2 *v) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (!(i & H)) {
+      const f2 a = v[i], b = v[i + H];
+      v[i] = add2(a, b), v[i + H] = sub2(a, b);
+    }
 }
 
-// v[p], p = 0..7: elements (2p, 2p + 1) of the lane's sixteen (p < 4: first half).
-template <int LPH>
-__device__ __forceinline__ void rotate16(f2 *v, int had_block, int lane) {
-  if (had_block < 2) return;
+// Eight lanes, R's piece k of lane l becomes piece l of lane k.
+__device__ __forceinline__ uint32_t turn_halves(uint32_t r, int l, int d) {
+  return __byte_perm(r, __shfl_xor_sync(~0u, r, d), l & d ? 0x3276 : 0x5410);
+}
+__device__ __forceinline__ uint32_t turn_bytes(uint32_t r, int l, int d) {
+  return __byte_perm(r, __shfl_xor_sync(~0u, r, d), l & d ? 0x3715 : 0x6240);
+}
+__device__ __forceinline__ uint32_t turn_nibbles(uint32_t r, int l) {
+  const uint32_t keep = l & 1 ? 0xf0f0f0f0u : 0x0f0f0f0fu, x = __shfl_xor_sync(~0u, r, 1);
+  return (r & keep) | (__funnelshift_l(x, x, l & 1 ? 28 : 4) & ~keep);
+}
+
+// Eight nibbles of BITS < 4 bits, closed up.
+template <int BITS>
+__device__ __forceinline__ uint32_t close_up(uint32_t w) {
+  w = (w | w >> (4 - BITS)) & (BITS == 3 ? 0x3f3f3f3fu : 0x0f0f0f0fu);
+  w = (w | w >> (8 - 2 * BITS)) & (BITS == 3 ? 0x0fff0fffu : 0x00ff00ffu);
+  return (w | w >> (16 - 4 * BITS)) & ((1u << (8 * BITS)) - 1u);
+}
+
+// Stores a unit's codes q[j] = 2^23 + code of element l + 8 j (fp32 bits): the
+// lane's share are elements 16 l .. 16 l + 15, all zero where `bad`.
+template <int BITS>
+__device__ __forceinline__ void store_unit(uint8_t *unit, const uint32_t *q, int l, bool live, bool bad) {
+  if constexpr (BITS == 8) {
+    uint32_t r[4];  // bytes: even j below and above 8, odd j below and above 8
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {  // stage 1, inside a pair
-    float a, b;
-    unpack2(v[p], a, b);
-    v[p] = pack2(a + b, a - b);
+    for (int i = 0; i < 4; ++i) {
+      r[i] = 0u - 0x4b000000u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[i] += q[8 * (i & 1) + 2 * k + (i >> 1)] << (8 * k);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const uint32_t x = __shfl_xor_sync(~0u, l & 4 ? r[i] : r[i + 1], 4);
+      if (l & 4) r[i] = x;
+      else r[i + 1] = x;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = turn_bytes(turn_halves(r[i], l, 2), l, 1);
+    if (!live) return;
+    *reinterpret_cast<uint4 *>(unit + 16 * l) = bad ? make_uint4(0, 0, 0, 0) : make_uint4(r[0], r[1], r[2], r[3]);
+  } else {
+    uint32_t r[2];  // nibbles: even j, odd j
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r[i] = 0u - 0xfb000000u;  // what the exponents of the first two leave
+#pragma unroll
+      for (int k = 0; k < 8; ++k) r[i] += q[2 * k + i] << (4 * k);
+      r[i] = turn_nibbles(turn_bytes(turn_halves(r[i], l, 4), l, 2), l);
+      if (bad) r[i] = 0;
+    }
+    if (!live) return;
+    if constexpr (BITS == 4) {
+      *reinterpret_cast<uint2 *>(unit + 8 * l) = make_uint2(r[0], r[1]);
+    } else if constexpr (BITS == 2) {
+      *reinterpret_cast<uint32_t *>(unit + 4 * l) = close_up<2>(r[0]) | close_up<2>(r[1]) << 16;
+    } else {
+      const uint32_t a = close_up<3>(r[0]), b = close_up<3>(r[1]);
+      uint16_t *p = reinterpret_cast<uint16_t *>(unit + 6 * l);
+      p[0] = (uint16_t)a, p[1] = (uint16_t)(a >> 16 | b << 8), p[2] = (uint16_t)(b >> 8);
+    }
   }
-#pragma unroll
-  for (int h = 1; h < 4; h *= 2)  // stages 2 and 4
-    if (had_block >= 4 * h)
-#pragma unroll
-      for (int p = 0; p < 8; ++p)
-        if (!(p & h)) {
-          const f2 a = v[p], b = v[p + h];
-          v[p] = add2(a, b), v[p + h] = sub2(a, b);
-        }
-#pragma unroll
-  for (int o = 1; o < (1 << LPH); o *= 2)
-    if (had_block >= 16 * o) {
-      const float sign = lane & o ? -1.f : 1.f;
-      const f2 sg = pack2(sign, sign);
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        float a, b;
-        unpack2(v[p], a, b);
-        v[p] = fma2(v[p], sg, pack2(__shfl_xor_sync(~0u, a, o), __shfl_xor_sync(~0u, b, o)));
-      }
-    }
-  if (had_block == (16 << LPH))
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const f2 a = v[p], b = v[p + 4];
-      v[p] = add2(a, b), v[p + 4] = sub2(a, b);
-    }
 }
 
-template <int BITS, int LPH>
+// NG groups in a unit.
+template <int BITS, int NG>
 __global__ void __launch_bounds__(kCacheThreads)
-    cache_write16_kernel(const CachePair c, const int64_t *__restrict__ slots, int64_t n, int tile, unsigned int *err) {
-  constexpr int HD = 16 << LPH, LANES = 1 << LPH, PER = kCacheThreads >> LPH;
+    cache_write_unit_kernel(const CachePair c, const int64_t *__restrict__ slots, int64_t n, int tile,
+                            unsigned int *err) {
+  constexpr int kWarps = kCacheThreads / 32, kTurn = 128 + 16 + 8;  // pairs of two units, padded: no bank twice
+  constexpr int C = 2 * NG, kShift = NG == 1 ? 2 : NG == 2 ? 1 : 0;  // groups of two units; their lanes: c << kShift
   constexpr float qmax = (float)((1 << BITS) - 1);
   __shared__ int64_t slot_s[kTileTokens];
+  __shared__ __align__(16) f2 turn_s[kWarps][4][kTurn];
   const qwha_cache &a = c.cache[blockIdx.y];
   const __nv_bfloat16 *rows = static_cast<const __nv_bfloat16 *>(c.rows[blockIdx.y]);
-  const int lane = threadIdx.x & (LANES - 1);
-  const int gl = a.group / 8, ng = HD / a.group;  // lanes of a group, groups of a row
-  const bool whole = a.group == HD;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 7;
+  const int units = a.heads * a.head_dim / 128, had = a.had_block;
   const float unit = (float)c.unit[blockIdx.y], step = 1.0f / qmax, half = (float)(0.5 + 1.0 / 4096);
+  f2 *turn = turn_s[warp][lane >> 3];
   for (int64_t t0 = (int64_t)blockIdx.x * tile; t0 < n; t0 += (int64_t)gridDim.x * tile) {
     const int tokens = n - t0 < tile ? (int)(n - t0) : tile;
-    __syncthreads();
+    __syncthreads();  // the last tile's slots are read
     if (threadIdx.x < tokens) slot_s[threadIdx.x] = write_slot(a, slots, t0 + threadIdx.x, err);
     __syncthreads();
-    Walk w(threadIdx.x >> LPH, PER, a.heads);
-    for (int base = 0; base < tokens * a.heads; base += PER, w.next()) {
-      const int64_t slot = w.token < tokens ? slot_s[w.token] : -1;
-      f2 v[8];
+    const int total = tokens * units;
+    Walk w(8 * warp + 2 * (lane >> 3), 8 * kWarps, units);
+    for (int at = 8 * warp; at < total; at += 8 * kWarps, w.next()) {
+      const int p = at + 2 * (lane >> 3);  // and p + 1
+      int64_t to[2];                       // units of the cache, -1: none
+      uint4 in[2][2];
 #pragma unroll
-      for (int p = 0; p < 8; ++p) v[p] = 0;
-      if (slot >= 0) {
-        const __nv_bfloat16 *src = rows + ((t0 + w.token) * a.heads + w.head) * HD + lane * 8;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 q = ld_stream(src + h * (HD / 2));
-          v[4 * h] = pack2(bf16_lo(q.x), bf16_hi(q.x)), v[4 * h + 1] = pack2(bf16_lo(q.y), bf16_hi(q.y));
-          v[4 * h + 2] = pack2(bf16_lo(q.z), bf16_hi(q.z)), v[4 * h + 3] = pack2(bf16_lo(q.w), bf16_hi(q.w));
+      for (int u = 0; u < 2; ++u) {
+        const bool wrap = w.head + u == units;
+        to[u] = -1;
+        in[u][0] = in[u][1] = make_uint4(0, 0, 0, 0);
+        if (p + u < total) {
+          const __nv_bfloat16 *src = rows + (t0 * units + p + u) * 128 + 16 * l;
+          in[u][0] = ld_stream(src), in[u][1] = ld_stream(src + 8);
+          const int64_t slot = slot_s[w.token + wrap];
+          if (slot >= 0) to[u] = slot * units + (wrap ? 0 : w.head + u);
         }
       }
-      rotate16<LPH>(v, a.had_block, lane);
-      if (a.had_block) {
-        const f2 u2 = pack2(unit, unit);
+      f2 v[16];
 #pragma unroll
-        for (int p = 0; p < 8; ++p) v[p] = mul2(v[p], u2);
+      for (int i = 0; i < 8; ++i) {
+        const uint4 &qa = in[0][i / 4], &qb = in[1][i / 4];
+        const uint32_t x = i % 4 == 0 ? qa.x : i % 4 == 1 ? qa.y : i % 4 == 2 ? qa.z : qa.w;
+        const uint32_t y = i % 4 == 0 ? qb.x : i % 4 == 1 ? qb.y : i % 4 == 2 ? qb.z : qb.w;
+        v[2 * i] = pack2(bf16_lo(x), bf16_lo(y)), v[2 * i + 1] = pack2(bf16_hi(x), bf16_hi(y));
       }
-      float lo[2] = {0.f, 0.f}, hi[2] = {0.f, 0.f};
+      if (had >= 2) stage16<1>(v);
+      if (had >= 4) stage16<2>(v);
+      if (had >= 8) stage16<4>(v);
+      if (had >= 16) stage16<8>(v);
+      __syncwarp();
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < 16; i += 2)
+        *reinterpret_cast<ulonglong2 *>(turn + 18 * l + i) = make_ulonglong2(v[i], v[i + 1]);
+      __syncwarp();
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          float x, y;
-          unpack2(v[4 * h + p], x, y);
-          lo[h] = min_nan(lo[h], min_nan(x, y)), hi[h] = max_nan(hi[h], max_nan(x, y));
-        }
-      if (whole) lo[0] = lo[1] = min_nan(lo[0], lo[1]), hi[0] = hi[1] = max_nan(hi[0], hi[1]);
+      for (int j = 0; j < 16; ++j) v[j] = turn[l + 8 * j + 2 * (j / 2)];
+      if (had >= 32) stage16<2>(v);
+      if (had >= 64) stage16<4>(v);
+      if (had >= 128) stage16<8>(v);
+      float lo[C], hi[C];
 #pragma unroll
-      for (int o = 1; o < LANES; o *= 2)
-        if (o < gl) {  // a whole row's group has more lanes than there are; half a row's exactly as many
-          lo[0] = min_nan(lo[0], __shfl_xor_sync(~0u, lo[0], o)), hi[0] = max_nan(hi[0], __shfl_xor_sync(~0u, hi[0], o));
-          if (!whole)
-            lo[1] = min_nan(lo[1], __shfl_xor_sync(~0u, lo[1], o)), hi[1] = max_nan(hi[1], __shfl_xor_sync(~0u, hi[1], o));
-        }
-      if (whole) lo[1] = lo[0], hi[1] = hi[0];
-      const int64_t row = slot * a.heads + w.head;
+      for (int i = 0; i < C; ++i) lo[i] = hi[i] = 0.f;
+      const f2 u2 = pack2(unit, unit);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const Step<float> g(lo[h], hi[h], qmax, step, half);
-        const float up = g.z + half;
-        const f2 inv2 = pack2(g.inv, g.inv), up2 = pack2(up, up);
-        uint32_t q[8];
+      for (int j = 0; j < 16; ++j) {
+        const int q = j / (16 / NG);
+        v[j] = mul2(v[j], u2);
+        float x, y;
+        unpack2(v[j], x, y);
+        lo[q] = min_nan(lo[q], x), hi[q] = max_nan(hi[q], x);
+        lo[NG + q] = min_nan(lo[NG + q], y), hi[NG + q] = max_nan(hi[NG + q], y);
+      }
+      // each round halves the groups a lane holds; with one left it adds lanes
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          float x, y;
-          unpack2(add2(mul2(v[4 * h + p], inv2), up2), x, y);
-          // within [0, qmax], then rounded down into the low bits of 2^23 + q
-          q[2 * p] = __float_as_uint(__fadd_rz(fminf(fmaxf(x, 0.f), qmax), 8388608.f));
-          q[2 * p + 1] = __float_as_uint(__fadd_rz(fminf(fmaxf(y, 0.f), qmax), 8388608.f));
-        }
-        if (slot >= 0) {
-          uint8_t *dst = a.codes + row * (HD / 8 * BITS) + h * (HD / 16 * BITS) + lane * BITS;
-          if constexpr (BITS == 8) {
-            uint2 o;
-            o.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
-            o.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
-            if (g.bad) o = make_uint2(0, 0);
-            *reinterpret_cast<uint2 *>(dst) = o;
-          } else {
-            uint32_t o = 0;
+      for (int d = 4, m = C; d; d /= 2) {
+        const bool upper = l & d;
+        if (m > 1) {
+          m /= 2;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o |= (q[i] & ((1u << BITS) - 1u)) << (BITS * i);
-            if (g.bad) o = 0;
-            if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(dst) = o;
-            else if constexpr (BITS == 2) *reinterpret_cast<uint16_t *>(dst) = (uint16_t)o;
-            else dst[0] = (uint8_t)o, dst[1] = (uint8_t)(o >> 8), dst[2] = (uint8_t)(o >> 16);
+          for (int i = 0; i < m; ++i) {
+            lo[i] = min_nan(upper ? lo[i + m] : lo[i], __shfl_xor_sync(~0u, upper ? lo[i] : lo[i + m], d));
+            hi[i] = max_nan(upper ? hi[i + m] : hi[i], __shfl_xor_sync(~0u, upper ? hi[i] : hi[i + m], d));
           }
-          const int gi = (h * (HD / 2) + lane * 8) / a.group;
-          if ((whole ? lane + h : lane % gl) == 0) {
-            a.scales[row * ng + gi] = g.bad ? __int_as_float(0x7fc00000) : g.s;
-            a.zeros[row * ng + gi] = g.bad ? 0 : (uint8_t)g.z;
-          }
+        } else {
+          lo[0] = min_nan(lo[0], __shfl_xor_sync(~0u, lo[0], d));
+          hi[0] = max_nan(hi[0], __shfl_xor_sync(~0u, hi[0], d));
         }
       }
+      Step<float> g(lo[0], hi[0], qmax, step, half);
+      const unsigned bad = __ballot_sync(~0u, g.bad) >> (lane & 24);  // of these eight lanes
+      if (g.bad) g.inv = g.z = 0.f;
+      {
+        const int mine = l >> kShift;
+        const int64_t unit_at = mine < NG ? to[0] : to[1];
+        if (unit_at >= 0 && (l & ((1 << kShift) - 1)) == 0) {
+          const int64_t at_group = unit_at * NG + mine % NG;
+          a.scales[at_group] = g.bad ? __int_as_float(0x7fc00000) : g.s;
+          a.zeros[at_group] = (uint8_t)g.z;
+        }
+      }
+      uint32_t code[2][16];
+#pragma unroll
+      for (int q = 0; q < NG; ++q) {
+        f2 inv2, up2;
+        {
+          const float i0 = __shfl_sync(~0u, g.inv, q << kShift, 8), i1 = __shfl_sync(~0u, g.inv, (q + NG) << kShift, 8);
+          const float z0 = __shfl_sync(~0u, g.z, q << kShift, 8), z1 = __shfl_sync(~0u, g.z, (q + NG) << kShift, 8);
+          inv2 = pack2(i0, i1), up2 = pack2(z0 + half, z1 + half);
+        }
+#pragma unroll
+        for (int j = q * (16 / NG); j < (q + 1) * (16 / NG); ++j) {
+          // Not below 0: -lo * inv + half < z + 1 up to 2^-16, and half is 2^-12 above
+          // one half, so lo * inv + z + half > 0. Rounding towards zero into 2^23 + code.
+          float x, y;
+          unpack2(add2(mul2(v[j], inv2), up2), x, y);
+          code[0][j] = __float_as_uint(__fadd_rz(fminf(x, qmax), 8388608.f));
+          code[1][j] = __float_as_uint(__fadd_rz(fminf(y, qmax), 8388608.f));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        store_unit<BITS>(a.codes + to[u] * (16 * BITS), code[u], l, to[u] >= 0, bad >> ((l * NG / 8 + u * NG) << kShift) & 1);
     }
   }
 }
@@ -697,24 +759,10 @@ int lanes_log2(const CachePair &c, int n_caches) {
   return ll;
 }
 
-// Whether the sixteen-element kernels take the call: caches alike in shape, rows
-// of 64 to 256 elements, power-of-two groups.
-bool takes16(qwha_dtype dt, const CachePair &c, int n_caches) {
-  const qwha_cache &a = c.cache[0], &b = c.cache[n_caches - 1];
-  return dt == QWHA_BF16 && a.bits == b.bits && a.head_dim == b.head_dim && is_pow2(a.head_dim) && a.head_dim >= 64 &&
-         is_pow2(a.group) && is_pow2(b.group);
-}
-
-template <int BITS>
-void write16(const CachePair &c, dim3 grid, int tile, const int64_t *slots, int64_t n, unsigned int *err, cudaStream_t s) {
-  const int hd = c.cache[0].head_dim;
-  if (hd == 64) cache_write16_kernel<BITS, 2><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err);
-  else if (hd == 128) cache_write16_kernel<BITS, 3><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err);
-  else cache_write16_kernel<BITS, 4><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err);
-}
-// Whether the tensor cores read the caches: units of 128 elements, groups that
-// hold whole columns of the first product, blocks inside a unit.
-bool takes_mma(const CachePair &c, int n_caches) {
+// Whether the kernels of units of 128 elements take the caches: groups of whole
+// columns of the first product, blocks inside a unit, and for writing bf16 rows
+// and groups inside a unit too.
+bool takes_units(const CachePair &c, int n_caches) {
   for (int i = 0; i < n_caches; ++i) {
     const qwha_cache &a = c.cache[i];
     if (a.bits != c.cache[0].bits || (int64_t)a.heads * a.head_dim % 128 || !is_pow2(a.group) || a.group < 32 ||
@@ -722,6 +770,20 @@ bool takes_mma(const CachePair &c, int n_caches) {
       return false;
   }
   return true;
+}
+bool writes_units(qwha_dtype dt, const CachePair &c, int n_caches) {
+  if (dt != QWHA_BF16 || !takes_units(c, n_caches)) return false;
+  const int g = c.cache[0].group;
+  return g <= 128 && g == c.cache[n_caches - 1].group;
+}
+template <int BITS>
+void write_units(const CachePair &c, dim3 grid, const int64_t *slots, int64_t n, int tile, unsigned int *err,
+                 cudaStream_t s) {
+  switch (c.cache[0].group) {
+    case 128: cache_write_unit_kernel<BITS, 1><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err); break;
+    case 64: cache_write_unit_kernel<BITS, 2><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err); break;
+    default: cache_write_unit_kernel<BITS, 4><<<grid, kCacheThreads, 0, s>>>(c, slots, n, tile, err);
+  }
 }
 template <typename T>
 void read_mma(const CachePair &c, dim3 grid, int tile, const ReadArgs &r, int64_t n, unsigned int *err,
@@ -740,7 +802,7 @@ int cache_max_head_dim() { return 256; }
 
 cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, const int64_t *slots, int64_t n,
                                cudaStream_t s) {
-  if (n_caches == 2 && !takes16(dt, c, 2) && (takes16(dt, c, 1) || takes16(dt, second(c), 1))) {
+  if (n_caches == 2 && !writes_units(dt, c, 2) && (writes_units(dt, c, 1) || writes_units(dt, second(c), 1))) {
     const cudaError_t e = launch_cache_write(dt, c, 1, slots, n, s);
     return e != cudaSuccess ? e : launch_cache_write(dt, second(c), 1, slots, n, s);
   }
@@ -748,12 +810,12 @@ cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, 
   const dim3 grid = tile_grid(n, tile, n_caches);
   unsigned int *err = device_error_word();
   if (!err) return cudaErrorInvalidDevicePointer;
-  if (takes16(dt, c, n_caches)) {
+  if (writes_units(dt, c, n_caches)) {
     switch (c.cache[0].bits) {
-      case 2: write16<2>(c, grid, tile, slots, n, err, s); break;
-      case 3: write16<3>(c, grid, tile, slots, n, err, s); break;
-      case 4: write16<4>(c, grid, tile, slots, n, err, s); break;
-      default: write16<8>(c, grid, tile, slots, n, err, s);
+      case 2: write_units<2>(c, grid, slots, n, tile, err, s); break;
+      case 3: write_units<3>(c, grid, slots, n, tile, err, s); break;
+      case 4: write_units<4>(c, grid, slots, n, tile, err, s); break;
+      default: write_units<8>(c, grid, slots, n, tile, err, s);
     }
     return cudaGetLastError();
   }
@@ -765,7 +827,7 @@ cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, 
 
 cudaError_t launch_cache_read(qwha_dtype dt, const CachePair &c, int n_caches, const ReadArgs &r, int64_t n,
                               cudaStream_t s) {
-  if (n_caches == 2 && !takes_mma(c, 2) && (takes_mma(c, 1) || takes_mma(second(c), 1))) {
+  if (n_caches == 2 && !takes_units(c, 2) && (takes_units(c, 1) || takes_units(second(c), 1))) {
     const cudaError_t e = launch_cache_read(dt, c, 1, r, n, s);
     return e != cudaSuccess ? e : launch_cache_read(dt, second(c), 1, r, n, s);
   }
@@ -773,7 +835,7 @@ cudaError_t launch_cache_read(qwha_dtype dt, const CachePair &c, int n_caches, c
   const dim3 grid = tile_grid(n, tile, n_caches);
   unsigned int *err = device_error_word();
   if (!err) return cudaErrorInvalidDevicePointer;
-  if (takes_mma(c, n_caches)) {
+  if (takes_units(c, n_caches)) {
     if (dt == QWHA_F32) read_mma<float>(c, grid, tile, r, n, err, s);
     else read_mma<__nv_bfloat16>(c, grid, tile, r, n, err, s);
     return cudaGetLastError();
