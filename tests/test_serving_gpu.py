@@ -421,6 +421,65 @@ def test_cache_read(shape, dtype):
         assert np.all(np.abs(got[:rows] - want) <= tol)
 
 
+def _written_and_read(W, g, shape, n, dtype, spoil):
+    """n rows in random slots, bit for bit, then read back one page after the other."""
+    import torch
+
+    heads, head_dim, bits, group, had_block, page_size = shape
+    n_pages = -(-n // page_size) + 1
+    c = _filled(W, g, n_pages, page_size, heads, head_dim, bits, group, had_block)
+    slots = g.permutation(n_pages * page_size)[:n].astype(np.int64)
+    slots[n // 3] = -1
+    x = _rows(g, n, heads, head_dim, dtype)
+    for i, v in enumerate(spoil):  # one value in a group, the rows around it stay whole
+        x[(5 * i + 1) % n, i % heads, (37 * i) % head_dim] = v
+    codes, scales, zeros = _state(c)
+    W.cache_write(c, _dev(x, dtype), to_dev(slots))
+    with np.errstate(invalid="ignore", over="ignore"):
+        q, s, z = quantize(x, bits, group, had_block, dtype)
+    live = slots >= 0
+    codes[slots[live]], scales[slots[live]], zeros[slots[live]] = pack(q, bits)[live], s[live], z[live]
+    got = _state(c)
+    assert np.array_equal(np.isnan(got[1]), np.isnan(scales))
+    assert np.array_equal(np.nan_to_num(got[1]), np.nan_to_num(scales))
+    assert np.array_equal(got[2], zeros)
+    assert np.array_equal(got[0], codes)
+    table = g.permutation(n_pages).astype(np.int32)[None]
+    rows = n_pages * page_size
+    out = W.cache_read(c, to_dev(table), to_dev(np.array([0, rows], np.int64)), rows,
+                       dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+    want, mag = _want_read(c, bits, group, had_block, table, [0], [rows], page_size)
+    m = had_block or 1
+    blk = np.repeat(mag.reshape(rows, heads, -1, m).sum(-1) / np.sqrt(m), m, axis=-1)
+    tol = half_step(dtype) * 1.01 * np.abs(want) + (np.log2(m) + 3) * 2.0**-24 * blk + 1e-30
+    got = host(out)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.all((np.abs(got - want) <= tol) | np.isnan(want))
+
+
+@pytest.mark.parametrize("had_block", [0, 2, 4, 8, 16, 32, 64, 128])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+def test_cache_units_of_128(bits, group, had_block):
+    """Every block with every group and code in rows that make up units of 128 elements: an odd number of units to a
+    token, values that spoil a group."""
+    W = _W()
+    g = rng_for(110, "units", bits, group, had_block)
+    for dtype in ("bf16", "f32"):
+        _written_and_read(W, g, (3, 128, bits, group, had_block, 5), 23, dtype, (np.inf, np.nan, -np.inf))
+        if group <= 64 and had_block <= 64:
+            _written_and_read(W, g, (2, 64, bits, group, had_block, 16), 9, dtype, ())
+
+
+@pytest.mark.parametrize("shape,n", [((300, 128, 4, 64, 128, 16), 9), ((8, 32, 4, 32, 32, 64), 5000),
+                                     ((1, 128, 3, 128, 64, 16), 20000), ((6, 64, 8, 32, 16, 32), 4000),
+                                     ((4, 256, 2, 256, 64, 16), 40)])
+def test_cache_many_units_to_a_tile(shape, n):
+    """Tiles of several tokens, tokens of more units than a tile holds, groups of two units."""
+    g = rng_for(111, "tiles", *shape)
+    _written_and_read(_W(), g, shape, n, "bf16", (np.inf,))
+
+
 def test_cache_read_bad_pages_are_left_and_reported():
     W = _W()
     import walsh_hadamard_sparse_b200._lib as L

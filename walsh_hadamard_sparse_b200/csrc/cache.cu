@@ -512,10 +512,13 @@ __device__ __forceinline__ f2 sub2(f2 a, f2 b) {
   asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// The products one by one: the assembler contracts a packed product and a packed
+// sum, .rn or not, into one rounding, and the quantizer has two.
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
+  float a0, a1, b0, b1;
+  unpack2(a, a0, a1);
+  unpack2(b, b0, b1);
+  return pack2(__fmul_rn(a0, b0), __fmul_rn(a1, b1));
 }
 
 // Butterflies between v[i] and v[i + H].
@@ -541,12 +544,18 @@ __device__ __forceinline__ uint32_t turn_nibbles(uint32_t r, int l) {
   return (r & keep) | (__funnelshift_l(x, x, l & 1 ? 28 : 4) & ~keep);
 }
 
-// Eight nibbles of BITS < 4 bits, closed up.
+// Eight nibbles of two or three bits, closed up.
 template <int BITS>
 __device__ __forceinline__ uint32_t close_up(uint32_t w) {
-  w = (w | w >> (4 - BITS)) & (BITS == 3 ? 0x3f3f3f3fu : 0x0f0f0f0fu);
-  w = (w | w >> (8 - 2 * BITS)) & (BITS == 3 ? 0x0fff0fffu : 0x00ff00ffu);
-  return (w | w >> (16 - 4 * BITS)) & ((1u << (8 * BITS)) - 1u);
+  if constexpr (BITS == 2) {
+    w = (w & 0x03030303u) | (w >> 2 & 0x0c0c0c0cu);
+    w = (w & 0x000f000fu) | (w >> 4 & 0x00f000f0u);
+    return (w & 0xffu) | (w >> 8 & 0xff00u);
+  } else {
+    w = (w & 0x07070707u) | (w >> 1 & 0x38383838u);
+    w = (w & 0x003f003fu) | (w >> 2 & 0x0fc00fc0u);
+    return (w & 0xfffu) | (w >> 4 & 0xfff000u);
+  }
 }
 
 // Stores a unit's codes q[j] = 2^23 + code of element l + 8 j (fp32 bits): the
