@@ -59,11 +59,13 @@ int sm_count() {
 }
 
 cudaError_t allow_smem(const void *kernel, size_t bytes, std::atomic<size_t> (&allowed)[64]) {
+  static std::mutex raising;  // the record follows the attribute
   std::atomic<size_t> &most = allowed[device_slot()];
-  if (bytes <= 48 * 1024 || bytes <= most.load(std::memory_order_relaxed)) return cudaSuccess;
+  if (bytes <= 32 * 1024 || bytes <= most.load(std::memory_order_acquire)) return cudaSuccess;
+  std::lock_guard<std::mutex> lock(raising);
+  if (bytes <= most.load(std::memory_order_relaxed)) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  // a smaller size set by another thread afterwards would only make this one ask again, so keep the smaller record
-  if (e == cudaSuccess) most.store(bytes, std::memory_order_relaxed);
+  if (e == cudaSuccess) most.store(bytes, std::memory_order_release);
   return e;
 }
 
@@ -876,6 +878,7 @@ qwha_status decode_call(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtyp
   if (tensor) gemv_place_x(&g, ws);
   if (a && a->p > 0) {
     g.row_ptr = a->row_ptr, g.col_idx = a->col_idx, g.coef = a->coef, g.p = a->p, g.alpha = alpha;
+    if (!(g.err = device_error_word())) return fail(QWHA_ERR_CUDA, "no error word");
     gemv_place_z(&g, static_cast<char *>(ws) + (wq ? qgemv_ws(d_in, T, g.f32) : 0));
   }
   g.prepared = tensor || g.zt || Z_out;

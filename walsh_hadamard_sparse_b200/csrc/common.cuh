@@ -31,7 +31,8 @@ int sm_count();  // multiprocessors of the current device
 int device_slot();  // index of the current device in [0, 64) (0 if unreadable), for per-device caches
 
 // Let `kernel` have `bytes` of dynamic shared memory on the current device: asked for once per kernel, size and device
-// (a launch of at most 48 KB needs no asking). `allowed` is the kernel's own record, one per device slot.
+// (48 KB of dynamic and static memory together need no asking; a kernel of this library has less than 16 KB static
+// where it asks). `allowed` is the kernel's own record, one per device slot.
 cudaError_t allow_smem(const void *kernel, size_t bytes, std::atomic<size_t> (&allowed)[64]);
 
 // Device error word for bounded waits (set by kernels, read by

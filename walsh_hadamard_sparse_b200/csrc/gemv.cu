@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const Gemv
                                                                       float scale, T *z_out) {
   extern __shared__ __align__(16) float row[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may start on the weight
+  if (a.ready && blockIdx.x == 0 && threadIdx.x == 0) *a.ready = 0;
   if ((int)blockIdx.x >= spans) {
     const int parts = (a.d_in + 127) / 128 * 16, i = (blockIdx.x - spans) * kPrepThreads + threadIdx.x;
     gemv::prepare_piece<BITS, T>(a, i / parts, i % parts, i < a.T * parts, a.T * a.pieces, a.xpieces, a.xsums);
@@ -152,11 +153,15 @@ __global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const Gemv
   }
 }
 
-constexpr int kEntThreads = 1024, kEntWarps = kEntThreads / 32;
+constexpr int kEntThreads = 512, kEntWarps = kEntThreads / 32;
 constexpr int kEntRows = 1024;  // rows of a CTA whose borders are kept in shared memory
 constexpr int kLongRow = 256, kHugeRow = 1024;
 constexpr size_t kEntSmem = 200 * 1024;
-constexpr unsigned kErrEntries = 0x8000u;  // a wait for a copy gave up
+
+// 16 bytes into shared memory, zeros behind the first `bytes`.
+__device__ __forceinline__ void copy16(void *dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(bulk::saddr(dst)), "l"(src), "r"(bytes) : "memory");
+}
 
 // Sum over n entries by 1 << LANES_LOG2 lanes, four entries a lane in flight.
 template <int TG, int LANES_LOG2>
@@ -171,8 +176,8 @@ __device__ __forceinline__ void row_sum(const int32_t *cols, const float *coefs,
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const bool in = j + u * L < n;
-      k[u] = in ? __ldg(cols + j + u * L) : -1;
-      c[u] = in ? __ldg(coefs + j + u * L) : 0.f;
+      k[u] = in ? cols[j + u * L] : -1;
+      c[u] = in ? coefs[j + u * L] : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -213,43 +218,63 @@ __device__ __forceinline__ void row_sum(const int32_t *cols, const float *coefs,
 // entries; 8 to 32 lanes, as the CTA's rows are many or few, take a row of up
 // to kLongRow entries, a warp a longer one, the CTA one above kHugeRow. Every sum has one place and one order.
 template <int TG>
-__global__ void __launch_bounds__(kEntThreads, 1)
-    decode_entries_kernel(const GemvArgs a, int buffers, unsigned int *err) {
-  extern __shared__ __align__(16) float zs_all[];  // [buffers][d_in][TG]
-  __shared__ int rp_s[kEntRows + 1], counts[2];
+__global__ void __launch_bounds__(kEntThreads, 2)
+    decode_entries_kernel(const GemvArgs a, int buffers, int stage) {
+  extern __shared__ __align__(16) float zs_all[];  // [buffers][d_in][TG], columns [stage], coefficients [stage]
+  __shared__ int rp_s[kEntRows + 1];
   __shared__ float part[kEntWarps][TG];
   __shared__ uint64_t s_bar[2];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may start on the weight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x < 2) {
     bulk::init(bulk::saddr(s_bar + threadIdx.x), 1);
     bulk::fence_init();
-    counts[threadIdx.x] = 0;
   }
-  __syncthreads();
   auto border = [&](int r) {
     const int b = a.row_ptr[r];
     return b < 0 ? 0 : b > a.p ? (int)a.p : b;
   };
-  // the CTA's rows: those whose entries start at or behind its share's first entry, before the next share's
-  const int64_t share = (a.p + gridDim.x - 1) / gridDim.x, s0 = blockIdx.x * share, s1 = s0 + share;
-  {
-    int n0 = 0, n1 = 0;
-#pragma unroll 4
-    for (int r = threadIdx.x; r < a.d_out; r += kEntThreads) {
-      const int b = border(r);
-      n0 += b < s0, n1 += b < s1;
+  // The CTA's rows: those whose entries start at or behind its share's first entry, before the next share's. The
+  // first such row lies behind the last of every step-th row that starts before the share.
+  const int64_t share = (a.p + gridDim.x - 1) / gridDim.x;
+  const int step = (a.d_out + kEntThreads - 1) / kEntThreads;
+  int r_of[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int64_t at = (blockIdx.x + e) * share;
+    const int r = (int)threadIdx.x * step;
+    const int n = __syncthreads_count(r < a.d_out && border(r) < at);
+    const int from = n ? (n - 1) * step + 1 : 0, to = n * step < a.d_out ? n * step : a.d_out;
+    int more = 0;
+    for (int q = from; q < to; q += kEntThreads) {
+      const int i = q + (int)threadIdx.x;
+      more += __syncthreads_count(i < to && border(i) < at);
     }
-    n0 = __reduce_add_sync(~0u, n0), n1 = __reduce_add_sync(~0u, n1);
-    if (lane == 0) atomicAdd(counts, n0), atomicAdd(counts + 1, n1);
+    r_of[e] = from + more;
   }
-  __syncthreads();
-  const int r0 = blockIdx.x == 0 ? 0 : counts[0], r1 = blockIdx.x == gridDim.x - 1 ? a.d_out : counts[1];
+  const int r0 = blockIdx.x == 0 ? 0 : r_of[0], r1 = blockIdx.x == gridDim.x - 1 ? a.d_out : r_of[1] > r0 ? r_of[1] : r0;
   const bool near = r1 - r0 <= kEntRows;
   for (int i = threadIdx.x; near && i <= r1 - r0; i += kEntThreads) rp_s[i] = border(r0 + i);
   auto row_at = [&](int r) { return near ? rp_s[r - r0] : border(r); };
+  // the entries of these rows, as many as there is room for, from a multiple of four on
+  const int e0 = border(r0) & ~3;
+  int staged = border(r1) - e0;
+  staged = staged < 0 ? 0 : staged < stage ? staged : stage;
+  int32_t *cols_s = reinterpret_cast<int32_t *>(zs_all + (size_t)buffers * a.d_in * TG);
+  float *coefs_s = reinterpret_cast<float *>(cols_s + stage);
+  for (int i = threadIdx.x * 4; i < staged; i += kEntThreads * 4) {
+    const int64_t left = a.p - e0 - i;
+    const uint32_t bytes = left < 4 ? (uint32_t)left * 4 : 16;
+    copy16(cols_s + i, a.col_idx + e0 + i, bytes);
+    copy16(coefs_s + i, a.coef + e0 + i, bytes);
+  }
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // Z is the preparing launch's output
+  // Z is the preparing launch's output. The product behind this launch may start once that is complete, and runs
+  // beside it: it waits for `ready` before it reads the operands and for this launch before it adds the sums.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0)
+    asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(a.ready) : "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("cp.async.wait_all;" ::: "memory");
   // turn n: the tokens of group n; with two buffers the next turn's Z is on its way
   const int turns = a.tp / TG;
   const uint32_t bytes = a.d_in * TG * 4;
@@ -267,7 +292,7 @@ __global__ void __launch_bounds__(kEntThreads, 1)
     if (buffers) {
       if (threadIdx.x == 0 && (buffers == 2 ? n + 1 < turns : n > 0)) copy_z(buffers == 2 ? n + 1 : n);
       // incomplete if it gives up, reported through the error word
-      if (!bulk::wait(bulk::saddr(s_bar + n % 2), (uint32_t)(n / 2 & 1))) atomicOr(err, kErrEntries);
+      if (!bulk::wait(bulk::saddr(s_bar + n % 2), (uint32_t)(n / 2 & 1))) atomicOr(a.err, kErrEntries);
       __syncwarp();
     }
     auto put = [&](int r, const float *acc) {
@@ -293,7 +318,10 @@ __global__ void __launch_bounds__(kEntThreads, 1)
           len = row_at(r + 1) - b;
           if (len < 0) len = 0;
         }
-        row_sum<TG, ll>(a.col_idx + b, a.coef + b, len > kLongRow ? 0 : len, zs, a.d_in, lane & ((1 << ll) - 1), acc);
+        const int at = b - e0;
+        const bool near_by = at >= 0 && at + len <= staged;
+        row_sum<TG, ll>(near_by ? cols_s + at : a.col_idx + b, near_by ? coefs_s + at : a.coef + b,
+                        len > kLongRow ? 0 : len, zs, a.d_in, lane & ((1 << ll) - 1), acc);
         if ((lane & ((1 << ll) - 1)) == 0 && len >= 0 && len <= kLongRow) put(r, acc);
       }
     };
@@ -309,7 +337,9 @@ __global__ void __launch_bounds__(kEntThreads, 1)
         const int at = __ffs(some) - 1, b = row_at(q + at), len = row_at(q + at + 1) - b;
         some &= some - 1;
         if (((q - r0) + at) % kEntWarps != warp) continue;
-        row_sum<TG, 5>(a.col_idx + b, a.coef + b, len, zs, a.d_in, lane, acc);
+        const bool near_by = b >= e0 && b - e0 + len <= staged;
+        row_sum<TG, 5>(near_by ? cols_s + (b - e0) : a.col_idx + b, near_by ? coefs_s + (b - e0) : a.coef + b, len, zs,
+                       a.d_in, lane, acc);
         if (lane == 0) put(q + at, acc);
       }
       while (huge) {
@@ -324,7 +354,7 @@ __global__ void __launch_bounds__(kEntThreads, 1)
         __syncthreads();
         if (warp == 0) {
 #pragma unroll
-          for (int i = 0; i < TG; ++i) acc[i] = warp_sum(part[lane][i]);
+          for (int i = 0; i < TG; ++i) acc[i] = warp_sum(lane < kEntWarps ? part[lane][i] : 0.f);
           if (lane == 0) put(q + at, acc);
         }
         __syncthreads();
@@ -336,25 +366,28 @@ __global__ void __launch_bounds__(kEntThreads, 1)
 template <int TG>
 cudaError_t entries(const GemvArgs &a, cudaStream_t s) {
   const size_t group_bytes = (size_t)a.d_in * TG * sizeof(float);
-  const int buffers = 2 * group_bytes <= kEntSmem && a.tp > TG ? 2 : group_bytes <= kEntSmem ? 1 : 0;
+  const int buffers = 2 * group_bytes <= kEntSmem * 2 / 3 && a.tp > TG ? 2 : group_bytes <= kEntSmem ? 1 : 0;
+  // a CTA an SM, with 256 entries at least
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(sm_count(), a.p / 256));
+  // room for a share of the entries, and half of one more: whole rows make shares uneven
+  const int64_t room = (int64_t)(kEntSmem - buffers * group_bytes) / 8, share = cdiv(a.p, grid);
+  const int stage = (int)std::min<int64_t>(room, share + share / 2 + 256) & ~3;
+  const size_t smem = buffers * group_bytes + (size_t)stage * 8;
   auto kernel = decode_entries_kernel<TG>;
   static std::atomic<size_t> allowed[64];
-  const cudaError_t e = allow_smem((const void *)kernel, buffers * group_bytes, allowed);
+  const cudaError_t e = allow_smem((const void *)kernel, smem, allowed);
   if (e != cudaSuccess) return e;
-  unsigned int *err = device_error_word();
-  if (!err) return cudaErrorInvalidDevicePointer;
   cudaLaunchConfig_t cfg = {};
-  // a CTA an SM, with 256 entries at least
-  cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(sm_count(), a.p / 256)));
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kEntThreads);
-  cfg.dynamicSmemBytes = buffers * group_bytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;  // overlaps the preparing launch, which is the one before
-  return cudaLaunchKernelEx(&cfg, kernel, a, buffers, err);
+  return cudaLaunchKernelEx(&cfg, kernel, a, buffers, stage);
 }
 
 template <int BITS, typename T>
@@ -405,14 +438,15 @@ int group_tokens(int64_t T) { return T <= 2 ? (int)T : T <= 4 ? 4 : 8; }
 size_t gemv_z_bytes(int32_t d_out, int32_t d_in, int64_t T) {
   if (T <= 0) return 0;
   const size_t tp = cdiv(T, group_tokens(T)) * group_tokens(T);
-  return align_up(tp * d_in * 4, 256) + align_up(tp * d_out * 4, 256);
+  return align_up(tp * d_in * 4, 256) + align_up(tp * d_out * 4, 256) + 256;
 }
 
 void gemv_place_z(GemvArgs *a, void *ws) {
   a->tg = group_tokens(a->T);
   a->tp = (a->T + a->tg - 1) / a->tg * a->tg;
-  a->zt = static_cast<float *>(ws);
-  a->y_ad = reinterpret_cast<float *>(static_cast<char *>(ws) + align_up((size_t)a->tp * a->d_in * 4, 256));
+  a->ready = static_cast<unsigned int *>(ws);
+  a->zt = reinterpret_cast<float *>(static_cast<char *>(ws) + 256);
+  a->y_ad = a->zt + align_up((size_t)a->tp * a->d_in * 4, 256) / 4;
 }
 
 cudaError_t launch_decode_entries(const GemvArgs &a, cudaStream_t s) {

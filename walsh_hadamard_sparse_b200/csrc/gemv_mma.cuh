@@ -37,6 +37,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "bulk.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -237,6 +238,17 @@ struct Chunk {
   uint32_t z[2 * MT];
 };
 
+// Whether the word became 1 (in time); what was written before it is visible then.
+__device__ __forceinline__ bool wait_ready(const unsigned int *word) {
+  const uint64_t begin = bulk::now_ns();
+  for (;;) {
+    unsigned int v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
+    if (v == 1) return true;
+    if (bulk::now_ns() - begin > bulk::kWaitNs) return false;
+  }
+}
+
 template <int BITS>
 __device__ __forceinline__ void f_zero(uint32_t *w) {
 #pragma unroll
@@ -325,8 +337,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
     }
   each<DEPTH>([&](auto I) { fetch(buf[decltype(I)::value], c_begin + decltype(I)::value, I); });
 
-  // the values (and the entries' sums) are outputs of the launches before: wait for them only here
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The values are the preparing launch's output: wait for it only here. With the entries' launch in between, which
+  // runs beside this one, its word says so.
+  if (a.y_ad) {
+    if (lane == 0 && !wait_ready(a.ready)) atomicOr(a.err, kErrEntries);
+    __syncwarp();
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
   const int pieces = a.pieces, v_end = np * pieces, v_most = tokens_per_pass * pieces;
   const int n_tiles = x_tiles(a.T * pieces, G), nt0 = t0 * pieces / TPN;
   // this lane's column of an n-tile: a piece, live where the column's group is the lane's own
@@ -411,6 +429,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
         if (v + j < v_end) dst[j * ROWS + m * 16] = acc[m][n][j], dst[j * ROWS + m * 16 + 8] = acc[m][n][2 + j];
   }
   const int rows_here = tiles_here * ROWS < a.d_out - row_first ? tiles_here * ROWS : a.d_out - row_first;
+  if (a.y_ad) asm volatile("griddepcontrol.wait;" ::: "memory");  // for the entries' sums
   __syncthreads();
   for (int i = threadIdx.x; i < tiles_here * ROWS * np; i += blockDim.x) {
     const int r = i % (tiles_here * ROWS), tok = i / (tiles_here * ROWS);
@@ -452,7 +471,7 @@ cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = a.prepared ? 1 : 0;  // overlaps the preparing launch
+  cfg.numAttrs = a.prepared ? 1 : 0;  // overlaps the launches of its call before it
   return cudaLaunchKernelEx(&cfg, kernel, a, tpp, slices);
 }
 

@@ -153,6 +153,7 @@ namespace qwha {
 // operands and transform (launch_decode_prepare), the entries of E
 // (launch_decode_entries), the product (launch_gemv). qw NULL: no base term;
 // row_ptr NULL: no adapter term.
+constexpr unsigned int kErrEntries = 0x8000u;  // a wait of the decode call gave up
 struct GemvArgs {
   const uint8_t *qw;
   const float *scales;
@@ -168,6 +169,8 @@ struct GemvArgs {
   // Z = X H in fp32 by groups of tg tokens: zt [tp / tg][d_in][tg]; the entries' sums y_ad [d_out][tp].
   float *zt, *y_ad;
   int tg, tp;
+  unsigned int *ready;  // 1 once the preparing launch is complete (beside zt)
+  unsigned int *err;    // the device's error word
   // The values as operands, `pieces` columns a token, TPN = 8 / G columns to an n-tile (G groups in a chunk of 128
   // columns): xpieces [chunk][n-tile][4][TPN][4 runs] of 16 bytes, xsums [chunk][n-tile][8] (sum, factor) pairs.
   int pieces;
