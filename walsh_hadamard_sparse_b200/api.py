@@ -173,10 +173,16 @@ def _fit(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int)
     return t.data_ptr()
 
 
-def _fit_ws(ws: torch.Tensor, dev: int) -> int:
+def _new_ws(X: torch.Tensor, nbytes: int) -> torch.Tensor | None:
+    return X.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+
+
+def _fit_ws(ws: torch.Tensor | None, dev: int) -> tuple[int | None, int]:
+    if ws is None:
+        return None, 0
     if not ws.is_cuda or not ws.is_contiguous() or ws.get_device() != dev:
         raise ValueError(f"ws: expected a contiguous tensor on cuda:{dev}")
-    return ws.data_ptr()
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _fit_weight(wq: QWeight, d_out: int, d_in: int, dev: int) -> QwhaQweight:
@@ -204,8 +210,8 @@ def qgemv(wq: QWeight, X: torch.Tensor, Y: torch.Tensor | None = None,
     if Y is None:
         Y = X.new_empty((T, d_out))
     if ws is None:
-        ws = X.new_empty(h.qwha_workspace_size(OP_QGEMV, d_out, d_in, 0, T, 2 - dt), dtype=torch.uint8)
-    check(h.qwha_qgemv(cw, d_out, d_in, dt, x, T, _fit("Y", Y, X.dtype, (T, d_out), dev), _fit_ws(ws, dev), ws.numel(),
+        ws = _new_ws(X, h.qwha_workspace_size(OP_QGEMV, d_out, d_in, 0, T, 2 - dt))
+    check(h.qwha_qgemv(cw, d_out, d_in, dt, x, T, _fit("Y", Y, X.dtype, (T, d_out), dev), *_fit_ws(ws, dev),
                        _raw_stream(dev)), "qwha_qgemv")
     return Y
 
@@ -228,11 +234,10 @@ def adapter_decode(a: Adapter, X: torch.Tensor, alpha: float = 1.0, wq: QWeight 
     if Y is None:
         Y = X.new_empty((T, d_out))
     if ws is None:
-        ws = X.new_empty(h.qwha_workspace_size(OP_DECODE, d_out, d_in, a.p, T, 0 if cw is None else 2 - dt),
-                         dtype=torch.uint8)
+        ws = _new_ws(X, h.qwha_workspace_size(OP_DECODE, d_out, d_in, a.p, T, 0 if cw is None else 2 - dt))
     check(h.qwha_adapter_decode(cs, cw, dt, x, T, alpha,
                                 None if Z_out is None else _fit("Z_out", Z_out, X.dtype, (T, d_in), dev),
-                                _fit("Y", Y, X.dtype, (T, d_out), dev), _fit_ws(ws, dev), ws.numel(), _raw_stream(dev)),
+                                _fit("Y", Y, X.dtype, (T, d_out), dev), *_fit_ws(ws, dev), _raw_stream(dev)),
           "qwha_adapter_decode")
     return Y
 
@@ -343,7 +348,7 @@ def validate_slots(cache: QCache, slots: torch.Tensor, ws: torch.Tensor | None =
     p = _fit("slots", slots, torch.int64, (slots.shape[0],), dev)
     cs = cache.c_struct(dev)
     ws = _ws(workspace_size(OP_SLOTS, 1, 1, cache.n_slots, 0, False), slots.device) if ws is None else ws
-    check(lib().qwha_validate_slots(cs, p, slots.shape[0], _fit_ws(ws, dev), ws.numel(), _raw_stream(dev)),
+    check(lib().qwha_validate_slots(cs, p, slots.shape[0], *_fit_ws(ws, dev), _raw_stream(dev)),
           "qwha_validate_slots")
 
 

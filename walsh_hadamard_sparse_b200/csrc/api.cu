@@ -404,11 +404,11 @@ size_t bwd_ws(int32_t d_out, int32_t d_in, int64_t p, int64_t T, bool base) {
 // The tokens as the tensor-core product reads them, then Z in fp32 and the
 // entries' sums.
 size_t qgemv_ws(int32_t d_in, int64_t T, bool f32) {
-  return gemv_x_bytes(d_in, std::min<int64_t>(T, QWHA_DECODE_MAX_T), f32);
+  return gemv_own_x(d_in, T, f32) ? 0 : gemv_x_bytes(d_in, std::min<int64_t>(T, QWHA_DECODE_MAX_T), f32);
 }
 size_t decode_ws(int32_t d_out, int32_t d_in, int64_t p, int64_t T, bool base, bool f32) {
   const int64_t n = std::min<int64_t>(T, QWHA_DECODE_MAX_T);
-  return (base ? qgemv_ws(d_in, T, f32) : 0) + (p > 0 ? gemv_z_bytes(d_out, d_in, n) : 0);
+  return (base ? gemv_x_bytes(d_in, n, f32) : 0) + (p > 0 ? gemv_z_bytes(d_out, d_in, n) : 0);
 }
 
 // Dense backward: W_eff, dX = dY W_eff (W_eff read MN-major), and dc = alpha *
@@ -876,12 +876,13 @@ qwha_status decode_call(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtyp
   g.d_out = d_out, g.d_in = d_in, g.x = X, g.T = (int)T, g.f32 = dt == QWHA_F32, g.y = Y;
   const bool tensor = gemv_on_tensor_cores(g.qw, g.group);
   if (tensor) gemv_place_x(&g, ws);
+  if (!a && gemv_own_x(d_in, T, g.f32)) g.xpieces = nullptr;
   if (a && a->p > 0) {
     g.row_ptr = a->row_ptr, g.col_idx = a->col_idx, g.coef = a->coef, g.p = a->p, g.alpha = alpha;
     if (!(g.err = device_error_word())) return fail(QWHA_ERR_CUDA, "no error word");
-    gemv_place_z(&g, static_cast<char *>(ws) + (wq ? qgemv_ws(d_in, T, g.f32) : 0));
+    gemv_place_z(&g, static_cast<char *>(ws) + (wq ? gemv_x_bytes(d_in, T, g.f32) : 0));
   }
-  g.prepared = tensor || g.zt || Z_out;
+  g.prepared = g.xpieces || g.zt || Z_out;
   if (g.prepared) {
     StageScope sc(ST_DECODE_PREPARE, 1, s);
     qwha_status st = cuda_status(launch_decode_prepare(g, a ? ilog2(a->had_block) : 0, Z_out, s), "decode preparation");

@@ -170,7 +170,9 @@ __device__ __forceinline__ float exp2i(int k) { return __int_as_float((k + 127) 
 // applied at the end, so that neither leaves fp32's range). A chunk with an
 // infinity or a NaN gets the factor NaN, which sends its rows' sums to the
 // plain path.
-template <int BITS, typename T>
+// In shared memory (OWN: one n-tile) a column's pieces lie together, `cols` being
+// the stride between columns.
+template <int BITS, bool OWN, typename T>
 __device__ __forceinline__ void prepare_piece(const GemvArgs &a, int tok, int i, bool live, int cols, uint4 *pieces,
                                               float2 *sums) {
   const int run = i >> 2, j = i & 3, chunk = run >> 2, t = run & 3, k0 = run * 32;
@@ -205,7 +207,7 @@ __device__ __forceinline__ void prepare_piece(const GemvArgs &a, int tok, int i,
   sum = G == 1 ? sum4 : G == 2 ? sum2 : sum;
   for (int p = 0; p < a.pieces; ++p) {
     const int col = tok * a.pieces + p, TPN = 8 / G;
-    const int64_t tile = (int64_t)chunk * x_tiles(cols, G) + col / TPN;
+    const int64_t tile = OWN ? chunk : (int64_t)chunk * x_tiles(cols, G) + col / TPN;
     uint32_t r[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -223,19 +225,21 @@ __device__ __forceinline__ void prepare_piece(const GemvArgs &a, int tok, int i,
       r[k] = *reinterpret_cast<const uint32_t *>(&d);
       v[k] -= __low2float(h), v[4 + k] -= __high2float(h);
     }
-    pieces[tile * (16 * TPN) + j * (4 * TPN) + col % TPN * 4 + t] = make_uint4(r[0], r[1], r[2], r[3]);
+    pieces[OWN ? col * cols + chunk * 16 + j * 4 + t : tile * (16 * TPN) + j * (4 * TPN) + col % TPN * 4 + t] =
+        make_uint4(r[0], r[1], r[2], r[3]);
     if (j == 0 && t % (4 / G) == 0)
       sums[tile * 8 + t * G / 4 * TPN + col % TPN] =
           make_float2(p == 0 ? sum * 0x1p-24f : 0.f, finite ? exp2i(12 - up) : __int_as_float(0x7fc00000));
   }
 }
 
-// What a lane holds of a chunk: its runs of 2 MT rows, their scales and zero points.
-template <int BITS, int MT>
+// What a lane holds of a chunk: its runs of 2 MT rows, with their scales and
+// zero points where it has groups of its own (G > 1).
+template <int BITS, int G, int MT>
 struct Chunk {
   uint32_t w[2 * MT][BITS];
-  float s[2 * MT];
-  uint32_t z[2 * MT];
+  float s[G > 1 ? 2 * MT : 1];
+  uint32_t z[G > 1 ? 2 * MT : 1];
 };
 
 // Whether the word became 1 (in time); what was written before it is visible then.
@@ -248,6 +252,12 @@ __device__ __forceinline__ bool wait_ready(const unsigned int *word) {
     if (bulk::now_ns() - begin > bulk::kWaitNs) return false;
   }
 }
+
+// A lane's operands of an n-tile, and the (sum, factor) pairs of its two columns.
+struct XTile {
+  uint4 x[4];
+  float4 f;
+};
 
 template <int BITS>
 __device__ __forceinline__ void f_zero(uint32_t *w) {
@@ -280,7 +290,8 @@ __device__ __forceinline__ void load_run(const uint8_t *p, uint32_t *w) {
 }
 
 // EXACT: the group is 128 / G columns, so a chunk's groups follow the chunk.
-template <int BITS, int G, int NT, int MT, int DEPTH, bool EXACT>
+// OWN: no launch prepared the operands; every CTA makes its own in shared memory.
+template <int BITS, int G, int NT, int MT, int DEPTH, bool EXACT, bool OWN>
 __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
     gemv_mma_kernel(const GemvArgs a, int tokens_per_pass, int slices) {
   constexpr int TPN = 8 / G, ROWS = 16 * MT, ROW_CHUNK = 16 * BITS;
@@ -312,45 +323,112 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
     }
   }
   // chunk c + I, I chunks behind the pointers
-  auto fetch = [&](Chunk<BITS, MT> &f, int c, auto I) {
+  auto fetch = [&](Chunk<BITS, G, MT> &f, int c, auto I) {
     constexpr int i = decltype(I)::value;
     const int k0 = c * 128 + t * 32;
     const bool on = c < c_end && (G == 1 || k0 < a.d_in);
 #pragma unroll
     for (int h = 0; h < 2 * MT; ++h) {
-      f.s[h] = 0.f;
-      if (on) {
-        load_run<BITS, i * ROW_CHUNK>(pw[h], f.w[h]);
+      if constexpr (G > 1) f.s[h] = 0.f;
+      if (!on) continue;
+      load_run<BITS, i * ROW_CHUNK>(pw[h], f.w[h]);
+      if constexpr (G > 1) {
         const int gi = EXACT ? i * G : k0 / a.group;
         f.s[h] = __ldg(ps[h] + gi);
         f.z[h] = __ldg(pz[h] + gi);
       }
     }
   };
-  Chunk<BITS, MT> buf[DEPTH];
+  // With one group to a chunk, the four lanes of a row load those of four chunks and hand them round: requests to
+  // the L1, eight rows to each, bound the product before memory does (a scale and a zero point a chunk and lane
+  // were half of them).
+  float sn[2 * MT], zn[2 * MT], s4[2 * MT], z4[2 * MT];
+  auto fetch_scales = [&](int c) {  // of chunks c .. c + 3
+    const int ct = c + t;
+#pragma unroll
+    for (int h = 0; h < 2 * MT; ++h) {
+      sn[h] = 0.f, zn[h] = 0.f;
+      if (ct < c_end) {
+        const int gi = EXACT ? ct - c_begin : ct * 128 / a.group;
+        sn[h] = __ldg(ps[h] + gi);
+        zn[h] = (float)__ldg(pz[h] + gi);
+      }
+    }
+  };
+  Chunk<BITS, G, MT> buf[DEPTH];
 #pragma unroll
   for (int i = 0; i < DEPTH; ++i)
 #pragma unroll
     for (int h = 0; h < 2 * MT; ++h) {
       f_zero<BITS>(buf[i].w[h]);
-      buf[i].z[h] = 0;
+      if constexpr (G > 1) buf[i].z[h] = 0;
     }
+  if constexpr (G == 1) fetch_scales(c_begin);
   each<DEPTH>([&](auto I) { fetch(buf[decltype(I)::value], c_begin + decltype(I)::value, I); });
 
-  // The values are the preparing launch's output: wait for it only here. With the entries' launch in between, which
-  // runs beside this one, its word says so.
-  if (a.y_ad) {
-    if (lane == 0 && !wait_ready(a.ready)) atomicOr(a.err, kErrEntries);
-    __syncwarp();
-  } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-  }
   const int pieces = a.pieces, v_end = np * pieces, v_most = tokens_per_pass * pieces;
   const int n_tiles = x_tiles(a.T * pieces, G), nt0 = t0 * pieces / TPN;
   // this lane's column of an n-tile: a piece, live where the column's group is the lane's own
   const bool mine = g / TPN == t * G / 4;
-  const uint4 *xp = a.xpieces + ((int64_t)c_begin * n_tiles + nt0) * (16 * TPN) + g % TPN * 4 + t;
-  const float4 *xs = reinterpret_cast<const float4 *>(a.xsums) + ((int64_t)c_begin * n_tiles + nt0) * 4 + t;
+  const uint4 *xp;
+  const float4 *xs;
+  if constexpr (OWN) {
+    const int column = chunks * 16 + 4, parts = chunks * 16;  // padded: two columns' quarters in different banks
+    uint4 *own = reinterpret_cast<uint4 *>(smem + kWarps * G * v_most * ROWS);
+    float2 *sums = reinterpret_cast<float2 *>(own + v_most * column);
+    for (int i = threadIdx.x; (i & ~31) < a.T * parts; i += kWarps * 32) {
+      const bool live = i < a.T * parts;
+      if (a.f32) prepare_piece<BITS, true, float>(a, i / parts, i % parts, live, column, own, sums);
+      else prepare_piece<BITS, true, __nv_bfloat16>(a, i / parts, i % parts, live, column, own, sums);
+    }
+    __syncthreads();
+    xp = own + g % TPN * column + c_begin * 16 + t;
+    xs = reinterpret_cast<const float4 *>(sums) + c_begin * 4 + t;
+  } else {
+    // The values are the preparing launch's output: wait for it only here. With the entries' launch in between,
+    // which runs beside this one, its word says so.
+    if (a.y_ad) {
+      if (lane == 0 && !wait_ready(a.ready)) atomicOr(a.err, kErrEntries);
+      __syncwarp();
+    } else {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
+    xp = a.xpieces + ((int64_t)c_begin * n_tiles + nt0) * (16 * TPN) + g % TPN * 4 + t;
+    xs = reinterpret_cast<const float4 *>(a.xsums) + ((int64_t)c_begin * n_tiles + nt0) * 4 + t;
+  }
+  // Tile n of the chunk `ahead` behind the pointers. The values are asked for as soon as the tile before in their
+  // registers is used: they come from L2 as often as not. Columns of other groups and behind the last piece are
+  // zero; runs behind the last column were prepared as zeros.
+  constexpr int S = NT < 8 ? 1 : 2;
+  const int tiles_of = NT == 1 ? 1 : n_tiles;  // a call with more n-tiles takes a wider variant
+  XTile xt[S];
+  const bool on1 = mine && g % TPN < v_end;
+  auto load_x = [&](XTile &f, int ahead, int n) {
+    if constexpr (OWN) {
+      if (on1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f.x[j] = xp[ahead * 16 + j * 4];
+    } else if constexpr (NT == 1) {  // the registers hold nothing else: cleared once
+      if (on1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f.x[j] = xp[ahead * (16 * TPN) + j * (4 * TPN)];
+    } else {
+      const bool on = mine && n * TPN + g % TPN < v_end;
+      const uint4 *p = xp + ((int64_t)ahead * tiles_of + n) * (16 * TPN);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f.x[j] = make_uint4(0, 0, 0, 0);
+        if (on) f.x[j] = p[j * (4 * TPN)];
+      }
+    }
+    f.f = xs[(ahead * tiles_of + n) * 4];
+  };
+#pragma unroll
+  for (int n = 0; n < S; ++n) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xt[n].x[j] = make_uint4(0, 0, 0, 0);
+    if (c_begin < c_end && n * TPN < v_end) load_x(xt[n], 0, n);
+  }
 
   float acc[MT][NT][4];
 #pragma unroll
@@ -364,33 +442,38 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
 #pragma unroll
     for (int h = 0; h < 2 * MT; ++h) {
       pw[h] += DEPTH * ROW_CHUNK;
-      if (EXACT) ps[h] += DEPTH * G, pz[h] += DEPTH * G;
+      if (EXACT && G > 1) ps[h] += DEPTH * G, pz[h] += DEPTH * G;
     }
     each<DEPTH>([&](auto I) {
       constexpr int i = decltype(I)::value;
       if (c + i < c_end) {
-        Chunk<BITS, MT> &f = buf[i];
-        const bool in = G == 1 || (c + i) * 128 + t * 32 < a.d_in;
+        Chunk<BITS, G, MT> &f = buf[i];
+        constexpr int at_chunk = i;
         uint32_t q[2 * MT][16];
         float s[2 * MT], zp[2 * MT];
+        [[maybe_unused]] const int of_four = DEPTH == 4 ? i : (c + i - c_begin) & 3;
+        if constexpr (G == 1) {
+          if (of_four == 0) {
+#pragma unroll
+            for (int h = 0; h < 2 * MT; ++h) s4[h] = sn[h], z4[h] = zn[h];
+            fetch_scales(c + i + 4);
+          }
+        }
 #pragma unroll
         for (int h = 0; h < 2 * MT; ++h) {
           unpack<BITS>(f.w[h], q[h]);
-          s[h] = f.s[h];
-          zp[h] = (float)f.z[h];
+          if constexpr (G == 1) {
+            s[h] = __shfl_sync(~0u, s4[h], of_four, 4), zp[h] = __shfl_sync(~0u, z4[h], of_four, 4);
+          } else {
+            s[h] = f.s[h], zp[h] = (float)f.z[h];
+          }
         }
         fetch(f, c + i + DEPTH, I);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if (NT > 1 && n * TPN >= v_end) break;
-          uint4 x[4];
-          const bool on = in && mine && n * TPN + g % TPN < v_end;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[j] = make_uint4(0, 0, 0, 0);
-            if (on) x[j] = xp[n * (16 * TPN) + j * (4 * TPN)];
-          }
-          const float4 fx = xs[n * 4];
+          const uint4 *x = xt[n % S].x;
+          const float4 fx = xt[n % S].f;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             const uint32_t *q0 = q[2 * m], *q1 = q[2 * m + 1];
@@ -409,11 +492,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
                   fmaf(s[2 * m + h] * fx.w, fmaf(-zp[2 * m + h], fx.z, d[2 * h + 1]), acc[m][n][2 * h + 1]);
             }
           }
+          if (n + S < NT && (n + S) * TPN < v_end) load_x(xt[n % S], at_chunk, n + S);
+          else if (c + i + 1 < c_end) load_x(xt[n % S], at_chunk + 1, n % S);
         }
-        xp += (int64_t)n_tiles * (16 * TPN);
-        xs += n_tiles * 4;
       }
     });
+    xp += OWN ? DEPTH * 16 : (int64_t)DEPTH * tiles_of * (16 * TPN);
+    xs += DEPTH * tiles_of * 4;
   }
 
   float *red = smem;  // [kWarps][G][v_most][ROWS]: the warps' sums
@@ -447,7 +532,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
   }
 }
 
-template <int BITS, int G, int NT, int MT, int DEPTH, bool EXACT>
+template <int BITS, int G, int NT, int MT, int DEPTH, bool EXACT, bool OWN = false>
 cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   constexpr int TPN = 8 / G, cols = NT * TPN, ROWS = 16 * MT;
   int tpp = cols / a.pieces;
@@ -458,7 +543,8 @@ cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   int slices = 1;
   while (slices < kWarps && tiles * slices < (int64_t)sm_count() * 12 && chunks >= 2 * slices) slices *= 2;
   size_t smem = sizeof(float) * (size_t)kWarps * G * tpp * a.pieces * ROWS;
-  auto kernel = gemv_mma_kernel<BITS, G, NT, MT, DEPTH, EXACT>;
+  if (OWN) smem += (size_t)a.T * a.pieces * (chunks * 16 + 4) * sizeof(uint4) + chunks * 64;
+  auto kernel = gemv_mma_kernel<BITS, G, NT, MT, DEPTH, EXACT, OWN>;
   static std::atomic<size_t> allowed[64];
   const cudaError_t e = allow_smem((const void *)kernel, smem, allowed);
   if (e != cudaSuccess) return e;
@@ -478,10 +564,11 @@ cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
 template <int BITS, int G, bool EXACT>
 cudaError_t launch_cols(const GemvArgs &a, cudaStream_t s) {
   const int tiles = x_tiles(a.T * a.pieces, G);
+  if (!a.xpieces) return launch_one<BITS, G, 1, 1, 4, EXACT, true>(a, s);
   if (tiles <= 1) return launch_one<BITS, G, 1, 1, 4, EXACT>(a, s);
-  if (tiles <= 2) return launch_one<BITS, G, 2, 1, 3, EXACT>(a, s);
-  if (tiles <= 4) return launch_one<BITS, G, 4, 1, 2, EXACT>(a, s);
-  return launch_one<BITS, G, 8, 2, 2, EXACT>(a, s);
+  if (tiles <= 2) return launch_one<BITS, G, 2, 1, 2, EXACT>(a, s);
+  if (tiles <= 4) return launch_one<BITS, G, 4, 1, 1, EXACT>(a, s);
+  return launch_one<BITS, G, 8, 2, 1, EXACT>(a, s);
 }
 
 template <int BITS>

@@ -174,12 +174,13 @@ struct GemvArgs {
   // The values as operands, `pieces` columns a token, TPN = 8 / G columns to an n-tile (G groups in a chunk of 128
   // columns): xpieces [chunk][n-tile][4][TPN][4 runs] of 16 bytes, xsums [chunk][n-tile][8] (sum, factor) pairs.
   int pieces;
-  uint4 *xpieces;
+  uint4 *xpieces;  // NULL: the product makes them itself
   float2 *xsums;
   int prepared;  // another launch of the call precedes the product
 };
 __host__ __device__ constexpr int x_tiles(int cols, int G) { return (cols * G + 7) / 8; }
 bool gemv_on_tensor_cores(const uint8_t *qw, int group);
+bool gemv_own_x(int32_t d_in, int64_t T, bool f32);  // whether a product by itself needs no prepared values
 // Workspaces, and where in them the arrays lie.
 size_t gemv_x_bytes(int32_t d_in, int64_t T, bool f32);
 void gemv_place_x(GemvArgs *a, void *ws);
