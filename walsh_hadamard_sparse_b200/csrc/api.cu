@@ -877,9 +877,9 @@ qwha_status decode_call(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtyp
   const bool tensor = gemv_on_tensor_cores(g.qw, g.group);
   if (tensor) gemv_place_x(&g, ws);
   if (!a && gemv_own_x(d_in, T, g.f32)) g.xpieces = nullptr;
+  if (!(g.err = device_error_word())) return fail(QWHA_ERR_CUDA, "no error word");
   if (a && a->p > 0) {
     g.row_ptr = a->row_ptr, g.col_idx = a->col_idx, g.coef = a->coef, g.p = a->p, g.alpha = alpha;
-    if (!(g.err = device_error_word())) return fail(QWHA_ERR_CUDA, "no error word");
     gemv_place_z(&g, static_cast<char *>(ws) + (wq ? gemv_x_bytes(d_in, T, g.f32) : 0));
   }
   g.prepared = g.xpieces || g.zt || Z_out;

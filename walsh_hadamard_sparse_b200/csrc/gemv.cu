@@ -13,6 +13,7 @@
 #include "bulk.cuh"
 #include "common.cuh"
 #include "gemv_mma.cuh"
+#include "gemv_wide.cuh"
 #include "kernels.h"
 
 namespace qwha {
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const GemvArgs a
 }
 
 constexpr int kPrepThreads = 256;
+constexpr int kWideAbove = 32;  // columns
 
 // Shared-memory place of element i of a span: four floats of padding every
 // sixteen, so that sixteen consecutive elements a thread and elements sixteen
@@ -119,12 +121,19 @@ __device__ __forceinline__ void span_pass(float *row, int d, int s) {
 // entry of E finds its column of all of them in one place, and z_out [T, d_in]
 // in X's type for the backward, on request. Latency bounds it:
 // four stages a pass, so 4096 columns take three turns through shared memory.
+// Token slots of a pass of the product for many columns: they cover the padding too.
+__host__ __device__ inline int wide_slots(const GemvArgs &a) { return (a.npad + a.pieces - 1) / a.pieces; }
+
 template <int BITS, typename T>
 __global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const GemvArgs a, int logn, int span, int spans,
                                                                       float scale, T *z_out) {
   extern __shared__ __align__(16) float row[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product may start on the weight
   if (a.ready && blockIdx.x == 0 && threadIdx.x == 0) *a.ready = 0;
+  if ((int)blockIdx.x >= spans && a.npad) {
+    wide::wide_prepare<BITS, T>(a, blockIdx.x - spans, wide_slots(a));
+    return;
+  }
   if ((int)blockIdx.x >= spans) {
     const int parts = (a.d_in + 127) / 128 * 16, i = (blockIdx.x - spans) * kPrepThreads + threadIdx.x;
     gemv::prepare_piece<BITS, false, T>(a, i / parts, i % parts, i < a.T * parts, a.T * a.pieces, a.xpieces, a.xsums);
@@ -156,7 +165,7 @@ __global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const Gemv
 constexpr int kEntThreads = 512, kEntWarps = kEntThreads / 32;
 constexpr int kEntRows = 1024;  // rows of a CTA whose borders are kept in shared memory
 constexpr int kLongRow = 256, kHugeRow = 1024;
-constexpr size_t kEntSmem = 200 * 1024;
+constexpr size_t kEntSmem = 200 * 1024, kEntZ = 136 * 1024;
 
 // 16 bytes into shared memory, zeros behind the first `bytes`.
 __device__ __forceinline__ void copy16(void *dst, const void *src, uint32_t bytes) {
@@ -396,7 +405,8 @@ cudaError_t prepare(const GemvArgs &a, int logn, void *z_out, cudaStream_t s) {
   // spans of whole blocks, about 2048 columns where the blocks are shorter
   const int span = n >= 2048 ? n : 2048;
   const int spans = a.zt || z_out ? a.T * (int)cdiv(a.d_in, span) : 0;
-  const int parts = a.xpieces ? a.T * (int)cdiv(a.d_in, 128) * 16 : 0;
+  const int passes = a.npad ? (int)cdiv(a.T, a.tpp) : 0;
+  const int parts = !a.xpieces ? 0 : a.npad ? passes * wide_slots(a) * kPrepThreads : a.T * (int)cdiv(a.d_in, 128) * 16;
   const size_t smem = spans ? (size_t)span_at(span) * sizeof(float) : 0;
   auto kernel = decode_prepare_kernel<BITS, T>;
   static std::atomic<size_t> allowed[64];
@@ -427,30 +437,56 @@ bool gemv_own_x(int32_t d_in, int64_t T, bool f32) {
   return T * pieces_of(f32) <= 2 && T * pieces_of(f32) * d_in <= 16384;
 }
 
+namespace {
+// Tokens of a pass and its padded columns for the product of many columns; npad 0 where the other takes the call.
+void wide_shape(int64_t T, bool f32, int *tpp, int *npad) {
+  const int P = pieces_of(f32);
+  *tpp = *npad = 0;
+  if (T * P <= kWideAbove) return;
+  const int64_t passes = cdiv(T * P, 128);
+  *tpp = (int)cdiv(T, passes);
+  *npad = (*tpp * P + 15) / 16 * 16;
+}
+}  // namespace
+
 size_t gemv_x_bytes(int32_t d_in, int64_t T, bool f32) {
   if (T <= 0) return 0;
+  int tpp, npad;
+  wide_shape(T, f32, &tpp, &npad);
+  if (npad) return (size_t)cdiv(T, tpp) * cdiv(d_in, 128) * npad * 256 + align_up(T * 4, 256);
   return xpieces_bytes(d_in, T, f32) + align_up((size_t)cdiv(d_in, 128) * 64 * x_tiles((int)T * pieces_of(f32), 4), 256);
 }
 
 void gemv_place_x(GemvArgs *a, void *ws) {
   a->pieces = pieces_of(a->f32);
   a->xpieces = static_cast<uint4 *>(ws);
+  wide_shape(a->T, a->f32, &a->tpp, &a->npad);
+  if (a->npad) {
+    const size_t bytes = (size_t)cdiv(a->T, a->tpp) * cdiv(a->d_in, 128) * a->npad * 256;
+    a->fac = reinterpret_cast<float *>(static_cast<char *>(ws) + bytes);
+    return;
+  }
   a->xsums = reinterpret_cast<float2 *>(static_cast<char *>(ws) + xpieces_bytes(a->d_in, a->T, a->f32));
 }
 
 namespace {
-// Tokens of a group: as many as there are up to two, then four (a 16-byte gather) or eight.
-int group_tokens(int64_t T) { return T <= 2 ? (int)T : T <= 4 ? 4 : 8; }
+// Tokens of a group: as many as there are up to two, then four (a 16-byte gather) or eight, and so few that a group's
+// Z fits into shared memory beside the entries where any does.
+int group_tokens(int64_t T, int32_t d_in) {
+  int n = T <= 2 ? (int)T : T <= 4 ? 4 : 8;
+  while (n > 1 && (int64_t)n * d_in * 4 > kEntZ) n /= 2;
+  return n;
+}
 }  // namespace
 
 size_t gemv_z_bytes(int32_t d_out, int32_t d_in, int64_t T) {
   if (T <= 0) return 0;
-  const size_t tp = cdiv(T, group_tokens(T)) * group_tokens(T);
+  const size_t tp = cdiv(T, group_tokens(T, d_in)) * group_tokens(T, d_in);
   return align_up(tp * d_in * 4, 256) + align_up(tp * d_out * 4, 256) + 256;
 }
 
 void gemv_place_z(GemvArgs *a, void *ws) {
-  a->tg = group_tokens(a->T);
+  a->tg = group_tokens(a->T, a->d_in);
   a->tp = (a->T + a->tg - 1) / a->tg * a->tg;
   a->ready = static_cast<unsigned int *>(ws);
   a->zt = reinterpret_cast<float *>(static_cast<char *>(ws) + 256);

@@ -176,6 +176,10 @@ struct GemvArgs {
   int pieces;
   uint4 *xpieces;  // NULL: the product makes them itself
   float2 *xsums;
+  // Many columns instead (npad > 0): passes of tpp tokens, padded to npad columns; xpieces [pass][chunk][2][npad][128]
+  // bytes, fac [T] the factors of fp32 tokens.
+  int tpp, npad;
+  float *fac;
   int prepared;  // another launch of the call precedes the product
 };
 __host__ __device__ constexpr int x_tiles(int cols, int G) { return (cols * G + 7) / 8; }
