@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const GemvArgs a
 }
 
 constexpr int kPrepThreads = 256;
-constexpr int kWideAbove = 32;  // columns
+constexpr int kWideAbove = 28;  // columns
 
 // Shared-memory place of element i of a span: four floats of padding every
 // sixteen, so that sixteen consecutive elements a thread and elements sixteen

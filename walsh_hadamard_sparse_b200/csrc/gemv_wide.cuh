@@ -32,7 +32,7 @@ namespace qwha {
 namespace wide {
 
 constexpr int kRows = 128, kUnpackWarps = 8, kScaleWarps = 8, kThreads = (kUnpackWarps + kScaleWarps + 2) * 32;
-constexpr int kAhead = 2, kMaxSlots = 8;
+constexpr int kAhead = 1, kMaxSlots = 8;
 template <int NB>
 constexpr int stages() { return NB <= 2 ? 4 : 3; }  // as many as fit
 constexpr uint32_t kABytes = kRows * 256, kTmemCols = 512;
@@ -80,7 +80,6 @@ __device__ __forceinline__ bool calm_wait(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity), "r"(2000u)
         : "memory");
     if (ok) return true;
-    __nanosleep(40);
     const uint64_t now = bulk::now_ns();
     if (begin == 0) begin = now;
     else if (now - begin > bulk::kWaitNs) return false;
@@ -419,36 +418,35 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_wide_kernel(const GemvArgs a
     if (elected()) {
       // D fp32, A and B bf16, both K-major, N / 8, M / 16
       const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(a.npad >> 3) << 17) | (8u << 24);
-      const int last = 8 / G - 1;  // a group's steps of 16 columns, less one
-      // a thread by itself: every instruction costs its latency, so nothing is divided and the descriptors step
-      uint64_t da = sw128(base), db = sw128(b_base);
-      const uint32_t slab = a.npad * 128 >> 4;
-      uint32_t parity = 0, turn = 1;  // of the stages; of the accumulators
-      bool ok = true;
-      for (int c = c_begin, s = 0, slot = 0; ok && c < c_end; ++c) {
-        if (!calm_wait(full(s), parity)) {
-          give_up();
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      // a thread by itself: every instruction costs its latency, so nothing is divided or tested per product
+      auto issue = [&](auto groups) {
+        constexpr int n = decltype(groups)::value;
+        uint64_t da = sw128(base), db = sw128(b_base);
+        const uint32_t slab = a.npad * 128 >> 4;
+        uint32_t parity = 0, turn = 1;  // of the stages; of the accumulators
+        for (int c = c_begin, s = 0, slot = 0; c < c_end; ++c) {
+          if (!calm_wait(full(s), parity)) return false;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if ((k & last) == 0) {
-            ok = ok && calm_wait(sum_empty(slot), turn);
+          for (int gi = 0; gi < n; ++gi) {
+            if (!calm_wait(sum_empty(slot), turn)) return false;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          }
-          if (ok)
-            product(tmem + slot * stride, da + (k >> 2) * (kRows * 128 >> 4) + (k & 3) * 2,
-                    db + (k >> 2) * slab + (k & 3) * 2, idesc, (k & last) != 0);
-          if ((k & last) == last) {
+            const uint32_t d = tmem + slot * stride;
+#pragma unroll
+            for (int k = gi * 8 / n; k < (gi + 1) * 8 / n; ++k)
+              product(d, da + (k >> 2) * (kRows * 128 >> 4) + (k & 3) * 2, db + (k >> 2) * slab + (k & 3) * 2, idesc,
+                      k != gi * 8 / n);
             commit(sum_full(slot));
             if (++slot == slots) slot = 0, turn ^= 1;
           }
+          commit(empty(s));
+          da += kABytes >> 4, db += b_bytes >> 4;
+          if (++s == kStages) s = 0, parity ^= 1, da = sw128(base), db = sw128(b_base);
         }
-        commit(empty(s));
-        da += kABytes >> 4, db += b_bytes >> 4;
-        if (++s == kStages) s = 0, parity ^= 1, da = sw128(base), db = sw128(b_base);
-      }
+        return true;
+      };
+      const bool ok = G == 1   ? issue(std::integral_constant<int, 1>())
+                      : G == 2 ? issue(std::integral_constant<int, 2>())
+                               : issue(std::integral_constant<int, 4>());
       if (!ok) give_up();
       commit(done);  // TMEM must not be freed under a product
       if (!calm_wait(done, 0)) give_up();
