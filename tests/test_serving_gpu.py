@@ -7,7 +7,7 @@ import pytest
 import oracle
 from _serving import (butterflies, dense_weight, half_step, pack, quantize, random_weight, round_to, unpack, values)
 from _util import bf16_dev, host, to_dev
-from workloads import f32_to_bf16_bits, random_pattern, rng_for
+from workloads import f32_to_bf16_bits, pack_codes, random_pattern, rng_for
 
 pytestmark = pytest.mark.gpu
 
@@ -119,6 +119,26 @@ def test_qgemv_large_and_tiny_fp32_values():
     x[1] *= np.float32(1e-25)
     x[2, ::2] *= np.float32(1e-20)
     _check_base(W.qgemv(wq, _dev(x, "f32")), x.astype(np.float64), w, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 7, 40])
+@pytest.mark.parametrize("bits,group", [(2, 32), (2, 64), (3, 128), (4, 128)])
+def test_qgemv_a_value_far_above_the_others(bits, group, T, dtype):
+    """A value of a thousand whose weight is zero (code = zero point) leaves the other columns' sums whole: fp32 sums of
+    codes below 2^bits times values, 24 bits of at most 8 + 8 roundings of the largest partial sum a group."""
+    W = _W()
+    g = rng_for(112, "outlier", bits, group, T)
+    q, packed, s, z = random_weight(g, 48, 512, bits, group)
+    q[:, [5, 300]] = z[:, [5 // group, 300 // group]]
+    packed = pack_codes(q, bits)
+    w = dense_weight(q, s, z, group)
+    x = round_to(g.standard_normal((T, 512)), dtype)
+    x[:, 5], x[:, 300] = 1000.0, -997.0
+    want = x.astype(np.float64) @ w.T
+    top = 2.0**bits * 1000.0 * np.abs(s).max(-1)
+    tol = half_step(dtype) * 1.01 * np.abs(want) + 16 * 2.0**-24 * 2 * top + 2.0**-20 * (np.abs(x) * (np.abs(x) < 100)) @ np.abs(w).T
+    assert np.all(np.abs(host(W.qgemv(_qweight(W, bits, group, packed, s, z), _dev(x, dtype))) - want) <= tol)
 
 
 def _decode_case(g, d_in, d_out, n, bits, group, counts, T, dtype, scale=0.05):

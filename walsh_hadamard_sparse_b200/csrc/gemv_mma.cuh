@@ -100,6 +100,19 @@ __device__ __forceinline__ void unpack(const uint32_t *w, uint32_t *q) {
   }
 }
 
+// The denormals q 2^(o - 24) as the numbers q 2^o: 1024 + q 2^o by its bits, less
+// 1024. The matrix unit aligns products by the operands' nominal exponents, so
+// denormal codes cost the sums about eight bits (4096 x 14336, 2 bits, token
+// values of up to 94 among ones: off by 1.5e-5 of the result, by 3e-7 with
+// normal codes), which a value of a thousand among ones would show in bf16 too.
+// One addition for two codes, on another pipe than the unpacking.
+__device__ __forceinline__ uint32_t normal(uint32_t q) {
+  q |= 0x64006400u;
+  const uint32_t of1024 = 0x64006400u;
+  const __half2 d = __hsub2(reinterpret_cast<const __half2 &>(q), reinterpret_cast<const __half2 &>(of1024));
+  return reinterpret_cast<const uint32_t &>(d);
+}
+
 // d = A B
 __device__ __forceinline__ void mma0(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1) {
@@ -462,6 +475,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
 #pragma unroll
         for (int h = 0; h < 2 * MT; ++h) {
           unpack<BITS>(f.w[h], q[h]);
+#pragma unroll
+          for (int p = 0; p < 16; ++p) q[h][p] = normal(q[h][p]);
           if constexpr (G == 1) {
             s[h] = __shfl_sync(~0u, s4[h], of_four, 4), zp[h] = __shfl_sync(~0u, z4[h], of_four, 4);
           } else {
@@ -487,9 +502,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
             // d[0], d[1]: row g, columns 2t and 2t + 1, whose group is this lane's; d[2], d[3]: row g + 8
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              acc[m][n][2 * h] = fmaf(s[2 * m + h] * fx.y, fmaf(-zp[2 * m + h], fx.x, d[2 * h]), acc[m][n][2 * h]);
+              constexpr float unit_of = 0x1p-24f;  // keeps sums of any tokens within fp32's range
+              acc[m][n][2 * h] =
+                  fmaf(s[2 * m + h] * fx.y, fmaf(-zp[2 * m + h], fx.x, d[2 * h] * unit_of), acc[m][n][2 * h]);
               acc[m][n][2 * h + 1] =
-                  fmaf(s[2 * m + h] * fx.w, fmaf(-zp[2 * m + h], fx.z, d[2 * h + 1]), acc[m][n][2 * h + 1]);
+                  fmaf(s[2 * m + h] * fx.w, fmaf(-zp[2 * m + h], fx.z, d[2 * h + 1] * unit_of), acc[m][n][2 * h + 1]);
             }
           }
           if (n + S < NT && (n + S) * TPN < v_end) load_x(xt[n % S], at_chunk, n + S);
