@@ -141,6 +141,22 @@ def test_qgemv_a_value_far_above_the_others(bits, group, T, dtype):
     assert np.all(np.abs(host(W.qgemv(_qweight(W, bits, group, packed, s, z), _dev(x, dtype))) - want) <= tol)
 
 
+@pytest.mark.parametrize("dtype,T,d_in", [
+    ("bf16", 1, 16384), ("bf16", 1, 16416), ("bf16", 2, 8192), ("bf16", 2, 8224),  # operands made in the product or not
+    ("bf16", 28, 480), ("bf16", 29, 480), ("f32", 9, 480), ("f32", 10, 480),  # the last and first of many columns
+    ("bf16", 64, 2176), ("f32", 42, 1376), ("f32", 43, 1376), ("f32", 64, 160)])  # empty and uneven slices, two passes
+@pytest.mark.parametrize("bits,group", [(2, 32), (3, 32), (4, 160)])
+def test_qgemv_borders_of_the_kernels(bits, group, dtype, T, d_in):
+    W = _W()
+    group = group if d_in % group == 0 else 32
+    for d_out in (1, 40, 129, 300):
+        g = rng_for(113, "borders", bits, T, d_in, d_out)
+        q, packed, s, z = random_weight(g, d_out, d_in, bits, group, zero_top=255 if d_out == 40 else None)
+        x = round_to(g.standard_normal((T, d_in)), dtype)
+        Y = W.qgemv(_qweight(W, bits, group, packed, s, z), _dev(x, dtype))
+        _check_base(Y, x.astype(np.float64), dense_weight(q, s, z, group), dtype)
+
+
 def _decode_case(g, d_in, d_out, n, bits, group, counts, T, dtype, scale=0.05):
     rp, ci, cf = random_pattern(d_out, d_in, counts=counts, rng=g, coef_scale=scale)
     q, packed, s, z = random_weight(g, d_out, d_in, bits, group)

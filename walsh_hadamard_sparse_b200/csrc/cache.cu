@@ -492,6 +492,11 @@ __global__ void __launch_bounds__(kCacheThreads)
 // with one group, computes its step and hands it round. Codes become nibbles
 // (8 bits: bytes) by one shifted addition each, and an eight by eight transpose
 // in registers brings each lane sixteen neighbours to store.
+//
+// 32768 tokens into two caches, 8 heads of 128, 4 bits, groups of 64: 76 us at
+// 3.1 instructions a clock (the bytes alone: 26 us). With the read-back of the
+// same rows 117 us; 282 us with eight elements a lane and butterflies between
+// lanes in both kernels, 154 us with sixteen a lane in this one.
 
 using f2 = unsigned long long;  // two fp32 values
 __device__ __forceinline__ f2 pack2(float a, float b) {

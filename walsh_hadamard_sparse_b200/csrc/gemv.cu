@@ -84,7 +84,12 @@ __global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const GemvArgs a
 }
 
 constexpr int kPrepThreads = 256;
-constexpr int kWideAbove = 28;  // columns
+// Columns above which tcgen05 takes the product. It costs 32 to 40 us for the layers below whatever the columns, unpacking
+// into shared memory; the other grows with them (bf16 tokens, us, mma.sync / tcgen05):
+//   14336 x 4096, 4 bits     24: 31 / 32   32: 39 / 32   64: 67 / 36
+//   4096 x 14336, 2 bits     24: 36 / 36   32: 45 / 37   64: 86 / 44
+//   4096 x 14336, 3 bits     24: 27 / 36   32: 34 / 38   64: 47 / 44
+constexpr int kWideAbove = 28;
 
 // Shared-memory place of element i of a span: four floats of padding every
 // sixteen, so that sixteen consecutive elements a thread and elements sixteen
@@ -215,12 +220,13 @@ __device__ __forceinline__ void row_sum(const int32_t *cols, const float *coefs,
 
 // The entries of E against the transformed tokens: y_ad[i][t] = sum_{j in row i}
 // c_j Z[t][k_j], fp32. Gathering Z from L2 costs a sector an entry and waits
-// for each (measured on the gate layer, sixteen tokens: 47 us inside the
-// product's kernel), so the columns of a group of TG tokens are brought into
-// shared memory where they fit, and an entry a lane gathers there; the entries
-// themselves stream from L2 once a group. Wider layers gather from L2 (three
-// turns of the entries with a third of the columns each cost more: 70 against
-// 54 us a pass on the down layer, five tokens).
+// for each, so a group of TG tokens is brought into shared memory and an entry
+// a lane gathers there (down layer, five fp32 tokens: three turns of two tokens
+// 51 us, eight from L2 62 us); only layers whose single token does not fit
+// gather from L2. The entries are copied to shared memory beside it, before the
+// preparing launch is complete. 512 threads of 64 registers leave a CTA of the
+// product room on the SM (gate layer, sixteen tokens: 49 us instead of 54 with
+// 1024 threads and the product behind).
 //
 // Rows differ in length by orders of magnitude (the budget follows the row's
 // quantization error): a CTA takes whole rows that hold its even share of the

@@ -1,11 +1,12 @@
 // The packed matrix-vector product on tensor cores (see gemv.cu): one
 // definition for the three code widths, instantiated by gemv_b2/3/4.cu.
 //
-// Unpacking bounds this kernel as much as memory does: at 6.5 TB/s a 4-bit
-// code leaves about three instruction slots, and half as many on the integer
-// pipe. Two exact representations keep the count below one slot a code:
-//   * a code masked out of a 16-bit half at bit o (o + bits <= 10) IS the f16
-//     denormal q * 2^(o - 24): most codes need one mask and no shift;
+// Unpacking bounds this kernel more than memory does: at 6.5 TB/s a 4-bit code
+// leaves about three instruction slots, and half as many on the integer pipe.
+// Two exact representations keep the count below one slot a code:
+//   * a code masked out of a 16-bit half at bit o (o + bits <= 10), ORed into
+//     the mantissa of the f16 1024, is 1024 + q * 2^o: one instruction for two
+//     codes, most need no shift, and a subtraction leaves q * 2^o (`normal`);
 //   * the tokens' values, scaled by a power of two per chunk of 128 columns so
 //     that the largest lies in [2^14, 2^15), are f16 numbers too: a bf16 value
 //     in one piece, an fp32 value in three (exact down to 2^-31 of the chunk's
@@ -27,8 +28,13 @@
 // lanes of its group and zeros elsewhere, so no sum crosses a group.
 //
 // Memory. Codes, scales and zero points go straight to the registers of the
-// lane that uses them, DEPTH chunks ahead, past L1; the values stay in L1. No
-// shared memory and no barrier until the slices are added.
+// lane that uses them, DEPTH chunks ahead, past L1; the values come through L1,
+// or with OWN from shared memory. No barrier until the slices are added.
+//
+// 14336 x 4096, 3 bits, one token: 17.8 us; 4096 x 14336, 4 bits, eight tokens:
+// 14.6 us (33% of the copy rate). Tried and slower: codes through rings of
+// shared memory filled by bulk copies (18 to 30 us), fp8 operands (converted on
+// the integer pipe, 26 us), values staged in shared memory (18 and 35 us).
 
 #pragma once
 
@@ -352,9 +358,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
       }
     }
   };
-  // With one group to a chunk, the four lanes of a row load those of four chunks and hand them round: requests to
-  // the L1, eight rows to each, bound the product before memory does (a scale and a zero point a chunk and lane
-  // were half of them).
+  // With one group to a chunk, the four lanes of a row load those of four chunks and hand them round: a quarter of
+  // the requests (each touches eight rows), and half the registers of a ring of them.
   float sn[2 * MT], zn[2 * MT], s4[2 * MT], z4[2 * MT];
   auto fetch_scales = [&](int c) {  // of chunks c .. c + 3
     const int ct = c + t;
@@ -555,7 +560,8 @@ cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   int tpp = cols / a.pieces;
   if (tpp < a.T) tpp &= ~(TPN - 1);  // a further pass starts with an n-tile
   else tpp = a.T;
-  // slices of the columns: as many as it takes to give every SM sixteen warps, two chunks a warp at least
+  // slices of the columns: as many as it takes to give every SM twelve warps, two chunks a warp at least (a target of
+  // 24 or 48 warps: 20 and 21 us instead of 17 for 14336 x 4096, 3 bits)
   const int64_t tiles = cdiv(a.d_out, ROWS), chunks = cdiv(a.d_in, 128);
   int slices = 1;
   while (slices < kWarps && tiles * slices < (int64_t)sm_count() * 12 && chunks >= 2 * slices) slices *= 2;
@@ -578,6 +584,8 @@ cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, a, tpp, slices);
 }
 
+// The n-tiles a warp keeps: more tiles leave fewer registers to codes in flight,
+// and each is worth its operands' latency less.
 template <int BITS, int G, bool EXACT>
 cudaError_t launch_cols(const GemvArgs &a, cudaStream_t s) {
   const int tiles = x_tiles(a.T * a.pieces, G);
