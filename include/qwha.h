@@ -247,7 +247,7 @@ typedef struct {
 
 /* Quantize rows[c] [n, heads, head_dim] (device, dtype dt) into the slots
  * slots[i] (device int64 [n]) of caches[c], c < n_caches (1 or 2: keys and
- * values in one launch). caches and rows are host arrays. slots[i] = -1 skips
+ * values in one call). caches and rows are host arrays. slots[i] = -1 skips
  * row i (padding); slots outside [-1, n_pages * page_size) are skipped and
  * reported by qwha_check_stream_status (QWHA_ERR_INVALID_ARG). The slots of a
  * call must be distinct apart from -1: of rows sent to one slot it is not

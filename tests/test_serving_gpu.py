@@ -94,7 +94,7 @@ def test_qgemv_infinities_and_nan_stay_with_their_token(group, dtype):
     q, packed, s, z = random_weight(g, 40, 512, 4, group)
     q[:, 200] = 9
     z[:] = 3  # q - z = 6 at column 200
-    packed = __import__("workloads").pack_codes(q, 4)
+    packed = pack_codes(q, 4)
     wq, w = _qweight(W, 4, group, packed, s, z), dense_weight(q, s, z, group)
     x = round_to(g.standard_normal((9, 512)), dtype)
     clean = W.qgemv(wq, _dev(x, dtype))
@@ -284,6 +284,63 @@ def test_products_repeat_bit_for_bit_on_other_streams_and_in_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want[k]) and torch.equal(y2, want[k]) and torch.equal(b, base[k])
+
+
+@pytest.mark.parametrize("dtype,T,d_out", [("bf16", 64, 1032), ("f32", 24, 4096), ("bf16", 33, 104), ("bf16", 1, 1032),
+                                            ("f32", 16, 520)])
+def test_products_of_many_tokens_repeat_on_two_streams_and_in_graphs(dtype, T, d_out):
+    """Clusters of two streams at once, each with its own workspace, and two calls of one workspace in a graph."""
+    import torch
+
+    W = _W()
+    d_in = 4096
+    g = rng_for(114, "many", T, d_out)
+    rp, ci, cf, q, packed, s, z, x = _decode_case(g, d_in, d_out, d_in, 4, 64, g.integers(0, 200, d_out), T, dtype)
+    a = W.Adapter(d_in, d_out, d_in, ci.size, to_dev(rp), to_dev(ci), to_dev(cf))
+    wq = _qweight(W, 4, 64, packed, s, z)
+    xs = [_dev(round_to(g.standard_normal((T, d_in)), dtype), dtype) for _ in range(2)]
+    want, base = [W.adapter_decode(a, v, 1.0, wq) for v in xs], [W.qgemv(wq, v) for v in xs]
+    torch.cuda.synchronize()
+    outs = []
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs.append((k, W.adapter_decode(a, xs[k], 1.0, wq), W.qgemv(wq, xs[k])))
+    torch.cuda.synchronize()
+    for k, y, b in outs:
+        assert torch.equal(y, want[k]) and torch.equal(b, base[k])
+    xin = xs[0].clone()
+    with_base = 1 if dtype == "bf16" else 2
+    ws = torch.empty(W.workspace_size(10, d_out, d_in, a.p, T, with_base), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = W.adapter_decode(a, xin, 1.0, wq, ws=ws)
+        y2 = W.adapter_decode(a, xin, 1.0, wq, ws=ws)
+        b = W.qgemv(wq, xin)
+    for k in (1, 0):
+        xin.copy_(xs[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[k]) and torch.equal(y2, want[k]) and torch.equal(b, base[k])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_qgemv_infinities_among_many_tokens(dtype):
+    W = _W()
+    g = rng_for(115, "inf many")
+    q, packed, s, z = random_weight(g, 200, 512, 4, 128)
+    q[:, 200], z[:] = 9, 3
+    packed = pack_codes(q, 4)
+    wq, w = _qweight(W, 4, 128, packed, s, z), dense_weight(q, s, z, 128)
+    x = round_to(g.standard_normal((64, 512)), dtype)
+    clean = host(W.qgemv(wq, _dev(x, dtype)))
+    x[2, 200], x[40, 200], x[63, 17] = np.inf, np.nan, -np.inf
+    got = host(W.qgemv(wq, _dev(x, dtype)))
+    keep = np.setdiff1d(np.arange(64), [2, 40, 63])
+    assert np.array_equal(got[keep], clean[keep])
+    assert np.array_equal(got[2], np.sign(w[:, 200]) * np.inf)
+    assert np.all(np.isnan(got[40])) and not np.any(np.isfinite(got[63]))
 
 
 # ---------------------------------------------------------------- the cache

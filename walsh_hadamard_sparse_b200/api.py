@@ -166,9 +166,9 @@ def _fit(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int)
     current stream the work goes to)."""
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor")
-    if t.get_device() != dev:
+    if t.get_device() != dev or not t.is_contiguous():
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous CUDA tensor")
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
     return t.data_ptr()
 
@@ -304,7 +304,8 @@ def _caches(caches) -> tuple:
 
 def cache_write(caches, rows, slots: torch.Tensor) -> None:
     """Quantize rows [n, heads, head_dim] (fp32 or bf16) into the slots [n] (int64, distinct; -1 skips a row) of a
-    cache; with a pair of caches and a pair of rows (keys and values) both in one launch."""
+    cache; with a pair of caches and a pair of rows (keys and values) both in one call (one launch where they are alike
+    in bits and group)."""
     cs, dev, m = _caches(caches), torch.cuda.current_device(), slots.shape[0]
     rs = (rows,) if isinstance(rows, torch.Tensor) else tuple(rows)
     k = len(cs)
@@ -319,7 +320,7 @@ def cache_write(caches, rows, slots: torch.Tensor) -> None:
 
 def cache_read(caches, pages: torch.Tensor, row_start: torch.Tensor, n: int, first: torch.Tensor | None = None,
                dtype: torch.dtype = torch.bfloat16, out=None):
-    """Sequences of a cache as dense rows [n, heads, head_dim] (a pair of caches: a pair of tensors, in one launch).
+    """Sequences of a cache as dense rows [n, heads, head_dim] (a pair of caches: a pair of tensors, in one call).
     Rows row_start[b] .. row_start[b+1] (int64 [n_seqs+1]) are the tokens first[b], first[b]+1, ... (int64 [n_seqs];
     None: 0) of sequence b, whose token t lies in page pages[b, t // page_size] (int32 [n_seqs, max_pages]). Rows from
     row_start[-1] on are left as they were (they are not initialised without `out`)."""
