@@ -143,7 +143,8 @@ def test_qgemv_a_value_far_above_the_others(bits, group, T, dtype):
 
 @pytest.mark.parametrize("dtype,T,d_in", [
     ("bf16", 1, 16384), ("bf16", 1, 16416), ("bf16", 2, 8192), ("bf16", 2, 8224),  # operands made in the product or not
-    ("bf16", 28, 480), ("bf16", 29, 480), ("f32", 9, 480), ("f32", 10, 480),  # the last and first of many columns
+    ("bf16", 20, 480), ("bf16", 21, 480), ("f32", 6, 480), ("f32", 7, 480),  # the last and first of many columns
+    ("bf16", 28, 480), ("bf16", 33, 480), ("f32", 10, 480), ("f32", 11, 480),  # two and three blocks of columns
     ("bf16", 64, 2176), ("f32", 42, 1376), ("f32", 43, 1376), ("f32", 64, 160)])  # empty and uneven slices, two passes
 @pytest.mark.parametrize("bits,group", [(2, 32), (3, 32), (4, 160)])
 def test_qgemv_borders_of_the_kernels(bits, group, dtype, T, d_in):

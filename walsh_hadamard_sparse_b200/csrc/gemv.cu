@@ -84,12 +84,13 @@ __global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const GemvArgs a
 }
 
 constexpr int kPrepThreads = 256;
-// Columns above which tcgen05 takes the product. It costs 32 to 40 us for the layers below whatever the columns, unpacking
+// Columns above which tcgen05 takes the product. It costs 26 to 36 us for the layers below whatever the columns, unpacking
 // into shared memory; the other grows with them (bf16 tokens, us, mma.sync / tcgen05):
-//   14336 x 4096, 4 bits     24: 31 / 32   32: 39 / 32   64: 67 / 36
-//   4096 x 14336, 2 bits     24: 36 / 36   32: 45 / 37   64: 86 / 44
-//   4096 x 14336, 3 bits     24: 27 / 36   32: 34 / 38   64: 47 / 44
-constexpr int kWideAbove = 28;
+//   14336 x 4096, 4 bits     16: 27 / 27   24: 33 / 27   32: 39 / 27   64: 67 / 30
+//   4096 x 14336, 2 bits     16: 33 / 32   24: 40 / 32   32: 45 / 34   64: 86 / 44
+//   4096 x 14336, 3 bits     16: 25 / 34   24: 29 / 35   32: 34 / 36   64: 47 / 43
+//   1024 x 4096, 4 bits      16: 19 / 16   24: 20 / 16   32: 19 / 18   64: 19 / 23
+constexpr int kWideAbove = 20;
 
 // Shared-memory place of element i of a span: four floats of padding every
 // sixteen, so that sixteen consecutive elements a thread and elements sixteen

@@ -11,17 +11,19 @@
 //
 // A CTA takes 128 rows and a slice of the columns (a cluster of slices shares
 // its rows and adds its sums through distributed shared memory in rank order).
-//   warps 0..7   unpack: a lane holds runs of 32 codes of four rows, kAhead
-//                chunks of 128 columns in flight from memory; a code ORed into
-//                the mantissa of 128 minus 128 + zero is q - zero; stored as a
-//                K-major tile with 128-byte swizzle.
-//   warps 8..15  scale: thread = row (TMEM lane), the two halves of the warps
-//                take alternate blocks of 16 columns.
-//   warp 16      copies the values' tile, laid out by the preparing launch as
-//                shared memory holds it: one bulk copy a chunk.
-//   warp 17      issues the products.
+//   12 or 8   unpack, teams of four in turn: a lane holds runs of 32 codes of
+//             four rows, kAhead chunks of its team in flight from memory; a code
+//             ORed into the mantissa of 128 minus 128 + zero is q - zero; stored
+//             as a K-major tile with 128-byte swizzle.
+//   8 warps   scale: thread = row (TMEM lane), the two halves of the warps take
+//             alternate blocks of 16 columns.
+//   1 warp    copies the values' tile, laid out by the preparing launch as
+//             shared memory holds it: one bulk copy a chunk.
+//   1 warp    issues the products.
 // The order of the columns inside a run is the one the codes' masks yield, in
-// both operands. Every wait is bounded; a thread that gives up sets the error
+// both operands. Unpacking sets the pace: 14336 x 4096, 4 bits, 64 bf16 tokens
+// take 30 us on 112 SMs, 0.75 us for a CTA's chunk of 128 x 128 codes, of which
+// the products need 0.5; the bytes alone 5 us. Every wait is bounded; a thread that gives up sets the error
 // word and leaves its loop, and TMEM is freed after the products issued so far.
 
 #pragma once
@@ -31,10 +33,18 @@
 namespace qwha {
 namespace wide {
 
-constexpr int kRows = 128, kUnpackWarps = 8, kScaleWarps = 8, kThreads = (kUnpackWarps + kScaleWarps + 2) * 32;
-constexpr int kAhead = 1, kMaxSlots = 8;
+constexpr int kRows = 128, kScaleWarps = 8, kAhead = 1, kMaxSlots = 8;
+// With NB blocks of 16 columns to a scaling warp: the stages that fit, and the
+// teams that the registers of the sums leave room for (64 bf16 tokens of
+// 14336 x 4096: two teams 36 us, three 30; 32 tokens: three 27, four with five
+// stages 29). A second chunk in flight to a team needs its loop unrolled once
+// more: 39 instead of 36 us, for the instructions' own fetches.
 template <int NB>
-constexpr int stages() { return NB <= 2 ? 4 : 3; }  // as many as fit
+constexpr int stages() { return NB <= 2 ? 4 : 3; }
+template <int NB>
+constexpr int teams() { return NB <= 2 ? 3 : 2; }
+template <int NB>
+constexpr int threads() { return (4 * teams<NB>() + kScaleWarps + 2) * 32; }
 constexpr uint32_t kABytes = kRows * 256, kTmemCols = 512;
 
 __device__ __forceinline__ uint64_t sw128(uint32_t saddr) {  // K-major rows of 128 bytes, eight to an atom
@@ -65,9 +75,8 @@ __device__ __forceinline__ bool elected() {
       : "=r"(one));
   return one;
 }
-// bulk::wait that leaves the issue slots to the warps that compute: the thread
-// is suspended for up to 2 us at a time (polling took most of them, 5700
-// instructions a chunk where the work is 2000).
+// bulk::wait with a hint that lets the thread be suspended for up to 2 us at a
+// time: most warps of the CTA wait for another at any moment.
 __device__ __forceinline__ bool calm_wait(uint32_t bar, uint32_t parity) {
   uint64_t begin = 0;
   for (;;) {
@@ -212,8 +221,9 @@ __device__ __forceinline__ void wide_prepare(const GemvArgs &a, int slot, int sl
 
 // NB blocks of 16 columns to each half of the scaling warps.
 template <int BITS, int NB>
-__global__ void __launch_bounds__(kThreads, 1) gemv_wide_kernel(const GemvArgs a, int slices) {
-  constexpr int kStages = stages<NB>();
+__global__ void __launch_bounds__(threads<NB>(), 1) gemv_wide_kernel(const GemvArgs a, int slices) {
+  constexpr int kStages = stages<NB>(), kTeams = teams<NB>(), kUnpackWarps = 4 * kTeams;
+  constexpr int kCopyWarp = kUnpackWarps + kScaleWarps, kIssueWarp = kCopyWarp + 1;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (bulk::saddr(raw) + 1023u) & ~1023u;
   uint8_t *smem = raw + (base - bulk::saddr(raw));
@@ -238,12 +248,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_wide_kernel(const GemvArgs a
   auto give_up = [&]() { atomicOr(a.err, kErrEntries); };
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) bulk::init(full(s), kUnpackWarps / 2 * 32 + 1), bulk::init(empty(s), 1);
+    for (int s = 0; s < kStages; ++s) bulk::init(full(s), 4 * 32 + 1), bulk::init(empty(s), 1);
     for (int s = 0; s < kMaxSlots; ++s) bulk::init(sum_full(s), 1), bulk::init(sum_empty(s), kScaleWarps);
     bulk::init(done, 1);
     bulk::fence_init();
   }
-  if (warp == 17) {
+  if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bulk::saddr(&tmem_s)),
                  "r"(kTmemCols)
                  : "memory");
@@ -257,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_wide_kernel(const GemvArgs a
   float *out = reinterpret_cast<float *>(smem);  // [kRows][out_stride], over the stages once they are used up
 
   if (warp < kUnpackWarps) {
-    // Two teams of four warps take alternate chunks, so that one waits while the other computes.
+    // Teams of four warps take the chunks in turn, so that some wait while others compute.
     const int team = warp / 4, g = lane >> 2, t = lane & 3;
     const uint8_t *next[4], *pz[4];
     const int c_first = c_begin + team;
@@ -273,9 +283,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_wide_kernel(const GemvArgs a
     const bool swap = BITS != 3 && (t & 2);
     uint8_t *dst0 = smem + (t >> 1) * (kRows * 128) + (warp % 4 * 32 + g) * 128;
     uint32_t w[kAhead][4][BITS], z[kAhead][4];
-    // the group of the lane's run in the chunk to fetch next: run / runs, by steps of eight runs
+    // the group of the lane's run in the chunk to fetch next: run / runs, by steps of a round of the teams
     int group = (c_first * 4 + t) / runs, in_group = (c_first * 4 + t) % runs;
-    const int group_step = 8 / runs, in_step = 8 % runs;
+    const int group_step = 4 * kTeams / runs, in_step = 4 * kTeams % runs;
     auto fetch = [&](auto I, int c) {
       constexpr int i = decltype(I)::value;
       const bool in = c < c_end && c * 4 + t < a.d_in / 32;
@@ -287,23 +297,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_wide_kernel(const GemvArgs a
           gemv::load_run<BITS, 0>(next[h], w[i][h]);
           z[i][h] = __ldg(pz[h] + group);
         }
-        next[h] += 2 * 16 * BITS;
+        next[h] += kTeams * 16 * BITS;
       }
       group += group_step, in_group += in_step;
       if (in_group >= runs) in_group -= runs, ++group;
     };
-    gemv::each<kAhead>([&](auto I) { fetch(I, c_first + 2 * decltype(I)::value); });
+    gemv::each<kAhead>([&](auto I) { fetch(I, c_first + kTeams * decltype(I)::value); });
     bool ok = true;
-    for (int c0 = c_first, it = team; ok && c0 < c_end; c0 += 2 * kAhead) {
+    for (int c0 = c_first, it = team; ok && c0 < c_end; c0 += kTeams * kAhead) {
       gemv::each<kAhead>([&](auto I) {
         constexpr int i = decltype(I)::value;
-        if (!ok || c0 + 2 * i >= c_end) return;
+        if (!ok || c0 + kTeams * i >= c_end) return;
         const int s = it % kStages;
         if (!warp_wait(empty(s), (it / kStages & 1) ^ 1)) {
           give_up();
           ok = false;
           return;
         }
+        const bool any_far = __any_sync(~0u, max(max(z[i][0], z[i][1]), max(z[i][2], z[i][3])) > 127);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           if constexpr (BITS != 3) {
@@ -320,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_wide_kernel(const GemvArgs a
           const uint32_t first = (0x4300u | (far ? 0u : z[i][h])) * 0x10001u;
 #pragma unroll
           for (int p = 0; p < 16; ++p) q[p] = sub_bf16x2(q[p], first);
-          if (__any_sync(~0u, far)) {
+          if (any_far) {
             const uint32_t rest = far ? bf16x2_of((float)z[i][h]) : 0u;
 #pragma unroll
             for (int p = 0; p < 16; ++p) q[p] = sub_bf16x2(q[p], rest);
@@ -331,10 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_wide_kernel(const GemvArgs a
             *reinterpret_cast<uint4 *>(dst + (((4 * (t & 1) + (u ^ (swap ? 2 : 0))) ^ g) << 4)) =
                 make_uint4(q[4 * u], q[4 * u + 1], q[4 * u + 2], q[4 * u + 3]);
         }
-        fetch(I, c0 + 2 * (i + kAhead));
+        fetch(I, c0 + kTeams * (i + kAhead));
         bulk::fence_proxy();
         arrive(full(s));
-        it += 2;
+        it += kTeams;
       });
     }
   } else if (warp < kUnpackWarps + kScaleWarps) {
@@ -394,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_wide_kernel(const GemvArgs a
       if ((2 * b + half) * 16 < a.npad)
 #pragma unroll
         for (int i = 0; i < 16; ++i) out[r * out_stride + (2 * b + half) * 16 + i] = acc[b][i];
-  } else if (warp == 16) {
+  } else if (warp == kCopyWarp) {
     if (lane == 0) {
       // the values are the preparing launch's output (see gemv_mma_kernel)
       if (a.y_ad) {
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_wide_kernel(const GemvArgs a
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   // before the cluster's barrier: another cluster's CTA may be waiting for these columns
-  if (warp == 17) {
+  if (warp == kIssueWarp) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
@@ -514,7 +525,7 @@ cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * slices), (unsigned)cdiv(a.T, a.tpp));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads<NB>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
