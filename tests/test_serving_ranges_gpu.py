@@ -1,0 +1,52 @@
+"""The serving operators at the ends of their ranges: values and zero points that a documented call may hold and that
+ordinary inputs do not."""
+
+import numpy as np
+import pytest
+
+from _serving import dense_weight, random_weight, round_to
+from _util import to_dev
+from test_serving_gpu import _W, _check_base, _check_decode, _decode_case, _dev, _qweight
+from workloads import rng_for
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 6, 8, 24])
+@pytest.mark.parametrize("bits,group", [(4, 128), (3, 64), (2, 32), (4, 8)])
+def test_qgemv_columns_of_tiny_values(bits, group, T, dtype):
+    """128 neighbouring columns whose largest value is the smallest normal number, twice that, or a denormal, by
+    themselves and beside ordinary ones. With scales of 2^100 the tiny columns' sums are ordinary numbers, held to the
+    precision of any other."""
+    W = _W()
+    g = rng_for(120, "tiny", bits, group, T)
+    q, packed, s, z = random_weight(g, 40, 384, bits, group)
+    s = (s * np.float32(2.0**100)).astype(np.float32)
+    wq, w = _qweight(W, bits, group, packed, s, z), dense_weight(q, s, z, group)
+    for top in (2.0**-125, 2.0**-126, 2.0**-130 if dtype == "bf16" else 2.0**-140):
+        for beside in (False, True):
+            x = g.standard_normal((T, 384)).astype(np.float32) if beside else np.zeros((T, 384), np.float32)
+            x[:, 128:256] = g.uniform(-1, 1, (T, 128)) * top
+            x[:, 130] = top
+            x[0, 128:256] = 0.0
+            x[0, 200] = -top  # one value among zeros
+            x = round_to(x, dtype)
+            _check_base(W.qgemv(wq, _dev(x, dtype)), x.astype(np.float64), w, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 3, 24])
+def test_adapter_decode_columns_of_tiny_values(T, dtype):
+    W = _W()
+    d_in, d_out, n = 512, 40, 128
+    g = rng_for(121, "tiny decode", T)
+    rp, ci, cf, q, packed, s, z, x = _decode_case(g, d_in, d_out, n, 4, 128, g.integers(0, 40, d_out), T, dtype)
+    s = (s * np.float32(2.0**100)).astype(np.float32)
+    a = W.Adapter(d_in, d_out, n, ci.size, to_dev(rp), to_dev(ci), to_dev(cf))
+    for top in (2.0**-125, 2.0**-126, 2.0**-130):
+        y = x.copy()
+        y[:, 128:256] = round_to(y[:, 128:256] * np.float32(top / 8), dtype)
+        y[:, 140] = top
+        Y = W.adapter_decode(a, _dev(y, dtype), 0.75, _qweight(W, 4, 128, packed, s, z))
+        _check_decode(Y, y, dense_weight(q, s, z, 128), rp, ci, cf, n, 0.75, dtype)

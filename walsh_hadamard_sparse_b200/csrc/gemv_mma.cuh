@@ -176,6 +176,7 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *v) {
 }
 
 __device__ __forceinline__ float exp2i(int k) { return __int_as_float((k + 127) << 23); }  // -126 <= k <= 127
+__device__ __forceinline__ float exp2_far(int k) { return exp2i(k >> 1) * exp2i(k - (k >> 1)); }  // -149 <= k <= 127
 
 // The tokens as operands: one thread per token, run of 32 columns and quarter
 // of its pairs, the sixteen of a chunk on neighbouring lanes (i = run * 4 + j).
@@ -186,8 +187,9 @@ __device__ __forceinline__ float exp2i(int k) { return __int_as_float((k + 127) 
 // gets, per group, the sum of the scaled values (times 2^-24, the unit of the
 // codes) beside the first piece's column and 0 beside the others, and the
 // factor that undoes the scaling, times 2^12 (the other 2^12 of the unit is
-// applied at the end, so that neither leaves fp32's range). A chunk with an
-// infinity or a NaN gets the factor NaN, which sends its rows' sums to the
+// applied at the end, so that neither leaves fp32's range; below 2^-126, of a
+// chunk whose largest is below 2^-124, the factor is a denormal). A chunk with
+// an infinity or a NaN gets the factor NaN, which sends its rows' sums to the
 // plain path.
 // In shared memory (OWN: one n-tile) a column's pieces lie together, `cols` being
 // the stride between columns.
@@ -248,7 +250,7 @@ __device__ __forceinline__ void prepare_piece(const GemvArgs &a, int tok, int i,
         make_uint4(r[0], r[1], r[2], r[3]);
     if (j == 0 && t % (4 / G) == 0)
       sums[tile * 8 + t * G / 4 * TPN + col % TPN] =
-          make_float2(p == 0 ? sum * 0x1p-24f : 0.f, finite ? exp2i(12 - up) : __int_as_float(0x7fc00000));
+          make_float2(p == 0 ? sum * 0x1p-24f : 0.f, finite ? exp2_far(12 - up) : __int_as_float(0x7fc00000));
   }
 }
 
