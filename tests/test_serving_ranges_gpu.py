@@ -4,9 +4,9 @@ ordinary inputs do not."""
 import numpy as np
 import pytest
 
-from _serving import dense_weight, random_weight, round_to
-from _util import to_dev
-from test_serving_gpu import _W, _check_base, _check_decode, _decode_case, _dev, _qweight
+from _serving import dense_weight, half_step, random_weight, round_to
+from _util import host, to_dev
+from test_serving_gpu import _W, _check_base, _check_decode, _decode_case, _dev, _filled, _qweight, _want_read
 from workloads import rng_for
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +50,28 @@ def test_adapter_decode_columns_of_tiny_values(T, dtype):
         y[:, 140] = top
         Y = W.adapter_decode(a, _dev(y, dtype), 0.75, _qweight(W, 4, 128, packed, s, z))
         _check_decode(Y, y, dense_weight(q, s, z, 128), rp, ci, cf, n, 0.75, dtype)
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+@pytest.mark.parametrize("shape", [(3, 128, 128), (3, 128, 64), (4, 64, 32), (1, 80, 40)])
+def test_cache_read_any_zero_point(shape, bits):
+    """Zero points are bytes of any value, as the weight's are: also above the largest code and above 128."""
+    import torch
+
+    W = _W()
+    heads, head_dim, group = shape
+    g = rng_for(122, "zeros", *shape, bits)
+    for had_block in [n for n in (0, 2, 16, 32, 64, 128) if n == 0 or head_dim % n == 0]:
+        c = _filled(W, g, 6, 16, heads, head_dim, bits, group, had_block)
+        z = g.integers(0, 256, tuple(c.zeros.shape)).astype(np.uint8)
+        z[0], z[1], z[2], z[3] = 255, 128, 129, 2**bits - 1  # page by page
+        c.zeros.copy_(to_dev(z))
+        c.codes[0].zero_()  # codes of 0 under zero points of 255: the largest sums there are
+        table = np.arange(6, dtype=np.int32)[None]
+        out = W.cache_read(c, to_dev(table), to_dev(np.array([0, 96], np.int64)), 96, dtype=torch.float32)
+        want, mag = _want_read(c, bits, group, had_block, table, [0], [96], 16)
+        n = had_block or 1
+        blk = np.repeat(mag.reshape(96, heads, -1, n).sum(-1) / np.sqrt(n), n, axis=-1)
+        tol = half_step("f32") * 1.01 * np.abs(want) + (np.log2(n) + 3) * 2.0**-24 * blk + 1e-30
+        err = np.abs(host(out) - want)
+        assert np.all(err <= tol), float((err / tol).max())

@@ -24,6 +24,7 @@
 // s = NaN, codes and zero point 0: it reads back as NaN and harms no other group.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -315,13 +316,15 @@ __global__ void __launch_bounds__(kCacheThreads)
 // lane reads the eight codes that differ in e0..e2, takes the four with its own
 // e1, and ends with four neighbours of the row. Bits e5 and e6 that lie between
 // two groups of a block are left to fp32 butterflies after the scales.
-// D is at most 16 (2^bits - 1): exact in f16 up to 2048, so for 8 bits it is
-// split into two f16 (D - f16(D) is at most 1).
+// A sum of sixteen in D is at most 16 max(zero, 2^bits - 1): exact in f16 up to
+// 2048, so with zero points up to 128 and 2 to 4 bits it is one f16. For 8 bits,
+// and in a CTA that has met a larger zero point (any byte is valid), it is split
+// into two f16 (D - f16(D) is at most 1).
 //
 // Memory bounds this: 2 bytes written and 0.53 read a value of 4 bits. A CTA
 // fetches 256 units of a tile with all its threads and computes from shared
 // memory; eight CTAs on an SM overlap each other's phases. Two caches, 8 heads
-// of 128, 4 bits, 192526 tokens, bf16: 182 us, 84 % of the copy rate. Loads
+// of 128, 4 bits, 192526 tokens, bf16: 186 us, 82 % of the copy rate. Loads
 // straight to the registers of the lane that uses them, four units in flight a
 // warp, took 285 us (waiting for memory), butterflies in registers and between
 // lanes 309 us (issue slots).
@@ -386,14 +389,18 @@ __device__ __forceinline__ void spread_codes(uint2 c, int word, int e1, uint32_t
 constexpr int kTileUnits = 256;
 constexpr uint32_t kNoSlot = ~0u;  // in place of a zero point
 
+// Five CTAs to an SM where the loop's 48 registers allow (with the rare split in the kernel the compiler takes 59 and
+// leaves room for four: 193 instead of 186 us for the case above).
 template <typename T, int BITS>
-__global__ void __launch_bounds__(kCacheThreads)
+__global__ void __launch_bounds__(kCacheThreads, BITS % 2 || BITS == 8 ? 4 : 5)
     cache_read_mma_kernel(const CachePair c, const ReadArgs r, int64_t n, int tile, unsigned int *err) {
   constexpr int kWarps = kCacheThreads / 32;
   __shared__ int64_t slot_s[kTileTokens];
   __shared__ __align__(16) uint8_t code_s[kTileUnits * 16 * BITS];
   __shared__ float scale_s[kTileUnits * 4];
   __shared__ uint32_t zero_s[kTileUnits * 4];  // 1024 + zero, two f16
+  __shared__ int far_s;  // a zero point above 128 was met: the CTA splits from there on
+  if (threadIdx.x == 0) far_s = 0;
   const qwha_cache &a = c.cache[blockIdx.y];
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, warp = threadIdx.x >> 5;
   const int lg = 31 - __clz(a.group), had = a.had_block > 1 ? a.had_block : 1;
@@ -432,51 +439,62 @@ __global__ void __launch_bounds__(kCacheThreads)
       for (int i = threadIdx.x; i < here * 128 >> lg; i += kCacheThreads) {
         const int token = (g0 + i) / groups;
         const int64_t slot = slot_s[token], group = slot * groups + (g0 + i - token * groups);
-        if (slot >= 0) scale_s[i] = a.scales[group] * scale, zero_s[i] = (a.zeros[group] | 0x6400u) * 0x10001u;
-        else zero_s[i] = kNoSlot;
+        if (slot >= 0) {
+          const uint32_t zero = a.zeros[group];
+          if (BITS != 8 && zero > 128) far_s = 1;
+          scale_s[i] = a.scales[group] * scale, zero_s[i] = (zero | 0x6400u) * 0x10001u;
+        } else {
+          zero_s[i] = kNoSlot;
+        }
       }
       cp_async_wait_all();
       __syncthreads();
-      T *out = rows + (t0 * units + u0 + warp) * 128;
-#pragma unroll 4
-      for (int u = warp; u < here; u += kWarps, out += kWarps * 128) {
-        const int group = u * 128 >> lg;
-        const uint32_t zz = zero_s[group + (g >> 1 >> up)];
-        const float f = scale_s[group + (t >> up)];
-        const bool live = zz != kNoSlot;
-        const uint2 code = load_codes<BITS>(code_s + u * (16 * BITS), word);
-        uint32_t b[2];
-        spread_codes<BITS>(code, word, e1, b);
+      auto compute = [&](auto split) {
+        constexpr bool kSplit = decltype(split)::value;
+        constexpr int kUnroll = kSplit && BITS != 8 ? 1 : 4;  // the rare one is short
+        T *out = rows + (t0 * units + u0 + warp) * 128;
+#pragma unroll kUnroll
+        for (int u = warp; u < here; u += kWarps, out += kWarps * 128) {
+          const int group = u * 128 >> lg;
+          const uint32_t zz = zero_s[group + (g >> 1 >> up)];
+          const float f = scale_s[group + (t >> up)];
+          const bool live = zz != kNoSlot;
+          const uint2 code = load_codes<BITS>(code_s + u * (16 * BITS), word);
+          uint32_t b[2];
+          spread_codes<BITS>(code, word, e1, b);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const __half2 d = __hsub2(reinterpret_cast<const __half2 &>(b[i]), reinterpret_cast<const __half2 &>(zz));
-          b[i] = reinterpret_cast<const uint32_t &>(d);
+          for (int i = 0; i < 2; ++i) {
+            const __half2 d = __hsub2(reinterpret_cast<const __half2 &>(b[i]), reinterpret_cast<const __half2 &>(zz));
+            b[i] = reinterpret_cast<const uint32_t &>(d);
+          }
+          float d[4], e[4];
+          mma_16816(d, ha, b);
+          const uint32_t d0 = f16x2(d[0], d[1]), d1 = f16x2(d[2], d[3]);
+          mma_1688(e, d0, d1, hb);
+          if constexpr (kSplit) {
+            const float2 f0 = __half22float2(reinterpret_cast<const __half2 &>(d0)),
+                         f1 = __half22float2(reinterpret_cast<const __half2 &>(d1));
+            float lo[4];
+            mma_1688(lo, f16x2(d[0] - f0.x, d[1] - f0.y), f16x2(d[2] - f1.x, d[3] - f1.y), hb);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] += lo[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] *= f;
+          if (cross5)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = fmaf(e[i], t & 1 ? -1.f : 1.f, __shfl_xor_sync(~0u, e[i], 1));
+          if (cross6)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = fmaf(e[i], t & 2 ? -1.f : 1.f, __shfl_xor_sync(~0u, e[i], 2));
+          // e0 is the bit of m above g, e1 the lower bit of n'
+          if (!live) continue;
+          if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(out) = make_float4(e[0], e[2], e[1], e[3]);
+          else *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(e[0], e[2]), pack_bf16x2(e[1], e[3]));
         }
-        float d[4], e[4];
-        mma_16816(d, ha, b);
-        const uint32_t d0 = f16x2(d[0], d[1]), d1 = f16x2(d[2], d[3]);
-        mma_1688(e, d0, d1, hb);
-        if constexpr (BITS == 8) {
-          const float2 f0 = __half22float2(reinterpret_cast<const __half2 &>(d0)),
-                       f1 = __half22float2(reinterpret_cast<const __half2 &>(d1));
-          float lo[4];
-          mma_1688(lo, f16x2(d[0] - f0.x, d[1] - f0.y), f16x2(d[2] - f1.x, d[3] - f1.y), hb);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] += lo[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] *= f;
-        if (cross5)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = fmaf(e[i], t & 1 ? -1.f : 1.f, __shfl_xor_sync(~0u, e[i], 1));
-        if (cross6)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = fmaf(e[i], t & 2 ? -1.f : 1.f, __shfl_xor_sync(~0u, e[i], 2));
-        // e0 is the bit of m above g, e1 the lower bit of n'
-        if (!live) continue;
-        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4 *>(out) = make_float4(e[0], e[2], e[1], e[3]);
-        else *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(e[0], e[2]), pack_bf16x2(e[1], e[3]));
-      }
+      };
+      if (BITS == 8 || far_s) compute(std::true_type());
+      else compute(std::integral_constant<bool, BITS == 8>());
     }
   }
 }
