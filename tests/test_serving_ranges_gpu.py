@@ -75,3 +75,18 @@ def test_cache_read_any_zero_point(shape, bits):
         tol = half_step("f32") * 1.01 * np.abs(want) + (np.log2(n) + 3) * 2.0**-24 * blk + 1e-30
         err = np.abs(host(out) - want)
         assert np.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 6, 8, 24, 64])
+@pytest.mark.parametrize("bits,group", [(4, 128), (3, 64), (2, 32), (4, 8)])
+def test_qgemv_values_near_the_largest(bits, group, T, dtype):
+    """Values near the type's largest: a group's sum is beyond fp32's range before its scale, the result is not."""
+    W = _W()
+    g = rng_for(124, "huge", bits, group, T)
+    q, packed, s, z = random_weight(g, 40, 512, bits, group)
+    s = (s * np.float32(1e-4)).astype(np.float32)
+    wq, w = _qweight(W, bits, group, packed, s, z), dense_weight(q, s, z, group)
+    x = round_to(g.uniform(0.5, 1.0, (T, 512)) * 3e38, dtype)
+    x[T // 2] = round_to(g.standard_normal(512), dtype)  # an ordinary token among them
+    _check_base(W.qgemv(wq, _dev(x, dtype)), x.astype(np.float64), w, dtype)

@@ -41,7 +41,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // run lies in one group, as groups are multiples of 8). Takes every group the
 // format has, and calls without a base term.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const GemvArgs a) {
+__global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const __grid_constant__ GemvArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
   const int t0 = blockIdx.y * kRowTokens;
@@ -72,14 +72,31 @@ __global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const GemvArgs a
       }
     }
   }
+  unsigned again = 0;  // tokens whose sum left fp32's range
+  auto put = [&](int u, float v) {
+    if (a.y_ad) v += a.alpha * a.y_ad[row * a.tp + t0 + u];
+    io<T>::store1(static_cast<T *>(a.y) + (int64_t)(t0 + u) * a.d_out + row, v);
+  };
 #pragma unroll
   for (int u = 0; u < kRowTokens; ++u) {
     if (u >= nt) break;
-    float v = warp_sum(base[u]);
-    if (lane == 0 && row < a.d_out) {
-      if (a.y_ad) v += a.alpha * a.y_ad[row * a.tp + t0 + u];
-      io<T>::store1(static_cast<T *>(a.y) + (int64_t)(t0 + u) * a.d_out + row, v);
+    const float v = warp_sum(base[u]);
+    if (!gemv::finite(v)) again |= 1u << u;
+    if (lane == 0 && row < a.d_out) put(u, v);
+  }
+  if (row >= a.d_out || !a.qw) return;
+  for (; again; again &= again - 1) {  // in fp64, as gemv::plain_dot
+    const int u = __ffs(again) - 1;
+    const T *x = static_cast<const T *>(a.x) + (int64_t)(t0 + u) * a.d_in;
+    double sum = 0.;
+    for (int r = lane; r < a.d_in / 8; r += 32) {
+      const int64_t g = row * (a.d_in / a.group) + r * 8 / a.group;
+      sum = fma((double)a.scales[g],
+                gemv::run_dot(run_word(a.qw + (row * (a.d_in / 8) + r) * a.bits, a.bits), a.bits, a.zeros[g], x + r * 8), sum);
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == 0) put(u, (float)sum);
   }
 }
 

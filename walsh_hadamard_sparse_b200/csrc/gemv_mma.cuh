@@ -136,28 +136,35 @@ __device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One row and token by the definition, for results the fast path leaves NaN: a
-// chunk with an infinity or a NaN has no pieces (its factor is NaN).
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.402823466e38f; }
+
+// sum of (q - z) x over a run of eight codes, in fp64.
+template <typename T>
+__device__ __forceinline__ double run_dot(uint32_t w, int bits, int z, const T *x) {
+  double sum = 0.;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i, w >>= bits)
+    sum = fma((double)((int)(w & ((1u << bits) - 1u)) - z), (double)io<T>::load1(x + i), sum);
+  return sum;
+}
+
+// One row and token by the definition in fp64, for results that the products
+// leave infinite or NaN: a token with an infinity or a NaN has no pieces, and a
+// sum of values near the type's largest may leave fp32's range before its scale
+// brings it back. A thread by itself: slow, and rare.
 static __device__ __noinline__ float plain_dot(const GemvArgs &a, int row, int tok) {
   const int ng = a.d_in / a.group;
   const uint8_t *qw = a.qw + (int64_t)row * (a.d_in / 8) * a.bits;
-  const uint32_t mask = (1u << a.bits) - 1u;
-  float sum = 0.f;
+  double sum = 0.;
   for (int r = 0; r < a.d_in / 8; ++r) {
     uint32_t w = 0;
     for (int b = 0; b < a.bits; ++b) w |= (uint32_t)qw[(int64_t)r * a.bits + b] << (8 * b);
-    const int64_t g = (int64_t)row * ng + r * 8 / a.group;
-    const float z = (float)a.zeros[g];
-    float part = 0.f;
-    for (int i = 0; i < 8; ++i) {
-      const int64_t at = (int64_t)tok * a.d_in + r * 8 + i;
-      const float v = a.f32 ? static_cast<const float *>(a.x)[at]
-                            : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.x)[at]);
-      part = fmaf((float)((w >> (a.bits * i)) & mask) - z, v, part);
-    }
-    sum = fmaf(a.scales[g], part, sum);
+    const int64_t g = (int64_t)row * ng + r * 8 / a.group, at = (int64_t)tok * a.d_in + r * 8;
+    const double part = a.f32 ? run_dot(w, a.bits, a.zeros[g], static_cast<const float *>(a.x) + at)
+                              : run_dot(w, a.bits, a.zeros[g], static_cast<const __nv_bfloat16 *>(a.x) + at);
+    sum = fma((double)a.scales[g], part, sum);
   }
-  return sum;
+  return (float)sum;
 }
 
 template <typename T>
@@ -210,13 +217,13 @@ __device__ __forceinline__ void prepare_piece(const GemvArgs &a, int tok, int i,
   for (int u = 0; u < 8; ++u) top = max(top, __float_as_uint(v[u]) & 0x7fffffffu);
 #pragma unroll
   for (int o = 1; o < 16; o *= 2) top = max(top, __shfl_xor_sync(~0u, top, o));
-  const bool finite = top < 0x7f800000u;
-  const int e = max(1, (int)(top >> 23)), up = top && finite ? 141 - e : 0;  // top < 2^(e - 126)
+  const bool whole = top < 0x7f800000u;  // no infinity, no NaN
+  const int e = max(1, (int)(top >> 23)), up = top && whole ? 141 - e : 0;  // top < 2^(e - 126)
   const float f0 = exp2i(up >> 1), f1 = exp2i(up - (up >> 1));
   float sum = 0.f;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    v[u] = finite ? v[u] * f0 * f1 : 0.f;
+    v[u] = whole ? v[u] * f0 * f1 : 0.f;
     sum += v[u];
   }
   const int G = a.group % 128 == 0 ? 1 : a.group % 64 == 0 ? 2 : 4;
@@ -250,7 +257,7 @@ __device__ __forceinline__ void prepare_piece(const GemvArgs &a, int tok, int i,
         make_uint4(r[0], r[1], r[2], r[3]);
     if (j == 0 && t % (4 / G) == 0)
       sums[tile * 8 + t * G / 4 * TPN + col % TPN] =
-          make_float2(p == 0 ? sum * 0x1p-24f : 0.f, finite ? exp2_far(12 - up) : __int_as_float(0x7fc00000));
+          make_float2(p == 0 ? sum * 0x1p-24f : 0.f, whole ? exp2_far(12 - up) : __int_as_float(0x7fc00000));
   }
 }
 
@@ -314,7 +321,7 @@ __device__ __forceinline__ void load_run(const uint8_t *p, uint32_t *w) {
 // OWN: no launch prepared the operands; every CTA makes its own in shared memory.
 template <int BITS, int G, int NT, int MT, int DEPTH, bool EXACT, bool OWN>
 __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
-    gemv_mma_kernel(const GemvArgs a, int tokens_per_pass, int slices) {
+    gemv_mma_kernel(const __grid_constant__ GemvArgs a, int tokens_per_pass, int slices) {
   constexpr int TPN = 8 / G, ROWS = 16 * MT, ROW_CHUNK = 16 * BITS;
   extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -548,7 +555,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
     for (int v = tok * pieces; v < (tok + 1) * pieces; ++v)
       for (int w = 0; w < slices * G; ++w) sum += src[(w * v_most + v) * ROWS];
     sum *= 0x1p12f;  // the rest of the codes' unit
-    if (sum != sum) sum = plain_dot(a, row_first + r, t0 + tok);
+    if (!finite(sum)) sum = plain_dot(a, row_first + r, t0 + tok);
     if (a.y_ad) sum += a.alpha * a.y_ad[(int64_t)(row_first + r) * a.tp + t0 + tok];
     const int64_t at = (int64_t)(t0 + tok) * a.d_out + row_first + r;
     if (a.f32) static_cast<float *>(a.y)[at] = sum;

@@ -221,7 +221,7 @@ __device__ __forceinline__ void wide_prepare(const GemvArgs &a, int slot, int sl
 
 // NB blocks of 16 columns to each half of the scaling warps.
 template <int BITS, int NB>
-__global__ void __launch_bounds__(threads<NB>(), 1) gemv_wide_kernel(const GemvArgs a, int slices) {
+__global__ void __launch_bounds__(threads<NB>(), 1) gemv_wide_kernel(const __grid_constant__ GemvArgs a, int slices) {
   constexpr int kStages = stages<NB>(), kTeams = teams<NB>(), kUnpackWarps = 4 * kTeams;
   constexpr int kCopyWarp = kUnpackWarps + kScaleWarps, kIssueWarp = kCopyWarp + 1;
   extern __shared__ uint8_t raw[];
@@ -500,13 +500,13 @@ __global__ void __launch_bounds__(threads<NB>(), 1) gemv_wide_kernel(const GemvA
 #pragma unroll 4
     for (int tok = first; tok < np; tok += step) {
       const float sum = sum_of(tok);
-      again |= sum != sum;
+      again |= !gemv::finite(sum);
       put(tok, sum);
     }
     if (again)
       for (int tok = first; tok < np; tok += step) {
         const float sum = sum_of(tok);
-        if (sum != sum) put(tok, gemv::plain_dot(a, row, t0 + tok));
+        if (!gemv::finite(sum)) put(tok, gemv::plain_dot(a, row, t0 + tok));
       }
   }
   if (slices > 1) cluster_sync();  // no CTA leaves while another reads its sums
