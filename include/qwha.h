@@ -203,7 +203,9 @@ qwha_status qwha_adapter_bwd(const qwha_adapter *a, const qwha_qweight *wq, qwha
 /* Y = X W_Q^T for 0 <= T <= QWHA_DECODE_MAX_T tokens, straight from the packed
  * codes: X [T, d_in], Y [T, d_out] of dtype dt (fp32 or bf16). Unlike the base
  * GEMM, which rounds W_Q to bf16, the products of q - zeros (an exact integer)
- * and X are summed in fp32 per group and scaled in fp32; Y is rounded once. An
+ * and X are summed in fp32 per group and scaled in fp32; Y is rounded once. (Of
+ * X only bf16 values below 2^-24 of the largest among their 128 columns are
+ * rounded, to 2^-32 of that.) An
  * output whose sums leave fp32's range (values near the type's largest, an
  * infinity, a NaN) is formed again in fp64, a row at a time: right, and slow.
  * d_out >= 1; d_in a multiple of wq->group (a multiple of 8). Deterministic.

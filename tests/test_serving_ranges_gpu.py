@@ -6,8 +6,9 @@ import pytest
 
 from _serving import dense_weight, half_step, random_weight, round_to
 from _util import host, to_dev
-from test_serving_gpu import _W, _check_base, _check_decode, _decode_case, _dev, _filled, _qweight, _want_read
-from workloads import rng_for
+from test_serving_gpu import (_W, _check_base, _check_decode, _decode_case, _dev, _filled,
+                              _qweight, _sum_tol, _want_read)
+from workloads import pack_codes, rng_for
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +91,29 @@ def test_qgemv_values_near_the_largest(bits, group, T, dtype):
     x = round_to(g.uniform(0.5, 1.0, (T, 512)) * 3e38, dtype)
     x[T // 2] = round_to(g.standard_normal(512), dtype)  # an ordinary token among them
     _check_base(W.qgemv(wq, _dev(x, dtype)), x.astype(np.float64), w, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 6, 8, 20, 24])
+@pytest.mark.parametrize("bits,group", [(4, 128), (3, 64), (2, 32), (4, 8), (3, 256)])
+def test_qgemv_values_on_zero_weights_vanish(bits, group, T, dtype):
+    """Values of 1e5 whose weight is zero (code = zero point) add nothing: the sum over the other columns is held as if
+    they were not there. fp32 sums of d_in products, and a value below 2^-24 of the largest among its 128 columns is
+    held to 2^-32 of that."""
+    W = _W()
+    g = rng_for(123, "vanish", bits, group, T)
+    q, packed, s, z = random_weight(g, 48, 512, bits, group, zero_top=None if bits == 3 else 255)
+    z[:, [5 // group, 300 // group]] %= 2**bits
+    q[:, [5, 300]] = z[:, [5 // group, 300 // group]]
+    packed = pack_codes(q, bits)
+    w = dense_weight(q, s, z, group)
+    assert not w[:, [5, 300]].any()
+    x = round_to(g.standard_normal((T, 512)), dtype)
+    x[:, 5], x[:, 300] = round_to(np.array([1e5, -98765.0]), dtype)
+    want = x.astype(np.float64) @ w.T
+    top = np.repeat(np.abs(x).reshape(T, -1, 128).max(-1), 128, axis=-1)
+    low = np.where(np.abs(x) < 2.0**-24 * top, 2.0**-32 * top, 0.0)
+    live = np.abs(x) * (np.abs(x) < 100)
+    tol = half_step(dtype) * 1.01 * np.abs(want) + (_sum_tol(512) * live + low) @ np.abs(w).T
+    err = np.abs(host(W.qgemv(_qweight(W, bits, group, packed, s, z), _dev(x, dtype))) - want)
+    assert np.all(err <= tol), float((err / tol).max())

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const Gemv
   }
   if ((int)blockIdx.x >= spans) {
     const int parts = (a.d_in + 127) / 128 * 16, i = (blockIdx.x - spans) * kPrepThreads + threadIdx.x;
-    gemv::prepare_piece<BITS, false, T>(a, i / parts, i % parts, i < a.T * parts, a.T * a.pieces, a.xpieces, a.xsums);
+    gemv::prepare_piece<BITS, false, T>(a, i / parts, i % parts, i < a.T * parts, a.T * a.pieces, a.xpieces, a.xfac);
     return;
   }
   const int per = (a.d_in + span - 1) / span;
@@ -478,7 +478,7 @@ size_t gemv_x_bytes(int32_t d_in, int64_t T, bool f32) {
   int tpp, npad;
   wide_shape(T, f32, &tpp, &npad);
   if (npad) return (size_t)cdiv(T, tpp) * cdiv(d_in, 128) * npad * 256 + align_up(T * 4, 256);
-  return xpieces_bytes(d_in, T, f32) + align_up((size_t)cdiv(d_in, 128) * 64 * x_tiles((int)T * pieces_of(f32), 4), 256);
+  return xpieces_bytes(d_in, T, f32) + align_up((size_t)cdiv(d_in, 128) * 32 * x_tiles((int)T * pieces_of(f32), 4), 256);
 }
 
 void gemv_place_x(GemvArgs *a, void *ws) {
@@ -490,7 +490,7 @@ void gemv_place_x(GemvArgs *a, void *ws) {
     a->fac = reinterpret_cast<float *>(static_cast<char *>(ws) + bytes);
     return;
   }
-  a->xsums = reinterpret_cast<float2 *>(static_cast<char *>(ws) + xpieces_bytes(a->d_in, a->T, a->f32));
+  a->xfac = reinterpret_cast<float *>(static_cast<char *>(ws) + xpieces_bytes(a->d_in, a->T, a->f32));
 }
 
 namespace {

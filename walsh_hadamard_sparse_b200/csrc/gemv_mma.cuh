@@ -4,19 +4,21 @@
 // Unpacking bounds this kernel more than memory does: at 6.5 TB/s a 4-bit code
 // leaves about three instruction slots, and half as many on the integer pipe.
 // Two exact representations keep the count below one slot a code:
-//   * a code masked out of a 16-bit half at bit o (o + bits <= 10), ORed into
-//     the mantissa of the f16 1024, is 1024 + q * 2^o: one instruction for two
-//     codes, most need no shift, and a subtraction leaves q * 2^o (`normal`);
+//   * a code masked out of a 16-bit half at bit o (o <= 7, o + bits <= 10), ORed
+//     into the mantissa of the f16 1024, is 1024 + q * 2^o: one instruction for
+//     two codes, most need no shift, and subtracting 1024 + zero * 2^o leaves
+//     (q - zero) * 2^o, all exact for any zero point of a byte (`less_zero`);
 //   * the tokens' values, scaled by a power of two per chunk of 128 columns so
 //     that the largest lies in [2^14, 2^15), are f16 numbers too: a bf16 value
-//     in one piece, an fp32 value in three (exact down to 2^-31 of the chunk's
-//     largest or less); 2^-o is folded into the values
-//     (decode_prepare_kernel). Each piece is a column of the instruction.
+//     in one piece (below 2^-24 of the chunk's largest it is held to 2^-32 of
+//     that), an fp32 value in three, each of what the one before leaves times
+//     2^11 (all 24 bits, down to 2^-54 of the largest); 2^-o is folded into the
+//     values (decode_prepare_kernel). Each piece is a column of the instruction.
 // The matrix unit (m16n8k16, 8.3 clocks measured for f16 and bf16 alike) adds
 // the exact products in fp32 over one quantization group; then, in fp32,
-//   acc += scale * 2^k * (sum_k q x - zero * sum_k x),
-// with 2^k and sum_k x per (group, piece) prepared beside the values. No
-// weight is rounded.
+//   acc += scale * (2^k * sum_k (q - zero) x),
+// with 2^k per (chunk, token) prepared beside the values. No weight is rounded,
+// and a value on a zero weight leaves nothing.
 //
 // Layout. A warp takes 16 MT rows and a slice of the columns; the warps of a
 // CTA are KS slices of kWarps / KS tiles. The four lanes of a row take a run of
@@ -31,8 +33,8 @@
 // lane that uses them, DEPTH chunks ahead, past L1; the values come through L1,
 // or with OWN from shared memory. No barrier until the slices are added.
 //
-// 14336 x 4096, 3 bits, one token: 17.8 us; 4096 x 14336, 4 bits, eight tokens:
-// 14.6 us (33% of the copy rate). Tried and slower: codes through rings of
+// 14336 x 4096, 3 bits, one token: 15.5 us; 4096 x 14336, 4 bits, eight tokens:
+// 13.2 us (37% of the copy rate). Tried and slower: codes through rings of
 // shared memory filled by bulk copies (18 to 30 us), fp8 operands (converted on
 // the integer pipe, 26 us), values staged in shared memory (18 and 35 us).
 
@@ -65,7 +67,7 @@ __host__ __device__ constexpr int gap() {
 template <int BITS>
 __host__ __device__ constexpr int unit(int p) {
   if (BITS == 4) return p % 2 * 4;
-  if (BITS == 2) return p % 8 < 5 ? 2 * (p % 8) : 2 * (p % 8 - 5);
+  if (BITS == 2) return p % 4 * 2;
   constexpr int u[16] = {0, 3, 6, 0, 3, 6, 2, 5, 0, 3, 6, 1, 4, 7, 0, 3};
   return u[p];
 }
@@ -83,11 +85,11 @@ __device__ __forceinline__ void unpack(const uint32_t *w, uint32_t *q) {
   } else if constexpr (BITS == 2) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t h = w[i] >> 10;
+      const uint32_t h = w[i] >> 8;
 #pragma unroll
-      for (int j = 0; j < 5; ++j) q[8 * i + j] = w[i] & (0x00030003u << (2 * j));
+      for (int j = 0; j < 4; ++j) q[8 * i + j] = w[i] & (0x00030003u << (2 * j));
 #pragma unroll
-      for (int j = 0; j < 3; ++j) q[8 * i + 5 + j] = h & (0x00030003u << (2 * j));
+      for (int j = 0; j < 4; ++j) q[8 * i + 4 + j] = h & (0x00030003u << (2 * j));
     }
   } else {
     // the 96 bits as halves h0..h5: codes 0..15 are h0..h2, codes 16..31 are h3..h5; side by side, halves i and
@@ -106,17 +108,31 @@ __device__ __forceinline__ void unpack(const uint32_t *w, uint32_t *q) {
   }
 }
 
-// The denormals q 2^(o - 24) as the numbers q 2^o: 1024 + q 2^o by its bits, less
-// 1024. The matrix unit aligns products by the operands' nominal exponents, so
-// denormal codes cost the sums about eight bits (4096 x 14336, 2 bits, token
-// values of up to 94 among ones: off by 1.5e-5 of the result, by 3e-7 with
-// normal codes), which a value of a thousand among ones would show in bf16 too.
-// One addition for two codes, on another pipe than the unpacking.
-__device__ __forceinline__ uint32_t normal(uint32_t q) {
-  q |= 0x64006400u;
-  const uint32_t of1024 = 0x64006400u;
-  const __half2 d = __hsub2(reinterpret_cast<const __half2 &>(q), reinterpret_cast<const __half2 &>(of1024));
-  return reinterpret_cast<const uint32_t &>(d);
+// (q - zero) 2^o of the sixteen pairs, from q at bit o of its half: 1024 + q 2^o
+// by its bits, less 1024 + zero 2^o (a multiple of 2^o up to 1024 + 255 * 2^7:
+// an f16 number). One addition for two codes, on another pipe than the
+// unpacking. The codes as they are, f16 denormals, would be exact too, but the
+// matrix unit aligns products by the operands' nominal exponents, so they cost
+// the sums about eight bits; and zero * sum x taken off a sum of q x costs the
+// bits of a large value that does not count (1e5 among ones, whose weight is 0:
+// off by 0.13).
+template <int BITS>
+__device__ __forceinline__ void less_zero(uint32_t *q, uint32_t zero) {
+  const uint32_t at0 = zero * 0x10001u + 0x64006400u, of1024 = 0x64006400u;
+  const __half2 z = __hsub2(reinterpret_cast<const __half2 &>(at0), reinterpret_cast<const __half2 &>(of1024));
+  __half2 off[8];
+#pragma unroll
+  for (int o = 0; o < 8; ++o) {
+    const uint32_t by = (0x3c00u + (o << 10)) * 0x10001u;  // 2^o
+    off[o] = o ? __hfma2(z, reinterpret_cast<const __half2 &>(by), reinterpret_cast<const __half2 &>(of1024))
+               : reinterpret_cast<const __half2 &>(at0);
+  }
+#pragma unroll
+  for (int p = 0; p < 16; ++p) {
+    q[p] |= of1024;
+    const __half2 d = __hsub2(reinterpret_cast<const __half2 &>(q[p]), off[unit<BITS>(p)]);
+    q[p] = reinterpret_cast<const uint32_t &>(d);
+  }
 }
 
 // d = A B
@@ -188,21 +204,17 @@ __device__ __forceinline__ float exp2_far(int k) { return exp2i(k >> 1) * exp2i(
 // The tokens as operands: one thread per token, run of 32 columns and quarter
 // of its pairs, the sixteen of a chunk on neighbouring lanes (i = run * 4 + j).
 // The chunk's values are scaled by the power of two that brings the largest
-// into [2^14, 2^15), then split into f16 pieces by rounding and subtracting
-// (exact in fp32: each piece takes the leading eleven bits, so a bf16 value is
-// one piece and an fp32 value three). A pair's unit divides its values. sums
-// gets, per group, the sum of the scaled values (times 2^-24, the unit of the
-// codes) beside the first piece's column and 0 beside the others, and the
-// factor that undoes the scaling, times 2^12 (the other 2^12 of the unit is
-// applied at the end, so that neither leaves fp32's range; below 2^-126, of a
-// chunk whose largest is below 2^-124, the factor is a denormal). A chunk with
-// an infinity or a NaN gets the factor NaN, which sends its rows' sums to the
-// plain path.
+// into [2^14, 2^15), then split into f16 pieces: the value rounded, and what
+// that leaves, exact in fp32, times 2^11 for the next (the product's end takes
+// the 2^-11 back). A pair's unit divides its values. factors gets, per group
+// beside each column, the power of two that undoes the scaling: a denormal for
+// a chunk whose largest is below 2^-112. A chunk with an infinity or a NaN gets
+// the factor NaN, which sends its rows' sums to the plain path.
 // In shared memory (OWN: one n-tile) a column's pieces lie together, `cols` being
 // the stride between columns.
 template <int BITS, bool OWN, typename T>
 __device__ __forceinline__ void prepare_piece(const GemvArgs &a, int tok, int i, bool live, int cols, uint4 *pieces,
-                                              float2 *sums) {
+                                              float *factors) {
   const int run = i >> 2, j = i & 3, chunk = run >> 2, t = run & 3, k0 = run * 32;
   // the pairs' first halves and second halves are four consecutive values each
   const int at = first<BITS>(0) + (BITS == 4 ? 8 * j : BITS == 2 ? 16 * (j >> 1) + 4 * (j & 1) : 4 * j);
@@ -220,44 +232,31 @@ __device__ __forceinline__ void prepare_piece(const GemvArgs &a, int tok, int i,
   const bool whole = top < 0x7f800000u;  // no infinity, no NaN
   const int e = max(1, (int)(top >> 23)), up = top && whole ? 141 - e : 0;  // top < 2^(e - 126)
   const float f0 = exp2i(up >> 1), f1 = exp2i(up - (up >> 1));
-  float sum = 0.f;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    v[u] = whole ? v[u] * f0 * f1 : 0.f;
-    sum += v[u];
-  }
-  const int G = a.group % 128 == 0 ? 1 : a.group % 64 == 0 ? 2 : 4;
-  sum += __shfl_xor_sync(~0u, sum, 1);
-  sum += __shfl_xor_sync(~0u, sum, 2);
-  const float sum2 = sum + __shfl_xor_sync(~0u, sum, 4);
-  const float sum4 = sum2 + __shfl_xor_sync(~0u, sum2, 8);
+  for (int u = 0; u < 8; ++u) v[u] = whole ? v[u] * f0 * f1 : 0.f;
   if (!live) return;
-  sum = G == 1 ? sum4 : G == 2 ? sum2 : sum;
+  const int G = a.group % 128 == 0 ? 1 : a.group % 64 == 0 ? 2 : 4;
   for (int p = 0; p < a.pieces; ++p) {
     const int col = tok * a.pieces + p, TPN = 8 / G;
     const int64_t tile = OWN ? chunk : (int64_t)chunk * x_tiles(cols, G) + col / TPN;
     uint32_t r[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      // 2^-unit of pair 4 j + k
-      float by;
-      if (BITS == 4) by = k % 2 ? 0x1p-4f : 1.f;
-      else {
-        constexpr int A[4] = {unit<BITS>(0), unit<BITS>(1), unit<BITS>(2), unit<BITS>(3)},
-                      B[4] = {unit<BITS>(4), unit<BITS>(5), unit<BITS>(6), unit<BITS>(7)},
-                      C[4] = {unit<BITS>(8), unit<BITS>(9), unit<BITS>(10), unit<BITS>(11)},
-                      D[4] = {unit<BITS>(12), unit<BITS>(13), unit<BITS>(14), unit<BITS>(15)};
-        by = exp2i(-(j == 0 ? A[k] : j == 1 ? B[k] : j == 2 ? C[k] : D[k]));
-      }
-      const __half2 h = __floats2half2_rn(v[k], v[4 + k]), d = __floats2half2_rn(v[k] * by, v[4 + k] * by);
+      // the unit of pair 4 j + k
+      constexpr int A[4] = {unit<BITS>(0), unit<BITS>(1), unit<BITS>(2), unit<BITS>(3)},
+                    B[4] = {unit<BITS>(4), unit<BITS>(5), unit<BITS>(6), unit<BITS>(7)},
+                    C[4] = {unit<BITS>(8), unit<BITS>(9), unit<BITS>(10), unit<BITS>(11)},
+                    D[4] = {unit<BITS>(12), unit<BITS>(13), unit<BITS>(14), unit<BITS>(15)};
+      const int o = j == 0 ? A[k] : j == 1 ? B[k] : j == 2 ? C[k] : D[k];
+      const float by = exp2i(-o), back = exp2i(o);
+      const __half2 d = __floats2half2_rn(v[k] * by, v[4 + k] * by);
       r[k] = *reinterpret_cast<const uint32_t *>(&d);
-      v[k] -= __low2float(h), v[4 + k] -= __high2float(h);
+      v[k] = (v[k] - __low2float(d) * back) * 2048.f, v[4 + k] = (v[4 + k] - __high2float(d) * back) * 2048.f;
     }
     pieces[OWN ? col * cols + chunk * 16 + j * 4 + t : tile * (16 * TPN) + j * (4 * TPN) + col % TPN * 4 + t] =
         make_uint4(r[0], r[1], r[2], r[3]);
     if (j == 0 && t % (4 / G) == 0)
-      sums[tile * 8 + t * G / 4 * TPN + col % TPN] =
-          make_float2(p == 0 ? sum * 0x1p-24f : 0.f, whole ? exp2_far(12 - up) : __int_as_float(0x7fc00000));
+      factors[tile * 8 + t * G / 4 * TPN + col % TPN] = whole ? exp2_far(-up) : __int_as_float(0x7fc00000);
   }
 }
 
@@ -281,10 +280,10 @@ __device__ __forceinline__ bool wait_ready(const unsigned int *word) {
   }
 }
 
-// A lane's operands of an n-tile, and the (sum, factor) pairs of its two columns.
+// A lane's operands of an n-tile, and the factors of its two columns.
 struct XTile {
   uint4 x[4];
-  float4 f;
+  float2 f;
 };
 
 template <int BITS>
@@ -369,16 +368,17 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
   };
   // With one group to a chunk, the four lanes of a row load those of four chunks and hand them round: a quarter of
   // the requests (each touches eight rows), and half the registers of a ring of them.
-  float sn[2 * MT], zn[2 * MT], s4[2 * MT], z4[2 * MT];
+  float sn[2 * MT], s4[2 * MT];
+  uint32_t zn[2 * MT], z4[2 * MT];
   auto fetch_scales = [&](int c) {  // of chunks c .. c + 3
     const int ct = c + t;
 #pragma unroll
     for (int h = 0; h < 2 * MT; ++h) {
-      sn[h] = 0.f, zn[h] = 0.f;
+      sn[h] = 0.f, zn[h] = 0;
       if (ct < c_end) {
         const int gi = EXACT ? ct - c_begin : ct * 128 / a.group;
         sn[h] = __ldg(ps[h] + gi);
-        zn[h] = (float)__ldg(pz[h] + gi);
+        zn[h] = __ldg(pz[h] + gi);
       }
     }
   };
@@ -398,19 +398,19 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
   // this lane's column of an n-tile: a piece, live where the column's group is the lane's own
   const bool mine = g / TPN == t * G / 4;
   const uint4 *xp;
-  const float4 *xs;
+  const float2 *xs;
   if constexpr (OWN) {
     const int column = chunks * 16 + 4, parts = chunks * 16;  // padded: two columns' quarters in different banks
     uint4 *own = reinterpret_cast<uint4 *>(smem + kWarps * G * v_most * ROWS);
-    float2 *sums = reinterpret_cast<float2 *>(own + v_most * column);
+    float *factors = reinterpret_cast<float *>(own + v_most * column);
     for (int i = threadIdx.x; (i & ~31) < a.T * parts; i += kWarps * 32) {
       const bool live = i < a.T * parts;
-      if (a.f32) prepare_piece<BITS, true, float>(a, i / parts, i % parts, live, column, own, sums);
-      else prepare_piece<BITS, true, __nv_bfloat16>(a, i / parts, i % parts, live, column, own, sums);
+      if (a.f32) prepare_piece<BITS, true, float>(a, i / parts, i % parts, live, column, own, factors);
+      else prepare_piece<BITS, true, __nv_bfloat16>(a, i / parts, i % parts, live, column, own, factors);
     }
     __syncthreads();
     xp = own + g % TPN * column + c_begin * 16 + t;
-    xs = reinterpret_cast<const float4 *>(sums) + c_begin * 4 + t;
+    xs = reinterpret_cast<const float2 *>(factors) + c_begin * 4 + t;
   } else {
     // The values are the preparing launch's output: wait for it only here. With the entries' launch in between,
     // which runs beside this one, its word says so.
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
       asm volatile("griddepcontrol.wait;" ::: "memory");
     }
     xp = a.xpieces + ((int64_t)c_begin * n_tiles + nt0) * (16 * TPN) + g % TPN * 4 + t;
-    xs = reinterpret_cast<const float4 *>(a.xsums) + ((int64_t)c_begin * n_tiles + nt0) * 4 + t;
+    xs = reinterpret_cast<const float2 *>(a.xfac) + ((int64_t)c_begin * n_tiles + nt0) * 4 + t;
   }
   // Tile n of the chunk `ahead` behind the pointers. The values are asked for as soon as the tile before in their
   // registers is used: they come from L2 as often as not. Columns of other groups and behind the last piece are
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
         Chunk<BITS, G, MT> &f = buf[i];
         constexpr int at_chunk = i;
         uint32_t q[2 * MT][16];
-        float s[2 * MT], zp[2 * MT];
+        float s[2 * MT];
         [[maybe_unused]] const int of_four = DEPTH == 4 ? i : (c + i - c_begin) & 3;
         if constexpr (G == 1) {
           if (of_four == 0) {
@@ -488,21 +488,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
         }
 #pragma unroll
         for (int h = 0; h < 2 * MT; ++h) {
-          unpack<BITS>(f.w[h], q[h]);
-#pragma unroll
-          for (int p = 0; p < 16; ++p) q[h][p] = normal(q[h][p]);
+          uint32_t zero;
           if constexpr (G == 1) {
-            s[h] = __shfl_sync(~0u, s4[h], of_four, 4), zp[h] = __shfl_sync(~0u, z4[h], of_four, 4);
+            s[h] = __shfl_sync(~0u, s4[h], of_four, 4), zero = __shfl_sync(~0u, z4[h], of_four, 4);
           } else {
-            s[h] = f.s[h], zp[h] = (float)f.z[h];
+            s[h] = f.s[h], zero = f.z[h];
           }
+          unpack<BITS>(f.w[h], q[h]);
+          less_zero<BITS>(q[h], zero);
         }
         fetch(f, c + i + DEPTH, I);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if (NT > 1 && n * TPN >= v_end) break;
           const uint4 *x = xt[n % S].x;
-          const float4 fx = xt[n % S].f;
+          const float2 fx = xt[n % S].f;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             const uint32_t *q0 = q[2 * m], *q1 = q[2 * m + 1];
@@ -516,11 +516,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
             // d[0], d[1]: row g, columns 2t and 2t + 1, whose group is this lane's; d[2], d[3]: row g + 8
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              constexpr float unit_of = 0x1p-24f;  // keeps sums of any tokens within fp32's range
-              acc[m][n][2 * h] =
-                  fmaf(s[2 * m + h] * fx.y, fmaf(-zp[2 * m + h], fx.x, d[2 * h] * unit_of), acc[m][n][2 * h]);
-              acc[m][n][2 * h + 1] =
-                  fmaf(s[2 * m + h] * fx.w, fmaf(-zp[2 * m + h], fx.z, d[2 * h + 1] * unit_of), acc[m][n][2 * h + 1]);
+              acc[m][n][2 * h] = fmaf(s[2 * m + h], d[2 * h] * fx.x, acc[m][n][2 * h]);
+              acc[m][n][2 * h + 1] = fmaf(s[2 * m + h], d[2 * h + 1] * fx.y, acc[m][n][2 * h + 1]);
             }
           }
           if (n + S < NT && (n + S) * TPN < v_end) load_x(xt[n % S], at_chunk, n + S);
@@ -552,9 +549,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT <= 4 ? 2 : 1)
     if (r >= rows_here) continue;
     const float *src = red + (r / ROWS) * slices * G * v_most * ROWS + r % ROWS;
     float sum = 0.f;
-    for (int v = tok * pieces; v < (tok + 1) * pieces; ++v)
-      for (int w = 0; w < slices * G; ++w) sum += src[(w * v_most + v) * ROWS];
-    sum *= 0x1p12f;  // the rest of the codes' unit
+    float by = 1.f;  // of the piece
+    for (int v = tok * pieces; v < (tok + 1) * pieces; ++v, by *= 0x1p-11f) {
+      float part = 0.f;
+      for (int w = 0; w < slices * G; ++w) part += src[(w * v_most + v) * ROWS];
+      sum = fmaf(part, by, sum);
+    }
     if (!finite(sum)) sum = plain_dot(a, row_first + r, t0 + tok);
     if (a.y_ad) sum += a.alpha * a.y_ad[(int64_t)(row_first + r) * a.tp + t0 + tok];
     const int64_t at = (int64_t)(t0 + tok) * a.d_out + row_first + r;
@@ -575,7 +575,7 @@ cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   int slices = 1;
   while (slices < kWarps && tiles * slices < (int64_t)sm_count() * 12 && chunks >= 2 * slices) slices *= 2;
   size_t smem = sizeof(float) * (size_t)kWarps * G * tpp * a.pieces * ROWS;
-  if (OWN) smem += (size_t)a.T * a.pieces * (chunks * 16 + 4) * sizeof(uint4) + chunks * 64;
+  if (OWN) smem += (size_t)a.T * a.pieces * (chunks * 16 + 4) * sizeof(uint4) + chunks * 32;
   auto kernel = gemv_mma_kernel<BITS, G, NT, MT, DEPTH, EXACT, OWN>;
   static std::atomic<size_t> allowed[64];
   const cudaError_t e = allow_smem((const void *)kernel, smem, allowed);

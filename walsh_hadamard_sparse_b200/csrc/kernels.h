@@ -172,10 +172,10 @@ struct GemvArgs {
   unsigned int *ready;  // 1 once the preparing launch is complete (beside zt)
   unsigned int *err;    // the device's error word
   // The values as operands, `pieces` columns a token, TPN = 8 / G columns to an n-tile (G groups in a chunk of 128
-  // columns): xpieces [chunk][n-tile][4][TPN][4 runs] of 16 bytes, xsums [chunk][n-tile][8] (sum, factor) pairs.
+  // columns): xpieces [chunk][n-tile][4][TPN][4 runs] of 16 bytes, xfac [chunk][n-tile][8] factors.
   int pieces;
   uint4 *xpieces;  // NULL: the product makes them itself
-  float2 *xsums;
+  float *xfac;
   // Many columns instead (npad > 0): passes of tpp tokens, padded to npad columns; xpieces [pass][chunk][2][npad][128]
   // bytes, fac [T] the factors of fp32 tokens.
   int tpp, npad;
@@ -190,7 +190,7 @@ size_t gemv_x_bytes(int32_t d_in, int64_t T, bool f32);
 void gemv_place_x(GemvArgs *a, void *ws);
 size_t gemv_z_bytes(int32_t d_out, int32_t d_in, int64_t T);
 void gemv_place_z(GemvArgs *a, void *ws);
-// Fills a.zt (if set), a.xpieces and a.xsums (if set) and z_out (if not NULL) from a.x.
+// Fills a.zt (if set), a.xpieces and its factors (if set) and z_out (if not NULL) from a.x.
 cudaError_t launch_decode_prepare(const GemvArgs &a, int logn, void *z_out, cudaStream_t s);
 cudaError_t launch_decode_entries(const GemvArgs &a, cudaStream_t s);
 cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s);
