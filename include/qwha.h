@@ -204,10 +204,10 @@ qwha_status qwha_adapter_bwd(const qwha_adapter *a, const qwha_qweight *wq, qwha
  * codes: X [T, d_in], Y [T, d_out] of dtype dt (fp32 or bf16). Unlike the base
  * GEMM, which rounds W_Q to bf16, the products of q - zeros (an exact integer)
  * and X are summed in fp32 per group and scaled in fp32; Y is rounded once. (Of
- * X only bf16 values below 2^-24 of the largest among their 128 columns are
- * rounded, to 2^-32 of that.) An
- * output whose sums leave fp32's range (values near the type's largest, an
- * infinity, a NaN) is formed again in fp64, a row at a time: right, and slow.
+ * X only values far below the largest of their 128 columns are rounded: bf16
+ * below 2^-24 of it to 2^-32 of it, fp32 below 2^-30 to 2^-54.) An output whose
+ * sums leave fp32's range (values near the type's largest, an infinity, a NaN)
+ * is formed again in fp64, a row at a time: right, and slow.
  * d_out >= 1; d_in a multiple of wq->group (a multiple of 8). Deterministic.
  * QWHA_ERR_UNSUPPORTED above QWHA_DECODE_MAX_T. ws:
  * qwha_workspace_size(QWHA_OP_QGEMV, d_out, d_in, 0, T, with_base) bytes,

@@ -117,3 +117,39 @@ def test_qgemv_values_on_zero_weights_vanish(bits, group, T, dtype):
     tol = half_step(dtype) * 1.01 * np.abs(want) + (_sum_tol(512) * live + low) @ np.abs(w).T
     err = np.abs(host(W.qgemv(_qweight(W, bits, group, packed, s, z), _dev(x, dtype))) - want)
     assert np.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 8, 9])
+@pytest.mark.parametrize("n_entries", [20, 400, 1500])
+def test_adapter_decode_infinities_stay_in_their_block(n_entries, T, dtype):
+    """An infinity or a NaN reaches, of the adapter's sums, the rows with an entry in its Hadamard block; others keep
+    their value, whatever their length, and columns outside the layer are skipped."""
+    W = _W()
+    d_in, d_out, n = 4096, 40, 1024
+    g = rng_for(125, "block", n_entries)
+    F = np.zeros((d_out, d_in), np.float32)
+    for i in range(d_out):
+        lo = 0 if i % 4 == 0 else 1024  # every fourth row has entries in the first block
+        k = max(1, n_entries - 3 * i)
+        F[i, lo + g.permutation(d_in - lo)[:k]] = g.standard_normal(k) * 0.05 + 0.2
+        if i % 4 == 0:
+            F[i, 17] = 0.25
+    rows, ci = np.nonzero(F)
+    cf = F[rows, ci]
+    rp = np.concatenate([[0], np.cumsum(np.bincount(rows, minlength=d_out))]).astype(np.int32)
+    ci = ci.astype(np.int32)
+    last = rp[1:] - 1
+    ci[last[1]], ci[last[2]] = -1, d_in + 5  # outside: skipped
+    a = W.Adapter(d_in, d_out, n, ci.size, to_dev(rp), to_dev(ci), to_dev(cf))
+    x = round_to(g.standard_normal((T, d_in)), dtype)
+    clean = host(W.adapter_decode(a, _dev(x, dtype), 0.5))
+    y = x.copy()
+    y[T // 2, 3], y[T - 1, 700] = np.inf, np.nan
+    got = host(W.adapter_decode(a, _dev(y, dtype), 0.5))
+    assert np.all(np.isfinite(clean))
+    whole = [t for t in range(T) if t not in (T // 2, T - 1)]
+    assert np.array_equal(got[whole], clean[whole])
+    touched = np.arange(d_out) % 4 == 0
+    assert np.array_equal(got[:, ~touched], clean[:, ~touched])
+    assert not np.any(np.isfinite(got[[T // 2, T - 1]][:, touched]))

@@ -207,27 +207,31 @@ __device__ __forceinline__ void row_sum(const int32_t *cols, const float *coefs,
     float c[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const bool in = j + u * L < n;
-      k[u] = in ? cols[j + u * L] : -1;
-      c[u] = in ? coefs[j + u * L] : 0.f;
+      const bool there = j + u * L < n;
+      k[u] = there ? cols[j + u * L] : -1;
+      c[u] = there ? coefs[j + u * L] : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      if ((unsigned)k[u] >= (unsigned)d_in) k[u] = 0, c[u] = 0.f;
-      const float *z = zs + (int64_t)k[u] * TG;
+      // behind the last entry and outside the layer nothing is added: 0 * Z would be NaN for an infinite Z
+      const bool in = (unsigned)k[u] < (unsigned)d_in;
+      const float *z = zs + (int64_t)(in ? k[u] : 0) * TG;
+      float v[TG];
       if constexpr (TG >= 4) {
 #pragma unroll
         for (int i = 0; i < TG; i += 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(z + i);
-          acc[i] = fmaf(c[u], v.x, acc[i]), acc[i + 1] = fmaf(c[u], v.y, acc[i + 1]);
-          acc[i + 2] = fmaf(c[u], v.z, acc[i + 2]), acc[i + 3] = fmaf(c[u], v.w, acc[i + 3]);
+          const float4 w = *reinterpret_cast<const float4 *>(z + i);
+          v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
         }
       } else if constexpr (TG == 2) {
-        const float2 v = *reinterpret_cast<const float2 *>(z);
-        acc[0] = fmaf(c[u], v.x, acc[0]), acc[1] = fmaf(c[u], v.y, acc[1]);
+        const float2 w = *reinterpret_cast<const float2 *>(z);
+        v[0] = w.x, v[1] = w.y;
       } else {
-        acc[0] = fmaf(c[u], *z, acc[0]);
+        v[0] = *z;
       }
+#pragma unroll
+      for (int i = 0; i < TG; ++i)
+        if (in) acc[i] = fmaf(c[u], v[i], acc[i]);
     }
   }
 #pragma unroll
