@@ -284,8 +284,9 @@ qwha_status qwha_cache_read(const qwha_cache *caches, int32_t n_caches, qwha_dty
                             void *const *rows, int64_t n, void *stream);
 
 /* Check on the device that slots [n] are -1 or within the cache and distinct.
- * Synchronises the stream. QWHA_ERR_INVALID_ARG names the first failure in
- * qwha_last_error(). ws: qwha_workspace_size(QWHA_OP_SLOTS, 1, 1, n_pages *
+ * Synchronises the stream. QWHA_ERR_INVALID_ARG names in qwha_last_error() the
+ * first row whose slot is outside the cache or is another row's too (the first
+ * of the two, then). ws: qwha_workspace_size(QWHA_OP_SLOTS, 1, 1, n_pages *
  * page_size, 0, 0) bytes. */
 qwha_status qwha_validate_slots(const qwha_cache *cache, const int64_t *slots, int64_t n, void *ws,
                                 size_t ws_bytes, void *stream);

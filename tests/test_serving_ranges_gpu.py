@@ -153,3 +153,22 @@ def test_adapter_decode_infinities_stay_in_their_block(n_entries, T, dtype):
     touched = np.arange(d_out) % 4 == 0
     assert np.array_equal(got[:, ~touched], clean[:, ~touched])
     assert not np.any(np.isfinite(got[[T // 2, T - 1]][:, touched]))
+
+
+def test_validate_slots_names_the_first_failure():
+    """The first row whose slot is outside the cache or is another row's too, the same on every call."""
+    W = _W()
+    c = W.cache_alloc(1024, 64, 1, 64)
+    g = rng_for(126, "slots")
+    for outside, pairs in (((), 11), ((60000, 64000), 5), ((9, 10), 5), ((40000,), 0)):
+        s = g.permutation(65536).astype(np.int64)
+        s[::50] = -1
+        for i in range(pairs):
+            s[1001 + 700 * i] = s[64999 - 600 * i]
+        s[list(outside)] = [-2, 65536][:len(outside)]
+        first = min(list(outside) + ([1001] if pairs else []))
+        text = "outside" if first in outside else "twice"
+        for _ in range(20):
+            with pytest.raises(W.QwhaError, match=rf"{text}.*\(at {first}\)"):
+                W.validate_slots(c, to_dev(s))
+    W.validate_slots(c, to_dev(g.permutation(65536).astype(np.int64)))

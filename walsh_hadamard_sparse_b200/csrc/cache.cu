@@ -754,16 +754,27 @@ __global__ void __launch_bounds__(kCacheThreads)
   }
 }
 
-// Each slot of `slots` sets its bit; a bit that was set already is a duplicate.
+// Each slot of `slots` sets its bit in `seen`; one that was set already is named
+// twice and sets it in `twice`. Which of its rows came second differs from run
+// to run, so the rows are looked up once both are complete: the first that is
+// outside or named twice is the same one every time.
+__global__ void __launch_bounds__(256) mark_slots_kernel(const int64_t *__restrict__ slots, int64_t n,
+                                                         int64_t n_slots, uint32_t *seen, uint32_t *twice) {
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t s = slots[i];
+    if (s < 0 || s >= n_slots) continue;
+    const uint32_t bit = 1u << (s & 31);
+    if (atomicOr(seen + (s >> 5), bit) & bit) atomicOr(twice + (s >> 5), bit);
+  }
+}
 __global__ void __launch_bounds__(256) check_slots_kernel(const int64_t *__restrict__ slots, int64_t n,
-                                                          int64_t n_slots, uint32_t *seen,
+                                                          int64_t n_slots, const uint32_t *twice,
                                                           unsigned long long *first_bad) {
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t s = slots[i];
     if (s == -1) continue;
     const bool out = s < -1 || s >= n_slots;
-    const bool twice = !out && (atomicOr(seen + (s >> 5), 1u << (s & 31)) >> (s & 31) & 1u);
-    if (out || twice) atomicMin(first_bad, (unsigned long long)i * 2 + (twice ? 1 : 0));
+    if (out || (twice[s >> 5] >> (s & 31) & 1u)) atomicMin(first_bad, (unsigned long long)i * 2 + (out ? 0 : 1));
   }
 }
 
@@ -878,18 +889,25 @@ cudaError_t launch_cache_read(qwha_dtype dt, const CachePair &c, int n_caches, c
   return cudaGetLastError();
 }
 
-size_t check_slots_bytes(int64_t n_slots) { return 256 + align_up((size_t)cdiv(n_slots, 32) * 4, 256); }
+namespace {
+size_t slot_bits_bytes(int64_t n_slots) { return align_up((size_t)cdiv(n_slots, 32) * 4, 256); }
+}  // namespace
+
+size_t check_slots_bytes(int64_t n_slots) { return 256 + 2 * slot_bits_bytes(n_slots); }
 
 cudaError_t launch_check_slots(const int64_t *slots, int64_t n, int64_t n_slots, void *ws, unsigned long long *bad,
                                cudaStream_t s) {
+  const size_t bits = slot_bits_bytes(n_slots);
   unsigned long long *word = static_cast<unsigned long long *>(ws);
-  uint32_t *seen = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + 256);
+  uint32_t *seen = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + 256), *twice = seen + bits / 4;
   cudaError_t e = cudaMemsetAsync(word, 0xff, sizeof(*word), s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(seen, 0, (size_t)cdiv(n_slots, 32) * 4, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(seen, 0, 2 * bits, s);
   if (e != cudaSuccess) return e;
   if (n > 0) {
     const unsigned grid = (unsigned)std::min<int64_t>(cdiv(n, 256), (int64_t)sm_count() * 8);
-    check_slots_kernel<<<grid, 256, 0, s>>>(slots, n, n_slots, seen, word);
+    mark_slots_kernel<<<grid, 256, 0, s>>>(slots, n, n_slots, seen, twice);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    check_slots_kernel<<<grid, 256, 0, s>>>(slots, n, n_slots, twice, word);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   e = cudaMemcpyAsync(bad, word, sizeof(*bad), cudaMemcpyDeviceToHost, s);
