@@ -172,3 +172,22 @@ def test_validate_slots_names_the_first_failure():
             with pytest.raises(W.QwhaError, match=rf"{text}.*\(at {first}\)"):
                 W.validate_slots(c, to_dev(s))
     W.validate_slots(c, to_dev(g.permutation(65536).astype(np.int64)))
+
+
+def test_what_the_kernels_met_is_reported_through_the_package():
+    import torch
+
+    W = _W()
+    c = W.cache_alloc(2, 4, 2, 64)
+    W.check_stream_status()
+    W.cache_write(c, torch.ones(3, 2, 64, device="cuda"), to_dev(np.array([1, 8, -1], np.int64)))
+    with pytest.raises(W.QwhaError, match="slot") as e:
+        W.check_stream_status()
+    assert e.value.status == 1
+    W.check_stream_status()  # the report is cleared
+    out = torch.full((8, 2, 64), 7.5, device="cuda")
+    W.cache_read(c, to_dev(np.array([[0, 2]], np.int32)), to_dev(np.array([0, 8], np.int64)), 8, out=out)
+    with pytest.raises(W.QwhaError, match="page"):
+        W.check_stream_status()
+    assert torch.allclose(out[1], torch.ones(2, 64, device="cuda"), rtol=1e-6) and torch.all(out[4:] == 7.5)
+    W.check_stream_status()

@@ -18,6 +18,7 @@ from .api import (  # noqa: F401
     cache_read,
     cache_write,
     calib_hessian,
+    check_stream_status,
     dp_backward,
     dp_step,
     energy_stats,

@@ -305,7 +305,7 @@ def _caches(caches) -> tuple:
 def cache_write(caches, rows, slots: torch.Tensor) -> None:
     """Quantize rows [n, heads, head_dim] (fp32 or bf16) into the slots [n] (int64, distinct; -1 skips a row) of a
     cache; with a pair of caches and a pair of rows (keys and values) both in one call (one launch where they are alike
-    in bits and group)."""
+    in bits and group). Rows with a slot outside the cache are skipped, which check_stream_status reports."""
     cs, dev, m = _caches(caches), torch.cuda.current_device(), slots.shape[0]
     rs = (rows,) if isinstance(rows, torch.Tensor) else tuple(rows)
     k = len(cs)
@@ -323,7 +323,8 @@ def cache_read(caches, pages: torch.Tensor, row_start: torch.Tensor, n: int, fir
     """Sequences of a cache as dense rows [n, heads, head_dim] (a pair of caches: a pair of tensors, in one call).
     Rows row_start[b] .. row_start[b+1] (int64 [n_seqs+1]) are the tokens first[b], first[b]+1, ... (int64 [n_seqs];
     None: 0) of sequence b, whose token t lies in page pages[b, t // page_size] (int32 [n_seqs, max_pages]). Rows from
-    row_start[-1] on are left as they were (they are not initialised without `out`)."""
+    row_start[-1] on, and rows whose page or token the table does not have, are left as they were (without `out` they
+    are not initialised); check_stream_status reports the latter."""
     cs, dev = _caches(caches), torch.cuda.current_device()
     n_seqs, max_pages = pages.shape
     k = len(cs)
@@ -351,6 +352,13 @@ def validate_slots(cache: QCache, slots: torch.Tensor, ws: torch.Tensor | None =
     ws = _ws(workspace_size(OP_SLOTS, 1, 1, cache.n_slots, 0, False), slots.device) if ws is None else ws
     check(lib().qwha_validate_slots(cs, p, slots.shape[0], *_fit_ws(ws, dev), _raw_stream(dev)),
           "qwha_validate_slots")
+
+
+def check_stream_status() -> None:
+    """Synchronise the current stream and raise QwhaError for what its kernels met on the way: a slot or a page outside
+    its cache (status 1; those rows were skipped), a wait that gave up (status 6), a CUDA error. Clears the report,
+    which is kept per device."""
+    check(lib().qwha_check_stream_status(_stream()), "qwha_check_stream_status")
 
 
 def dp_backward(a: Adapter, dY: torch.Tensor, Z: torch.Tensor, alpha: float = 1.0, wq: QWeight | None = None,
