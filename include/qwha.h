@@ -209,7 +209,7 @@ qwha_status qwha_adapter_bwd(const qwha_adapter *a, const qwha_qweight *wq, qwha
  * sums leave fp32's range (values near the type's largest, an infinity, a NaN)
  * is formed again in fp64, a row at a time: right, and slow.
  * d_out >= 1; d_in a multiple of wq->group (a multiple of 8). Deterministic.
- * QWHA_ERR_UNSUPPORTED above QWHA_DECODE_MAX_T. ws:
+ * X and Y must not overlap. QWHA_ERR_UNSUPPORTED above QWHA_DECODE_MAX_T. ws:
  * qwha_workspace_size(QWHA_OP_QGEMV, d_out, d_in, 0, T, with_base) bytes,
  * with_base 1 for bf16 and 2 for fp32 (the tokens as operands of the tensor
  * cores). */
@@ -225,7 +225,8 @@ qwha_status qwha_qgemv(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha
  * Z for qwha_adapter_bwd, which is the backward of these tokens too. ws:
  * qwha_workspace_size(QWHA_OP_DECODE, d_out, d_in, p, T, with_base) bytes,
  * with_base 0 without wq, else as for qwha_qgemv (its operands, and when p > 0
- * Z and the entries' sums in fp32). Columns of E outside [0, d_in) are skipped. Deterministic. */
+ * Z and the entries' sums in fp32). Columns of E outside [0, d_in) are skipped.
+ * X, Y and Z_out must not overlap. Deterministic. */
 qwha_status qwha_adapter_decode(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtype dt, const void *X,
                                 int64_t T, float alpha, void *Z_out, void *Y, void *ws, size_t ws_bytes,
                                 void *stream);

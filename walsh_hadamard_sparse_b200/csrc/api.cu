@@ -865,6 +865,13 @@ qwha_status check_tokens(int64_t T) {
   return QWHA_OK;
 }
 
+// A product's CTAs store their outputs while others still read the tokens.
+qwha_status check_apart(const char *names, const void *p, size_t p_bytes, const void *q, size_t q_bytes) {
+  const char *a = static_cast<const char *>(p), *b = static_cast<const char *>(q);
+  if (a < b + q_bytes && b < a + p_bytes) return fail(QWHA_ERR_INVALID_ARG, "%s overlap", names);
+  return QWHA_OK;
+}
+
 // The launches of a checked qwha_qgemv (a NULL) or qwha_adapter_decode call.
 qwha_status decode_call(const qwha_adapter *a, const qwha_qweight *wq, qwha_dtype dt, const void *X, int64_t T,
                         int32_t d_out, int32_t d_in, float alpha, void *Z_out, void *Y, void *ws, cudaStream_t s) {
@@ -961,6 +968,8 @@ qwha_status qwha_qgemv(const qwha_qweight *wq, int32_t d_out, int32_t d_in, qwha
   QWHA_CHECK_PTR(X, "X");
   QWHA_CHECK_PTR(Y, "Y");
   if ((st = check_ws(ws, ws_bytes, qgemv_ws(d_in, T, dt == QWHA_F32))) != QWHA_OK) return st;
+  const size_t row = (size_t)T * (dt == QWHA_F32 ? 4 : 2);
+  if ((st = check_apart("X and Y", X, row * d_in, Y, row * d_out)) != QWHA_OK) return st;
   return decode_call(nullptr, wq, dt, X, T, d_out, d_in, 0.f, nullptr, Y, ws, (cudaStream_t)stream);
 }
 
@@ -979,6 +988,11 @@ qwha_status qwha_adapter_decode(const qwha_adapter *a, const qwha_qweight *wq, q
   QWHA_CHECK_PTR(Y, "Y");
   if (Z_out) QWHA_CHECK_PTR(Z_out, "Z_out");
   if ((st = check_ws(ws, ws_bytes, decode_ws(a->d_out, a->d_in, a->p, T, wq != nullptr, dt == QWHA_F32))) != QWHA_OK) return st;
+  const size_t row = (size_t)T * (dt == QWHA_F32 ? 4 : 2), x_bytes = row * a->d_in, y_bytes = row * a->d_out;
+  if ((st = check_apart("X and Y", X, x_bytes, Y, y_bytes)) != QWHA_OK) return st;
+  if (Z_out && ((st = check_apart("X and Z_out", X, x_bytes, Z_out, x_bytes)) != QWHA_OK ||
+                (st = check_apart("Y and Z_out", Y, y_bytes, Z_out, x_bytes)) != QWHA_OK))
+    return st;
   return decode_call(a, wq, dt, X, T, a->d_out, a->d_in, alpha, Z_out, Y, ws, (cudaStream_t)stream);
 }
 
