@@ -191,3 +191,20 @@ def test_what_the_kernels_met_is_reported_through_the_package():
         W.check_stream_status()
     assert torch.allclose(out[1], torch.ones(2, 64, device="cuda"), rtol=1e-6) and torch.all(out[4:] == 7.5)
     W.check_stream_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d_in,n,T", [(40960, 8192, 3), (51200, 2048, 2), (65536, 32768, 1), (65536, 32768, 3)])
+def test_adapter_decode_wide_inputs(d_in, n, T, dtype):
+    """Inputs whose Z of one token fills shared memory (no room for a second one, then none for entries) or does not fit
+    there; the largest Hadamard block."""
+    W = _W()
+    g = rng_for(127, "wide", d_in, T)
+    d_out = 24
+    counts = g.integers(0, 300, d_out)
+    counts[0], counts[1], counts[2], counts[-1] = 0, 3000, 700, 1
+    rp, ci, cf, q, packed, s, z, x = _decode_case(g, d_in, d_out, n, 4, 128, counts, T, dtype)
+    a = W.Adapter(d_in, d_out, n, ci.size, to_dev(rp), to_dev(ci), to_dev(cf))
+    Y = W.adapter_decode(a, _dev(x, dtype), 0.75, _qweight(W, 4, 128, packed, s, z))
+    _check_decode(Y, x, dense_weight(q, s, z, 128), rp, ci, cf, n, 0.75, dtype)
+    _check_decode(W.adapter_decode(a, _dev(x, dtype), -1.5), x, None, rp, ci, cf, n, -1.5, dtype)
