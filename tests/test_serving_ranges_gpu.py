@@ -208,3 +208,27 @@ def test_adapter_decode_wide_inputs(d_in, n, T, dtype):
     Y = W.adapter_decode(a, _dev(x, dtype), 0.75, _qweight(W, 4, 128, packed, s, z))
     _check_decode(Y, x, dense_weight(q, s, z, 128), rp, ci, cf, n, 0.75, dtype)
     _check_decode(W.adapter_decode(a, _dev(x, dtype), -1.5), x, None, rp, ci, cf, n, -1.5, dtype)
+
+
+def test_stage_report_counts_the_launches_of_a_pair():
+    """Caches that need different kernels take a launch each."""
+    import torch
+
+    W = _W()
+    wide = [W.cache_alloc(2, 4, 2, 64, 4, 64, 64) for _ in range(2)]
+    odd = [W.cache_alloc(2, 4, 2, 24, 4, 8, 8) for _ in range(2)]
+    slots = to_dev(np.arange(5, dtype=np.int64))
+    where = (to_dev(np.array([[0, 1]], np.int32)), to_dev(np.array([0, 5], np.int64)), 5)
+    rows = lambda pair: [torch.ones(5, 2, c.head_dim, device="cuda", dtype=torch.bfloat16) for c in pair]  # noqa: E731
+    W.stage_timing(True)
+    try:
+        W.stage_report()
+        for pair, launches in ((wide[0], odd[0]), 2), ((odd[0], wide[0]), 2), (wide, 1), (odd, 1):
+            W.cache_write(pair, rows(pair), slots)
+            W.cache_read(pair, *where)
+            rep = W.stage_report()
+            assert rep["cache_write"][:2] == (1, launches) and rep["cache_read"][:2] == (1, launches)
+        W.cache_write((wide[0], odd[0]), [r.float() for r in rows((wide[0], odd[0]))], slots)  # one kernel for fp32 rows
+        assert W.stage_report()["cache_write"][:2] == (1, 1)
+    finally:
+        W.stage_timing(False)

@@ -1002,10 +1002,9 @@ qwha_status qwha_cache_write(const qwha_cache *caches, int32_t n_caches, qwha_dt
   if (st != QWHA_OK) return st;
   if (n == 0) return QWHA_OK;
   QWHA_CHECK_PTR(slots, "slots");
-  StageScope sc(ST_CACHE_WRITE, 1, (cudaStream_t)stream);
-  return cuda_status(launch_cache_write(dt, cache_pair(caches, n_caches, rows), n_caches, slots, n,
-                                        (cudaStream_t)stream),
-                     "cache_write");
+  const CachePair c = cache_pair(caches, n_caches, rows);
+  StageScope sc(ST_CACHE_WRITE, cache_write_launches(dt, c, n_caches), (cudaStream_t)stream);
+  return cuda_status(launch_cache_write(dt, c, n_caches, slots, n, (cudaStream_t)stream), "cache_write");
 }
 
 qwha_status qwha_cache_read(const qwha_cache *caches, int32_t n_caches, qwha_dtype dt, const int32_t *pages,
@@ -1018,10 +1017,10 @@ qwha_status qwha_cache_read(const qwha_cache *caches, int32_t n_caches, qwha_dty
   if (max_pages > 0) QWHA_CHECK_PTR(pages, "pages");
   QWHA_CHECK_PTR(row_start, "row_start");
   if (first) QWHA_CHECK_PTR(first, "first");
-  StageScope sc(ST_CACHE_READ, 1, (cudaStream_t)stream);
+  const CachePair c = cache_pair(caches, n_caches, rows);
+  StageScope sc(ST_CACHE_READ, cache_read_launches(c, n_caches), (cudaStream_t)stream);
   const ReadArgs r = {pages, max_pages, n_seqs, row_start, first};
-  return cuda_status(launch_cache_read(dt, cache_pair(caches, n_caches, rows), n_caches, r, n, (cudaStream_t)stream),
-                     "cache_read");
+  return cuda_status(launch_cache_read(dt, c, n_caches, r, n, (cudaStream_t)stream), "cache_read");
 }
 
 qwha_status qwha_validate_slots(const qwha_cache *cache, const int64_t *slots, int64_t n, void *ws, size_t ws_bytes,

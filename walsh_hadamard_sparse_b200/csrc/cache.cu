@@ -843,9 +843,17 @@ void read_mma(const CachePair &c, dim3 grid, int tile, const ReadArgs &r, int64_
 
 int cache_max_head_dim() { return 256; }
 
+int cache_write_launches(qwha_dtype dt, const CachePair &c, int n_caches) {
+  const bool apart = n_caches == 2 && !writes_units(dt, c, 2) && (writes_units(dt, c, 1) || writes_units(dt, second(c), 1));
+  return apart ? 2 : 1;
+}
+int cache_read_launches(const CachePair &c, int n_caches) {
+  return n_caches == 2 && !takes_units(c, 2) && (takes_units(c, 1) || takes_units(second(c), 1)) ? 2 : 1;
+}
+
 cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, const int64_t *slots, int64_t n,
                                cudaStream_t s) {
-  if (n_caches == 2 && !writes_units(dt, c, 2) && (writes_units(dt, c, 1) || writes_units(dt, second(c), 1))) {
+  if (cache_write_launches(dt, c, n_caches) == 2) {
     const cudaError_t e = launch_cache_write(dt, c, 1, slots, n, s);
     return e != cudaSuccess ? e : launch_cache_write(dt, second(c), 1, slots, n, s);
   }
@@ -870,7 +878,7 @@ cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, 
 
 cudaError_t launch_cache_read(qwha_dtype dt, const CachePair &c, int n_caches, const ReadArgs &r, int64_t n,
                               cudaStream_t s) {
-  if (n_caches == 2 && !takes_units(c, 2) && (takes_units(c, 1) || takes_units(second(c), 1))) {
+  if (cache_read_launches(c, n_caches) == 2) {
     const cudaError_t e = launch_cache_read(dt, c, 1, r, n, s);
     return e != cudaSuccess ? e : launch_cache_read(dt, second(c), 1, r, n, s);
   }

@@ -209,6 +209,9 @@ struct CachePair {
 // Bits of the device error word.
 constexpr unsigned int kErrSlot = 0x1000u, kErrPage = 0x2000u;
 int cache_max_head_dim();
+// Launches of a call: a pair whose caches need different kernels takes two.
+int cache_write_launches(qwha_dtype dt, const CachePair &c, int n_caches);
+int cache_read_launches(const CachePair &c, int n_caches);
 cudaError_t launch_cache_write(qwha_dtype dt, const CachePair &c, int n_caches, const int64_t *slots, int64_t n,
                                cudaStream_t s);
 // Where the rows of a read come from (qwha_cache_read).
