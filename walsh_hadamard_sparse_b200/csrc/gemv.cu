@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const __grid_con
     for (int r = lane; r < a.d_in / 8; r += 32) {
       const int64_t g = row * (a.d_in / a.group) + r * 8 / a.group;
       sum = fma((double)a.scales[g],
-                gemv::run_dot(run_word(a.qw + (row * (a.d_in / 8) + r) * a.bits, a.bits), a.bits, a.zeros[g], x + r * 8), sum);
+                gemv::run_dot<1>(run_word(a.qw + (row * (a.d_in / 8) + r) * a.bits, a.bits), a.bits, a.zeros[g], x + r * 8), sum);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);

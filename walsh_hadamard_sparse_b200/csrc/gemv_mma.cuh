@@ -154,13 +154,19 @@ __device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t
 
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.402823466e38f; }
 
-// sum of (q - z) x over a run of eight codes, in fp64.
 template <typename T>
+__device__ __forceinline__ void load8(const T *p, float *v) {
+#pragma unroll
+  for (int u = 0; u < 8; u += io<T>::kVec) io<T>::unpack(*reinterpret_cast<const uint4 *>(p + u), v + u);
+}
+
+// sum of (q - z) x over a run of eight codes, in fp64, U of them unrolled.
+template <int U, typename T>
 __device__ __forceinline__ double run_dot(uint32_t w, int bits, int z, const T *x) {
   double sum = 0.;
-#pragma unroll 1
+#pragma unroll U
   for (int i = 0; i < 8; ++i, w >>= bits)
-    sum = fma((double)((int)(w & ((1u << bits) - 1u)) - z), (double)io<T>::load1(x + i), sum);
+    sum = fma((double)((float)(w & ((1u << bits) - 1u)) - (float)z), (double)io<T>::load1(x + i), sum);
   return sum;
 }
 
@@ -176,20 +182,12 @@ static __device__ __noinline__ float plain_dot(const GemvArgs &a, int row, int t
     uint32_t w = 0;
     for (int b = 0; b < a.bits; ++b) w |= (uint32_t)qw[(int64_t)r * a.bits + b] << (8 * b);
     const int64_t g = (int64_t)row * ng + r * 8 / a.group, at = (int64_t)tok * a.d_in + r * 8;
-    const double part = a.f32 ? run_dot(w, a.bits, a.zeros[g], static_cast<const float *>(a.x) + at)
-                              : run_dot(w, a.bits, a.zeros[g], static_cast<const __nv_bfloat16 *>(a.x) + at);
+    const double part = a.f32 ? run_dot<8>(w, a.bits, a.zeros[g], static_cast<const float *>(a.x) + at)
+                              : run_dot<8>(w, a.bits, a.zeros[g], static_cast<const __nv_bfloat16 *>(a.x) + at);
     sum = fma((double)a.scales[g], part, sum);
   }
   return (float)sum;
 }
-
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, float *v) {
-#pragma unroll
-  for (int u = 0; u < 8; u += io<T>::kVec) io<T>::unpack(*reinterpret_cast<const uint4 *>(p + u), v + u);
-}
-
-__host__ __device__ constexpr int even(int n) { return (n + 1) & ~1; }
 
 // Four consecutive values.
 __device__ __forceinline__ void load4(const float *p, float *v) { io<float>::unpack(*reinterpret_cast<const uint4 *>(p), v); }
