@@ -101,12 +101,14 @@ __global__ void __launch_bounds__(kRowThreads) gemv_rows_kernel(const __grid_con
 }
 
 constexpr int kPrepThreads = 256;
-// Columns above which tcgen05 takes the product. It costs 26 to 36 us for the layers below whatever the columns, unpacking
-// into shared memory; the other grows with them (bf16 tokens, us, mma.sync / tcgen05):
-//   14336 x 4096, 4 bits     16: 27 / 27   24: 33 / 27   32: 39 / 27   64: 67 / 30
-//   4096 x 14336, 2 bits     16: 33 / 32   24: 40 / 32   32: 45 / 34   64: 86 / 44
-//   4096 x 14336, 3 bits     16: 25 / 34   24: 29 / 35   32: 34 / 36   64: 47 / 43
-//   1024 x 4096, 4 bits      16: 19 / 16   24: 20 / 16   32: 19 / 18   64: 19 / 23
+// Columns above which tcgen05 takes the product: one border, a compromise. Both sides grow with the columns, the
+// unpacking into shared memory less than the other (bf16 tokens, groups of 128, us, mma.sync / tcgen05):
+//   14336 x 4096, 4 bits     16: 23 / 24   20: 29 / 24   24: 31 / 24   32: 38 / 25   64: 64 / 28
+//   4096 x 14336, 2 bits     16: 19 / 25   20: 25 / 27   24: 25 / 27   32: 31 / 29   64: 47 / 36
+//   4096 x 14336, 3 bits     16: 21 / 29   20: 27 / 31   24: 26 / 32   32: 32 / 34   64: 48 / 42
+//   1024 x 4096, 4 bits      16: 7.5 / 11  20: 9.7 / 12  24: 10 / 12   32: 11 / 14   64: 18 / 18
+// At 20 columns it leaves 5 us of 29 in the first row; above it costs up to 6 of 26 where codes have three bits or
+// rows are few: a border by width and rows would serve these better.
 constexpr int kWideAbove = 20;
 
 // Shared-memory place of element i of a span: four floats of padding every
@@ -138,15 +140,15 @@ __device__ __forceinline__ void span_pass(float *row, int d, int s) {
   __syncthreads();
 }
 
+// Token slots of a pass of the product for many columns: they cover the padding too.
+__host__ __device__ inline int wide_slots(const GemvArgs &a) { return (a.npad + a.pieces - 1) / a.pieces; }
+
 // What a product needs of its tokens beforehand: the operands (CTAs from
 // `spans` on), and Z = X H, one CTA per token and span of whole Hadamard
 // blocks: zt in fp32 with the tg tokens of a group side by side, so that an
 // entry of E finds its column of all of them in one place, and z_out [T, d_in]
 // in X's type for the backward, on request. Latency bounds it:
 // four stages a pass, so 4096 columns take three turns through shared memory.
-// Token slots of a pass of the product for many columns: they cover the padding too.
-__host__ __device__ inline int wide_slots(const GemvArgs &a) { return (a.npad + a.pieces - 1) / a.pieces; }
-
 template <int BITS, typename T>
 __global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const GemvArgs a, int logn, int span, int spans,
                                                                       float scale, T *z_out) {
@@ -243,12 +245,13 @@ __device__ __forceinline__ void row_sum(const int32_t *cols, const float *coefs,
 // The entries of E against the transformed tokens: y_ad[i][t] = sum_{j in row i}
 // c_j Z[t][k_j], fp32. Gathering Z from L2 costs a sector an entry and waits
 // for each, so a group of TG tokens is brought into shared memory and an entry
-// a lane gathers there (down layer, five fp32 tokens: three turns of two tokens
-// 51 us, eight from L2 62 us); only layers whose single token does not fit
-// gather from L2. The entries are copied to shared memory beside it, before the
-// preparing launch is complete. 512 threads of 64 registers leave a CTA of the
-// product room on the SM (gate layer, sixteen tokens: 49 us instead of 54 with
-// 1024 threads and the product behind).
+// a lane gathers there (down layer, five fp32 tokens, the whole call: three
+// turns of two tokens 50 us, eight from L2 11 more); only layers whose single
+// token does not fit gather from L2. The entries are copied to shared memory
+// beside it, before the preparing launch is complete. 512 threads of 64
+// registers leave a CTA of the product room on the SM (gate layer, sixteen
+// tokens, the whole call: 48 us; with 1024 threads and the product behind 5
+// more).
 //
 // Rows differ in length by orders of magnitude (the budget follows the row's
 // quantization error): a CTA takes whole rows that hold its even share of the
@@ -457,10 +460,10 @@ size_t xpieces_bytes(int32_t d_in, int64_t T, bool f32) {
 }
 }  // namespace
 
-// A bf16 token or two by themselves: the product's CTAs make the operands, which saves the call a launch and a workspace
-// (1 of 18 us on the host; the GPU takes 5.8 us instead of 6.0 for 1024 x 4096, 16.6 instead of 15.8 for 14336 x 4096,
-// where more CTAs repeat the work). The size bounds that work to 1 us. One n-tile has to hold the columns; with two at
-// most it does for every group, which workspace sizes do not know.
+// A bf16 token or two by themselves: the product's CTAs make the operands, which saves the call a launch and a workspace.
+// That is 4 of 17 us of an eager call of 1024 x 4096. On the GPU one token takes 5.0 us instead of 5.3 (14336 x 4096: 15.5
+// instead of 15.7), two take 6.3 instead of 5.1 (17.7 instead of 15.7): every CTA repeats the work. The size bounds that
+// work. One n-tile has to hold the columns; with two at most it does for every group, which workspace sizes do not know.
 bool gemv_own_x(int32_t d_in, int64_t T, bool f32) {
   return T * pieces_of(f32) <= 2 && T * pieces_of(f32) * d_in <= 16384;
 }

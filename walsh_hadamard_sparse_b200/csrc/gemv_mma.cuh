@@ -34,9 +34,11 @@
 // or with OWN from shared memory. No barrier until the slices are added.
 //
 // 14336 x 4096, 3 bits, one token: 15.5 us; 4096 x 14336, 4 bits, eight tokens:
-// 13.2 us (37% of the copy rate). Tried and slower: codes through rings of
-// shared memory filled by bulk copies (18 to 30 us), fp8 operands (converted on
-// the integer pipe, 26 us), values staged in shared memory (18 and 35 us).
+// 13.2 us (37% of the copy rate). Tried and slower, when these took 18 and 15:
+// codes through rings of shared memory filled by bulk copies (18 to 30 us), fp8
+// operands (converted on the integer pipe, 26 us), values staged in shared
+// memory (18 and 35 us). The arguments are __grid_constant__: a copy of them in
+// every thread, for the function that takes them by reference, cost 1 to 2 us.
 
 #pragma once
 
@@ -568,7 +570,7 @@ cudaError_t launch_one(const GemvArgs &a, cudaStream_t s) {
   if (tpp < a.T) tpp &= ~(TPN - 1);  // a further pass starts with an n-tile
   else tpp = a.T;
   // slices of the columns: as many as it takes to give every SM twelve warps, two chunks a warp at least (a target of
-  // 24 or 48 warps: 20 and 21 us instead of 17 for 14336 x 4096, 3 bits)
+  // 24 or 48 warps took 3 and 4 us more for 14336 x 4096, 3 bits)
   const int64_t tiles = cdiv(a.d_out, ROWS), chunks = cdiv(a.d_in, 128);
   int slices = 1;
   while (slices < kWarps && tiles * slices < (int64_t)sm_count() * 12 && chunks >= 2 * slices) slices *= 2;

@@ -22,7 +22,7 @@
 //   1 warp    issues the products.
 // The order of the columns inside a run is the one the codes' masks yield, in
 // both operands. Unpacking sets the pace: 14336 x 4096, 4 bits, 64 bf16 tokens
-// take 30 us on 112 SMs, 0.75 us for a CTA's chunk of 128 x 128 codes, of which
+// take 27.6 us on 112 SMs, 0.7 us for a CTA's chunk of 128 x 128 codes, of which
 // the products need 0.5; the bytes alone 5 us. Every wait is bounded; a thread that gives up sets the error
 // word and leaves its loop, and TMEM is freed after the products issued so far.
 
@@ -36,9 +36,10 @@ namespace wide {
 constexpr int kRows = 128, kScaleWarps = 8, kAhead = 1, kMaxSlots = 8;
 // With NB blocks of 16 columns to a scaling warp: the stages that fit, and the
 // teams that the registers of the sums leave room for (64 bf16 tokens of
-// 14336 x 4096: two teams 36 us, three 30; 32 tokens: three 27, four with five
-// stages 29). A second chunk in flight to a team needs its loop unrolled once
-// more: 39 instead of 36 us, for the instructions' own fetches.
+// 14336 x 4096, when three teams took 30 us: two 36; 32 tokens: three 27, four
+// with five stages 29). A second chunk in flight to a team needs its loop
+// unrolled once more: 39 instead of 36 us with two teams, for the instructions'
+// own fetches.
 template <int NB>
 constexpr int stages() { return NB <= 2 ? 4 : 3; }
 template <int NB>
