@@ -146,9 +146,9 @@ __host__ __device__ inline int wide_slots(const GemvArgs &a) { return (a.npad + 
 // What a product needs of its tokens beforehand: the operands (CTAs from
 // `spans` on), and Z = X H, one CTA per token and span of whole Hadamard
 // blocks: zt in fp32 with the tg tokens of a group side by side, so that an
-// entry of E finds its column of all of them in one place, and z_out [T, d_in]
-// in X's type for the backward, on request. Latency bounds it:
-// four stages a pass, so 4096 columns take three turns through shared memory.
+// entry of E finds its column of all of them in one place, and columns of zeros
+// behind; z_out [T, d_in] in X's type for the backward, on request. Latency
+// bounds it: four stages a pass, so 4096 columns take three turns through shared memory.
 template <int BITS, typename T>
 __global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const GemvArgs a, int logn, int span, int spans,
                                                                       float scale, T *z_out) {
@@ -182,9 +182,11 @@ __global__ void __launch_bounds__(kPrepThreads) decode_prepare_kernel(const Gemv
   }
   for (int k = threadIdx.x; k < d; k += kPrepThreads) {
     const float v = row[span_at(k)] * scale;
-    if (a.zt) a.zt[((int64_t)(t / a.tg) * a.d_in + k0 + k) * a.tg + t % a.tg] = v;
+    if (a.zt) a.zt[((int64_t)(t / a.tg) * z_cols(a.d_in) + k0 + k) * a.tg + t % a.tg] = v;
     if (z_out) io<T>::store1(z_out + (int64_t)t * a.d_in + k0 + k, v);
   }
+  if (a.zt && k0 + d == a.d_in && threadIdx.x < z_cols(a.d_in) - a.d_in)
+    a.zt[((int64_t)(t / a.tg) * z_cols(a.d_in) + a.d_in + threadIdx.x) * a.tg + t % a.tg] = 0.f;
 }
 
 constexpr int kEntThreads = 512, kEntWarps = kEntThreads / 32;
@@ -215,25 +217,22 @@ __device__ __forceinline__ void row_sum(const int32_t *cols, const float *coefs,
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      // behind the last entry and outside the layer nothing is added: 0 * Z would be NaN for an infinite Z
-      const bool in = (unsigned)k[u] < (unsigned)d_in;
-      const float *z = zs + (int64_t)(in ? k[u] : 0) * TG;
-      float v[TG];
+      // behind the last entry and outside the layer: 0 times the column of zeros (0 * Z would be NaN for an infinite Z)
+      if ((unsigned)k[u] >= (unsigned)d_in) k[u] = d_in, c[u] = 0.f;
+      const float *z = zs + (int64_t)k[u] * TG;
       if constexpr (TG >= 4) {
 #pragma unroll
         for (int i = 0; i < TG; i += 4) {
-          const float4 w = *reinterpret_cast<const float4 *>(z + i);
-          v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
+          const float4 v = *reinterpret_cast<const float4 *>(z + i);
+          acc[i] = fmaf(c[u], v.x, acc[i]), acc[i + 1] = fmaf(c[u], v.y, acc[i + 1]);
+          acc[i + 2] = fmaf(c[u], v.z, acc[i + 2]), acc[i + 3] = fmaf(c[u], v.w, acc[i + 3]);
         }
       } else if constexpr (TG == 2) {
-        const float2 w = *reinterpret_cast<const float2 *>(z);
-        v[0] = w.x, v[1] = w.y;
+        const float2 v = *reinterpret_cast<const float2 *>(z);
+        acc[0] = fmaf(c[u], v.x, acc[0]), acc[1] = fmaf(c[u], v.y, acc[1]);
       } else {
-        v[0] = *z;
+        acc[0] = fmaf(c[u], *z, acc[0]);
       }
-#pragma unroll
-      for (int i = 0; i < TG; ++i)
-        if (in) acc[i] = fmaf(c[u], v[i], acc[i]);
     }
   }
 #pragma unroll
@@ -260,7 +259,7 @@ __device__ __forceinline__ void row_sum(const int32_t *cols, const float *coefs,
 template <int TG>
 __global__ void __launch_bounds__(kEntThreads, 2)
     decode_entries_kernel(const GemvArgs a, int buffers, int stage) {
-  extern __shared__ __align__(16) float zs_all[];  // [buffers][d_in][TG], columns [stage], coefficients [stage]
+  extern __shared__ __align__(16) float zs_all[];  // [buffers][z_cols][TG], columns [stage], coefficients [stage]
   __shared__ int rp_s[kEntRows + 1];
   __shared__ float part[kEntWarps][TG];
   __shared__ uint64_t s_bar[2];
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(kEntThreads, 2)
   const int e0 = border(r0) & ~3;
   int staged = border(r1) - e0;
   staged = staged < 0 ? 0 : staged < stage ? staged : stage;
-  int32_t *cols_s = reinterpret_cast<int32_t *>(zs_all + (size_t)buffers * a.d_in * TG);
+  int32_t *cols_s = reinterpret_cast<int32_t *>(zs_all + (size_t)buffers * z_cols(a.d_in) * TG);
   float *coefs_s = reinterpret_cast<float *>(cols_s + stage);
   for (int i = threadIdx.x * 4; i < staged; i += kEntThreads * 4) {
     const int64_t left = a.p - e0 - i;
@@ -316,18 +315,18 @@ __global__ void __launch_bounds__(kEntThreads, 2)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("cp.async.wait_all;" ::: "memory");
   // turn n: the tokens of group n; with two buffers the next turn's Z is on its way
-  const int turns = a.tp / TG;
-  const uint32_t bytes = a.d_in * TG * 4;
+  const int turns = a.tp / TG, group = z_cols(a.d_in) * TG;
+  const uint32_t bytes = group * 4;
   auto copy_z = [&](int n) {
     const uint32_t bar = bulk::saddr(s_bar + n % 2);
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
     bulk::fence_proxy();
-    bulk::copy(bulk::saddr(zs_all) + (buffers == 2 ? n % 2 * bytes : 0), a.zt + (int64_t)n * a.d_in * TG, bytes, bar);
+    bulk::copy(bulk::saddr(zs_all) + (buffers == 2 ? n % 2 * bytes : 0), a.zt + (int64_t)n * group, bytes, bar);
   };
   if (buffers && threadIdx.x == 0) copy_z(0);
   for (int n = 0; n < turns; ++n) {
     const int t0 = n * TG;
-    const float *zs = !buffers ? a.zt + (int64_t)n * a.d_in * TG : zs_all + (buffers == 2 ? n % 2 * (a.d_in * TG) : 0);
+    const float *zs = !buffers ? a.zt + (int64_t)n * group : zs_all + (buffers == 2 ? n % 2 * group : 0);
     __syncthreads();  // the last turn's gathers are done (and the rows' borders are there)
     if (buffers) {
       if (threadIdx.x == 0 && (buffers == 2 ? n + 1 < turns : n > 0)) copy_z(buffers == 2 ? n + 1 : n);
@@ -405,7 +404,7 @@ __global__ void __launch_bounds__(kEntThreads, 2)
 
 template <int TG>
 cudaError_t entries(const GemvArgs &a, cudaStream_t s) {
-  const size_t group_bytes = (size_t)a.d_in * TG * sizeof(float);
+  const size_t group_bytes = (size_t)z_cols(a.d_in) * TG * sizeof(float);
   const int buffers = 2 * group_bytes <= kEntSmem * 2 / 3 && a.tp > TG ? 2 : group_bytes <= kEntSmem ? 1 : 0;
   // a CTA an SM, with 256 entries at least
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(sm_count(), a.p / 256));
@@ -513,7 +512,7 @@ int group_tokens(int64_t T, int32_t d_in) {
 size_t gemv_z_bytes(int32_t d_out, int32_t d_in, int64_t T) {
   if (T <= 0) return 0;
   const size_t tp = cdiv(T, group_tokens(T, d_in)) * group_tokens(T, d_in);
-  return align_up(tp * d_in * 4, 256) + align_up(tp * d_out * 4, 256) + 256;
+  return align_up(tp * z_cols(d_in) * 4, 256) + align_up(tp * d_out * 4, 256) + 256;
 }
 
 void gemv_place_z(GemvArgs *a, void *ws) {
@@ -521,7 +520,7 @@ void gemv_place_z(GemvArgs *a, void *ws) {
   a->tp = (a->T + a->tg - 1) / a->tg * a->tg;
   a->ready = static_cast<unsigned int *>(ws);
   a->zt = reinterpret_cast<float *>(static_cast<char *>(ws) + 256);
-  a->y_ad = a->zt + align_up((size_t)a->tp * a->d_in * 4, 256) / 4;
+  a->y_ad = a->zt + align_up((size_t)a->tp * z_cols(a->d_in) * 4, 256) / 4;
 }
 
 cudaError_t launch_decode_entries(const GemvArgs &a, cudaStream_t s) {

@@ -166,7 +166,7 @@ struct GemvArgs {
   const float *coef;
   int64_t p;
   float alpha;
-  // Z = X H in fp32 by groups of tg tokens: zt [tp / tg][d_in][tg]; the entries' sums y_ad [d_out][tp].
+  // Z = X H in fp32 by groups of tg tokens: zt [tp / tg][z_cols(d_in)][tg]; the entries' sums y_ad [d_out][tp].
   float *zt, *y_ad;
   int tg, tp;
   unsigned int *ready;  // 1 once the preparing launch is complete (beside zt)
@@ -182,6 +182,8 @@ struct GemvArgs {
   float *fac;
   int prepared;  // another launch of the call precedes the product
 };
+// Columns of zt: those of the layer, and zeros for entries that count nothing (four keep copies to whole 16 bytes).
+__host__ __device__ constexpr int z_cols(int d_in) { return d_in + 4; }
 __host__ __device__ constexpr int x_tiles(int cols, int G) { return (cols * G + 7) / 8; }
 bool gemv_on_tensor_cores(const uint8_t *qw, int group);
 bool gemv_own_x(int32_t d_in, int64_t T, bool f32);  // whether a product by itself needs no prepared values
