@@ -147,7 +147,11 @@ typedef enum {
   QWHA_OP_PATTERN = 9,       /* qwha_pattern_stats */
   QWHA_OP_DECODE = 10,       /* qwha_adapter_decode; with_base: 0 without a base weight, else as below */
   QWHA_OP_SLOTS = 11,        /* qwha_validate_slots; p = slots of the cache, other sizes 1 */
-  QWHA_OP_QGEMV = 12         /* qwha_qgemv; with_base: 1 for bf16 tokens, 2 for fp32 */
+  QWHA_OP_QGEMV = 12,        /* qwha_qgemv; with_base: 1 for bf16 tokens, 2 for fp32 */
+  QWHA_OP_ATTENTION = 13,    /* qwha_cache_attention; d_out = q_heads, d_in = head_dim, p = heads of the cache,
+                                T = n, with_base: 1 for bf16, 2 for fp32 */
+  QWHA_OP_PAGES = 14         /* qwha_pages_resize, qwha_pages_fork; d_out = n_seqs, p = n_pages, T = pairs of a
+                                fork (0 for resize), d_in = 1 */
 } qwha_op;
 
 /* Z = X H row by row: x and z are [rows, n] of dtype dt (device), each row
@@ -291,6 +295,112 @@ qwha_status qwha_cache_read(const qwha_cache *caches, int32_t n_caches, qwha_dty
  * page_size, 0, 0) bytes. */
 qwha_status qwha_validate_slots(const qwha_cache *cache, const int64_t *slots, int64_t n, void *ws,
                                 size_t ws_bytes, void *stream);
+
+/* Rotary positions: channels of each head of x turn in pairs by the angle
+ * positions[i] * freq[c] of their token,
+ *   y[a] = factor (x[a] cos - x[b] sin),  y[b] = factor (x[b] cos + x[a] sin),
+ * with (a, b) = (c, c + rot/2) for layout QWHA_ROTARY_HALF, (2c, 2c + 1) for
+ * QWHA_ROTARY_PAIRS, c < rot/2; channels from rot on are copied. inverse turns
+ * back (the transpose with the same factor: the gradient of x from that of y).
+ * n_x is 1 or 2 (queries and keys in one launch): x[i] and y[i] (host arrays of
+ * device pointers) hold n tokens of heads[i] * head_dim values, x_stride[i] and
+ * y_stride[i] elements from token to token (multiples of 16 bytes, at least
+ * heads[i] * head_dim), so slices of a fused projection are taken as they lie.
+ * y[i] may be x[i] with its stride (in place); other overlaps are refused.
+ * positions int64 [n], freq fp64 [rot/2], both device; angles are formed in
+ * fp64 and reduced to a part of a turn before sine and cosine are taken in
+ * fp32, so far positions lose nothing. rot even, 0 <= rot <= head_dim;
+ * head_dim a multiple of 8; one rounding to dt. */
+typedef enum { QWHA_ROTARY_HALF = 0, QWHA_ROTARY_PAIRS = 1 } qwha_rotary_layout;
+qwha_status qwha_rotary(qwha_dtype dt, int32_t n_x, const void *const *x, const int64_t *x_stride, void *const *y,
+                        const int64_t *y_stride, const int32_t *heads, int32_t head_dim, int64_t n,
+                        const int64_t *positions, const double *freq, int32_t rot, qwha_rotary_layout layout,
+                        float factor, int32_t inverse, void *stream);
+
+/* Attention of the queries of n_seqs sequences over their cached tokens, read
+ * from the codes: q [n, q_heads, head_dim] (dt; q_stride elements from token to
+ * token, a multiple of 16 bytes), rows q_start[b] <= i < q_start[b + 1] are the
+ * newest tokens of sequence b (device int64 [n_seqs + 1], non-decreasing from
+ * 0), whose keys and values are in the cache already, behind past[b] (device
+ * int64 [n_seqs]) earlier ones: token t of sequence b lies in page
+ * pages[b * max_pages + t / page_size]. Row i sees every t < past[b], and of
+ * the sequence's new tokens u (t = past[b] + u)
+ *   tree == NULL: those up to itself, u <= i - q_start[b];
+ *   tree int64 [n]: u < 64 where bit u of tree[i] is set (drafted trees: itself
+ *   and its ancestors).
+ * For query head h, cached head h / (q_heads / heads):
+ *   s_t = scale q . k_t,  out = sum_t softmax(s)_t v_t,  lse = log sum_t exp(s_t).
+ * A row that sees nothing gets out = 0 and lse = -inf. lse fp32 [n, q_heads] or
+ * NULL; out [n, q_heads, head_dim] of type dt. Rows from q_start[n_seqs] on are
+ * left as they were. k and v have the same heads, head_dim, page_size and
+ * n_pages; bits, group and had_block may differ. Tokens whose page is outside
+ * [0, n_pages) or the page table are not seen; qwha_check_stream_status reports
+ * them (QWHA_ERR_INVALID_ARG). What masked tokens hold has no effect (a group
+ * stored as NaN included).
+ * A rotated cache costs nothing per token: H is applied to the query and to the
+ * output. Scores, softmax and sums are fp32. out must not overlap q.
+ * Deterministic. ws: qwha_workspace_size(QWHA_OP_ATTENTION, q_heads, head_dim,
+ * heads, n, 1 for bf16 or 2 for fp32) bytes. */
+qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_dtype dt, const void *q, int64_t n,
+                                 int32_t q_heads, int64_t q_stride, const int32_t *pages, int32_t max_pages,
+                                 const int64_t *q_start, const int64_t *past, int32_t n_seqs, const int64_t *tree,
+                                 float scale, void *out, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Which pages of a cache (of all caches of a model: every layer's keys and
+ * values use the same page numbers) hold the tokens of which sequence. Device
+ * memory, owned by the caller and kept by the two calls below:
+ *   refs  int32 [n_pages]            rows of the table that name the page; 0: free
+ *   pages int32 [n_seqs, max_pages]  row b: the first ceil(held[b] / page_size)
+ *                                    entries are its pages, -1 behind them
+ *   held  int64 [n_seqs]             tokens of sequence b
+ * An empty table has refs = 0, pages = -1, held = 0. */
+typedef struct {
+  int32_t page_size, max_pages, n_seqs;
+  int32_t n_pages;
+  int32_t *refs, *pages;
+  int64_t *held;
+} qwha_page_table;
+
+/* Give every sequence b room for want[b] tokens (device int64 [n_seqs]; -1: as
+ * it is): pages past the end are given back first (a page nobody names any more
+ * is free), then sequences that grow take the lowest free pages, in the order of
+ * b. held[b] becomes want[b]; where the free pages end, the sequence that cannot
+ * be served and all that grow behind it stay as they were (held tells). want
+ * below -1 or above max_pages * page_size, and rows whose held or pages
+ * contradict the table, are left and reported by qwha_check_stream_status
+ * (QWHA_ERR_INVALID_ARG). ws: qwha_workspace_size(QWHA_OP_PAGES, n_seqs, 1,
+ * n_pages, 0, 0) bytes. Deterministic. */
+qwha_status qwha_pages_resize(const qwha_page_table *t, const int64_t *want, void *ws, size_t ws_bytes, void *stream);
+
+/* Row dst[i] becomes a copy of row src[i] as it was at the call's start, i < m
+ * (device int64 [m]; src[i] = -1: nothing): whole pages are shared, a last page
+ * that is only partly filled gets a fresh page (lowest free first, in the order
+ * of i), since both sequences will write to it: from[i] and to[i] (device int32
+ * [m]) name it and its copy for qwha_cache_copy_pages, -1 where there is none.
+ * dst[i] must be an empty row (held 0) and named once; a pair that breaks this
+ * or leaves the table is skipped and reported as above (of pairs with one dst
+ * the first counts). Where the free pages end, the pair and those behind it that
+ * need a page leave their dst empty. ws as above with T = m. Deterministic. */
+qwha_status qwha_pages_fork(const qwha_page_table *t, const int64_t *src, const int64_t *dst, int32_t m, int32_t *from,
+                            int32_t *to, void *ws, size_t ws_bytes, void *stream);
+
+/* Copy page from[i] to page to[i] of n_caches caches (1 or 2), i < m (device
+ * int32 [m]; -1 in either skips). The pages of `to` must be distinct and none of
+ * them in `from`. Pages outside the cache are skipped and reported by
+ * qwha_check_stream_status. */
+qwha_status qwha_cache_copy_pages(const qwha_cache *caches, int32_t n_caches, const int32_t *from, const int32_t *to,
+                                  int32_t m, void *stream);
+
+/* Move the tokens of each sequence that are kept together: token first[b] +
+ * keep[b][i] goes to first[b] + i, for i up to the first -1 of keep[b] (device
+ * int32 [n_seqs, width], strictly ascending; first device int64 [n_seqs]); pages
+ * as in qwha_cache_read. E.g. the accepted nodes of a drafted tree, or what stays
+ * of a long context. The pages written must not belong to another sequence of
+ * the call. Where keep stops ascending the rest of the row is left, and moves to
+ * or from a page outside the cache or its table are skipped; both are reported
+ * by qwha_check_stream_status. */
+qwha_status qwha_cache_compact(const qwha_cache *caches, int32_t n_caches, const int32_t *pages, int32_t max_pages,
+                               const int64_t *first, const int32_t *keep, int32_t width, int32_t n_seqs, void *stream);
 
 /* AdaAlloc initialisation from the quantization error dW_Q = W0 - W_Q
  * (papernotes.org 关键设计 2 and 3; gist.science 2.2). dWq fp32 [d_out, d_in]
@@ -479,7 +589,8 @@ size_t qwha_workspace_size(qwha_op op, int32_t d_out, int32_t d_in, int64_t p, i
 qwha_status qwha_validate_plan(const qwha_adapter *a, void *stream);
 
 /* Synchronise `stream` and report a device-side error word set by a bounded
- * wait (QWHA_ERR_TIMEOUT) or by a slot or page outside its cache
+ * wait (QWHA_ERR_TIMEOUT), by a slot or page outside its cache, or by rows of a
+ * page table or of a move that were refused on the device
  * (QWHA_ERR_INVALID_ARG), or a CUDA error (QWHA_ERR_CUDA); clears the word. */
 qwha_status qwha_check_stream_status(void *stream);
 

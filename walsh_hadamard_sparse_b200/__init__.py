@@ -9,12 +9,16 @@ from ._lib import QwhaError, lib  # noqa: F401
 from .api import (  # noqa: F401
     DECODE_MAX_T,
     Adapter,
+    PageTable,
     QCache,
     QWeight,
     adapter_bwd,
     adapter_decode,
     adapter_fwd,
     cache_alloc,
+    cache_attention,
+    cache_compact,
+    cache_copy_pages,
     cache_read,
     cache_write,
     calib_hessian,
@@ -29,11 +33,16 @@ from .api import (  # noqa: F401
     init_norms,
     init_select,
     init_select_global,
+    page_table,
+    pages_fork,
+    pages_resize,
     pattern_stats,
     plan_build,
     plan_tiles,
     qgemv,
     refine_values,
+    rotary,
+    rotary_frequencies,
     shard_rows,
     stage_report,
     stage_timing,

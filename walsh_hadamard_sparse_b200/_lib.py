@@ -46,6 +46,11 @@ class QwhaCache(ctypes.Structure):
                 ("page_size", i32), ("n_pages", i64), ("codes", P), ("scales", P), ("zeros", P)]
 
 
+class QwhaPageTable(ctypes.Structure):
+    _fields_ = [("page_size", i32), ("max_pages", i32), ("n_seqs", i32), ("n_pages", i32), ("refs", P), ("pages", P),
+                ("held", P)]
+
+
 _SIGNATURES = {
     "qwha_fwht": (ctypes.c_int, [ctypes.c_int, P, P, i64, i32, i32, P]),
     "qwha_adapter_fwd": (
@@ -64,6 +69,13 @@ _SIGNATURES = {
     "qwha_cache_write": (ctypes.c_int, [ctypes.POINTER(QwhaCache), i32, ctypes.c_int, ctypes.POINTER(P), P, i64, P]),
     "qwha_cache_read": (ctypes.c_int, [ctypes.POINTER(QwhaCache), i32, ctypes.c_int, P, i32, P, P, i32,
                                        ctypes.POINTER(P), i64, P]),
+    "qwha_rotary": (ctypes.c_int, [ctypes.c_int, i32, P, P, P, P, P, i32, i64, P, P, i32, ctypes.c_int, f32, i32, P]),
+    "qwha_cache_attention": (ctypes.c_int, [ctypes.POINTER(QwhaCache), ctypes.POINTER(QwhaCache), ctypes.c_int, P, i64, i32,
+                                            i64, P, i32, P, P, i32, P, f32, P, P, P, sz, P]),
+    "qwha_pages_resize": (ctypes.c_int, [ctypes.POINTER(QwhaPageTable), P, P, sz, P]),
+    "qwha_pages_fork": (ctypes.c_int, [ctypes.POINTER(QwhaPageTable), P, P, i32, P, P, P, sz, P]),
+    "qwha_cache_copy_pages": (ctypes.c_int, [ctypes.POINTER(QwhaCache), i32, P, P, i32, P]),
+    "qwha_cache_compact": (ctypes.c_int, [ctypes.POINTER(QwhaCache), i32, P, i32, P, P, i32, i32, P]),
     "qwha_validate_slots": (ctypes.c_int, [ctypes.POINTER(QwhaCache), P, i64, P, sz, P]),
     "qwha_coef_grad_noalloc": (ctypes.c_int, [ctypes.POINTER(QwhaAdapter), ctypes.c_int, P, P, i64, f32, P, P]),
     "qwha_init_alloc": (ctypes.c_int, [P, i32, i32, i32, i64, i32, ctypes.c_int, P, P, P, P, P, sz, P]),

@@ -8,15 +8,17 @@ allocator and is passed to the library as the `ws` argument.
 from __future__ import annotations
 
 import ctypes
+import math
 from dataclasses import dataclass
 
 import torch
 
-from ._lib import P, QwhaAdapter, QwhaCache, QwhaQweight, check, lib
+from ._lib import P, QwhaAdapter, QwhaCache, QwhaPageTable, QwhaQweight, check, i32, i64, lib
 
 F32, BF16 = 0, 1
 OP_FWD, OP_BWD, OP_INIT, OP_PLAN, OP_FWD_DENSE, OP_BWD_DENSE, OP_SELECT_GLOBAL, OP_REFINE = 0, 1, 2, 3, 4, 5, 6, 7
 OP_ENERGY, OP_PATTERN, OP_DECODE, OP_SLOTS, OP_QGEMV = 8, 9, 10, 11, 12
+OP_ATTENTION, OP_PAGES = 13, 14
 DECODE_MAX_T = 64  # most tokens of a qgemv or adapter_decode call
 PATTERN_STATS = ("empty_rows", "empty_cols", "min_row", "max_row", "min_col", "max_col", "rank_bound", "half_rows")
 SELECTION = {"magnitude": 0, "random": 1}
@@ -344,6 +346,194 @@ def cache_read(caches, pages: torch.Tensor, row_start: torch.Tensor, n: int, fir
     return outs[0] if isinstance(caches, QCache) else outs
 
 
+def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                       trained: int = 8192, low: float = 1.0, high: float = 32.0,
+                       device="cuda") -> tuple[torch.Tensor, float]:
+    """(freq fp64 [rot/2], factor of the rotated channels) for rotary: freq[c] = base^(-2c/rot), for contexts `factor`
+    times the `trained` one stretched by
+    "linear": every frequency divided by factor;
+    "base": the base raised to base * factor^(rot/(rot-2)), which leaves the fastest and divides the slowest by factor;
+    "ramp": channels that make more than `high` turns in the trained context as they are, those with fewer than `low`
+    divided by factor, linearly in the channel's index between, and the rotated channels scaled by 0.1 ln(factor) + 1;
+    "bands": the same with the border linear in the number of turns, without the scaling."""
+    if rot < 0 or rot % 2:
+        raise ValueError(f"rot {rot}: a non-negative even number")
+    if scaling not in (None, "linear", "base", "ramp", "bands"):
+        raise ValueError(f"scaling {scaling!r}: None, linear, base, ramp or bands")
+    if base <= 1 or factor <= 0 or trained <= 0 or not 0 < low < high:
+        raise ValueError(f"base {base}, factor {factor}, trained {trained}, low {low}, high {high}")
+    if scaling == "base" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    f = [base ** (-2 * c / rot) for c in range(rot // 2)]
+    if scaling == "linear":
+        f = [v / factor for v in f]
+    elif scaling == "ramp":
+        at = [rot * math.log(trained / (t * 2 * math.pi)) / (2 * math.log(base)) for t in (high, low)]
+        lo, hi = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot - 1)
+        u = [min(max((c - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for c in range(rot // 2)]
+        f = [v / factor * w + v * (1 - w) for v, w in zip(f, u)]
+    elif scaling == "bands":
+        u = [min(max((trained * v / (2 * math.pi) - low) / (high - low), 0.0), 1.0) for v in f]
+        f = [v / factor * (1 - w) + v * w for v, w in zip(f, u)]
+    return torch.tensor(f, dtype=torch.float64, device=device), 0.1 * math.log(factor) + 1.0 if scaling == "ramp" else 1.0
+
+
+def _fit_rows(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: int) -> tuple[int, int]:
+    """(address, elements from token to token) of rows whose tokens may lie apart: slices of a wider tensor."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or (t.numel() and (t.stride(2) != 1 and shape[2] > 1 or t.stride(1) != shape[2] and shape[1] > 1)):
+        raise ValueError(f"{name}: expected a CUDA tensor whose heads are contiguous within a token")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+
+
+_STRIDES = (None, i64 * 1, i64 * 2)
+_HEADS = (None, i32 * 1, i32 * 2)
+
+
+def rotary(x, positions: torch.Tensor, freq: torch.Tensor, interleaved: bool = False, factor: float = 1.0,
+           inverse: bool = False, out=None):
+    """Rotary positions of rows x [n, heads, head_dim] (fp32 or bf16; a pair, queries and keys, in one launch): channel
+    pairs (c, c + rot/2), or (2c, 2c + 1) with interleaved, of token i turn by positions[i] * freq[c] (int64 [n], fp64
+    [rot/2]) and are multiplied by factor; channels from rot on are copied. inverse turns back: the gradient of x from
+    that of the result. The tokens of x and out may lie apart (slices of a fused projection); out may be x."""
+    xs, dev, n = (x,) if isinstance(x, torch.Tensor) else tuple(x), torch.cuda.current_device(), positions.shape[0]
+    k = len(xs)
+    if not 1 <= k <= 2:
+        raise ValueError(f"{k} tensors: one or two")
+    if any(t.dim() != 3 for t in xs):
+        raise ValueError("x: expected [n, heads, head_dim]")
+    dtype, head_dim = xs[0].dtype, xs[0].shape[2]
+    if out is None:
+        outs = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs)
+    else:
+        outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(outs) != k:
+            raise ValueError(f"{k} tensors and {len(outs)} outputs")
+    shapes = [(n, t.shape[1], head_dim) for t in xs]
+    a = [_fit_rows("x", t, dtype, s, dev) for t, s in zip(xs, shapes)]
+    b = [_fit_rows("out", t, dtype, s, dev) for t, s in zip(outs, shapes)]
+    check(lib().qwha_rotary(_dt(xs[0]), k, _ROWS[k](*(p for p, _ in a)), _STRIDES[k](*(s for _, s in a)),
+                            _ROWS[k](*(p for p, _ in b)), _STRIDES[k](*(s for _, s in b)),
+                            _HEADS[k](*(s[1] for s in shapes)), head_dim, n, _fit("positions", positions, torch.int64, (n,), dev),
+                            _fit("freq", freq, torch.float64, (freq.shape[0],), dev), 2 * freq.shape[0], int(interleaved),
+                            factor, int(inverse), _raw_stream(dev)), "qwha_rotary")
+    return outs[0] if isinstance(x, torch.Tensor) else outs
+
+
+def cache_attention(kv, q: torch.Tensor, pages: torch.Tensor, q_start: torch.Tensor, past: torch.Tensor,
+                    tree: torch.Tensor | None = None, scale: float | None = None, out: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of queries q [n, q_heads, head_dim] (fp32 or bf16; tokens may lie apart) over the cached keys and values
+    kv, read from their codes. Rows q_start[b] .. q_start[b+1] (int64 [n_seqs+1]) are the newest tokens of sequence b,
+    cached already behind past[b] (int64 [n_seqs]) earlier ones, token t in page pages[b, t // page_size] (int32
+    [n_seqs, max_pages]). A row sees the past and, of its sequence's new tokens, those up to itself, or with tree (int64
+    [n]) those whose bit is set in its mask (up to 64: a drafted tree's node and its ancestors). q_heads is a multiple of
+    the cache's heads; scale defaults to 1/sqrt(head_dim). lse (fp32 [n, q_heads]) receives the log of the softmax sums.
+    A row that sees nothing gets zeros (lse -inf); rows from q_start[-1] on are left as they were (without `out` they are
+    not initialised)."""
+    h, dev, dt = lib(), torch.cuda.current_device(), _dt(q)
+    k, v = kv
+    ck, cv = k.c_struct(dev), v.c_struct(dev)
+    n, q_heads, head_dim = q.shape
+    n_seqs, max_pages = pages.shape
+    at, stride = _fit_rows("q", q, q.dtype, (n, q_heads, ck.head_dim), dev)
+    if out is None:
+        out = q.new_empty((n, q_heads, head_dim))
+    if ws is None:
+        ws = _new_ws(q, h.qwha_workspace_size(OP_ATTENTION, q_heads, head_dim, ck.heads, n, 2 - dt))
+    check(h.qwha_cache_attention(ck, cv, dt, at, n, q_heads, stride, _fit("pages", pages, torch.int32, (n_seqs, max_pages), dev),
+                                 max_pages, _fit("q_start", q_start, torch.int64, (n_seqs + 1,), dev),
+                                 _fit("past", past, torch.int64, (n_seqs,), dev), n_seqs,
+                                 None if tree is None else _fit("tree", tree, torch.int64, (n,), dev),
+                                 head_dim**-0.5 if scale is None else scale,
+                                 _fit("out", out, q.dtype, (n, q_heads, head_dim), dev),
+                                 None if lse is None else _fit("lse", lse, torch.float32, (n, q_heads), dev),
+                                 *_fit_ws(ws, dev), _raw_stream(dev)), "qwha_cache_attention")
+    return out
+
+
+@dataclass
+class PageTable:
+    """Which pages hold which sequence's tokens, on the device: refs int32 [n_pages] (rows that name the page; 0: free),
+    pages int32 [n_seqs, max_pages] (the first ceil(held / page_size) entries of a row; -1 behind), held int64 [n_seqs].
+    One table serves all caches of a model."""
+
+    page_size: int
+    refs: torch.Tensor
+    pages: torch.Tensor
+    held: torch.Tensor
+
+    def c_struct(self, dev: int | None = None) -> QwhaPageTable:
+        dev = torch.cuda.current_device() if dev is None else dev
+        n_seqs, max_pages = self.pages.shape
+        n_pages = self.refs.shape[0]
+        return QwhaPageTable(self.page_size, max_pages, n_seqs, n_pages, _fit("refs", self.refs, torch.int32, (n_pages,), dev),
+                             _fit("pages", self.pages, torch.int32, (n_seqs, max_pages), dev),
+                             _fit("held", self.held, torch.int64, (n_seqs,), dev))
+
+
+def page_table(n_pages: int, page_size: int, n_seqs: int, max_pages: int, device="cuda") -> PageTable:
+    """A table of empty sequences over free pages."""
+    return PageTable(page_size, torch.zeros(n_pages, dtype=torch.int32, device=device),
+                     torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device),
+                     torch.zeros(n_seqs, dtype=torch.int64, device=device))
+
+
+def pages_resize(t: PageTable, want: torch.Tensor, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Give each sequence room for want[b] tokens (int64 [n_seqs]; -1: as it is, 0: free it): pages past the end are given
+    back, then growing sequences take the lowest free pages in their order. Returns t.held, which is want[b] where the
+    sequence was served; when the free pages end, the sequence and the growing ones behind it stay as they were."""
+    h, dev = lib(), torch.cuda.current_device()
+    c = t.c_struct(dev)
+    w = _fit("want", want, torch.int64, (c.n_seqs,), dev)
+    if ws is None:
+        ws = _new_ws(want, h.qwha_workspace_size(OP_PAGES, c.n_seqs, 1, c.n_pages, 0, 0))
+    check(h.qwha_pages_resize(c, w, *_fit_ws(ws, dev), _raw_stream(dev)), "qwha_pages_resize")
+    return t.held
+
+
+def pages_fork(t: PageTable, src: torch.Tensor, dst: torch.Tensor,
+               ws: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Make the empty rows dst (int64 [m]) copies of the rows src (int64 [m]; -1: none): whole pages are shared, a partly
+    filled last page gets a fresh one. Returns (from, to), int32 [m]: the pages to copy with cache_copy_pages in every
+    cache (-1: none). A dst for whose page no free one was left stays empty."""
+    h, dev, m = lib(), torch.cuda.current_device(), src.shape[0]
+    c = t.c_struct(dev)
+    a, b = _fit("src", src, torch.int64, (m,), dev), _fit("dst", dst, torch.int64, (m,), dev)
+    origin, fresh = src.new_empty(m, dtype=torch.int32), src.new_empty(m, dtype=torch.int32)
+    if ws is None:
+        ws = _new_ws(src, h.qwha_workspace_size(OP_PAGES, c.n_seqs, 1, c.n_pages, m, 0))
+    check(h.qwha_pages_fork(c, a, b, m, origin.data_ptr(), fresh.data_ptr(), *_fit_ws(ws, dev), _raw_stream(dev)),
+          "qwha_pages_fork")
+    return origin, fresh
+
+
+def cache_copy_pages(caches, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Copy pages src to pages dst (int32 [m]; -1 in either skips) of a cache or a pair of caches. dst must be distinct
+    and hold no page of src."""
+    cs, dev, m = _caches(caches), torch.cuda.current_device(), src.shape[0]
+    structs = _CACHES[len(cs)](*(c.c_struct(dev) for c in cs))
+    check(lib().qwha_cache_copy_pages(structs, len(cs), _fit("src", src, torch.int32, (m,), dev),
+                                      _fit("dst", dst, torch.int32, (m,), dev), m, _raw_stream(dev)), "qwha_cache_copy_pages")
+
+
+def cache_compact(caches, pages: torch.Tensor, first: torch.Tensor, keep: torch.Tensor) -> None:
+    """Move the kept tokens of each sequence together, in a cache or a pair of caches: token first[b] + keep[b, i] goes to
+    first[b] + i for i up to the first -1 of keep[b] (int32 [n_seqs, width], ascending; first int64 [n_seqs]); pages as
+    in cache_read. For the accepted nodes of a drafted tree, or for what stays of a long context."""
+    cs, dev = _caches(caches), torch.cuda.current_device()
+    n_seqs, max_pages = pages.shape
+    width = keep.shape[1]
+    structs = _CACHES[len(cs)](*(c.c_struct(dev) for c in cs))
+    check(lib().qwha_cache_compact(structs, len(cs), _fit("pages", pages, torch.int32, (n_seqs, max_pages), dev), max_pages,
+                                   _fit("first", first, torch.int64, (n_seqs,), dev),
+                                   _fit("keep", keep, torch.int32, (n_seqs, width), dev), width, n_seqs, _raw_stream(dev)),
+          "qwha_cache_compact")
+
+
 def validate_slots(cache: QCache, slots: torch.Tensor, ws: torch.Tensor | None = None) -> None:
     """Raise QwhaError unless every slot is -1 or within the cache and no slot is named twice (synchronises)."""
     dev = torch.cuda.current_device()
@@ -356,8 +546,8 @@ def validate_slots(cache: QCache, slots: torch.Tensor, ws: torch.Tensor | None =
 
 def check_stream_status() -> None:
     """Synchronise the current stream and raise QwhaError for what its kernels met on the way: a slot or a page outside
-    its cache (status 1; those rows were skipped), a wait that gave up (status 6), a CUDA error. Clears the report,
-    which is kept per device."""
+    its cache, rows of a page table or of a move that were refused (status 1; those rows were skipped), a wait that gave
+    up (status 6), a CUDA error. Clears the report, which is kept per device."""
     check(lib().qwha_check_stream_status(_stream()), "qwha_check_stream_status")
 
 

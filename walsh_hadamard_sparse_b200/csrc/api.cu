@@ -153,12 +153,17 @@ enum Stage {
   ST_GEMV,
   ST_CACHE_WRITE,
   ST_CACHE_READ,
+  ST_ROTARY,
+  ST_ATTENTION,
+  ST_PAGES,
+  ST_CACHE_MOVE,
   ST_COUNT
 };
 const char *kStageNames[ST_COUNT] = {"fwht_fwd",   "spmm_fwd",   "dequant",  "gemm_fwd",  "sddmm_dc",
                                      "gather_bwd", "fwht_bwd",   "gemm_bwd", "init_alloc",
                                      "plan_build", "fwht",       "weff",      "gemm_dc",
-                                     "decode_prepare", "decode_entries", "gemv",      "cache_write", "cache_read"};
+                                     "decode_prepare", "decode_entries", "gemv",      "cache_write", "cache_read",
+                                     "rotary", "cache_attention", "page_table", "cache_move"};
 
 struct StageRec {
   int stage, kernels;
@@ -466,6 +471,9 @@ size_t qwha_workspace_size(qwha_op op, int32_t d_out, int32_t d_in, int64_t p, i
     case QWHA_OP_DECODE: return decode_ws(d_out, d_in, p, T, with_base != 0, with_base == 2);
     case QWHA_OP_QGEMV: return qgemv_ws(d_in, T, with_base == 2);
     case QWHA_OP_SLOTS: return check_slots_bytes(p);
+    case QWHA_OP_ATTENTION:
+      return p > 0 && p <= 65535 ? attention_workspace(d_out, d_in, (int32_t)p, T, with_base == 2) : 0;
+    case QWHA_OP_PAGES: return pages_workspace(d_out, p, T);
   }
   return 0;
 }
@@ -680,10 +688,12 @@ qwha_status qwha_check_stream_status(void *stream) {
   unsigned int word = 0;
   e = read_and_clear_error_word(&word, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_status(e, "error word");
-  if (word && !(word & ~(kErrSlot | kErrPage)))
-    return fail(QWHA_ERR_INVALID_ARG, "cache: %s%s%s", word & kErrSlot ? "a slot outside the cache" : "",
-                word == (kErrSlot | kErrPage) ? ", " : "",
-                word & kErrPage ? "a page outside the cache or its page table" : "");
+  if (word && !(word & ~(kErrSlot | kErrPage | kErrTable)))
+    return fail(QWHA_ERR_INVALID_ARG, "cache: %s%s%s%s%s", word & kErrSlot ? "a slot outside the cache" : "",
+                word & kErrSlot && word & (kErrPage | kErrTable) ? ", " : "",
+                word & kErrPage ? "a page outside the cache or its page table" : "",
+                word & kErrPage && word & kErrTable ? ", " : "",
+                word & kErrTable ? "a row that contradicts the page table, or kept tokens that do not ascend" : "");
   if (word) return fail(QWHA_ERR_TIMEOUT, "device wait gave up (code 0x%x)", word);
   return QWHA_OK;
 }
@@ -1040,6 +1050,203 @@ qwha_status qwha_validate_slots(const qwha_cache *cache, const int64_t *slots, i
     return fail(QWHA_ERR_INVALID_ARG, "%s (at %llu)", bad & 1 ? "a slot named twice" : "a slot outside the cache",
                 bad >> 1);
   return QWHA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// n rows of `width` elements, `stride` apart, of two blocks: whether one writes
+// what the other holds. Blocks with one stride may interleave.
+bool rows_apart(const void *x, int64_t xs, int64_t xw, const void *y, int64_t ys, int64_t yw, int64_t n, int64_t esz) {
+  const int64_t a = (int64_t)(uintptr_t)x, b = (int64_t)(uintptr_t)y;
+  const int64_t a1 = a + ((n - 1) * xs + xw) * esz, b1 = b + ((n - 1) * ys + yw) * esz;
+  if (a1 <= b || b1 <= a) return true;
+  if (xs != ys) return false;
+  const int64_t step = xs * esz, off = ((b - a) % step + step) % step;  // of a row of y behind one of x
+  return off >= xw * esz && off + yw * esz <= step;
+}
+
+qwha_status check_table(const qwha_page_table *t) {
+  if (!t) return fail(QWHA_ERR_INVALID_ARG, "the page table is NULL");
+  if (t->page_size < 1 || t->max_pages < 0 || t->n_seqs < 0 || t->n_pages < 0)
+    return fail(QWHA_ERR_INVALID_ARG, "page_size %d, max_pages %d, n_seqs %d, n_pages %d", t->page_size, t->max_pages,
+                t->n_seqs, t->n_pages);
+  if (t->n_pages > 0) QWHA_CHECK_PTR(t->refs, "refs");
+  if (t->n_seqs > 0 && t->max_pages > 0) QWHA_CHECK_PTR(t->pages, "pages");
+  if (t->n_seqs > 0) QWHA_CHECK_PTR(t->held, "held");
+  return QWHA_OK;
+}
+
+qwha_status check_moved(const qwha_cache *caches, int32_t n_caches) {
+  if (n_caches < 1 || n_caches > 2) return fail(QWHA_ERR_INVALID_ARG, "n_caches %d not 1 or 2", n_caches);
+  if (!caches) return fail(QWHA_ERR_INVALID_ARG, "caches is NULL");
+  for (int i = 0; i < n_caches; ++i) {
+    const qwha_status st = check_cache(caches + i);
+    if (st != QWHA_OK) return st;
+  }
+  return QWHA_OK;
+}
+
+CachePair moved_pair(const qwha_cache *caches, int32_t n_caches) {
+  CachePair c = {};
+  for (int i = 0; i < n_caches; ++i) c.cache[i] = caches[i];
+  return c;
+}
+
+}  // namespace
+
+extern "C" {
+
+qwha_status qwha_rotary(qwha_dtype dt, int32_t n_x, const void *const *x, const int64_t *x_stride, void *const *y,
+                        const int64_t *y_stride, const int32_t *heads, int32_t head_dim, int64_t n,
+                        const int64_t *positions, const double *freq, int32_t rot, qwha_rotary_layout layout,
+                        float factor, int32_t inverse, void *stream) {
+  if (!valid_dtype(dt)) return fail(QWHA_ERR_INVALID_ARG, "dtype %d", (int)dt);
+  if (n_x < 1 || n_x > 2) return fail(QWHA_ERR_INVALID_ARG, "n_x %d not 1 or 2", n_x);
+  if (!x || !y || !x_stride || !y_stride || !heads) return fail(QWHA_ERR_INVALID_ARG, "x, y, strides or heads is NULL");
+  if (head_dim < 8 || head_dim % 8 || head_dim > 32768)
+    return fail(QWHA_ERR_INVALID_ARG, "head_dim %d must be a positive multiple of 8", head_dim);
+  if (head_dim > cache_max_head_dim())
+    return fail(QWHA_ERR_UNSUPPORTED, "head_dim %d above %d", head_dim, cache_max_head_dim());
+  if (rot < 0 || rot % 2 || rot > head_dim)
+    return fail(QWHA_ERR_INVALID_ARG, "rot %d must be even and at most head_dim %d", rot, head_dim);
+  if (layout != QWHA_ROTARY_HALF && layout != QWHA_ROTARY_PAIRS) return fail(QWHA_ERR_INVALID_ARG, "layout %d", (int)layout);
+  if (n < 0 || n > (1LL << 40)) return fail(QWHA_ERR_INVALID_ARG, "n %lld out of range", (long long)n);
+  if (!isfinite(factor)) return fail(QWHA_ERR_INVALID_ARG, "factor is not finite");
+  const int64_t esz = dt == QWHA_F32 ? 4 : 2;
+  for (int i = 0; i < n_x; ++i) {
+    if (heads[i] < 1 || heads[i] > 65535) return fail(QWHA_ERR_INVALID_ARG, "heads %d", heads[i]);
+    const int64_t w = (int64_t)heads[i] * head_dim;
+    if (x_stride[i] < w || y_stride[i] < w || x_stride[i] > (1LL << 32) || y_stride[i] > (1LL << 32))
+      return fail(QWHA_ERR_INVALID_ARG, "strides %lld and %lld of tokens of %lld elements", (long long)x_stride[i],
+                  (long long)y_stride[i], (long long)w);
+    if (x_stride[i] * esz % 16 || y_stride[i] * esz % 16)
+      return fail(QWHA_ERR_MISALIGNED, "the strides of tokens must be multiples of 16 bytes");
+  }
+  if (n == 0) return QWHA_OK;
+  RotaryArgs r = {};
+  for (int i = 0; i < n_x; ++i) {
+    QWHA_CHECK_PTR(x[i], "x");
+    QWHA_CHECK_PTR(y[i], "y");
+    r.x[i] = x[i], r.y[i] = y[i], r.x_stride[i] = x_stride[i], r.y_stride[i] = y_stride[i], r.heads[i] = heads[i];
+  }
+  QWHA_CHECK_PTR(positions, "positions");
+  if (rot > 0) QWHA_CHECK_PTR(freq, "freq");
+  for (int i = 0; i < n_x; ++i)
+    for (int j = 0; j < n_x; ++j) {
+      const int64_t xw = (int64_t)heads[i] * head_dim, yw = (int64_t)heads[j] * head_dim;
+      if (i == j && x[i] == y[i] && x_stride[i] == y_stride[i]) continue;  // in place
+      if (!rows_apart(x[i], x_stride[i], xw, y[j], y_stride[j], yw, n, esz))
+        return fail(QWHA_ERR_INVALID_ARG, "x and y overlap (in place is x itself, with its stride)");
+    }
+  if (n_x == 2 && !rows_apart(y[0], y_stride[0], (int64_t)heads[0] * head_dim, y[1], y_stride[1],
+                              (int64_t)heads[1] * head_dim, n, esz))
+    return fail(QWHA_ERR_INVALID_ARG, "the two outputs overlap");
+  r.head_dim = head_dim, r.rot = rot, r.n = n, r.positions = positions, r.freq = freq, r.factor = factor;
+  r.pairs = layout == QWHA_ROTARY_PAIRS, r.inverse = inverse != 0;
+  StageScope sc(ST_ROTARY, 1, (cudaStream_t)stream);
+  return cuda_status(launch_rotary(dt, r, (cudaStream_t)stream), "rotary");
+}
+
+qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_dtype dt, const void *q, int64_t n,
+                                 int32_t q_heads, int64_t q_stride, const int32_t *pages, int32_t max_pages,
+                                 const int64_t *q_start, const int64_t *past, int32_t n_seqs, const int64_t *tree,
+                                 float scale, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
+  if (!valid_dtype(dt)) return fail(QWHA_ERR_INVALID_ARG, "dtype %d", (int)dt);
+  if (!k || !v) return fail(QWHA_ERR_INVALID_ARG, "%s is NULL", k ? "v" : "k");
+  qwha_status st = check_cache(k);
+  if (st != QWHA_OK || (st = check_cache(v)) != QWHA_OK) return st;
+  if (k->heads != v->heads || k->head_dim != v->head_dim || k->page_size != v->page_size || k->n_pages != v->n_pages)
+    return fail(QWHA_ERR_INVALID_ARG, "the caches of keys and values differ in heads, head_dim, page_size or n_pages");
+  if (q_heads < 1 || q_heads > 65535 || q_heads % k->heads)
+    return fail(QWHA_ERR_INVALID_ARG, "q_heads %d must be a multiple of the cache's heads %d", q_heads, k->heads);
+  if (n < 0 || n > 2147483647LL) return fail(QWHA_ERR_INVALID_ARG, "n %lld out of range", (long long)n);
+  if (n_seqs < 0 || max_pages < 0) return fail(QWHA_ERR_INVALID_ARG, "n_seqs %d, max_pages %d", n_seqs, max_pages);
+  if (!isfinite(scale)) return fail(QWHA_ERR_INVALID_ARG, "scale is not finite");
+  const int64_t esz = dt == QWHA_F32 ? 4 : 2, row = (int64_t)q_heads * k->head_dim;
+  if (q_stride < row || q_stride > (1LL << 32))
+    return fail(QWHA_ERR_INVALID_ARG, "q_stride %lld of tokens of %lld elements", (long long)q_stride, (long long)row);
+  if (q_stride * esz % 16) return fail(QWHA_ERR_MISALIGNED, "q_stride must be a multiple of 16 bytes");
+  if (n == 0 || n_seqs == 0) return QWHA_OK;
+  QWHA_CHECK_PTR(q, "q");
+  QWHA_CHECK_PTR(out, "out");
+  if (max_pages > 0) QWHA_CHECK_PTR(pages, "pages");
+  QWHA_CHECK_PTR(q_start, "q_start");
+  QWHA_CHECK_PTR(past, "past");
+  if (tree) QWHA_CHECK_PTR(tree, "tree");
+  if (lse) QWHA_CHECK_PTR(lse, "lse");
+  if ((st = check_ws(ws, ws_bytes, attention_workspace(q_heads, k->head_dim, k->heads, n, dt == QWHA_F32))) != QWHA_OK)
+    return st;
+  const size_t q_bytes = (size_t)(((n - 1) * q_stride + row) * esz), out_bytes = (size_t)(n * row * esz);
+  if ((st = check_apart("q and out", q, q_bytes, out, out_bytes)) != QWHA_OK) return st;
+  if (lse && ((st = check_apart("q and lse", q, q_bytes, lse, (size_t)n * q_heads * 4)) != QWHA_OK ||
+              (st = check_apart("out and lse", out, out_bytes, lse, (size_t)n * q_heads * 4)) != QWHA_OK))
+    return st;
+  AttnArgs a = {};
+  a.k = *k, a.v = *v;
+  a.unit_k = k->had_block ? (float)(1.0 / sqrt((double)k->had_block)) : 1.f;
+  a.unit_v = v->had_block ? (float)(1.0 / sqrt((double)v->had_block)) : 1.f;
+  a.q = q, a.q_stride = q_stride, a.n = n, a.q_heads = q_heads, a.grp = q_heads / k->heads;
+  a.pages = pages, a.max_pages = max_pages;
+  a.cap = (int)std::min<int64_t>((int64_t)max_pages * k->page_size, 1 << 30);
+  a.q_start = q_start, a.past = past, a.n_seqs = n_seqs, a.tree = tree;
+  a.scale2 = (float)(scale * 1.4426950408889634), a.out = out, a.lse = lse, a.f32 = dt == QWHA_F32;
+  StageScope sc(ST_ATTENTION, attention_launches(), (cudaStream_t)stream);
+  return cuda_status(launch_attention(a, ws, (cudaStream_t)stream), "cache_attention");
+}
+
+qwha_status qwha_pages_resize(const qwha_page_table *t, const int64_t *want, void *ws, size_t ws_bytes, void *stream) {
+  qwha_status st = check_table(t);
+  if (st != QWHA_OK || t->n_seqs == 0) return st;
+  QWHA_CHECK_PTR(want, "want");
+  if ((st = check_ws(ws, ws_bytes, pages_workspace(t->n_seqs, t->n_pages, 0))) != QWHA_OK) return st;
+  StageScope sc(ST_PAGES, 1, (cudaStream_t)stream);
+  return cuda_status(launch_pages_resize(*t, want, ws, (cudaStream_t)stream), "pages_resize");
+}
+
+qwha_status qwha_pages_fork(const qwha_page_table *t, const int64_t *src, const int64_t *dst, int32_t m, int32_t *from,
+                            int32_t *to, void *ws, size_t ws_bytes, void *stream) {
+  qwha_status st = check_table(t);
+  if (st != QWHA_OK) return st;
+  if (m < 0) return fail(QWHA_ERR_INVALID_ARG, "m %d", m);
+  if (m == 0) return QWHA_OK;
+  QWHA_CHECK_PTR(src, "src");
+  QWHA_CHECK_PTR(dst, "dst");
+  QWHA_CHECK_PTR(from, "from");
+  QWHA_CHECK_PTR(to, "to");
+  if ((st = check_ws(ws, ws_bytes, pages_workspace(t->n_seqs, t->n_pages, m))) != QWHA_OK) return st;
+  StageScope sc(ST_PAGES, 1, (cudaStream_t)stream);
+  return cuda_status(launch_pages_fork(*t, src, dst, m, from, to, ws, (cudaStream_t)stream), "pages_fork");
+}
+
+qwha_status qwha_cache_copy_pages(const qwha_cache *caches, int32_t n_caches, const int32_t *from, const int32_t *to,
+                                  int32_t m, void *stream) {
+  const qwha_status st = check_moved(caches, n_caches);
+  if (st != QWHA_OK) return st;
+  if (m < 0) return fail(QWHA_ERR_INVALID_ARG, "m %d", m);
+  if (m == 0) return QWHA_OK;
+  QWHA_CHECK_PTR(from, "from");
+  QWHA_CHECK_PTR(to, "to");
+  StageScope sc(ST_CACHE_MOVE, 1, (cudaStream_t)stream);
+  return cuda_status(launch_copy_pages(moved_pair(caches, n_caches), n_caches, from, to, m, (cudaStream_t)stream),
+                     "cache_copy_pages");
+}
+
+qwha_status qwha_cache_compact(const qwha_cache *caches, int32_t n_caches, const int32_t *pages, int32_t max_pages,
+                               const int64_t *first, const int32_t *keep, int32_t width, int32_t n_seqs, void *stream) {
+  const qwha_status st = check_moved(caches, n_caches);
+  if (st != QWHA_OK) return st;
+  if (n_seqs < 0 || max_pages < 0 || width < 0)
+    return fail(QWHA_ERR_INVALID_ARG, "n_seqs %d, max_pages %d, width %d", n_seqs, max_pages, width);
+  if (n_seqs == 0 || width == 0) return QWHA_OK;
+  if (max_pages > 0) QWHA_CHECK_PTR(pages, "pages");
+  QWHA_CHECK_PTR(first, "first");
+  QWHA_CHECK_PTR(keep, "keep");
+  StageScope sc(ST_CACHE_MOVE, (int)cdiv(n_seqs, 65535), (cudaStream_t)stream);
+  return cuda_status(launch_compact(moved_pair(caches, n_caches), n_caches, pages, max_pages, first, keep, width, n_seqs,
+                                    (cudaStream_t)stream),
+                     "cache_compact");
 }
 
 }  // extern "C"

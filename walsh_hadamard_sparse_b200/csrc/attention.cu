@@ -1,0 +1,269 @@
+// Attention over the quantized cache: the kernel for every format, the joining of
+// tiles that were cut between CTAs, and the choice of the kernels.
+
+#include <algorithm>
+
+#include "attention.cuh"
+
+namespace qwha {
+namespace {
+
+using namespace attn;
+
+// ---------------------------------------------------------------- every format
+
+constexpr int kAnyThreads = 128, kAnyRows = 8, kAnyTokens = 32;
+
+__device__ __forceinline__ void unpack_run(const uint8_t *p, float *q, int bits) {
+  const uint32_t mask = (1u << bits) - 1u;
+  uint32_t w = 0, hi = 0;
+  if (bits == 8) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w = v.x, hi = v.y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = (float)((w >> (8 * i)) & 255u), q[i + 4] = (float)((hi >> (8 * i)) & 255u);
+    return;
+  }
+  if (bits == 4) w = *reinterpret_cast<const uint32_t *>(p);
+  else if (bits == 2) w = *reinterpret_cast<const uint16_t *>(p);
+  else w = (uint32_t)p[0] | (uint32_t)p[1] << 8 | (uint32_t)p[2] << 16;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = (float)((w >> (bits * i)) & mask);
+}
+
+// scale (code - zero) of eight codes of a row.
+__device__ __forceinline__ void load_values(const qwha_cache &c, int64_t row, int run, float *v) {
+  unpack_run(c.codes + row * (c.head_dim / 8 * c.bits) + run * c.bits, v, c.bits);
+  const int64_t group = row * (c.head_dim / c.group) + run * 8 / c.group;
+  const float s = c.scales[group], z = (float)c.zeros[group];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = s * (v[i] - z);
+}
+
+// One cached head and up to eight rows of queries a tile: 32 tokens at a time go
+// to shared memory as fp32 values; lane t of a warp holds the scores of token t
+// for the warp's two rows, a thread the values of one or two channels.
+__global__ void __launch_bounds__(kAnyThreads) attention_any_kernel(const AttnArgs a) {
+  extern __shared__ __align__(16) float smem[];
+  const int D = a.k.head_dim, pitch = D + 4;
+  float *q_s = smem;                          // [8][D]
+  float *k_s = q_s + kAnyRows * D;            // [32][D + 4]
+  float *v_s = k_s + kAnyTokens * pitch;      // [32][D]
+  float *p_s = v_s + kAnyTokens * D;          // [8][32]
+  __shared__ float m_s[kAnyRows], l_s[kAnyRows], turn_s[kAnyRows];
+  __shared__ int64_t slot_s[kAnyTokens];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Place at;
+  long long left = my_share<kAnyThreads>(a, &at);
+  int4 begun = make_int4(0, 0, 0, 0), gone_on = begun;
+  bool first = true;
+  while (left > 0) {
+    const Seq s(a, at.b);
+    if (s.rows == 0) {
+      ++at.b;
+      continue;
+    }
+    if (threadIdx.x == 0 && (long long)s.past + (a.tree && s.rows > 64 ? 64 : s.rows) > a.cap) atomicOr(a.err, kErrPage);
+    const int kv = at.block / a.parts, units = s.units(a, at.tile), length = s.length(a, at.tile);
+    const Rows rows = rows_of(a, s, kv, at.block % a.parts, at.tile);
+    const int run = left < units - at.unit ? (int)left : units - at.unit;
+    __syncthreads();
+    for (int r = warp; r < kAnyRows; r += kAnyThreads / 32) {
+      if (r < rows.n) warp_query(a, q_s + r * D, rows.q_row(r), rows.q_head(r));
+      if (lane == 0) m_s[r] = -INFINITY, l_s[r] = 0.f;
+    }
+    float acc[2][kAnyRows];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < kAnyRows; ++r) acc[i][r] = 0.f;
+    for (int u = at.unit; u < at.unit + run; ++u) {
+      const int t0 = u * kAnyTokens;
+      __syncthreads();
+      if (threadIdx.x < kAnyTokens) slot_s[threadIdx.x] = t0 + (int)threadIdx.x < length ? slot_of(a, at.b, t0 + threadIdx.x) : -1;
+      __syncthreads();
+      for (int i = threadIdx.x; i < kAnyTokens * (D / 8); i += kAnyThreads) {
+        const int t = i / (D / 8), c = i - t * (D / 8);
+        float k[8], v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) k[e] = v[e] = 0.f;
+        if (slot_s[t] >= 0) {
+          load_values(a.k, slot_s[t] * a.k.heads + kv, c, k);
+          load_values(a.v, slot_s[t] * a.k.heads + kv, c, v);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) k_s[t * pitch + c * 8 + e] = k[e], v_s[t * D + c * 8 + e] = v[e];
+      }
+      __syncthreads();
+      for (int r = warp * 2; r < warp * 2 + 2; ++r) {
+        float x = 0.f;
+        for (int d = 0; d < D; ++d) x = fmaf(q_s[r * D + d], k_s[lane * pitch + d], x);
+        bool on = r < rows.n && slot_s[lane] >= 0;
+        if (on) {
+          const int j = rows.j0 + r / rows.heads;
+          on = s.sees(a, j, a.tree ? (unsigned long long)a.tree[s.row0 + j] : 0, t0 + lane);
+        }
+        // a score that is not a number stays one; a masked one counts nothing
+        float top = on ? x : -INFINITY;
+#pragma unroll
+        for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        const float old = m_s[r], m = fmaxf(old, top), base = m == -INFINITY ? 0.f : m;
+        const float p = on ? exp2f(x - base) : 0.f;
+        float sum = p;
+#pragma unroll
+        for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
+        p_s[r * kAnyTokens + lane] = p;
+        __syncwarp();
+        if (lane == 0) {
+          const float f = exp2f(old - base);
+          turn_s[r] = f, m_s[r] = m, l_s[r] = l_s[r] * f + sum;
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int d = threadIdx.x + i * kAnyThreads;
+        if (d >= D) break;
+#pragma unroll
+        for (int r = 0; r < kAnyRows; ++r) acc[i][r] *= turn_s[r];
+        for (int t = 0; t < kAnyTokens; ++t) {
+          if (slot_s[t] < 0) continue;
+          const float v = v_s[t * D + d];
+#pragma unroll
+          for (int r = 0; r < kAnyRows; ++r) {
+            const float p = p_s[r * kAnyTokens + t];
+            if (p != 0.f) acc[i][r] = fmaf(p, v, acc[i][r]);  // a masked value may be a NaN
+          }
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int d = threadIdx.x + i * kAnyThreads;
+      if (d < D)
+#pragma unroll
+        for (int r = 0; r < kAnyRows; ++r) q_s[r * D + d] = acc[i][r];
+    }
+    __syncthreads();
+    const bool starts = at.unit == 0, ends = at.unit + run == units;
+    const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
+    for (int r = warp; r < rows.n; r += kAnyThreads / 32) {
+      if (starts && ends) {
+        warp_finish(a, q_s + r * D, m_s[r], l_s[r], rows.q_row(r), rows.q_head(r));
+      } else {
+        for (int d = lane; d < D; d += 32) piece_values(a, slot, r)[d] = q_s[r * D + d];
+        if (lane == 0) piece_stats(a, slot, r)[0] = m_s[r], piece_stats(a, slot, r)[1] = l_s[r];
+      }
+    }
+    if (starts && !ends) begun = make_int4(at.b, at.block, at.tile, 1);
+    if (!starts && first) gone_on = make_int4(at.b, at.block, at.tile, ends ? 3 : 1);
+    first = false;
+    left -= run;
+    at.unit = 0;
+    if (++at.tile == s.tiles) {
+      at.tile = 0;
+      if (++at.block == a.blocks) at.block = 0, ++at.b;
+    }
+  }
+  if (threadIdx.x == 0) a.part_desc[2 * blockIdx.x] = gone_on, a.part_desc[2 * blockIdx.x + 1] = begun;
+}
+
+// ---------------------------------------------------------------- joining
+
+// The tile that CTA blockIdx.x of the kernel before began and left: its piece and
+// those of the CTAs that went on with it, a warp a row, in order.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a) {
+  __shared__ float x_s[kJoinThreads / 32][256];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.v.head_dim;
+  const int4 begun = a.part_desc[2 * c + 1];
+  if (!(begun.w & 1)) return;
+  const int each = a.tq * a.gh, rr = blockIdx.y * (kJoinThreads / 32) + warp;
+  if (rr >= a.part_rows) return;
+  const int kv = begun.y / a.parts * a.hb + rr / each, r = rr % each;
+  if (kv >= a.k.heads) return;
+  const Seq s(a, begun.x);
+  const Rows rows = rows_of(a, s, kv, begun.y % a.parts, begun.z);
+  if (r >= rows.n) return;
+  float m = -INFINITY, l = 0.f, acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int p = c; p < a.ctas; ++p) {
+    const int slot = p == c ? 2 * p + 1 : 2 * p;
+    const int flags = p == c ? 1 : a.part_desc[slot].w;
+    if (!(flags & 1)) continue;  // a CTA without units
+    const float pm = piece_stats(a, slot, rr)[0], pl = piece_stats(a, slot, rr)[1];
+    // NaN goes on as it is: fmaxf drops it, but the sum carries it
+    const float top = fmaxf(m, pm), base = top == -INFINITY ? 0.f : top;
+    const float f = exp2f(m - base), g = exp2f(pm - base);
+    const float *v = piece_values(a, slot, rr);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i < D) acc[i] = acc[i] * f + v[lane + 32 * i] * g;
+    l = l * f + pl * g, m = top;
+    if (flags & 2) break;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (lane + 32 * i < D) x_s[warp][lane + 32 * i] = acc[i];
+  __syncwarp();
+  warp_finish(a, x_s[warp], m, l, rows.q_row(r), rows.q_head(r));
+}
+
+size_t any_smem(int D) {
+  return (size_t)(kAnyRows * D + kAnyTokens * (D + 4) + kAnyTokens * D + kAnyRows * kAnyTokens) * 4;
+}
+
+}  // namespace
+
+int attention_launches() { return 2; }
+
+namespace {
+constexpr int kMaxCtasPerSm = 4;
+
+struct Cut {
+  int ctas, part_rows;
+};
+Cut any_cut(int grp) {
+  const int gh = std::min(grp, kAnyRows);
+  return {sm_count() * 3, std::max(1, kAnyRows / gh) * gh};
+}
+size_t cut_bytes(const Cut &c, int D) {
+  return align_up((size_t)c.ctas * 2 * sizeof(int4), 256) + align_up((size_t)c.ctas * 2 * c.part_rows * 8, 256) +
+         align_up((size_t)c.ctas * 2 * c.part_rows * D * 4, 256);
+}
+}  // namespace
+
+size_t attention_workspace(int32_t q_heads, int32_t head_dim, int32_t heads, int64_t n, bool f32) {
+  if (heads <= 0 || q_heads % heads || n <= 0) return 0;
+  return cut_bytes(any_cut(q_heads / heads), head_dim);
+}
+
+cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
+  static std::atomic<size_t> allowed[64];
+  a.err = device_error_word();
+  if (!a.err) return cudaErrorInvalidDevicePointer;
+  const Cut c = any_cut(a.grp);
+  a.gh = std::min(a.grp, kAnyRows), a.tq = std::max(1, kAnyRows / a.gh), a.parts = (int)cdiv(a.grp, a.gh);
+  a.hb = 1, a.blocks = a.k.heads * a.parts, a.kt = kAnyTokens, a.ctas = c.ctas, a.part_rows = c.part_rows;
+  char *p = static_cast<char *>(ws);
+  a.part_desc = reinterpret_cast<int4 *>(p), p += align_up((size_t)c.ctas * 2 * sizeof(int4), 256);
+  a.part_stats = reinterpret_cast<float *>(p), p += align_up((size_t)c.ctas * 2 * c.part_rows * 8, 256);
+  a.part = reinterpret_cast<float *>(p);
+  const size_t smem = any_smem(a.k.head_dim);
+  cudaError_t e = allow_smem(reinterpret_cast<const void *>(attention_any_kernel), smem, allowed);
+  if (e != cudaSuccess) return e;
+  attention_any_kernel<<<a.ctas, kAnyThreads, smem, s>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.ctas, (unsigned)cdiv(a.part_rows, kJoinThreads / 32)), cfg.blockDim = dim3(kJoinThreads), cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr, cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel, a);
+}
+
+}  // namespace qwha

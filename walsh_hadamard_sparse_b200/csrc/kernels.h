@@ -228,4 +228,62 @@ size_t check_slots_bytes(int64_t n_slots);
 cudaError_t launch_check_slots(const int64_t *slots, int64_t n, int64_t n_slots, void *ws, unsigned long long *bad,
                                cudaStream_t s);
 
+// Rotary positions (rotary.cu).
+struct RotaryArgs {
+  const void *x[2];
+  void *y[2];
+  int64_t x_stride[2], y_stride[2];
+  int heads[2];  // heads[1] 0: one tensor
+  int head_dim, rot;
+  int64_t n;
+  const int64_t *positions;
+  const double *freq;
+  float factor;
+  bool pairs, inverse;
+};
+cudaError_t launch_rotary(qwha_dtype dt, const RotaryArgs &r, cudaStream_t s);
+
+// Page table and moves of cached rows (pages.cu).
+constexpr unsigned int kErrTable = 0x4000u;  // rows of a table or of a move that were refused
+size_t pages_workspace(int64_t n_seqs, int64_t n_pages, int64_t m);
+cudaError_t launch_pages_resize(const qwha_page_table &t, const int64_t *want, void *ws, cudaStream_t s);
+cudaError_t launch_pages_fork(const qwha_page_table &t, const int64_t *src, const int64_t *dst, int32_t m,
+                              int32_t *from, int32_t *to, void *ws, cudaStream_t s);
+cudaError_t launch_copy_pages(const CachePair &c, int n_caches, const int32_t *from, const int32_t *to, int32_t m,
+                              cudaStream_t s);
+cudaError_t launch_compact(const CachePair &c, int n_caches, const int32_t *pages, int32_t max_pages,
+                           const int64_t *first, const int32_t *keep, int32_t width, int32_t n_seqs, cudaStream_t s);
+
+// Attention over the quantized cache (attention.cu, attention.cuh).
+struct AttnArgs {
+  qwha_cache k, v;
+  float unit_k, unit_v;  // 1 / sqrt(had_block)
+  const void *q;
+  int64_t q_stride, n;
+  int q_heads, grp;  // query heads, and of one cached head
+  const int32_t *pages;
+  int max_pages;
+  int cap;  // tokens the page table has room for
+  const int64_t *q_start, *past;
+  int n_seqs;
+  const int64_t *tree;
+  float scale2;  // scale log2(e)
+  void *out;
+  float *lse;
+  int f32;
+  unsigned int *err;
+  // How the work is cut (launch_attention).
+  int tq, gh, parts;  // new tokens and query heads (of a cached head) of a tile; parts of the group
+  int hb, blocks;     // cached heads of a CTA; blocks of heads times parts
+  int kt;             // cached tokens of a unit
+  int ctas;
+  // Pieces of tiles that are cut between CTAs.
+  int part_rows;
+  float *part, *part_stats;
+  int4 *part_desc;  // of CTA c: [2 c] and [2 c + 1]
+};
+size_t attention_workspace(int32_t q_heads, int32_t head_dim, int32_t heads, int64_t n, bool f32);
+int attention_launches();
+cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s);
+
 }  // namespace qwha
