@@ -29,7 +29,9 @@
  *     only enqueues work on it and returns without synchronising, except
  *     qwha_validate_plan, qwha_validate_slots and qwha_check_stream_status,
  *     which synchronise it.
- *   - Device buffers must be 16-byte aligned (QWHA_ERR_MISALIGNED otherwise).
+ *   - Device buffers must be 16-byte aligned (QWHA_ERR_MISALIGNED otherwise);
+ *     index arrays of qwha_rotary, qwha_cache_attention and the calls on pages
+ *     (int32, int64, and the fp64 frequencies) to their elements only.
  *   - The caller owns all memory. Calls that need scratch take `ws` (device,
  *     256-byte aligned) and `ws_bytes`; qwha_workspace_size gives the need.
  *   - Errors are returned as qwha_status; nothing is thrown across the ABI.

@@ -1,5 +1,7 @@
 """Plain statements (numpy, 64 bits) of the operators around the cache: rotary positions, attention, page table, moves."""
 
+import functools
+
 import numpy as np
 
 from _serving import unpack
@@ -23,6 +25,15 @@ def dense_pool(pool, bits, group):
     return v.reshape(-1, *v.shape[2:])
 
 
+def largest_steps(pool, bits, group):
+    """|scale| times the largest |code - zero| of any code, per value of a pool: [slots, heads, head_dim]."""
+    _, s, z = pool
+    with np.errstate(all="ignore"):
+        v = np.repeat(np.abs(s.astype(np.float64)) * np.maximum(z, 2**bits - 1 - z.astype(np.float64)), group, -1)
+    return v.reshape(-1, *v.shape[2:])
+
+
+@functools.cache
 def hadamard(n):
     i = np.arange(n)
     par = np.array([[bin(a & b).count("1") & 1 for b in i] for a in i])
@@ -50,43 +61,53 @@ def shuffled_table(g, totals, page_size, spare=2):
     return table, n_pages
 
 
-def attention(q, kd, vd, had_k, had_v, table, page_size, past, new, tree, scale, eps):
-    """(out, lse, bound of out, bound of lse): fp64, for stored-frame pools kd, vd [slots, heads, D]. The bounds allow
-    an arithmetic that rounds the rotated query and the softmax weights to relative eps each, and sums in fp32."""
+def attention(q, kd, vd, vstep, had_k, had_v, table, page_size, past, new, tree, scale, eps):
+    """(out, lse, bound of out, bound of lse): fp64, for stored-frame pools kd, vd [slots, heads, D]; vstep: the largest
+    |scale (code - zero)| each stored value could have. The bounds allow an arithmetic that rounds the rotated query and
+    the softmax weights to relative eps each and sums in fp32, with weights below 2^-33 of the largest held to that: p
+    scale is kept in f16, whose smallest numbers are 2^-24 apart, scaled so that 2^8 stands for p = 1 at the largest
+    scale."""
     n, q_heads, D = q.shape
-    grp = q_heads // kd.shape[1]
+    heads = kd.shape[1]
+    grp, at, f32 = q_heads // heads, 0, 2.0**-24
     out, lse = np.zeros((n, q_heads, D)), np.full((n, q_heads), -np.inf)
     tol, lse_tol = np.zeros((n, q_heads, D)), np.zeros((n, q_heads))
-    at, f32 = 0, 2.0**-24
     for b, (p, m) in enumerate(zip(past, new)):
         t = np.arange(p + m)
-        pages = table[b, t // page_size] if len(t) else np.zeros(0, int)
-        slots = pages.astype(np.int64) * page_size + t % page_size
-        for j in range(m):
-            u = t - p
-            if tree is None:
-                seen = u <= j
-            else:
-                bits = int(tree[at + j]) & (2**64 - 1)
-                seen = (u < 0) | ((u < 64) & np.array([(bits >> max(0, min(int(x), 63))) & 1 for x in u], bool))
-            sl = slots[seen & (pages >= 0)]
-            for h in range(q_heads):
-                if not len(sl):
-                    continue
-                qr = rotate(q[at + j, h].astype(np.float64), had_k) * scale
-                k, v = kd[sl, h // grp], vd[sl, h // grp]
-                s = k @ qr
-                w = np.exp(s - s.max())
-                total = w.sum()
-                w = w / total
-                out[at + j, h] = rotate(w @ v, had_v)
-                lse[at + j, h] = s.max() + np.log(total)
-                # a rounded query moves a score by eps sum |k q| at most, plus fp32 sums; weights move by twice that
-                # (their own score and the total), are rounded once, and are summed in fp32
-                ds = (eps + (D + 16) * f32) * (np.abs(k) @ np.abs(qr)).max() + 4 * f32 * np.abs(s).max()
-                rel = 2 * np.expm1(ds) + 2 * eps + (len(sl) + 64) * f32
-                tol[at + j, h] = spread_abs(rel * (w @ np.abs(v)), had_v) * (1 + 16 * f32) + 1e-30
-                lse_tol[at + j, h] = ds + eps + (len(sl) + 64) * f32 + 4 * f32 * abs(lse[at + j, h])
+        pages = table[b, t // page_size].astype(np.int64)
+        u = t - p
+        if tree is None:
+            seen = u[None] <= np.arange(m)[:, None]
+        else:
+            bits = tree[at:at + m].astype(np.int64).view(np.uint64)[:, None] >> np.clip(u, 0, 63).astype(np.uint64)[None]
+            seen = (u < 0)[None] | ((u < 64)[None] & (bits & np.uint64(1)).astype(bool))
+        live = np.flatnonzero(pages >= 0)
+        slots, seen = (pages * page_size + t % page_size)[live], seen[:, live]
+        some = seen.any(1)
+        if len(live) and m:
+            qr = (rotate(q[at:at + m].astype(np.float64), had_k) * scale).reshape(m, heads, grp, D)
+            with np.errstate(all="ignore"):
+                for h in range(heads):
+                    k, v = kd[slots, h], vd[slots, h]
+                    used = seen.any(0)[:, None]
+                    k, v = np.where(used, k, 0), np.where(used, v, 0)
+                    s = np.where(seen[:, None], qr[:, h] @ k.T, -np.inf)
+                    top = np.where(some[:, None], s.max(-1), 0)
+                    w = np.exp(s - top[..., None])
+                    total = np.where(some[:, None], w.sum(-1), 1)
+                    w = w / total[..., None]
+                    rows, cols = slice(at, at + m), slice(h * grp, (h + 1) * grp)
+                    out[rows, cols] = rotate(w @ v, had_v)
+                    lse[rows, cols] = np.where(some[:, None], top + np.log(total), -np.inf)
+                    # a rounded query moves a score by eps sum |k q| at most, plus fp32 sums; weights move by twice
+                    # that (their own score and the total), are rounded once, and are summed in fp32
+                    count = seen.sum(1)[:, None]
+                    kq = np.where(seen[:, None], np.abs(qr[:, h]) @ np.abs(k).T, 0).max(-1)
+                    ds = (eps + (D + 16) * f32) * kq + 4 * f32 * np.where(np.isfinite(s), np.abs(s), 0).max(-1)
+                    rel = 2 * np.expm1(ds) + 2 * eps + (count + 64) * f32
+                    least = (count * 2.0**-33)[..., None] * np.where(used, vstep[slots, h], 0).max(0)
+                    tol[rows, cols] = spread_abs(rel[..., None] * (w @ np.abs(v)) + least, had_v) * (1 + 16 * f32) + 1e-30
+                    lse_tol[rows, cols] = ds + eps + (count + 64) * f32 + 4 * f32 * np.abs(np.where(some[:, None], lse[rows, cols], 0))
         at += m
     return out, lse, tol, lse_tol
 

@@ -27,7 +27,7 @@ def test_rotary_refusals():
     assert call(xs=(248, 256)) == INVALID  # tokens overlap
     assert call(xs=(260, 256)) == MISALIGNED
     assert call(x=(None, 1 << 21)) == INVALID and call(x=((1 << 20) + 8, 1 << 21)) == MISALIGNED
-    assert call(pos=None) == INVALID and call(freq=None) == INVALID and call(freq=P(4)) == MISALIGNED
+    assert call(pos=None) == INVALID and call(freq=None) == INVALID and call(freq=P(4)) == MISALIGNED and call(pos=P(4)) == MISALIGNED
     # overlaps: shifted, the other's input, two outputs; slices side by side and in place pass the check (n = 0 launches
     # nothing, so they are tried with the overlap of the next argument instead)
     assert call(y=((1 << 20) + 512, 1 << 23)) == INVALID
@@ -64,8 +64,8 @@ def test_attention_refusals():
     assert call(stride=504) == INVALID and call(stride=516) == MISALIGNED
     for name in ("q", "out", "pages", "q_start", "past", "ws"):
         assert call(**{name: None}) == (WORKSPACE if name == "ws" else INVALID), name
-        assert call(**{name: P(4100)}) == MISALIGNED, name
-    assert call(tree=P(8)) == MISALIGNED and call(lse=P(8)) == MISALIGNED
+        assert call(**{name: P(4098)}) == MISALIGNED, name  # index arrays: not aligned to their elements
+    assert call(tree=P(4)) == MISALIGNED and call(lse=P(8)) == MISALIGNED
     need = h.qwha_workspace_size(13, 4, 128, 2, 4, 1)
     assert need > 0 and call(nbytes=need - 1) == WORKSPACE
     assert call(out=P((1 << 20) + 1024)) == INVALID  # q and out overlap
@@ -86,7 +86,7 @@ def test_page_refusals():
     more = h.qwha_workspace_size(14, 4, 1, 32, 3, 0)
     assert more > need >= 4 * 32
     for kw, want in ((dict(page_size=0), INVALID), (dict(max_pages=-1), INVALID), (dict(n_seqs=-1), INVALID),
-                     (dict(n_pages=-1), INVALID), (dict(refs=None), INVALID), (dict(pages=4100), MISALIGNED),
+                     (dict(n_pages=-1), INVALID), (dict(refs=None), INVALID), (dict(pages=4098), MISALIGNED),
                      (dict(held=None), INVALID)):
         assert h.qwha_pages_resize(table(**kw), BUF, BUF, need, None) == want, kw
         assert h.qwha_pages_fork(table(**kw), BUF, BUF, 3, BUF, BUF, BUF, more, None) == want, kw
@@ -96,7 +96,7 @@ def test_page_refusals():
     assert h.qwha_pages_resize(table(n_seqs=0), None, None, 0, None) == OK
     assert h.qwha_pages_fork(table(), BUF, BUF, -1, BUF, BUF, BUF, more, None) == INVALID
     assert h.qwha_pages_fork(table(), BUF, None, 3, BUF, BUF, BUF, more, None) == INVALID
-    assert h.qwha_pages_fork(table(), BUF, BUF, 3, BUF, P(8), BUF, more, None) == MISALIGNED
+    assert h.qwha_pages_fork(table(), BUF, BUF, 3, BUF, P(6), BUF, more, None) == MISALIGNED
     assert h.qwha_pages_fork(table(), BUF, BUF, 3, BUF, BUF, BUF, more - 1, None) == WORKSPACE
     assert h.qwha_pages_fork(table(), None, None, 0, None, None, None, 0, None) == OK
 
@@ -119,7 +119,7 @@ def test_move_refusals():
     assert h.qwha_cache_copy_pages(None, 1, BUF, BUF, 3, None) == INVALID
     assert h.qwha_cache_copy_pages(c, 1, BUF, BUF, -1, None) == INVALID
     assert h.qwha_cache_copy_pages(c, 1, None, BUF, 3, None) == INVALID
-    assert h.qwha_cache_copy_pages(c, 1, BUF, P(4), 3, None) == MISALIGNED
+    assert h.qwha_cache_copy_pages(c, 1, BUF, P(6), 3, None) == MISALIGNED
     assert h.qwha_cache_copy_pages(c, 1, None, None, 0, None) == OK
     assert h.qwha_cache_compact(c, 3, BUF, 2, BUF, BUF, 4, 2, None) == INVALID
     assert h.qwha_cache_compact(c, 1, BUF, -1, BUF, BUF, 4, 2, None) == INVALID

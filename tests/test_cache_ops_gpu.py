@@ -137,8 +137,8 @@ class Setup:
     def ref(self):
         bits, bits_v, group, had_k, had_v = self.fmt
         eps = 2.0**-11 if self.dtype == "bf16" else 2.0**-21
-        return R.attention(self.qv, R.dense_pool(self.pk, bits, group), R.dense_pool(self.pv, bits_v, group), had_k, had_v,
-                           self.table, self.page_size, self.past, self.new, self.tree, self.scale, eps)
+        return R.attention(self.qv, R.dense_pool(self.pk, bits, group), R.dense_pool(self.pv, bits_v, group),
+                           R.largest_steps(self.pv, bits_v, group), had_k, had_v, self.table, self.page_size, self.past, self.new, self.tree, self.scale, eps)
 
     def check(self, out=None):
         got = host(self.run() if out is None else out)
@@ -576,11 +576,13 @@ def test_a_step_of_speculative_answering(dtype):
         for rows in (host(k), host(v)):
             c, s, z = quantize(rows.astype(np.float32), bits, 32, 64, dtype)
             stored.append(values(pack(c, bits), s, z, bits, 32))
-        kd, vd = [], []
+        stored.append(np.repeat(np.abs(s), 32, -1) * (2.0**bits - 1))
+        kd, vd, sd = [], [], []
         for b, m in enumerate(counts):
             for j in range(m):
-                tokens[b].append((stored[0][starts[b] + j], stored[1][starts[b] + j]))
-            kd.append([r[0] for r in tokens[b]]), vd.append([r[1] for r in tokens[b]])
+                tokens[b].append(tuple(part[starts[b] + j] for part in stored))
+            for part, held in enumerate((kd, vd, sd)):
+                held.append([r[part] for r in tokens[b]])
         flat = lambda l: np.array([r for s in l for r in s])  # noqa: E731
         lens = [len(s) for s in kd]
         order = np.zeros((len(counts), max(lens)), np.int64)  # page size 1: row after row
@@ -588,7 +590,7 @@ def test_a_step_of_speculative_answering(dtype):
         for b, m in enumerate(lens):
             order[b, :m] = np.arange(at, at + m)
             at += m
-        ref, _, tol, _ = R.attention(host(q), flat(kd), flat(vd), 64, 64, order, 1, [int(p) for p in pv[:len(counts)]], counts,
+        ref, _, tol, _ = R.attention(host(q), flat(kd), flat(vd), flat(sd), 64, 64, order, 1, [int(p) for p in pv[:len(counts)]], counts,
                                      tree, D**-0.5, 2.0**-11 if dtype == "bf16" else 2.0**-21)
         assert np.all(np.abs(host(out) - ref) <= tol + half_step(dtype) * np.abs(ref))
 

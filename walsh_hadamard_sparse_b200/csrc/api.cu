@@ -1067,14 +1067,23 @@ bool rows_apart(const void *x, int64_t xs, int64_t xw, const void *y, int64_t ys
   return off >= xw * esz && off + yw * esz <= step;
 }
 
+// Index arrays, which the kernels read one element at a time, need only the
+// alignment of their elements: rows of a table or parts of a batch are passed as
+// they lie.
+#define QWHA_CHECK_INDEX(p, name)                                                                                \
+  do {                                                                                                           \
+    if (!(p)) return fail(QWHA_ERR_INVALID_ARG, "%s is NULL", name);                                             \
+    if ((uintptr_t)(p) % sizeof(*(p))) return fail(QWHA_ERR_MISALIGNED, "%s is not aligned to its elements", name); \
+  } while (0)
+
 qwha_status check_table(const qwha_page_table *t) {
   if (!t) return fail(QWHA_ERR_INVALID_ARG, "the page table is NULL");
   if (t->page_size < 1 || t->max_pages < 0 || t->n_seqs < 0 || t->n_pages < 0)
     return fail(QWHA_ERR_INVALID_ARG, "page_size %d, max_pages %d, n_seqs %d, n_pages %d", t->page_size, t->max_pages,
                 t->n_seqs, t->n_pages);
-  if (t->n_pages > 0) QWHA_CHECK_PTR(t->refs, "refs");
-  if (t->n_seqs > 0 && t->max_pages > 0) QWHA_CHECK_PTR(t->pages, "pages");
-  if (t->n_seqs > 0) QWHA_CHECK_PTR(t->held, "held");
+  if (t->n_pages > 0) QWHA_CHECK_INDEX(t->refs, "refs");
+  if (t->n_seqs > 0 && t->max_pages > 0) QWHA_CHECK_INDEX(t->pages, "pages");
+  if (t->n_seqs > 0) QWHA_CHECK_INDEX(t->held, "held");
   return QWHA_OK;
 }
 
@@ -1131,8 +1140,8 @@ qwha_status qwha_rotary(qwha_dtype dt, int32_t n_x, const void *const *x, const 
     QWHA_CHECK_PTR(y[i], "y");
     r.x[i] = x[i], r.y[i] = y[i], r.x_stride[i] = x_stride[i], r.y_stride[i] = y_stride[i], r.heads[i] = heads[i];
   }
-  QWHA_CHECK_PTR(positions, "positions");
-  if (rot > 0) QWHA_CHECK_PTR(freq, "freq");
+  QWHA_CHECK_INDEX(positions, "positions");
+  if (rot > 0) QWHA_CHECK_INDEX(freq, "freq");
   for (int i = 0; i < n_x; ++i)
     for (int j = 0; j < n_x; ++j) {
       const int64_t xw = (int64_t)heads[i] * head_dim, yw = (int64_t)heads[j] * head_dim;
@@ -1171,10 +1180,10 @@ qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_
   if (n == 0 || n_seqs == 0) return QWHA_OK;
   QWHA_CHECK_PTR(q, "q");
   QWHA_CHECK_PTR(out, "out");
-  if (max_pages > 0) QWHA_CHECK_PTR(pages, "pages");
-  QWHA_CHECK_PTR(q_start, "q_start");
-  QWHA_CHECK_PTR(past, "past");
-  if (tree) QWHA_CHECK_PTR(tree, "tree");
+  if (max_pages > 0) QWHA_CHECK_INDEX(pages, "pages");
+  QWHA_CHECK_INDEX(q_start, "q_start");
+  QWHA_CHECK_INDEX(past, "past");
+  if (tree) QWHA_CHECK_INDEX(tree, "tree");
   if (lse) QWHA_CHECK_PTR(lse, "lse");
   if ((st = check_ws(ws, ws_bytes, attention_workspace(q_heads, k->head_dim, k->heads, n, dt == QWHA_F32))) != QWHA_OK)
     return st;
@@ -1190,6 +1199,8 @@ qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_
   a.q = q, a.q_stride = q_stride, a.n = n, a.q_heads = q_heads, a.grp = q_heads / k->heads;
   a.pages = pages, a.max_pages = max_pages;
   a.cap = (int)std::min<int64_t>((int64_t)max_pages * k->page_size, 1 << 30);
+  const int lg = ilog2(k->page_size);  // 2^lg >= page_size: the product of 31 and 32 bits is exact where it counts
+  a.page_shift = 31 + lg, a.page_mul = (unsigned int)(((1ull << a.page_shift) + k->page_size - 1) / k->page_size);
   a.q_start = q_start, a.past = past, a.n_seqs = n_seqs, a.tree = tree;
   a.scale2 = (float)(scale * 1.4426950408889634), a.out = out, a.lse = lse, a.f32 = dt == QWHA_F32;
   StageScope sc(ST_ATTENTION, attention_launches(), (cudaStream_t)stream);
@@ -1199,7 +1210,7 @@ qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_
 qwha_status qwha_pages_resize(const qwha_page_table *t, const int64_t *want, void *ws, size_t ws_bytes, void *stream) {
   qwha_status st = check_table(t);
   if (st != QWHA_OK || t->n_seqs == 0) return st;
-  QWHA_CHECK_PTR(want, "want");
+  QWHA_CHECK_INDEX(want, "want");
   if ((st = check_ws(ws, ws_bytes, pages_workspace(t->n_seqs, t->n_pages, 0))) != QWHA_OK) return st;
   StageScope sc(ST_PAGES, 1, (cudaStream_t)stream);
   return cuda_status(launch_pages_resize(*t, want, ws, (cudaStream_t)stream), "pages_resize");
@@ -1211,10 +1222,10 @@ qwha_status qwha_pages_fork(const qwha_page_table *t, const int64_t *src, const 
   if (st != QWHA_OK) return st;
   if (m < 0) return fail(QWHA_ERR_INVALID_ARG, "m %d", m);
   if (m == 0) return QWHA_OK;
-  QWHA_CHECK_PTR(src, "src");
-  QWHA_CHECK_PTR(dst, "dst");
-  QWHA_CHECK_PTR(from, "from");
-  QWHA_CHECK_PTR(to, "to");
+  QWHA_CHECK_INDEX(src, "src");
+  QWHA_CHECK_INDEX(dst, "dst");
+  QWHA_CHECK_INDEX(from, "from");
+  QWHA_CHECK_INDEX(to, "to");
   if ((st = check_ws(ws, ws_bytes, pages_workspace(t->n_seqs, t->n_pages, m))) != QWHA_OK) return st;
   StageScope sc(ST_PAGES, 1, (cudaStream_t)stream);
   return cuda_status(launch_pages_fork(*t, src, dst, m, from, to, ws, (cudaStream_t)stream), "pages_fork");
@@ -1226,8 +1237,8 @@ qwha_status qwha_cache_copy_pages(const qwha_cache *caches, int32_t n_caches, co
   if (st != QWHA_OK) return st;
   if (m < 0) return fail(QWHA_ERR_INVALID_ARG, "m %d", m);
   if (m == 0) return QWHA_OK;
-  QWHA_CHECK_PTR(from, "from");
-  QWHA_CHECK_PTR(to, "to");
+  QWHA_CHECK_INDEX(from, "from");
+  QWHA_CHECK_INDEX(to, "to");
   StageScope sc(ST_CACHE_MOVE, 1, (cudaStream_t)stream);
   return cuda_status(launch_copy_pages(moved_pair(caches, n_caches), n_caches, from, to, m, (cudaStream_t)stream),
                      "cache_copy_pages");
@@ -1240,9 +1251,9 @@ qwha_status qwha_cache_compact(const qwha_cache *caches, int32_t n_caches, const
   if (n_seqs < 0 || max_pages < 0 || width < 0)
     return fail(QWHA_ERR_INVALID_ARG, "n_seqs %d, max_pages %d, width %d", n_seqs, max_pages, width);
   if (n_seqs == 0 || width == 0) return QWHA_OK;
-  if (max_pages > 0) QWHA_CHECK_PTR(pages, "pages");
-  QWHA_CHECK_PTR(first, "first");
-  QWHA_CHECK_PTR(keep, "keep");
+  if (max_pages > 0) QWHA_CHECK_INDEX(pages, "pages");
+  QWHA_CHECK_INDEX(first, "first");
+  QWHA_CHECK_INDEX(keep, "keep");
   StageScope sc(ST_CACHE_MOVE, (int)cdiv(n_seqs, 65535), (cudaStream_t)stream);
   return cuda_status(launch_compact(moved_pair(caches, n_caches), n_caches, pages, max_pages, first, keep, width, n_seqs,
                                     (cudaStream_t)stream),

@@ -3,7 +3,7 @@
 
 #include <algorithm>
 
-#include "attention.cuh"
+#include "attention_mma.cuh"
 
 namespace qwha {
 namespace {
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kAnyThreads) attention_any_kernel(const AttnAr
   __shared__ int64_t slot_s[kAnyTokens];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Place at;
-  long long left = my_share<kAnyThreads>(a, &at);
+  long long left = my_share(a, &at);
   int4 begun = make_int4(0, 0, 0, 0), gone_on = begun;
   bool first = true;
   while (left > 0) {
@@ -172,8 +172,9 @@ __global__ void __launch_bounds__(kAnyThreads) attention_any_kernel(const AttnAr
 // ---------------------------------------------------------------- joining
 
 // The tile that CTA blockIdx.x of the kernel before began and left: its piece and
-// those of the CTAs that went on with it, a warp a row, in order.
-constexpr int kJoinThreads = 256;
+// those of the CTAs that went on with it, a warp a row, in order. Lanes look at 32
+// CTAs at once; the values are then read eight pieces at a time.
+constexpr int kJoinThreads = 256, kJoinAhead = 8;
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a) {
   __shared__ float x_s[kJoinThreads / 32][256];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -190,20 +191,48 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
   float m = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  for (int p = c; p < a.ctas; ++p) {
-    const int slot = p == c ? 2 * p + 1 : 2 * p;
-    const int flags = p == c ? 1 : a.part_desc[slot].w;
-    if (!(flags & 1)) continue;  // a CTA without units
-    const float pm = piece_stats(a, slot, rr)[0], pl = piece_stats(a, slot, rr)[1];
-    // NaN goes on as it is: fmaxf drops it, but the sum carries it
-    const float top = fmaxf(m, pm), base = top == -INFINITY ? 0.f : top;
-    const float f = exp2f(m - base), g = exp2f(pm - base);
-    const float *v = piece_values(a, slot, rr);
+  bool more = true;
+  for (int p0 = c; more && p0 < a.ctas; p0 += 32) {
+    const int p = p0 + lane, slot = p == c ? 2 * p + 1 : 2 * p;
+    const int flags = p == c ? 1 : p < a.ctas ? a.part_desc[slot].w : 0;  // 0: a CTA without units
+    const unsigned ends = __ballot_sync(~0u, flags & 2);
+    more = !ends;
+    const unsigned upto = ends ? (ends & -ends) * 2 - 1 : ~0u;
+    unsigned on = __ballot_sync(~0u, flags & 1) & upto;
+    const bool mine = on >> lane & 1;
+    const float pm = mine ? piece_stats(a, slot, rr)[0] : -INFINITY, pl = mine ? piece_stats(a, slot, rr)[1] : 0.f;
+    float top = fmaxf(m, pm);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane + 32 * i < D) acc[i] = acc[i] * f + v[lane + 32 * i] * g;
-    l = l * f + pl * g, m = top;
-    if (flags & 2) break;
+    for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    // a NaN is dropped from the maximum, but the sums carry it
+    const float base = top == -INFINITY ? 0.f : top, turn = exp2f(m - base), w = mine ? exp2f(pm - base) : 0.f;
+    float sum = mine ? pl * w : 0.f;
+#pragma unroll
+    for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
+    l = l * turn + sum, m = top;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] *= turn;
+    while (on) {
+      float v[kJoinAhead][8], wt[kJoinAhead];
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) {
+        wt[u] = 0.f;
+        const int q = on ? __ffs(on) - 1 : -1;
+        on &= on - 1;
+        const float f = __shfl_sync(~0u, w, q & 31);
+        const int from = __shfl_sync(~0u, slot, q & 31);
+        if (q < 0) continue;
+        wt[u] = f;
+        const float *src = piece_values(a, from, rr) + lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = lane + 32 * i < D ? src[32 * i] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u)
+        if (wt[u] != 0.f)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[u][i], wt[u], acc[i]);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -221,42 +250,98 @@ size_t any_smem(int D) {
 int attention_launches() { return 2; }
 
 namespace {
-constexpr int kMaxCtasPerSm = 4;
 
+constexpr size_t kSmemLimit = 227 * 1024, kSmemStatic = 8 * 1024;
+
+// How a call is cut and launched.
 struct Cut {
-  int ctas, part_rows;
+  int tq, gh, parts, hb, kt, least, ctas;
+  MmaLaunch mma;
+  int part_rows() const { return hb * tq * gh; }
 };
-Cut any_cut(int grp) {
-  const int gh = std::min(grp, kAnyRows);
-  return {sm_count() * 3, std::max(1, kAnyRows / gh) * gh};
+Cut cut_rows(int grp, int rows, int64_t n) {
+  Cut c = {};
+  c.parts = (int)cdiv(grp, rows), c.gh = (int)cdiv(grp, c.parts);
+  c.tq = (int)std::clamp<int64_t>(rows / c.gh, 1, n);
+  return c;
+}
+Cut any_cut(int grp, int64_t n) {
+  Cut c = cut_rows(grp, kAnyRows, n);
+  c.hb = 1, c.kt = kAnyTokens, c.least = 1, c.ctas = sm_count() * 3;
+  return c;
+}
+int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+Cut mma_cut(int D, int heads, int grp, int64_t n, int nt, int pieces, int bits_k, int bits_v, int group) {
+  Cut c = cut_rows(grp, 8 * nt, n);
+  const int dp = padded(D);
+  const MmaShape sh(D, dp, bits_k, bits_v, group, nt, pieces, heads);
+  for (int warps = kMmaWarps;; warps /= 2) {
+    c.hb = (int)cdiv(heads, cdiv(heads, warps));
+    c.mma.per_head = std::max(1, warps / c.hb), c.mma.warps = c.hb * c.mma.per_head;
+    c.mma.smem = (size_t)c.mma.warps * sh.ring + (size_t)c.hb * sh.q_bytes;
+    if (warps == 1 || c.mma.smem + kSmemStatic <= kSmemLimit) break;
+  }
+  // registers leave two CTAs of eight warps to an SM for tiles of one n-tile, else one
+  const int by_regs = (nt == 1 && dp <= 128 ? 2 : 1) * kMmaWarps / c.mma.warps;
+  const int by_smem = (int)(kSmemLimit / (c.mma.smem + kSmemStatic));
+  c.ctas = sm_count() * std::max(1, std::min(by_regs, by_smem));
+  c.mma.nt = nt, c.mma.ctas = c.ctas;
+  c.kt = kTokens * c.mma.per_head, c.least = 4;
+  return c;
 }
 size_t cut_bytes(const Cut &c, int D) {
-  return align_up((size_t)c.ctas * 2 * sizeof(int4), 256) + align_up((size_t)c.ctas * 2 * c.part_rows * 8, 256) +
-         align_up((size_t)c.ctas * 2 * c.part_rows * D * 4, 256);
+  return align_up((size_t)c.ctas * 2 * sizeof(int4), 256) + align_up((size_t)c.ctas * 2 * c.part_rows() * 8, 256) +
+         align_up((size_t)c.ctas * 2 * c.part_rows() * D * 4, 256);
 }
+
+// Whether the tensor-core kernels take a cache's codes: rows that four-byte copies
+// can fetch (3-bit rows lie as they may).
+bool takes_codes(const qwha_cache &c) { return c.bits == 3 || c.head_dim / 8 * c.bits % 4 == 0; }
+
 }  // namespace
 
 size_t attention_workspace(int32_t q_heads, int32_t head_dim, int32_t heads, int64_t n, bool f32) {
   if (heads <= 0 || q_heads % heads || n <= 0) return 0;
-  return cut_bytes(any_cut(q_heads / heads), head_dim);
+  const int grp = q_heads / heads;
+  size_t most = cut_bytes(any_cut(grp, n), head_dim);
+  // whatever the formats: fewer bits, more CTAs to an SM
+  for (int nt = 1; nt <= 4; nt *= 2)
+    for (int bits = 2; bits <= 8; ++bits)
+      most = std::max(most, cut_bytes(mma_cut(head_dim, heads, grp, n, nt, f32 ? 2 : 1, bits, bits, head_dim), head_dim));
+  return most;
 }
 
 cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
   static std::atomic<size_t> allowed[64];
   a.err = device_error_word();
   if (!a.err) return cudaErrorInvalidDevicePointer;
-  const Cut c = any_cut(a.grp);
-  a.gh = std::min(a.grp, kAnyRows), a.tq = std::max(1, kAnyRows / a.gh), a.parts = (int)cdiv(a.grp, a.gh);
-  a.hb = 1, a.blocks = a.k.heads * a.parts, a.kt = kAnyTokens, a.ctas = c.ctas, a.part_rows = c.part_rows;
+  const int D = a.k.head_dim;
+  const bool mma = takes_codes(a.k) && takes_codes(a.v) && a.k.group == a.v.group;
+  Cut c;
+  if (mma) {
+    const int64_t rows = cdiv(a.n, a.n_seqs) * a.grp;
+    const int nt = rows <= 8 ? 1 : rows <= 16 || D > 128 ? 2 : 4;
+    c = mma_cut(D, a.k.heads, a.grp, a.n, nt, a.f32 ? 2 : 1, a.k.bits, a.v.bits, a.k.group);
+  } else {
+    c = any_cut(a.grp, a.n);
+  }
+  a.tq = c.tq, a.gh = c.gh, a.parts = c.parts, a.hb = c.hb, a.kt = c.kt, a.least = c.least, a.ctas = c.ctas;
+  a.blocks = (int)cdiv(a.k.heads, a.hb) * a.parts, a.part_rows = c.part_rows();
   char *p = static_cast<char *>(ws);
-  a.part_desc = reinterpret_cast<int4 *>(p), p += align_up((size_t)c.ctas * 2 * sizeof(int4), 256);
-  a.part_stats = reinterpret_cast<float *>(p), p += align_up((size_t)c.ctas * 2 * c.part_rows * 8, 256);
+  a.part_desc = reinterpret_cast<int4 *>(p), p += align_up((size_t)a.ctas * 2 * sizeof(int4), 256);
+  a.part_stats = reinterpret_cast<float *>(p), p += align_up((size_t)a.ctas * 2 * a.part_rows * 8, 256);
   a.part = reinterpret_cast<float *>(p);
-  const size_t smem = any_smem(a.k.head_dim);
-  cudaError_t e = allow_smem(reinterpret_cast<const void *>(attention_any_kernel), smem, allowed);
+  cudaError_t e;
+  if (mma) {
+    e = D <= 64 ? launch_attention_d64(a, c.mma, s) : D <= 128 ? launch_attention_d128(a, c.mma, s) : launch_attention_d256(a, c.mma, s);
+  } else {
+    const size_t smem = any_smem(D);
+    e = allow_smem(reinterpret_cast<const void *>(attention_any_kernel), smem, allowed);
+    if (e != cudaSuccess) return e;
+    attention_any_kernel<<<a.ctas, kAnyThreads, smem, s>>>(a);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
-  attention_any_kernel<<<a.ctas, kAnyThreads, smem, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.ctas, (unsigned)cdiv(a.part_rows, kJoinThreads / 32)), cfg.blockDim = dim3(kJoinThreads), cfg.stream = s;
   cudaLaunchAttribute attr[1];

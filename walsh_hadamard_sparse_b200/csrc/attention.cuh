@@ -81,13 +81,13 @@ struct Place {
   int b, block, tile, unit;  // block: of heads and parts together
 };
 
-// A CTA's share of the units and where it begins. All threads of the CTA call it.
-template <int THREADS>
+// A CTA's share of the units and where it begins: `least` units or more, so that
+// little work is not cut into more pieces than it is worth. All threads of the
+// CTA (whole warps) call it.
 __device__ __forceinline__ long long my_share(const AttnArgs &a, Place *at) {
-  static_assert(THREADS % 32 == 0, "whole warps");
-  __shared__ long long warp_s[THREADS / 32];
+  __shared__ long long warp_s[32];
   __shared__ Place place_s;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, THREADS = blockDim.x;
   const long long blocks = a.blocks;
   long long all = 0, mine = 0;
   auto add_up = [&](int b0) {  // units of sequence b0 + thread, of those before it, of all of these
@@ -115,8 +115,11 @@ __device__ __forceinline__ long long my_share(const AttnArgs &a, Place *at) {
     add_up(b0);
     total += all;
   }
-  const long long u0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
-  const long long u1 = total / gridDim.x * (blockIdx.x + 1) + total % gridDim.x * (blockIdx.x + 1) / gridDim.x;
+  const long long most = (total + a.least - 1) / a.least;
+  const int ctas = most < gridDim.x ? (int)most : gridDim.x, c = blockIdx.x;
+  if (c >= ctas) return 0;
+  const long long u0 = total / ctas * c + total % ctas * c / ctas;
+  const long long u1 = total / ctas * (c + 1) + total % ctas * (c + 1) / ctas;
   if (u0 == u1) return 0;
   long long done = 0;
   for (int b0 = 0; b0 < a.n_seqs; b0 += THREADS) {
@@ -164,9 +167,13 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs &a, const Seq &s, int kv,
   return r;
 }
 
+__device__ __forceinline__ int page_of(const AttnArgs &a, int t) {
+  return (int)((unsigned long long)(unsigned int)t * a.page_mul >> a.page_shift);
+}
+
 // Slot of token t of sequence b, -1 (reported) where the table or the cache ends.
 __device__ __forceinline__ int64_t slot_of(const AttnArgs &a, int b, int t) {
-  const int pg = t / a.k.page_size;
+  const int pg = page_of(a, t);
   int64_t page = -1;
   if (pg < a.max_pages) page = a.pages[(int64_t)b * a.max_pages + pg];
   if (page >= 0 && page < a.k.n_pages) return page * a.k.page_size + (t - pg * a.k.page_size);

@@ -1,0 +1,12 @@
+// Attention over the quantized cache: heads of up to 64 channels.
+#include "attention_mma.cuh"
+
+namespace qwha {
+
+cudaError_t launch_attention_d64(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s) {
+  if (l.nt == 1) return attn::launch_mma_nt<64, 1>(a, l, s);
+  if (l.nt == 2) return attn::launch_mma_nt<64, 2>(a, l, s);
+  return attn::launch_mma_nt<64, 4>(a, l, s);
+}
+
+}  // namespace qwha

@@ -264,6 +264,8 @@ struct AttnArgs {
   const int32_t *pages;
   int max_pages;
   int cap;  // tokens the page table has room for
+  unsigned int page_mul;  // t / page_size = t page_mul >> page_shift for t below 2^31
+  int page_shift;
   const int64_t *q_start, *past;
   int n_seqs;
   const int64_t *tree;
@@ -276,6 +278,7 @@ struct AttnArgs {
   int tq, gh, parts;  // new tokens and query heads (of a cached head) of a tile; parts of the group
   int hb, blocks;     // cached heads of a CTA; blocks of heads times parts
   int kt;             // cached tokens of a unit
+  int least;          // units that are worth a CTA
   int ctas;
   // Pieces of tiles that are cut between CTAs.
   int part_rows;
@@ -285,5 +288,14 @@ struct AttnArgs {
 size_t attention_workspace(int32_t q_heads, int32_t head_dim, int32_t heads, int64_t n, bool f32);
 int attention_launches();
 cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s);
+// The tensor-core kernels (attention_mma.cuh): heads padded to 64, 128 or 256
+// channels, tiles of 8 nt rows. grid, warps and the cut are the caller's.
+struct MmaLaunch {
+  int nt, warps, per_head, ctas;
+  size_t smem;
+};
+cudaError_t launch_attention_d64(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s);
+cudaError_t launch_attention_d128(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s);
+cudaError_t launch_attention_d256(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s);
 
 }  // namespace qwha
