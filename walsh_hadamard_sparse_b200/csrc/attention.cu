@@ -64,8 +64,8 @@ __global__ void __launch_bounds__(kAnyThreads) attention_any_kernel(const AttnAr
       continue;
     }
     if (threadIdx.x == 0 && (long long)s.past + (a.tree && s.rows > 64 ? 64 : s.rows) > a.cap) atomicOr(a.err, kErrPage);
-    const int kv = at.block / a.parts, units = s.units(a, at.tile), length = s.length(a, at.tile);
-    const Rows rows = rows_of(a, s, kv, at.block % a.parts, at.tile);
+    const int kv = block_of(a, at.block), units = s.units(a, at.tile), length = s.length(a, at.tile);
+    const Rows rows = rows_of(a, s, kv, at.block - block_of(a, at.block) * a.parts, at.tile);
     const int run = left < units - at.unit ? (int)left : units - at.unit;
     __syncthreads();
     for (int r = warp; r < kAnyRows; r += kAnyThreads / 32) {
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
   if (!(begun.w & 1)) return;
   const int each = a.tq * a.gh, rr = blockIdx.y * (kJoinThreads / 32) + warp;
   if (rr >= a.part_rows) return;
-  const int kv = begun.y / a.parts * a.hb + rr / each, r = rr % each;
+  const int kv = block_of(a, begun.y) * a.hb + rr / each, r = rr % each;
   if (kv >= a.k.heads) return;
   const Seq s(a, begun.x);
   const Rows rows = rows_of(a, s, kv, begun.y % a.parts, begun.z);
@@ -251,11 +251,11 @@ int attention_launches() { return 2; }
 
 namespace {
 
-constexpr size_t kSmemLimit = 227 * 1024, kSmemStatic = 8 * 1024;
+constexpr size_t kSmemLimit = 227 * 1024, kSmemStatic = 9 * 1024;  // (static: 8.2 KB at most, and 1 KB of the system's)
 
 // How a call is cut and launched.
 struct Cut {
-  int tq, gh, parts, hb, kt, least, ctas;
+  int tq, gh, parts, hb, kt_log2, least_log2, ctas;
   MmaLaunch mma;
   int part_rows() const { return hb * tq * gh; }
 };
@@ -267,26 +267,25 @@ Cut cut_rows(int grp, int rows, int64_t n) {
 }
 Cut any_cut(int grp, int64_t n) {
   Cut c = cut_rows(grp, kAnyRows, n);
-  c.hb = 1, c.kt = kAnyTokens, c.least = 1, c.ctas = sm_count() * 3;
+  c.hb = 1, c.kt_log2 = ilog2(kAnyTokens), c.least_log2 = 0, c.ctas = sm_count() * 3;
   return c;
 }
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 Cut mma_cut(int D, int heads, int grp, int64_t n, int nt, int pieces, int bits_k, int bits_v, int group) {
   Cut c = cut_rows(grp, 8 * nt, n);
   const int dp = padded(D);
-  const MmaShape sh(D, dp, bits_k, bits_v, group, nt, pieces, heads);
   for (int warps = kMmaWarps;; warps /= 2) {
     c.hb = (int)cdiv(heads, cdiv(heads, warps));
     c.mma.per_head = std::max(1, warps / c.hb), c.mma.warps = c.hb * c.mma.per_head;
-    c.mma.smem = (size_t)c.mma.warps * sh.ring + (size_t)c.hb * sh.q_bytes;
+    c.mma.smem = MmaShape(D, dp, bits_k, bits_v, group, nt, pieces, heads, c.hb, c.mma.per_head, c.mma.warps).total;
     if (warps == 1 || c.mma.smem + kSmemStatic <= kSmemLimit) break;
   }
   // registers leave two CTAs of eight warps to an SM for tiles of one n-tile, else one
-  const int by_regs = (nt == 1 && dp <= 128 ? 2 : 1) * kMmaWarps / c.mma.warps;
+  const int by_regs = std::max(1, (nt == 1 && dp <= 128 ? 2 : 1) * kMmaWarps / c.mma.warps);
   const int by_smem = (int)(kSmemLimit / (c.mma.smem + kSmemStatic));
   c.ctas = sm_count() * std::max(1, std::min(by_regs, by_smem));
   c.mma.nt = nt, c.mma.ctas = c.ctas;
-  c.kt = kTokens * c.mma.per_head, c.least = 4;
+  c.kt_log2 = ilog2(kTokens * c.mma.per_head), c.least_log2 = 2;
   return c;
 }
 size_t cut_bytes(const Cut &c, int D) {
@@ -294,9 +293,9 @@ size_t cut_bytes(const Cut &c, int D) {
          align_up((size_t)c.ctas * 2 * c.part_rows() * D * 4, 256);
 }
 
-// Whether the tensor-core kernels take a cache's codes: rows that four-byte copies
-// can fetch (3-bit rows lie as they may).
-bool takes_codes(const qwha_cache &c) { return c.bits == 3 || c.head_dim / 8 * c.bits % 4 == 0; }
+// Whether the tensor-core kernels take a cache's codes: rows of whole words (3-bit
+// ones lie as they may).
+bool takes_codes(const qwha_cache &c) { return c.bits != 2 || c.head_dim % 16 == 0; }
 
 }  // namespace
 
@@ -316,7 +315,8 @@ cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
   a.err = device_error_word();
   if (!a.err) return cudaErrorInvalidDevicePointer;
   const int D = a.k.head_dim;
-  const bool mma = takes_codes(a.k) && takes_codes(a.v) && a.k.group == a.v.group;
+  // (slots in 32 bits: a cache of more has rows of a few bytes)
+  const bool mma = takes_codes(a.k) && takes_codes(a.v) && a.k.group == a.v.group && a.k.n_pages * a.k.page_size < (1LL << 31);
   Cut c;
   if (mma) {
     const int64_t rows = cdiv(a.n, a.n_seqs) * a.grp;
@@ -325,7 +325,7 @@ cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
   } else {
     c = any_cut(a.grp, a.n);
   }
-  a.tq = c.tq, a.gh = c.gh, a.parts = c.parts, a.hb = c.hb, a.kt = c.kt, a.least = c.least, a.ctas = c.ctas;
+  a.tq = c.tq, a.gh = c.gh, a.parts = c.parts, a.hb = c.hb, a.kt_log2 = c.kt_log2, a.least_log2 = c.least_log2, a.ctas = c.ctas;
   a.blocks = (int)cdiv(a.k.heads, a.hb) * a.parts, a.part_rows = c.part_rows();
   char *p = static_cast<char *>(ws);
   a.part_desc = reinterpret_cast<int4 *>(p), p += align_up((size_t)a.ctas * 2 * sizeof(int4), 256);

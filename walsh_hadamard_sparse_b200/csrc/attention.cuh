@@ -3,7 +3,7 @@
 //
 // The work of a call is the list of its units, in this order: sequence, block of
 // cached heads, part of their query heads, tile of the sequence's new tokens, run
-// of `kt` cached tokens. Its length follows from lengths that only the device
+// of 2^kt_log2 cached tokens. Its length follows from lengths that only the device
 // knows, so each CTA adds them up itself and takes an equal share of the units,
 // whatever sequences they belong to: one long sequence and many short ones fill
 // the GPU alike. A segment is what a CTA does of one tile of rows; a tile whose
@@ -38,7 +38,7 @@ struct Seq {
     const int fresh = a.tree && rows > 64 ? 64 : rows;
     flat = a.tree || (long long)past + fresh > a.cap;
     seen = (long long)past + fresh > a.cap ? a.cap : past + fresh;
-    tiles = (rows + a.tq - 1) / a.tq;
+    tiles = rows <= a.tq ? rows > 0 : (rows + a.tq - 1) / a.tq;
   }
   // units of one block of heads and part: sum over the tiles
   __device__ __forceinline__ long long per_block(const AttnArgs &a) const { return upto(a, tiles); }
@@ -52,7 +52,7 @@ struct Seq {
     return flat || end >= rows ? seen : past + (int)end;
   }
   __device__ __forceinline__ int units(const AttnArgs &a, int tile) const {
-    const int n = (length(a, tile) + a.kt - 1) / a.kt;
+    const int n = (length(a, tile) + (1 << a.kt_log2) - 1) >> a.kt_log2;
     return n > 0 ? n : 1;
   }
   // Units of the tiles before `tile`: sums of floor((tq i + c) / kt), by the
@@ -62,7 +62,7 @@ struct Seq {
     if (flat || tile == 1) return (long long)tile * units(a, 0);
     const bool all = tile == tiles;
     long long n = all ? tile - 1 : tile, sum = all ? units(a, tile - 1) : 0;
-    long long m = a.kt, s = a.tq, c = (long long)past + a.tq + a.kt - 1;
+    long long m = 1 << a.kt_log2, s = a.tq, c = (long long)past + a.tq + m - 1;
     for (;;) {
       sum += n * (n - 1) / 2 * (s / m) + n * (c / m);
       s %= m, c %= m;
@@ -76,12 +76,15 @@ struct Seq {
   }
 };
 
+// The quotient by the parts of a group, which is nearly always whole.
+__device__ __forceinline__ int block_of(const AttnArgs &a, int block) { return a.parts == 1 ? block : block / a.parts; }
+
 // Where a CTA is in the list.
 struct Place {
   int b, block, tile, unit;  // block: of heads and parts together
 };
 
-// A CTA's share of the units and where it begins: `least` units or more, so that
+// A CTA's share of the units and where it begins: 2^least_log2 units or more, so that
 // little work is not cut into more pieces than it is worth. All threads of the
 // CTA (whole warps) call it.
 __device__ __forceinline__ long long my_share(const AttnArgs &a, Place *at) {
@@ -115,11 +118,12 @@ __device__ __forceinline__ long long my_share(const AttnArgs &a, Place *at) {
     add_up(b0);
     total += all;
   }
-  const long long most = (total + a.least - 1) / a.least;
+  const long long most = (total + (1 << a.least_log2) - 1) >> a.least_log2;
   const int ctas = most < gridDim.x ? (int)most : gridDim.x, c = blockIdx.x;
   if (c >= ctas) return 0;
-  const long long u0 = total / ctas * c + total % ctas * c / ctas;
-  const long long u1 = total / ctas * (c + 1) + total % ctas * (c + 1) / ctas;
+  // (any function that grows with c and ends at total would do: no 64-bit division)
+  const double each = (double)total / ctas;
+  const long long u0 = (long long)(each * c), u1 = c + 1 == ctas ? total : (long long)(each * (c + 1));
   if (u0 == u1) return 0;
   long long done = 0;
   for (int b0 = 0; b0 < a.n_seqs; b0 += THREADS) {
@@ -130,7 +134,7 @@ __device__ __forceinline__ long long my_share(const AttnArgs &a, Place *at) {
       Place p;
       p.b = b0 + threadIdx.x;
       const long long each = s.per_block(a);
-      p.block = (int)(r / each);
+      p.block = r >> 32 | each >> 32 ? (int)(r / each) : (int)((unsigned int)r / (unsigned int)each);
       r -= p.block * each;
       int lo = 0, hi = s.tiles;
       while (hi - lo > 1) {
@@ -153,6 +157,7 @@ __device__ __forceinline__ long long my_share(const AttnArgs &a, Place *at) {
 struct Rows {
   int row0, j0, tokens, heads, head;  // row0: the sequence's first row of q
   int n;                              // tokens * heads
+  int all;                            // tokens of the sequence
   __device__ __forceinline__ int64_t q_row(int r) const { return row0 + j0 + r / heads; }
   __device__ __forceinline__ int q_head(int r) const { return head + r % heads; }
 };
@@ -163,7 +168,7 @@ __device__ __forceinline__ Rows rows_of(const AttnArgs &a, const Seq &s, int kv,
   r.tokens = s.rows - r.j0 < a.tq ? s.rows - r.j0 : a.tq;
   const int h0 = part * a.gh, h1 = h0 + a.gh < a.grp ? h0 + a.gh : a.grp;
   r.heads = h1 - h0, r.head = kv * a.grp + h0;
-  r.n = r.tokens * r.heads;
+  r.n = r.tokens * r.heads, r.all = s.rows;
   return r;
 }
 

@@ -12,12 +12,13 @@
 // scale (11 bits, scaled to the largest scale met): 2^-12 each against the 2^-9
 // of a bf16 output. fp32 calls carry both in two pieces, 22 bits.
 //
-// A warp has one cached head and every so-manieth run of 16 tokens, by itself: a
-// ring of stages that its own asynchronous copies fill, its own running maximum
-// and sums; warps of a CTA meet only at the ends of segments. With as many warps
-// as heads a CTA reads whole tokens, all heads of them, so the codes' 64-byte
-// rows and the 4-byte scales and single zero points of a token come from the same
-// sectors at about the same time.
+// A warp has one cached head and 16 tokens of each stage, with its own running
+// maximum and sums. The CTA's warps fill a ring of stages together with
+// asynchronous copies: whole tokens, the rows of all the CTA's heads, so that the
+// codes, the 4-byte scales and the single zero points of a token come in wide
+// pieces, a thread always of the same token of the stage. With fewer heads than
+// warps several warps share a head, and join their sums through shared memory at
+// the end of a segment.
 //
 // The maximum is not kept exactly: a tile raises it only where a score passes it
 // by 2^5, which a vote finds out; shuffles and the scaling of the sums are left
@@ -33,45 +34,70 @@
 namespace qwha {
 namespace attn {
 
-constexpr int kMmaWarps = 8;   // of a CTA, at most
-constexpr int kStages = 3;     // of a warp's ring
-constexpr int kTokens = 16;    // of a stage
+constexpr int kMmaWarps = 8;   // consumers of a CTA, at most
+constexpr int kStages = 4;     // of the ring
+constexpr int kTokens = 16;    // of a warp's part of a stage
 constexpr float kSlack = 5.f;  // by how much (base 2) a score may pass the maximum
 constexpr float kTop = 1024.f;  // p scale stays below this times 2^kSlack in f16
 constexpr float kNoScale = 1.329227995784916e36f;  // 2^120: no scale met yet
 
-// Sizes of a warp's stage and of a CTA's shared memory, in bytes.
-struct MmaShape {
-  int row_k, row_v;      // codes of a cached row
-  int pitch_k, pitch_v;  // of a token in a stage
-  int ng, words;         // groups of a head; words that cover their zero points
-  int k_at, v_at, ks_at, vs_at, kz_at, vz_at, off_at, live_at, stage;
-  int ring;              // of a warp: its stages, or a tile of its values
-  int q_bytes;           // of a head: the queries as operands
-  int fixed;             // zero points (and codes) begin at the same place of a word in every token
-  __host__ __device__ MmaShape() {}
-  __host__ __device__ static int pitch(int bytes, int bits) {
-    // rows of a quarter warp on distinct banks: 16-byte (8 bits: 32-byte) steps, an odd number of them
-    const int step = bits == 8 ? 32 : 16;
-    return ((bytes + step - 1) / step | 1) * step;
+// A head of one group, of groups of whole 64-channel blocks, of any groups.
+enum { kSingle, kBlocked, kMixed };
+
+// An array of the cache in a stage: `bytes` of each token, `stride` apart in memory
+// from `first` on, at `at` in the stage, `pitch` apart; fetched in pieces of `wide`
+// bytes. wide 0: a token's bytes begin anywhere in a word; the words that cover
+// them are fetched, and where they begin in the first is kept per token.
+struct Part {
+  int bytes, stride, at, pitch, wide, per;
+  __host__ __device__ void set(int bytes_, int stride_, int step, int *end, int tokens) {
+    bytes = bytes_, stride = stride_;
+    wide = (bytes | stride) % 16 == 0 ? 16 : (bytes | stride) % 8 == 0 ? 8 : (bytes | stride) % 4 == 0 ? 4 : 0;
+    per = wide ? bytes / wide : (bytes + 3 + 3) / 4;
+    const int room = wide ? bytes : per * 4;
+    // step: rows of a quarter warp on distinct banks (an odd number of steps apart)
+    pitch = step ? ((room + step - 1) / step | 1) * step : room;
+    at = *end;
+    *end = (at + tokens * pitch + 15) / 16 * 16;
   }
-  __host__ __device__ MmaShape(int D, int dp, int bits_k, int bits_v, int group, int nt, int pieces, int heads) {
-    row_k = D / 8 * bits_k, row_v = D / 8 * bits_v;
-    // (the words that cover a row of 3-bit codes may be one more than it fills)
-    pitch_k = pitch(dp / 8 * bits_k + (bits_k == 3 ? 4 : 0), bits_k);
-    pitch_v = pitch(dp / 8 * bits_v + (bits_v == 3 ? 4 : 0), bits_v);
-    ng = D / group, words = (ng + 3 + 3) / 4;
-    fixed = heads * ng % 4 == 0 && row_k % 4 == 0 && row_v % 4 == 0;
-    k_at = 0, v_at = k_at + kTokens * pitch_k;
-    ks_at = v_at + kTokens * pitch_v, vs_at = ks_at + kTokens * ng * 4;
-    kz_at = vs_at + kTokens * ng * 4, vz_at = kz_at + kTokens * words * 4;
-    off_at = vz_at + kTokens * words * 4;  // bytes: where zero points (and codes of 3 bits) begin in their first word
-    live_at = off_at + 2 * kTokens * 2;
-    stage = (live_at + 4 + 15) / 16 * 16;
-    const int values = 8 * (dp + 4) * 4;
-    ring = kStages * stage > values ? kStages * stage : values;
-    ring = (ring + 127) / 128 * 128;
+};
+
+// A CTA's stages and shared memory, in bytes.
+struct MmaShape {
+  Part codes[2], scales[2], zeros[2];  // keys, values
+  int row[2];                          // codes of a cached head's row
+  int ng;                              // groups of a head
+  int tokens;                          // of a stage
+  int off_at, live_at, stage;          // off: 4 bytes a token, where its zero points and codes begin in their words
+  int all_wide;                        // they begin at words in every token
+  int two;                             // two pieces of keys' and values' codes a thread
+  int fast;                            // codes in 16-byte pieces, a thread at most one piece of scales and zero points
+  int q_at, q_bytes;                   // queries as operands: after the ring; of a head
+  int join_at, total;                  // where warps that share a head join
+  __host__ __device__ MmaShape() {}
+  __host__ __device__ MmaShape(int D, int dp, int bits_k, int bits_v, int group, int nt, int pieces, int heads, int hb,
+                               int per_head, int warps) {
+    const int bits[2] = {bits_k, bits_v};
+    ng = D / group, tokens = kTokens * per_head;
+    int end = 0;
+    for (int i = 0; i < 2; ++i) {
+      row[i] = D / 8 * bits[i];
+      codes[i].set(hb * row[i], heads * row[i], bits[i] == 8 ? 32 : 16, &end, tokens);
+      end += 48;  // the last chunks of padded channels, and of 3 bits, are read past the row's end
+      end = (end + dp / 8 * bits[i] - row[i] + 15) / 16 * 16;
+    }
+    for (int i = 0; i < 2; ++i) scales[i].set(hb * ng * 4, heads * ng * 4, 0, &end, tokens);
+    for (int i = 0; i < 2; ++i) zeros[i].set(hb * ng, heads * ng, 0, &end, tokens);
+    all_wide = codes[0].wide && codes[1].wide && zeros[0].wide && zeros[1].wide;
+    two = hb > 0 && codes[0].per == 4 * hb && codes[1].per == 4 * hb;
+    fast = all_wide && codes[0].wide == 16 && codes[1].wide == 16 &&
+           scales[0].per + scales[1].per + zeros[0].per + zeros[1].per <= 2 * hb;
+    off_at = end, live_at = off_at + tokens * 4;
+    stage = (live_at + tokens + 15) / 16 * 16;
+    q_at = kStages * stage;
     q_bytes = nt * pieces * (dp / 32) * 32 * 16;
+    join_at = q_at + hb * q_bytes;
+    total = join_at + (per_head > 1 ? warps * 8 * (dp + 4) * 4 : 0);
   }
 };
 
@@ -107,6 +133,9 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   return d;
 }
 
+// 1 / x of a power of two
+__device__ __forceinline__ float inverse2(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
+
 template <int N>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
   if constexpr (N == 16)
@@ -118,51 +147,42 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
 __device__ __forceinline__ void copy_async_part(uint32_t dst, const void *src, int n) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
-// How the lanes of a warp fetch the rows of a stage's 16 tokens: pieces of 16, 8
-// or 4 bytes, dealt to the lanes in order. (3-bit rows that are no multiple of
-// four bytes: the words that cover them.)
-struct Pieces {
-  int tk, p, per, wide, step_t, step_p;
-  __device__ __forceinline__ Pieces(int bytes, int bits) {
-    wide = bits == 3 && bytes % 4 ? 0 : bytes % 16 == 0 ? 16 : bytes % 8 == 0 ? 8 : 4;
-    per = wide ? bytes / wide : bytes / 4 + 2;
-    const int lane = threadIdx.x & 31;
-    tk = lane / per, p = lane - tk * per;
-    step_t = 32 / per, step_p = 32 - step_t * per;
+// Fetches a token's bytes of one array: piece i and every `step`-th after it.
+// src: where the token's bytes begin; dst: its place in the stage.
+template <int N>
+__device__ __forceinline__ void fetch_wide(const Part &p, const char *src, uint32_t dst, int i, int step) {
+  for (; i < p.per; i += step) copy_async<N>(dst + i * N, src + i * N);
+}
+__device__ __forceinline__ void fetch(const Part &p, const char *src, const char *end, uint32_t dst, int i, int step) {
+  if (p.wide == 16) return fetch_wide<16>(p, src, dst, i, step);
+  if (p.wide == 8) return fetch_wide<8>(p, src, dst, i, step);
+  if (p.wide == 4) return fetch_wide<4>(p, src, dst, i, step);
+  src -= reinterpret_cast<uintptr_t>(src) & 3;
+  for (; i < p.per; i += step)
+    if (src + 4 * i < end) copy_async_part(dst + 4 * i, src + 4 * i, end - (src + 4 * i) < 4 ? (int)(end - (src + 4 * i)) : 4);
+}
+// All arrays of a token, whatever the format. Returns where zero points and codes
+// begin in their words. (Not inlined: the kernel's usual path is short.)
+static __device__ __noinline__ uint32_t fetch_any(const AttnArgs &a, const MmaShape &sh, uint32_t slot, int kv0, uint32_t to,
+                                           int token, int piece, int step) {
+  uint32_t off = 0;
+  const int64_t slots = a.k.n_pages * a.k.page_size;
+  for (int i = 0; i < 2; ++i) {
+    const qwha_cache &c = i ? a.v : a.k;
+    const char *codes = reinterpret_cast<const char *>(c.codes), *zeros = reinterpret_cast<const char *>(c.zeros);
+    const char *code_end = codes + slots * sh.codes[i].stride, *zero_end = zeros + slots * sh.zeros[i].stride;
+    codes += (int64_t)slot * sh.codes[i].stride + kv0 * sh.row[i];
+    zeros += (int64_t)slot * sh.zeros[i].stride + kv0 * sh.ng;
+    const char *scales = reinterpret_cast<const char *>(c.scales) + (int64_t)slot * sh.scales[i].stride + kv0 * sh.ng * 4;
+    fetch(sh.codes[i], codes, code_end, to + sh.codes[i].at + token * sh.codes[i].pitch, piece, step);
+    fetch(sh.scales[i], scales, nullptr, to + sh.scales[i].at + token * sh.scales[i].pitch, piece, step);
+    fetch(sh.zeros[i], zeros, zero_end, to + sh.zeros[i].at + token * sh.zeros[i].pitch, piece, step);
+    if (!sh.zeros[i].wide) off |= (uint32_t)(reinterpret_cast<uintptr_t>(zeros) & 3) << (8 * i);
+    if (!sh.codes[i].wide) off |= (uint32_t)(reinterpret_cast<uintptr_t>(codes) & 3) << (16 + 8 * i);
   }
-  template <int N>
-  __device__ __forceinline__ void copy_wide(const uint8_t *row, uint32_t live, int from, uint32_t to, int pitch) const {
-    int k = tk, q = p;
-    for (int x = 0; x < kTokens * per; x += 32) {
-      const uint8_t *r = reinterpret_cast<const uint8_t *>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(row), from + (k & 15)));
-      if (k < kTokens && live >> k & 1) copy_async<N>(to + k * pitch + q * N, r + q * N);
-      k += step_t, q += step_p;
-      if (q >= per) q -= per, ++k;
-    }
-  }
-  // row: the lane's token's codes; those of token 0 in lane `from`.
-  __device__ __forceinline__ void copy(const uint8_t *row, uint32_t live, int from, uint32_t to, int bytes, int pitch,
-                                       const qwha_cache &c) const {
-    if (wide == 16) return copy_wide<16>(row, live, from, to, pitch);
-    if (wide == 8) return copy_wide<8>(row, live, from, to, pitch);
-    if (wide == 4) return copy_wide<4>(row, live, from, to, pitch);
-    const uint8_t *end = c.codes + c.n_pages * c.page_size * c.heads * bytes;
-    int k = tk, q = p;
-    for (int x = 0; x < kTokens * per; x += 32) {
-      const uint8_t *r = reinterpret_cast<const uint8_t *>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(row), from + (k & 15)));
-      r = reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(r) & ~(uintptr_t)3) + 4 * q;
-      if (k < kTokens && live >> k & 1 && r < end) copy_async_part(to + k * pitch + 4 * q, r, end - r < 4 ? (int)(end - r) : 4);
-      k += step_t, q += step_p;
-      if (q >= per) q -= per, ++k;
-    }
-  }
-};
+  return off;
+}
 
 // Minus the zero points of a pair as the subtrahends of the forms that a field of
 // a half-word takes without a shift: 1024 + c, and with the field 2, 4 or 6 bits
@@ -170,9 +190,9 @@ struct Pieces {
 template <int BITS>
 struct Zero {
   uint32_t z[4];
-  // zz: 1024 + z, two f16
+  // zz: -(1024 + z), two f16
   __device__ __forceinline__ void set(uint32_t zz) {
-    z[0] = zz ^ 0x80008000u;
+    z[0] = zz;
     if constexpr (BITS == 4) z[1] = hadd2(z[0], 0x63806380u);  // - (64 + z): + 960
     if constexpr (BITS == 3) {
       z[1] = hadd2(z[0], 0x63006300u);  // - (128 + z): + 896
@@ -189,9 +209,13 @@ struct Zero {
 // Codes of eight channels as fields of two half-words, field i at bit BITS i: x.
 // The pair i (c - z) of both halves.
 template <int BITS>
-__device__ __forceinline__ void unpack4(uint32_t x, const Zero<BITS> &z, uint32_t *out) {
-  constexpr uint32_t kOne = 0x64006400u;
-  auto field = [&](uint32_t w, uint32_t mask) { return (w & mask) | kOne; };
+__device__ __forceinline__ void unpack4(uint32_t x, const Zero<BITS> &z, uint32_t one, uint32_t *out) {
+  // one: 0x64006400 in a register, so that mask and or are one instruction
+  auto field = [&](uint32_t w, uint32_t mask) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(one));
+    return d;
+  };
   if constexpr (BITS == 4) {
     out[0] = hadd2(field(x, 0x000f000fu), z.z[0]);
     out[1] = hfma2(field(x, 0x00f000f0u), 0x2c002c00u, z.z[1]);
@@ -210,8 +234,10 @@ __device__ __forceinline__ void unpack4(uint32_t x, const Zero<BITS> &z, uint32_
     out[3] = hadd2(field(x >> 9, 0x00070007u), z.z[0]);
   }
 }
-__device__ __forceinline__ uint32_t byte_pair(uint32_t a, uint32_t b, int i) {
-  return (__byte_perm(a, b, 0x4000 + 0x0400 + i * 0x1111) & 0x00ff00ffu) | 0x64006400u;
+__device__ __forceinline__ uint32_t byte_pair(uint32_t a, uint32_t b, int i, uint32_t one) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(__byte_perm(a, b, 0x4400 + i * 0x1111)), "r"(0x00ff00ffu), "r"(one));
+  return d;
 }
 
 // Eight codes of a row in shared memory: two words of which 8 bits use both.
@@ -227,133 +253,273 @@ __device__ __forceinline__ uint2 load_run(const char *row, int chunk, int mis) {
 
 // Channels of a row in the pairs (i, i + 4), i < 4: the first product's operand.
 template <int BITS>
-__device__ __forceinline__ void unpack_row(uint2 c, const Zero<BITS> &z, uint32_t *out) {
+__device__ __forceinline__ void unpack_row(uint2 c, const Zero<BITS> &z, uint32_t one, uint32_t *out) {
   if constexpr (BITS == 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = hadd2(byte_pair(c.x, c.y, i), z.z[0]);
+    for (int i = 0; i < 4; ++i) out[i] = hadd2(byte_pair(c.x, c.y, i, one), z.z[0]);
   } else {
     uint32_t x = c.x;
     if constexpr (BITS == 2) x = __byte_perm(x, 0, 0x4140);
     if constexpr (BITS == 3) x = (x & 0xfffu) | (x << 4 & 0x0fff0000u);
-    unpack4<BITS>(x, z, out);
+    unpack4<BITS>(x, z, one, out);
   }
 }
 // Tokens a and b side by side, channels 0..3 in out[0..3], 4..7 in out[4..7]: the
 // second product's operand.
 template <int BITS>
-__device__ __forceinline__ void unpack_columns(uint2 a, uint2 b, const Zero<BITS> &z, uint32_t *out) {
+__device__ __forceinline__ void unpack_columns(uint2 a, uint2 b, const Zero<BITS> &z, uint32_t one, uint32_t *out) {
   if constexpr (BITS == 8) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      out[i] = hadd2(byte_pair(a.x, b.x, i), z.z[0]);
-      out[4 + i] = hadd2(byte_pair(a.y, b.y, i), z.z[0]);
+      out[i] = hadd2(byte_pair(a.x, b.x, i, one), z.z[0]);
+      out[4 + i] = hadd2(byte_pair(a.y, b.y, i, one), z.z[0]);
     }
   } else if constexpr (BITS == 4) {
-    unpack4<4>(__byte_perm(a.x, b.x, 0x5410), z, out);
-    unpack4<4>(__byte_perm(a.x, b.x, 0x7632), z, out + 4);
+    unpack4<4>(__byte_perm(a.x, b.x, 0x5410), z, one, out);
+    unpack4<4>(__byte_perm(a.x, b.x, 0x7632), z, one, out + 4);
   } else if constexpr (BITS == 2) {
     const uint32_t x = __byte_perm(a.x, b.x, 0x5410);
-    unpack4<2>(x, z, out);
-    unpack4<2>(x >> 8, z, out + 4);
+    unpack4<2>(x, z, one, out);
+    unpack4<2>(x >> 8, z, one, out + 4);
   } else {
-    unpack4<3>((a.x & 0xfffu) | (b.x << 16 & 0x0fff0000u), z, out);
-    unpack4<3>((a.x >> 12 & 0xfffu) | (b.x << 4 & 0x0fff0000u), z, out + 4);
+    unpack4<3>((a.x & 0xfffu) | (b.x << 16 & 0x0fff0000u), z, one, out);
+    unpack4<3>((a.x >> 12 & 0xfffu) | (b.x << 4 & 0x0fff0000u), z, one, out + 4);
   }
 }
 
-// The largest |s| of the warp as bits (finite ones; zero if none).
-__device__ __forceinline__ uint32_t warp_max_bits(uint32_t v) { return __reduce_max_sync(~0u, v); }
+// x H (blocks of had) for rows that lie over L lanes, eight consecutive channels
+// each.
+template <int L>
+__device__ __forceinline__ void rotate_lanes(float *v, int had, float unit, int lane) {
+  if (had < 2) return;
+  auto inside = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & h)) {
+        const float x = v[i], y = v[i + h];
+        v[i] = x + y, v[i + h] = x - y;
+      }
+  };
+  inside(1);
+  if (had >= 4) inside(2);
+  if (had >= 8) inside(4);
+#pragma unroll
+  for (int o = 1; o < L; o *= 2)
+    if (had > 8 * o) {
+      const float sign = lane & o ? -1.f : 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], sign, __shfl_xor_sync(~0u, v[i], o));
+    }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= unit;
+}
 
-template <int DP, int NT, int PIECES, bool MIXED>
+template <int DP, int NT, int PIECES, int GROUPS>
 __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
-    attention_mma_kernel(const AttnArgs a, const MmaShape sh, int per_head) {
+    attention_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ MmaShape sh, int per_head, uint32_t one) {
   extern __shared__ __align__(128) char smem[];
   constexpr int kSteps = DP / 32, kBlocks = DP / 64;
-  constexpr bool kKeepQ = NT == 1 && kSteps * PIECES <= 8;
-  __shared__ float c_s[kMmaWarps][32];                       // factor of the scales of each group
+  constexpr bool MIXED = GROUPS == kMixed;
+  __shared__ float c_s[kMmaWarps][32];                              // factor of the scales of each group
   __shared__ float m_s[kMmaWarps][8 * NT], l_s[kMmaWarps][8 * NT];  // of each warp's rows
-  __shared__ float f_s[kMmaWarps][8 * NT];                   // by head: factor of a row's scores
-  __shared__ uint8_t group_s[32];                            // of a chunk of eight channels
+  __shared__ float f_s[kMmaWarps][8 * NT];                          // by head: factor of a row's scores
+  __shared__ Rows rows_s[kMmaWarps];                                // kept out of the loop's registers
+  __shared__ uint8_t group_s[32];                                   // of a chunk of eight channels
   __shared__ int lim_s[kMmaWarps][8 * NT];
   __shared__ unsigned long long bits_s[kMmaWarps][8 * NT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int warps = blockDim.x >> 5;
-  const int hl = warp / per_head, sub = warp - hl * per_head;  // head of the block; place among its warps
-  char *ring = smem + warp * sh.ring;
-  char *q_at = smem + warps * sh.ring + hl * sh.q_bytes;
-  const int D = a.k.head_dim, ng = sh.ng, group = a.k.group;
-  const uint32_t ring_u = (uint32_t)__cvta_generic_to_shared(ring);
-
+  const int warps = blockDim.x >> 5, ng = sh.ng, group = a.k.group, D = a.k.head_dim;
+  if (MIXED && threadIdx.x < 32) group_s[threadIdx.x] = (uint8_t)min(8 * (int)threadIdx.x / group, ng - 1);
   Place at;
   long long left = my_share(a, &at);
-  int4 begun = make_int4(0, 0, 0, 0), gone_on = begun;
-  bool first = true;
-  const bool upper = lane >> 4;
-  const qwha_cache own = upper ? a.v : a.k;
-  const int own_bytes = upper ? sh.row_v : sh.row_k;
-  const int64_t slots = a.k.n_pages * a.k.page_size, zeros_end = slots * a.k.heads * ng;
-  const Pieces pieces_k(sh.row_k, a.k.bits), pieces_v(sh.row_v, a.v.bits);
-  if (MIXED && threadIdx.x < 32) group_s[threadIdx.x] = (uint8_t)min(8 * (int)threadIdx.x / group, ng - 1);
+  __syncthreads();
+  const int kt = 1 << a.kt_log2;
+  const int hl = per_head == 1 ? warp : warp / per_head, sub = warp - hl * per_head;  // head of the block; place among its warps
+  char *q_at = smem + sh.q_at + hl * sh.q_bytes;
+  auto meet = [&] {  // the warps that share a head
+    if (per_head > 1) __syncthreads();
+    else __syncwarp();
+  };
+  if (threadIdx.x == 0) a.part_desc[2 * blockIdx.x] = a.part_desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+  // what the thread fetches: of one token of each stage, every fetch_step-th piece
+  const int fetch_step = 2 * a.hb, fetch_token = threadIdx.x / fetch_step, fetch_piece = threadIdx.x - fetch_token * fetch_step;
+  const uint32_t slots = (uint32_t)(a.k.n_pages * a.k.page_size);
+  const uint32_t smem_u = (uint32_t)__cvta_generic_to_shared(smem);
+  // its piece of scales or zero points, where each has one at most
+  const char *small = nullptr;
+  uint32_t small_stride = 0, small_to = 0;
+  int small_wide = 0, small_head = 0;
+  if (sh.fast) {
+    int p = fetch_piece;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Part &x = i < 2 ? sh.scales[i] : sh.zeros[i - 2];
+      const qwha_cache &c = i & 1 ? a.v : a.k;
+      if (p >= 0 && p < x.per) {
+        small = (i < 2 ? reinterpret_cast<const char *>(c.scales) : reinterpret_cast<const char *>(c.zeros)) + p * x.wide;
+        small_stride = x.stride, small_to = x.at + fetch_token * x.pitch + p * x.wide, small_wide = x.wide;
+        small_head = i < 2 ? ng * 4 : ng;
+      }
+      p = p < 0 ? p : p - x.per;
+    }
+  }
+  const uint32_t k_to = sh.codes[0].at + fetch_token * sh.codes[0].pitch + fetch_piece * 16;
+  const uint32_t v_to = sh.codes[1].at + fetch_token * sh.codes[1].pitch + fetch_piece * 16;
+  // the lane's tokens and head in a stage's parts
+  const int k_row = sh.codes[0].at + (16 * sub + g) * sh.codes[0].pitch + hl * sh.row[0];
+  const int k_scale = sh.scales[0].at + (16 * sub + g) * sh.scales[0].pitch + hl * ng * 4;
+  const int v_scale = sh.scales[1].at + (16 * sub + g) * sh.scales[1].pitch + hl * ng * 4;
+  const int k_zero = sh.zeros[0].at + (16 * sub + g) * sh.zeros[0].pitch + hl * ng;
+  const int v_row = sh.codes[1].at + (16 * sub + 2 * t) * sh.codes[1].pitch + hl * sh.row[1];
+  const int v_zero = sh.zeros[1].at + (16 * sub + 2 * t) * sh.zeros[1].pitch + hl * ng;
   while (left > 0) {
     const Seq s(a, at.b);
     if (s.rows == 0) {
       ++at.b;
       continue;
     }
+    const int units = s.units(a, at.tile), past = s.past;
     if (threadIdx.x == 0 && (long long)s.past + (a.tree && s.rows > 64 ? 64 : s.rows) > a.cap) atomicOr(a.err, kErrPage);
-    const int units = s.units(a, at.tile), length = s.length(a, at.tile);
-    const int block = at.block / a.parts, kv = block * a.hb + hl;
+    const int length = s.length(a, at.tile), block = block_of(a, at.block), kv0 = block * a.hb, kv = kv0 + hl;
     const bool mine = kv < a.k.heads;  // (the last block may have fewer heads)
-    const Rows rows = rows_of(a, s, kv, at.block % a.parts, at.tile);
+    Rows rows = rows_of(a, s, mine ? kv : 0, at.block - block * a.parts, at.tile);
     const int run = left < units - at.unit ? (int)left : units - at.unit;
-    const int t_lo = at.unit * a.kt, t_hi = min(length, (at.unit + run) * a.kt);
 
-    // ---- queries as operands: row r of the head by the warps of the head in turn
-    __syncthreads();  // the last segment's values are read
-    if (mine) {
-      float *x = reinterpret_cast<float *>(ring);
-      for (int r = sub; r < 8 * NT; r += per_head) {
-        __syncwarp();
-        float top = 0.f;
-        for (int d = lane; d < DP; d += 32) x[d] = 0.f;
-        __syncwarp();
-        if (r < rows.n) {
-          warp_query(a, x, rows.q_row(r), rows.q_head(r));
-          for (int d = lane; d < D; d += 32) top = fmaxf(top, fabsf(x[d]));
+    // ---- the ring: stage j of the segment holds the tokens from (at.unit + j) kt on
+    const int32_t *table = a.pages + (int64_t)at.b * a.max_pages;
+    int fetch_t = at.unit * kt + fetch_token;
+    const char *k_from = reinterpret_cast<const char *>(a.k.codes) + kv0 * sh.row[0] + fetch_piece * 16;
+    const char *v_from = reinterpret_cast<const char *>(a.v.codes) + kv0 * sh.row[1] + fetch_piece * 16;
+    const char *small_from = small + kv0 * small_head;
+    // the page of token t, which is within the table, since lengths are cut there; and its place in the page
+    auto page_at = [&](int t, int *in) -> int {
+      const int pg = page_of(a, t);
+      *in = t - pg * a.k.page_size;
+      return t < length ? table[pg] : -2;
+    };
+    int fill_at = 0;
+    auto fill = [&](int page, int in) {
+      const bool on = (uint32_t)page < (uint32_t)a.k.n_pages;
+      if (page != -2 && !on) atomicOr(a.err, kErrPage);
+      const uint32_t slot = (uint32_t)page * (uint32_t)a.k.page_size + (uint32_t)in, to = smem_u + fill_at;
+      uint32_t off = 0;
+      if (on && sh.fast) {
+        const char *src = k_from + (uint64_t)slot * (uint32_t)sh.codes[0].stride;
+        uint32_t dst = to + k_to;
+        if (sh.two) {  // the usual sizes: two pieces of each
+          copy_async<16>(dst, src), copy_async<16>(dst + 16 * fetch_step, src + 16 * fetch_step);
+          src = v_from + (uint64_t)slot * (uint32_t)sh.codes[1].stride, dst = to + v_to;
+          copy_async<16>(dst, src), copy_async<16>(dst + 16 * fetch_step, src + 16 * fetch_step);
+        } else {
+          for (int p = fetch_piece; p < sh.codes[0].per; p += fetch_step, src += 16 * fetch_step, dst += 16 * fetch_step) copy_async<16>(dst, src);
+          src = v_from + (uint64_t)slot * (uint32_t)sh.codes[1].stride, dst = to + v_to;
+          for (int p = fetch_piece; p < sh.codes[1].per; p += fetch_step, src += 16 * fetch_step, dst += 16 * fetch_step) copy_async<16>(dst, src);
         }
-        const uint32_t bits = warp_max_bits(__float_as_uint(top));
-        // 2^15 / 2^ceil: exact, the row's largest comes to lie in [2^14, 2^15]; infinities stay what they are
-        int e = (int)(bits >> 23) - 127 + 1;
-        e = bits == 0 || bits >= 0x7f800000u ? 0 : e < -100 ? -100 : e;
-        const float up = __uint_as_float((uint32_t)(127 + 15 - e) << 23);
-        uint4 *dst = reinterpret_cast<uint4 *>(q_at);
-        if (lane < DP / 8) {  // chunk lane = 4 step + t of row r: operand lane (r & 7, t)
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = x[lane * 8 + i] * up;
-          const int to = ((r >> 3) * kSteps + (lane >> 2)) * PIECES * 32 + (r & 7) * 4 + (lane & 3);
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = pair16(v[i], v[i + 4]);
-          dst[to] = make_uint4(w[0], w[1], w[2], w[3]);
-          if constexpr (PIECES == 2) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 h = wide16(w[i]);
-              w[i] = pair16(v[i] - h.x, v[i + 4] - h.y);
-            }
-            dst[to + 32] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+        if (small_wide) {
+          src = small_from + (uint64_t)slot * small_stride, dst = to + small_to;
+          if (small_wide == 16) copy_async<16>(dst, src);
+          else if (small_wide == 8) copy_async<8>(dst, src);
+          else copy_async<4>(dst, src);
         }
-        if (lane == 0) {
-          f_s[hl][r] = 1.f / up;
-          const int j = rows.j0 + (r < rows.n ? r / rows.heads : 0);
-          lim_s[hl][r] = r >= rows.n ? 0 : a.tree ? s.past : s.past + j + 1;
-          bits_s[hl][r] = r < rows.n && a.tree ? (unsigned long long)a.tree[s.row0 + j] : 0;
-        }
+      } else if (on) {
+        off = fetch_any(a, sh, slot, kv0, to, fetch_token, fetch_piece, fetch_step);
+      } else {  // codes and zero points are finite whatever they are; scales have to be
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          for (int x = fetch_piece; x < a.hb * ng; x += fetch_step)
+            reinterpret_cast<float *>(smem + fill_at + sh.scales[i].at + fetch_token * sh.scales[i].pitch)[x] = 0.f;
+      }
+      if (fetch_piece == 0) {
+        if (!sh.all_wide) *reinterpret_cast<uint32_t *>(smem + fill_at + sh.off_at + fetch_token * 4) = off;
+        smem[fill_at + sh.live_at + fetch_token] = on;
+      }
+      fill_at = fill_at + sh.stage == kStages * sh.stage ? 0 : fill_at + sh.stage;
+    };
+    int pages[kStages], ins[kStages];  // of the token's next stages, on their way while the ones before are filled
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) pages[i] = page_at(fetch_t + i * kt, &ins[i]);
+    fetch_t += kStages * kt;  // of the stage after these
+    __syncthreads();  // the last segment's stages are read
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (i < run) fill(pages[i], ins[i]);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int next_page = pages[kStages - 1], next_in = ins[kStages - 1];
+
+    // ---- queries as operands: rows of a head by its warps in turn, 32 / L at once
+    constexpr int L = DP / 8, kAtOnce = 32 / L;
+    meet();  // the last segment's queries and masks are read
+    constexpr int kPasses = 8 * NT / kAtOnce < 4 ? 8 * NT / kAtOnce : 4;  // whose loads are under way together
+    const int c = lane % L;                                                // chunk of eight channels
+#pragma unroll 1
+    for (int p0 = 0; p0 * kAtOnce * per_head < 8 * NT; p0 += kPasses) {
+    uint4 raw[kPasses][2];
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int r = ((p0 + p) * per_head + sub) * kAtOnce + lane / L;
+      raw[p][0] = raw[p][1] = make_uint4(0, 0, 0, 0);
+      if (r < rows.n && c * 8 < D) {
+        const int64_t from = rows.q_row(r) * a.q_stride + (int64_t)rows.q_head(r) * D + c * 8;
+        const uint4 *src = a.f32 ? reinterpret_cast<const uint4 *>(static_cast<const float *>(a.q) + from)
+                                 : reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + from);
+        raw[p][0] = __ldg(src);
+        if (a.f32) raw[p][1] = __ldg(src + 1);
       }
     }
-    __syncthreads();
+#pragma unroll 1
+    for (int p = 0; p < kPasses; ++p) {
+      const int r = ((p0 + p) * per_head + sub) * kAtOnce + lane / L;
+      uint4 x = raw[0][0], y = raw[0][1];
+#pragma unroll
+      for (int i = 1; i < kPasses; ++i)
+        if (p == i) x = raw[i][0], y = raw[i][1];
+      const int r_first = ((p0 + p) * per_head + sub) * kAtOnce;
+      if (r_first >= 8 * NT) break;
+      uint4 *dst = reinterpret_cast<uint4 *>(q_at) + ((r >> 3) * kSteps + (c >> 2)) * PIECES * 32 + (r & 7) * 4 + (c & 3);
+      if (r_first >= rows.n) {  // rows that the tile does not have
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) dst[32 * i] = make_uint4(0, 0, 0, 0);
+        if (c == 0) f_s[hl][r] = 1.f, lim_s[hl][r] = 0, bits_s[hl][r] = 0;
+        continue;
+      }
+      float v[8];
+      if (a.f32) io<float>::unpack(x, v), io<float>::unpack(y, v + 4);
+      else io<__nv_bfloat16>::unpack(x, v);
+      rotate_lanes<L>(v, a.k.had_block, a.unit_k, lane);
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= a.scale2, top = fmaxf(top, fabsf(v[i]));
+#pragma unroll
+      for (int o = 1; o < L; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      // 2^15 / 2^ceil: exact, the row's largest comes to lie in [2^14, 2^15]; infinities stay what they are
+      const uint32_t bits = __float_as_uint(top);
+      int e = (int)(bits >> 23) - 127 + 1;
+      e = bits == 0 || bits >= 0x7f800000u ? 0 : e < -100 ? -100 : e;
+      const float up = __uint_as_float((uint32_t)(127 + 15 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= up;
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pair16(v[i], v[i + 4]);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      if constexpr (PIECES == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 h = wide16(w[i]);
+          w[i] = pair16(v[i] - h.x, v[i + 4] - h.y);
+        }
+        dst[32] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (c == 0) {
+        f_s[hl][r] = __uint_as_float((uint32_t)(127 - 15 + e) << 23);  // 1 / up
+        const int j = rows.j0 + (r < rows.n ? r / rows.heads : 0);
+        lim_s[hl][r] = r >= rows.n ? 0 : a.tree ? s.past : s.past + j + 1;
+        bits_s[hl][r] = r < rows.n && a.tree ? (unsigned long long)a.tree[s.row0 + j] : 0;
+      }
+    }
+    }
+    meet();
 
     float acc[kBlocks][4][NT][4], m[NT][2], l[NT][2], f[NT][2], thr[NT][2];
 #pragma unroll
@@ -372,394 +538,433 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[b][i][n][e] = 0.f;
     c_s[warp][lane] = kNoScale;
+    __syncwarp();
     const uint4 *q_op = reinterpret_cast<const uint4 *>(q_at) + lane;
-    uint4 q_keep[kKeepQ ? kSteps * PIECES : 1];
-    if constexpr (kKeepQ) {
-#pragma unroll
-      for (int i = 0; i < kSteps * PIECES; ++i) q_keep[i] = q_op[i * 32];
-    }
-    const int z_in = kv * ng & 3;  // where a token's zero points begin in their first word, if it is the same for all
-    const int safe = a.tree ? s.past : s.past + rows.j0 + 1;  // every row sees the tokens below
+    const int safe = a.tree ? past : past + rows.j0 + 1;  // every row sees the tokens below
+    int t0 = at.unit * kt + 16 * sub, use_at = 0;
+    __syncwarp();
+    if (lane == 0) rows_s[warp] = rows;
 
-    // ---- the warp's runs of 16 tokens
-    const int stride = per_head * kTokens, t_first = t_lo + sub * kTokens;
-    const int tiles = mine && t_first < t_hi ? (t_hi - t_first + stride - 1) / stride : 0;
-    const int32_t *table = a.pages + (int64_t)at.b * a.max_pages;
-    auto look_up = [&](int i) -> int64_t {  // slot of the lane's token (lanes 16.. again) of tile i
-      const int tok = t_first + i * stride + (lane & 15);
-      if (i >= tiles || tok >= t_hi) return -1;
-      const int pg = page_of(a, tok);  // within the table, since lengths are cut there
-      return (int64_t)table[pg] * a.k.page_size + (tok - pg * a.k.page_size);  // pages outside: sorted out when used
-    };
-    int fill = 0;  // the stage that is filled next
-    auto issue = [&](int i, int64_t slot) {
-      const uint32_t st = ring_u + fill;
-      fill = fill + sh.stage == kStages * sh.stage ? 0 : fill + sh.stage;
-      if (i < tiles) {
-        const int tok = t_first + i * stride + (lane & 15);
-        bool on = tok < t_hi;
-        if (on && (slot < 0 || slot >= slots)) {
-          atomicOr(a.err, kErrPage);
-          on = false;
-        }
-        const int64_t row = slot * a.k.heads + kv;
-        const uint32_t live = __ballot_sync(~0u, on) & 0xffffu;
-        // keys by the lower lanes, values by the upper: each has its token's row
-        const uint8_t *mine_codes = own.codes + row * own_bytes;
-        pieces_k.copy(mine_codes, live, 0, st + sh.k_at, sh.row_k, sh.pitch_k, a.k);
-        pieces_v.copy(mine_codes, live, 16, st + sh.v_at, sh.row_v, sh.pitch_v, a.v);
-        const uint32_t s_to = st + (upper ? sh.vs_at : sh.ks_at) + (lane & 15) * 4;
-        char *off = ring + (st - ring_u) + sh.off_at + lane * 2;
-        if (on) {
-          const int64_t z = row * ng;
-          for (int x = 0; x < ng; ++x) copy_async<4>(s_to + x * kTokens * 4, own.scales + z + x);
-          const uint32_t z_to = st + (upper ? sh.vz_at : sh.kz_at) + (lane & 15) * sh.words * 4;
-          const int in = (int)z & 3;
-          for (int w = -in; w < ng; w += 4) {
-            const int64_t rest = zeros_end - (z + w);
-            copy_async_part(z_to + w + in, own.zeros + z + w, rest < 4 ? (int)rest : 4);
-          }
-          if (!sh.fixed) off[0] = (char)in, off[1] = (char)(own.bits == 3 ? row * own_bytes & 3 : 0);
-        } else {
-          for (int x = 0; x < ng; ++x) *reinterpret_cast<float *>(ring + (s_to - ring_u) + x * kTokens * 4) = 0.f;
-          if (!sh.fixed) off[0] = off[1] = 0;
-        }
-        if (lane == 0) *reinterpret_cast<uint32_t *>(ring + (st - ring_u) + sh.live_at) = live;
+#pragma unroll 1
+    for (int u = 0; u < run; ++u, t0 += kt) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncthreads();  // stage u has landed, and all have read stage u - 1
+      const char *st = smem + use_at;
+      use_at = use_at + sh.stage == kStages * sh.stage ? 0 : use_at + sh.stage;
+      if (u + kStages - 1 < run) {
+        const int page = next_page, in = next_in;
+        next_page = page_at(fetch_t, &next_in);
+        fetch_t += kt;
+        fill(page, in);
       }
-      copy_commit();
-    };
-    int use = 0;  // the stage that is used next
-    int64_t slot = look_up(0);
-#pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) {
-      const int64_t next = look_up(i + 1);
-      issue(i, slot);
-      slot = next;
-    }
-#pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-      copy_wait<kStages - 2>();
-      __syncwarp();
-      const int64_t next = look_up(i + kStages);
-      issue(i + kStages - 1, slot);
-      slot = next;
-      const char *st = ring + use;
-      use = use + sh.stage == kStages * sh.stage ? 0 : use + sh.stage;
-      const int t0 = t_first + i * stride;
-      const uint32_t live = *reinterpret_cast<const uint32_t *>(st + sh.live_at);
-      const uint8_t *off = reinterpret_cast<const uint8_t *>(st) + sh.off_at;
-      const float *ks = reinterpret_cast<const float *>(st + sh.ks_at);
-      const float *vs = reinterpret_cast<const float *>(st + sh.vs_at);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (t0 < length && mine) {
+        // a byte a token: whether it is there
+        const uint32_t live = __ballot_sync(~0u, st[sh.live_at + 16 * sub + (lane & 15)]) & 0xffffu;
+        const uint8_t *off = reinterpret_cast<const uint8_t *>(st) + sh.off_at + 64 * sub;  // of the warp's tokens
 
-      // ---- scores of tokens g, g + 8 for queries 2 t, 2 t + 1 of each tile
-      float sc[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
-      auto scores = [&](auto bits) {
-        constexpr int B = decltype(bits)::value;
-        float part[NT][4];
+        // ---- scores of tokens g, g + 8 for queries 2 t, 2 t + 1 of each tile
+        float sc[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) part[n][e] = 0.f;
-        const uint8_t *z0 = reinterpret_cast<const uint8_t *>(st + sh.kz_at) + g * sh.words * 4, *z1 = z0 + 8 * sh.words * 4;
-        int mis0 = 0, mis1 = 0;
-        if (sh.fixed) {
-          z0 += z_in, z1 += z_in;
-        } else {
-          z0 += off[2 * g], z1 += off[2 * (g + 8)];
-          if (B == 3) mis0 = off[2 * g + 1], mis1 = off[2 * (g + 8) + 1];
-        }
-        const char *r0 = st + sh.k_at + g * sh.pitch_k, *r1 = r0 + 8 * sh.pitch_k;
-        int gr = 0, edge = group;  // the group of the running sums, and where it ends
-        Zero<B> za, zb;
-        auto zeros = [&](int x) {
-          za.set((z0[x] | 0x6400u) * 0x10001u), zb.set((z1[x] | 0x6400u) * 0x10001u);
-        };
-        if (!MIXED) zeros(0);
+          for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+        auto scores = [&](auto bits) {
+          constexpr int B = decltype(bits)::value;
+          float part[NT][4];
 #pragma unroll
-        for (int step = 0; step < kSteps; ++step) {
-          const int chunk = 4 * step + t;
-          const int lane_group = MIXED ? group_s[chunk] : 0;
-          if (MIXED) zeros(lane_group);
-          uint32_t x[4], y[4];
-          unpack_row<B>(load_run<B>(r0, chunk, mis0), za, x);
-          unpack_row<B>(load_run<B>(r1, chunk, mis1), zb, y);
-          const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
-          for (;;) {  // once, where a step lies in one group
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int p = 0; p < PIECES; ++p) {
-                uint4 q;
-                if constexpr (kKeepQ) q = q_keep[step * PIECES + p];
-                else q = q_op[((n * kSteps + step) * PIECES + p) * 32];
-                if (MIXED && lane_group != gr) q = make_uint4(0, 0, 0, 0);
-                mma16816(part[n], a0, q.x, q.y);
-                mma16816(part[n], a1, q.z, q.w);
-              }
-            const bool last = step + 1 == kSteps;
-            if (edge > 32 * (step + 1) && !last) break;
-            const float s0 = ks[gr * kTokens + g], s1 = ks[gr * kTokens + g + 8];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              sc[n][0] = fmaf(part[n][0], s0, sc[n][0]), sc[n][1] = fmaf(part[n][1], s0, sc[n][1]);
-              sc[n][2] = fmaf(part[n][2], s1, sc[n][2]), sc[n][3] = fmaf(part[n][3], s1, sc[n][3]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) part[n][e] = 0.f;
-            }
-            if (gr + 1 == ng) break;
-            ++gr;
-            const bool more = edge < 32 * (step + 1);
-            edge += group;
-            if (!MIXED) zeros(gr);
-            if (!MIXED || !more) break;
+            for (int e = 0; e < 4; ++e) part[n][e] = 0.f;
+          const char *r0 = st + k_row, *r1 = r0 + 8 * sh.codes[0].pitch;
+          const uint8_t *z0 = reinterpret_cast<const uint8_t *>(st) + k_zero, *z1 = z0 + 8 * sh.zeros[0].pitch;
+          const float *s0 = reinterpret_cast<const float *>(st + k_scale);
+          const float *s1 = reinterpret_cast<const float *>(st + k_scale + 8 * sh.scales[0].pitch);
+          int mis0 = 0, mis1 = 0;
+          if (!sh.zeros[0].wide) z0 += off[4 * g], z1 += off[4 * g + 32];
+          if (B == 3 && !sh.codes[0].wide) {
+            mis0 = (int)((off[4 * g + 2] + reinterpret_cast<uintptr_t>(r0)) & 3), r0 += off[4 * g + 2] - mis0;
+            mis1 = (int)((off[4 * g + 34] + reinterpret_cast<uintptr_t>(r1)) & 3), r1 += off[4 * g + 34] - mis1;
+          } else if (B == 3) {
+            mis0 = (int)(reinterpret_cast<uintptr_t>(r0) & 3), r0 -= mis0;
+            mis1 = (int)(reinterpret_cast<uintptr_t>(r1) & 3), r1 -= mis1;
           }
+          int gr = 0, edge = group;  // the group of the running sums, and where it ends
+          Zero<B> za, zb;
+          auto zeros = [&](int x) {
+            za.set((z0[x] | 0xe400u) * 0x10001u), zb.set((z1[x] | 0xe400u) * 0x10001u);
+          };
+          if (!MIXED) zeros(0);
+#pragma unroll
+          for (int step = 0; step < kSteps; ++step) {
+            const int chunk = 4 * step + t;
+            const int lane_group = MIXED ? group_s[chunk] : 0;
+            if (MIXED) zeros(lane_group);
+            uint32_t x[4], y[4];
+            unpack_row<B>(load_run<B>(r0, chunk, mis0), za, one, x);
+            unpack_row<B>(load_run<B>(r1, chunk, mis1), zb, one, y);
+            const uint32_t a0[4] = {x[0], y[0], x[1], y[1]}, a1[4] = {x[2], y[2], x[3], y[3]};
+            for (;;) {  // once, where a step lies in one group
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p) {
+                  uint4 q = q_op[((n * kSteps + step) * PIECES + p) * 32];
+                  if (MIXED && lane_group != gr) q = make_uint4(0, 0, 0, 0);
+                  mma16816(part[n], a0, q.x, q.y);
+                  mma16816(part[n], a1, q.z, q.w);
+                }
+              const bool last = step + 1 == kSteps;
+              if (GROUPS == kSingle ? !last : edge > 32 * (step + 1) && !last) break;
+              const float f0 = s0[gr], f1 = s1[gr];
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                sc[n][0] = fmaf(part[n][0], f0, sc[n][0]), sc[n][1] = fmaf(part[n][1], f0, sc[n][1]);
+                sc[n][2] = fmaf(part[n][2], f1, sc[n][2]), sc[n][3] = fmaf(part[n][3], f1, sc[n][3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) part[n][e] = 0.f;
+              }
+              if (GROUPS == kSingle || gr + 1 == ng) break;
+              ++gr;
+              const bool more = edge < 32 * (step + 1);
+              edge += group;
+              if (!MIXED) zeros(gr);
+              if (!MIXED || !more) break;
+            }
+          }
+        };
+        switch (a.k.bits) {
+          case 2: scores(std::integral_constant<int, 2>()); break;
+          case 3: scores(std::integral_constant<int, 3>()); break;
+          case 4: scores(std::integral_constant<int, 4>()); break;
+          default: scores(std::integral_constant<int, 8>());
         }
-      };
-      switch (a.k.bits) {
-        case 2: scores(std::integral_constant<int, 2>()); break;
-        case 3: scores(std::integral_constant<int, 3>()); break;
-        case 4: scores(std::integral_constant<int, 4>()); break;
-        default: scores(std::integral_constant<int, 8>());
-      }
 
-      // ---- masks
-      const bool masked = live != 0xffffu || t0 + kTokens > safe;
-      bool any0 = true, any1 = true;  // whether any row sees token g, g + 8
-      if (masked) {
-        any0 = any1 = false;
+        // ---- masks
+        const bool masked = live != 0xffffu || t0 + kTokens > safe;
+        bool any0 = true, any1 = true;  // whether any row sees token g, g + 8
+        if (masked) {
+          any0 = any1 = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = 8 * n + 2 * t + (e & 1), tl = g + (e >> 1) * 8, tok = t0 + tl, w = tok - past;
+              const bool on = (live >> tl & 1) && (tok < lim_s[hl][r] || (w >= 0 && w < 64 && (bits_s[hl][r] >> w & 1)));
+              if (!on) sc[n][e] = -INFINITY;
+              (e >> 1 ? any1 : any0) |= on;
+            }
+          const unsigned b0 = __ballot_sync(~0u, any0), b1 = __ballot_sync(~0u, any1);
+          any0 = b0 >> (4 * g) & 15u, any1 = b1 >> (4 * g) & 15u;
+        }
+
+        // ---- the maximum, where a score has passed it by 2^kSlack
+        bool passed = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) passed |= sc[n][e] > thr[n][e & 1];
+        if (__any_sync(~0u, passed)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float top = fmaxf(sc[n][i], sc[n][i + 2]);
+#pragma unroll
+              for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+              const float now = fmaxf(m[n][i], top * f[n][i]);
+              const float turn = now == -INFINITY ? 1.f : exp2_fast(m[n][i] - now);
+              m[n][i] = now;
+              thr[n][i] = (now + kSlack) * inverse2(f[n][i]);
+              l[n][i] *= turn;
+#pragma unroll
+              for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[b][k][n][i] *= turn, acc[b][k][n][i + 2] *= turn;
+            }
+        }
+        // ---- weights
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = 8 * n + 2 * t + (e & 1), tl = g + (e >> 1) * 8, tok = t0 + tl, u = tok - s.past;
-            const bool on = (live >> tl & 1) && (tok < lim_s[hl][r] || (u >= 0 && u < 64 && (bits_s[hl][r] >> u & 1)));
-            if (!on) sc[n][e] = -INFINITY;
-            (e >> 1 ? any1 : any0) |= on;
+            const float base = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
+            sc[n][e] = exp2_fast(fmaf(sc[n][e], f[n][e & 1], -base));
+            l[n][e & 1] += sc[n][e];
           }
-        unsigned b0 = __ballot_sync(~0u, any0), b1 = __ballot_sync(~0u, any1);
-        any0 = b0 >> (4 * g) & 15u, any1 = b1 >> (4 * g) & 15u;
-      }
 
-      // ---- the maximum, where a score has passed it by 2^kSlack
-      bool passed = false;
+        // ---- values: channels 64 b + 8 g + i and + 4, tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+        auto add_values = [&](auto bits) {
+          constexpr int B = decltype(bits)::value;
+          uint32_t w[NT][PIECES][2];  // weights times scales of the group, as operands
+          auto weights = [&](int gr) {
+            float s0 = reinterpret_cast<const float *>(st + v_scale)[gr];
+            float s1 = reinterpret_cast<const float *>(st + v_scale + 8 * sh.scales[1].pitch)[gr];
+            if (masked) s0 = any0 ? s0 : 0.f, s1 = any1 ? s1 : 0.f;
+            float c = c_s[warp][gr];
+            if (__any_sync(~0u, fabsf(s0) * c > kTop || fabsf(s1) * c > kTop)) {
+              // a scale above all before it: twice its power of two. Infinities stay what they are
+              const float x0 = fabsf(s0), x1 = fabsf(s1);
+              const uint32_t top = __reduce_max_sync(~0u, max(x0 < INFINITY ? __float_as_uint(x0) : 0u, x1 < INFINITY ? __float_as_uint(x1) : 0u));
+              int e = 127 + 10 - ((int)(top >> 23) - 127 + 2);
+              e = e < 1 ? 1 : e > 247 ? 247 : e;
+              const float now = fminf(c, __uint_as_float((uint32_t)e << 23)), turn = now * inverse2(c);
+              c = now;
+              __syncwarp();
+              if (lane == 0) c_s[warp][gr] = now;
+              __syncwarp();
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+              for (int b = 0; b < kBlocks; ++b)
+                if (GROUPS == kSingle || min(8 * (8 * b + g) / group, ng - 1) == gr)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) passed |= sc[n][e] > thr[n][e & 1];
-      if (__any_sync(~0u, passed)) {
+                  for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float top = fmaxf(sc[n][i], sc[n][i + 2]);
+                      for (int x = 0; x < 4; ++x) acc[b][k][n][x] *= turn;
+            }
+            s0 *= c, s1 *= c;
 #pragma unroll
-            for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-            const float now = fmaxf(m[n][i], top * f[n][i]);
-            const float turn = now == -INFINITY ? 1.f : exp2_fast(m[n][i] - now);
-            m[n][i] = now;
-            thr[n][i] = (now + kSlack) / f[n][i];
-            l[n][i] *= turn;
+            for (int n = 0; n < NT; ++n) {
+              float v[4] = {sc[n][0] * s0, sc[n][1] * s0, sc[n][2] * s1, sc[n][3] * s1};
+              if (masked)
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
+                for (int e = 0; e < 4; ++e) v[e] = sc[n][e] == 0.f ? 0.f : v[e];  // the scale may be a NaN
 #pragma unroll
-              for (int k = 0; k < 4; ++k) acc[b][k][n][i] *= turn, acc[b][k][n][i + 2] *= turn;
+              for (int p = 0; p < PIECES; ++p) {
+                const uint32_t lo = pair16(v[0], v[1]), hi = pair16(v[2], v[3]);
+                w[n][p][0] = turn8x8(lo), w[n][p][1] = turn8x8(hi);
+                if (p + 1 < PIECES) {
+                  const float2 h0 = wide16(lo), h1 = wide16(hi);
+                  v[0] -= h0.x, v[1] -= h0.y, v[2] -= h1.x, v[3] -= h1.y;
+                }
+              }
+            }
+          };
+          const char *r[4];
+          const uint8_t *z[4];
+          int mis[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int tk = (k & 1) + (k >> 1) * 8;
+            r[k] = st + v_row + tk * sh.codes[1].pitch;
+            z[k] = reinterpret_cast<const uint8_t *>(st) + v_zero + tk * sh.zeros[1].pitch;
+            const uint8_t *o = off + 4 * (2 * t + tk);
+            if (!sh.zeros[1].wide) z[k] += o[1];
+            mis[k] = 0;
+            if (B == 3) {
+              if (!sh.codes[1].wide) r[k] += o[3];
+              mis[k] = (int)(reinterpret_cast<uintptr_t>(r[k]) & 3), r[k] -= mis[k];
+            }
           }
-      }
-      // ---- weights
+          int have = -1, v_group = 0, v_edge = group;
+          Zero<B> za, zb;
+          auto zeros = [&](int x) {
+            za.set(z[0][x] | (uint32_t)z[1][x] << 16 | 0xe400e400u);
+            zb.set(z[2][x] | (uint32_t)z[3][x] << 16 | 0xe400e400u);
+          };
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+          for (int b = 0; b < kBlocks; ++b) {
+            const int chunk = 8 * b + g;
+            if (GROUPS == kBlocked && b > 0 && 64 * b == v_edge) ++v_group, v_edge += group;
+            const int lane_group = MIXED ? group_s[chunk] : v_group;
+            if (MIXED || (GROUPS == kSingle ? b == 0 : lane_group != have)) zeros(lane_group);
+            uint32_t x[8], y[8];
+            unpack_columns<B>(load_run<B>(r[0], chunk, mis[0]), load_run<B>(r[1], chunk, mis[1]), za, one, x);
+            unpack_columns<B>(load_run<B>(r[2], chunk, mis[2]), load_run<B>(r[3], chunk, mis[3]), zb, one, y);
+            const int g0 = MIXED ? group_s[8 * b] : lane_group, g1 = MIXED ? group_s[8 * b + 7] : lane_group;
+            for (int gr = g0; gr <= g1; ++gr) {
+              if (MIXED || (GROUPS == kSingle ? b == 0 : gr != have)) weights(gr), have = gr;
+              const uint32_t keep = !MIXED || lane_group == gr ? ~0u : 0u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float base = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
-          sc[n][e] = exp2_fast(fmaf(sc[n][e], f[n][e & 1], -base));
-          l[n][e & 1] += sc[n][e];
-        }
-
-      // ---- values: channels 64 b + 8 g + i and + 4, tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-      auto add_values = [&](auto bits) {
-        constexpr int B = decltype(bits)::value;
-        uint32_t w[NT][PIECES][2];  // weights times scales of the group, as operands
-        auto weights = [&](int gr) {
-          float s0 = vs[gr * kTokens + g], s1 = vs[gr * kTokens + g + 8];
-          if (masked) s0 = any0 ? s0 : 0.f, s1 = any1 ? s1 : 0.f;
-          float c = c_s[warp][gr];
-          const float x0 = fabsf(s0), x1 = fabsf(s1);
-          const bool far0 = x0 * c > kTop && x0 < INFINITY, far1 = x1 * c > kTop && x1 < INFINITY;
-          if (__any_sync(~0u, far0 || far1)) {  // a scale above all before it: twice its power of two
-            const uint32_t top = warp_max_bits(max(far0 ? __float_as_uint(x0) : 0u, far1 ? __float_as_uint(x1) : 0u));
-            int e = 127 + 10 - ((int)(top >> 23) - 127 + 2);
-            e = e < 1 ? 1 : e > 247 ? 247 : e;
-            const float now = __uint_as_float((uint32_t)e << 23), turn = now / c;
-            c = now;
-            __syncwarp();
-            if (lane == 0) c_s[warp][gr] = now;
-            __syncwarp();
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t op[4] = {x[k] & keep, x[k + 4] & keep, y[k] & keep, y[k + 4] & keep};
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-              if (min(8 * (8 * b + g) / group, ng - 1) == gr)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                  for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) acc[b][k][n][x] *= turn;
-          }
-          s0 *= c, s1 *= c;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float v[4] = {sc[n][0] * s0, sc[n][1] * s0, sc[n][2] * s1, sc[n][3] * s1};
-            if (masked)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = sc[n][e] == 0.f ? 0.f : v[e];  // the scale may be a NaN
-#pragma unroll
-            for (int p = 0; p < PIECES; ++p) {
-              const uint32_t lo = pair16(v[0], v[1]), hi = pair16(v[2], v[3]);
-              w[n][p][0] = turn8x8(lo), w[n][p][1] = turn8x8(hi);
-              if (p + 1 < PIECES) {
-                const float2 a0 = wide16(lo), a1 = wide16(hi);
-                v[0] -= a0.x, v[1] -= a0.y, v[2] -= a1.x, v[3] -= a1.y;
+                  for (int p = 0; p < PIECES; ++p) mma16816(acc[b][k][n], op, w[n][p][0], w[n][p][1]);
               }
             }
           }
         };
-        const char *r[4];
-        const uint8_t *z[4];
-        int mis[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int tk = 2 * t + (k & 1) + (k >> 1) * 8;
-          r[k] = st + sh.v_at + tk * sh.pitch_v;
-          z[k] = reinterpret_cast<const uint8_t *>(st + sh.vz_at) + tk * sh.words * 4 + (sh.fixed ? z_in : off[2 * (16 + tk)]);
-          mis[k] = B == 3 && !sh.fixed ? off[2 * (16 + tk) + 1] : 0;
+        switch (a.v.bits) {
+          case 2: add_values(std::integral_constant<int, 2>()); break;
+          case 3: add_values(std::integral_constant<int, 3>()); break;
+          case 4: add_values(std::integral_constant<int, 4>()); break;
+          default: add_values(std::integral_constant<int, 8>());
         }
-        int have = -1, v_group = 0, v_edge = group;
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          const int chunk = 8 * b + g;
-          if (b > 0 && 64 * b == v_edge && v_group + 1 < ng) ++v_group, v_edge += group;
-          const int lane_group = MIXED ? group_s[chunk] : v_group;
-          Zero<B> za, zb;
-          za.set(z[0][lane_group] | (uint32_t)z[1][lane_group] << 16 | 0x64006400u);
-          zb.set(z[2][lane_group] | (uint32_t)z[3][lane_group] << 16 | 0x64006400u);
-          uint32_t x[8], y[8];
-          unpack_columns<B>(load_run<B>(r[0], chunk, mis[0]), load_run<B>(r[1], chunk, mis[1]), za, x);
-          unpack_columns<B>(load_run<B>(r[2], chunk, mis[2]), load_run<B>(r[3], chunk, mis[3]), zb, y);
-          const int g0 = MIXED ? group_s[8 * b] : lane_group, g1 = MIXED ? group_s[8 * b + 7] : lane_group;
-          for (int gr = g0; gr <= g1; ++gr) {
-            if (MIXED || gr != have) weights(gr), have = gr;
-            const uint32_t keep = !MIXED || lane_group == gr ? ~0u : 0u;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t op[4] = {x[k] & keep, x[k + 4] & keep, y[k] & keep, y[k + 4] & keep};
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int p = 0; p < PIECES; ++p) mma16816(acc[b][k][n], op, w[n][p][0], w[n][p][1]);
-            }
-          }
-        }
-      };
-      switch (a.v.bits) {
-        case 2: add_values(std::integral_constant<int, 2>()); break;
-        case 3: add_values(std::integral_constant<int, 3>()); break;
-        case 4: add_values(std::integral_constant<int, 4>()); break;
-        default: add_values(std::integral_constant<int, 8>());
       }
-      __syncwarp();  // the stage is read
     }
-    copy_wait<0>();
 
-    // ---- the warp's sums, and those of a head's warps together
+    // ---- the rows' sums: of the warp, then of the warps that share the head
+    __syncwarp();
+    rows = rows_s[warp];
     const bool starts = at.unit == 0, ends = at.unit + run == units;
     const int slot_out = 2 * blockIdx.x + (starts ? 1 : 0);
+    float back[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) back[b] = inverse2(c_s[warp][GROUPS == kSingle ? 0 : min(8 * (8 * b + g) / group, ng - 1)]);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int o = 4; o < 32; o *= 2) l[n][i] += __shfl_xor_sync(~0u, l[n][i], o);
-        if (g == 0) m_s[warp][8 * n + 2 * t + i] = m[n][i], l_s[warp][8 * n + 2 * t + i] = l[n][i];
+    // eight channels 64 b + 8 g .. of query 2 t + i
+    auto chunk_of = [&](int b, int n, int i, float *v) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = acc[b][k][n][i] * back[b], v[k + 4] = acc[b][k][n][i + 2] * back[b];
+    };
+    auto store_piece = [&](int r, int c0, const float *v, float mm, float ll) {
+      const int rr = hl * a.tq * a.gh + r;
+      if (c0 < D) {
+        float4 *dst = reinterpret_cast<float4 *>(piece_values(a, slot_out, rr) + c0);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]), dst[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
-    float *x = reinterpret_cast<float *>(ring);
-    constexpr int kPitch = DP + 4;
+      if (c0 == 0) piece_stats(a, slot_out, rr)[0] = mm, piece_stats(a, slot_out, rr)[1] = ll;
+    };
+    if (per_head == 1) {
+      if (mine) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      __syncthreads();
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        const int c0 = 64 * b + 8 * g;
-        const float back = 1.f / c_s[warp][min(c0 / group, ng - 1)];
+          for (int i = 0; i < 2; ++i) {
+            const int r = 8 * n + 2 * t + i;
+            float v[kBlocks][8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+            for (int b = 0; b < kBlocks; ++b) chunk_of(b, n, i, v[b]);
+            if (starts && ends) {
+              const float inv = l[n][i] == 0.f ? 0.f : 1.f / l[n][i];
+              // H: channels' bits 0..2 within a chunk, 3..5 over the lanes g, 6 and 7 over the blocks
+              const int had = a.v.had_block;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[(2 * t + (e & 1)) * kPitch + c0 + k + 4 * (e >> 1)] = acc[b][k][n][e] * back;
+              for (int b = 0; b < kBlocks; ++b) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[b][k] *= inv;
+                rotate_lanes<1>(v[b], had, a.unit_v, 0);
+#pragma unroll
+                for (int o = 1; o < 8; o *= 2)
+                  if (had > 8 * o) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                      v[b][k] = fmaf(v[b][k], g & o ? -1.f : 1.f, __shfl_xor_sync(~0u, v[b][k], 4 * o));
+                  }
+              }
+#pragma unroll
+              for (int o = 1; o < kBlocks; o *= 2)
+                if (had > 64 * o)
+#pragma unroll
+                  for (int b = 0; b < kBlocks; ++b)
+                    if (!(b & o))
+#pragma unroll
+                      for (int k = 0; k < 8; ++k) {
+                        const float x = v[b][k], y = v[b + o][k];
+                        v[b][k] = x + y, v[b + o][k] = x - y;
+                      }
+              if (r < rows.n) {
+                const int64_t row = rows.q_row(r), head = rows.q_head(r);
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                  const int c0 = 64 * b + 8 * g;
+                  if (c0 >= D) continue;
+                  const int64_t to = (row * a.q_heads + head) * D + c0;
+                  if (a.f32) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(a.out) + to);
+                    dst[0] = io<float>::pack(v[b]), dst[1] = io<float>::pack(v[b] + 4);
+                  } else {
+                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + to) = io<__nv_bfloat16>::pack(v[b]);
+                  }
+                }
+                if (a.lse && g == 0) a.lse[row * a.q_heads + head] = l[n][i] == 0.f ? -INFINITY : (m[n][i] + log2f(l[n][i])) * kLn2;
+              }
+            } else if (r < rows.n) {
+#pragma unroll
+              for (int b = 0; b < kBlocks; ++b) store_piece(r, 64 * b + 8 * g, v[b], m[n][i], l[n][i]);
+            }
+          }
       }
-      __syncthreads();
-      if (!mine) continue;
-      for (int i = sub; i < 8; i += per_head) {
-        const int r = 8 * n + i;
-        if (r >= rows.n) break;
-        float mm = -INFINITY, ll = 0.f;
-        for (int w = hl * per_head; w < (hl + 1) * per_head; ++w) mm = fmaxf(mm, m_s[w][r]);
-        const float base = mm == -INFINITY ? 0.f : mm;
-        float v[DP / 32];
+    } else {
+      constexpr int kPitch = DP + 4;
+      float *x = reinterpret_cast<float *>(smem + sh.join_at) + warp * 8 * kPitch;
 #pragma unroll
-        for (int d = 0; d < DP / 32; ++d) v[d] = 0.f;
-        for (int w = hl * per_head; w < (hl + 1) * per_head; ++w) {
-          const float turn = exp2_fast(m_s[w][r] - base);
-          const float *o = reinterpret_cast<const float *>(smem + w * sh.ring) + i * kPitch;
-          ll += l_s[w][r] * turn;
+      for (int n = 0; n < NT; ++n) {
+        meet();
 #pragma unroll
-          for (int d = 0; d < DP / 32; ++d) v[d] += o[lane + 32 * d] * turn;
+        for (int i = 0; i < 2; ++i) {
+          if (g == 0) m_s[warp][8 * n + 2 * t + i] = m[n][i], l_s[warp][8 * n + 2 * t + i] = l[n][i];
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            float v[8];
+            chunk_of(b, n, i, v);
+            float4 *dst = reinterpret_cast<float4 *>(x + (2 * t + i) * kPitch + 64 * b + 8 * g);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]), dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
         }
-        if (starts && ends) {
-          float *mine_row = x + i * kPitch;  // row i is read by this warp alone
-          __syncwarp();
+        meet();
+        for (int i = sub; i < 8; i += per_head) {
+          const int r = 8 * n + i;
+          if (!mine || r >= rows.n) break;
+          float mm = -INFINITY, ll = 0.f;
+          for (int w = hl * per_head; w < (hl + 1) * per_head; ++w) mm = fmaxf(mm, m_s[w][r]);
+          const float base = mm == -INFINITY ? 0.f : mm;
+          float v[DP / 32];
 #pragma unroll
-          for (int d = 0; d < DP / 32; ++d) mine_row[lane + 32 * d] = v[d];
-          __syncwarp();
-          warp_finish(a, mine_row, mm, ll, rows.q_row(r), rows.q_head(r));
-        } else {
-          const int rr = hl * a.tq * a.gh + r;
+          for (int d = 0; d < DP / 32; ++d) v[d] = 0.f;
+          for (int w = 0; w < per_head; ++w) {
+            const float turn = exp2_fast(m_s[hl * per_head + w][r] - base);
+            const float *o = x + ((w - sub) * 8 + i) * kPitch;
+            ll += l_s[hl * per_head + w][r] * turn;
 #pragma unroll
-          for (int d = 0; d < DP / 32; ++d)
-            if (lane + 32 * d < D) piece_values(a, slot_out, rr)[lane + 32 * d] = v[d];
-          if (lane == 0) piece_stats(a, slot_out, rr)[0] = mm, piece_stats(a, slot_out, rr)[1] = ll;
+            for (int d = 0; d < DP / 32; ++d) v[d] += o[lane + 32 * d] * turn;
+          }
+          if (starts && ends) {
+            float *own = x + i * kPitch;  // row i is read by this warp alone
+            __syncwarp();
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d) own[lane + 32 * d] = v[d];
+            __syncwarp();
+            warp_finish(a, own, mm, ll, rows.q_row(r), rows.q_head(r));
+          } else {
+            const int rr = hl * a.tq * a.gh + r;
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d)
+              if (lane + 32 * d < D) piece_values(a, slot_out, rr)[lane + 32 * d] = v[d];
+            if (lane == 0) piece_stats(a, slot_out, rr)[0] = mm, piece_stats(a, slot_out, rr)[1] = ll;
+          }
         }
       }
     }
-    if (starts && !ends) begun = make_int4(at.b, at.block, at.tile, 1);
-    if (!starts && first) gone_on = make_int4(at.b, at.block, at.tile, ends ? 3 : 1);
-    first = false;
+    if (threadIdx.x == 0 && !(starts && ends)) a.part_desc[slot_out] = make_int4(at.b, at.block, at.tile, ends ? 3 : 1);
     left -= run;
     at.unit = 0;
-    if (++at.tile == s.tiles) {
+    if (rows.j0 + a.tq >= rows.all) {  // the sequence's last tile
       at.tile = 0;
       if (++at.block == a.blocks) at.block = 0, ++at.b;
+    } else {
+      ++at.tile;
     }
   }
-  if (threadIdx.x == 0) a.part_desc[2 * blockIdx.x] = gone_on, a.part_desc[2 * blockIdx.x + 1] = begun;
 }
 
-template <int DP, int NT, int PIECES, bool MIXED>
+template <int DP, int NT, int PIECES, int GROUPS>
 cudaError_t launch_mma(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s) {
   static std::atomic<size_t> allowed[64];
-  auto kernel = attention_mma_kernel<DP, NT, PIECES, MIXED>;
+  auto kernel = attention_mma_kernel<DP, NT, PIECES, GROUPS>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), l.smem, allowed);
   if (e != cudaSuccess) return e;
-  const MmaShape sh(a.k.head_dim, DP, a.k.bits, a.v.bits, a.k.group, NT, PIECES, a.k.heads);
-  kernel<<<l.ctas, l.warps * 32, l.smem, s>>>(a, sh, l.per_head);
+  const MmaShape sh(a.k.head_dim, DP, a.k.bits, a.v.bits, a.k.group, NT, PIECES, a.k.heads, a.hb, l.per_head, l.warps);
+  kernel<<<l.ctas, l.warps * 32, l.smem, s>>>(a, sh, l.per_head, 0x64006400u);
   return cudaGetLastError();
+}
+template <int DP, int NT, int PIECES>
+cudaError_t launch_mma_groups(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s) {
+  if (a.k.group == a.k.head_dim) return launch_mma<DP, NT, PIECES, kSingle>(a, l, s);
+  if (a.k.group % 64 == 0) return launch_mma<DP, NT, PIECES, kBlocked>(a, l, s);
+  return launch_mma<DP, NT, PIECES, kMixed>(a, l, s);
 }
 template <int DP, int NT>
 cudaError_t launch_mma_nt(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s) {
-  const bool mixed = a.k.group != a.k.head_dim && a.k.group % 64;
-  if (a.f32) return mixed ? launch_mma<DP, NT, 2, true>(a, l, s) : launch_mma<DP, NT, 2, false>(a, l, s);
-  return mixed ? launch_mma<DP, NT, 1, true>(a, l, s) : launch_mma<DP, NT, 1, false>(a, l, s);
+  return a.f32 ? launch_mma_groups<DP, NT, 2>(a, l, s) : launch_mma_groups<DP, NT, 1>(a, l, s);
 }
 
 }  // namespace attn
