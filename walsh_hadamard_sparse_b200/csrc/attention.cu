@@ -251,6 +251,9 @@ int attention_launches() { return 2; }
 
 namespace {
 
+// Rows of a cached head above which tiles of 128 on tcgen05 are taken instead of 32 on mma.sync.
+constexpr int kTcAbove = 32;
+
 constexpr size_t kSmemLimit = 227 * 1024, kSmemStatic = 9 * 1024;  // (static: 8.2 KB at most, and 1 KB of the system's)
 
 // How a call is cut and launched.
@@ -268,6 +271,11 @@ Cut cut_rows(int grp, int rows, int64_t n) {
 Cut any_cut(int grp, int64_t n) {
   Cut c = cut_rows(grp, kAnyRows, n);
   c.hb = 1, c.kt_log2 = ilog2(kAnyTokens), c.least_log2 = 0, c.ctas = sm_count() * 3;
+  return c;
+}
+Cut tc_cut(int grp, int64_t n) {
+  Cut c = cut_rows(grp, kTcRows, n);
+  c.hb = 1, c.kt_log2 = kTcKeysLog2, c.least_log2 = 0, c.ctas = sm_count();
   return c;
 }
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
@@ -303,6 +311,7 @@ size_t attention_workspace(int32_t q_heads, int32_t head_dim, int32_t heads, int
   if (heads <= 0 || q_heads % heads || n <= 0) return 0;
   const int grp = q_heads / heads;
   size_t most = cut_bytes(any_cut(grp, n), head_dim);
+  if (!f32) most = std::max(most, cut_bytes(tc_cut(grp, n), head_dim));
   // whatever the formats: fewer bits, more CTAs to an SM
   for (int nt = 1; nt <= 4; nt *= 2)
     for (int bits = 2; bits <= 8; ++bits)
@@ -317,9 +326,12 @@ cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
   const int D = a.k.head_dim;
   // (slots in 32 bits: a cache of more has rows of a few bytes)
   const bool mma = takes_codes(a.k) && takes_codes(a.v) && a.k.group == a.v.group && a.k.n_pages * a.k.page_size < (1LL << 31);
+  const int64_t rows = cdiv(a.n, a.n_seqs) * a.grp;  // of a cached head, on average
+  const bool tc = rows > kTcAbove && attention_tc_takes(a);
   Cut c;
-  if (mma) {
-    const int64_t rows = cdiv(a.n, a.n_seqs) * a.grp;
+  if (tc) {
+    c = tc_cut(a.grp, a.n);
+  } else if (mma) {
     const int nt = rows <= 8 ? 1 : rows <= 16 || D > 128 ? 2 : 4;
     c = mma_cut(D, a.k.heads, a.grp, a.n, nt, a.f32 ? 2 : 1, a.k.bits, a.v.bits, a.k.group);
   } else {
@@ -332,7 +344,9 @@ cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
   a.part_stats = reinterpret_cast<float *>(p), p += align_up((size_t)a.ctas * 2 * a.part_rows * 8, 256);
   a.part = reinterpret_cast<float *>(p);
   cudaError_t e;
-  if (mma) {
+  if (tc) {
+    e = launch_attention_tc(a, s);
+  } else if (mma) {
     e = D <= 64 ? launch_attention_d64(a, c.mma, s) : D <= 128 ? launch_attention_d128(a, c.mma, s) : launch_attention_d256(a, c.mma, s);
   } else {
     const size_t smem = any_smem(D);

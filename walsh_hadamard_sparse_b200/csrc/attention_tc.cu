@@ -1,0 +1,845 @@
+// Attention over the quantized cache on the 5th-generation tensor cores: bf16
+// calls with more rows to a cached head than the kernel of attention_mma.cuh
+// likes (drafted trees, chunks of prompts).
+//
+// A CTA takes one cached head and up to 256 rows of queries (tokens times the
+// query heads that share the head), two tiles of 128, and walks 128 cached tokens
+// at a time:
+//   S_w = Q_w C_k^T    tcgen05, operands in shared memory, fp32 in TMEM
+//   P_w = 2^(S_w - m)  by the 128 threads of the tile, a row each; f16 over S_w
+//   O_w += P_w C_v     tcgen05, P from TMEM, C_v in shared memory
+// C holds the integers code - zero, exact in f16, so a token's scale multiplies
+// a column of S, and of P, in fp32; where a head has several groups a token's
+// largest scale does, and C the rest: (code - zero) times scale / largest, rounded
+// twice to 11 bits. The query (rotated, its largest value near 2^15) and P are
+// rounded to 11 bits as in attention_mma.cuh, and the maximum is kept to within
+// what f16 leaves room for: a tile whose weights sum to more than 2^9 has its
+// maximum taken and is done again, others need none.
+//   4 warps  unpack: a lane's 32 codes of a token, fetched a tile ahead, to two
+//            swizzled tiles of f16 (keys and values, two of each).
+//   8 warps  softmax: four for each tile of rows.
+//   1 warp   issues the products: S_w of the next tokens behind O_w of these, so
+//            that one tile of rows is multiplied while the other's weights are
+//            made.
+// Bound: the 16384 exponentials and about 80 thousand other operations of a tile of 128
+// rows and tokens, and 1024 clocks of products. Every wait is bounded; a thread
+// that gives up sets the error word and goes on without waiting.
+
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "attention_mma.cuh"
+#include "gemv_wide.cuh"
+
+namespace qwha {
+namespace {
+
+using namespace attn;
+using bulk::saddr;
+using wide::arrive;
+using wide::calm_wait;
+using wide::commit;
+using wide::sw128;
+
+constexpr int kRowsTile = 128, kKeys = 128, kUnpackWarps = 4, kSoftWarps = 8;
+constexpr int kTcThreads = (kUnpackWarps + kSoftWarps + 1) * 32;
+constexpr int kScaleSlots = 4;      // tiles whose scales are kept: a tile's are read until its weights are made
+constexpr float kTcTop = 64.f;      // of a value's scale in f16; times kTcSum below the largest f16
+constexpr float kTcSum = 512.f;     // of a tile's weights, before its maximum is taken again
+constexpr uint32_t kTcCols = 512;   // TMEM: S_0, S_1, O_0, O_1
+constexpr unsigned int kErrTc = 0x10000u;  // a wait gave up
+
+__device__ __forceinline__ uint64_t sw128_mn(uint32_t at) {  // slabs of 64 channels x 128 tokens, rows of 128 bytes
+  return (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)(kKeys * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// D += A B with A in TMEM
+__device__ __forceinline__ void product_t(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+#define QWHA_R32(x)                                                                                              \
+  x(0), x(1), x(2), x(3), x(4), x(5), x(6), x(7), x(8), x(9), x(10), x(11), x(12), x(13), x(14), x(15), x(16), x(17), \
+      x(18), x(19), x(20), x(21), x(22), x(23), x(24), x(25), x(26), x(27), x(28), x(29), x(30), x(31)
+__device__ __forceinline__ void load32(uint32_t at, uint32_t *r) {
+#define X(i) "=r"(r[i])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : QWHA_R32(X)
+      : "r"(at)
+      : "memory");
+#undef X
+}
+__device__ __forceinline__ void store32(uint32_t at, const uint32_t *r) {
+#define X(i) "r"(r[i])
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::QWHA_R32(X),
+      "r"(at)
+      : "memory");
+#undef X
+}
+__device__ __forceinline__ void load8(uint32_t at, uint32_t *r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void loads_done(uint32_t *r) {  // (32 registers that the loads wrote)
+#define X(i) "+r"(r[i])
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : QWHA_R32(X)::"memory");
+#undef X
+}
+__device__ __forceinline__ void stores_done() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 both(float a, float b) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void split(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Scales of a tile of tokens, as the softmax threads read them.
+struct alignas(16) TileScales {
+  float k[kKeys], v[kKeys];  // of the scores; of the weights, times c
+  uint32_t live[4];          // a bit a token
+  float c;                   // what the values' scales are multiplied by, a power of two
+  int bad;                   // some token's values have a group that is no number
+  uint8_t groups[kKeys];     // which groups, where bad
+};
+
+template <int DP>
+struct TcSmem {
+  static constexpr int kTile = kKeys * DP * 2;  // bytes of a tile of 128 rows or tokens
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = kK + 2 * kTile, kScales = kV + 2 * kTile;
+  static constexpr int kBars = kScales + kScaleSlots * (int)sizeof(TileScales), kTotal = kBars + 256 + 1024;
+};
+// barriers
+enum { kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kOFull = 12, kQReady = 14, kBarCount = 16 };
+
+// A segment's geometry, as every role works it out.
+struct Segment {
+  Seq s;
+  int units, length, run, kv, starts, ends;
+  Rows rows;
+  __device__ __forceinline__ Segment(const AttnArgs &a, const Place &at, long long left) : s(a, at.b) {
+    if (s.rows == 0) return;
+    units = s.units(a, at.tile), length = s.length(a, at.tile);
+    run = left < units - at.unit ? (int)left : units - at.unit;
+    kv = block_of(a, at.block);
+    rows = rows_of(a, s, kv, at.block - kv * a.parts, at.tile);
+    starts = at.unit == 0, ends = at.unit + run == units;
+  }
+  __device__ __forceinline__ void next(const AttnArgs &a, Place *at, long long *left) const {
+    *left -= run;
+    at->unit = 0;
+    if (++at->tile == s.tiles) {
+      at->tile = 0;
+      if (++at->block == a.blocks) at->block = 0, ++at->b;
+    }
+  }
+};
+
+// What one unpacking thread fetches of a tile: per round (two) and slab (DP / 64)
+// 32 codes of a token, its scales and zero point.
+template <int BITS>
+struct Raw {
+  uint32_t w[BITS];
+};
+template <int BITS>
+__device__ __forceinline__ void fetch_codes(const uint8_t *p, uint32_t *w) {
+  if constexpr (BITS == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+    w[0] = v.x, w[1] = v.y;
+  } else if constexpr (BITS == 3) {
+    const uint32_t *s = reinterpret_cast<const uint32_t *>(p);
+    w[0] = __ldg(s), w[1] = __ldg(s + 1), w[2] = __ldg(s + 2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < BITS / 4; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+}
+// Codes 8 x .. 8 x + 7 of 32 as unpack_row takes them.
+template <int BITS>
+__device__ __forceinline__ uint2 chunk_of(const uint32_t *w, int x) {
+  if constexpr (BITS == 8) return make_uint2(w[2 * x], w[2 * x + 1]);
+  if constexpr (BITS == 4) return make_uint2(w[x], 0);
+  if constexpr (BITS == 2) return make_uint2(x & 1 ? w[x >> 1] >> 16 : w[x >> 1] & 0xffffu, 0);
+  const uint32_t v = x == 0 ? w[0] : x == 1 ? __funnelshift_r(w[0], w[1], 24) : x == 2 ? __funnelshift_r(w[1], w[2], 16) : w[2] >> 8;
+  return make_uint2(v & 0xffffffu, 0);
+}
+
+// The unpacking warps: tokens of a segment to tiles of f16.
+template <int DP, int BK, int BV>
+struct Unpacker {
+  static constexpr int kSlabs = DP / 64;
+  using S = TcSmem<DP>;
+  const AttnArgs &a;
+  uint8_t *smem;
+  uint32_t bars, one;
+  bool ok = true;
+  uint32_t it = 0;      // tiles so far
+  uint32_t k[2][kSlabs][BK], v[2][kSlabs][BV];  // raw codes of the next tile
+  float ks[2], vs[2];        // scales: the largest of the token, finite or of bad
+  __half kr[2][kSlabs], vr[2][kSlabs];  // this lane's groups' share of it
+  uint8_t kz[2][kSlabs], vz[2][kSlabs], bad[2];
+  bool on[2];
+
+  __device__ __forceinline__ Unpacker(const AttnArgs &a_, uint8_t *smem_, uint32_t bars_, uint32_t one_)
+      : a(a_), smem(smem_), bars(bars_), one(one_) {}
+
+  // The token's largest scale, the shares of the lane's groups, which groups are no numbers.
+  __device__ __forceinline__ void scales(const qwha_cache &c, int64_t row, int ng, float *most, __half *share, uint8_t *zero,
+                                         uint8_t *bad_groups) {
+    const float *s = c.scales + row * ng;
+    const uint8_t *z = c.zeros + row * ng;
+    const int half = threadIdx.x & 1;
+    if (ng == 1) {
+      *most = __ldg(s), *bad_groups = 0;
+#pragma unroll
+      for (int i = 0; i < kSlabs; ++i) share[i] = __float2half_rn(1.f), zero[i] = __ldg(z);
+      return;
+    }
+    float all[4], top = 0.f;
+    int b = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      all[i] = i < ng ? __ldg(s + i) : 0.f;
+      if (fabsf(all[i]) < INFINITY) top = fmaxf(top, fabsf(all[i]));
+      else b |= 1 << i, all[i] = 0.f;
+    }
+    const float inv = top > 0.f ? 1.f / top : 0.f;
+    *most = top, *bad_groups = (uint8_t)b;
+#pragma unroll
+    for (int i = 0; i < kSlabs; ++i) {
+      const int d = 64 * i + 32 * half, g = d < c.head_dim ? d / c.group : 0;
+      const float mine = g == 0 ? all[0] : g == 1 ? all[1] : g == 2 ? all[2] : all[3];
+      share[i] = __float2half_rn(mine * inv), zero[i] = __ldg(z + g);
+    }
+  }
+
+  template <int B>
+  __device__ __forceinline__ void write(uint8_t *tile, int token, int slab, const uint32_t *w, uint32_t zero, __half share,
+                                        bool scaled, bool live) {
+    Zero<B> z;
+    z.set((zero | 0xe400u) * 0x10001u);
+    const uint32_t f = (uint32_t)__half_as_ushort(share) * 0x10001u;
+    const int half = threadIdx.x & 1;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      uint32_t r[4] = {0, 0, 0, 0};
+      if (live) {
+        unpack_row<B>(chunk_of<B>(w, x), z, one, r);
+        if (scaled)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __half2 p = __hmul2(reinterpret_cast<const __half2 &>(r[i]), reinterpret_cast<const __half2 &>(f));
+            r[i] = reinterpret_cast<const uint32_t &>(p);
+          }
+      }
+      *reinterpret_cast<uint4 *>(tile + slab * (kKeys * 128) + token * 128 + (((4 * half + x) ^ (token & 7)) << 4)) =
+          make_uint4(r[0], r[1], r[2], r[3]);
+    }
+  }
+
+  __device__ __forceinline__ void wait(int bar, uint32_t parity) { ok = ok && wide::warp_wait(bars + 8 * bar, parity); }
+
+  __device__ __forceinline__ void run(const Segment &g, const Place &at, float *c_now) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = lane & 1, D = a.k.head_dim, ng = D / a.k.group;
+    const int32_t *table = a.pages + (int64_t)at.b * a.max_pages;
+    // which new tokens of a tree any row of the tile sees
+    unsigned long long seen = ~0ull;
+    if (a.tree) {
+      seen = 0;
+      for (int j = lane; j < g.rows.tokens; j += 32) seen |= (unsigned long long)a.tree[g.s.row0 + g.rows.j0 + j];
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) seen |= __shfl_xor_sync(~0u, seen, o);
+    }
+    const int past = g.s.past;
+    auto slot_at = [&](int t) -> int64_t {
+      if (t >= g.length) return -1;
+      const int pg = page_of(a, t);
+      const int page = table[pg];
+      if ((uint32_t)page >= (uint32_t)a.k.n_pages) {
+        atomicOr(a.err, kErrPage);
+        return -1;
+      }
+      if (a.tree && t >= past && !(seen >> (t - past) & 1)) return -1;
+      return (int64_t)page * a.k.page_size + (t - pg * a.k.page_size);
+    };
+    const int mine = warp * 32 + (lane >> 1);  // token of round 0; 16 more in round 1
+    int64_t slot[2];
+    int t0 = at.unit * kKeys;
+    auto look_up = [&] {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) slot[r] = slot_at(t0 + mine + 16 * r);
+    };
+    // keys' codes and all scales; values' codes
+    auto fetch_keys = [&] {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        on[r] = slot[r] >= 0;
+        ks[r] = vs[r] = 0.f, bad[r] = 0;
+        if (!on[r]) continue;
+        const int64_t row = slot[r] * a.k.heads + g.kv;
+#pragma unroll
+        for (int i = 0; i < kSlabs; ++i)
+          if (32 * (2 * i + half) < D) fetch_codes<BK>(a.k.codes + row * (D / 8 * BK) + (2 * i + half) * (4 * BK), k[r][i]);
+        uint8_t k_bad;
+        scales(a.k, row, ng, &ks[r], kr[r], kz[r], &k_bad);
+        scales(a.v, row, ng, &vs[r], vr[r], vz[r], &bad[r]);
+        if (k_bad) ks[r] = __int_as_float(0x7fc00000);
+      }
+    };
+    auto fetch_values = [&](const int64_t *from) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (from[r] < 0) continue;
+        const int64_t row = from[r] * a.k.heads + g.kv;
+#pragma unroll
+        for (int i = 0; i < kSlabs; ++i)
+          if (32 * (2 * i + half) < D) fetch_codes<BV>(a.v.codes + row * (D / 8 * BV) + (2 * i + half) * (4 * BV), v[r][i]);
+      }
+    };
+    look_up();
+    fetch_keys();
+    fetch_values(slot);
+    t0 += kKeys;
+    if (g.run > 1) look_up();  // (only of tokens that the run has: each page that is none is reported once a run)
+    for (int u = 0; u < g.run; ++u, ++it) {
+      const int st = it & 1;
+      const uint32_t phase = (it >> 1 & 1) ^ 1;
+      uint8_t *k_tile = smem + S::kK + st * S::kTile, *v_tile = smem + S::kV + st * S::kTile;
+      TileScales &sc = *reinterpret_cast<TileScales *>(smem + S::kScales + (it % kScaleSlots) * sizeof(TileScales));
+      // the factor of the values' scales: follows the largest met, over the four warps
+      float top = 0.f;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float x = fabsf(vs[r]);
+        if (x < INFINITY) top = fmaxf(top, x);
+      }
+      const bool up = __any_sync(~0u, top * *c_now > kTcTop);
+      int any = 0;
+      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, 2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                   : "=r"(any)
+                   : "r"((int)up)
+                   : "memory");
+      if (any) {
+        uint32_t *top_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount + 16);
+        if (threadIdx.x == 0) *top_s = 0;
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+        atomicMax(top_s, __float_as_uint(top));
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+        int e = 127 + 6 - ((int)(*top_s >> 23) - 127 + 2);
+        e = e < 1 ? 1 : e > 247 ? 247 : e;
+        *c_now = fminf(*c_now, __uint_as_float((uint32_t)e << 23));
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+      }
+      wait(kKEmpty + st, phase);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int token = mine + 16 * r;
+        const unsigned b = __ballot_sync(~0u, on[r]);  // two lanes a token
+        if (half == 0) sc.k[token] = ks[r], sc.v[token] = vs[r] * *c_now, sc.groups[token] = bad[r];
+        if (lane == 0) {
+          unsigned x = b & 0x55555555u;  // the even bits together
+          x = (x | x >> 1) & 0x33333333u, x = (x | x >> 2) & 0x0f0f0f0fu, x = (x | x >> 4) & 0x00ff00ffu, x = (x | x >> 8) & 0xffffu;
+          reinterpret_cast<uint16_t *>(sc.live)[warp * 2 + r] = (uint16_t)x;
+        }
+#pragma unroll
+        for (int i = 0; i < kSlabs; ++i)
+          write<BK>(k_tile, token, i, k[r][i], kz[r][i], kr[r][i], ng > 1, on[r] && 32 * (2 * i + half) < D);
+      }
+      int any_bad = 0;
+      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, 2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                   : "=r"(any_bad)
+                   : "r"((int)(bad[0] | bad[1]))
+                   : "memory");
+      if (threadIdx.x == 0) sc.c = *c_now, sc.bad = any_bad;
+      bulk::fence_proxy();
+      arrive(bars + 8 * (kKFull + st));
+      // the next tile's keys and scales are on their way while this one's values are unpacked, and so on
+      uint8_t zero[2][kSlabs];
+      __half share[2][kSlabs];
+      const bool was[2] = {on[0], on[1]};
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < kSlabs; ++i) zero[r][i] = vz[r][i], share[r][i] = vr[r][i];
+      const int64_t next[2] = {slot[0], slot[1]};
+      if (u + 1 < g.run) {
+        fetch_keys();
+        t0 += kKeys;
+        if (u + 2 < g.run) look_up();
+      }
+      wait(kVEmpty + st, phase);
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < kSlabs; ++i)
+          write<BV>(v_tile, mine + 16 * r, i, v[r][i], zero[r][i], share[r][i], ng > 1, was[r] && 32 * (2 * i + half) < D);
+      if (u + 1 < g.run) fetch_values(next);
+      bulk::fence_proxy();
+      arrive(bars + 8 * (kVFull + st));
+    }
+  }
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __grid_constant__ AttnArgs a, uint32_t one) {
+  using S = TcSmem<DP>;
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
+  const uint32_t base = saddr(smem), bars = base + S::kBars;
+  uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kIssue = kUnpackWarps + kSoftWarps;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bulk::init(bars + 8 * (kKFull + i), kUnpackWarps * 32), bulk::init(bars + 8 * (kVFull + i), kUnpackWarps * 32);
+      bulk::init(bars + 8 * (kKEmpty + i), 1), bulk::init(bars + 8 * (kVEmpty + i), 1);
+      bulk::init(bars + 8 * (kSFull + i), 1), bulk::init(bars + 8 * (kOFull + i), 1);
+      bulk::init(bars + 8 * (kPReady + i), 128), bulk::init(bars + 8 * (kQReady + i), 128);
+    }
+    bulk::fence_init();
+  }
+  if (warp == kIssue) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_s)), "r"(kTcCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    fence_before();
+  }
+  if (threadIdx.x == 0) a.part_desc[2 * blockIdx.x] = a.part_desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+  Place at;
+  long long left = my_share(a, &at);
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_s;
+
+  if (warp < kUnpackWarps) {
+    // ------------------------------------------------------------ unpacking
+    auto work = [&](auto bk, auto bv) {
+      Unpacker<DP, decltype(bk)::value, decltype(bv)::value> unpack(a, smem, bars, one);
+      float c = kNoScale;
+      while (left > 0) {
+        const Segment g(a, at, left);
+        if (g.s.rows == 0) {
+          ++at.b;
+          continue;
+        }
+        if (threadIdx.x == 0 && (long long)g.s.past + (a.tree && g.s.rows > 64 ? 64 : g.s.rows) > a.cap) atomicOr(a.err, kErrPage);
+        c = kNoScale;
+        unpack.run(g, at, &c);
+        g.next(a, &at, &left);
+      }
+      if (!unpack.ok && lane == 0) atomicOr(a.err, kErrTc);
+    };
+    using std::integral_constant;
+    auto keys = [&](auto bk) {
+      switch (a.v.bits) {
+        case 2: work(bk, integral_constant<int, 2>()); break;
+        case 3: work(bk, integral_constant<int, 3>()); break;
+        case 4: work(bk, integral_constant<int, 4>()); break;
+        default: work(bk, integral_constant<int, 8>());
+      }
+    };
+    switch (a.k.bits) {
+      case 2: keys(integral_constant<int, 2>()); break;
+      case 3: keys(integral_constant<int, 3>()); break;
+      case 4: keys(integral_constant<int, 4>()); break;
+      default: keys(integral_constant<int, 8>());
+    }
+  } else if (warp < kIssue) {
+    // ------------------------------------------------------------ softmax: a row a thread
+    const int w = (warp - kUnpackWarps) / 4, r = (warp & 3) * 32 + lane;  // tile of rows; row of it (TMEM lane)
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // (unpacking takes four warps: warp % 4 is the quarter)
+    const uint32_t s_at = tmem + lanes + 128 * w, o_at = tmem + lanes + 256 + 128 * w;
+    uint8_t *q_tile = smem + S::kQ + w * S::kTile;
+    bool ok = true;
+    uint32_t it = 0, slot = 0, segment = 0;  // tiles of this tile of rows, and of the CTA; segments with rows in it
+    auto wait = [&](int bar, uint32_t parity) { ok = ok && wide::warp_wait(bars + 8 * bar, parity); };
+    while (left > 0) {
+      const Segment g(a, at, left);
+      if (g.s.rows == 0) {
+        ++at.b;
+        continue;
+      }
+      const int n = g.rows.n - 128 * w;  // rows of this tile
+      const int out_slot = 2 * blockIdx.x + (g.starts ? 1 : 0);
+      if (n > 0) {
+        // ---- queries: 2^15 near the row's largest, rotated, eight channels a lane
+        constexpr int L = DP / 8, kAtOnce = 32 / L;
+        const int c = lane % L, D = a.k.head_dim;
+        float f = 1.f;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += 4 * kAtOnce) {
+          uint4 x[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int i = (warp & 3) * 32 + r0 + p * kAtOnce + lane / L;
+            x[p] = make_uint4(0, 0, 0, 0);
+            if (i < n && c * 8 < D)
+              x[p] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + g.rows.q_row(128 * w + i) * a.q_stride +
+                                                           (int64_t)g.rows.q_head(128 * w + i) * D + c * 8));
+          }
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const int in = r0 + p * kAtOnce + lane / L, i = (warp & 3) * 32 + in;
+            float v[8];
+            io<__nv_bfloat16>::unpack(x[p], v);
+            rotate_lanes<L>(v, a.k.had_block, a.unit_k, lane);
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= a.scale2, top = fmaxf(top, fabsf(v[k]));
+#pragma unroll
+            for (int o = 1; o < L; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+            const uint32_t bits = __float_as_uint(top);
+            int e = (int)(bits >> 23) - 127 + 1;
+            e = bits == 0 || bits >= 0x7f800000u ? 0 : e < -100 ? -100 : e;
+            const float up = __uint_as_float((uint32_t)(127 + 15 - e) << 23);
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = pair16(v[k] * up, v[k + 4] * up);
+            *reinterpret_cast<uint4 *>(q_tile + (c >> 3) * (kRowsTile * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+            // the lane whose row this is keeps its factor
+            const float down = __uint_as_float((uint32_t)(127 - 15 + e) << 23);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+              const float other = __shfl_sync(~0u, down, k * L);
+              if (lane == r0 + p * kAtOnce + k) f = other;
+            }
+          }
+        }
+        bulk::fence_proxy();
+        arrive(bars + 8 * (kQReady + w));
+
+        // ---- what the row sees
+        const int rr = 128 * w + r, j = g.rows.j0 + (r < n ? rr / g.rows.heads : 0);
+        const int past = g.s.past, lim = a.tree ? past : past + j + 1, safe = a.tree ? past : past + g.rows.j0 + 1;
+        const unsigned long long mask = a.tree && r < n ? (unsigned long long)a.tree[g.s.row0 + j] : 0;
+        float m = -INFINITY, l = 0.f, c_old = 0.f;
+        uint32_t nan_groups = 0;
+        int t0 = at.unit * kKeys;
+        const f32x2 ff = both(f, f);
+        for (int u = 0; u < g.run; ++u, ++it, t0 += kKeys) {
+          wait(kSFull + w, it & 1);
+          fence_after();
+          const TileScales &sc = *reinterpret_cast<const TileScales *>(smem + S::kScales + ((slot + u) % kScaleSlots) * sizeof(TileScales));
+          const uint4 live = *reinterpret_cast<const uint4 *>(sc.live);
+          const bool masked = t0 + kKeys > safe || (live.x & live.y & live.z & live.w) != ~0u;
+          uint32_t vis[4] = {live.x, live.y, live.z, live.w};
+          if (masked) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int tb = t0 + 32 * x, left_of = lim - tb, d = tb - past;
+              uint32_t s = left_of >= 32 ? ~0u : left_of > 0 ? (1u << left_of) - 1u : 0u;
+              if (a.tree) s |= d >= 64 || d <= -32 ? 0u : d >= 0 ? (uint32_t)(mask >> d) : (uint32_t)(mask << -d);
+              vis[x] &= s;
+            }
+          }
+          if (sc.bad) {
+            for (int t = 0; t < 32; ++t)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (vis[x] >> t & 1) nan_groups |= sc.groups[32 * x + t];
+          }
+          // the largest visible score
+          auto largest = [&] {
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t on = x == 0 ? vis[0] : x == 1 ? vis[1] : x == 2 ? vis[2] : vis[3];
+              uint32_t v[32];
+              load32(s_at + 32 * x, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (on >> i & 1) top = fmaxf(top, __uint_as_float(v[i]) * sc.k[32 * x + i]);
+            }
+            return top * f;
+          };
+          float turn = 1.f;  // of the sums so far
+          auto raise = [&] {
+            const float top = largest(), now = fmaxf(m, top);
+            turn = now == -INFINITY ? 1.f : exp2_fast(m - now);
+            m = now;
+          };
+          if (u == 0) raise();
+          uint32_t p[64];
+          float sum;
+          auto weights = [&](auto hidden) {
+            const float base = m == -INFINITY ? 0.f : m;
+            const f32x2 mm = both(-base, -base);
+            f32x2 total = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t v[32];
+              load32(s_at + 32 * x, v);
+              const float4 *k4 = reinterpret_cast<const float4 *>(sc.k + 32 * x), *v4 = reinterpret_cast<const float4 *>(sc.v + 32 * x);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 kk = k4[i], vv = v4[i];
+                float e[4];
+                split(fma2(mul2(both(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), both(kk.x, kk.y)), ff, mm), e[0], e[1]);
+                split(fma2(mul2(both(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), both(kk.z, kk.w)), ff, mm), e[2], e[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  e[k] = exp2_fast(e[k]);
+                  if constexpr (decltype(hidden)::value) e[k] = vis[x] >> (4 * i + k) & 1 ? e[k] : 0.f;
+                }
+                const f32x2 e01 = both(e[0], e[1]), e23 = both(e[2], e[3]);
+                total = add2(total, add2(e01, e23));
+                float y[4];
+                split(mul2(e01, both(vv.x, vv.y)), y[0], y[1]);
+                split(mul2(e23, both(vv.z, vv.w)), y[2], y[3]);
+                if constexpr (decltype(hidden)::value)  // a hidden token's scale may be no number
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) y[k] = e[k] == 0.f ? 0.f : y[k];
+                p[16 * x + 2 * i] = pair16(y[0], y[1]), p[16 * x + 2 * i + 1] = pair16(y[2], y[3]);
+              }
+            }
+            float s0, s1;
+            split(total, s0, s1);
+            sum = s0 + s1;
+          };
+          auto all_weights = [&] {
+            if (masked) weights(std::true_type());
+            else weights(std::false_type());
+          };
+          for (bool again = u > 0;; again = false) {
+            all_weights();
+            if (!again || !__any_sync(~0u, !(sum <= kTcSum))) break;
+            raise();
+          }
+          // ---- the sums so far in the new units: nothing of this tile of rows is being multiplied now
+          const float grow = sc.c * (c_old == 0.f ? 0.f : inverse2(c_old));  // a power of two, at most 1
+          const bool first = u == 0;
+          if (!first && __any_sync(~0u, turn != 1.f || grow != 1.f)) {
+            const float by = turn * grow;
+#pragma unroll 1
+            for (int x = 0; x < DP / 32; ++x) {
+              uint32_t v[32];
+              load32(o_at + 32 * x, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
+              store32(o_at + 32 * x, v);
+            }
+          }
+          c_old = sc.c;
+          l = l * turn + sum;
+          store32(s_at, p), store32(s_at + 32, p + 32);
+          stores_done();
+          fence_before();
+          arrive(bars + 8 * (kPReady + w));
+        }
+        // ---- the rows
+        wait(kOFull + w, segment & 1);
+        ++segment;
+        fence_after();
+        const bool done = g.starts && g.ends;
+        const float by = inverse2(c_old) * (done ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
+        const int had = done ? a.v.had_block : 0;
+        const bool real = r < n;
+        const int64_t row = real ? g.rows.q_row(rr) : 0, head = real ? g.rows.q_head(rr) : 0;
+        const int DV = a.v.head_dim;
+        auto put = [&](int c0, float *v) {  // eight channels from c0 on
+          if (!real || c0 >= DV) return;
+          if (done) {
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (row * a.q_heads + head) * DV + c0) = io<__nv_bfloat16>::pack(v);
+          } else {
+            float4 *dst = reinterpret_cast<float4 *>(piece_values(a, out_slot, rr) + c0);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]), dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        };
+#pragma unroll 1
+        for (int x = 0; x < DP / 32; ++x) {
+          uint32_t u[32];
+          load32(o_at + 32 * x, u);
+          float v[32];  // (place i of a chunk of eight is channel (i >> 1) + 4 (i & 1))
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[(i & ~7) + (i >> 1 & 3) + 4 * (i & 1)] = __uint_as_float(u[i]) * by;
+          if (nan_groups && nan_groups >> (32 * x / a.v.group) & 1)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __int_as_float(0x7fc00000);
+#pragma unroll
+          for (int h = 1; h < 32; h *= 2)
+            if (had > h)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(i & h)) {
+                  const float p = v[i], q = v[i + h];
+                  v[i] = p + q, v[i + h] = p - q;
+                }
+          if (had > 1)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= a.unit_v;
+          if (had > 32) {  // bits 5 and 6 of the channel: once all are back
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i]);
+            store32(o_at + 32 * x, u);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put(32 * x + 8 * i, v + 8 * i);
+          }
+        }
+        if (had > 32) {
+          stores_done();
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            uint32_t u[32];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (x < DP / 32) load8(o_at + 32 * x + 8 * i, u + 8 * x);
+              else for (int k = 0; k < 8; ++k) u[8 * x + k] = 0;
+            loads_done(u);
+            float v[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(u[k]);
+#pragma unroll
+            for (int h = 8; h < 32; h *= 2)
+              if (had > 4 * h)
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!(k & h)) {
+                    const float p = v[k], q = v[k + h];
+                    v[k] = p + q, v[k + h] = p - q;
+                  }
+#pragma unroll
+            for (int x = 0; x < DP / 32; ++x) put(32 * x + 8 * i, v + 8 * x);
+          }
+        }
+        if (real) {
+          if (!done) piece_stats(a, out_slot, rr)[0] = m, piece_stats(a, out_slot, rr)[1] = l;
+          else if (a.lse) a.lse[row * a.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+        fence_before();
+      }
+      slot += g.run;
+      if (threadIdx.x == kUnpackWarps * 32 && !(g.starts && g.ends))
+        a.part_desc[out_slot] = make_int4(at.b, at.block, at.tile, g.ends ? 3 : 1);
+      g.next(a, &at, &left);
+    }
+    if (!ok && lane == 0) atomicOr(a.err, kErrTc);
+  } else {
+    // ------------------------------------------------------------ products
+    bool ok = true;
+    if (wide::elected()) {
+      // D fp32, A and B f16; S: both K-major, N 128; O: A in TMEM, B MN-major, N DP
+      constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);
+      constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(DP >> 3) << 17) | (8u << 24);
+      uint32_t it = 0, tiles[2] = {0, 0}, segment[2] = {0, 0};
+      auto wait = [&](int bar, uint32_t parity) {
+        ok = ok && calm_wait(bars + 8 * bar, parity);
+        fence_after();
+      };
+      auto scores = [&](int w, int st) {
+        const uint64_t q = sw128(base + S::kQ + w * S::kTile), k = sw128(base + S::kK + st * S::kTile);
+#pragma unroll
+        for (int x = 0; x < DP / 16; ++x) {
+          const uint32_t off = (x >> 2) * (kKeys * 128 >> 4) + (x & 3) * 2;
+          wide::product(tmem + 128 * w, q + off, k + off, kIdescS, x != 0);
+        }
+        commit(bars + 8 * (kSFull + w));
+      };
+      auto values = [&](int w, int st, bool add) {
+        const uint64_t v = sw128_mn(base + S::kV + st * S::kTile);
+#pragma unroll
+        for (int x = 0; x < kKeys / 16; ++x)
+          product_t(tmem + 256 + 128 * w, tmem + 128 * w + 8 * x, v + x * (16 * 128 >> 4), kIdescO, add || x != 0);
+      };
+      while (left > 0) {
+        const Segment g(a, at, left);
+        if (g.s.rows == 0) {
+          ++at.b;
+          continue;
+        }
+        const int count = g.rows.n > 128 ? 2 : 1;
+        for (int w = 0; w < count; ++w) wait(kQReady + w, segment[w] & 1);
+        for (int u = 0; u < g.run; ++u, ++it) {
+          const int st = it & 1, before = (it - 1) & 1;
+          wait(kKFull + st, it >> 1 & 1);
+          if (u > 0) wait(kVFull + before, (it - 1) >> 1 & 1);
+          for (int w = 0; w < count; ++w) {
+            if (u > 0) {
+              wait(kPReady + w, (tiles[w] - 1) & 1);
+              values(w, before, u > 1);
+            }
+            scores(w, st);
+            ++tiles[w];
+          }
+          commit(bars + 8 * (kKEmpty + st));
+          if (u > 0) commit(bars + 8 * (kVEmpty + before));
+        }
+        const int last = (it - 1) & 1;
+        wait(kVFull + last, (it - 1) >> 1 & 1);
+        for (int w = 0; w < count; ++w) {
+          wait(kPReady + w, (tiles[w] - 1) & 1);
+          values(w, last, g.run > 1);
+          commit(bars + 8 * (kOFull + w));
+          ++segment[w];
+        }
+        commit(bars + 8 * (kVEmpty + last));
+        g.next(a, &at, &left);
+      }
+      // the last rows' readers have met kOFull; nothing is in flight behind it
+      if (!ok) atomicOr(a.err, kErrTc);
+    }
+    __syncwarp();
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kIssue) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcCols) : "memory");
+  }
+}
+
+template <int DP>
+cudaError_t launch_tc(const AttnArgs &a, cudaStream_t s) {
+  static std::atomic<size_t> allowed[64];
+  auto kernel = attention_tc_kernel<DP>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), TcSmem<DP>::kTotal, allowed);
+  if (e != cudaSuccess) return e;
+  kernel<<<a.ctas, kTcThreads, TcSmem<DP>::kTotal, s>>>(a, 0x64006400u);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Heads of whole runs of 32 channels up to 128, in groups of whole runs; bf16.
+bool attention_tc_takes(const AttnArgs &a) {
+  const int D = a.k.head_dim;
+  return !a.f32 && D % 32 == 0 && D <= 128 && a.k.group == a.v.group && a.k.group % 32 == 0;
+}
+cudaError_t launch_attention_tc(const AttnArgs &a, cudaStream_t s) {
+  return a.k.head_dim <= 64 ? launch_tc<64>(a, s) : launch_tc<128>(a, s);
+}
+
+}  // namespace qwha

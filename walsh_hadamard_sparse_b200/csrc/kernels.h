@@ -297,5 +297,9 @@ struct MmaLaunch {
 cudaError_t launch_attention_d64(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s);
 cudaError_t launch_attention_d128(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s);
 cudaError_t launch_attention_d256(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s);
+// The tcgen05 kernel (attention_tc.cu): tiles of up to 256 rows, runs of 128 cached tokens.
+constexpr int kTcRows = 256, kTcKeysLog2 = 7;
+bool attention_tc_takes(const AttnArgs &a);
+cudaError_t launch_attention_tc(const AttnArgs &a, cudaStream_t s);
 
 }  // namespace qwha
