@@ -172,73 +172,97 @@ __global__ void __launch_bounds__(kAnyThreads) attention_any_kernel(const AttnAr
 // ---------------------------------------------------------------- joining
 
 // The tile that CTA blockIdx.x of the kernel before began and left: its piece and
-// those of the CTAs that went on with it, a warp a row, in order. Lanes look at 32
-// CTAs at once; the values are then read eight pieces at a time.
-constexpr int kJoinThreads = 256, kJoinAhead = 8;
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnArgs a) {
-  __shared__ float x_s[kJoinThreads / 32][256];
+// those of the CTAs that went on with it, in order. L lanes have a row, eight
+// channels each; they look at L pieces' maxima and sums at once and read the values
+// of four pieces ahead.
+constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinAhead = 4;
+template <int L>
+__global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const __grid_constant__ AttnArgs a) {
+  __shared__ Rows rows_s;
+  __shared__ int count_s;
+  extern __shared__ int slots_s[];  // the pieces
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = a.v.head_dim;
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
   const int4 begun = a.part_desc[2 * c + 1];
   if (!(begun.w & 1)) return;
-  const int each = a.tq * a.gh, rr = blockIdx.y * (kJoinThreads / 32) + warp;
-  if (rr >= a.part_rows) return;
-  const int kv = block_of(a, begun.y) * a.hb + rr / each, r = rr % each;
-  if (kv >= a.k.heads) return;
-  const Seq s(a, begun.x);
-  const Rows rows = rows_of(a, s, kv, begun.y % a.parts, begun.z);
-  if (r >= rows.n) return;
-  float m = -INFINITY, l = 0.f, acc[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  bool more = true;
-  for (int p0 = c; more && p0 < a.ctas; p0 += 32) {
-    const int p = p0 + lane, slot = p == c ? 2 * p + 1 : 2 * p;
-    const int flags = p == c ? 1 : p < a.ctas ? a.part_desc[slot].w : 0;  // 0: a CTA without units
-    const unsigned ends = __ballot_sync(~0u, flags & 2);
-    more = !ends;
-    const unsigned upto = ends ? (ends & -ends) * 2 - 1 : ~0u;
-    unsigned on = __ballot_sync(~0u, flags & 1) & upto;
-    const bool mine = on >> lane & 1;
-    const float pm = mine ? piece_stats(a, slot, rr)[0] : -INFINITY, pl = mine ? piece_stats(a, slot, rr)[1] : 0.f;
-    float top = fmaxf(m, pm);
-#pragma unroll
-    for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    // a NaN is dropped from the maximum, but the sums carry it
-    const float base = top == -INFINITY ? 0.f : top, turn = exp2f(m - base), w = mine ? exp2f(pm - base) : 0.f;
-    float sum = mine ? pl * w : 0.f;
-#pragma unroll
-    for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
-    l = l * turn + sum, m = top;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] *= turn;
-    while (on) {
-      float v[kJoinAhead][8], wt[kJoinAhead];
-#pragma unroll
-      for (int u = 0; u < kJoinAhead; ++u) {
-        wt[u] = 0.f;
-        const int q = on ? __ffs(on) - 1 : -1;
-        on &= on - 1;
-        const float f = __shfl_sync(~0u, w, q & 31);
-        const int from = __shfl_sync(~0u, slot, q & 31);
-        if (q < 0) continue;
-        wt[u] = f;
-        const float *src = piece_values(a, from, rr) + lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = lane + 32 * i < D ? src[32 * i] : 0.f;
-      }
-#pragma unroll
-      for (int u = 0; u < kJoinAhead; ++u)
-        if (wt[u] != 0.f)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[u][i], wt[u], acc[i]);
+  const int part = begun.y - block_of(a, begun.y) * a.parts, kv0 = block_of(a, begun.y) * a.hb, each = a.tq * a.gh;
+  if (threadIdx.x < 32) {
+    int n = 1;
+    if (lane == 0) slots_s[0] = 2 * c + 1;
+    for (int p0 = c + 1; p0 < a.ctas; p0 += 32) {
+      const int p = p0 + lane, flags = p < a.ctas ? a.part_desc[2 * p].w : 0;  // 0: a CTA without units
+      const unsigned ends = __ballot_sync(~0u, flags & 2), upto = ends ? (ends & -ends) * 2 - 1 : ~0u;
+      const unsigned on = __ballot_sync(~0u, flags & 1) & upto;
+      if (on >> lane & 1) slots_s[n + __popc(on & ((1u << lane) - 1))] = 2 * p;
+      n += __popc(on);
+      if (ends) break;
     }
+    if (lane == 0) count_s = n;
+  } else if (threadIdx.x == 32) {
+    const Seq s(a, begun.x);
+    rows_s = rows_of(a, s, 0, part, begun.z);
   }
+  __syncthreads();
+  const Rows rows = rows_s;
+  const int count = count_s, at = threadIdx.x % L, c0 = 8 * at, D = a.v.head_dim;
+#pragma unroll 1
+  for (int i = threadIdx.x / L; i < kJoinRows; i += kJoinThreads / L) {
+    const int rr = blockIdx.y * kJoinRows + i, hl = rr / each, r = rr - hl * each;
+    const bool real = rr < a.part_rows && kv0 + hl < a.k.heads && r < rows.n;
+    float m = -INFINITY, l = 0.f, v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (lane + 32 * i < D) x_s[warp][lane + 32 * i] = acc[i];
-  __syncwarp();
-  warp_finish(a, x_s[warp], m, l, rows.q_row(r), rows.q_head(r));
+    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    if (__any_sync(~0u, real)) {
+      for (int p0 = 0; p0 < count; p0 += L) {
+        const int n = count - p0 < L ? count - p0 : L;
+        const int slot = slots_s[p0 + (at < n ? at : 0)];
+        const bool mine = real && at < n;
+        const float2 st = mine ? *reinterpret_cast<const float2 *>(piece_stats(a, slot, rr)) : make_float2(-INFINITY, 0.f);
+        float top = fmaxf(m, st.x);
+#pragma unroll
+        for (int o = 1; o < L; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        // a NaN is dropped from the maximum, but the sums carry it
+        const float base = top == -INFINITY ? 0.f : top, turn = exp2f(m - base), w = mine ? exp2f(st.x - base) : 0.f;
+        float sum = mine ? st.y * w : 0.f;
+#pragma unroll
+        for (int o = 1; o < L; o *= 2) sum += __shfl_xor_sync(~0u, sum, o);
+        l = l * turn + sum, m = top;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= turn;
+        for (int p = 0; p < n; p += kJoinAhead) {
+          float4 x[kJoinAhead][2];
+#pragma unroll
+          for (int u = 0; u < kJoinAhead; ++u)
+            if (p + u < n && real && c0 < D) {
+              const float4 *src = reinterpret_cast<const float4 *>(piece_values(a, slots_s[p0 + p + u], rr) + c0);
+              x[u][0] = src[0], x[u][1] = src[1];
+            }
+#pragma unroll
+          for (int u = 0; u < kJoinAhead; ++u) {
+            const float f = __shfl_sync(~0u, w, (p + u) % L, L);
+            if (p + u < n && real && c0 < D && f != 0.f) {
+              const float4 y = x[u][0], z = x[u][1];
+              v[0] = fmaf(y.x, f, v[0]), v[1] = fmaf(y.y, f, v[1]), v[2] = fmaf(y.z, f, v[2]), v[3] = fmaf(y.w, f, v[3]);
+              v[4] = fmaf(z.x, f, v[4]), v[5] = fmaf(z.y, f, v[5]), v[6] = fmaf(z.z, f, v[6]), v[7] = fmaf(z.w, f, v[7]);
+            }
+          }
+        }
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= inv;
+      rotate_lanes<L>(v, a.v.had_block, a.unit_v, lane);
+    }
+    if (!real || c0 >= D) continue;
+    const int64_t row = rows.q_row(r), head = rows.q_head(r) + (kv0 + hl) * a.grp, to = (row * a.q_heads + head) * D + c0;
+    if (a.f32) {
+      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(a.out) + to);
+      dst[0] = io<float>::pack(v), dst[1] = io<float>::pack(v + 4);
+    } else {
+      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + to) = io<__nv_bfloat16>::pack(v);
+    }
+    if (a.lse && at == 0) a.lse[row * a.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
 }
 
 size_t any_smem(int D) {
@@ -357,12 +381,13 @@ cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
   }
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas, (unsigned)cdiv(a.part_rows, kJoinThreads / 32)), cfg.blockDim = dim3(kJoinThreads), cfg.stream = s;
+  cfg.gridDim = dim3(a.ctas, (unsigned)cdiv(a.part_rows, kJoinRows)), cfg.blockDim = dim3(kJoinThreads), cfg.stream = s;
+  cfg.dynamicSmemBytes = a.ctas * sizeof(int);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel, a);
+  return cudaLaunchKernelEx(&cfg, D <= 64 ? attention_join_kernel<8> : D <= 128 ? attention_join_kernel<16> : attention_join_kernel<32>, a);
 }
 
 }  // namespace qwha

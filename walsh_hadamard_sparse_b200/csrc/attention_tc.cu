@@ -15,8 +15,8 @@
 // rounded to 11 bits as in attention_mma.cuh, and the maximum is kept to within
 // what f16 leaves room for: a tile whose weights sum to more than 2^9 has its
 // maximum taken and is done again, others need none.
-//   4 warps  unpack: a lane's 32 codes of a token, fetched a tile ahead, to two
-//            swizzled tiles of f16 (keys and values, two of each).
+//   8 warps  unpack, four the keys and four the values: a lane's 32 codes of a
+//            token, fetched a tile ahead, to swizzled tiles of f16 (two of each).
 //   8 warps  softmax: four for each tile of rows.
 //   1 warp   issues the products: S_w of the next tokens behind O_w of these, so
 //            that one tile of rows is multiplied while the other's weights are
@@ -38,12 +38,11 @@ namespace {
 using namespace attn;
 using bulk::saddr;
 using wide::arrive;
-using wide::calm_wait;
 using wide::commit;
 using wide::sw128;
 
-constexpr int kRowsTile = 128, kKeys = 128, kUnpackWarps = 4, kSoftWarps = 8;
-constexpr int kTcThreads = (kUnpackWarps + kSoftWarps + 1) * 32;
+constexpr int kRowsTile = 128, kKeys = 128, kUnpackWarps = 8, kSoftWarps = 8;  // (unpacking: half for the keys)
+constexpr int kUnpackers = kUnpackWarps * 16, kRounds = 128 / kUnpackers * 2, kTcThreads = (kUnpackWarps + kSoftWarps + 1) * 32;
 constexpr int kScaleSlots = 4;      // tiles whose scales are kept: a tile's are read until its weights are made
 constexpr float kTcTop = 64.f;      // of a value's scale in f16; times kTcSum below the largest f16
 constexpr float kTcSum = 512.f;     // of a tile's weights, before its maximum is taken again
@@ -101,6 +100,40 @@ __device__ __forceinline__ void stores_done() { asm volatile("tcgen05.wait::st.s
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
+__device__ __forceinline__ void store8(uint32_t at, const float *v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "r"(at)
+               : "memory");
+}
+// Eight columns from `at` on of every 32 of a row.
+template <int DP>
+__device__ __forceinline__ void load_across(uint32_t at, float *v) {
+  uint32_t u[32];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    if (x < DP / 32) load8(at + 32 * x, u + 8 * x);
+    else
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[8 * x + k] = 0;
+  }
+  loads_done(u);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(u[k]);
+}
+// Sixteen columns, and the wait for them: no memory but TMEM, so that the compiler may move other loads past them.
+__device__ __forceinline__ void columns16(uint32_t at, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void columns_done(float *v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
+
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 both(float a, float b) {
   f32x2 d;
@@ -124,6 +157,31 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   return d;
 }
 
+// Butterflies of the places H, 2 H, ... below N H of 32 values, those below had.
+template <int H, int N>
+__device__ __forceinline__ void rotate32(float *v, int had) {
+#pragma unroll
+  for (int h = H; h < H * N; h *= 2)
+    if (had > h) {
+      if (h == 1) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float x = v[i], y = v[i + 1];
+          v[i] = x + y, v[i + 1] = x - y;
+        }
+      } else {  // two at once
+        const f32x2 minus = both(-1.f, -1.f);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+          if (!(i & h)) {
+            const f32x2 x = both(v[i], v[i + 1]), y = both(v[i + h], v[i + h + 1]);
+            split(add2(x, y), v[i], v[i + 1]);
+            split(fma2(y, minus, x), v[i + h], v[i + h + 1]);
+          }
+      }
+    }
+}
+
 // Scales of a tile of tokens, as the softmax threads read them.
 struct alignas(16) TileScales {
   float k[kKeys], v[kKeys];  // of the scores; of the weights, times c
@@ -140,7 +198,29 @@ struct TcSmem {
   static constexpr int kBars = kScales + kScaleSlots * (int)sizeof(TileScales), kTotal = kBars + 256 + 1024;
 };
 // barriers
-enum { kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kOFull = 12, kQReady = 14, kBarCount = 16 };
+enum { kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kOFull = 12, kQReady = 14, kScFull = 16, kBarCount = 20 };
+
+// Waits for a phase of a barrier, suspended for up to a microsecond at a time; false after two seconds.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+  uint64_t begin = 0;
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity), "r"(1000u)
+          : "memory");
+      if (ok) return true;
+    }
+    const uint64_t now = bulk::now_ns();
+    if (begin == 0) begin = now;
+    else if (now - begin > bulk::kWaitNs) return false;
+  }
+}
 
 // A segment's geometry, as every role works it out.
 struct Segment {
@@ -197,35 +277,40 @@ __device__ __forceinline__ uint2 chunk_of(const uint32_t *w, int x) {
   return make_uint2(v & 0xffffffu, 0);
 }
 
-// The unpacking warps: tokens of a segment to tiles of f16.
-template <int DP, int BK, int BV>
+// The unpacking warps of the keys or of the values: a segment's tokens to tiles of
+// f16. Two lanes have a token, 32 channels each of a slab of 64; a lane has a token
+// in each of kRounds runs of 16.
+template <int DP, int B>
 struct Unpacker {
   static constexpr int kSlabs = DP / 64;
   using S = TcSmem<DP>;
   const AttnArgs &a;
+  const qwha_cache &c;
+  const bool values;
   uint8_t *smem;
   uint32_t bars, one;
   bool ok = true;
-  uint32_t it = 0;      // tiles so far
-  uint32_t k[2][kSlabs][BK], v[2][kSlabs][BV];  // raw codes of the next tile
-  float ks[2], vs[2];        // scales: the largest of the token, finite or of bad
-  __half kr[2][kSlabs], vr[2][kSlabs];  // this lane's groups' share of it
-  uint8_t kz[2][kSlabs], vz[2][kSlabs], bad[2];
-  bool on[2];
+  uint32_t it = 0;           // tiles so far
+  uint32_t w[kRounds][kSlabs][B];  // raw codes of the next tile's tokens
+  float most[kRounds];       // scales: the largest of a token; no number where the keys have a bad group
+  uint32_t share[kRounds][kSlabs];  // the lane's groups' part of it, two f16
+  uint8_t zero[kRounds][kSlabs], bad[kRounds];
+  bool on[kRounds];
 
-  __device__ __forceinline__ Unpacker(const AttnArgs &a_, uint8_t *smem_, uint32_t bars_, uint32_t one_)
-      : a(a_), smem(smem_), bars(bars_), one(one_) {}
+  __device__ __forceinline__ Unpacker(const AttnArgs &a_, bool values_, uint8_t *smem_, uint32_t bars_, uint32_t one_)
+      : a(a_), c(values_ ? a_.v : a_.k), values(values_), smem(smem_), bars(bars_), one(one_) {}
 
   // The token's largest scale, the shares of the lane's groups, which groups are no numbers.
-  __device__ __forceinline__ void scales(const qwha_cache &c, int64_t row, int ng, float *most, __half *share, uint8_t *zero,
-                                         uint8_t *bad_groups) {
+  __device__ __forceinline__ void scales(int64_t row, int ng, int r) {
     const float *s = c.scales + row * ng;
     const uint8_t *z = c.zeros + row * ng;
     const int half = threadIdx.x & 1;
+    bad[r] = 0;
     if (ng == 1) {
-      *most = __ldg(s), *bad_groups = 0;
+      most[r] = __ldg(s);
+      const uint8_t z0 = __ldg(z);
 #pragma unroll
-      for (int i = 0; i < kSlabs; ++i) share[i] = __float2half_rn(1.f), zero[i] = __ldg(z);
+      for (int i = 0; i < kSlabs; ++i) zero[r][i] = z0;
       return;
     }
     float all[4], top = 0.f;
@@ -237,43 +322,39 @@ struct Unpacker {
       else b |= 1 << i, all[i] = 0.f;
     }
     const float inv = top > 0.f ? 1.f / top : 0.f;
-    *most = top, *bad_groups = (uint8_t)b;
+    most[r] = b && !values ? __int_as_float(0x7fc00000) : top, bad[r] = (uint8_t)b;
 #pragma unroll
     for (int i = 0; i < kSlabs; ++i) {
       const int d = 64 * i + 32 * half, g = d < c.head_dim ? d / c.group : 0;
-      const float mine = g == 0 ? all[0] : g == 1 ? all[1] : g == 2 ? all[2] : all[3];
-      share[i] = __float2half_rn(mine * inv), zero[i] = __ldg(z + g);
+      const float mine = (g == 0 ? all[0] : g == 1 ? all[1] : g == 2 ? all[2] : all[3]) * inv;
+      share[r][i] = pair16(mine, mine), zero[r][i] = __ldg(z + g);
     }
   }
 
-  template <int B>
-  __device__ __forceinline__ void write(uint8_t *tile, int token, int slab, const uint32_t *w, uint32_t zero, __half share,
-                                        bool scaled, bool live) {
+  __device__ __forceinline__ void write(uint8_t *row, int token, int r, int i, bool scaled, bool live) {
     Zero<B> z;
-    z.set((zero | 0xe400u) * 0x10001u);
-    const uint32_t f = (uint32_t)__half_as_ushort(share) * 0x10001u;
+    z.set((zero[r][i] | 0xe400u) * 0x10001u);
     const int half = threadIdx.x & 1;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      uint32_t r[4] = {0, 0, 0, 0};
+      uint32_t v[4] = {0, 0, 0, 0};
       if (live) {
-        unpack_row<B>(chunk_of<B>(w, x), z, one, r);
+        unpack_row<B>(chunk_of<B>(w[r][i], x), z, one, v);
         if (scaled)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __half2 p = __hmul2(reinterpret_cast<const __half2 &>(r[i]), reinterpret_cast<const __half2 &>(f));
-            r[i] = reinterpret_cast<const uint32_t &>(p);
+          for (int k = 0; k < 4; ++k) {
+            const __half2 p = __hmul2(reinterpret_cast<const __half2 &>(v[k]), reinterpret_cast<const __half2 &>(share[r][i]));
+            v[k] = reinterpret_cast<const uint32_t &>(p);
           }
       }
-      *reinterpret_cast<uint4 *>(tile + slab * (kKeys * 128) + token * 128 + (((4 * half + x) ^ (token & 7)) << 4)) =
-          make_uint4(r[0], r[1], r[2], r[3]);
+      *reinterpret_cast<uint4 *>(row + (((4 * half + x) ^ (token & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
 
-  __device__ __forceinline__ void wait(int bar, uint32_t parity) { ok = ok && wide::warp_wait(bars + 8 * bar, parity); }
+  __device__ __forceinline__ void wait(int bar, uint32_t parity) { ok = ok && wait_for(bars + 8 * bar, parity); }
 
-  __device__ __forceinline__ void run(const Segment &g, const Place &at, float *c_now) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = lane & 1, D = a.k.head_dim, ng = D / a.k.group;
+  __device__ __forceinline__ void run(const Segment &g, const Place &at) {
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % (kUnpackWarps / 2), half = lane & 1, D = c.head_dim, ng = D / c.group;
     const int32_t *table = a.pages + (int64_t)at.b * a.max_pages;
     // which new tokens of a tree any row of the tile sees
     unsigned long long seen = ~0ull;
@@ -283,133 +364,105 @@ struct Unpacker {
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) seen |= __shfl_xor_sync(~0u, seen, o);
     }
-    const int past = g.s.past;
-    auto slot_at = [&](int t) -> int64_t {
-      if (t >= g.length) return -1;
-      const int pg = page_of(a, t);
-      const int page = table[pg];
-      if ((uint32_t)page >= (uint32_t)a.k.n_pages) {
-        atomicOr(a.err, kErrPage);
-        return -1;
+    const int past = g.s.past, mine = warp * (16 * kRounds) + (lane >> 1);
+    int t0 = at.unit * kKeys + mine;
+    int page[kRounds];
+    // the pages of the lane's tokens, which are within the table, since lengths are cut there; -2 where there is none to
+    // fetch. They are used a tile later.
+    auto ask = [&](bool any) {
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const int t = t0 + 16 * r;
+        page[r] = !any || t >= g.length || (a.tree && t >= past && !(seen >> (t - past) & 1)) ? -2 : __ldg(table + page_of(a, t));
       }
-      if (a.tree && t >= past && !(seen >> (t - past) & 1)) return -1;
-      return (int64_t)page * a.k.page_size + (t - pg * a.k.page_size);
     };
-    const int mine = warp * 32 + (lane >> 1);  // token of round 0; 16 more in round 1
-    int64_t slot[2];
-    int t0 = at.unit * kKeys;
-    auto look_up = [&] {
+    auto fetch = [&] {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) slot[r] = slot_at(t0 + mine + 16 * r);
-    };
-    // keys' codes and all scales; values' codes
-    auto fetch_keys = [&] {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        on[r] = slot[r] >= 0;
-        ks[r] = vs[r] = 0.f, bad[r] = 0;
-        if (!on[r]) continue;
-        const int64_t row = slot[r] * a.k.heads + g.kv;
+      for (int r = 0; r < kRounds; ++r) {
+        on[r] = (uint32_t)page[r] < (uint32_t)a.k.n_pages;
+        most[r] = 0.f, bad[r] = 0;
+        if (!on[r]) {
+          if (page[r] != -2) atomicOr(a.err, kErrPage);
+          continue;
+        }
+        const int t = t0 + 16 * r;
+        const int64_t row = ((int64_t)page[r] * a.k.page_size + (t - page_of(a, t) * a.k.page_size)) * c.heads + g.kv;
+        const uint8_t *src = c.codes + row * (D / 8 * B) + half * (4 * B);
 #pragma unroll
         for (int i = 0; i < kSlabs; ++i)
-          if (32 * (2 * i + half) < D) fetch_codes<BK>(a.k.codes + row * (D / 8 * BK) + (2 * i + half) * (4 * BK), k[r][i]);
-        uint8_t k_bad;
-        scales(a.k, row, ng, &ks[r], kr[r], kz[r], &k_bad);
-        scales(a.v, row, ng, &vs[r], vr[r], vz[r], &bad[r]);
-        if (k_bad) ks[r] = __int_as_float(0x7fc00000);
+          if (32 * (2 * i + half) < D) fetch_codes<B>(src + i * (8 * B), w[r][i]);
+        scales(row, ng, r);
       }
     };
-    auto fetch_values = [&](const int64_t *from) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (from[r] < 0) continue;
-        const int64_t row = from[r] * a.k.heads + g.kv;
-#pragma unroll
-        for (int i = 0; i < kSlabs; ++i)
-          if (32 * (2 * i + half) < D) fetch_codes<BV>(a.v.codes + row * (D / 8 * BV) + (2 * i + half) * (4 * BV), v[r][i]);
-      }
-    };
-    look_up();
-    fetch_keys();
-    fetch_values(slot);
+    ask(true);
+    fetch();
     t0 += kKeys;
-    if (g.run > 1) look_up();  // (only of tokens that the run has: each page that is none is reported once a run)
+    ask(g.run > 1);
+    float factor = kNoScale;  // of the values' scales: follows the largest met by any of the warps
+    uint8_t *tiles = smem + (values ? S::kV : S::kK);
     for (int u = 0; u < g.run; ++u, ++it) {
       const int st = it & 1;
-      const uint32_t phase = (it >> 1 & 1) ^ 1;
-      uint8_t *k_tile = smem + S::kK + st * S::kTile, *v_tile = smem + S::kV + st * S::kTile;
       TileScales &sc = *reinterpret_cast<TileScales *>(smem + S::kScales + (it % kScaleSlots) * sizeof(TileScales));
-      // the factor of the values' scales: follows the largest met, over the four warps
-      float top = 0.f;
+      if (values) {
+        float top = 0.f;
+        int any_bad_lane = 0;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float x = fabsf(vs[r]);
-        if (x < INFINITY) top = fmaxf(top, x);
+        for (int r = 0; r < kRounds; ++r) top = fmaxf(top, fabsf(most[r]) < INFINITY ? fabsf(most[r]) : 0.f), any_bad_lane |= bad[r];
+        const int flags = any_of(top * factor > kTcTop);
+        if (flags) {
+          uint32_t *top_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount + 16);
+          if (threadIdx.x % kUnpackers == 0) *top_s = 0;
+          meet();
+          atomicMax(top_s, __float_as_uint(top));
+          meet();
+          int e = 127 + 6 - ((int)(*top_s >> 23) - 127 + 2);
+          e = e < 1 ? 1 : e > 247 ? 247 : e;
+          factor = fminf(factor, __uint_as_float((uint32_t)e << 23));
+          meet();
+        }
+        const int any_bad = ng > 1 ? any_of(any_bad_lane) : 0;
+        if (threadIdx.x % kUnpackers == 0) sc.c = factor, sc.bad = any_bad;
       }
-      const bool up = __any_sync(~0u, top * *c_now > kTcTop);
-      int any = 0;
-      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, 2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-                   : "=r"(any)
-                   : "r"((int)up)
-                   : "memory");
-      if (any) {
-        uint32_t *top_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount + 16);
-        if (threadIdx.x == 0) *top_s = 0;
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        atomicMax(top_s, __float_as_uint(top));
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        int e = 127 + 6 - ((int)(*top_s >> 23) - 127 + 2);
-        e = e < 1 ? 1 : e > 247 ? 247 : e;
-        *c_now = fminf(*c_now, __uint_as_float((uint32_t)e << 23));
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-      }
-      wait(kKEmpty + st, phase);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int r = 0; r < kRounds; ++r) {
         const int token = mine + 16 * r;
-        const unsigned b = __ballot_sync(~0u, on[r]);  // two lanes a token
-        if (half == 0) sc.k[token] = ks[r], sc.v[token] = vs[r] * *c_now, sc.groups[token] = bad[r];
+        if (values) {
+          if (half == 0) sc.v[token] = most[r] * factor, sc.groups[token] = bad[r];
+          continue;
+        }
+        const unsigned b = __ballot_sync(~0u, on[r]);
+        if (half == 0) sc.k[token] = most[r];
         if (lane == 0) {
           unsigned x = b & 0x55555555u;  // the even bits together
           x = (x | x >> 1) & 0x33333333u, x = (x | x >> 2) & 0x0f0f0f0fu, x = (x | x >> 4) & 0x00ff00ffu, x = (x | x >> 8) & 0xffffu;
-          reinterpret_cast<uint16_t *>(sc.live)[warp * 2 + r] = (uint16_t)x;
+          reinterpret_cast<uint16_t *>(sc.live)[warp * kRounds + r] = (uint16_t)x;
         }
+      }
+      arrive(bars + 8 * (kScFull + it % kScaleSlots));
+      wait((values ? kVEmpty : kKEmpty) + st, (it >> 1 & 1) ^ 1);
+      uint8_t *tile = tiles + st * S::kTile + mine * 128;
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r)
 #pragma unroll
         for (int i = 0; i < kSlabs; ++i)
-          write<BK>(k_tile, token, i, k[r][i], kz[r][i], kr[r][i], ng > 1, on[r] && 32 * (2 * i + half) < D);
-      }
-      int any_bad = 0;
-      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, 2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-                   : "=r"(any_bad)
-                   : "r"((int)(bad[0] | bad[1]))
-                   : "memory");
-      if (threadIdx.x == 0) sc.c = *c_now, sc.bad = any_bad;
+          write(tile + i * (kKeys * 128) + r * (16 * 128), mine, r, i, ng > 1, on[r] && 32 * (2 * i + half) < D);
       bulk::fence_proxy();
-      arrive(bars + 8 * (kKFull + st));
-      // the next tile's keys and scales are on their way while this one's values are unpacked, and so on
-      uint8_t zero[2][kSlabs];
-      __half share[2][kSlabs];
-      const bool was[2] = {on[0], on[1]};
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int i = 0; i < kSlabs; ++i) zero[r][i] = vz[r][i], share[r][i] = vr[r][i];
-      const int64_t next[2] = {slot[0], slot[1]};
-      if (u + 1 < g.run) {
-        fetch_keys();
+      arrive(bars + 8 * ((values ? kVFull : kKFull) + st));
+      if (u + 1 < g.run) {  // the next tile's codes are on their way while this one is multiplied
+        fetch();
         t0 += kKeys;
-        if (u + 2 < g.run) look_up();
+        ask(u + 2 < g.run);
       }
-      wait(kVEmpty + st, phase);
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int i = 0; i < kSlabs; ++i)
-          write<BV>(v_tile, mine + 16 * r, i, v[r][i], zero[r][i], share[r][i], ng > 1, was[r] && 32 * (2 * i + half) < D);
-      if (u + 1 < g.run) fetch_values(next);
-      bulk::fence_proxy();
-      arrive(bars + 8 * (kVFull + st));
     }
+  }
+  __device__ __forceinline__ static void meet() { asm volatile("bar.sync 2, %0;" ::"n"(kUnpackers) : "memory"); }
+  __device__ __forceinline__ static int any_of(int x) {  // whether it is true of any unpacking thread
+    int any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, 2, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"(x), "n"(kUnpackers)
+                 : "memory");
+    return any;
   }
 };
 
@@ -424,11 +477,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
   constexpr int kIssue = kUnpackWarps + kSoftWarps;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      bulk::init(bars + 8 * (kKFull + i), kUnpackWarps * 32), bulk::init(bars + 8 * (kVFull + i), kUnpackWarps * 32);
+      bulk::init(bars + 8 * (kKFull + i), kUnpackers), bulk::init(bars + 8 * (kVFull + i), kUnpackers);
       bulk::init(bars + 8 * (kKEmpty + i), 1), bulk::init(bars + 8 * (kVEmpty + i), 1);
       bulk::init(bars + 8 * (kSFull + i), 1), bulk::init(bars + 8 * (kOFull + i), 1);
       bulk::init(bars + 8 * (kPReady + i), 128), bulk::init(bars + 8 * (kQReady + i), 128);
     }
+    for (int i = 0; i < kScaleSlots; ++i) bulk::init(bars + 8 * (kScFull + i), kUnpackWarps * 32);
     bulk::fence_init();
   }
   if (warp == kIssue) {
@@ -445,9 +499,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
 
   if (warp < kUnpackWarps) {
     // ------------------------------------------------------------ unpacking
-    auto work = [&](auto bk, auto bv) {
-      Unpacker<DP, decltype(bk)::value, decltype(bv)::value> unpack(a, smem, bars, one);
-      float c = kNoScale;
+    const bool values = warp >= kUnpackWarps / 2;
+    auto work = [&](auto bits) {
+      Unpacker<DP, decltype(bits)::value> unpack(a, values, smem, bars, one);
       while (left > 0) {
         const Segment g(a, at, left);
         if (g.s.rows == 0) {
@@ -455,36 +509,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
           continue;
         }
         if (threadIdx.x == 0 && (long long)g.s.past + (a.tree && g.s.rows > 64 ? 64 : g.s.rows) > a.cap) atomicOr(a.err, kErrPage);
-        c = kNoScale;
-        unpack.run(g, at, &c);
+        unpack.run(g, at);
         g.next(a, &at, &left);
       }
-      if (!unpack.ok && lane == 0) atomicOr(a.err, kErrTc);
+      if (!unpack.ok) atomicOr(a.err, kErrTc);
     };
-    using std::integral_constant;
-    auto keys = [&](auto bk) {
-      switch (a.v.bits) {
-        case 2: work(bk, integral_constant<int, 2>()); break;
-        case 3: work(bk, integral_constant<int, 3>()); break;
-        case 4: work(bk, integral_constant<int, 4>()); break;
-        default: work(bk, integral_constant<int, 8>());
-      }
-    };
-    switch (a.k.bits) {
-      case 2: keys(integral_constant<int, 2>()); break;
-      case 3: keys(integral_constant<int, 3>()); break;
-      case 4: keys(integral_constant<int, 4>()); break;
-      default: keys(integral_constant<int, 8>());
+    switch (values ? a.v.bits : a.k.bits) {
+      case 2: work(std::integral_constant<int, 2>()); break;
+      case 3: work(std::integral_constant<int, 3>()); break;
+      case 4: work(std::integral_constant<int, 4>()); break;
+      default: work(std::integral_constant<int, 8>());
     }
   } else if (warp < kIssue) {
     // ------------------------------------------------------------ softmax: a row a thread
     const int w = (warp - kUnpackWarps) / 4, r = (warp & 3) * 32 + lane;  // tile of rows; row of it (TMEM lane)
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // (unpacking takes four warps: warp % 4 is the quarter)
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // (unpacking takes whole groups of four warps: warp % 4 is the quarter)
     const uint32_t s_at = tmem + lanes + 128 * w, o_at = tmem + lanes + 256 + 128 * w;
     uint8_t *q_tile = smem + S::kQ + w * S::kTile;
     bool ok = true;
     uint32_t it = 0, slot = 0, segment = 0;  // tiles of this tile of rows, and of the CTA; segments with rows in it
-    auto wait = [&](int bar, uint32_t parity) { ok = ok && wide::warp_wait(bars + 8 * bar, parity); };
+    auto wait = [&](int bar, uint32_t parity) { ok = ok && wait_for(bars + 8 * bar, parity); };
     while (left > 0) {
       const Segment g(a, at, left);
       if (g.s.rows == 0) {
@@ -494,65 +538,78 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
       const int n = g.rows.n - 128 * w;  // rows of this tile
       const int out_slot = 2 * blockIdx.x + (g.starts ? 1 : 0);
       if (n > 0) {
-        // ---- queries: 2^15 near the row's largest, rotated, eight channels a lane
-        constexpr int L = DP / 8, kAtOnce = 32 / L;
-        const int c = lane % L, D = a.k.head_dim;
-        float f = 1.f;
+        // ---- queries: 2^15 near the row's largest, rotated; S's columns keep what registers do not
+        const int rr = 128 * w + r, D = a.k.head_dim, had = a.k.had_block;
+        const bool real = r < n;
+        const __nv_bfloat16 *q_row = static_cast<const __nv_bfloat16 *>(a.q) +
+                                     (real ? g.rows.q_row(rr) * a.q_stride + (int64_t)g.rows.q_head(rr) * D : 0);
+        float top = 0.f;
 #pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += 4 * kAtOnce) {
-          uint4 x[4];
+        for (int x = 0; x < DP / 32; ++x) {
+          float v[32];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const int i = (warp & 3) * 32 + r0 + p * kAtOnce + lane / L;
-            x[p] = make_uint4(0, 0, 0, 0);
-            if (i < n && c * 8 < D)
-              x[p] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + g.rows.q_row(128 * w + i) * a.q_stride +
-                                                           (int64_t)g.rows.q_head(128 * w + i) * D + c * 8));
+          for (int i = 0; i < 4; ++i) {
+            const bool in = real && 32 * x < D;  // (whole runs of 32)
+            io<__nv_bfloat16>::unpack(in ? __ldg(reinterpret_cast<const uint4 *>(q_row + 32 * x) + i) : make_uint4(0, 0, 0, 0), v + 8 * i);
           }
+          rotate32<1, 32>(v, had);
+          uint32_t u[32];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const int in = r0 + p * kAtOnce + lane / L, i = (warp & 3) * 32 + in;
-            float v[8];
-            io<__nv_bfloat16>::unpack(x[p], v);
-            rotate_lanes<L>(v, a.k.had_block, a.unit_k, lane);
-            float top = 0.f;
+          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i]), top = fmaxf(top, fabsf(v[i]));
+          store32(s_at + 32 * x, u);
+        }
+        stores_done();
+        if (had > 32) {
+          top = 0.f;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            float v[32];
+            load_across<DP>(s_at + 8 * i, v);
+            rotate32<8, 4>(v, had / 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= a.scale2, top = fmaxf(top, fabsf(v[k]));
+            for (int k = 0; k < 32; ++k) top = fmaxf(top, fabsf(v[k]));
 #pragma unroll
-            for (int o = 1; o < L; o *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-            const uint32_t bits = __float_as_uint(top);
-            int e = (int)(bits >> 23) - 127 + 1;
-            e = bits == 0 || bits >= 0x7f800000u ? 0 : e < -100 ? -100 : e;
-            const float up = __uint_as_float((uint32_t)(127 + 15 - e) << 23);
+            for (int x = 0; x < DP / 32; ++x) store8(s_at + 32 * x + 8 * i, v + 8 * x);
+          }
+          stores_done();
+        }
+        const float by_q = a.scale2 * (had > 1 ? a.unit_k : 1.f);
+        const uint32_t top_bits = __float_as_uint(fabsf(top * by_q));
+        int e = (int)(top_bits >> 23) - 127 + 1;
+        e = top_bits == 0 || top_bits >= 0x7f800000u ? 0 : e < -100 ? -100 : e;
+        const float up = __uint_as_float((uint32_t)(127 + 15 - e) << 23), f = __uint_as_float((uint32_t)(127 - 15 + e) << 23);
+#pragma unroll 1
+        for (int x = 0; x < DP / 32; ++x) {
+          uint32_t u[32];
+          load32(s_at + 32 * x, u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
             uint32_t h[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = pair16(v[k] * up, v[k + 4] * up);
-            *reinterpret_cast<uint4 *>(q_tile + (c >> 3) * (kRowsTile * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4)) =
+            for (int k = 0; k < 4; ++k)
+              h[k] = pair16(__uint_as_float(u[8 * i + k]) * by_q * up, __uint_as_float(u[8 * i + k + 4]) * by_q * up);
+            *reinterpret_cast<uint4 *>(q_tile + (x >> 1) * (kRowsTile * 128) + r * 128 + (((4 * (x & 1) + i) ^ (r & 7)) << 4)) =
                 make_uint4(h[0], h[1], h[2], h[3]);
-            // the lane whose row this is keeps its factor
-            const float down = __uint_as_float((uint32_t)(127 - 15 + e) << 23);
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-              const float other = __shfl_sync(~0u, down, k * L);
-              if (lane == r0 + p * kAtOnce + k) f = other;
-            }
           }
         }
+        fence_before();
         bulk::fence_proxy();
         arrive(bars + 8 * (kQReady + w));
 
         // ---- what the row sees
-        const int rr = 128 * w + r, j = g.rows.j0 + (r < n ? rr / g.rows.heads : 0);
+        const int j = g.rows.j0 + (real ? rr / g.rows.heads : 0);
         const int past = g.s.past, lim = a.tree ? past : past + j + 1, safe = a.tree ? past : past + g.rows.j0 + 1;
-        const unsigned long long mask = a.tree && r < n ? (unsigned long long)a.tree[g.s.row0 + j] : 0;
+        const unsigned long long mask = a.tree && real ? (unsigned long long)a.tree[g.s.row0 + j] : 0;
         float m = -INFINITY, l = 0.f, c_old = 0.f;
         uint32_t nan_groups = 0;
         int t0 = at.unit * kKeys;
         const f32x2 ff = both(f, f);
         for (int u = 0; u < g.run; ++u, ++it, t0 += kKeys) {
+          const uint32_t tile = slot + u;
+          wait(kScFull + tile % kScaleSlots, tile / kScaleSlots & 1);
           wait(kSFull + w, it & 1);
           fence_after();
-          const TileScales &sc = *reinterpret_cast<const TileScales *>(smem + S::kScales + ((slot + u) % kScaleSlots) * sizeof(TileScales));
+          const TileScales &sc = *reinterpret_cast<const TileScales *>(smem + S::kScales + (tile % kScaleSlots) * sizeof(TileScales));
           const uint4 live = *reinterpret_cast<const uint4 *>(sc.live);
           const bool masked = t0 + kKeys > safe || (live.x & live.y & live.z & live.w) != ~0u;
           uint32_t vis[4] = {live.x, live.y, live.z, live.w};
@@ -571,11 +628,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
               for (int x = 0; x < 4; ++x)
                 if (vis[x] >> t & 1) nan_groups |= sc.groups[32 * x + t];
           }
-          // the largest visible score
-          auto largest = [&] {
+          // the largest visible score of columns 32 first .. 127 (before them lie weights in place of scores)
+          auto largest = [&](int first) {
             float top = -INFINITY;
 #pragma unroll 1
-            for (int x = 0; x < 4; ++x) {
+            for (int x = first; x < 4; ++x) {
               const uint32_t on = x == 0 ? vis[0] : x == 1 ? vis[1] : x == 2 ? vis[2] : vis[3];
               uint32_t v[32];
               load32(s_at + 32 * x, v);
@@ -586,33 +643,44 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             return top * f;
           };
           float turn = 1.f;  // of the sums so far
-          auto raise = [&] {
-            const float top = largest(), now = fmaxf(m, top);
+          auto raise = [&](int first) {
+            const float top = largest(first), now = fmaxf(m, top);
             turn = now == -INFINITY ? 1.f : exp2_fast(m - now);
             m = now;
           };
-          if (u == 0) raise();
-          uint32_t p[64];
-          float sum;
-          auto weights = [&](auto hidden) {
+          // rows that have seen nothing have no maximum yet
+          if (__any_sync(~0u, m == -INFINITY)) {
+            raise(0);
+            if (u == 0) turn = 1.f;
+          }
+          // the weights of columns 64 h .. 64 h + 63, for the maximum as it stands, and their sum
+          float sum = 0.f;
+          uint32_t p[32];
+          auto weights = [&](int h, auto hidden) {
             const float base = m == -INFINITY ? 0.f : m;
             const f32x2 mm = both(-base, -base);
             f32x2 total = 0;
+            float v[2][16];
+            const uint32_t from = s_at + 64 * h;
+            const float4 *k4 = reinterpret_cast<const float4 *>(sc.k + 64 * h), *v4 = reinterpret_cast<const float4 *>(sc.v + 64 * h);
+            columns16(from, v[0]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              uint32_t v[32];
-              load32(s_at + 32 * x, v);
-              const float4 *k4 = reinterpret_cast<const float4 *>(sc.k + 32 * x), *v4 = reinterpret_cast<const float4 *>(sc.v + 32 * x);
+              float *z = v[x & 1];
+              columns_done(z);
+              if (x < 3) columns16(from + 16 * (x + 1), v[(x + 1) & 1]);  // on its way meanwhile
+              uint32_t on = ~0u;
+              if constexpr (decltype(hidden)::value) on = (h ? x >> 1 ? vis[3] : vis[2] : x >> 1 ? vis[1] : vis[0]) >> (16 * (x & 1));
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 kk = k4[i], vv = v4[i];
+              for (int i = 0; i < 4; ++i) {
+                const float4 kk = k4[4 * x + i], vv = v4[4 * x + i];
                 float e[4];
-                split(fma2(mul2(both(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), both(kk.x, kk.y)), ff, mm), e[0], e[1]);
-                split(fma2(mul2(both(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), both(kk.z, kk.w)), ff, mm), e[2], e[3]);
+                split(fma2(mul2(both(z[4 * i], z[4 * i + 1]), both(kk.x, kk.y)), ff, mm), e[0], e[1]);
+                split(fma2(mul2(both(z[4 * i + 2], z[4 * i + 3]), both(kk.z, kk.w)), ff, mm), e[2], e[3]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   e[k] = exp2_fast(e[k]);
-                  if constexpr (decltype(hidden)::value) e[k] = vis[x] >> (4 * i + k) & 1 ? e[k] : 0.f;
+                  if constexpr (decltype(hidden)::value) e[k] = on >> (4 * i + k) & 1 ? e[k] : 0.f;
                 }
                 const f32x2 e01 = both(e[0], e[1]), e23 = both(e[2], e[3]);
                 total = add2(total, add2(e01, e23));
@@ -622,21 +690,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 if constexpr (decltype(hidden)::value)  // a hidden token's scale may be no number
 #pragma unroll
                   for (int k = 0; k < 4; ++k) y[k] = e[k] == 0.f ? 0.f : y[k];
-                p[16 * x + 2 * i] = pair16(y[0], y[1]), p[16 * x + 2 * i + 1] = pair16(y[2], y[3]);
+                p[8 * x + 2 * i] = pair16(y[0], y[1]), p[8 * x + 2 * i + 1] = pair16(y[2], y[3]);
               }
             }
             float s0, s1;
             split(total, s0, s1);
-            sum = s0 + s1;
+            return s0 + s1;
           };
-          auto all_weights = [&] {
-            if (masked) weights(std::true_type());
-            else weights(std::false_type());
-          };
-          for (bool again = u > 0;; again = false) {
-            all_weights();
-            if (!again || !__any_sync(~0u, !(sum <= kTcSum))) break;
-            raise();
+          // One copy of this loop's code for both halves and both tries: more of it does not stay in the instruction
+          // cache (unrolled, 730 us for 4 chunks of 1021 behind 2048, 440 so).
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            float part;
+#pragma unroll 1
+            for (bool again = u > 0;; again = false) {
+              part = masked ? weights(h, std::true_type()) : weights(h, std::false_type());
+              if (!again || !__any_sync(~0u, !(part <= kTcSum / 2))) break;
+              const float before = turn;
+              raise(2 * h);
+              if (h == 1 && __any_sync(~0u, turn != 1.f)) {  // the first half's weights are stored, in the old units
+                uint32_t z[32];
+                stores_done();
+                load32(s_at, z);
+                const uint32_t t2 = pair16(turn, turn);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const __half2 y = __hmul2(reinterpret_cast<const __half2 &>(z[i]), reinterpret_cast<const __half2 &>(t2));
+                  z[i] = reinterpret_cast<const uint32_t &>(y);
+                }
+                store32(s_at, z);
+                sum *= turn;
+              }
+              turn *= before;
+            }
+            sum += part;
+            store32(s_at + 32 * h, p);  // over scores that have been read: the first half's, both times
           }
           // ---- the sums so far in the new units: nothing of this tile of rows is being multiplied now
           const float grow = sc.c * (c_old == 0.f ? 0.f : inverse2(c_old));  // a power of two, at most 1
@@ -654,7 +742,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
           }
           c_old = sc.c;
           l = l * turn + sum;
-          store32(s_at, p), store32(s_at + 32, p + 32);
           stores_done();
           fence_before();
           arrive(bars + 8 * (kPReady + w));
@@ -665,8 +752,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         fence_after();
         const bool done = g.starts && g.ends;
         const float by = inverse2(c_old) * (done ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
-        const int had = done ? a.v.had_block : 0;
-        const bool real = r < n;
+        const int had_v = done ? a.v.had_block : 0;
         const int64_t row = real ? g.rows.q_row(rr) : 0, head = real ? g.rows.q_head(rr) : 0;
         const int DV = a.v.head_dim;
         auto put = [&](int c0, float *v) {  // eight channels from c0 on
@@ -688,19 +774,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
           if (nan_groups && nan_groups >> (32 * x / a.v.group) & 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __int_as_float(0x7fc00000);
-#pragma unroll
-          for (int h = 1; h < 32; h *= 2)
-            if (had > h)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(i & h)) {
-                  const float p = v[i], q = v[i + h];
-                  v[i] = p + q, v[i + h] = p - q;
-                }
-          if (had > 1)
+          rotate32<1, 32>(v, had_v);
+          if (had_v > 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= a.unit_v;
-          if (had > 32) {  // bits 5 and 6 of the channel: once all are back
+          if (had_v > 32) {  // bits 5 and 6 of the channel: once all are back
 #pragma unroll
             for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i]);
             store32(o_at + 32 * x, u);
@@ -709,28 +787,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             for (int i = 0; i < 4; ++i) put(32 * x + 8 * i, v + 8 * i);
           }
         }
-        if (had > 32) {
+        if (had_v > 32) {
           stores_done();
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
-            uint32_t u[32];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (x < DP / 32) load8(o_at + 32 * x + 8 * i, u + 8 * x);
-              else for (int k = 0; k < 8; ++k) u[8 * x + k] = 0;
-            loads_done(u);
             float v[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(u[k]);
-#pragma unroll
-            for (int h = 8; h < 32; h *= 2)
-              if (had > 4 * h)
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (!(k & h)) {
-                    const float p = v[k], q = v[k + h];
-                    v[k] = p + q, v[k + h] = p - q;
-                  }
+            load_across<DP>(o_at + 8 * i, v);
+            rotate32<8, 4>(v, had_v / 4);
 #pragma unroll
             for (int x = 0; x < DP / 32; ++x) put(32 * x + 8 * i, v + 8 * x);
           }
@@ -746,7 +809,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         a.part_desc[out_slot] = make_int4(at.b, at.block, at.tile, g.ends ? 3 : 1);
       g.next(a, &at, &left);
     }
-    if (!ok && lane == 0) atomicOr(a.err, kErrTc);
+    if (!ok) atomicOr(a.err, kErrTc);
   } else {
     // ------------------------------------------------------------ products
     bool ok = true;
@@ -756,7 +819,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
       constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(DP >> 3) << 17) | (8u << 24);
       uint32_t it = 0, tiles[2] = {0, 0}, segment[2] = {0, 0};
       auto wait = [&](int bar, uint32_t parity) {
-        ok = ok && calm_wait(bars + 8 * bar, parity);
+        ok = ok && wait_for(bars + 8 * bar, parity);
         fence_after();
       };
       auto scores = [&](int w, int st) {
