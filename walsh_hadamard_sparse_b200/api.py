@@ -272,14 +272,15 @@ class QCache:
 
     def c_struct(self, dev: int | None = None) -> QwhaCache:
         dev = torch.cuda.current_device() if dev is None else dev
-        if self.scales.dim() != 4:
-            raise ValueError(f"scales: expected 4 dimensions, got {tuple(self.scales.shape)}")
-        n_pages, page_size, heads, groups = self.scales.shape
+        shape = self.scales.shape
+        if len(shape) != 4:
+            raise ValueError(f"scales: expected 4 dimensions, got {tuple(shape)}")
+        n_pages, page_size, heads, groups = shape
         head_dim = groups * self.group
         return QwhaCache(self.bits, self.group, self.had_block, heads, head_dim, page_size, n_pages,
                          _fit("codes", self.codes, torch.uint8, (n_pages, page_size, heads, head_dim * self.bits // 8), dev),
-                         _fit("scales", self.scales, torch.float32, self.scales.shape, dev),
-                         _fit("zeros", self.zeros, torch.uint8, self.scales.shape, dev))
+                         _fit("scales", self.scales, torch.float32, shape, dev),
+                         _fit("zeros", self.zeros, torch.uint8, shape, dev))
 
 
 def cache_alloc(n_pages: int, page_size: int, heads: int, head_dim: int, bits: int = 4, group: int | None = None,
@@ -382,11 +383,13 @@ def _fit_rows(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev:
     """(address, elements from token to token) of rows whose tokens may lie apart: slices of a wider tensor."""
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or (t.numel() and (t.stride(2) != 1 and shape[2] > 1 or t.stride(1) != shape[2] and shape[1] > 1)):
-        raise ValueError(f"{name}: expected a CUDA tensor whose heads are contiguous within a token")
-    if t.get_device() != dev:
+    n, heads, width = shape
+    apart, head, one = t.stride()
+    if t.get_device() != dev or (one != 1 and width > 1 or head != width and heads > 1) and n:
+        if not t.is_cuda or t.get_device() == dev:
+            raise ValueError(f"{name}: expected a CUDA tensor whose heads are contiguous within a token")
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+    return t.data_ptr(), apart if n > 1 else heads * width
 
 
 _STRIDES = (None, i64 * 1, i64 * 2)
@@ -399,28 +402,34 @@ def rotary(x, positions: torch.Tensor, freq: torch.Tensor, interleaved: bool = F
     pairs (c, c + rot/2), or (2c, 2c + 1) with interleaved, of token i turn by positions[i] * freq[c] (int64 [n], fp64
     [rot/2]) and are multiplied by factor; channels from rot on are copied. inverse turns back: the gradient of x from
     that of the result. The tokens of x and out may lie apart (slices of a fused projection); out may be x."""
-    xs, dev, n = (x,) if isinstance(x, torch.Tensor) else tuple(x), torch.cuda.current_device(), positions.shape[0]
+    dev, n, single = torch.cuda.current_device(), positions.shape[0], isinstance(x, torch.Tensor)
+    xs = (x,) if single else tuple(x)
     k = len(xs)
     if not 1 <= k <= 2:
         raise ValueError(f"{k} tensors: one or two")
-    if any(t.dim() != 3 for t in xs):
-        raise ValueError("x: expected [n, heads, head_dim]")
-    dtype, head_dim = xs[0].dtype, xs[0].shape[2]
+    for t in xs:
+        if t.dim() != 3:
+            raise ValueError("x: expected [n, heads, head_dim]")
+    q = xs[0]
+    dtype, _, head_dim = q.dtype, *q.shape[1:]
     if out is None:
-        outs = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs)
+        outs = tuple([t.new_empty(t.shape) for t in xs])
     else:
         outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
         if len(outs) != k:
             raise ValueError(f"{k} tensors and {len(outs)} outputs")
-    shapes = [(n, t.shape[1], head_dim) for t in xs]
-    a = [_fit_rows("x", t, dtype, s, dev) for t, s in zip(xs, shapes)]
-    b = [_fit_rows("out", t, dtype, s, dev) for t, s in zip(outs, shapes)]
-    check(lib().qwha_rotary(_dt(xs[0]), k, _ROWS[k](*(p for p, _ in a)), _STRIDES[k](*(s for _, s in a)),
-                            _ROWS[k](*(p for p, _ in b)), _STRIDES[k](*(s for _, s in b)),
-                            _HEADS[k](*(s[1] for s in shapes)), head_dim, n, _fit("positions", positions, torch.int64, (n,), dev),
-                            _fit("freq", freq, torch.float64, (freq.shape[0],), dev), 2 * freq.shape[0], int(interleaved),
-                            factor, int(inverse), _raw_stream(dev)), "qwha_rotary")
-    return outs[0] if isinstance(x, torch.Tensor) else outs
+    src, src_apart, dst, dst_apart, heads = _ROWS[k](), _STRIDES[k](), _ROWS[k](), _STRIDES[k](), _HEADS[k]()
+    for i in range(k):
+        shape = (n, xs[i].shape[1], head_dim)
+        heads[i] = shape[1]
+        src[i], src_apart[i] = _fit_rows("x", xs[i], dtype, shape, dev)
+        dst[i], dst_apart[i] = _fit_rows("out", outs[i], dtype, shape, dev)
+    half = freq.shape[0]
+    check(lib().qwha_rotary(_dt(q), k, src, src_apart, dst, dst_apart, heads, head_dim, n,
+                            _fit("positions", positions, torch.int64, (n,), dev),
+                            _fit("freq", freq, torch.float64, (half,), dev), 2 * half, interleaved, factor, inverse,
+                            _raw_stream(dev)), "qwha_rotary")
+    return outs[0] if single else outs
 
 
 def cache_attention(kv, q: torch.Tensor, pages: torch.Tensor, q_start: torch.Tensor, past: torch.Tensor,

@@ -303,22 +303,26 @@ Cut tc_cut(int grp, int64_t n) {
   return c;
 }
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-Cut mma_cut(int D, int heads, int grp, int64_t n, int nt, int pieces, int bits_k, int bits_v, int group) {
+// Of a CTA of up to `warps` warps, as many CTAs as registers allow: two of eight
+// warps to an SM for tiles of one n-tile, else one.
+Cut cut_warps(int D, int heads, int grp, int64_t n, int nt, int warps) {
   Cut c = cut_rows(grp, 8 * nt, n);
-  const int dp = padded(D);
-  for (int warps = kMmaWarps;; warps /= 2) {
-    c.hb = (int)cdiv(heads, cdiv(heads, warps));
-    c.mma.per_head = std::max(1, warps / c.hb), c.mma.warps = c.hb * c.mma.per_head;
-    c.mma.smem = MmaShape(D, dp, bits_k, bits_v, group, nt, pieces, heads, c.hb, c.mma.per_head, c.mma.warps).total;
-    if (warps == 1 || c.mma.smem + kSmemStatic <= kSmemLimit) break;
-  }
-  // registers leave two CTAs of eight warps to an SM for tiles of one n-tile, else one
-  const int by_regs = std::max(1, (nt == 1 && dp <= 128 ? 2 : 1) * kMmaWarps / c.mma.warps);
-  const int by_smem = (int)(kSmemLimit / (c.mma.smem + kSmemStatic));
-  c.ctas = sm_count() * std::max(1, std::min(by_regs, by_smem));
-  c.mma.nt = nt, c.mma.ctas = c.ctas;
+  c.hb = (int)cdiv(heads, cdiv(heads, warps));
+  c.mma.per_head = std::max(1, warps / c.hb), c.mma.warps = c.hb * c.mma.per_head, c.mma.nt = nt;
+  c.ctas = sm_count() * std::max(1, (nt == 1 && padded(D) <= 128 ? 2 : 1) * kMmaWarps / c.mma.warps);
   c.kt_log2 = ilog2(kTokens * c.mma.per_head), c.least_log2 = 2;
   return c;
+}
+Cut mma_cut(int D, int heads, int grp, int64_t n, int nt, int pieces, int bits_k, int bits_v, int group) {
+  for (int warps = kMmaWarps;; warps /= 2) {
+    Cut c = cut_warps(D, heads, grp, n, nt, warps);
+    c.mma.smem = MmaShape(D, padded(D), bits_k, bits_v, group, nt, pieces, heads, c.hb, c.mma.per_head, c.mma.warps).total;
+    const size_t fit = kSmemLimit / (c.mma.smem + kSmemStatic);
+    if (fit == 0 && warps > 1) continue;
+    c.ctas = std::min(c.ctas, sm_count() * (int)std::max<size_t>(1, fit));
+    c.mma.ctas = c.ctas;
+    return c;
+  }
 }
 size_t cut_bytes(const Cut &c, int D) {
   return align_up((size_t)c.ctas * 2 * sizeof(int4), 256) + align_up((size_t)c.ctas * 2 * c.part_rows() * 8, 256) +
@@ -331,15 +335,16 @@ bool takes_codes(const qwha_cache &c) { return c.bits != 2 || c.head_dim % 16 ==
 
 }  // namespace
 
+// Enough for any formats of the caches: their sizes decide how many warps a CTA
+// gets and how many CTAs fit, of which cut_warps's are the most.
 size_t attention_workspace(int32_t q_heads, int32_t head_dim, int32_t heads, int64_t n, bool f32) {
   if (heads <= 0 || q_heads % heads || n <= 0) return 0;
   const int grp = q_heads / heads;
   size_t most = cut_bytes(any_cut(grp, n), head_dim);
   if (!f32) most = std::max(most, cut_bytes(tc_cut(grp, n), head_dim));
-  // whatever the formats: fewer bits, more CTAs to an SM
   for (int nt = 1; nt <= 4; nt *= 2)
-    for (int bits = 2; bits <= 8; ++bits)
-      most = std::max(most, cut_bytes(mma_cut(head_dim, heads, grp, n, nt, f32 ? 2 : 1, bits, bits, head_dim), head_dim));
+    for (int warps = kMmaWarps; warps; warps /= 2)
+      most = std::max(most, cut_bytes(cut_warps(head_dim, heads, grp, n, nt, warps), head_dim));
   return most;
 }
 

@@ -34,6 +34,20 @@ struct Shared {
   long long granted[kMaxCtas];  // pages that they get
 };
 
+// The sum of the values in warp_s of the warps before this one, and of all (32 warps).
+__device__ __forceinline__ long long warps_before(const long long *warp_s, long long *sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long mine = warp_s[lane];
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const long long p = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += p;
+  }
+  *sum = __shfl_sync(~0u, upto, 31);
+  return __shfl_sync(~0u, upto - mine, warp);
+}
+
 // The `v` of the threads before this one in the CTA, and the CTA's sum.
 __device__ __forceinline__ long long block_before(long long v, long long *warp_s, long long *sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -46,13 +60,13 @@ __device__ __forceinline__ long long block_before(long long v, long long *warp_s
   __syncthreads();  // warp_s is free
   if (lane == 31) warp_s[warp] = upto;
   __syncthreads();
-  long long before = 0, all = 0;
-  for (int w = 0; w < kTableWarps; ++w) {
-    if (w < warp) before += warp_s[w];
-    all += warp_s[w];
-  }
-  *sum = all;
-  return before + upto - v;
+  return warps_before(warp_s, sum) + upto - v;
+}
+
+// Pages of a sequence's tokens: x / ps rounded up, for 0 <= x (in 32 bits where x fits, a third of the time).
+__device__ __forceinline__ int64_t pages_of(int64_t x, int ps) {
+  x += ps - 1;
+  return x >> 32 ? x / ps : (int64_t)((uint32_t)x / (uint32_t)ps);
 }
 
 // The CTA's share [lo, hi) of n things, in order.
@@ -98,12 +112,8 @@ __device__ __forceinline__ void count_free(const qwha_page_table &t, int rank, i
   __syncthreads();
   if (lane == 0) warp_s[warp] = mine;
   __syncthreads();
-  long long b = 0, all = 0;
-  for (int w = 0; w < kTableWarps; ++w) {
-    if (w < warp) b += warp_s[w];
-    all += warp_s[w];
-  }
-  *before = b;
+  long long all;
+  *before = warps_before(warp_s, &all);
   if (threadIdx.x == 0) sh->free[rank] = all;
   __syncthreads();
 }
@@ -121,7 +131,8 @@ __global__ void __launch_bounds__(kTableThreads, 1)
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t ps = t.page_size, room = ps * t.max_pages;
+  const int ps = t.page_size;
+  const int64_t room = (int64_t)ps * t.max_pages;
   int s0, s1;
   share(t.n_seqs, rank, ctas, &s0, &s1);
   // pages each sequence asks for, and how many are asked for before it in the CTA
@@ -135,7 +146,7 @@ __global__ void __launch_bounds__(kTableThreads, 1)
       } else if (w < -1 || w > room || h < 0 || h > room) {
         atomicOr(err, kErrTable);
       } else {
-        need = (w + ps - 1) / ps - (h + ps - 1) / ps;
+        need = pages_of(w, ps) - pages_of(h, ps);
         if (need < 0) need = 0;
       }
     }
@@ -145,13 +156,18 @@ __global__ void __launch_bounds__(kTableThreads, 1)
     asked += sum;
   }
   if (threadIdx.x == 0) sh->wanted[rank] = asked;
-  // the ends that are given back: a warp a sequence
-  for (int b = s0 + warp; b < s1; b += kTableWarps) {
+  // The ends that are given back: eight lanes a sequence, neighbours to different CTAs, since long ends come together and
+  // an SM makes about one atomic operation in two clocks. (What this changes of held is of sequences that do not grow,
+  // whose held nobody needs from here on.)
+  const int eighth = threadIdx.x & 7, group = threadIdx.x >> 3;
+  constexpr int kGroups = kTableThreads / 8;
+  for (int b = group * ctas + rank; b < t.n_seqs; b += kGroups * ctas) {
     const int64_t w = want[b], h = t.held[b];
     if (w < 0 || w > room || h < 0 || h > room) continue;
-    const int64_t have = (h + ps - 1) / ps, to = (w + ps - 1) / ps;
+    const int64_t have = pages_of(h, ps), to = pages_of(w, ps);
     int32_t *row = t.pages + (int64_t)b * t.max_pages;
-    for (int64_t j = to + lane; j < have; j += 32) {
+#pragma unroll 4
+    for (int64_t j = to + eighth; j < have; j += 8) {
       const int32_t p = row[j];
       row[j] = -1;
       if (p < 0 || p >= t.n_pages) {
@@ -161,8 +177,8 @@ __global__ void __launch_bounds__(kTableThreads, 1)
         atomicOr(err, kErrTable);
       }
     }
-    __syncwarp();
-    if (lane == 0 && to <= have) t.held[b] = w;
+    __syncwarp(0xffu << (threadIdx.x & 24));  // the eight lanes have read held
+    if (eighth == 0 && to <= have) t.held[b] = w;
   }
   cluster.sync();
   const long long total = sum_of(sh->wanted, ctas);
@@ -178,7 +194,7 @@ __global__ void __launch_bounds__(kTableThreads, 1)
   __syncthreads();
   for (int b = s0 + threadIdx.x; b < s1; b += kTableThreads) {
     if (from[b] == kNone) continue;
-    const long long need = (want[b] + ps - 1) / ps - (t.held[b] + ps - 1) / ps, at = asked_before + from[b];
+    const long long need = pages_of(want[b], ps) - pages_of(t.held[b], ps), at = asked_before + from[b];
     if (at + need <= n_free) atomicMax(&granted_s, (unsigned long long)(at + need));
     from[b] = at + need <= n_free ? at : kNone;
   }
@@ -190,14 +206,14 @@ __global__ void __launch_bounds__(kTableThreads, 1)
   const long long free_before = sum_of(sh->free, rank) + before;
   if (free_before < granted) warp_free(t.refs, lo, hi, list, free_before, granted, t.refs);
   cluster.sync();
-  for (int b = s0 + warp; b < s1; b += kTableWarps) {
+  for (int b = s0 + group; b < s1; b += kGroups) {
     const int64_t at = from[b];
     if (at == kNone) continue;
-    const int64_t w = want[b], have = (t.held[b] + ps - 1) / ps, to = (w + ps - 1) / ps;
+    const int64_t w = want[b], have = pages_of(t.held[b], ps), to = pages_of(w, ps);
     int32_t *row = t.pages + (int64_t)b * t.max_pages;
-    for (int64_t j = have + lane; j < to; j += 32) row[j] = __ldcg(list + at + (j - have));
-    __syncwarp();
-    if (lane == 0) t.held[b] = w;
+    for (int64_t j = have + eighth; j < to; j += 8) row[j] = __ldcg(list + at + (j - have));
+    __syncwarp(0xffu << (threadIdx.x & 24));  // the eight lanes have read held
+    if (eighth == 0) t.held[b] = w;
   }
 }
 
@@ -209,7 +225,8 @@ __global__ void __launch_bounds__(kTableThreads, 1)
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t ps = t.page_size, room = ps * t.max_pages;
+  const int ps = t.page_size;
+  const int64_t room = (int64_t)ps * t.max_pages;
   int m0, m1;
   share(m, rank, ctas, &m0, &m1);
   auto in_table = [&](int64_t b) { return b >= 0 && b < t.n_seqs; };
@@ -230,7 +247,7 @@ __global__ void __launch_bounds__(kTableThreads, 1)
       if (h > room) h = -1;
       if (h < 0 && a != -1) atomicOr(err, kErrTable);
       tokens[i] = h;
-      need = h > 0 && h % ps;
+      need = h > 0 && pages_of(h, ps) * ps != h;
     }
     long long sum;
     const long long before = block_before(need, warp_s, &sum);
@@ -248,7 +265,7 @@ __global__ void __launch_bounds__(kTableThreads, 1)
   if (free_before < granted) warp_free(t.refs, lo, hi, list, free_before, granted, t.refs);
   cluster.sync();
   for (int i = m0 + warp; i < m1; i += kTableWarps) {
-    const int64_t h = tokens[i], full = h / ps, at = from[i] == kNone ? -1 : asked_before + from[i];
+    const int64_t h = tokens[i], full = h < 0 ? 0 : pages_of(h - ps + 1, ps), at = from[i] == kNone ? -1 : asked_before + from[i];
     const bool served = h >= 0 && at < granted;
     int32_t o = -1, f = -1;
     if (served) {
@@ -297,13 +314,13 @@ TableWs carve(void *ws, int64_t n_seqs, int64_t n_pages, int64_t m) {
 template <typename... K, typename... A>
 cudaError_t launch_table(void (*kernel)(K...), int64_t pages, int64_t rows, cudaStream_t s, A... args) {
   // one CTA for a small table: a cluster's barriers cost more than they save there
-  const int ctas = pages <= 4096 && rows <= 512 ? 1 : kMaxCtas;
+  const int ctas = pages <= 16384 && rows <= 1024 ? 1 : kMaxCtas;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(ctas), c.blockDim = dim3(kTableThreads), c.stream = s;
   cudaLaunchAttribute a[1];
   a[0].id = cudaLaunchAttributeClusterDimension;
   a[0].val.clusterDim.x = ctas, a[0].val.clusterDim.y = 1, a[0].val.clusterDim.z = 1;
-  c.attrs = a, c.numAttrs = 1;
+  c.attrs = a, c.numAttrs = ctas > 1;
   return cudaLaunchKernelEx(&c, kernel, static_cast<K>(args)...);
 }
 
@@ -316,8 +333,10 @@ __host__ __device__ __forceinline__ int width_of(int64_t n) {
   return n % 16 == 0 ? 16 : n % 8 == 0 ? 8 : n % 4 == 0 ? 4 : n % 2 == 0 ? 2 : 1;
 }
 
-template <typename V, int U>
+// Eight loads of a thread in flight.
+template <typename V>
 __device__ __forceinline__ void copy_run(char *dst, const char *src, int64_t bytes) {
+  constexpr int U = 8;
   const int64_t n = bytes / (int64_t)sizeof(V);
   for (int64_t i = threadIdx.x; i < n; i += kMoveThreads * U) {
     V v[U];
@@ -331,39 +350,38 @@ __device__ __forceinline__ void copy_run(char *dst, const char *src, int64_t byt
 }
 __device__ __forceinline__ void copy_bytes(char *dst, const char *src, int64_t bytes, int width) {
   switch (width) {
-    case 16: copy_run<uint4, 4>(dst, src, bytes); break;
-    case 8: copy_run<uint2, 4>(dst, src, bytes); break;
-    case 4: copy_run<uint32_t, 4>(dst, src, bytes); break;
-    case 2: copy_run<uint16_t, 4>(dst, src, bytes); break;
-    default: copy_run<uint8_t, 4>(dst, src, bytes);
+    case 16: copy_run<uint4>(dst, src, bytes); break;
+    case 8: copy_run<uint2>(dst, src, bytes); break;
+    case 4: copy_run<uint32_t>(dst, src, bytes); break;
+    case 2: copy_run<uint16_t>(dst, src, bytes); break;
+    default: copy_run<uint8_t>(dst, src, bytes);
   }
 }
 
-constexpr int64_t kPiece = 16384;  // bytes of codes a CTA copies at a time
+constexpr int64_t kPiece = kMoveThreads * 8 * 16;  // bytes a CTA copies at a time
 
-__global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(const CachePair c, const int32_t *__restrict__ from,
-                                                                  const int32_t *__restrict__ to, int m, int pieces,
-                                                                  unsigned int *err) {
-  const qwha_cache &a = c.cache[blockIdx.y];
-  const int64_t row = (int64_t)a.page_size * a.heads, codes = row * (a.head_dim / 8 * a.bits);
-  const int64_t groups = row * (a.head_dim / a.group);
-  for (int64_t w = blockIdx.x; w < (int64_t)m * pieces; w += gridDim.x) {
-    const int i = (int)(w / pieces), piece = (int)(w - (int64_t)i * pieces);
+// blockIdx.y: 3 cache + 0 codes, 1 scales, 2 zero points.
+__global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(const __grid_constant__ CachePair c,
+                                                                  const int32_t *__restrict__ from,
+                                                                  const int32_t *__restrict__ to, int m, unsigned int *err) {
+  const int what = blockIdx.y % 3;
+  const qwha_cache &a = c.cache[blockIdx.y / 3];
+  const int64_t row = (int64_t)a.page_size * a.heads, groups = row * (a.head_dim / a.group);
+  const int64_t bytes = what == 0 ? row * (a.head_dim / 8 * a.bits) : what == 1 ? groups * 4 : groups;
+  char *base = what == 0 ? reinterpret_cast<char *>(a.codes) : what == 1 ? reinterpret_cast<char *>(a.scales) : reinterpret_cast<char *>(a.zeros);
+  const int width = width_of(bytes);
+  const int64_t pieces = (bytes + kPiece - 1) / kPiece;
+  // pieces of a page one after the other in one CTA's turns, while pages alone fill the grid
+  for (int64_t w = blockIdx.x; w < m * pieces; w += gridDim.x) {
+    const int i = pieces == 1 ? (int)w : (int)(w / pieces);
+    const int64_t lo = (w - i * pieces) * kPiece, hi = lo + kPiece < bytes ? lo + kPiece : bytes;
     const int64_t f = from[i], t = to[i];
     if (f == -1 || t == -1) continue;
     if (f < 0 || t < 0 || f >= a.n_pages || t >= a.n_pages) {
       if (threadIdx.x == 0) atomicOr(err, kErrPage);
       continue;
     }
-    char *base = reinterpret_cast<char *>(a.codes);
-    const int64_t lo = piece * kPiece, hi = lo + kPiece < codes ? lo + kPiece : codes;
-    if (lo < hi) copy_bytes(base + t * codes + lo, base + f * codes + lo, hi - lo, width_of(codes));
-    if (piece == 0) {
-      base = reinterpret_cast<char *>(a.scales);
-      copy_bytes(base + t * groups * 4, base + f * groups * 4, groups * 4, width_of(groups * 4));
-      base = reinterpret_cast<char *>(a.zeros);
-      copy_bytes(base + t * groups, base + f * groups, groups, width_of(groups));
-    }
+    copy_bytes(base + t * bytes + lo, base + f * bytes + lo, hi - lo, width);
   }
 }
 
@@ -372,7 +390,7 @@ __global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(const CachePai
 // writes. keep ascends, so keep[i] >= i and the place that move i writes is read
 // by no later move: nothing has to wait for another thread.
 constexpr int kAhead = 8;
-constexpr int kMoves = 128;  // moves whose slots are looked up at a time
+constexpr int kMoves = 128;  // moves whose slots are looked up at a time, one a thread
 
 template <typename V>
 __device__ __forceinline__ void move_column(char *base, int64_t row, int64_t at, const int64_t *from, const int64_t *to,
@@ -387,31 +405,32 @@ __device__ __forceinline__ void move_column(char *base, int64_t row, int64_t at,
       if (i + u < n && from[i + u] >= 0) *reinterpret_cast<V *>(base + to[i + u] * row + at) = v[u];
   }
 }
-__device__ __forceinline__ void move_columns(void *rows, int64_t row, int64_t first, int64_t step, const int64_t *from,
-                                             const int64_t *to, int n) {
-  char *base = static_cast<char *>(rows);
-  const int w = width_of(row);
-  for (int64_t at = first * w; at < row; at += step * w) switch (w) {
-      case 16: move_column<uint4>(base, row, at, from, to, n); break;
-      case 8: move_column<uint2>(base, row, at, from, to, n); break;
-      case 4: move_column<uint32_t>(base, row, at, from, to, n); break;
-      case 2: move_column<uint16_t>(base, row, at, from, to, n); break;
-      default: move_column<uint8_t>(base, row, at, from, to, n);
-    }
-}
+// A token's bytes in one cache: codes, scales and zero points, each in accesses as
+// wide as its rows allow.
+struct Columns {
+  int64_t row[3], count[3];
+  int width[3];
+  __host__ __device__ explicit Columns(const qwha_cache &a) {
+    const int64_t groups = (int64_t)a.heads * (a.head_dim / a.group);
+    row[0] = (int64_t)a.heads * (a.head_dim / 8 * a.bits), row[1] = groups * 4, row[2] = groups;
+    for (int i = 0; i < 3; ++i) width[i] = width_of(row[i]), count[i] = row[i] / width[i];
+  }
+  __host__ __device__ int64_t total() const { return count[0] + count[1] + count[2]; }
+};
 
 __global__ void __launch_bounds__(kMoveThreads)
-    compact_kernel(const CachePair c, const int32_t *__restrict__ pages, int max_pages,
+    compact_kernel(const __grid_constant__ CachePair c, const int32_t *__restrict__ pages, int max_pages,
                    const int64_t *__restrict__ first, const int32_t *__restrict__ keep, int width, unsigned int *err) {
   __shared__ int64_t from_s[kMoves], to_s[kMoves];
   __shared__ int stop_s;
   const qwha_cache &a = c.cache[blockIdx.y];
   const int b = blockIdx.z;
   const int32_t *row = keep + (int64_t)b * width;
-  const int64_t codes = (int64_t)a.heads * (a.head_dim / 8 * a.bits), groups = (int64_t)a.heads * (a.head_dim / a.group);
+  const Columns col(a);
   auto slot = [&](int64_t t) -> int64_t {
-    const int64_t pg = t / a.page_size;
-    if (t < 0 || pg >= max_pages) return -1;
+    if (t < 0) return -1;
+    const int64_t pg = t >> 32 ? t / a.page_size : (int64_t)((uint32_t)t / (uint32_t)a.page_size);
+    if (pg >= max_pages) return -1;
     const int64_t page = pages[(int64_t)b * max_pages + pg];
     return page < 0 || page >= a.n_pages ? -1 : page * a.page_size + (t - pg * a.page_size);
   };
@@ -420,16 +439,16 @@ __global__ void __launch_bounds__(kMoveThreads)
     __syncthreads();
     if (threadIdx.x == 0) stop_s = n;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kMoveThreads) {
-      const int k = row[i0 + i], last = i0 + i ? row[i0 + i - 1] : -1;
+    const int i = threadIdx.x, k = i < n ? row[i0 + i] : 0;
+    if (i < n) {
+      const int last = i0 + i ? row[i0 + i - 1] : -1;
       if (k <= last || k < 0) atomicMin(&stop_s, i);
     }
     __syncthreads();
     const int stop = stop_s;
     // -1 ends the row; anything else that does not ascend breaks it off
     if (threadIdx.x == 0 && stop < n && row[i0 + stop] != -1) atomicOr(err, kErrTable);
-    for (int i = threadIdx.x; i < stop; i += kMoveThreads) {
-      const int k = row[i0 + i];
+    if (i < stop) {
       int64_t f = -1, t = -1;
       if (k != i0 + i) {
         f = slot(first[b] + k), t = slot(first[b] + i0 + i);
@@ -441,10 +460,20 @@ __global__ void __launch_bounds__(kMoveThreads)
       from_s[i] = f, to_s[i] = t;
     }
     __syncthreads();
-    const int64_t t0 = blockIdx.x * kMoveThreads + threadIdx.x, step = (int64_t)gridDim.x * kMoveThreads;
-    move_columns(a.codes, codes, t0, step, from_s, to_s, stop);
-    move_columns(a.scales, groups * 4, t0, step, from_s, to_s, stop);
-    move_columns(a.zeros, groups, t0, step, from_s, to_s, stop);
+    for (int64_t x = blockIdx.x * kMoveThreads + threadIdx.x; x < col.total(); x += (int64_t)gridDim.x * kMoveThreads) {
+      const int what = x < col.count[0] ? 0 : x < col.count[0] + col.count[1] ? 1 : 2;
+      const int64_t in = what == 0 ? x : what == 1 ? x - col.count[0] : x - col.count[0] - col.count[1];
+      const int64_t bytes = what == 0 ? col.row[0] : what == 1 ? col.row[1] : col.row[2];
+      const int w = what == 0 ? col.width[0] : what == 1 ? col.width[1] : col.width[2];
+      char *base = what == 0 ? reinterpret_cast<char *>(a.codes) : what == 1 ? reinterpret_cast<char *>(a.scales) : reinterpret_cast<char *>(a.zeros);
+      switch (w) {
+        case 16: move_column<uint4>(base, bytes, in * 16, from_s, to_s, stop); break;
+        case 8: move_column<uint2>(base, bytes, in * 8, from_s, to_s, stop); break;
+        case 4: move_column<uint32_t>(base, bytes, in * 4, from_s, to_s, stop); break;
+        case 2: move_column<uint16_t>(base, bytes, in * 2, from_s, to_s, stop); break;
+        default: move_column<uint8_t>(base, bytes, in, from_s, to_s, stop);
+      }
+    }
     if (stop < n) break;
   }
 }
@@ -477,8 +506,8 @@ cudaError_t launch_copy_pages(const CachePair &c, int n_caches, const int32_t *f
     const qwha_cache &a = c.cache[i];
     most = std::max<int64_t>(most, cdiv((int64_t)a.page_size * a.heads * (a.head_dim / 8 * a.bits), kPiece));
   }
-  const dim3 grid((unsigned)std::min<int64_t>((int64_t)m * most, (int64_t)sm_count() * 64), (unsigned)n_caches);
-  copy_pages_kernel<<<grid, kMoveThreads, 0, s>>>(c, from, to, m, (int)most, err);
+  const dim3 grid((unsigned)std::min<int64_t>((int64_t)m * most, (int64_t)sm_count() * 64), (unsigned)n_caches * 3);
+  copy_pages_kernel<<<grid, kMoveThreads, 0, s>>>(c, from, to, m, err);
   return cudaGetLastError();
 }
 
@@ -488,8 +517,7 @@ cudaError_t launch_compact(const CachePair &c, int n_caches, const int32_t *page
   if (!err) return cudaErrorInvalidDevicePointer;
   int64_t columns = 1;
   for (int i = 0; i < n_caches; ++i) {
-    const int64_t codes = (int64_t)c.cache[i].heads * (c.cache[i].head_dim / 8 * c.cache[i].bits);
-    columns = std::max(columns, codes / width_of(codes));
+    columns = std::max(columns, Columns(c.cache[i]).total());
   }
   for (int32_t b0 = 0; b0 < n_seqs; b0 += 65535) {
     const int32_t here = std::min(n_seqs - b0, 65535);
