@@ -278,7 +278,10 @@ namespace {
 // Rows of a cached head above which tiles of 128 on tcgen05 are taken instead of 32 on mma.sync.
 constexpr int kTcAbove = 32;
 
-constexpr size_t kSmemLimit = 227 * 1024, kSmemStatic = 9 * 1024;  // (static: 8.2 KB at most, and 1 KB of the system's)
+// Shared memory of an SM, and what a CTA has of it besides the dynamic part: the kernels' arrays (more with more rows)
+// and 1 KB of the system's.
+constexpr size_t kSmemLimit = 228 * 1024;
+constexpr size_t smem_besides(int nt) { return nt == 1 ? 6400 : 11 * 1024; }
 
 // How a call is cut and launched.
 struct Cut {
@@ -310,14 +313,14 @@ Cut cut_warps(int D, int heads, int grp, int64_t n, int nt, int warps) {
   c.hb = (int)cdiv(heads, cdiv(heads, warps));
   c.mma.per_head = std::max(1, warps / c.hb), c.mma.warps = c.hb * c.mma.per_head, c.mma.nt = nt;
   c.ctas = sm_count() * std::max(1, (nt == 1 && padded(D) <= 128 ? 2 : 1) * kMmaWarps / c.mma.warps);
-  c.kt_log2 = ilog2(kTokens * c.mma.per_head), c.least_log2 = 2;
+  c.kt_log2 = ilog2(kTokens * kTilesPerStage * c.mma.per_head), c.least_log2 = 1;
   return c;
 }
 Cut mma_cut(int D, int heads, int grp, int64_t n, int nt, int pieces, int bits_k, int bits_v, int group) {
   for (int warps = kMmaWarps;; warps /= 2) {
     Cut c = cut_warps(D, heads, grp, n, nt, warps);
     c.mma.smem = MmaShape(D, padded(D), bits_k, bits_v, group, nt, pieces, heads, c.hb, c.mma.per_head, c.mma.warps).total;
-    const size_t fit = kSmemLimit / (c.mma.smem + kSmemStatic);
+    const size_t fit = kSmemLimit / (c.mma.smem + smem_besides(nt));
     if (fit == 0 && warps > 1) continue;
     c.ctas = std::min(c.ctas, sm_count() * (int)std::max<size_t>(1, fit));
     c.mma.ctas = c.ctas;

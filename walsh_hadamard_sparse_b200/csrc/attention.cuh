@@ -158,8 +158,9 @@ struct Rows {
   int row0, j0, tokens, heads, head;  // row0: the sequence's first row of q
   int n;                              // tokens * heads
   int all;                            // tokens of the sequence
-  __device__ __forceinline__ int64_t q_row(int r) const { return row0 + j0 + r / heads; }
-  __device__ __forceinline__ int q_head(int r) const { return head + r % heads; }
+  __device__ __forceinline__ int token(int r) const { return tokens == 1 ? 0 : r / heads; }  // (no division for one)
+  __device__ __forceinline__ int64_t q_row(int r) const { return row0 + j0 + token(r); }
+  __device__ __forceinline__ int q_head(int r) const { return head + r - token(r) * heads; }
 };
 // kv: the cached head.
 __device__ __forceinline__ Rows rows_of(const AttnArgs &a, const Seq &s, int kv, int part, int tile) {

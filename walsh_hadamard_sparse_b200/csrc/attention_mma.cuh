@@ -35,8 +35,9 @@ namespace qwha {
 namespace attn {
 
 constexpr int kMmaWarps = 8;   // consumers of a CTA, at most
-constexpr int kStages = 4;     // of the ring
-constexpr int kTokens = 16;    // of a warp's part of a stage
+constexpr int kStages = 2;     // of the ring
+constexpr int kTokens = 16;    // of a warp's tile
+constexpr int kTilesPerStage = 2;  // of a warp
 constexpr float kSlack = 5.f;  // by how much (base 2) a score may pass the maximum
 constexpr float kTop = 1024.f;  // p scale stays below this times 2^kSlack in f16
 constexpr float kNoScale = 1.329227995784916e36f;  // 2^120: no scale met yet
@@ -62,6 +63,14 @@ struct Part {
   }
 };
 
+constexpr int kMaxSmalls = 64;
+// A piece of scales or zero points of the token in slot 0 and cached head 0.
+struct alignas(16) Small {
+  const char *from;
+  uint32_t stride, to;  // of a slot; place of token 0 in a stage
+  uint32_t head, pitch, wide;  // bytes of a head; from token to token in a stage
+};
+
 // A CTA's stages and shared memory, in bytes.
 struct MmaShape {
   Part codes[2], scales[2], zeros[2];  // keys, values
@@ -70,15 +79,15 @@ struct MmaShape {
   int tokens;                          // of a stage
   int off_at, live_at, stage;          // off: 4 bytes a token, where its zero points and codes begin in their words
   int all_wide;                        // they begin at words in every token
-  int two;                             // two pieces of keys' and values' codes a thread
-  int fast;                            // codes in 16-byte pieces, a thread at most one piece of scales and zero points
+  int smalls;                          // pieces of a token's scales and zero points
+  int fast;                            // codes in 16-byte pieces, scales and zero points in whole pieces
   int q_at, q_bytes;                   // queries as operands: after the ring; of a head
   int join_at, total;                  // where warps that share a head join
   __host__ __device__ MmaShape() {}
   __host__ __device__ MmaShape(int D, int dp, int bits_k, int bits_v, int group, int nt, int pieces, int heads, int hb,
                                int per_head, int warps) {
     const int bits[2] = {bits_k, bits_v};
-    ng = D / group, tokens = kTokens * per_head;
+    ng = D / group, tokens = kTokens * kTilesPerStage * per_head;
     int end = 0;
     for (int i = 0; i < 2; ++i) {
       row[i] = D / 8 * bits[i];
@@ -89,9 +98,8 @@ struct MmaShape {
     for (int i = 0; i < 2; ++i) scales[i].set(hb * ng * 4, heads * ng * 4, 0, &end, tokens);
     for (int i = 0; i < 2; ++i) zeros[i].set(hb * ng, heads * ng, 0, &end, tokens);
     all_wide = codes[0].wide && codes[1].wide && zeros[0].wide && zeros[1].wide;
-    two = hb > 0 && codes[0].per == 4 * hb && codes[1].per == 4 * hb;
-    fast = all_wide && codes[0].wide == 16 && codes[1].wide == 16 &&
-           scales[0].per + scales[1].per + zeros[0].per + zeros[1].per <= 2 * hb;
+    smalls = scales[0].per + scales[1].per + zeros[0].per + zeros[1].per;
+    fast = all_wide && codes[0].wide == 16 && codes[1].wide == 16 && smalls <= kMaxSmalls;
     off_at = end, live_at = off_at + tokens * 4;
     stage = (live_at + tokens + 15) / 16 * 16;
     q_at = kStages * stage;
@@ -323,6 +331,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
   __shared__ float c_s[kMmaWarps][32];                              // factor of the scales of each group
   __shared__ float m_s[kMmaWarps][8 * NT], l_s[kMmaWarps][8 * NT];  // of each warp's rows
   __shared__ float f_s[kMmaWarps][8 * NT];                          // by head: factor of a row's scores
+  __shared__ Small small_s[kMaxSmalls];
   __shared__ Rows rows_s[kMmaWarps];                                // kept out of the loop's registers
   __shared__ uint8_t group_s[32];                                   // of a chunk of eight channels
   __shared__ int lim_s[kMmaWarps][8 * NT];
@@ -342,36 +351,29 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
   };
   if (threadIdx.x == 0) a.part_desc[2 * blockIdx.x] = a.part_desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
   // what the thread fetches: of one token of each stage, every fetch_step-th piece
-  const int fetch_step = 2 * a.hb, fetch_token = threadIdx.x / fetch_step, fetch_piece = threadIdx.x - fetch_token * fetch_step;
+  const int fetch_step = a.hb, fetch_token = threadIdx.x / fetch_step, fetch_piece = threadIdx.x - fetch_token * fetch_step;
   const uint32_t slots = (uint32_t)(a.k.n_pages * a.k.page_size);
   const uint32_t smem_u = (uint32_t)__cvta_generic_to_shared(smem);
-  // its piece of scales or zero points, where each has one at most
-  const char *small = nullptr;
-  uint32_t small_stride = 0, small_to = 0;
-  int small_wide = 0, small_head = 0;
-  if (sh.fast) {
-    int p = fetch_piece;
-#pragma unroll
+  if (sh.fast && threadIdx.x == 0) {
+    int n = 0;
     for (int i = 0; i < 4; ++i) {
       const Part &x = i < 2 ? sh.scales[i] : sh.zeros[i - 2];
       const qwha_cache &c = i & 1 ? a.v : a.k;
-      if (p >= 0 && p < x.per) {
-        small = (i < 2 ? reinterpret_cast<const char *>(c.scales) : reinterpret_cast<const char *>(c.zeros)) + p * x.wide;
-        small_stride = x.stride, small_to = x.at + fetch_token * x.pitch + p * x.wide, small_wide = x.wide;
-        small_head = i < 2 ? ng * 4 : ng;
-      }
-      p = p < 0 ? p : p - x.per;
+      const char *from = i < 2 ? reinterpret_cast<const char *>(c.scales) : reinterpret_cast<const char *>(c.zeros);
+      for (int p = 0; p < x.per; ++p)
+        small_s[n++] = {from + p * x.wide, (uint32_t)x.stride, (uint32_t)(x.at + p * x.wide), (uint32_t)(i < 2 ? ng * 4 : ng), (uint32_t)x.pitch, (uint32_t)x.wide};
     }
   }
+  __syncthreads();
   const uint32_t k_to = sh.codes[0].at + fetch_token * sh.codes[0].pitch + fetch_piece * 16;
   const uint32_t v_to = sh.codes[1].at + fetch_token * sh.codes[1].pitch + fetch_piece * 16;
   // the lane's tokens and head in a stage's parts
-  const int k_row = sh.codes[0].at + (16 * sub + g) * sh.codes[0].pitch + hl * sh.row[0];
-  const int k_scale = sh.scales[0].at + (16 * sub + g) * sh.scales[0].pitch + hl * ng * 4;
-  const int v_scale = sh.scales[1].at + (16 * sub + g) * sh.scales[1].pitch + hl * ng * 4;
-  const int k_zero = sh.zeros[0].at + (16 * sub + g) * sh.zeros[0].pitch + hl * ng;
-  const int v_row = sh.codes[1].at + (16 * sub + 2 * t) * sh.codes[1].pitch + hl * sh.row[1];
-  const int v_zero = sh.zeros[1].at + (16 * sub + 2 * t) * sh.zeros[1].pitch + hl * ng;
+  const int k_row = sh.codes[0].at + (kTokens * kTilesPerStage * sub + g) * sh.codes[0].pitch + hl * sh.row[0];
+  const int k_scale = sh.scales[0].at + (kTokens * kTilesPerStage * sub + g) * sh.scales[0].pitch + hl * ng * 4;
+  const int v_scale = sh.scales[1].at + (kTokens * kTilesPerStage * sub + g) * sh.scales[1].pitch + hl * ng * 4;
+  const int k_zero = sh.zeros[0].at + (kTokens * kTilesPerStage * sub + g) * sh.zeros[0].pitch + hl * ng;
+  const int v_row = sh.codes[1].at + (kTokens * kTilesPerStage * sub + 2 * t) * sh.codes[1].pitch + hl * sh.row[1];
+  const int v_zero = sh.zeros[1].at + (kTokens * kTilesPerStage * sub + 2 * t) * sh.zeros[1].pitch + hl * ng;
   while (left > 0) {
     const Seq s(a, at.b);
     if (s.rows == 0) {
@@ -390,7 +392,6 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
     int fetch_t = at.unit * kt + fetch_token;
     const char *k_from = reinterpret_cast<const char *>(a.k.codes) + kv0 * sh.row[0] + fetch_piece * 16;
     const char *v_from = reinterpret_cast<const char *>(a.v.codes) + kv0 * sh.row[1] + fetch_piece * 16;
-    const char *small_from = small + kv0 * small_head;
     // the page of token t, which is within the table, since lengths are cut there; and its place in the page
     auto page_at = [&](int t, int *in) -> int {
       const int pg = page_of(a, t);
@@ -404,21 +405,26 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
       const uint32_t slot = (uint32_t)page * (uint32_t)a.k.page_size + (uint32_t)in, to = smem_u + fill_at;
       uint32_t off = 0;
       if (on && sh.fast) {
-        const char *src = k_from + (uint64_t)slot * (uint32_t)sh.codes[0].stride;
-        uint32_t dst = to + k_to;
-        if (sh.two) {  // the usual sizes: two pieces of each
-          copy_async<16>(dst, src), copy_async<16>(dst + 16 * fetch_step, src + 16 * fetch_step);
-          src = v_from + (uint64_t)slot * (uint32_t)sh.codes[1].stride, dst = to + v_to;
-          copy_async<16>(dst, src), copy_async<16>(dst + 16 * fetch_step, src + 16 * fetch_step);
-        } else {
-          for (int p = fetch_piece; p < sh.codes[0].per; p += fetch_step, src += 16 * fetch_step, dst += 16 * fetch_step) copy_async<16>(dst, src);
-          src = v_from + (uint64_t)slot * (uint32_t)sh.codes[1].stride, dst = to + v_to;
-          for (int p = fetch_piece; p < sh.codes[1].per; p += fetch_step, src += 16 * fetch_step, dst += 16 * fetch_step) copy_async<16>(dst, src);
-        }
-        if (small_wide) {
-          src = small_from + (uint64_t)slot * small_stride, dst = to + small_to;
-          if (small_wide == 16) copy_async<16>(dst, src);
-          else if (small_wide == 8) copy_async<8>(dst, src);
+        // pieces p, p + fetch_step, ... of a token's codes; a row has whole pieces
+        auto codes = [&](const char *src, uint32_t dst, int n) {
+          const int step = 16 * fetch_step;
+          for (; n >= 4; n -= 4, src += 4 * step, dst += 4 * step)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) copy_async<16>(dst + p * step, src + p * step);
+          if (n & 2) {
+            copy_async<16>(dst, src), copy_async<16>(dst + step, src + step);
+            src += 2 * step, dst += 2 * step;
+          }
+          if (n & 1) copy_async<16>(dst, src);
+        };
+        codes(k_from + (uint64_t)slot * (uint32_t)sh.codes[0].stride, to + k_to, sh.row[0] >> 4);
+        codes(v_from + (uint64_t)slot * (uint32_t)sh.codes[1].stride, to + v_to, sh.row[1] >> 4);
+        for (int q = fetch_piece; q < sh.smalls; q += fetch_step) {
+          const Small &x = small_s[q];
+          const char *src = x.from + (uint64_t)slot * x.stride + kv0 * x.head;
+          const uint32_t dst = to + x.to + fetch_token * x.pitch;
+          if (x.wide == 16) copy_async<16>(dst, src);
+          else if (x.wide == 8) copy_async<8>(dst, src);
           else copy_async<4>(dst, src);
         }
       } else if (on) {
@@ -541,15 +547,15 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
     __syncwarp();
     const uint4 *q_op = reinterpret_cast<const uint4 *>(q_at) + lane;
     const int safe = a.tree ? past : past + rows.j0 + 1;  // every row sees the tokens below
-    int t0 = at.unit * kt + 16 * sub, use_at = 0;
+    int t_stage = at.unit * kt + kTokens * kTilesPerStage * sub, use_at = 0;
     __syncwarp();
     if (lane == 0) rows_s[warp] = rows;
 
 #pragma unroll 1
-    for (int u = 0; u < run; ++u, t0 += kt) {
+    for (int u = 0; u < run; ++u, t_stage += kt) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncthreads();  // stage u has landed, and all have read stage u - 1
-      const char *st = smem + use_at;
+      const char *stage = smem + use_at;
       use_at = use_at + sh.stage == kStages * sh.stage ? 0 : use_at + sh.stage;
       if (u + kStages - 1 < run) {
         const int page = next_page, in = next_in;
@@ -558,10 +564,18 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
         fill(page, in);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
-      if (t0 < length && mine) {
+#pragma unroll 1
+      for (int h = 0; h < kTilesPerStage; ++h) {
+        const int t0 = t_stage + kTokens * h;
+        if (t0 >= length || !mine) break;
+        // the tile in the stage's parts
+        const char *st_k = stage + h * kTokens * sh.codes[0].pitch, *st_v = stage + h * kTokens * sh.codes[1].pitch;
+        const char *st_ks = stage + h * kTokens * sh.scales[0].pitch, *st_vs = stage + h * kTokens * sh.scales[1].pitch;
+        const char *st_kz = stage + h * kTokens * sh.zeros[0].pitch, *st_vz = stage + h * kTokens * sh.zeros[1].pitch;
+        const int first_token = kTokens * (kTilesPerStage * sub + h);
         // a byte a token: whether it is there
-        const uint32_t live = __ballot_sync(~0u, st[sh.live_at + 16 * sub + (lane & 15)]) & 0xffffu;
-        const uint8_t *off = reinterpret_cast<const uint8_t *>(st) + sh.off_at + 64 * sub;  // of the warp's tokens
+        const uint32_t live = __ballot_sync(~0u, stage[sh.live_at + first_token + (lane & 15)]) & 0xffffu;
+        const uint8_t *off = reinterpret_cast<const uint8_t *>(stage) + sh.off_at + 4 * first_token;  // of the tile's tokens
 
         // ---- scores of tokens g, g + 8 for queries 2 t, 2 t + 1 of each tile
         float sc[NT][4];
@@ -576,10 +590,10 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) part[n][e] = 0.f;
-          const char *r0 = st + k_row, *r1 = r0 + 8 * sh.codes[0].pitch;
-          const uint8_t *z0 = reinterpret_cast<const uint8_t *>(st) + k_zero, *z1 = z0 + 8 * sh.zeros[0].pitch;
-          const float *s0 = reinterpret_cast<const float *>(st + k_scale);
-          const float *s1 = reinterpret_cast<const float *>(st + k_scale + 8 * sh.scales[0].pitch);
+          const char *r0 = st_k + k_row, *r1 = r0 + 8 * sh.codes[0].pitch;
+          const uint8_t *z0 = reinterpret_cast<const uint8_t *>(st_kz) + k_zero, *z1 = z0 + 8 * sh.zeros[0].pitch;
+          const float *s0 = reinterpret_cast<const float *>(st_ks + k_scale);
+          const float *s1 = reinterpret_cast<const float *>(st_ks + k_scale + 8 * sh.scales[0].pitch);
           int mis0 = 0, mis1 = 0;
           if (!sh.zeros[0].wide) z0 += off[4 * g], z1 += off[4 * g + 32];
           if (B == 3 && !sh.codes[0].wide) {
@@ -677,10 +691,11 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
               m[n][i] = now;
               thr[n][i] = (now + kSlack) * inverse2(f[n][i]);
               l[n][i] *= turn;
+              if (u + h > 0)
 #pragma unroll
-              for (int b = 0; b < kBlocks; ++b)
+                for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[b][k][n][i] *= turn, acc[b][k][n][i + 2] *= turn;
+                  for (int k = 0; k < 4; ++k) acc[b][k][n][i] *= turn, acc[b][k][n][i + 2] *= turn;
             }
         }
         // ---- weights
@@ -698,8 +713,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
           constexpr int B = decltype(bits)::value;
           uint32_t w[NT][PIECES][2];  // weights times scales of the group, as operands
           auto weights = [&](int gr) {
-            float s0 = reinterpret_cast<const float *>(st + v_scale)[gr];
-            float s1 = reinterpret_cast<const float *>(st + v_scale + 8 * sh.scales[1].pitch)[gr];
+            float s0 = reinterpret_cast<const float *>(st_vs + v_scale)[gr];
+            float s1 = reinterpret_cast<const float *>(st_vs + v_scale + 8 * sh.scales[1].pitch)[gr];
             if (masked) s0 = any0 ? s0 : 0.f, s1 = any1 ? s1 : 0.f;
             float c = c_s[warp][gr];
             if (__any_sync(~0u, fabsf(s0) * c > kTop || fabsf(s1) * c > kTop)) {
@@ -713,6 +728,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
               __syncwarp();
               if (lane == 0) c_s[warp][gr] = now;
               __syncwarp();
+              if (u + h > 0)
 #pragma unroll
               for (int b = 0; b < kBlocks; ++b)
                 if (GROUPS == kSingle || min(8 * (8 * b + g) / group, ng - 1) == gr)
@@ -747,8 +763,8 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int tk = (k & 1) + (k >> 1) * 8;
-            r[k] = st + v_row + tk * sh.codes[1].pitch;
-            z[k] = reinterpret_cast<const uint8_t *>(st) + v_zero + tk * sh.zeros[1].pitch;
+            r[k] = st_v + v_row + tk * sh.codes[1].pitch;
+            z[k] = reinterpret_cast<const uint8_t *>(st_vz) + v_zero + tk * sh.zeros[1].pitch;
             const uint8_t *o = off + 4 * (2 * t + tk);
             if (!sh.zeros[1].wide) z[k] += o[1];
             mis[k] = 0;
