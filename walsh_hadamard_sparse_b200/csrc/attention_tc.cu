@@ -5,22 +5,24 @@
 // A CTA takes one cached head and up to 256 rows of queries (tokens times the
 // query heads that share the head), two tiles of 128, and walks 128 cached tokens
 // at a time:
-//   S_w = Q_w C_k^T    tcgen05, operands in shared memory, fp32 in TMEM
+//   S_w = Q_w C_k^T    tcgen05, operands in shared memory, fp32 in TMEM, 64 tokens
+//                      at a time: one half is multiplied while the other is read
 //   P_w = 2^(S_w - m)  by the 128 threads of the tile, a row each; f16 over S_w
 //   O_w += P_w C_v     tcgen05, P from TMEM, C_v in shared memory
-// C holds the integers code - zero, exact in f16, so a token's scale multiplies
-// a column of S, and of P, in fp32; where a head has several groups a token's
-// largest scale does, and C the rest: (code - zero) times scale / largest, rounded
-// twice to 11 bits. The query (rotated, its largest value near 2^15) and P are
-// rounded to 11 bits as in attention_mma.cuh, and the maximum is kept to within
-// what f16 leaves room for: a tile whose weights sum to more than 2^9 has its
-// maximum taken and is done again, others need none.
+// C holds (code - zero) times scale in f16: the difference is exact, the scale
+// (times a power of two that follows the largest) and the product are rounded to
+// 11 bits each, 2^-12 beside the 2^-9 of a bf16 output. (Scales left to the
+// columns of S and P in fp32 were two multiplications and 16 loads more for 16
+// scores: 384 us for 4 chunks of 1021 behind 2048.) The query (rotated, its
+// largest value near 2^15) and P are rounded to 11 bits as in attention_mma.cuh;
+// the maximum is kept to within what f16 leaves room for: half a tile whose
+// weights sum to more than 2^7 has its maximum taken and is done again, others
+// need none.
 //   8 warps  unpack, four the keys and four the values: a lane's 32 codes of a
 //            token, fetched a tile ahead, to swizzled tiles of f16 (two of each).
 //   8 warps  softmax: four for each tile of rows.
-//   1 warp   issues the products: S_w of the next tokens behind O_w of these, so
-//            that one tile of rows is multiplied while the other's weights are
-//            made.
+//   1 warp   issues the products: S_w of the next tile's half behind O_w of this
+//            one's.
 // Bound: the 16384 exponentials and about 80 thousand other operations of a tile of 128
 // rows and tokens, and 1024 clocks of products. Every wait is bounded; a thread
 // that gives up sets the error word and goes on without waiting.
@@ -44,8 +46,9 @@ using wide::sw128;
 constexpr int kRowsTile = 128, kKeys = 128, kUnpackWarps = 8, kSoftWarps = 8;  // (unpacking: half for the keys)
 constexpr int kUnpackers = kUnpackWarps * 16, kRounds = 128 / kUnpackers * 2, kTcThreads = (kUnpackWarps + kSoftWarps + 1) * 32;
 constexpr int kScaleSlots = 4;      // tiles whose scales are kept: a tile's are read until its weights are made
-constexpr float kTcTop = 64.f;      // of a value's scale in f16; times kTcSum below the largest f16
-constexpr float kTcSum = 512.f;     // of a tile's weights, before its maximum is taken again
+constexpr float kTcTop = 64.f;      // of a scale in f16, times 255 of a code below the largest
+constexpr float kTcShift = 8.f;     // weights are kept 2^8 times as large: f16 holds them to 2^-33 of the maximum's
+constexpr float kTcSum = 32768.f;   // of the weights of half a tile, before its maximum is taken again
 constexpr uint32_t kTcCols = 512;   // TMEM: S_0, S_1, O_0, O_1
 constexpr unsigned int kErrTc = 0x10000u;  // a wait gave up
 
@@ -182,13 +185,13 @@ __device__ __forceinline__ void rotate32(float *v, int had) {
     }
 }
 
-// Scales of a tile of tokens, as the softmax threads read them.
+// What the softmax threads know of a tile of tokens.
 struct alignas(16) TileScales {
-  float k[kKeys], v[kKeys];  // of the scores; of the weights, times c
-  uint32_t live[4];          // a bit a token
-  float c;                   // what the values' scales are multiplied by, a power of two
-  int bad;                   // some token's values have a group that is no number
-  uint8_t groups[kKeys];     // which groups, where bad
+  uint32_t live[4];       // a bit a token
+  float factor[2];        // what the keys' and the values' scales were multiplied by, powers of two
+  int bad;                // some token's values have a group that is no number
+  int pad;
+  uint8_t groups[kKeys];  // which groups, where bad
 };
 
 template <int DP>
@@ -198,7 +201,7 @@ struct TcSmem {
   static constexpr int kBars = kScales + kScaleSlots * (int)sizeof(TileScales), kTotal = kBars + 256 + 1024;
 };
 // barriers
-enum { kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kOFull = 12, kQReady = 14, kScFull = 16, kBarCount = 20 };
+enum { kKFull = 0, kVFull = 2, kKEmpty = 4, kVEmpty = 6, kSFull = 8, kPReady = 12, kPDone = 16, kOFull = 18, kQReady = 20, kScFull = 22, kBarCount = 26 };  // kSFull, kPReady: 2 w + half
 
 // Waits for a phase of a barrier, suspended for up to a microsecond at a time; false after two seconds.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
@@ -292,60 +295,51 @@ struct Unpacker {
   bool ok = true;
   uint32_t it = 0;           // tiles so far
   uint32_t w[kRounds][kSlabs][B];  // raw codes of the next tile's tokens
-  float most[kRounds];       // scales: the largest of a token; no number where the keys have a bad group
-  uint32_t share[kRounds][kSlabs];  // the lane's groups' part of it, two f16
+  float most[kRounds];       // the largest scale of a token that is a number
+  float scale[kRounds][kSlabs];  // of the lane's groups
   uint8_t zero[kRounds][kSlabs], bad[kRounds];
   bool on[kRounds];
 
   __device__ __forceinline__ Unpacker(const AttnArgs &a_, bool values_, uint8_t *smem_, uint32_t bars_, uint32_t one_)
       : a(a_), c(values_ ? a_.v : a_.k), values(values_), smem(smem_), bars(bars_), one(one_) {}
 
-  // The token's largest scale, the shares of the lane's groups, which groups are no numbers.
+  // The scales and zero points of the lane's groups, the token's largest scale, which groups are no numbers. Values of
+  // such a group stay out of the products, where they would meet weights of zero; keys go in as they are.
   __device__ __forceinline__ void scales(int64_t row, int ng, int r) {
     const float *s = c.scales + row * ng;
     const uint8_t *z = c.zeros + row * ng;
-    const int half = threadIdx.x & 1;
-    bad[r] = 0;
-    if (ng == 1) {
-      most[r] = __ldg(s);
-      const uint8_t z0 = __ldg(z);
-#pragma unroll
-      for (int i = 0; i < kSlabs; ++i) zero[r][i] = z0;
-      return;
-    }
     float all[4], top = 0.f;
     int b = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       all[i] = i < ng ? __ldg(s + i) : 0.f;
       if (fabsf(all[i]) < INFINITY) top = fmaxf(top, fabsf(all[i]));
-      else b |= 1 << i, all[i] = 0.f;
+      else if (values) b |= 1 << i, all[i] = 0.f;
     }
-    const float inv = top > 0.f ? 1.f / top : 0.f;
-    most[r] = b && !values ? __int_as_float(0x7fc00000) : top, bad[r] = (uint8_t)b;
+    most[r] = top, bad[r] = (uint8_t)b;
 #pragma unroll
     for (int i = 0; i < kSlabs; ++i) {
-      const int d = 64 * i + 32 * half, g = d < c.head_dim ? d / c.group : 0;
-      const float mine = (g == 0 ? all[0] : g == 1 ? all[1] : g == 2 ? all[2] : all[3]) * inv;
-      share[r][i] = pair16(mine, mine), zero[r][i] = __ldg(z + g);
+      const int d = 64 * i + 32 * (threadIdx.x & 1), g = ng > 1 && d < c.head_dim ? d / c.group : 0;
+      scale[r][i] = g == 0 ? all[0] : g == 1 ? all[1] : g == 2 ? all[2] : all[3], zero[r][i] = __ldg(z + g);
     }
   }
 
-  __device__ __forceinline__ void write(uint8_t *row, int token, int r, int i, bool scaled, bool live) {
+  // (code - zero) times the scale, both exact or rounded once in f16, and their product once.
+  __device__ __forceinline__ void write(uint8_t *row, int token, int r, int i, float factor, bool live) {
     Zero<B> z;
     z.set((zero[r][i] | 0xe400u) * 0x10001u);
     const int half = threadIdx.x & 1;
+    const uint32_t share = pair16(scale[r][i] * factor, scale[r][i] * factor);
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       uint32_t v[4] = {0, 0, 0, 0};
       if (live) {
         unpack_row<B>(chunk_of<B>(w[r][i], x), z, one, v);
-        if (scaled)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __half2 p = __hmul2(reinterpret_cast<const __half2 &>(v[k]), reinterpret_cast<const __half2 &>(share[r][i]));
-            v[k] = reinterpret_cast<const uint32_t &>(p);
-          }
+        for (int k = 0; k < 4; ++k) {
+          const __half2 p = __hmul2(reinterpret_cast<const __half2 &>(v[k]), reinterpret_cast<const __half2 &>(share));
+          v[k] = reinterpret_cast<const uint32_t &>(p);
+        }
       }
       *reinterpret_cast<uint4 *>(row + (((4 * half + x) ^ (token & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
@@ -398,45 +392,40 @@ struct Unpacker {
     fetch();
     t0 += kKeys;
     ask(g.run > 1);
-    float factor = kNoScale;  // of the values' scales: follows the largest met by any of the warps
+    float factor = kNoScale;  // of the scales: follows the largest met by any of the warps
     uint8_t *tiles = smem + (values ? S::kV : S::kK);
     for (int u = 0; u < g.run; ++u, ++it) {
       const int st = it & 1;
       TileScales &sc = *reinterpret_cast<TileScales *>(smem + S::kScales + (it % kScaleSlots) * sizeof(TileScales));
-      if (values) {
-        float top = 0.f;
-        int any_bad_lane = 0;
+      float top = 0.f;
+      int any_bad = 0;
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) top = fmaxf(top, fabsf(most[r]) < INFINITY ? fabsf(most[r]) : 0.f), any_bad_lane |= bad[r];
-        const int flags = any_of(top * factor > kTcTop);
-        if (flags) {
-          uint32_t *top_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount + 16);
-          if (threadIdx.x % kUnpackers == 0) *top_s = 0;
-          meet();
-          atomicMax(top_s, __float_as_uint(top));
-          meet();
-          int e = 127 + 6 - ((int)(*top_s >> 23) - 127 + 2);
-          e = e < 1 ? 1 : e > 247 ? 247 : e;
-          factor = fminf(factor, __uint_as_float((uint32_t)e << 23));
-          meet();
-        }
-        const int any_bad = ng > 1 ? any_of(any_bad_lane) : 0;
-        if (threadIdx.x % kUnpackers == 0) sc.c = factor, sc.bad = any_bad;
+      for (int r = 0; r < kRounds; ++r) top = fmaxf(top, most[r]), any_bad |= bad[r];
+      if (any_of(top * factor > kTcTop)) {
+        uint32_t *top_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount + 16) + values;
+        if (threadIdx.x % kUnpackers == 0) *top_s = 0;
+        meet();
+        atomicMax(top_s, __float_as_uint(top));
+        meet();
+        int e = 127 + 6 - ((int)(*top_s >> 23) - 127 + 2);
+        e = e < 1 ? 1 : e > 247 ? 247 : e;
+        factor = fminf(factor, __uint_as_float((uint32_t)e << 23));
+        meet();
       }
+      if (values) {
+        any_bad = any_of(any_bad);
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r) {
-        const int token = mine + 16 * r;
-        if (values) {
-          if (half == 0) sc.v[token] = most[r] * factor, sc.groups[token] = bad[r];
-          continue;
-        }
-        const unsigned b = __ballot_sync(~0u, on[r]);
-        if (half == 0) sc.k[token] = most[r];
-        if (lane == 0) {
-          unsigned x = b & 0x55555555u;  // the even bits together
+        for (int r = 0; r < kRounds; ++r)
+          if (half == 0) sc.groups[mine + 16 * r] = bad[r];
+        if (threadIdx.x % kUnpackers == 0) sc.factor[1] = factor, sc.bad = any_bad;
+      } else {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+          unsigned x = __ballot_sync(~0u, on[r]) & 0x55555555u;  // two lanes a token: the even bits together
           x = (x | x >> 1) & 0x33333333u, x = (x | x >> 2) & 0x0f0f0f0fu, x = (x | x >> 4) & 0x00ff00ffu, x = (x | x >> 8) & 0xffffu;
-          reinterpret_cast<uint16_t *>(sc.live)[warp * kRounds + r] = (uint16_t)x;
+          if (lane == 0) reinterpret_cast<uint16_t *>(sc.live)[warp * kRounds + r] = (uint16_t)x;
         }
+        if (threadIdx.x % kUnpackers == 0) sc.factor[0] = factor;
       }
       arrive(bars + 8 * (kScFull + it % kScaleSlots));
       wait((values ? kVEmpty : kKEmpty) + st, (it >> 1 & 1) ^ 1);
@@ -445,7 +434,7 @@ struct Unpacker {
       for (int r = 0; r < kRounds; ++r)
 #pragma unroll
         for (int i = 0; i < kSlabs; ++i)
-          write(tile + i * (kKeys * 128) + r * (16 * 128), mine, r, i, ng > 1, on[r] && 32 * (2 * i + half) < D);
+          write(tile + i * (kKeys * 128) + r * (16 * 128), mine, r, i, factor, on[r] && 32 * (2 * i + half) < D);
       bulk::fence_proxy();
       arrive(bars + 8 * ((values ? kVFull : kKFull) + st));
       if (u + 1 < g.run) {  // the next tile's codes are on their way while this one is multiplied
@@ -455,12 +444,13 @@ struct Unpacker {
       }
     }
   }
-  __device__ __forceinline__ static void meet() { asm volatile("bar.sync 2, %0;" ::"n"(kUnpackers) : "memory"); }
-  __device__ __forceinline__ static int any_of(int x) {  // whether it is true of any unpacking thread
+  // the unpacking threads of the keys, or of the values
+  __device__ __forceinline__ void meet() const { asm volatile("bar.sync %0, %1;" ::"r"(values ? 3 : 2), "n"(kUnpackers) : "memory"); }
+  __device__ __forceinline__ int any_of(int x) const {  // whether it is true of any of them
     int any;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, 2, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, %3, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
                  : "=r"(any)
-                 : "r"(x), "n"(kUnpackers)
+                 : "r"(x), "n"(kUnpackers), "r"(values ? 3 : 2)
                  : "memory");
     return any;
   }
@@ -479,9 +469,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     for (int i = 0; i < 2; ++i) {
       bulk::init(bars + 8 * (kKFull + i), kUnpackers), bulk::init(bars + 8 * (kVFull + i), kUnpackers);
       bulk::init(bars + 8 * (kKEmpty + i), 1), bulk::init(bars + 8 * (kVEmpty + i), 1);
-      bulk::init(bars + 8 * (kSFull + i), 1), bulk::init(bars + 8 * (kOFull + i), 1);
-      bulk::init(bars + 8 * (kPReady + i), 128), bulk::init(bars + 8 * (kQReady + i), 128);
+      bulk::init(bars + 8 * (kPDone + i), 1), bulk::init(bars + 8 * (kOFull + i), 1), bulk::init(bars + 8 * (kQReady + i), 128);
     }
+    for (int i = 0; i < 4; ++i) bulk::init(bars + 8 * (kSFull + i), 1), bulk::init(bars + 8 * (kPReady + i), 128);
     for (int i = 0; i < kScaleSlots; ++i) bulk::init(bars + 8 * (kScFull + i), kUnpackWarps * 32);
     bulk::fence_init();
   }
@@ -527,7 +517,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     const uint32_t s_at = tmem + lanes + 128 * w, o_at = tmem + lanes + 256 + 128 * w;
     uint8_t *q_tile = smem + S::kQ + w * S::kTile;
     bool ok = true;
-    uint32_t it = 0, slot = 0, segment = 0;  // tiles of this tile of rows, and of the CTA; segments with rows in it
+    uint32_t it = 0, halves = 0, slot = 0, segment = 0;  // tiles (and halves) of this tile of rows, tiles of the CTA; segments with rows in it
     auto wait = [&](int bar, uint32_t parity) { ok = ok && wait_for(bars + 8 * bar, parity); };
     while (left > 0) {
       const Segment g(a, at, left);
@@ -600,17 +590,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         const int j = g.rows.j0 + (real ? rr / g.rows.heads : 0);
         const int past = g.s.past, lim = a.tree ? past : past + j + 1, safe = a.tree ? past : past + g.rows.j0 + 1;
         const unsigned long long mask = a.tree && real ? (unsigned long long)a.tree[g.s.row0 + j] : 0;
-        float m = -INFINITY, l = 0.f, c_old = 0.f;
+        float m = -INFINITY, l = 0.f, c_old = 0.f;  // m: the maximum less kTcShift, so that weights are 2^kTcShift at it
         uint32_t nan_groups = 0;
         int t0 = at.unit * kKeys;
-        const f32x2 ff = both(f, f);
         for (int u = 0; u < g.run; ++u, ++it, t0 += kKeys) {
           const uint32_t tile = slot + u;
           wait(kScFull + tile % kScaleSlots, tile / kScaleSlots & 1);
-          wait(kSFull + w, it & 1);
-          fence_after();
           const TileScales &sc = *reinterpret_cast<const TileScales *>(smem + S::kScales + (tile % kScaleSlots) * sizeof(TileScales));
           const uint4 live = *reinterpret_cast<const uint4 *>(sc.live);
+          const float c_now = sc.factor[1], fk = f * inverse2(sc.factor[0]);
+          const f32x2 ff = both(fk, fk);
           const bool masked = t0 + kKeys > safe || (live.x & live.y & live.z & live.w) != ~0u;
           uint32_t vis[4] = {live.x, live.y, live.z, live.w};
           if (masked) {
@@ -628,123 +617,93 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
               for (int x = 0; x < 4; ++x)
                 if (vis[x] >> t & 1) nan_groups |= sc.groups[32 * x + t];
           }
-          // the largest visible score of columns 32 first .. 127 (before them lie weights in place of scores)
-          auto largest = [&](int first) {
-            float top = -INFINITY;
-#pragma unroll 1
-            for (int x = first; x < 4; ++x) {
-              const uint32_t on = x == 0 ? vis[0] : x == 1 ? vis[1] : x == 2 ? vis[2] : vis[3];
-              uint32_t v[32];
-              load32(s_at + 32 * x, v);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (on >> i & 1) top = fmaxf(top, __uint_as_float(v[i]) * sc.k[32 * x + i]);
-            }
-            return top * f;
-          };
-          float turn = 1.f;  // of the sums so far
-          auto raise = [&](int first) {
-            const float top = largest(first), now = fmaxf(m, top);
-            turn = now == -INFINITY ? 1.f : exp2_fast(m - now);
-            m = now;
-          };
-          // rows that have seen nothing have no maximum yet
-          if (__any_sync(~0u, m == -INFINITY)) {
-            raise(0);
-            if (u == 0) turn = 1.f;
-          }
-          // the weights of columns 64 h .. 64 h + 63, for the maximum as it stands, and their sum
-          float sum = 0.f;
-          uint32_t p[32];
-          auto weights = [&](int h, auto hidden) {
-            const float base = m == -INFINITY ? 0.f : m;
-            const f32x2 mm = both(-base, -base);
-            f32x2 total = 0;
-            float v[2][16];
-            const uint32_t from = s_at + 64 * h;
-            const float4 *k4 = reinterpret_cast<const float4 *>(sc.k + 64 * h), *v4 = reinterpret_cast<const float4 *>(sc.v + 64 * h);
-            columns16(from, v[0]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float *z = v[x & 1];
-              columns_done(z);
-              if (x < 3) columns16(from + 16 * (x + 1), v[(x + 1) & 1]);  // on its way meanwhile
-              uint32_t on = ~0u;
-              if constexpr (decltype(hidden)::value) on = (h ? x >> 1 ? vis[3] : vis[2] : x >> 1 ? vis[1] : vis[0]) >> (16 * (x & 1));
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float4 kk = k4[4 * x + i], vv = v4[4 * x + i];
-                float e[4];
-                split(fma2(mul2(both(z[4 * i], z[4 * i + 1]), both(kk.x, kk.y)), ff, mm), e[0], e[1]);
-                split(fma2(mul2(both(z[4 * i + 2], z[4 * i + 3]), both(kk.z, kk.w)), ff, mm), e[2], e[3]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  e[k] = exp2_fast(e[k]);
-                  if constexpr (decltype(hidden)::value) e[k] = on >> (4 * i + k) & 1 ? e[k] : 0.f;
-                }
-                const f32x2 e01 = both(e[0], e[1]), e23 = both(e[2], e[3]);
-                total = add2(total, add2(e01, e23));
-                float y[4];
-                split(mul2(e01, both(vv.x, vv.y)), y[0], y[1]);
-                split(mul2(e23, both(vv.z, vv.w)), y[2], y[3]);
-                if constexpr (decltype(hidden)::value)  // a hidden token's scale may be no number
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) y[k] = e[k] == 0.f ? 0.f : y[k];
-                p[8 * x + 2 * i] = pair16(y[0], y[1]), p[8 * x + 2 * i + 1] = pair16(y[2], y[3]);
-              }
-            }
-            float s0, s1;
-            split(total, s0, s1);
-            return s0 + s1;
-          };
           // One copy of this loop's code for both halves and both tries: more of it does not stay in the instruction
-          // cache (unrolled, 730 us for 4 chunks of 1021 behind 2048, 440 so).
+          // cache (unrolled, 730 us for 4 chunks of 1021 behind 2048 where this took 440).
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h, ++halves) {
+            const uint32_t from = s_at + 64 * h, on0 = h ? vis[2] : vis[0], on1 = h ? vis[3] : vis[1];
+            wait(kSFull + 2 * w + h, it & 1);
+            fence_after();
+            float turn = 1.f;  // of the sums so far
+            auto raise = [&] {  // the maximum to the half's largest visible score
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t on = x ? on1 : on0;
+                uint32_t v[32];
+                load32(from + 32 * x, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (on >> i & 1) top = fmaxf(top, __uint_as_float(v[i]));
+              }
+              const float now = fmaxf(m, top * fk - kTcShift);
+              turn = now == -INFINITY ? 1.f : exp2_fast(m - now);
+              m = now;
+            };
+            // rows that have seen nothing have no maximum yet
+            if (__any_sync(~0u, m == -INFINITY)) raise();
+            uint32_t p[32];
+            auto weights = [&](auto hidden) {  // and their sum, for the maximum as it stands
+              const float base = m == -INFINITY ? 0.f : m;
+              const f32x2 mm = both(-base, -base);
+              f32x2 total[2] = {0, 0};
+              float v[2][16];
+              columns16(from, v[0]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                float *z = v[x & 1];
+                columns_done(z);
+                if (x < 3) columns16(from + 16 * (x + 1), v[(x + 1) & 1]);  // on its way meanwhile
+                uint32_t on = ~0u;
+                if constexpr (decltype(hidden)::value) on = (x >> 1 ? on1 : on0) >> (16 * (x & 1));
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                  float e[2];
+                  split(fma2(both(z[i], z[i + 1]), ff, mm), e[0], e[1]);
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) {
+                    e[k] = exp2_fast(e[k]);
+                    if constexpr (decltype(hidden)::value) e[k] = on >> (i + k) & 1 ? e[k] : 0.f;
+                  }
+                  total[i >> 1 & 1] = add2(total[i >> 1 & 1], both(e[0], e[1]));
+                  p[8 * x + i / 2] = pair16(e[0], e[1]);
+                }
+              }
+              float s0, s1;
+              split(add2(total[0], total[1]), s0, s1);
+              return s0 + s1;
+            };
             float part;
 #pragma unroll 1
-            for (bool again = u > 0;; again = false) {
-              part = masked ? weights(h, std::true_type()) : weights(h, std::false_type());
-              if (!again || !__any_sync(~0u, !(part <= kTcSum / 2))) break;
+            for (bool again = u + h > 0;; again = false) {
+              part = masked ? weights(std::true_type()) : weights(std::false_type());
+              if (!again || !__any_sync(~0u, !(part <= kTcSum))) break;
               const float before = turn;
-              raise(2 * h);
-              if (h == 1 && __any_sync(~0u, turn != 1.f)) {  // the first half's weights are stored, in the old units
-                uint32_t z[32];
-                stores_done();
-                load32(s_at, z);
-                const uint32_t t2 = pair16(turn, turn);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const __half2 y = __hmul2(reinterpret_cast<const __half2 &>(z[i]), reinterpret_cast<const __half2 &>(t2));
-                  z[i] = reinterpret_cast<const uint32_t &>(y);
-                }
-                store32(s_at, z);
-                sum *= turn;
-              }
+              raise();
               turn *= before;
             }
-            sum += part;
-            store32(s_at + 32 * h, p);  // over scores that have been read: the first half's, both times
-          }
-          // ---- the sums so far in the new units: nothing of this tile of rows is being multiplied now
-          const float grow = sc.c * (c_old == 0.f ? 0.f : inverse2(c_old));  // a power of two, at most 1
-          const bool first = u == 0;
-          if (!first && __any_sync(~0u, turn != 1.f || grow != 1.f)) {
-            const float by = turn * grow;
+            store32(from, p);  // over scores that have been read
+            // the sums so far in the new units, once the products before are done
+            const float grow = h ? 1.f : c_now * (c_old == 0.f ? 0.f : inverse2(c_old));  // a power of two, at most 1
+            if (u + h > 0 && __any_sync(~0u, turn != 1.f || grow != 1.f)) {
+              wait(kPDone + w, (halves - 1) & 1);
+              fence_after();
+              const float by = turn * grow;
 #pragma unroll 1
-            for (int x = 0; x < DP / 32; ++x) {
-              uint32_t v[32];
-              load32(o_at + 32 * x, v);
+              for (int x = 0; x < DP / 32; ++x) {
+                uint32_t v[32];
+                load32(o_at + 32 * x, v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
-              store32(o_at + 32 * x, v);
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * by);
+                store32(o_at + 32 * x, v);
+              }
             }
+            l = (u + h > 0 ? l * turn : 0.f) + part;
+            stores_done();
+            fence_before();
+            arrive(bars + 8 * (kPReady + 2 * w + h));
           }
-          c_old = sc.c;
-          l = l * turn + sum;
-          stores_done();
-          fence_before();
-          arrive(bars + 8 * (kPReady + w));
+          c_old = c_now;
         }
         // ---- the rows
         wait(kOFull + w, segment & 1);
@@ -815,27 +774,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     bool ok = true;
     if (wide::elected()) {
       // D fp32, A and B f16; S: both K-major, N 128; O: A in TMEM, B MN-major, N DP
-      constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys >> 3) << 17) | (8u << 24);
+      constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kKeys / 2 >> 3) << 17) | (8u << 24);
       constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(DP >> 3) << 17) | (8u << 24);
       uint32_t it = 0, tiles[2] = {0, 0}, segment[2] = {0, 0};
       auto wait = [&](int bar, uint32_t parity) {
         ok = ok && wait_for(bars + 8 * bar, parity);
         fence_after();
       };
-      auto scores = [&](int w, int st) {
-        const uint64_t q = sw128(base + S::kQ + w * S::kTile), k = sw128(base + S::kK + st * S::kTile);
+      // half h of the tile's tokens: 64 rows of 128 bytes on in a slab
+      auto scores = [&](int w, int st, int h) {
+        const uint64_t q = sw128(base + S::kQ + w * S::kTile), k = sw128(base + S::kK + st * S::kTile + h * (64 * 128));
 #pragma unroll
         for (int x = 0; x < DP / 16; ++x) {
           const uint32_t off = (x >> 2) * (kKeys * 128 >> 4) + (x & 3) * 2;
-          wide::product(tmem + 128 * w, q + off, k + off, kIdescS, x != 0);
+          wide::product(tmem + 128 * w + 64 * h, q + off, k + off, kIdescS, x != 0);
         }
-        commit(bars + 8 * (kSFull + w));
+        commit(bars + 8 * (kSFull + 2 * w + h));
       };
-      auto values = [&](int w, int st, bool add) {
-        const uint64_t v = sw128_mn(base + S::kV + st * S::kTile);
+      auto values = [&](int w, int st, int h, bool add) {
+        const uint64_t v = sw128_mn(base + S::kV + st * S::kTile + h * (64 * 128));
 #pragma unroll
-        for (int x = 0; x < kKeys / 16; ++x)
-          product_t(tmem + 256 + 128 * w, tmem + 128 * w + 8 * x, v + x * (16 * 128 >> 4), kIdescO, add || x != 0);
+        for (int x = 0; x < kKeys / 32; ++x)
+          product_t(tmem + 256 + 128 * w, tmem + 128 * w + 64 * h + 8 * x, v + x * (16 * 128 >> 4), kIdescO, add || x != 0);
+        commit(bars + 8 * (kPDone + w));
       };
       while (left > 0) {
         const Segment g(a, at, left);
@@ -845,30 +806,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         }
         const int count = g.rows.n > 128 ? 2 : 1;
         for (int w = 0; w < count; ++w) wait(kQReady + w, segment[w] & 1);
-        for (int u = 0; u < g.run; ++u, ++it) {
+        for (int u = 0; u <= g.run; ++u) {  // scores of tile u behind values of tile u - 1, half by half
           const int st = it & 1, before = (it - 1) & 1;
-          wait(kKFull + st, it >> 1 & 1);
+          const bool more = u < g.run;
+          if (more) wait(kKFull + st, it >> 1 & 1);
           if (u > 0) wait(kVFull + before, (it - 1) >> 1 & 1);
-          for (int w = 0; w < count; ++w) {
-            if (u > 0) {
-              wait(kPReady + w, (tiles[w] - 1) & 1);
-              values(w, before, u > 1);
+          for (int h = 0; h < 2; ++h)
+            for (int w = 0; w < count; ++w) {
+              if (u > 0) {
+                wait(kPReady + 2 * w + h, (tiles[w] - 1) & 1);
+                values(w, before, h, u + h > 1);
+                if (!more && h) commit(bars + 8 * (kOFull + w));
+              }
+              if (more) scores(w, st, h);
             }
-            scores(w, st);
-            ++tiles[w];
-          }
-          commit(bars + 8 * (kKEmpty + st));
+          for (int w = 0; w < count; ++w) tiles[w] += more, segment[w] += !more;
+          if (more) commit(bars + 8 * (kKEmpty + st));
           if (u > 0) commit(bars + 8 * (kVEmpty + before));
+          it += more;
         }
-        const int last = (it - 1) & 1;
-        wait(kVFull + last, (it - 1) >> 1 & 1);
-        for (int w = 0; w < count; ++w) {
-          wait(kPReady + w, (tiles[w] - 1) & 1);
-          values(w, last, g.run > 1);
-          commit(bars + 8 * (kOFull + w));
-          ++segment[w];
-        }
-        commit(bars + 8 * (kVEmpty + last));
         g.next(a, &at, &left);
       }
       // the last rows' readers have met kOFull; nothing is in flight behind it
