@@ -61,12 +61,16 @@ def shuffled_table(g, totals, page_size, spare=2):
     return table, n_pages
 
 
-def attention(q, kd, vd, vstep, had_k, had_v, table, page_size, past, new, tree, scale, eps):
+def attention(q, kd, vd, vstep, had_k, had_v, table, page_size, past, new, tree, scale, eps, cached=0.0):
     """(out, lse, bound of out, bound of lse): fp64, for stored-frame pools kd, vd [slots, heads, D]; vstep: the largest
     |scale (code - zero)| each stored value could have. The bounds allow an arithmetic that rounds the rotated query and
     the softmax weights to relative eps each and sums in fp32, with weights below 2^-33 of the largest held to that: p
     scale is kept in f16, whose smallest numbers are 2^-24 apart, scaled so that 2^8 stands for p = 1 at the largest
-    scale."""
+    scale of a token that any row of the tile sees, or at one that is 2^10 times the largest that the row sees, whichever
+    is less (where there are larger ones the rows are done in fp32; 2^11 here, since the zero points let |code - zero|
+    differ twofold). cached: what rounding the cached values costs, relative
+    to each: 2^-10 where a scale and its product with (code - zero) are rounded to f16, 2^-11 each; keys' errors move
+    scores as the query's do, values' the sum in proportion."""
     n, q_heads, D = q.shape
     heads = kd.shape[1]
     grp, at, f32 = q_heads // heads, 0, 2.0**-24
@@ -103,10 +107,14 @@ def attention(q, kd, vd, vstep, had_k, had_v, table, page_size, past, new, tree,
                     # that (their own score and the total), are rounded once, and are summed in fp32
                     count = seen.sum(1)[:, None]
                     kq = np.where(seen[:, None], np.abs(qr[:, h]) @ np.abs(k).T, 0).max(-1)
-                    ds = (eps + (D + 16) * f32) * kq + 4 * f32 * np.where(np.isfinite(s), np.abs(s), 0).max(-1)
-                    rel = 2 * np.expm1(ds) + 2 * eps + (count + 64) * f32
-                    least = (count * 2.0**-33)[..., None] * np.where(used, vstep[slots, h], 0).max(0)
-                    tol[rows, cols] = spread_abs(rel[..., None] * (w @ np.abs(v)) + least, had_v) * (1 + 16 * f32) + 1e-30
+                    ds = (eps + cached * (1 + eps) + (D + 16) * f32) * kq + 4 * f32 * np.where(np.isfinite(s), np.abs(s), 0).max(-1)
+                    rel = 2 * np.expm1(ds) + 2 * eps + cached * (1 + 2 * eps) + (count + 64) * f32
+                    far = np.where(used, vstep[slots, h], 0)
+                    own = np.where(seen[..., None], far, 0).max(1)
+                    least = ((count * 2.0**-33) * np.minimum(far.max(0), 2.0**11 * own))[:, None]
+                    # (whatever the weights, both results lie between the values: twice the largest is never passed)
+                    moved = np.fmin(rel[..., None] * (w @ np.abs(v)), 2.1 * own[:, None])
+                    tol[rows, cols] = spread_abs(moved + least, had_v) * (1 + 16 * f32) + 1e-30
                     lse_tol[rows, cols] = ds + eps + (count + 64) * f32 + 4 * f32 * np.abs(np.where(some[:, None], lse[rows, cols], 0))
         at += m
     return out, lse, tol, lse_tol

@@ -134,11 +134,13 @@ class Setup:
         return W.cache_attention(self.kv, self.q, to_dev(self.table), to_dev(self.starts), to_dev(np.array(self.past, np.int64)),
                                  **args)
 
+    cached = 0.0  # rounding of cached values that the call does
+
     def ref(self):
         bits, bits_v, group, had_k, had_v = self.fmt
         eps = 2.0**-11 if self.dtype == "bf16" else 2.0**-21
         return R.attention(self.qv, R.dense_pool(self.pk, bits, group), R.dense_pool(self.pv, bits_v, group),
-                           R.largest_steps(self.pv, bits_v, group), had_k, had_v, self.table, self.page_size, self.past, self.new, self.tree, self.scale, eps)
+                           R.largest_steps(self.pv, bits_v, group), had_k, had_v, self.table, self.page_size, self.past, self.new, self.tree, self.scale, eps, self.cached)
 
     def check(self, out=None):
         got = host(self.run() if out is None else out)
@@ -285,6 +287,177 @@ def test_attention_bad_groups_in_masked_places():
             assert np.all(np.isnan(got[2])) and np.array_equal(np.delete(got, 2, 0), np.delete(clean, 2, 0))
             c.scales.view(n_slots, -1)[slot] = keep
         torch.cuda.synchronize()
+
+
+# Calls of many rows to a cached head, whose cached values are rounded to f16 with their scales.
+MANY = [(32, 4, 4, 32, 0, 0), (64, 2, 3, 64, 64, 0), (64, 3, 2, 32, 0, 64), (96, 4, 8, 32, 32, 32), (96, 8, 4, 96, 0, 2),
+        (128, 4, 4, 128, 128, 128), (128, 4, 4, 64, 64, 0), (128, 8, 8, 32, 8, 128), (128, 3, 3, 64, 128, 64), (128, 2, 2, 128, 0, 32)]
+
+
+def many_rows(*args, **kw):
+    s = Setup(*args, **kw)
+    s.cached = 2.0**-10
+    return s
+
+
+@pytest.mark.parametrize("D,bits,bits_v,group,had_k,had_v", MANY)
+def test_attention_of_many_rows(D, bits, bits_v, group, had_k, had_v):
+    """Chunks and trees of more than 32 rows to a cached head: every width, and other widths for the values; pasts around
+    the borders of tiles of tokens; sequences of one row or none beside them; 200 rows to a token."""
+    fmt = dict(D=D, bits=bits, bits_v=bits_v, group=group, had_k=had_k, had_v=had_v)
+    key = "-".join(map(str, fmt.values()))
+    many_rows("a" + key, [0, 127, 128, 129, 300, 1], [64, 1, 40, 33, 64, 0], grp=4, tree=random_trees, **fmt).check()
+    many_rows("b" + key, [0, 1000, 64], [300, 130, 1], grp=3, heads=1, page_size=100, **fmt).check()
+    many_rows("c" + key, [5, 140], [3, 1], grp=200, heads=1, **fmt).check()
+
+
+@pytest.mark.parametrize("past,new,heads,grp", [([100] * 60, [17] * 60, 8, 2), ([0] * 30, [130] * 30, 3, 5), ([3000, 0, 10], [50, 1, 300], 2, 4),
+                                                ([5000], [64], 1, 4)])
+def test_attention_of_many_rows_cut_between_ctas(past, new, heads, grp):
+    """Several tiles to a CTA, and a tile to all of them; again with the same bits."""
+    s = many_rows(f"cut{past[0]}-{grp}", past, new, heads=heads, grp=grp, D=128, group=128, had_k=128, had_v=128)
+    got = s.check()
+    for _ in range(3):
+        assert np.array_equal(host(s.run()), got)
+
+
+def test_attention_of_many_rows_scores_and_scales():
+    """Peaked and flat scores, queries of zeros, scales over many powers of two, the largest key or value last."""
+    s = many_rows("peaked", [300], [40], D=64, size=60.0)
+    s.check()
+    s = many_rows("flat", [500], [40], D=64)
+    s.scale = 0.0
+    s.check()
+    s = many_rows("negative", [100, 3], [40, 40], D=128, group=64, size=8.0)
+    s.scale = -0.3
+    s.check()
+    s = many_rows("nothing", [100], [64], D=128, group=128)
+    s.qv[...] = 0.0
+    s.q.zero_()
+    s.check()
+    for which in (0, 1):
+        for at in (0, 150, 299):
+            s = many_rows(f"end{which}{at}", [300], [40], D=64, size=2.0)
+            slot = int(s.table[0, at // 16]) * 16 + at % 16
+            sc = (s.pk, s.pv)[which][1]
+            sc.reshape(-1, *sc.shape[2:])[slot] *= 20.0
+            s.kv[which].scales.copy_(to_dev(sc))
+            s.check()
+
+
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 32), (128, 64), (128, 128)])
+def test_attention_of_many_rows_scales_of_many_powers_of_two(D, group):
+    """Values whose groups and tokens lie many powers of two apart, each group to its own measure."""
+    s = many_rows(f"powers{D}{group}", [260, 60], [40, 30], D=D, group=group)
+    for pool, cache in zip((s.pk, s.pv), s.kv):
+        if cache is s.kv[1]:
+            pool[1][...] *= (2.0 ** s.g.integers(-50, 40, (1, 1, 1, D // group))).astype(np.float32)
+            pool[1][...] *= (2.0 ** s.g.integers(-5, 5, pool[1].shape)).astype(np.float32)
+        else:
+            pool[1][...] *= 2.0**-20
+        cache.scales.copy_(to_dev(pool[1]))
+    s.check()
+
+
+def poison(s, where, factor, which):
+    """Scales of token `where` (sequence, token) times factor."""
+    b, t = where
+    slot = int(s.table[b, t // s.page_size]) * s.page_size + t % s.page_size
+    for i, pool in enumerate((s.pk, s.pv)):
+        if i in which:
+            sc = pool[1].reshape(-1, *pool[1].shape[2:])
+            sc[slot] *= np.float32(factor)
+            s.kv[i].scales.copy_(to_dev(pool[1]))
+
+
+@pytest.mark.parametrize("dtype,grp,new", [("bf16", 4, 40), ("bf16", 2, 8), ("f32", 2, 8), ("bf16", 2, 2), ("f32", 1, 3), ("f32", 4, 40)])
+@pytest.mark.parametrize("factor", [2.0**9, 2.0**13, 2.0**20, 1e30])
+@pytest.mark.parametrize("which", [(0,), (1,), (0, 1)])
+def test_attention_scales_that_only_some_rows_see(dtype, grp, new, factor, which):
+    """A token of far larger scales than the others takes nothing from the rows that do not see it: behind them in a chunk,
+    or on another branch of a tree; with and without tokens that all rows see."""
+    for past in (200, 0):
+        for tree in (None, random_trees):
+            for D, group in ((128, 64), (64, 64), (40, 8)):
+                s = Setup(f"wide{dtype}{grp}{new}{factor}{which}{past}{D}", [past, 30], [new, new], heads=2, grp=grp, D=D, group=group, dtype=dtype,
+                          tree=tree, size=0.5 if 0 in which else 1.0)
+                s.cached = 2.0**-10 if dtype == "bf16" and D != 40 else 0.0
+                poison(s, (0, past + new - 1), factor, which)
+                s.check()
+
+
+def test_attention_of_many_rows_scales_that_only_some_rows_see_in_whole_tiles():
+    """The same where CTAs have several tiles each, none cut; lse too (checked with the outputs)."""
+    s = many_rows("whole", [100] * 200, [24] * 200, heads=4, grp=2, D=128, group=128, had_v=128)
+    for b in (0, 77, 199):
+        poison(s, (b, 110), 1e25, (0, 1))
+    s.check()
+
+
+def test_attention_of_many_rows_bad_groups_in_masked_places():
+    """NaN and infinite groups in tokens that no row sees, or that some rows see."""
+    for D, group in ((128, 64), (64, 64), (128, 32)):
+        tree = np.zeros(64, np.int64)
+        for j in range(64):
+            tree[j] = 0 if j in (7, 50) else np.int64((1 << (j // 8 * 8)) | (1 << j) if j < 63 else -2**63)
+        s = many_rows(f"nan{D}{group}", [150], [64], D=D, group=group, tree=tree, grp=4)
+        clean = s.check()
+        n_slots = s.kv[0].n_slots
+        for value in (float("nan"), float("inf"), -float("inf")):
+            keep = [c.scales.clone() for c in s.kv]
+            seen = set()
+            for t in range(214):
+                if t < 150 or any(int(m) >> (t - 150) & 1 for m in tree):
+                    seen.add(int(s.table[0, t // 16]) * 16 + t % 16)
+            for c in s.kv:
+                flat = c.scales.view(n_slots, -1)
+                for slot in range(n_slots):
+                    if slot not in seen:
+                        flat[slot] = value
+            assert np.array_equal(host(s.run()), clean)
+            for at, rows in ((150 + 13, [13]), (150 + 16, [j for j in range(16, 24)])):  # a leaf; the root of a branch
+                slot = int(s.table[0, at // 16]) * 16 + at % 16
+                rows = [j for j in rows if j not in (7, 50)]
+                for c in s.kv:
+                    old = c.scales.view(n_slots, -1)[slot].clone()
+                    c.scales.view(n_slots, -1)[slot] = value
+                    got = host(s.run())
+                    assert np.array_equal(np.delete(got, rows, 0), np.delete(clean, rows, 0))
+                    if value != value:
+                        assert np.all(np.isnan(got[rows]))
+                    elif c is s.kv[1]:
+                        assert not np.any(np.isfinite(got[rows]))
+                    c.scales.view(n_slots, -1)[slot] = old
+            for c, k in zip(s.kv, keep):
+                c.scales.copy_(k)
+
+
+def test_attention_of_many_rows_pages_and_rows_behind():
+    """Pages that are none, rows behind the last sequence, and keys and values in groups of different sizes."""
+    import torch
+
+    W = _W()
+    s = many_rows("bad", [200, 40], [40, 40], D=128, group=128, grp=2)
+    q = torch.cat((s.q, s.q[:2]))
+    out = torch.full_like(q, 3.0)
+    lse = torch.full(q.shape[:2], 5.0, device="cuda")
+    W.cache_attention(s.kv, q, to_dev(s.table), to_dev(s.starts), to_dev(np.array(s.past)), out=out, lse=lse)
+    assert torch.all(out[80:] == 3.0) and torch.all(lse[80:] == 5.0)
+    for bad in (-1, int(s.kv[0].scales.shape[0])):
+        keep = s.table.copy()
+        s.table[0, 3] = bad
+        got = s.run()
+        with pytest.raises(W.QwhaError, match="page"):
+            W.check_stream_status()
+        s.table[0, 3] = -1
+        s.check(got)
+        s.table = keep
+    other = R.random_pool(s.g, s.kv[0].scales.shape[0], 16, 2, 128, 4, 64)
+    kv = (s.kv[0], W.QCache(4, 64, 0, *(to_dev(t) for t in other)))
+    got = host(W.cache_attention(kv, s.q, to_dev(s.table), to_dev(s.starts), to_dev(np.array(s.past)), scale=s.scale))
+    want, _, tol, _ = R.attention(s.qv, R.dense_pool(s.pk, 4, 128), R.dense_pool(other, 4, 64), R.largest_steps(other, 4, 64), 0, 0, s.table,
+                                  16, s.past, s.new, None, s.scale, 2.0**-11, 2.0**-10)
+    assert np.all(np.abs(got - want) <= tol + half_step("bf16") * np.abs(want))
 
 
 def test_attention_rows_behind_the_last_sequence_and_bad_pages():

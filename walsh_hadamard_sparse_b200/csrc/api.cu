@@ -1203,7 +1203,7 @@ qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_
   a.page_shift = 31 + lg, a.page_mul = (unsigned int)(((1ull << a.page_shift) + k->page_size - 1) / k->page_size);
   a.q_start = q_start, a.past = past, a.n_seqs = n_seqs, a.tree = tree;
   a.scale2 = (float)(scale * 1.4426950408889634), a.out = out, a.lse = lse, a.f32 = dt == QWHA_F32;
-  StageScope sc(ST_ATTENTION, attention_launches(), (cudaStream_t)stream);
+  StageScope sc(ST_ATTENTION, attention_launches(a), (cudaStream_t)stream);
   return cuda_status(launch_attention(a, ws, (cudaStream_t)stream), "cache_attention");
 }
 

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const _
   __shared__ Rows rows_s;
   __shared__ int count_s;
   extern __shared__ int slots_s[];  // the pieces
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (it waits for this launch before it writes)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, lane = threadIdx.x & 31;
   const int4 begun = a.part_desc[2 * c + 1];
@@ -265,13 +266,154 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const _
   }
 }
 
+// ---------------------------------------------------------------- repairing
+
+// The tensor-core kernels keep scales in f16 relative to the largest that any row of
+// the tile sees. A row that does not see that token has the less room for its own.
+// Tiles where tokens that not all rows see have scales so far above the others' that
+// bits would be lost are done again in fp32: 2^8 in attention_mma.cuh, where p scale has
+// steps of 2^-33 of the largest, so that a token costs 2^-25 of a row's own; 2^16 in
+// attention_tc.cu, where 2^-16 of the largest is still a normal number, and for the
+// keys too, whose scales are in f16 there. Caches of values of ordinary spread have none
+// of these; a third launch looks for them while the second runs, which costs 1.3 us.
+// (The same in the kernels themselves took registers and instruction cache from them:
+// 325 to 375 us for 304 where four chunks of 1021 tokens are answered behind 2048.)
+constexpr float kRoomMma = 256.f, kRoomTc = 65536.f;
+
+// The rows of a tile again, in fp32, a warp a row and a token at a time. Slow, and
+// right whatever the scales are.
+__device__ __forceinline__ void repair(const AttnArgs &a, int b, int block, int tile) {
+  const Seq s(a, b);
+  const int head_block = block_of(a, block), part = block - head_block * a.parts, each = a.tq * a.gh, length = s.length(a, tile);
+  const int lane = threadIdx.x & 31, D = a.k.head_dim, c0 = 8 * lane;
+  const Rows rows = rows_of(a, s, 0, part, tile);
+#pragma unroll 1
+  for (int rr = threadIdx.x >> 5; rr < a.part_rows; rr += blockDim.x >> 5) {
+    const int hl = rr / each, r = rr - hl * each, kv = head_block * a.hb + hl;
+    if (kv >= a.k.heads || r >= rows.n) continue;
+    const int j = rows.j0 + rows.token(r);
+    const int64_t row = rows.q_row(r), head = rows.q_head(r) + kv * a.grp;
+    const unsigned long long bits = a.tree ? (unsigned long long)a.tree[row] : 0;
+    float q[8], acc[8], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t at = row * a.q_stride + head * D + c0 + k;
+      q[k] = c0 >= D ? 0.f : a.f32 ? static_cast<const float *>(a.q)[at] : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q)[at]);
+      acc[k] = 0.f;
+    }
+    rotate_lanes<32>(q, a.k.had_block, a.unit_k, lane);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) q[k] *= a.scale2;
+#pragma unroll 1
+    for (int t = 0; t < length; ++t) {
+      if (!s.sees(a, j, bits, t)) continue;
+      const int64_t slot = slot_of(a, b, t);
+      if (slot < 0) continue;
+      float v[8], x = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = 0.f;
+      if (c0 < D) load_values(a.k, slot * a.k.heads + kv, lane, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x = fmaf(q[k], v[k], x);
+#pragma unroll
+      for (int o = 16; o; o /= 2) x += __shfl_xor_sync(~0u, x, o);
+      const float now = fmaxf(m, x), base = now == -INFINITY ? 0.f : now, turn = exp2f(m - base), p = exp2f(x - base);
+      m = now, l = l * turn + p;
+      if (c0 < D) load_values(a.v, slot * a.k.heads + kv, lane, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = p != 0.f ? fmaf(p, v[k], acc[k] * turn) : acc[k] * turn;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] *= inv;
+    rotate_lanes<32>(acc, a.v.had_block, a.unit_v, lane);
+    if (c0 < D) {
+      const int64_t to = (row * a.q_heads + head) * D + c0;
+      if (a.f32) {
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(a.out) + to);
+        dst[0] = io<float>::pack(acc), dst[1] = io<float>::pack(acc + 4);
+      } else {
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + to) = io<__nv_bfloat16>::pack(acc);
+      }
+    }
+    if (a.lse && lane == 0) a.lse[row * a.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+// Whether a tile is one of those. A row has at least the largest scale of the tokens that
+// all rows see, of which up to 32 are looked at, or, where there are none, maybe the
+// least of the others alone. The keys' groups count together: a score is their sum.
+struct Scales {
+  uint32_t top, all, some;  // the largest of tokens that not all rows see; of those that all see; the least of the first
+};
+template <bool TC>
+__device__ __forceinline__ bool needs_repair(const AttnArgs &a, const Seq &s, int b, int block, int tile, Scales (*of)[33]) {
+  const int ng = a.k.head_dim / a.k.group, head_block = block_of(a, block), length = s.length(a, tile);
+  const int safe = a.tree ? s.past : s.past + tile * a.tq + 1;  // every row sees the tokens below
+  if (s.rows == 1 || length <= safe) return false;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
+  const int per_head = (threads >> 5) / a.hb, hl = warp % a.hb, sub = warp / a.hb, kv = head_block * a.hb + hl;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.hb * 33; i += threads) of[i / 33][i % 33] = {0u, 0u, 0x7f800000u};
+  __syncthreads();
+  if (sub < per_head && kv < a.k.heads) {
+    const int32_t *table = a.pages + (int64_t)b * a.max_pages;
+    auto row_of = [&](int t) -> int64_t {  // of the token's scales; -1: none
+      const int pg = page_of(a, t), page = __ldg(table + pg);
+      return (uint32_t)page < (uint32_t)a.v.n_pages ? (((int64_t)page * a.v.page_size + t - pg * a.v.page_size) * a.v.heads + kv) * ng : -1;
+    };
+    auto put = [&](int g, float top, float all, float some) {
+      const uint32_t top_u = __reduce_max_sync(~0u, __float_as_uint(top)), all_u = __reduce_max_sync(~0u, __float_as_uint(all));
+      const uint32_t some_u = __reduce_min_sync(~0u, __float_as_uint(some));
+      if (lane == 0) atomicMax(&of[hl][g].top, top_u), atomicMax(&of[hl][g].all, all_u), atomicMin(&of[hl][g].some, some_u);
+    };
+    auto finite = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.f; };
+    const int step = 32 * per_head, first = 32 * sub + lane, near = max(safe - 32, 0) + first;
+    for (int g = 0; g < (TC ? ng + 1 : ng); ++g) {  // the last: the keys
+      const bool keys = g == ng;
+      float top = 0.f, all = 0.f, some = INFINITY;
+      for (int t = near; t < length; t += step) {
+        const int64_t row = row_of(t);
+        float x = 0.f;
+        if (row >= 0 && !keys) x = finite(__ldg(a.v.scales + row + g));
+        if (row >= 0 && keys)
+          for (int i = 0; i < ng; ++i) x = fmaxf(x, finite(__ldg(a.k.scales + row + i)));
+        if (t < safe) all = fmaxf(all, x);
+        else top = fmaxf(top, x), some = x > 0.f ? fminf(some, x) : some;
+      }
+      put(keys ? 32 : g, top, all, some);
+    }
+  }
+  __syncthreads();
+  bool far = false;
+  for (int i = threadIdx.x; i < a.hb * 33; i += threads) {
+    const int h = i / 33, g = i - h * 33;
+    if (g >= ng && !(TC && g == 32)) continue;
+    const Scales x = of[h][g];
+    far |= __uint_as_float(x.top) > (TC ? kRoomTc : kRoomMma) * __uint_as_float(x.all ? x.all : x.some);
+  }
+  return __syncthreads_or(far);
+}
+// CTA (x, y): tiles y, y + gridDim.y, ... of sequences x, x + gridDim.x, ...
+template <bool TC>
+__global__ void __launch_bounds__(256) attention_repair_kernel(const __grid_constant__ AttnArgs a) {
+  __shared__ Scales of[kMmaWarps][33];
+  for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
+    const Seq s(a, b);
+    for (long long i = blockIdx.y; i < (long long)s.tiles * a.blocks; i += gridDim.y) {
+      const int block = (int)(i / s.tiles), tile = (int)(i - (long long)block * s.tiles);
+      if (!needs_repair<TC>(a, s, b, block, tile, of)) continue;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      repair(a, b, block, tile);
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 size_t any_smem(int D) {
   return (size_t)(kAnyRows * D + kAnyTokens * (D + 4) + kAnyTokens * D + kAnyRows * kAnyTokens) * 4;
 }
 
 }  // namespace
-
-int attention_launches() { return 2; }
 
 namespace {
 
@@ -335,6 +477,13 @@ size_t cut_bytes(const Cut &c, int D) {
 // Whether the tensor-core kernels take a cache's codes: rows of whole words (3-bit
 // ones lie as they may).
 bool takes_codes(const qwha_cache &c) { return c.bits != 2 || c.head_dim % 16 == 0; }
+// (slots in 32 bits: a cache of more has rows of a few bytes)
+bool mma_takes(const AttnArgs &a) {
+  return takes_codes(a.k) && takes_codes(a.v) && a.k.group == a.v.group && a.k.n_pages * a.k.page_size < (1LL << 31);
+}
+bool tc_takes(const AttnArgs &a) { return cdiv(a.n, a.n_seqs) * a.grp > kTcAbove && attention_tc_takes(a); }
+// Whether rows may have to be done again: not where a tile has one token, whose rows all see the same.
+bool repairs(const AttnArgs &a) { return (tc_takes(a) || mma_takes(a)) && a.n > a.n_seqs; }
 
 }  // namespace
 
@@ -351,21 +500,22 @@ size_t attention_workspace(int32_t q_heads, int32_t head_dim, int32_t heads, int
   return most;
 }
 
+int attention_launches(const AttnArgs &a) { return repairs(a) ? 3 : 2; }
+
 cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
   static std::atomic<size_t> allowed[64];
   a.err = device_error_word();
   if (!a.err) return cudaErrorInvalidDevicePointer;
   const int D = a.k.head_dim;
-  // (slots in 32 bits: a cache of more has rows of a few bytes)
-  const bool mma = takes_codes(a.k) && takes_codes(a.v) && a.k.group == a.v.group && a.k.n_pages * a.k.page_size < (1LL << 31);
   const int64_t rows = cdiv(a.n, a.n_seqs) * a.grp;  // of a cached head, on average
-  const bool tc = rows > kTcAbove && attention_tc_takes(a);
+  const bool tc = tc_takes(a), mma = mma_takes(a);
+  const int64_t most = a.n <= a.n_seqs ? 1 : a.n;  // tokens of a tile
   Cut c;
   if (tc) {
-    c = tc_cut(a.grp, a.n);
+    c = tc_cut(a.grp, most);
   } else if (mma) {
     const int nt = rows <= 8 ? 1 : rows <= 16 || D > 128 ? 2 : 4;
-    c = mma_cut(D, a.k.heads, a.grp, a.n, nt, a.f32 ? 2 : 1, a.k.bits, a.v.bits, a.k.group);
+    c = mma_cut(D, a.k.heads, a.grp, most, nt, a.f32 ? 2 : 1, a.k.bits, a.v.bits, a.k.group);
   } else {
     c = any_cut(a.grp, a.n);
   }
@@ -395,7 +545,11 @@ cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr, cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, D <= 64 ? attention_join_kernel<8> : D <= 128 ? attention_join_kernel<16> : attention_join_kernel<32>, a);
+  e = cudaLaunchKernelEx(&cfg, D <= 64 ? attention_join_kernel<8> : D <= 128 ? attention_join_kernel<16> : attention_join_kernel<32>, a);
+  if (e != cudaSuccess || !repairs(a)) return e;
+  const int ctas = 2 * sm_count(), seqs = std::min(a.n_seqs, ctas);
+  cfg.gridDim = dim3(seqs, ctas / seqs), cfg.blockDim = dim3(256), cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, tc ? attention_repair_kernel<true> : attention_repair_kernel<false>, a);
 }
 
 }  // namespace qwha

@@ -188,7 +188,10 @@ __device__ __forceinline__ void rotate32(float *v, int had) {
 // What the softmax threads know of a tile of tokens.
 struct alignas(16) TileScales {
   uint32_t live[4];       // a bit a token
-  float factor[2];        // what the keys' and the values' scales were multiplied by, powers of two
+  float values[4];        // what the values' scales were multiplied by, of each 32 channels: powers of two
+  float grow[4];          // these against the last tile's, where grown
+  float keys;             // the keys'
+  int grown;
   int bad;                // some token's values have a group that is no number
   int pad;
   uint8_t groups[kKeys];  // which groups, where bad
@@ -376,6 +379,8 @@ struct Unpacker {
         on[r] = (uint32_t)page[r] < (uint32_t)a.k.n_pages;
         most[r] = 0.f, bad[r] = 0;
         if (!on[r]) {
+#pragma unroll
+          for (int i = 0; i < kSlabs; ++i) scale[r][i] = 0.f;
           if (page[r] != -2) atomicOr(a.err, kErrPage);
           continue;
         }
@@ -392,24 +397,39 @@ struct Unpacker {
     fetch();
     t0 += kKeys;
     ask(g.run > 1);
-    float factor = kNoScale;  // of the scales: follows the largest met by any of the warps
+    float factor[kSlabs];  // of the scales of the lane's channels (the keys: of all): follows the largest met by any of the warps
+#pragma unroll
+    for (int i = 0; i < kSlabs; ++i) factor[i] = kNoScale;
     uint8_t *tiles = smem + (values ? S::kV : S::kK);
     for (int u = 0; u < g.run; ++u, ++it) {
       const int st = it & 1;
       TileScales &sc = *reinterpret_cast<TileScales *>(smem + S::kScales + (it % kScaleSlots) * sizeof(TileScales));
-      float top = 0.f;
-      int any_bad = 0;
+      float top[kSlabs], grow[kSlabs];
+      int any_bad = 0, over = 0;
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r) top = fmaxf(top, most[r]), any_bad |= bad[r];
-      if (any_of(top * factor > kTcTop)) {
-        uint32_t *top_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount + 16) + values;
-        if (threadIdx.x % kUnpackers == 0) *top_s = 0;
+      for (int i = 0; i < kSlabs; ++i) {
+        top[i] = 0.f, grow[i] = 1.f;
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) top[i] = fmaxf(top[i], values ? fabsf(scale[r][i]) : most[r]);
+        over |= top[i] * factor[i] > kTcTop;
+      }
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) any_bad |= bad[r];
+      const int grown = any_of(over);
+      if (grown) {
+        uint32_t *top_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount + 16) + (values ? 4 : 0);
+        if (threadIdx.x % kUnpackers < 4) top_s[threadIdx.x % kUnpackers] = 0;
         meet();
-        atomicMax(top_s, __float_as_uint(top));
+#pragma unroll
+        for (int i = 0; i < kSlabs; ++i) atomicMax(top_s + (values ? 2 * i + half : 0), __float_as_uint(top[i]));
         meet();
-        int e = 127 + 6 - ((int)(*top_s >> 23) - 127 + 2);
-        e = e < 1 ? 1 : e > 247 ? 247 : e;
-        factor = fminf(factor, __uint_as_float((uint32_t)e << 23));
+#pragma unroll
+        for (int i = 0; i < kSlabs; ++i) {
+          int e = 127 + 6 - ((int)(top_s[values ? 2 * i + half : 0] >> 23) - 127 + 2);
+          e = e < 1 ? 1 : e > 247 ? 247 : e;
+          const float now = fminf(factor[i], __uint_as_float((uint32_t)e << 23));
+          grow[i] = now * inverse2(factor[i]), factor[i] = now;
+        }
         meet();
       }
       if (values) {
@@ -417,7 +437,11 @@ struct Unpacker {
 #pragma unroll
         for (int r = 0; r < kRounds; ++r)
           if (half == 0) sc.groups[mine + 16 * r] = bad[r];
-        if (threadIdx.x % kUnpackers == 0) sc.factor[1] = factor, sc.bad = any_bad;
+        if (threadIdx.x % kUnpackers < 2) {
+#pragma unroll
+          for (int i = 0; i < kSlabs; ++i) sc.values[2 * i + half] = factor[i], sc.grow[2 * i + half] = grow[i];
+          sc.bad = any_bad, sc.grown = grown;
+        }
       } else {
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
@@ -425,7 +449,7 @@ struct Unpacker {
           x = (x | x >> 1) & 0x33333333u, x = (x | x >> 2) & 0x0f0f0f0fu, x = (x | x >> 4) & 0x00ff00ffu, x = (x | x >> 8) & 0xffffu;
           if (lane == 0) reinterpret_cast<uint16_t *>(sc.live)[warp * kRounds + r] = (uint16_t)x;
         }
-        if (threadIdx.x % kUnpackers == 0) sc.factor[0] = factor;
+        if (threadIdx.x % kUnpackers == 0) sc.keys = factor[0];
       }
       arrive(bars + 8 * (kScFull + it % kScaleSlots));
       wait((values ? kVEmpty : kKEmpty) + st, (it >> 1 & 1) ^ 1);
@@ -434,7 +458,7 @@ struct Unpacker {
       for (int r = 0; r < kRounds; ++r)
 #pragma unroll
         for (int i = 0; i < kSlabs; ++i)
-          write(tile + i * (kKeys * 128) + r * (16 * 128), mine, r, i, factor, on[r] && 32 * (2 * i + half) < D);
+          write(tile + i * (kKeys * 128) + r * (16 * 128), mine, r, i, factor[i], on[r] && 32 * (2 * i + half) < D);
       bulk::fence_proxy();
       arrive(bars + 8 * ((values ? kVFull : kKFull) + st));
       if (u + 1 < g.run) {  // the next tile's codes are on their way while this one is multiplied
@@ -590,7 +614,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         const int j = g.rows.j0 + (real ? rr / g.rows.heads : 0);
         const int past = g.s.past, lim = a.tree ? past : past + j + 1, safe = a.tree ? past : past + g.rows.j0 + 1;
         const unsigned long long mask = a.tree && real ? (unsigned long long)a.tree[g.s.row0 + j] : 0;
-        float m = -INFINITY, l = 0.f, c_old = 0.f;  // m: the maximum less kTcShift, so that weights are 2^kTcShift at it
+        float m = -INFINITY, l = 0.f;  // m: the maximum less kTcShift, so that weights are 2^kTcShift at it
         uint32_t nan_groups = 0;
         int t0 = at.unit * kKeys;
         for (int u = 0; u < g.run; ++u, ++it, t0 += kKeys) {
@@ -598,7 +622,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
           wait(kScFull + tile % kScaleSlots, tile / kScaleSlots & 1);
           const TileScales &sc = *reinterpret_cast<const TileScales *>(smem + S::kScales + (tile % kScaleSlots) * sizeof(TileScales));
           const uint4 live = *reinterpret_cast<const uint4 *>(sc.live);
-          const float c_now = sc.factor[1], fk = f * inverse2(sc.factor[0]);
+          const float fk = f * inverse2(sc.keys);
           const f32x2 ff = both(fk, fk);
           const bool masked = t0 + kKeys > safe || (live.x & live.y & live.z & live.w) != ~0u;
           uint32_t vis[4] = {live.x, live.y, live.z, live.w};
@@ -684,13 +708,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             }
             store32(from, p);  // over scores that have been read
             // the sums so far in the new units, once the products before are done
-            const float grow = h ? 1.f : c_now * (c_old == 0.f ? 0.f : inverse2(c_old));  // a power of two, at most 1
-            if (u + h > 0 && __any_sync(~0u, turn != 1.f || grow != 1.f)) {
+            const bool grown = h == 0 && sc.grown;
+            if (u + h > 0 && __any_sync(~0u, turn != 1.f || grown)) {
               wait(kPDone + w, (halves - 1) & 1);
               fence_after();
-              const float by = turn * grow;
 #pragma unroll 1
               for (int x = 0; x < DP / 32; ++x) {
+                const float by = grown ? turn * sc.grow[x] : turn;
                 uint32_t v[32];
                 load32(o_at + 32 * x, v);
 #pragma unroll
@@ -703,14 +727,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             fence_before();
             arrive(bars + 8 * (kPReady + 2 * w + h));
           }
-          c_old = c_now;
         }
         // ---- the rows
         wait(kOFull + w, segment & 1);
         ++segment;
         fence_after();
         const bool done = g.starts && g.ends;
-        const float by = inverse2(c_old) * (done ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
+        const float share = done ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        // (kept until four tiles on, whose scores wait for the next segment's queries)
+        const TileScales &last = *reinterpret_cast<const TileScales *>(smem + S::kScales + ((slot + g.run - 1) % kScaleSlots) * sizeof(TileScales));
         const int had_v = done ? a.v.had_block : 0;
         const int64_t row = real ? g.rows.q_row(rr) : 0, head = real ? g.rows.q_head(rr) : 0;
         const int DV = a.v.head_dim;
@@ -725,6 +750,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         };
 #pragma unroll 1
         for (int x = 0; x < DP / 32; ++x) {
+          const float by = inverse2(last.values[x]) * share;
           uint32_t u[32];
           load32(o_at + 32 * x, u);
           float v[32];  // (place i of a chunk of eight is channel (i >> 1) + 4 (i & 1))

@@ -286,7 +286,7 @@ struct AttnArgs {
   int4 *part_desc;  // of CTA c: [2 c] and [2 c + 1]
 };
 size_t attention_workspace(int32_t q_heads, int32_t head_dim, int32_t heads, int64_t n, bool f32);
-int attention_launches();
+int attention_launches(const AttnArgs &a);
 cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s);
 // The tensor-core kernels (attention_mma.cuh): heads padded to 64, 128 or 256
 // channels, tiles of 8 nt rows. grid, warps and the cut are the caller's.
