@@ -108,11 +108,13 @@ class Setup:
     """A pool, a table and queries of an attention call, on both sides."""
 
     def __init__(self, key, past, new, heads=2, grp=2, D=64, bits=4, bits_v=None, group=64, had_k=0, had_v=0, page_size=16,
-                 dtype="bf16", tree=None, zero_top=None, size=1.0):
+                 dtype="bf16", tree=None, zero_top=None, size=1.0, room=0):
         W, g = _W(), rng_for(310, key)
         self.past, self.new, self.dtype, self.g = past, new, dtype, g
         bits_v = bits_v or bits
         self.table, n_pages = R.shuffled_table(g, [a + b for a, b in zip(past, new)], page_size)
+        # a table of more room than is used: calls that are not known to be small have other kernels
+        self.table = np.pad(self.table, ((0, 0), (0, max(0, room // page_size - self.table.shape[1]))), constant_values=-1)
         self.pk = R.random_pool(g, n_pages, page_size, heads, D, bits, group, zero_top)
         self.pv = R.random_pool(g, n_pages, page_size, heads, D, bits_v, group, zero_top)
         self.fmt, self.page_size = (bits, bits_v, group, had_k, had_v), page_size
@@ -122,6 +124,9 @@ class Setup:
         self.starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int64)
         self.tree = tree(g, new) if callable(tree) else tree
         self.scale = D**-0.5
+        # calls of more than 8 rows to a cached head may round cached values (R.attention)
+        rows = -(-sum(new) // len(new)) * grp
+        self.cached = 2.0**-10 if dtype == "bf16" and D % 32 == 0 and D <= 128 and group % 32 == 0 and rows > 8 else 0.0
 
     def run(self, **kw):
         import torch
@@ -133,8 +138,6 @@ class Setup:
         args.update(kw)
         return W.cache_attention(self.kv, self.q, to_dev(self.table), to_dev(self.starts), to_dev(np.array(self.past, np.int64)),
                                  **args)
-
-    cached = 0.0  # rounding of cached values that the call does
 
     def ref(self):
         bits, bits_v, group, had_k, had_v = self.fmt
@@ -180,8 +183,9 @@ def test_attention_formats(D, bits, group, had, dtype):
     key = f"{D}-{bits}-{group}-{had}-{dtype}"
     Setup("one" + key, [0, 1, 15, 16, 63, 64, 65, 200], [1] * 8, D=D, bits=bits, group=group, had_k=had, had_v=had,
           dtype=dtype).check()
-    Setup("tree" + key, [0, 33, 128], [3, 7, 1], D=D, bits=bits, group=group, had_k=0, had_v=had, dtype=dtype,
-          tree=random_trees, grp=3).check()
+    for room in (0, 1 << 20):
+        Setup("tree" + key, [0, 33, 128], [3, 7, 1], D=D, bits=bits, group=group, had_k=0, had_v=had, dtype=dtype,
+              tree=random_trees, grp=3, room=room).check()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -189,8 +193,9 @@ def test_attention_formats(D, bits, group, had, dtype):
                                            (2, 4, 33), (1, 16, 17), (2, 3, 64), (9, 2, 1), (12, 5, 4)])
 def test_attention_heads_and_rows(heads, grp, new, dtype):
     for tree in (None, random_trees):
-        Setup(f"{heads}-{grp}-{new}-{dtype}-{tree is None}", [17, 0, 90], [new, max(1, new - 2), new], heads=heads, grp=grp,
-              D=128, group=128, had_k=128, had_v=128, dtype=dtype, tree=tree).check()
+        for room in (0, 1 << 20):
+            Setup(f"{heads}-{grp}-{new}-{dtype}-{tree is None}", [17, 0, 90], [new, max(1, new - 2), new], heads=heads, grp=grp,
+                  D=128, group=128, had_k=128, had_v=128, dtype=dtype, tree=tree, room=room).check()
 
 
 @pytest.mark.parametrize("page_size", [1, 3, 16, 100])
@@ -296,7 +301,7 @@ MANY = [(32, 4, 4, 32, 0, 0), (64, 2, 3, 64, 64, 0), (64, 3, 2, 32, 0, 64), (96,
 
 def many_rows(*args, **kw):
     s = Setup(*args, **kw)
-    s.cached = 2.0**-10
+    assert s.cached
     return s
 
 
@@ -376,12 +381,11 @@ def poison(s, where, factor, which):
 def test_attention_scales_that_only_some_rows_see(dtype, grp, new, factor, which):
     """A token of far larger scales than the others takes nothing from the rows that do not see it: behind them in a chunk,
     or on another branch of a tree; with and without tokens that all rows see."""
-    for past in (200, 0):
+    for past, room in ((200, 0), (0, 0), (200, 1 << 20), (0, 1 << 20)):
         for tree in (None, random_trees):
             for D, group in ((128, 64), (64, 64), (40, 8)):
                 s = Setup(f"wide{dtype}{grp}{new}{factor}{which}{past}{D}", [past, 30], [new, new], heads=2, grp=grp, D=D, group=group, dtype=dtype,
-                          tree=tree, size=0.5 if 0 in which else 1.0)
-                s.cached = 2.0**-10 if dtype == "bf16" and D != 40 else 0.0
+                          room=room, tree=tree, size=0.5 if 0 in which else 1.0)
                 poison(s, (0, past + new - 1), factor, which)
                 s.check()
 

@@ -417,8 +417,15 @@ size_t any_smem(int D) {
 
 namespace {
 
-// Rows of a cached head above which tiles of 128 on tcgen05 are taken instead of 32 on mma.sync.
-constexpr int kTcAbove = 32;
+// Rows of a cached head above which tiles of 128 on tcgen05 are taken instead of 32 on
+// mma.sync, which does as many rows as there are (64 contexts of 4096, 8 heads: 328 us
+// against 163 with 16 rows, 242 with 32, 294 with 40, 327 with 48, 415 with 64); and
+// those above which it is where the call is small: its tiles are a head's, not all
+// heads', and are cut into fewer pieces (2 contexts of 1024: 22 us against 27 with 8
+// rows, 22 against 37 with 16, 25 against 63 with 32). Between the two measurements the
+// times are taken for linear, which puts the border near 2^14 tokens of a cached head
+// for each row; the table's room stands for the tokens, which only the device knows.
+constexpr int kTcAbove = 44, kTcAboveIfSmall = 8, kTcSmallLog2 = 14;
 
 // Shared memory of an SM, and what a CTA has of it besides the dynamic part: the kernels' arrays (more with more rows)
 // and 1 KB of the system's.
@@ -481,7 +488,10 @@ bool takes_codes(const qwha_cache &c) { return c.bits != 2 || c.head_dim % 16 ==
 bool mma_takes(const AttnArgs &a) {
   return takes_codes(a.k) && takes_codes(a.v) && a.k.group == a.v.group && a.k.n_pages * a.k.page_size < (1LL << 31);
 }
-bool tc_takes(const AttnArgs &a) { return cdiv(a.n, a.n_seqs) * a.grp > kTcAbove && attention_tc_takes(a); }
+bool tc_takes(const AttnArgs &a) {
+  const int64_t rows = cdiv(a.n, a.n_seqs) * a.grp, tokens = (int64_t)a.n_seqs * a.k.heads * a.cap;
+  return (rows > kTcAbove || (rows > kTcAboveIfSmall && tokens <= rows << kTcSmallLog2)) && attention_tc_takes(a);
+}
 // Whether rows may have to be done again: not where a tile has one token, whose rows all see the same.
 bool repairs(const AttnArgs &a) { return (tc_takes(a) || mma_takes(a)) && a.n > a.n_seqs; }
 
