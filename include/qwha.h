@@ -340,9 +340,15 @@ qwha_status qwha_rotary(qwha_dtype dt, int32_t n_x, const void *const *x, const 
  * them (QWHA_ERR_INVALID_ARG). What masked tokens hold has no effect (a group
  * stored as NaN included).
  * A rotated cache costs nothing per token: H is applied to the query and to the
- * output. Scores, softmax and sums are fp32. out must not overlap q.
- * Deterministic. ws: qwha_workspace_size(QWHA_OP_ATTENTION, q_heads, head_dim,
- * heads, n, 1 for bf16 or 2 for fp32) bytes. */
+ * output. Scores, softmax and sums are fp32. Before the products the rotated
+ * query and the softmax weights are rounded, each value by 2^-11 of itself for
+ * bf16 and 2^-21 for fp32 at most (weights below 2^-24 of a row's largest by
+ * 2^-33 of that), and in bf16 calls of many rows to a cached head the cached
+ * values too, by 2^-11; else these are exact.
+ * Rows whose tokens' scales are far below those of tokens that only other rows
+ * see are done in fp32, more slowly. out must not overlap q. Deterministic.
+ * ws: qwha_workspace_size(QWHA_OP_ATTENTION, q_heads, head_dim, heads, n, 1 for
+ * bf16 or 2 for fp32) bytes. */
 qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_dtype dt, const void *q, int64_t n,
                                  int32_t q_heads, int64_t q_stride, const int32_t *pages, int32_t max_pages,
                                  const int64_t *q_start, const int64_t *past, int32_t n_seqs, const int64_t *tree,

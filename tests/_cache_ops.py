@@ -69,7 +69,7 @@ def attention(q, kd, vd, vstep, had_k, had_v, table, page_size, past, new, tree,
     scale of a token that any row of the tile sees, or at one that is 2^10 times the largest that the row sees, whichever
     is less (where there are larger ones the rows are done in fp32; 2^11 here, since the zero points let |code - zero|
     differ twofold). cached: what rounding the cached values costs, relative
-    to each: 2^-10 where a scale and its product with (code - zero) are rounded to f16, 2^-11 each; keys' errors move
+    to each: 2^-11 where scale (code - zero) is rounded to f16 (the scale itself in two pieces, 2^-22); keys' errors move
     scores as the query's do, values' the sum in proportion."""
     n, q_heads, D = q.shape
     heads = kd.shape[1]

@@ -42,7 +42,10 @@ __device__ __forceinline__ void load_values(const qwha_cache &c, int64_t row, in
 
 // One cached head and up to eight rows of queries a tile: 32 tokens at a time go
 // to shared memory as fp32 values; lane t of a warp holds the scores of token t
-// for the warp's two rows, a thread the values of one or two channels.
+// for the warp's two rows, a thread the values of one or two channels. Bound by
+// its shared-memory reads: 64 contexts of 4096 tokens, 8 heads of 128, take 2.9 ms
+// where the kernels below take 0.1. It has what those leave: heads of 2-bit codes
+// that are no whole words, and keys and values in groups of different sizes.
 __global__ void __launch_bounds__(kAnyThreads) attention_any_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) float smem[];
   const int D = a.k.head_dim, pitch = D + 4;
@@ -174,7 +177,8 @@ __global__ void __launch_bounds__(kAnyThreads) attention_any_kernel(const AttnAr
 // The tile that CTA blockIdx.x of the kernel before began and left: its piece and
 // those of the CTAs that went on with it, in order. L lanes have a row, eight
 // channels each; they look at L pieces' maxima and sums at once and read the values
-// of four pieces ahead.
+// of four pieces ahead. Bound by the latency of those loads: 15 us of the 333 that 4
+// chunks of 1021 tokens behind 2048 take.
 constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinAhead = 4;
 template <int L>
 __global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const __grid_constant__ AttnArgs a) {

@@ -9,23 +9,28 @@
 //                      at a time: one half is multiplied while the other is read
 //   P_w = 2^(S_w - m)  by the 128 threads of the tile, a row each; f16 over S_w
 //   O_w += P_w C_v     tcgen05, P from TMEM, C_v in shared memory
-// C holds (code - zero) times scale in f16: the difference is exact, the scale
-// (times a power of two that follows the largest) and the product are rounded to
-// 11 bits each, 2^-12 beside the 2^-9 of a bf16 output. (Scales left to the
-// columns of S and P in fp32 were two multiplications and 16 loads more for 16
-// scores: 384 us for 4 chunks of 1021 behind 2048.) The query (rotated, its
-// largest value near 2^15) and P are rounded to 11 bits as in attention_mma.cuh;
-// the maximum is kept to within what f16 leaves room for: half a tile whose
-// weights sum to more than 2^7 has its maximum taken and is done again, others
-// need none.
+// C holds (code - zero) times scale in f16, rounded once (the difference is exact, the
+// scale, times a power of two that follows the largest of its group, comes in two
+// pieces): 2^-11 at the most beside the 2^-9 of a bf16 output, and different for each
+// channel, so that a score's errors average out. (A scale of one piece errs alike in all
+// channels of a token: 0.0023 against 0.0019 of error for a tree of 64, 0.0017 of it
+// the output's own rounding.) Scales left to the columns of S and P in fp32 were two
+// multiplications and 16 loads more for 16 scores: 384 us for 4 chunks of 1021 tokens
+// behind 2048, where this takes 333. The query (rotated, its largest value near 2^15)
+// and P are rounded to 11 bits as in attention_mma.cuh; the maximum is kept to within
+// what f16 leaves room for: half a tile whose weights sum to more than 2^7 has its
+// maximum taken and is done again, others need none.
 //   8 warps  unpack, four the keys and four the values: a lane's 32 codes of a
 //            token, fetched a tile ahead, to swizzled tiles of f16 (two of each).
 //   8 warps  softmax: four for each tile of rows.
 //   1 warp   issues the products: S_w of the next tile's half behind O_w of this
 //            one's.
 // Bound: the 16384 exponentials and about 80 thousand other operations of a tile of 128
-// rows and tokens, and 1024 clocks of products. Every wait is bounded; a thread
-// that gives up sets the error word and goes on without waiting.
+// rows and tokens, and 1024 clocks of products. 4 chunks of 1021 tokens behind 2048 (32
+// and 8 heads of 128, 8 bits): 333 us, 400 TFLOP/s; trees of 64 tokens on 16 contexts of
+// 4096, 4 bits: 142 us. Of a CTA's clocks in the first the softmax warps spend 38% on
+// weights, 14% on writing rows out, 11% on queries, 11% waiting for scores. Every wait is
+// bounded; a thread that gives up sets the error word and goes on without waiting.
 
 #include <cuda_fp16.h>
 
@@ -327,12 +332,13 @@ struct Unpacker {
     }
   }
 
-  // (code - zero) times the scale, both exact or rounded once in f16, and their product once.
+  // (code - zero) times the scale, which comes as the sum of two f16 numbers: the product is rounded once.
   __device__ __forceinline__ void write(uint8_t *row, int token, int r, int i, float factor, bool live) {
     Zero<B> z;
     z.set((zero[r][i] | 0xe400u) * 0x10001u);
     const int half = threadIdx.x & 1;
-    const uint32_t share = pair16(scale[r][i] * factor, scale[r][i] * factor);
+    const float full = scale[r][i] * factor;
+    const __half2 share = __float2half2_rn(full), rest = __float2half2_rn(full - __low2float(share));
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       uint32_t v[4] = {0, 0, 0, 0};
@@ -340,7 +346,7 @@ struct Unpacker {
         unpack_row<B>(chunk_of<B>(w[r][i], x), z, one, v);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const __half2 p = __hmul2(reinterpret_cast<const __half2 &>(v[k]), reinterpret_cast<const __half2 &>(share));
+          const __half2 d = reinterpret_cast<const __half2 &>(v[k]), p = __hfma2(d, share, __hmul2(d, rest));
           v[k] = reinterpret_cast<const uint32_t &>(p);
         }
       }

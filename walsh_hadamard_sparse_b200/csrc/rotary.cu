@@ -1,7 +1,9 @@
 // Rotary positions: pairs of channels of every head turn by the angle
 // positions[i] * freq[c], and are scaled by a factor.
 //
-// Memory bounds it (each value read and written once). The sines and cosines of
+// Memory bounds it (each value read and written once; 16381 tokens of 40 heads of
+// 80 in fp32, 419 MB both ways: 92 us, 4.6 TB/s, where a copy takes 64; 64 tokens of 40
+// heads of 128 in bf16: 5 us, a launch and two latencies). The sines and cosines of
 // a token are shared by all its heads: a CTA takes a tile of tokens (or some heads
 // of one, while the tokens alone do not fill the GPU), computes them into shared
 // memory while its first values are on their way, and then streams 16-byte
