@@ -108,25 +108,25 @@ class Setup:
     """A pool, a table and queries of an attention call, on both sides."""
 
     def __init__(self, key, past, new, heads=2, grp=2, D=64, bits=4, bits_v=None, group=64, had_k=0, had_v=0, page_size=16,
-                 dtype="bf16", tree=None, zero_top=None, size=1.0, room=0):
+                 dtype="bf16", tree=None, zero_top=None, size=1.0, room=0, group_v=None):
         W, g = _W(), rng_for(310, key)
         self.past, self.new, self.dtype, self.g = past, new, dtype, g
-        bits_v = bits_v or bits
+        bits_v, group_v = bits_v or bits, group_v or group
         self.table, n_pages = R.shuffled_table(g, [a + b for a, b in zip(past, new)], page_size)
         # a table of more room than is used: calls that are not known to be small have other kernels
         self.table = np.pad(self.table, ((0, 0), (0, max(0, room // page_size - self.table.shape[1]))), constant_values=-1)
         self.pk = R.random_pool(g, n_pages, page_size, heads, D, bits, group, zero_top)
-        self.pv = R.random_pool(g, n_pages, page_size, heads, D, bits_v, group, zero_top)
-        self.fmt, self.page_size = (bits, bits_v, group, had_k, had_v), page_size
+        self.pv = R.random_pool(g, n_pages, page_size, heads, D, bits_v, group_v, zero_top)
+        self.fmt, self.page_size, self.group_v = (bits, bits_v, group, had_k, had_v), page_size, group_v
         self.kv = (W.QCache(bits, group, had_k, *(to_dev(t) for t in self.pk)),
-                   W.QCache(bits_v, group, had_v, *(to_dev(t) for t in self.pv)))
+                   W.QCache(bits_v, group_v, had_v, *(to_dev(t) for t in self.pv)))
         self.q, self.qv = _rows(g, (sum(new), heads * grp, D), dtype, size)
         self.starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int64)
         self.tree = tree(g, new) if callable(tree) else tree
         self.scale = D**-0.5
         # calls of more than 8 rows to a cached head may round cached values (R.attention)
         rows = -(-sum(new) // len(new)) * grp
-        self.cached = 2.0**-11 + 2.0**-21 if dtype == "bf16" and D % 32 == 0 and D <= 128 and group % 32 == 0 and rows > 8 else 0.0
+        self.cached = 2.0**-11 + 2.0**-21 if dtype == "bf16" and D % 32 == 0 and D <= 128 and group % 32 == group_v % 32 == 0 and rows > 8 else 0.0
 
     def run(self, **kw):
         import torch
@@ -142,8 +142,8 @@ class Setup:
     def ref(self):
         bits, bits_v, group, had_k, had_v = self.fmt
         eps = 2.0**-11 if self.dtype == "bf16" else 2.0**-21
-        return R.attention(self.qv, R.dense_pool(self.pk, bits, group), R.dense_pool(self.pv, bits_v, group),
-                           R.largest_steps(self.pv, bits_v, group), had_k, had_v, self.table, self.page_size, self.past, self.new, self.tree, self.scale, eps, self.cached)
+        return R.attention(self.qv, R.dense_pool(self.pk, bits, group), R.dense_pool(self.pv, bits_v, self.group_v),
+                           R.largest_steps(self.pv, bits_v, self.group_v), had_k, had_v, self.table, self.page_size, self.past, self.new, self.tree, self.scale, eps, self.cached)
 
     def check(self, out=None):
         got = host(self.run() if out is None else out)
@@ -206,6 +206,20 @@ def test_attention_chunks_of_prompts(page_size, D, group):
         s = Setup(f"chunk{page_size}-{D}-{dtype}", [0, 5, 131, 7], [70, 150, 33, 0], D=D, group=group, had_k=8, had_v=0,
                   page_size=page_size, dtype=dtype)
         s.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,group,group_v,bits,bits_v", [(128, 64, 128, 4, 4), (128, 128, 32, 4, 2), (128, 8, 64, 3, 8), (64, 64, 16, 2, 4),
+                                                         (256, 256, 32, 4, 4), (80, 40, 80, 4, 3), (24, 24, 8, 8, 4), (96, 32, 96, 4, 4)])
+def test_attention_groups_of_different_sizes(D, group, group_v, bits, bits_v, dtype):
+    """Keys and values in groups of their own, one token each, small trees, chunks; one cached head and several."""
+    fmt = dict(D=D, group=group, group_v=group_v, bits=bits, bits_v=bits_v, dtype=dtype, had_v=8)
+    key = f"groups{D}-{group}-{group_v}-{dtype}"
+    Setup("one" + key, [0, 15, 64, 200], [1] * 4, heads=1, **fmt).check()
+    Setup("three" + key, [700, 3], [1, 1], heads=3, grp=5, **fmt).check()
+    for room in (0, 1 << 20):
+        Setup("tree" + key, [0, 33, 128], [3, 7, 1], heads=5, grp=3, tree=random_trees, room=room, **fmt).check()
+    Setup("chunk" + key, [0, 131], [70, 33], heads=2, grp=2, **fmt).check()
 
 
 def test_attention_many_and_long_sequences():

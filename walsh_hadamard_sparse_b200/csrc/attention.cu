@@ -44,8 +44,8 @@ __device__ __forceinline__ void load_values(const qwha_cache &c, int64_t row, in
 // to shared memory as fp32 values; lane t of a warp holds the scores of token t
 // for the warp's two rows, a thread the values of one or two channels. Bound by
 // its shared-memory reads: 64 contexts of 4096 tokens, 8 heads of 128, take 2.9 ms
-// where the kernels below take 0.1. It has what those leave: heads of 2-bit codes
-// that are no whole words, and keys and values in groups of different sizes.
+// where the kernels below take 0.1. It has what those leave: heads whose 2-bit codes
+// are no whole words, and caches of 2^31 slots.
 __global__ void __launch_bounds__(kAnyThreads) attention_any_kernel(const AttnArgs a) {
   extern __shared__ __align__(16) float smem[];
   const int D = a.k.head_dim, pitch = D + 4;
@@ -351,7 +351,7 @@ struct Scales {
 };
 template <bool TC>
 __device__ __forceinline__ bool needs_repair(const AttnArgs &a, const Seq &s, int b, int block, int tile, Scales (*of)[33]) {
-  const int ng = a.k.head_dim / a.k.group, head_block = block_of(a, block), length = s.length(a, tile);
+  const int ng = a.v.head_dim / a.v.group, ng_k = a.k.head_dim / a.k.group, head_block = block_of(a, block), length = s.length(a, tile);
   const int safe = a.tree ? s.past : s.past + tile * a.tq + 1;  // every row sees the tokens below
   if (s.rows == 1 || length <= safe) return false;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
@@ -363,7 +363,7 @@ __device__ __forceinline__ bool needs_repair(const AttnArgs &a, const Seq &s, in
     const int32_t *table = a.pages + (int64_t)b * a.max_pages;
     auto row_of = [&](int t) -> int64_t {  // of the token's scales; -1: none
       const int pg = page_of(a, t), page = __ldg(table + pg);
-      return (uint32_t)page < (uint32_t)a.v.n_pages ? (((int64_t)page * a.v.page_size + t - pg * a.v.page_size) * a.v.heads + kv) * ng : -1;
+      return (uint32_t)page < (uint32_t)a.v.n_pages ? (((int64_t)page * a.v.page_size + t - pg * a.v.page_size) * a.v.heads + kv) : -1;
     };
     auto put = [&](int g, float top, float all, float some) {
       const uint32_t top_u = __reduce_max_sync(~0u, __float_as_uint(top)), all_u = __reduce_max_sync(~0u, __float_as_uint(all));
@@ -378,9 +378,9 @@ __device__ __forceinline__ bool needs_repair(const AttnArgs &a, const Seq &s, in
       for (int t = near; t < length; t += step) {
         const int64_t row = row_of(t);
         float x = 0.f;
-        if (row >= 0 && !keys) x = finite(__ldg(a.v.scales + row + g));
+        if (row >= 0 && !keys) x = finite(__ldg(a.v.scales + row * ng + g));
         if (row >= 0 && keys)
-          for (int i = 0; i < ng; ++i) x = fmaxf(x, finite(__ldg(a.k.scales + row + i)));
+          for (int i = 0; i < ng_k; ++i) x = fmaxf(x, finite(__ldg(a.k.scales + row * ng_k + i)));
         if (t < safe) all = fmaxf(all, x);
         else top = fmaxf(top, x), some = x > 0.f ? fminf(some, x) : some;
       }
@@ -469,10 +469,10 @@ Cut cut_warps(int D, int heads, int grp, int64_t n, int nt, int warps) {
   c.kt_log2 = ilog2(kTokens * kTilesPerStage * c.mma.per_head), c.least_log2 = 1;
   return c;
 }
-Cut mma_cut(int D, int heads, int grp, int64_t n, int nt, int pieces, int bits_k, int bits_v, int group) {
+Cut mma_cut(int D, int heads, int grp, int64_t n, int nt, int pieces, int bits_k, int bits_v, int group_k, int group_v) {
   for (int warps = kMmaWarps;; warps /= 2) {
     Cut c = cut_warps(D, heads, grp, n, nt, warps);
-    c.mma.smem = MmaShape(D, padded(D), bits_k, bits_v, group, nt, pieces, heads, c.hb, c.mma.per_head, c.mma.warps).total;
+    c.mma.smem = MmaShape(D, padded(D), bits_k, bits_v, group_k, group_v, nt, pieces, heads, c.hb, c.mma.per_head, c.mma.warps).total;
     const size_t fit = kSmemLimit / (c.mma.smem + smem_besides(nt));
     if (fit == 0 && warps > 1) continue;
     c.ctas = std::min(c.ctas, sm_count() * (int)std::max<size_t>(1, fit));
@@ -490,7 +490,7 @@ size_t cut_bytes(const Cut &c, int D) {
 bool takes_codes(const qwha_cache &c) { return c.bits != 2 || c.head_dim % 16 == 0; }
 // (slots in 32 bits: a cache of more has rows of a few bytes)
 bool mma_takes(const AttnArgs &a) {
-  return takes_codes(a.k) && takes_codes(a.v) && a.k.group == a.v.group && a.k.n_pages * a.k.page_size < (1LL << 31);
+  return takes_codes(a.k) && takes_codes(a.v) && a.k.n_pages * a.k.page_size < (1LL << 31);
 }
 bool tc_takes(const AttnArgs &a) {
   const int64_t rows = cdiv(a.n, a.n_seqs) * a.grp, tokens = (int64_t)a.n_seqs * a.k.heads * a.cap;
@@ -529,7 +529,7 @@ cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
     c = tc_cut(a.grp, most);
   } else if (mma) {
     const int nt = rows <= 8 ? 1 : rows <= 16 || D > 128 ? 2 : 4;
-    c = mma_cut(D, a.k.heads, a.grp, most, nt, a.f32 ? 2 : 1, a.k.bits, a.v.bits, a.k.group);
+    c = mma_cut(D, a.k.heads, a.grp, most, nt, a.f32 ? 2 : 1, a.k.bits, a.v.bits, a.k.group, a.v.group);
   } else {
     c = any_cut(a.grp, a.n);
   }

@@ -48,7 +48,7 @@ constexpr float kSlack = 5.f;  // by how much (base 2) a score may pass the maxi
 constexpr float kTop = 1024.f;  // p scale stays below this times 2^kSlack in f16
 constexpr float kNoScale = 1.329227995784916e36f;  // 2^120: no scale met yet
 
-// A head of one group, of groups of whole 64-channel blocks, of any groups.
+// A head of one group, of groups of whole 64-channel blocks, of any groups (keys and values of their own).
 enum { kSingle, kBlocked, kMixed };
 
 // An array of the cache in a stage: `bytes` of each token, `stride` apart in memory
@@ -81,7 +81,7 @@ struct alignas(16) Small {
 struct MmaShape {
   Part codes[2], scales[2], zeros[2];  // keys, values
   int row[2];                          // codes of a cached head's row
-  int ng;                              // groups of a head
+  int ng[2];                           // groups of a head
   int tokens;                          // of a stage
   int off_at, live_at, stage;          // off: 4 bytes a token, where its zero points and codes begin in their words
   int all_wide;                        // they begin at words in every token
@@ -90,10 +90,10 @@ struct MmaShape {
   int q_at, q_bytes;                   // queries as operands: after the ring; of a head
   int join_at, total;                  // where warps that share a head join
   __host__ __device__ MmaShape() {}
-  __host__ __device__ MmaShape(int D, int dp, int bits_k, int bits_v, int group, int nt, int pieces, int heads, int hb,
+  __host__ __device__ MmaShape(int D, int dp, int bits_k, int bits_v, int group_k, int group_v, int nt, int pieces, int heads, int hb,
                                int per_head, int warps) {
     const int bits[2] = {bits_k, bits_v};
-    ng = D / group, tokens = kTokens * kTilesPerStage * per_head;
+    ng[0] = D / group_k, ng[1] = D / group_v, tokens = kTokens * kTilesPerStage * per_head;
     int end = 0;
     for (int i = 0; i < 2; ++i) {
       row[i] = D / 8 * bits[i];
@@ -101,8 +101,8 @@ struct MmaShape {
       end += 48;  // the last chunks of padded channels, and of 3 bits, are read past the row's end
       end = (end + dp / 8 * bits[i] - row[i] + 15) / 16 * 16;
     }
-    for (int i = 0; i < 2; ++i) scales[i].set(hb * ng * 4, heads * ng * 4, 0, &end, tokens);
-    for (int i = 0; i < 2; ++i) zeros[i].set(hb * ng, heads * ng, 0, &end, tokens);
+    for (int i = 0; i < 2; ++i) scales[i].set(hb * ng[i] * 4, heads * ng[i] * 4, 0, &end, tokens);
+    for (int i = 0; i < 2; ++i) zeros[i].set(hb * ng[i], heads * ng[i], 0, &end, tokens);
     all_wide = codes[0].wide && codes[1].wide && zeros[0].wide && zeros[1].wide;
     smalls = scales[0].per + scales[1].per + zeros[0].per + zeros[1].per;
     fast = all_wide && codes[0].wide == 16 && codes[1].wide == 16 && smalls <= kMaxSmalls;
@@ -187,8 +187,8 @@ static __device__ __noinline__ uint32_t fetch_any(const AttnArgs &a, const MmaSh
     const char *codes = reinterpret_cast<const char *>(c.codes), *zeros = reinterpret_cast<const char *>(c.zeros);
     const char *code_end = codes + slots * sh.codes[i].stride, *zero_end = zeros + slots * sh.zeros[i].stride;
     codes += (int64_t)slot * sh.codes[i].stride + kv0 * sh.row[i];
-    zeros += (int64_t)slot * sh.zeros[i].stride + kv0 * sh.ng;
-    const char *scales = reinterpret_cast<const char *>(c.scales) + (int64_t)slot * sh.scales[i].stride + kv0 * sh.ng * 4;
+    zeros += (int64_t)slot * sh.zeros[i].stride + kv0 * sh.ng[i];
+    const char *scales = reinterpret_cast<const char *>(c.scales) + (int64_t)slot * sh.scales[i].stride + kv0 * sh.ng[i] * 4;
     fetch(sh.codes[i], codes, code_end, to + sh.codes[i].at + token * sh.codes[i].pitch, piece, step);
     fetch(sh.scales[i], scales, nullptr, to + sh.scales[i].at + token * sh.scales[i].pitch, piece, step);
     fetch(sh.zeros[i], zeros, zero_end, to + sh.zeros[i].at + token * sh.zeros[i].pitch, piece, step);
@@ -339,12 +339,15 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
   __shared__ float f_s[kMmaWarps][8 * NT];                          // by head: factor of a row's scores
   __shared__ Small small_s[kMaxSmalls];
   __shared__ Rows rows_s[kMmaWarps];                                // kept out of the loop's registers
-  __shared__ uint8_t group_s[32];                                   // of a chunk of eight channels
+  __shared__ uint8_t group_s[2][32];                                  // of a chunk of eight channels
   __shared__ int lim_s[kMmaWarps][8 * NT];
   __shared__ unsigned long long bits_s[kMmaWarps][8 * NT];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int warps = blockDim.x >> 5, ng = sh.ng, group = a.k.group, D = a.k.head_dim;
-  if (MIXED && threadIdx.x < 32) group_s[threadIdx.x] = (uint8_t)min(8 * (int)threadIdx.x / group, ng - 1);
+  const int warps = blockDim.x >> 5, D = a.k.head_dim;
+  const int ng_k = sh.ng[0], group_k = a.k.group, ng_v = MIXED ? sh.ng[1] : ng_k, group_v = MIXED ? a.v.group : group_k;
+  if (MIXED)
+    for (int x = threadIdx.x; x < 64; x += blockDim.x)
+      group_s[x >> 5][x & 31] = (uint8_t)min(8 * (x & 31) / (x >> 5 ? group_v : group_k), sh.ng[x >> 5] - 1);
   Place at;
   long long left = my_share(a, &at);
   __syncthreads();
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
       const qwha_cache &c = i & 1 ? a.v : a.k;
       const char *from = i < 2 ? reinterpret_cast<const char *>(c.scales) : reinterpret_cast<const char *>(c.zeros);
       for (int p = 0; p < x.per; ++p)
-        small_s[n++] = {from + p * x.wide, (uint32_t)x.stride, (uint32_t)(x.at + p * x.wide), (uint32_t)(i < 2 ? ng * 4 : ng), (uint32_t)x.pitch, (uint32_t)x.wide};
+        small_s[n++] = {from + p * x.wide, (uint32_t)x.stride, (uint32_t)(x.at + p * x.wide), (uint32_t)(i < 2 ? sh.ng[i] * 4 : sh.ng[i - 2]), (uint32_t)x.pitch, (uint32_t)x.wide};
     }
   }
   __syncthreads();
@@ -375,11 +378,11 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
   const uint32_t v_to = sh.codes[1].at + fetch_token * sh.codes[1].pitch + fetch_piece * 16;
   // the lane's tokens and head in a stage's parts
   const int k_row = sh.codes[0].at + (kTokens * kTilesPerStage * sub + g) * sh.codes[0].pitch + hl * sh.row[0];
-  const int k_scale = sh.scales[0].at + (kTokens * kTilesPerStage * sub + g) * sh.scales[0].pitch + hl * ng * 4;
-  const int v_scale = sh.scales[1].at + (kTokens * kTilesPerStage * sub + g) * sh.scales[1].pitch + hl * ng * 4;
-  const int k_zero = sh.zeros[0].at + (kTokens * kTilesPerStage * sub + g) * sh.zeros[0].pitch + hl * ng;
+  const int k_scale = sh.scales[0].at + (kTokens * kTilesPerStage * sub + g) * sh.scales[0].pitch + hl * ng_k * 4;
+  const int v_scale = sh.scales[1].at + (kTokens * kTilesPerStage * sub + g) * sh.scales[1].pitch + hl * ng_v * 4;
+  const int k_zero = sh.zeros[0].at + (kTokens * kTilesPerStage * sub + g) * sh.zeros[0].pitch + hl * ng_k;
   const int v_row = sh.codes[1].at + (kTokens * kTilesPerStage * sub + 2 * t) * sh.codes[1].pitch + hl * sh.row[1];
-  const int v_zero = sh.zeros[1].at + (kTokens * kTilesPerStage * sub + 2 * t) * sh.zeros[1].pitch + hl * ng;
+  const int v_zero = sh.zeros[1].at + (kTokens * kTilesPerStage * sub + 2 * t) * sh.zeros[1].pitch + hl * ng_v;
   while (left > 0) {
     const Seq s(a, at.b);
     if (s.rows == 0) {
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
       } else {  // codes and zero points are finite whatever they are; scales have to be
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          for (int x = fetch_piece; x < a.hb * ng; x += fetch_step)
+          for (int x = fetch_piece; x < a.hb * (i ? ng_v : ng_k); x += fetch_step)
             reinterpret_cast<float *>(smem + fill_at + sh.scales[i].at + fetch_token * sh.scales[i].pitch)[x] = 0.f;
       }
       if (fetch_piece == 0) {
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
             mis0 = (int)(reinterpret_cast<uintptr_t>(r0) & 3), r0 -= mis0;
             mis1 = (int)(reinterpret_cast<uintptr_t>(r1) & 3), r1 -= mis1;
           }
-          int gr = 0, edge = group;  // the group of the running sums, and where it ends
+          int gr = 0, edge = group_k;  // the group of the running sums, and where it ends
           Zero<B> za, zb;
           auto zeros = [&](int x) {
             za.set((z0[x] | 0xe400u) * 0x10001u), zb.set((z1[x] | 0xe400u) * 0x10001u);
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
 #pragma unroll
           for (int step = 0; step < kSteps; ++step) {
             const int chunk = 4 * step + t;
-            const int lane_group = MIXED ? group_s[chunk] : 0;
+            const int lane_group = MIXED ? group_s[0][chunk] : 0;
             if (MIXED) zeros(lane_group);
             uint32_t x[4], y[4];
             unpack_row<B>(load_run<B>(r0, chunk, mis0), za, one, x);
@@ -644,10 +647,10 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) part[n][e] = 0.f;
               }
-              if (GROUPS == kSingle || gr + 1 == ng) break;
+              if (GROUPS == kSingle || gr + 1 == ng_k) break;
               ++gr;
               const bool more = edge < 32 * (step + 1);
-              edge += group;
+              edge += group_k;
               if (!MIXED) zeros(gr);
               if (!MIXED || !more) break;
             }
@@ -737,7 +740,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
               if (u + h > 0)
 #pragma unroll
               for (int b = 0; b < kBlocks; ++b)
-                if (GROUPS == kSingle || min(8 * (8 * b + g) / group, ng - 1) == gr)
+                if (GROUPS == kSingle || min(8 * (8 * b + g) / group_v, ng_v - 1) == gr)
 #pragma unroll
                   for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -779,7 +782,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
               mis[k] = (int)(reinterpret_cast<uintptr_t>(r[k]) & 3), r[k] -= mis[k];
             }
           }
-          int have = -1, v_group = 0, v_edge = group;
+          int have = -1, v_group = 0, v_edge = group_v;
           Zero<B> za, zb;
           auto zeros = [&](int x) {
             za.set(z[0][x] | (uint32_t)z[1][x] << 16 | 0xe400e400u);
@@ -788,13 +791,13 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b) {
             const int chunk = 8 * b + g;
-            if (GROUPS == kBlocked && b > 0 && 64 * b == v_edge) ++v_group, v_edge += group;
-            const int lane_group = MIXED ? group_s[chunk] : v_group;
+            if (GROUPS == kBlocked && b > 0 && 64 * b == v_edge) ++v_group, v_edge += group_v;
+            const int lane_group = MIXED ? group_s[1][chunk] : v_group;
             if (MIXED || (GROUPS == kSingle ? b == 0 : lane_group != have)) zeros(lane_group);
             uint32_t x[8], y[8];
             unpack_columns<B>(load_run<B>(r[0], chunk, mis[0]), load_run<B>(r[1], chunk, mis[1]), za, one, x);
             unpack_columns<B>(load_run<B>(r[2], chunk, mis[2]), load_run<B>(r[3], chunk, mis[3]), zb, one, y);
-            const int g0 = MIXED ? group_s[8 * b] : lane_group, g1 = MIXED ? group_s[8 * b + 7] : lane_group;
+            const int g0 = MIXED ? group_s[1][8 * b] : lane_group, g1 = MIXED ? group_s[1][8 * b + 7] : lane_group;
             for (int gr = g0; gr <= g1; ++gr) {
               if (MIXED || (GROUPS == kSingle ? b == 0 : gr != have)) weights(gr), have = gr;
               const uint32_t keep = !MIXED || lane_group == gr ? ~0u : 0u;
@@ -825,7 +828,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
     const int slot_out = 2 * blockIdx.x + (starts ? 1 : 0);
     float back[kBlocks];
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) back[b] = inverse2(c_s[warp][GROUPS == kSingle ? 0 : min(8 * (8 * b + g) / group, ng - 1)]);
+    for (int b = 0; b < kBlocks; ++b) back[b] = inverse2(c_s[warp][GROUPS == kSingle ? 0 : min(8 * (8 * b + g) / group_v, ng_v - 1)]);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -974,14 +977,15 @@ cudaError_t launch_mma(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s) {
   auto kernel = attention_mma_kernel<DP, NT, PIECES, GROUPS>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), l.smem, allowed);
   if (e != cudaSuccess) return e;
-  const MmaShape sh(a.k.head_dim, DP, a.k.bits, a.v.bits, a.k.group, NT, PIECES, a.k.heads, a.hb, l.per_head, l.warps);
+  const MmaShape sh(a.k.head_dim, DP, a.k.bits, a.v.bits, a.k.group, a.v.group, NT, PIECES, a.k.heads, a.hb, l.per_head, l.warps);
   kernel<<<l.ctas, l.warps * 32, l.smem, s>>>(a, sh, l.per_head, 0x64006400u);
   return cudaGetLastError();
 }
 template <int DP, int NT, int PIECES>
 cudaError_t launch_mma_groups(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s) {
-  if (a.k.group == a.k.head_dim) return launch_mma<DP, NT, PIECES, kSingle>(a, l, s);
-  if (a.k.group % 64 == 0) return launch_mma<DP, NT, PIECES, kBlocked>(a, l, s);
+  const bool alike = a.k.group == a.v.group;
+  if (alike && a.k.group == a.k.head_dim) return launch_mma<DP, NT, PIECES, kSingle>(a, l, s);
+  if (alike && a.k.group % 64 == 0) return launch_mma<DP, NT, PIECES, kBlocked>(a, l, s);
   return launch_mma<DP, NT, PIECES, kMixed>(a, l, s);
 }
 template <int DP, int NT>

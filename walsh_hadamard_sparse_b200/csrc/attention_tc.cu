@@ -887,7 +887,7 @@ cudaError_t launch_tc(const AttnArgs &a, cudaStream_t s) {
 // Heads of whole runs of 32 channels up to 128, in groups of whole runs; bf16.
 bool attention_tc_takes(const AttnArgs &a) {
   const int D = a.k.head_dim;
-  return !a.f32 && D % 32 == 0 && D <= 128 && a.k.group == a.v.group && a.k.group % 32 == 0;
+  return !a.f32 && D % 32 == 0 && D <= 128 && a.k.group % 32 == 0 && a.v.group % 32 == 0;
 }
 cudaError_t launch_attention_tc(const AttnArgs &a, cudaStream_t s) {
   return a.k.head_dim <= 64 ? launch_tc<64>(a, s) : launch_tc<128>(a, s);
