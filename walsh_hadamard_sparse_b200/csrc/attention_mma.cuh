@@ -24,11 +24,11 @@
 // by 2^5, which a vote finds out; shuffles and the scaling of the sums are left
 // to those tiles.
 //
-// Bound: instruction issue on the ALU pipe, which unpacks (a mask, an or and half a
-// subtraction for two codes; three bits, twice that), not memory: 64 contexts of 4096
-// tokens, 8 heads of 128, 4 bits, one token each of 32 query heads take 97 us, 2.2 TB/s
-// of the 6.5 that a copy moves; 8 contexts of 32768, keys of 4 and values of 2 bits, 120
-// us; one context of 700, 19 us, of which both launches' latencies are most.
+// Bound: instructions, not memory: 2.4 of 4 a clock, the ALU pipe, which unpacks,
+// 47% busy, warps waiting for fixed latencies. 64 contexts of 4096 tokens, 8 heads of
+// 128, 4 bits, one token each of 32 query heads take 97 us, 2.2 TB/s of the 6.5 that
+// a copy moves; 8 contexts of 32768, keys of 4 and values of 2 bits, 120 us; one
+// context of 700, 19 us, of which both launches' latencies are most.
 #pragma once
 
 #include <cuda_fp16.h>
