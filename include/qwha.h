@@ -342,8 +342,8 @@ qwha_status qwha_rotary(qwha_dtype dt, int32_t n_x, const void *const *x, const 
  * A rotated cache costs nothing per token: H is applied to the query and to the
  * output. Scores, softmax and sums are fp32. Before the products the rotated
  * query and the softmax weights are rounded, each value by 2^-11 of itself for
- * bf16 and 2^-21 for fp32 at most (weights below 2^-24 of a row's largest by
- * 2^-33 of that), and in bf16 calls of many rows to a cached head the cached
+ * bf16 and 2^-21 for fp32 at most (a weight times a scale below 2^-24 of the
+ * largest scale that the row sees in the group by 2^-33 of that), and in bf16 calls of many rows to a cached head the cached
  * values too, by 2^-11; else these are exact.
  * Rows whose tokens' scales are far below those of tokens that only other rows
  * see are done in fp32, more slowly. out must not overlap q. Deterministic.

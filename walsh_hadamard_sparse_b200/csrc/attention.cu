@@ -438,7 +438,7 @@ constexpr size_t smem_besides(int nt) { return nt == 1 ? 6400 : 11 * 1024; }
 
 // How a call is cut and launched.
 struct Cut {
-  int tq, gh, parts, hb, kt_log2, least_log2, ctas;
+  int tq, gh, parts, hb, kt_log2, ctas;
   MmaLaunch mma;
   int part_rows() const { return hb * tq * gh; }
 };
@@ -450,12 +450,12 @@ Cut cut_rows(int grp, int rows, int64_t n) {
 }
 Cut any_cut(int grp, int64_t n) {
   Cut c = cut_rows(grp, kAnyRows, n);
-  c.hb = 1, c.kt_log2 = ilog2(kAnyTokens), c.least_log2 = 0, c.ctas = sm_count() * 3;
+  c.hb = 1, c.kt_log2 = ilog2(kAnyTokens), c.ctas = sm_count() * 3;
   return c;
 }
 Cut tc_cut(int grp, int64_t n) {
   Cut c = cut_rows(grp, kTcRows, n);
-  c.hb = 1, c.kt_log2 = kTcKeysLog2, c.least_log2 = 0, c.ctas = sm_count();
+  c.hb = 1, c.kt_log2 = kTcKeysLog2, c.ctas = sm_count();
   return c;
 }
 int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
@@ -466,7 +466,7 @@ Cut cut_warps(int D, int heads, int grp, int64_t n, int nt, int warps) {
   c.hb = (int)cdiv(heads, cdiv(heads, warps));
   c.mma.per_head = std::max(1, warps / c.hb), c.mma.warps = c.hb * c.mma.per_head, c.mma.nt = nt;
   c.ctas = sm_count() * std::max(1, (nt == 1 && padded(D) <= 128 ? 2 : 1) * kMmaWarps / c.mma.warps);
-  c.kt_log2 = ilog2(kTokens * kTilesPerStage * c.mma.per_head), c.least_log2 = 1;
+  c.kt_log2 = ilog2(kTokens * kTilesPerStage * c.mma.per_head);
   return c;
 }
 Cut mma_cut(int D, int heads, int grp, int64_t n, int nt, int pieces, int bits_k, int bits_v, int group_k, int group_v) {
@@ -533,7 +533,7 @@ cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
   } else {
     c = any_cut(a.grp, a.n);
   }
-  a.tq = c.tq, a.gh = c.gh, a.parts = c.parts, a.hb = c.hb, a.kt_log2 = c.kt_log2, a.least_log2 = c.least_log2, a.ctas = c.ctas;
+  a.tq = c.tq, a.gh = c.gh, a.parts = c.parts, a.hb = c.hb, a.kt_log2 = c.kt_log2, a.ctas = c.ctas;
   a.blocks = (int)cdiv(a.k.heads, a.hb) * a.parts, a.part_rows = c.part_rows();
   char *p = static_cast<char *>(ws);
   a.part_desc = reinterpret_cast<int4 *>(p), p += align_up((size_t)a.ctas * 2 * sizeof(int4), 256);

@@ -278,7 +278,6 @@ struct AttnArgs {
   int tq, gh, parts;  // new tokens and query heads (of a cached head) of a tile; parts of the group
   int hb, blocks;     // cached heads of a CTA; blocks of heads times parts
   int kt_log2;        // cached tokens of a unit: a power of two
-  int least_log2;     // units that are worth a CTA
   int ctas;
   // Pieces of tiles that are cut between CTAs.
   int part_rows;
