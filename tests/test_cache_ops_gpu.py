@@ -222,6 +222,16 @@ def test_attention_groups_of_different_sizes(D, group, group_v, bits, bits_v, dt
     Setup("chunk" + key, [0, 131], [70, 33], heads=2, grp=2, **fmt).check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,bits,bits_v,group", [(80, 4, 4, 40), (80, 2, 8, 40), (64, 3, 3, 64), (64, 3, 2, 32), (96, 2, 2, 96), (96, 3, 3, 96),
+                                                 (80, 3, 2, 40), (24, 4, 8, 24), (8, 8, 8, 8), (32, 2, 2, 32), (16, 4, 2, 16)])
+def test_attention_heads_that_share_pieces_of_16_bytes(D, bits, bits_v, group, dtype):
+    """All heads' codes of a token are whole 16-byte pieces, one head's are not."""
+    for heads in (1, 2, 3, 4, 8, 16):
+        Setup(f"pieces{heads}-{D}-{bits}-{bits_v}-{dtype}", [33, 0, 400], [1, 2, 1], heads=heads, D=D, bits=bits, bits_v=bits_v, group=group,
+              dtype=dtype, room=1 << 20).check()
+
+
 def test_attention_many_and_long_sequences():
     """More sequences than a CTA has threads; one long context cut between all CTAs beside short ones."""
     g = rng_for(311, "many")

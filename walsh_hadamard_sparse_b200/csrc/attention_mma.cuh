@@ -86,7 +86,7 @@ struct MmaShape {
   int off_at, live_at, stage;          // off: 4 bytes a token, where its zero points and codes begin in their words
   int all_wide;                        // they begin at words in every token
   int smalls;                          // pieces of a token's scales and zero points
-  int fast;                            // codes in 16-byte pieces, scales and zero points in whole pieces
+  int fast;                            // codes of a head in 16-byte pieces, scales and zero points in whole pieces
   int q_at, q_bytes;                   // queries as operands: after the ring; of a head
   int join_at, total;                  // where warps that share a head join
   __host__ __device__ MmaShape() {}
@@ -105,7 +105,7 @@ struct MmaShape {
     for (int i = 0; i < 2; ++i) zeros[i].set(hb * ng[i], heads * ng[i], 0, &end, tokens);
     all_wide = codes[0].wide && codes[1].wide && zeros[0].wide && zeros[1].wide;
     smalls = scales[0].per + scales[1].per + zeros[0].per + zeros[1].per;
-    fast = all_wide && codes[0].wide == 16 && codes[1].wide == 16 && smalls <= kMaxSmalls;
+    fast = all_wide && row[0] % 16 == 0 && row[1] % 16 == 0 && smalls <= kMaxSmalls;
     off_at = end, live_at = off_at + tokens * 4;
     stage = (live_at + tokens + 15) / 16 * 16;
     q_at = kStages * stage;
