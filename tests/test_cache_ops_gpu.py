@@ -350,6 +350,18 @@ def test_attention_of_many_rows_cut_between_ctas(past, new, heads, grp):
         assert np.array_equal(host(s.run()), got)
 
 
+@pytest.mark.parametrize("past,new,heads,grp,tree", [([13000, 9000], [126, 117], 8, 3, False), ([3000] * 18, [46, 43, 40] * 6, 4, 7, True),
+                                                     ([900, 300, 800] * 5, [161, 90, 33] * 5, 2, 8, False), ([7000, 5000], [513, 200], 2, 8, False)])
+def test_attention_of_many_rows_whose_last_tiles_are_short(past, new, heads, grp, tree):
+    """Segments with rows in one of the two tiles between segments with rows in both, over many tokens; the same bits again
+    and again, from the first run on."""
+    s = many_rows(f"short{past[0]}-{grp}", past, new, heads=heads, grp=grp, D=64, group=64, had_k=64, had_v=64, page_size=64,
+                  tree=random_trees if tree else None)
+    got = s.check()
+    for _ in range(8):
+        assert np.array_equal(host(s.run()), got)
+
+
 def test_attention_of_many_rows_scores_and_scales():
     """Peaked and flat scores, queries of zeros, scales over many powers of two, the largest key or value last."""
     s = many_rows("peaked", [300], [40], D=64, size=60.0)

@@ -622,9 +622,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         const unsigned long long mask = a.tree && real ? (unsigned long long)a.tree[g.s.row0 + j] : 0;
         float m = -INFINITY, l = 0.f;  // m: the maximum less kTcShift, so that weights are 2^kTcShift at it
         uint32_t nan_groups = 0;
+        float4 factors = make_float4(1.f, 1.f, 1.f, 1.f);  // the values' after the last tile
         int t0 = at.unit * kKeys;
         for (int u = 0; u < g.run; ++u, ++it, t0 += kKeys) {
           const uint32_t tile = slot + u;
+          // The scores first: they are made for these rows alone and not before the weights of the tile before are taken,
+          // so that the slot's barrier is at this tile's phase or has just left it. (Rows that skip segments are ahead of
+          // the others: the barrier alone might be at the phase of a tile before, of the same parity.)
+          wait(kSFull + 2 * w, it & 1);
           wait(kScFull + tile % kScaleSlots, tile / kScaleSlots & 1);
           const TileScales &sc = *reinterpret_cast<const TileScales *>(smem + S::kScales + (tile % kScaleSlots) * sizeof(TileScales));
           const uint4 live = *reinterpret_cast<const uint4 *>(sc.live);
@@ -641,6 +646,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
               vis[x] &= s;
             }
           }
+          // (taken while the weights are due: behind them the slot may be another tile's)
+          if (u + 1 == g.run) factors = *reinterpret_cast<const float4 *>(sc.values);
           if (sc.bad) {
             for (int t = 0; t < 32; ++t)
 #pragma unroll
@@ -740,8 +747,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         fence_after();
         const bool done = g.starts && g.ends;
         const float share = done ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        // (kept until four tiles on, whose scores wait for the next segment's queries)
-        const TileScales &last = *reinterpret_cast<const TileScales *>(smem + S::kScales + ((slot + g.run - 1) % kScaleSlots) * sizeof(TileScales));
         const int had_v = done ? a.v.had_block : 0;
         const int64_t row = real ? g.rows.q_row(rr) : 0, head = real ? g.rows.q_head(rr) : 0;
         const int DV = a.v.head_dim;
@@ -756,7 +761,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         };
 #pragma unroll 1
         for (int x = 0; x < DP / 32; ++x) {
-          const float by = inverse2(last.values[x]) * share;
+          const float by = inverse2(x == 0 ? factors.x : x == 1 ? factors.y : x == 2 ? factors.z : factors.w) * share;
           uint32_t u[32];
           load32(o_at + 32 * x, u);
           float v[32];  // (place i of a chunk of eight is channel (i >> 1) + 4 (i & 1))
