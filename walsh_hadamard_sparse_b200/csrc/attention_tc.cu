@@ -16,7 +16,7 @@
 // channels of a token: 0.0023 against 0.0019 of error for a tree of 64, 0.0017 of it
 // the output's own rounding.) Scales left to the columns of S and P in fp32 were two
 // multiplications and 16 loads more for 16 scores: 384 us for 4 chunks of 1021 tokens
-// behind 2048, where this takes 333. The query (rotated, its largest value near 2^15)
+// behind 2048, where this takes 350. The query (rotated, its largest value near 2^15)
 // and P are rounded to 11 bits as in attention_mma.cuh; the maximum is kept to within
 // what f16 leaves room for: half a tile whose weights sum to more than 2^7 has its
 // maximum taken and is done again, others need none.
@@ -27,8 +27,8 @@
 //            one's.
 // Bound: the 16384 exponentials and about 80 thousand other operations of a tile of 128
 // rows and tokens, and 1024 clocks of products. 4 chunks of 1021 tokens behind 2048 (32
-// and 8 heads of 128, 8 bits): 333 us, 400 TFLOP/s; trees of 64 tokens on 16 contexts of
-// 4096, 4 bits: 142 us. Of a CTA's clocks in the first the softmax warps spend 38% on
+// and 8 heads of 128, 8 bits): 350 us, 380 TFLOP/s; trees of 64 tokens on 16 contexts of
+// 4096, 4 bits: 150 us. Of a CTA's clocks in the first the softmax warps spend 38% on
 // weights, 14% on writing rows out, 11% on queries, 11% waiting for scores. Every wait is
 // bounded; a thread that gives up sets the error word and goes on without waiting.
 
