@@ -626,10 +626,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         int t0 = at.unit * kKeys;
         for (int u = 0; u < g.run; ++u, ++it, t0 += kKeys) {
           const uint32_t tile = slot + u;
-          // The scores first: they are made for these rows alone and not before the weights of the tile before are taken,
-          // so that the slot's barrier is at this tile's phase or has just left it. (Rows that skip segments are ahead of
-          // the others: the barrier alone might be at the phase of a tile before, of the same parity.)
-          wait(kSFull + 2 * w, it & 1);
+          // A segment's first scores before its scales: rows that skip segments are ahead of the others, and the slot's
+          // barrier might still be at an earlier phase of the same parity. Scores are not made before the weights of the
+          // tile before are taken, so that from the first ones on the barrier is at this tile's phase or has just left it.
+          if (u == 0) wait(kSFull + 2 * w, it & 1);
           wait(kScFull + tile % kScaleSlots, tile / kScaleSlots & 1);
           const TileScales &sc = *reinterpret_cast<const TileScales *>(smem + S::kScales + (tile % kScaleSlots) * sizeof(TileScales));
           const uint4 live = *reinterpret_cast<const uint4 *>(sc.live);
