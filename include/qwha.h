@@ -387,8 +387,8 @@ qwha_status qwha_pages_resize(const qwha_page_table *t, const int64_t *want, voi
  * [m]) name it and its copy for qwha_cache_copy_pages, -1 where there is none.
  * dst[i] must be an empty row (held 0) and named once; a pair that breaks this
  * or leaves the table is skipped and reported as above (of pairs with one dst
- * the first counts). Where the free pages end, the pair and those behind it that
- * need a page leave their dst empty. ws as above with T = m. Deterministic. */
+ * the first counts). Where the free pages end, the pair that cannot be served and
+ * all behind it leave their dst empty. ws as above with T = m. Deterministic. */
 qwha_status qwha_pages_fork(const qwha_page_table *t, const int64_t *src, const int64_t *dst, int32_t m, int32_t *from,
                             int32_t *to, void *ws, size_t ws_bytes, void *stream);
 

@@ -190,10 +190,10 @@ class Table:
                 continue
             used.add(int(b))
             full, part = int(held[a]) // self.ps, int(held[a]) % self.ps > 0
+            at += part
+            if at > len(free):
+                continue
             if part:
-                at += 1
-                if at > len(free):
-                    continue
                 origin[i], fresh[i] = pages[a, full], free[at - 1]
                 self.pages[b, full] = fresh[i]
                 self.refs[fresh[i]] = 1

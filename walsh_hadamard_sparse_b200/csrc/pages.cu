@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kTableThreads, 1)
     }
     long long sum;
     const long long before = block_before(need, warp_s, &sum);
-    if (i < m1) from[i] = need ? asked + before : kNone;
+    if (i < m1) from[i] = asked + before;  // pages that the pairs before it need
     asked += sum;
   }
   if (threadIdx.x == 0) sh->wanted[rank] = asked;
@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(kTableThreads, 1)
   if (free_before < granted) warp_free(t.refs, lo, hi, list, free_before, granted, t.refs);
   cluster.sync();
   for (int i = m0 + warp; i < m1; i += kTableWarps) {
-    const int64_t h = tokens[i], full = h < 0 ? 0 : pages_of(h - ps + 1, ps), at = from[i] == kNone ? -1 : asked_before + from[i];
-    const bool served = h >= 0 && at < granted;
+    const int64_t h = tokens[i], full = h < 0 ? 0 : pages_of(h - ps + 1, ps), at = asked_before + from[i];
+    const bool needs = h > full * ps, served = h >= 0 && at + needs <= n_free;
     int32_t o = -1, f = -1;
     if (served) {
       const int32_t *row = t.pages + src[i] * t.max_pages;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kTableThreads, 1)
         copy[j] = p;
         if (p < 0 || p >= t.n_pages || atomicAdd(t.refs + p, 1) <= 0) atomicOr(err, kErrTable);
       }
-      if (at >= 0) {
+      if (needs) {
         o = row[full], f = __ldcg(list + at);
         if (lane == 0) copy[full] = f;
       }
