@@ -51,16 +51,21 @@ constexpr float kNoScale = 1.329227995784916e36f;  // 2^120: no scale met yet
 // A head of one group, of groups of whole 64-channel blocks, of any groups (keys and values of their own).
 enum { kSingle, kBlocked, kMixed };
 
-// An array of the cache in a stage: `bytes` of each token, `stride` apart in memory
-// from `first` on, at `at` in the stage, `pitch` apart; fetched in pieces of `wide`
-// bytes. wide 0: a token's bytes begin anywhere in a word; the words that cover
-// them are fetched, and where they begin in the first is kept per token.
+// An array of the cache in a stage: `bytes` of each token (`head` of each cached
+// head), `stride` apart in memory, at `at` in the stage, `pitch` apart; fetched in
+// `per` pieces of `wide` bytes. wide 0: a token's bytes begin anywhere in a word; the
+// words that cover them are fetched, and where they begin in the first is kept per token.
 struct Part {
-  int bytes, stride, at, pitch, wide, per;
-  __host__ __device__ void set(int bytes_, int stride_, int step, int *end, int tokens) {
-    bytes = bytes_, stride = stride_;
+  int head, bytes, stride, at, pitch, wide, per;
+  // Pieces of a token's first `heads` heads. (The last block of cached heads may have
+  // fewer than the others; what follows its last head is the next token, or behind the
+  // last one nothing that may be read. `wide` divides both a block's bytes and a token's,
+  // so what is left for the last block is whole pieces too.)
+  __host__ __device__ int pieces(int heads) const { return wide ? heads * head / wide : (heads * head + 3 + 3) / 4; }
+  __host__ __device__ void set(int head_, int hb, int heads, int step, int *end, int tokens) {
+    head = head_, bytes = hb * head, stride = heads * head;
     wide = (bytes | stride) % 16 == 0 ? 16 : (bytes | stride) % 8 == 0 ? 8 : (bytes | stride) % 4 == 0 ? 4 : 0;
-    per = wide ? bytes / wide : (bytes + 3 + 3) / 4;
+    per = pieces(hb);
     const int room = wide ? bytes : per * 4;
     // step: rows of a quarter warp on distinct banks (an odd number of steps apart)
     pitch = step ? ((room + step - 1) / step | 1) * step : room;
@@ -97,12 +102,12 @@ struct MmaShape {
     int end = 0;
     for (int i = 0; i < 2; ++i) {
       row[i] = D / 8 * bits[i];
-      codes[i].set(hb * row[i], heads * row[i], bits[i] == 8 ? 32 : 16, &end, tokens);
+      codes[i].set(row[i], hb, heads, bits[i] == 8 ? 32 : 16, &end, tokens);
       end += 48;  // the last chunks of padded channels, and of 3 bits, are read past the row's end
       end = (end + dp / 8 * bits[i] - row[i] + 15) / 16 * 16;
     }
-    for (int i = 0; i < 2; ++i) scales[i].set(hb * ng[i] * 4, heads * ng[i] * 4, 0, &end, tokens);
-    for (int i = 0; i < 2; ++i) zeros[i].set(hb * ng[i], heads * ng[i], 0, &end, tokens);
+    for (int i = 0; i < 2; ++i) scales[i].set(ng[i] * 4, hb, heads, 0, &end, tokens);
+    for (int i = 0; i < 2; ++i) zeros[i].set(ng[i], hb, heads, 0, &end, tokens);
     all_wide = codes[0].wide && codes[1].wide && zeros[0].wide && zeros[1].wide;
     smalls = scales[0].per + scales[1].per + zeros[0].per + zeros[1].per;
     fast = all_wide && row[0] % 16 == 0 && row[1] % 16 == 0 && smalls <= kMaxSmalls;
@@ -162,18 +167,18 @@ __device__ __forceinline__ void copy_async_part(uint32_t dst, const void *src, i
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
-// Fetches a token's bytes of one array: piece i and every `step`-th after it.
+// Fetches a token's bytes of one array, n pieces: piece i and every `step`-th after it.
 // src: where the token's bytes begin; dst: its place in the stage.
 template <int N>
-__device__ __forceinline__ void fetch_wide(const Part &p, const char *src, uint32_t dst, int i, int step) {
-  for (; i < p.per; i += step) copy_async<N>(dst + i * N, src + i * N);
+__device__ __forceinline__ void fetch_wide(int n, const char *src, uint32_t dst, int i, int step) {
+  for (; i < n; i += step) copy_async<N>(dst + i * N, src + i * N);
 }
-__device__ __forceinline__ void fetch(const Part &p, const char *src, const char *end, uint32_t dst, int i, int step) {
-  if (p.wide == 16) return fetch_wide<16>(p, src, dst, i, step);
-  if (p.wide == 8) return fetch_wide<8>(p, src, dst, i, step);
-  if (p.wide == 4) return fetch_wide<4>(p, src, dst, i, step);
+__device__ __forceinline__ void fetch(const Part &p, int n, const char *src, const char *end, uint32_t dst, int i, int step) {
+  if (p.wide == 16) return fetch_wide<16>(n, src, dst, i, step);
+  if (p.wide == 8) return fetch_wide<8>(n, src, dst, i, step);
+  if (p.wide == 4) return fetch_wide<4>(n, src, dst, i, step);
   src -= reinterpret_cast<uintptr_t>(src) & 3;
-  for (; i < p.per; i += step)
+  for (; i < n; i += step)
     if (src + 4 * i < end) copy_async_part(dst + 4 * i, src + 4 * i, end - (src + 4 * i) < 4 ? (int)(end - (src + 4 * i)) : 4);
 }
 // All arrays of a token, whatever the format. Returns where zero points and codes
@@ -182,6 +187,8 @@ static __device__ __noinline__ uint32_t fetch_any(const AttnArgs &a, const MmaSh
                                            int token, int piece, int step) {
   uint32_t off = 0;
   const int64_t slots = a.k.n_pages * a.k.page_size;
+  const int here = a.k.heads - kv0;
+  auto count = [&](const Part &p) { return here >= a.hb ? p.per : p.pieces(here); };
   for (int i = 0; i < 2; ++i) {
     const qwha_cache &c = i ? a.v : a.k;
     const char *codes = reinterpret_cast<const char *>(c.codes), *zeros = reinterpret_cast<const char *>(c.zeros);
@@ -189,9 +196,9 @@ static __device__ __noinline__ uint32_t fetch_any(const AttnArgs &a, const MmaSh
     codes += (int64_t)slot * sh.codes[i].stride + kv0 * sh.row[i];
     zeros += (int64_t)slot * sh.zeros[i].stride + kv0 * sh.ng[i];
     const char *scales = reinterpret_cast<const char *>(c.scales) + (int64_t)slot * sh.scales[i].stride + kv0 * sh.ng[i] * 4;
-    fetch(sh.codes[i], codes, code_end, to + sh.codes[i].at + token * sh.codes[i].pitch, piece, step);
-    fetch(sh.scales[i], scales, nullptr, to + sh.scales[i].at + token * sh.scales[i].pitch, piece, step);
-    fetch(sh.zeros[i], zeros, zero_end, to + sh.zeros[i].at + token * sh.zeros[i].pitch, piece, step);
+    fetch(sh.codes[i], count(sh.codes[i]), codes, code_end, to + sh.codes[i].at + token * sh.codes[i].pitch, piece, step);
+    fetch(sh.scales[i], count(sh.scales[i]), scales, nullptr, to + sh.scales[i].at + token * sh.scales[i].pitch, piece, step);
+    fetch(sh.zeros[i], count(sh.zeros[i]), zeros, zero_end, to + sh.zeros[i].at + token * sh.zeros[i].pitch, piece, step);
     if (!sh.zeros[i].wide) off |= (uint32_t)(reinterpret_cast<uintptr_t>(zeros) & 3) << (8 * i);
     if (!sh.codes[i].wide) off |= (uint32_t)(reinterpret_cast<uintptr_t>(codes) & 3) << (16 + 8 * i);
   }
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
       const qwha_cache &c = i & 1 ? a.v : a.k;
       const char *from = i < 2 ? reinterpret_cast<const char *>(c.scales) : reinterpret_cast<const char *>(c.zeros);
       for (int p = 0; p < x.per; ++p)
-        small_s[n++] = {from + p * x.wide, (uint32_t)x.stride, (uint32_t)(x.at + p * x.wide), (uint32_t)(i < 2 ? sh.ng[i] * 4 : sh.ng[i - 2]), (uint32_t)x.pitch, (uint32_t)x.wide};
+        small_s[n++] = {from + p * x.wide, (uint32_t)x.stride, (uint32_t)(x.at + p * x.wide), (uint32_t)x.head, (uint32_t)x.pitch, (uint32_t)x.wide};
     }
   }
   __syncthreads();
@@ -413,7 +420,9 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
       if (page != -2 && !on) atomicOr(a.err, kErrPage);
       const uint32_t slot = (uint32_t)page * (uint32_t)a.k.page_size + (uint32_t)in, to = smem_u + fill_at;
       uint32_t off = 0;
-      if (on && sh.fast) {
+      if (on && sh.fast && kv0 + fetch_step <= a.k.heads) {
+        // a block that has all its heads (one that has fewer goes by fetch_any, which costs it 6 to 9%: a count of pieces
+        // here took 2 to 3% from all calls);
         // pieces p, p + fetch_step, ... of a token's codes; a row has whole pieces
         auto codes = [&](const char *src, uint32_t dst, int n) {
           const int step = 16 * fetch_step;
