@@ -152,7 +152,7 @@ typedef enum {
   QWHA_OP_QGEMV = 12,        /* qwha_qgemv; with_base: 1 for bf16 tokens, 2 for fp32 */
   QWHA_OP_ATTENTION = 13,    /* qwha_cache_attention; d_out = q_heads, d_in = head_dim, p = heads of the cache,
                                 T = n, with_base: 1 for bf16, 2 for fp32 */
-  QWHA_OP_PAGES = 14         /* qwha_pages_resize, qwha_pages_fork; d_out = n_seqs, p = n_pages, T = pairs of a
+  QWHA_OP_PAGES = 14         /* qwha_pages_resize, _resize_copies, qwha_pages_fork; d_out = n_seqs, p = n_pages, T = pairs of a
                                 fork (0 for resize), d_in = 1 */
 } qwha_op;
 
@@ -361,24 +361,42 @@ qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_
  *   pages int32 [n_seqs, max_pages]  row b: the first ceil(held[b] / page_size)
  *                                    entries are its pages, -1 behind them
  *   held  int64 [n_seqs]             tokens of sequence b
- * An empty table has refs = 0, pages = -1, held = 0. */
+ * An empty table has refs = 0, pages = -1, held = 0.
+ *
+ * A page that several rows name may be read through all of them and is to be
+ * written through none. qwha_pages_fork shares pages that are full, but a row
+ * that is cut back afterwards, its own or the one it was copied from, may end
+ * inside a shared page: the tokens it grows by would be written there, over the
+ * other's. guard != 0: qwha_pages_resize does not let such a row grow (it stays as
+ * it was and is reported), and qwha_pages_resize_copies gives it a page of its
+ * own. guard == 0: nobody looks, and such tokens must not be written. */
 typedef struct {
   int32_t page_size, max_pages, n_seqs;
   int32_t n_pages;
   int32_t *refs, *pages;
   int64_t *held;
+  int32_t guard;
 } qwha_page_table;
 
 /* Give every sequence b room for want[b] tokens (device int64 [n_seqs]; -1: as
  * it is): pages past the end are given back first (a page nobody names any more
  * is free), then sequences that grow take the lowest free pages, in the order of
  * b. held[b] becomes want[b]; where the free pages end, the sequence that cannot
- * be served and all that grow behind it stay as they were (held tells). want
+ * be served and all behind it that need pages stay as they were (held tells). want
  * below -1 or above max_pages * page_size, and rows whose held or pages
  * contradict the table, are left and reported by qwha_check_stream_status
  * (QWHA_ERR_INVALID_ARG). ws: qwha_workspace_size(QWHA_OP_PAGES, n_seqs, 1,
  * n_pages, 0, 0) bytes. Deterministic. */
 qwha_status qwha_pages_resize(const qwha_page_table *t, const int64_t *want, void *ws, size_t ws_bytes, void *stream);
+
+/* The same (whatever t->guard is), and a sequence that grows from an end inside a
+ * page that other rows name too, behind the pages given back, takes one page more,
+ * the first of its pages, in that page's place: from[b] and to[b] (device int32
+ * [n_seqs]) name the two for qwha_cache_copy_pages, -1 where there is none. The
+ * copies are due before the new tokens are written and before the table's next
+ * call, since a page that all its rows leave so is free. */
+qwha_status qwha_pages_resize_copies(const qwha_page_table *t, const int64_t *want, int32_t *from, int32_t *to, void *ws,
+                                     size_t ws_bytes, void *stream);
 
 /* Row dst[i] becomes a copy of row src[i] as it was at the call's start, i < m
  * (device int64 [m]; src[i] = -1: nothing): whole pages are shared, a last page

@@ -7,7 +7,9 @@ import numpy as np
 import pytest
 
 import _cache_ops as R
-from test_cache_ops_gpu import Setup, random_trees
+from _util import to_dev
+from test_cache_ops_gpu import Setup, _W, _ints, random_trees
+from workloads import rng_for
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +30,163 @@ def test_attention_blocks_of_heads_that_are_not_full(heads, D, bits, group, dtyp
                   page_size=1, tree=random_trees if new > 1 else None)
         assert s.kv[0].n_slots == sum(s.past) + 4 * new  # no page is left over
         s.check()
+
+
+# ---------------------------------------------------------------- pages that two sequences name
+
+
+class GuardedTable(R.Table):
+    """The page table whose sequences do not grow inside a page with other users: they claim one (copies) or stay."""
+
+    def resize(self, want, copies=False):
+        n, ps = len(want), self.ps
+        origin, fresh, bad = np.full(n, -1, np.int32), np.full(n, -1, np.int32), False
+        grow = []
+        for b, w in enumerate(want):
+            if w == -1:
+                continue
+            if w < -1 or w > self.pages.shape[1] * ps:
+                bad = True
+            elif w <= self.held[b]:
+                for j in range(self.count(w), self.count(self.held[b])):
+                    self.refs[self.pages[b, j]] -= 1
+                    self.pages[b, j] = -1
+                self.held[b] = w
+            else:
+                grow.append(b)
+        free, at, refs = self.free(), 0, self.refs.copy()
+        for b in grow:
+            have, to = self.count(self.held[b]), self.count(want[b])
+            claim = int(self.held[b] % ps > 0 and refs[self.pages[b, have - 1]] > 1)
+            if claim and not copies:
+                bad = True
+                continue
+            at += to - have + claim
+            if at > len(free) and to - have + claim:
+                continue
+            got = free[at - (to - have + claim):at]
+            if claim:
+                origin[b], fresh[b] = self.pages[b, have - 1], got[0]
+                self.refs[origin[b]] -= 1
+                self.pages[b, have - 1] = got[0]
+            self.pages[b, have:to] = got[claim:]
+            self.refs[got] = 1
+            self.held[b] = want[b]
+        return origin, fresh, bad
+
+
+def _same(t, d):
+    assert np.array_equal(_ints(d.refs), t.refs) and np.array_equal(_ints(d.pages), t.pages) and np.array_equal(_ints(d.held), t.held)
+
+
+@pytest.mark.parametrize("copies", [False, True])
+@pytest.mark.parametrize("n_seqs,n_pages,max_pages,page_size", [(3, 10, 4, 16), (40, 200, 12, 5), (600, 3000, 9, 16), (600, 1100, 9, 16),
+                                                                (2100, 9000, 7, 16), (33, 4097, 64, 3), (20, 70000, 400, 3)])
+def test_a_guarded_page_table(n_seqs, n_pages, max_pages, page_size, copies):
+    """Random growth, cuts and forks: no sequence grows inside a page that another one names, pages running out among them."""
+    import torch
+
+    W, g = _W(), rng_for(350, str(n_seqs), str(n_pages))
+    t = GuardedTable(np.zeros(n_pages, np.int32), np.full((n_seqs, max_pages), -1, np.int32), np.zeros(n_seqs, np.int64), page_size)
+    d = W.PageTable(page_size, to_dev(t.refs), to_dev(t.pages), to_dev(t.held), guard=not copies)
+    room, share, claims, refused = max_pages * page_size, max(1, n_pages * page_size // n_seqs), 0, 0
+    for step in range(10):
+        want = g.integers(0, min(room, 2 * share) + 1, n_seqs)
+        want[g.random(n_seqs) < 0.3] = -1
+        want[g.random(n_seqs) < 0.1] = 0
+        out = (torch.full((n_seqs,), 7, dtype=torch.int32, device="cuda"), torch.full((n_seqs,), 7, dtype=torch.int32, device="cuda"))
+        W.pages_resize(d, to_dev(want), copies=out if copies else None)
+        origin, fresh, bad = t.resize(want, copies)
+        _same(t, d)
+        if copies:
+            assert np.array_equal(_ints(out[0]), origin) and np.array_equal(_ints(out[1]), fresh) and not bad
+            claims += int((origin >= 0).sum())
+            assert not set(origin[origin >= 0]) & set(fresh[fresh >= 0])  # as cache_copy_pages wants them
+        refused += bad
+        if bad:
+            with pytest.raises(W.QwhaError, match="shared page"):
+                W.check_stream_status()
+        dst = g.permutation(np.flatnonzero(t.held == 0))[:max(1, n_seqs // 3)]
+        src = g.integers(-1, n_seqs, len(dst))
+        if len(dst):
+            t.fork(src, dst)
+            W.pages_fork(d, to_dev(src), to_dev(dst))
+            _same(t, d)
+    W.check_stream_status()
+    assert n_seqs < 10 or (claims if copies else refused)
+
+
+def test_a_sequence_cut_back_to_a_shared_prefix_writes_to_its_own_page():
+    """A's 32 tokens in two pages, B a fork of it that is cut back to 20 tokens and goes on: A keeps its tokens, B has A's first
+    20; and A cut back itself, with B reading."""
+    import torch
+
+    W, g = _W(), rng_for(351)
+    ps, heads, D = 16, 2, 64
+    for which in (0, 1):  # who is cut back and grows
+        t = W.page_table(12, ps, 2, 4)
+        caches = tuple(W.cache_alloc(12, ps, heads, D, bits=4, group=64, had_block=0) for _ in range(2))
+
+        def write(b, lo, hi):
+            rows = [torch.randn(hi - lo, heads, D, generator=torch.Generator(device="cuda").manual_seed(int(g.integers(1 << 30))),
+                                device="cuda") for _ in range(2)]
+            table = _ints(t.pages)
+            slots = np.array([table[b, i // ps] * ps + i % ps for i in range(lo, hi)], np.int64)
+            W.cache_write(caches, tuple(rows), to_dev(slots))
+
+        def read(b, n):
+            return [x.clone() for x in W.cache_read(caches, t.pages[b:b + 1].contiguous(), to_dev(np.array([0, n], np.int64)), n,
+                                                    dtype=torch.float32)]
+
+        W.pages_resize(t, to_dev(np.array([32, 0])))
+        write(0, 0, 32)
+        copies = W.pages_fork(t, to_dev(np.array([0])), to_dev(np.array([1])))
+        W.cache_copy_pages(caches, *copies)
+        assert int(t.refs.max()) == 2
+        both = [read(b, 32) for b in (0, 1)]
+        cut, other = which, 1 - which
+        want = np.array([-1, -1])
+        want[cut] = 20
+        W.pages_resize(t, to_dev(want))
+        assert t.held.tolist()[cut] == 20
+        want[cut] = 21
+        W.pages_resize(t, to_dev(want))  # without copies: it stays, and is reported
+        assert t.held.tolist()[cut] == 20 and int(t.refs.sum()) == 4
+        with pytest.raises(W.QwhaError, match="shared page"):
+            W.check_stream_status()
+        out = (torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda"))
+        W.pages_resize(t, to_dev(want), copies=out)
+        assert t.held.tolist()[cut] == 21 and int(t.refs.max()) == 2 and int(t.refs.sum()) == 4
+        assert out[0].tolist()[cut] == int(t.pages[other, 1]) and out[1].tolist()[cut] == int(t.pages[cut, 1])
+        W.cache_copy_pages(caches, *out)
+        write(cut, 20, 21)
+        for x, y in zip(read(other, 32), both[other]):
+            assert torch.equal(x, y)
+        for x, y in zip(read(cut, 21), both[cut]):
+            assert torch.equal(x[:20], y[:20]) and not torch.equal(x[20], y[20])
+        W.pages_resize(t, to_dev(want + 3 * (want >= 0)))  # its own page now: nothing more to ask
+        assert t.held.tolist()[cut] == 24
+        W.check_stream_status()
+
+
+def test_a_guarded_page_table_in_a_graph():
+    import torch
+
+    W = _W()
+    d = W.page_table(64, 16, 4, 8)
+    W.pages_resize(d, torch.tensor([32, 0, 0, 16], device="cuda"))
+    W.pages_fork(d, torch.tensor([0, 0], device="cuda"), torch.tensor([1, 2], device="cuda"))
+    cut, want = torch.tensor([20, 20, 32, 16], device="cuda"), torch.tensor([40, 21, 33, 17], device="cuda")
+    out = tuple(torch.empty(4, dtype=torch.int32, device="cuda") for _ in range(2))
+    ws = torch.empty(W.workspace_size(W.api.OP_PAGES, 4, 1, 64, 0, 0), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        W.pages_resize(d, cut, ws=ws)
+        W.pages_resize(d, want, ws=ws, copies=out)
+    g.replay()
+    first = [x.tolist() for x in (d.pages, d.held, *out)]
+    assert first[1] == [40, 21, 33, 17] and first[2][:2] == [1, 1] and first[2][2:] == [-1, -1] and first[0][2][1] == 1
+    g.replay()  # the pages are their own now
+    assert out[0].tolist() == [-1] * 4 and d.held.tolist() == first[1]
+    assert int((d.refs > 0).sum()) == d.pages[d.pages >= 0].unique().numel()
+    W.check_stream_status()

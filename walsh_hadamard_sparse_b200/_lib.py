@@ -48,7 +48,7 @@ class QwhaCache(ctypes.Structure):
 
 class QwhaPageTable(ctypes.Structure):
     _fields_ = [("page_size", i32), ("max_pages", i32), ("n_seqs", i32), ("n_pages", i32), ("refs", P), ("pages", P),
-                ("held", P)]
+                ("held", P), ("guard", i32)]
 
 
 _SIGNATURES = {
@@ -73,6 +73,7 @@ _SIGNATURES = {
     "qwha_cache_attention": (ctypes.c_int, [ctypes.POINTER(QwhaCache), ctypes.POINTER(QwhaCache), ctypes.c_int, P, i64, i32,
                                             i64, P, i32, P, P, i32, P, f32, P, P, P, sz, P]),
     "qwha_pages_resize": (ctypes.c_int, [ctypes.POINTER(QwhaPageTable), P, P, sz, P]),
+    "qwha_pages_resize_copies": (ctypes.c_int, [ctypes.POINTER(QwhaPageTable), P, P, P, P, sz, P]),
     "qwha_pages_fork": (ctypes.c_int, [ctypes.POINTER(QwhaPageTable), P, P, i32, P, P, P, sz, P]),
     "qwha_cache_copy_pages": (ctypes.c_int, [ctypes.POINTER(QwhaCache), i32, P, P, i32, P]),
     "qwha_cache_compact": (ctypes.c_int, [ctypes.POINTER(QwhaCache), i32, P, i32, P, P, i32, i32, P]),

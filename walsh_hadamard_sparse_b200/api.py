@@ -468,12 +468,15 @@ def cache_attention(kv, q: torch.Tensor, pages: torch.Tensor, q_start: torch.Ten
 class PageTable:
     """Which pages hold which sequence's tokens, on the device: refs int32 [n_pages] (rows that name the page; 0: free),
     pages int32 [n_seqs, max_pages] (the first ceil(held / page_size) entries of a row; -1 behind), held int64 [n_seqs].
-    One table serves all caches of a model."""
+    One table serves all caches of a model. With guard, a sequence that was cut back into a page that another one names too
+    does not grow there, where its tokens would go over the other's: pages_resize leaves and reports it, or with `copies`
+    gives it a page of its own. Without, nobody looks."""
 
     page_size: int
     refs: torch.Tensor
     pages: torch.Tensor
     held: torch.Tensor
+    guard: bool = False
 
     def c_struct(self, dev: int | None = None) -> QwhaPageTable:
         dev = torch.cuda.current_device() if dev is None else dev
@@ -481,26 +484,34 @@ class PageTable:
         n_pages = self.refs.shape[0]
         return QwhaPageTable(self.page_size, max_pages, n_seqs, n_pages, _fit("refs", self.refs, torch.int32, (n_pages,), dev),
                              _fit("pages", self.pages, torch.int32, (n_seqs, max_pages), dev),
-                             _fit("held", self.held, torch.int64, (n_seqs,), dev))
+                             _fit("held", self.held, torch.int64, (n_seqs,), dev), self.guard)
 
 
 def page_table(n_pages: int, page_size: int, n_seqs: int, max_pages: int, device="cuda") -> PageTable:
-    """A table of empty sequences over free pages."""
+    """A table of empty sequences over free pages, with guard."""
     return PageTable(page_size, torch.zeros(n_pages, dtype=torch.int32, device=device),
                      torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=device),
-                     torch.zeros(n_seqs, dtype=torch.int64, device=device))
+                     torch.zeros(n_seqs, dtype=torch.int64, device=device), True)
 
 
-def pages_resize(t: PageTable, want: torch.Tensor, ws: torch.Tensor | None = None) -> torch.Tensor:
+def pages_resize(t: PageTable, want: torch.Tensor, ws: torch.Tensor | None = None,
+                 copies: tuple[torch.Tensor, torch.Tensor] | None = None) -> torch.Tensor:
     """Give each sequence room for want[b] tokens (int64 [n_seqs]; -1: as it is, 0: free it): pages past the end are given
     back, then growing sequences take the lowest free pages in their order. Returns t.held, which is want[b] where the
-    sequence was served; when the free pages end, the sequence and the growing ones behind it stay as they were."""
+    sequence was served; when the free pages end, the sequence and those behind it that need pages stay as they were.
+    copies (from, to), int32 [n_seqs] each: a sequence that grows from an end inside a page that others name too gets a
+    page of its own there, and these receive the pages to copy with cache_copy_pages in every cache, before the new tokens
+    are written and before the table's next call (-1: none)."""
     h, dev = lib(), torch.cuda.current_device()
     c = t.c_struct(dev)
     w = _fit("want", want, torch.int64, (c.n_seqs,), dev)
     if ws is None:
         ws = _new_ws(want, h.qwha_workspace_size(OP_PAGES, c.n_seqs, 1, c.n_pages, 0, 0))
-    check(h.qwha_pages_resize(c, w, *_fit_ws(ws, dev), _raw_stream(dev)), "qwha_pages_resize")
+    if copies is None:
+        check(h.qwha_pages_resize(c, w, *_fit_ws(ws, dev), _raw_stream(dev)), "qwha_pages_resize")
+    else:
+        origin, fresh = (_fit("copies", x, torch.int32, (c.n_seqs,), dev) for x in copies)
+        check(h.qwha_pages_resize_copies(c, w, origin, fresh, *_fit_ws(ws, dev), _raw_stream(dev)), "qwha_pages_resize_copies")
     return t.held
 
 

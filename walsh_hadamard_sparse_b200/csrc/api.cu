@@ -693,7 +693,7 @@ qwha_status qwha_check_stream_status(void *stream) {
                 word & kErrSlot && word & (kErrPage | kErrTable) ? ", " : "",
                 word & kErrPage ? "a page outside the cache or its page table" : "",
                 word & kErrPage && word & kErrTable ? ", " : "",
-                word & kErrTable ? "a row that contradicts the page table, or kept tokens that do not ascend" : "");
+                word & kErrTable ? "a row that contradicts the page table or would write to a shared page, or kept tokens that do not ascend" : "");
   if (word) return fail(QWHA_ERR_TIMEOUT, "device wait gave up (code 0x%x)", word);
   return QWHA_OK;
 }
@@ -1097,6 +1097,15 @@ qwha_status check_moved(const qwha_cache *caches, int32_t n_caches) {
   return QWHA_OK;
 }
 
+qwha_status resize(const qwha_page_table &t, const int64_t *want, int32_t *from, int32_t *to, void *ws, size_t ws_bytes,
+                   void *stream) {
+  QWHA_CHECK_INDEX(want, "want");
+  const qwha_status st = check_ws(ws, ws_bytes, pages_workspace(t.n_seqs, t.n_pages, 0));
+  if (st != QWHA_OK) return st;
+  StageScope sc(ST_PAGES, 1, (cudaStream_t)stream);
+  return cuda_status(launch_pages_resize(t, want, from, to, ws, (cudaStream_t)stream), "pages_resize");
+}
+
 CachePair moved_pair(const qwha_cache *caches, int32_t n_caches) {
   CachePair c = {};
   for (int i = 0; i < n_caches; ++i) c.cache[i] = caches[i];
@@ -1210,10 +1219,17 @@ qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_
 qwha_status qwha_pages_resize(const qwha_page_table *t, const int64_t *want, void *ws, size_t ws_bytes, void *stream) {
   qwha_status st = check_table(t);
   if (st != QWHA_OK || t->n_seqs == 0) return st;
-  QWHA_CHECK_INDEX(want, "want");
-  if ((st = check_ws(ws, ws_bytes, pages_workspace(t->n_seqs, t->n_pages, 0))) != QWHA_OK) return st;
-  StageScope sc(ST_PAGES, 1, (cudaStream_t)stream);
-  return cuda_status(launch_pages_resize(*t, want, ws, (cudaStream_t)stream), "pages_resize");
+  return resize(*t, want, nullptr, nullptr, ws, ws_bytes, stream);
+}
+
+qwha_status qwha_pages_resize_copies(const qwha_page_table *t, const int64_t *want, int32_t *from, int32_t *to, void *ws,
+                                     size_t ws_bytes, void *stream) {
+  qwha_status st = check_table(t);
+  if (st != QWHA_OK || t->n_seqs == 0) return st;
+  QWHA_CHECK_INDEX(from, "from");
+  QWHA_CHECK_INDEX(to, "to");
+  if ((st = check_apart("from and to", from, (size_t)t->n_seqs * 4, to, (size_t)t->n_seqs * 4)) != QWHA_OK) return st;
+  return resize(*t, want, from, to, ws, ws_bytes, stream);
 }
 
 qwha_status qwha_pages_fork(const qwha_page_table *t, const int64_t *src, const int64_t *dst, int32_t m, int32_t *from,

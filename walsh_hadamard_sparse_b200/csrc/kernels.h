@@ -246,7 +246,9 @@ cudaError_t launch_rotary(qwha_dtype dt, const RotaryArgs &r, cudaStream_t s);
 // Page table and moves of cached rows (pages.cu).
 constexpr unsigned int kErrTable = 0x4000u;  // rows of a table or of a move that were refused
 size_t pages_workspace(int64_t n_seqs, int64_t n_pages, int64_t m);
-cudaError_t launch_pages_resize(const qwha_page_table &t, const int64_t *want, void *ws, cudaStream_t s);
+// from, to: NULL, or where the pages to copy are named (the table is guarded then).
+cudaError_t launch_pages_resize(const qwha_page_table &t, const int64_t *want, int32_t *from, int32_t *to, void *ws,
+                                cudaStream_t s);
 cudaError_t launch_pages_fork(const qwha_page_table &t, const int64_t *src, const int64_t *dst, int32_t m,
                               int32_t *from, int32_t *to, void *ws, cudaStream_t s);
 cudaError_t launch_copy_pages(const CachePair &c, int n_caches, const int32_t *from, const int32_t *to, int32_t m,

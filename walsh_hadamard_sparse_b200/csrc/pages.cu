@@ -129,9 +129,13 @@ __device__ __forceinline__ long long sum_of(const long long *v, int n) {
   return s;
 }
 
+// GUARD: a row that grows from an end inside a page with other users claims a page
+// in its place (origin, fresh: where the two are named), or, without these, is left.
+// Which rows do is known only behind the pages given back: a barrier more.
+template <bool GUARD>
 __global__ void __launch_bounds__(kTableThreads, 1)
-    resize_kernel(const qwha_page_table t, const int64_t *__restrict__ want, Shared *sh, int64_t *from, int32_t *list,
-                  unsigned int *err) {
+    resize_kernel(const qwha_page_table t, const int64_t *__restrict__ want, int32_t *origin, int32_t *fresh, Shared *sh,
+                  int64_t *from, int32_t *list, unsigned int *err) {
   __shared__ long long warp_s[kTableWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
@@ -140,27 +144,49 @@ __global__ void __launch_bounds__(kTableThreads, 1)
   const int64_t room = (int64_t)ps * t.max_pages;
   int s0, s1;
   share(t.n_seqs, rank, ctas, &s0, &s1);
-  // pages each sequence asks for, and how many are asked for before it in the CTA
+  // pages each sequence asks for, and how many are asked for before it in the CTA: from[b], twice that and whether the first
+  // of them is claimed
   long long asked = 0;
-  for (int b0 = s0; b0 < s1; b0 += kTableThreads) {
-    const int b = b0 + threadIdx.x;
-    long long need = 0;
-    if (b < s1) {
-      const int64_t w = want[b], h = t.held[b];
-      if (w == -1) {
-      } else if (w < -1 || w > room || h < 0 || h > room) {
-        atomicOr(err, kErrTable);
-      } else {
-        need = pages_of(w, ps) - pages_of(h, ps);
-        if (need < 0) need = 0;
+  auto ask = [&] {
+    for (int b0 = s0; b0 < s1; b0 += kTableThreads) {
+      const int b = b0 + threadIdx.x;
+      long long need = 0;
+      int claim = 0;
+      if (b < s1) {
+        const int64_t w = want[b], h = t.held[b];
+        if (w == -1) {
+        } else if (w < -1 || w > room || h < 0 || h > room) {
+          atomicOr(err, kErrTable);
+        } else {
+          need = pages_of(w, ps) - pages_of(h, ps);
+          if (need < 0) need = 0;
+          if constexpr (GUARD) {
+            if (w > h) {
+              const int64_t end = pages_of(h, ps) - 1;
+              if (end >= 0 && (end + 1) * ps != h) {
+                const int32_t p = t.pages[(int64_t)b * t.max_pages + end];
+                const bool in = p >= 0 && p < t.n_pages;
+                claim = !in || __ldcg(t.refs + p) > 1;
+                if (claim && !(in && origin)) {  // it cannot be given a page of its own
+                  atomicOr(err, kErrTable);
+                  claim = -1, need = 0;
+                }
+              }
+              if (claim == 0 && need == 0) t.held[b] = w;
+            }
+          }
+          need += claim > 0;
+        }
+        if (GUARD && origin) origin[b] = fresh[b] = -1;
       }
+      long long sum;
+      const long long before = block_before(need, warp_s, &sum);
+      if (b < s1) from[b] = need > 0 ? 2 * (asked + before) + (claim > 0) : kNone;
+      asked += sum;
     }
-    long long sum;
-    const long long before = block_before(need, warp_s, &sum);
-    if (b < s1) from[b] = need > 0 ? asked + before : kNone;
-    asked += sum;
-  }
-  if (threadIdx.x == 0) sh->wanted[rank] = asked;
+    if (threadIdx.x == 0) sh->wanted[rank] = asked;
+  };
+  if (!GUARD) ask();
   // The ends that are given back: eight lanes a sequence, neighbours to different CTAs, since long ends come together and
   // an SM makes about one atomic operation in two clocks. (What this changes of held is of sequences that do not grow,
   // whose held nobody needs from here on.)
@@ -183,9 +209,13 @@ __global__ void __launch_bounds__(kTableThreads, 1)
       }
     }
     __syncwarp(0xffu << (threadIdx.x & 24));  // the eight lanes have read held
-    if (eighth == 0 && to <= have) t.held[b] = w;
+    if (eighth == 0 && (GUARD ? w <= h : to <= have)) t.held[b] = w;
   }
   cluster.sync();
+  if (GUARD) {
+    ask();
+    cluster.sync();
+  }
   const long long total = sum_of(sh->wanted, ctas);
   if (total == 0) return;  // every CTA sees the same
   int lo, hi;
@@ -199,9 +229,10 @@ __global__ void __launch_bounds__(kTableThreads, 1)
   __syncthreads();
   for (int b = s0 + threadIdx.x; b < s1; b += kTableThreads) {
     if (from[b] == kNone) continue;
-    const long long need = pages_of(want[b], ps) - pages_of(t.held[b], ps), at = asked_before + from[b];
+    const int claim = (int)(from[b] & 1);
+    const long long need = pages_of(want[b], ps) - pages_of(t.held[b], ps) + claim, at = asked_before + (from[b] >> 1);
     if (at + need <= n_free) atomicMax(&granted_s, (unsigned long long)(at + need));
-    from[b] = at + need <= n_free ? at : kNone;
+    from[b] = at + need <= n_free ? 2 * at + claim : kNone;
   }
   __syncthreads();
   if (threadIdx.x == 0) sh->granted[rank] = (long long)granted_s;
@@ -212,11 +243,17 @@ __global__ void __launch_bounds__(kTableThreads, 1)
   if (free_before < granted) warp_free(t.refs, lo, hi, list, free_before, granted, t.refs);
   cluster.sync();
   for (int b = s0 + group; b < s1; b += kGroups) {
-    const int64_t at = from[b];
-    if (at == kNone) continue;
+    if (from[b] == kNone) continue;
+    const int64_t at = from[b] >> 1, claim = from[b] & 1;
     const int64_t w = want[b], have = pages_of(t.held[b], ps), to = pages_of(w, ps);
     int32_t *row = t.pages + (int64_t)b * t.max_pages;
-    for (int64_t j = have + eighth; j < to; j += 8) row[j] = __ldcg(list + at + (j - have));
+    for (int64_t j = have + eighth; j < to; j += 8) row[j] = __ldcg(list + at + claim + (j - have));
+    if (GUARD && claim && eighth == 0) {
+      const int32_t old = row[have - 1], own = __ldcg(list + at);
+      row[have - 1] = own;
+      atomicSub(t.refs + old, 1);
+      origin[b] = old, fresh[b] = own;
+    }
     __syncwarp(0xffu << (threadIdx.x & 24));  // the eight lanes have read held
     if (eighth == 0) t.held[b] = w;
   }
@@ -487,11 +524,13 @@ __global__ void __launch_bounds__(kMoveThreads)
 
 size_t pages_workspace(int64_t n_seqs, int64_t n_pages, int64_t m) { return carve(nullptr, n_seqs, n_pages, m).bytes; }
 
-cudaError_t launch_pages_resize(const qwha_page_table &t, const int64_t *want, void *ws, cudaStream_t s) {
+cudaError_t launch_pages_resize(const qwha_page_table &t, const int64_t *want, int32_t *from, int32_t *to, void *ws,
+                                cudaStream_t s) {
   unsigned int *err = device_error_word();
   if (!err) return cudaErrorInvalidDevicePointer;
   const TableWs w = carve(ws, t.n_seqs, t.n_pages, 0);
-  return launch_table(resize_kernel, t.n_pages, t.n_seqs, s, t, want, w.sh, w.from, w.list, err);
+  return launch_table(t.guard || from ? resize_kernel<true> : resize_kernel<false>, t.n_pages, t.n_seqs, s, t, want, from, to,
+                      w.sh, w.from, w.list, err);
 }
 
 cudaError_t launch_pages_fork(const qwha_page_table &t, const int64_t *src, const int64_t *dst, int32_t m,
