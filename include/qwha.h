@@ -383,10 +383,12 @@ typedef struct {
  * is free), then sequences that grow take the lowest free pages, in the order of
  * b. held[b] becomes want[b]; where the free pages end, the sequence that cannot
  * be served and all behind it that need pages stay as they were (held tells). want
- * below -1 or above max_pages * page_size, and rows whose held or pages
- * contradict the table, are left and reported by qwha_check_stream_status
- * (QWHA_ERR_INVALID_ARG). ws: qwha_workspace_size(QWHA_OP_PAGES, n_seqs, 1,
- * n_pages, 0, 0) bytes. Deterministic. */
+ * below -1 or above max_pages * page_size, and rows whose held or whose entries
+ * to give back are outside the table, are left and reported by
+ * qwha_check_stream_status (QWHA_ERR_INVALID_ARG); so is an entry given back
+ * whose page counts fewer users than there are (its count stays 0). ws:
+ * qwha_workspace_size(QWHA_OP_PAGES, n_seqs, 1, n_pages, 0, 0) bytes.
+ * Deterministic. */
 qwha_status qwha_pages_resize(const qwha_page_table *t, const int64_t *want, void *ws, size_t ws_bytes, void *stream);
 
 /* The same (whatever t->guard is), and a sequence that grows from an end inside a
@@ -403,10 +405,11 @@ qwha_status qwha_pages_resize_copies(const qwha_page_table *t, const int64_t *wa
  * that is only partly filled gets a fresh page (lowest free first, in the order
  * of i), since both sequences will write to it: from[i] and to[i] (device int32
  * [m]) name it and its copy for qwha_cache_copy_pages, -1 where there is none.
- * dst[i] must be an empty row (held 0) and named once; a pair that breaks this
- * or leaves the table is skipped and reported as above (of pairs with one dst
- * the first counts). Where the free pages end, the pair that cannot be served and
- * all behind it leave their dst empty. ws as above with T = m. Deterministic. */
+ * dst[i] must be an empty row (held 0) and named once; a pair that breaks this,
+ * leaves the table, or whose src has pages outside the cache or without users by
+ * refs, is skipped and reported as above (of pairs with one dst the first
+ * counts). Where the free pages end, the pair that cannot be served and all
+ * behind it leave their dst empty. ws as above with T = m. Deterministic. */
 qwha_status qwha_pages_fork(const qwha_page_table *t, const int64_t *src, const int64_t *dst, int32_t m, int32_t *from,
                             int32_t *to, void *ws, size_t ws_bytes, void *stream);
 

@@ -190,3 +190,39 @@ def test_a_guarded_page_table_in_a_graph():
     assert out[0].tolist() == [-1] * 4 and d.held.tolist() == first[1]
     assert int((d.refs > 0).sum()) == d.pages[d.pages >= 0].unique().numel()
     W.check_stream_status()
+
+
+def test_rows_that_contradict_the_table_are_left():
+    """Entries outside the cache, counts of no users: the rows and pairs that hold them change nothing, the others are served."""
+    import torch
+
+    W = _W()
+    pages = np.full((8, 4), -1, np.int32)
+    pages[0], pages[1, :2], pages[2, :2], pages[3, :3] = [0, 1, 2, 3], [4, 77], [-5, 5], [6, 7, 8]
+    refs = np.zeros(20, np.int32)
+    refs[[0, 1, 2, 3, 4, 5, 6, 8]] = 1  # page 7 is named by row 3 and counts no users
+    held = np.array([16, 8, 7, 10, 0, 0, 0, 0], np.int64)
+
+    def table(guard):
+        return W.PageTable(4, to_dev(refs), to_dev(pages), to_dev(held), guard)
+
+    for guard in (False, True):
+        d = table(guard)
+        W.pages_resize(d, to_dev(np.array([5, 0, 0, -1, 6, -1, -1, -1])))
+        with pytest.raises(W.QwhaError, match="page table"):
+            W.check_stream_status()
+        assert d.held.tolist() == [5, 8, 7, 10, 6, 0, 0, 0]
+        assert d.pages.tolist() == [[0, 1, -1, -1], *pages[1:4].tolist(), [2, 3, -1, -1], *pages[5:].tolist()]
+        assert d.refs[:9].tolist() == [1, 1, 1, 1, 1, 1, 1, 0, 1] and int(d.refs.sum()) == 8
+        # the page without users: given back, its count stays 0
+        W.pages_resize(d, to_dev(np.array([-1, -1, -1, 4, -1, -1, -1, -1])))
+        with pytest.raises(W.QwhaError, match="page table"):
+            W.check_stream_status()
+        assert d.held.tolist()[3] == 4 and d.refs[6:9].tolist() == [1, 0, 0]
+    d = table(False)
+    a, b = W.pages_fork(d, to_dev(np.array([1, 2, 3, 0])), to_dev(np.array([4, 5, 6, 7])))
+    with pytest.raises(W.QwhaError, match="page table"):
+        W.check_stream_status()
+    assert a.tolist() == b.tolist() == [-1] * 4
+    assert d.held.tolist() == [16, 8, 7, 10, 0, 0, 0, 16] and torch.equal(d.pages[:7], to_dev(pages)[:7])
+    assert d.pages[7].tolist() == [0, 1, 2, 3] and d.refs[:9].tolist() == [2, 2, 2, 2, 1, 1, 1, 0, 1] and int(d.refs[9:].max()) == 0

@@ -197,13 +197,18 @@ __global__ void __launch_bounds__(kTableThreads, 1)
     if (w < 0 || w > room || h < 0 || h > room) continue;
     const int64_t have = pages_of(h, ps), to = pages_of(w, ps);
     int32_t *row = t.pages + (int64_t)b * t.max_pages;
+    bool bad = false;
+#pragma unroll 4
+    for (int64_t j = to + eighth; j < have; j += 8) bad |= (uint32_t)row[j] >= (uint32_t)t.n_pages;
+    if (__any_sync(0xffu << (threadIdx.x & 24), bad)) {  // left as it is
+      if (bad) atomicOr(err, kErrTable);
+      continue;
+    }
 #pragma unroll 4
     for (int64_t j = to + eighth; j < have; j += 8) {
       const int32_t p = row[j];
       row[j] = -1;
-      if (p < 0 || p >= t.n_pages) {
-        atomicOr(err, kErrTable);
-      } else if (atomicSub(t.refs + p, 1) <= 0) {
+      if (atomicSub(t.refs + p, 1) <= 0) {  // fewer users counted than there are
         atomicAdd(t.refs + p, 1);
         atomicOr(err, kErrTable);
       }
@@ -274,6 +279,19 @@ __global__ void __launch_bounds__(kTableThreads, 1)
   auto in_table = [&](int64_t b) { return b >= 0 && b < t.n_seqs; };
   for (int i = m0 + threadIdx.x; i < m1; i += kTableThreads)
     if (in_table(src[i]) && in_table(dst[i])) owner[dst[i]] = INT32_MAX;
+  // rows whose pages are none, or count no users, are not copied: tokens[i] -1
+  for (int i = m0 + warp; i < m1; i += kTableWarps) {
+    bool bad = false;
+    if (in_table(src[i]) && in_table(dst[i])) {
+      const int64_t h = t.held[src[i]];
+      const int32_t *row = t.pages + src[i] * t.max_pages;
+      if (h > 0 && h <= room)
+#pragma unroll 4
+        for (int64_t j = lane; j < pages_of(h, ps); j += 32) bad |= (uint32_t)row[j] >= (uint32_t)t.n_pages || t.refs[row[j]] <= 0;
+    }
+    bad = __any_sync(~0u, bad);
+    if (lane == 0) tokens[i] = bad ? -1 : 0;
+  }
   cluster.sync();
   for (int i = m0 + threadIdx.x; i < m1; i += kTableThreads)
     if (in_table(src[i]) && in_table(dst[i])) atomicMin(owner + dst[i], i);
@@ -285,7 +303,7 @@ __global__ void __launch_bounds__(kTableThreads, 1)
     if (i < m1) {
       const int64_t a = src[i], b = dst[i];
       int64_t h = -1;
-      if (in_table(a) && in_table(b) && __ldcg(owner + b) == i && t.held[b] == 0) h = t.held[a];
+      if (in_table(a) && in_table(b) && __ldcg(owner + b) == i && t.held[b] == 0 && tokens[i] == 0) h = t.held[a];
       if (h > room) h = -1;
       if (h < 0 && a != -1) atomicOr(err, kErrTable);
       tokens[i] = h;
@@ -316,7 +334,7 @@ __global__ void __launch_bounds__(kTableThreads, 1)
       for (int64_t j = lane; j < full; j += 32) {
         const int32_t p = row[j];
         copy[j] = p;
-        if (p < 0 || p >= t.n_pages || atomicAdd(t.refs + p, 1) <= 0) atomicOr(err, kErrTable);
+        atomicAdd(t.refs + p, 1);
       }
       if (needs) {
         o = row[full], f = __ldcg(list + at);
