@@ -7,7 +7,8 @@ import numpy as np
 import pytest
 
 import _cache_ops as R
-from _util import to_dev
+from _serving import pack, unpack
+from _util import host, to_dev
 from test_cache_ops_gpu import Setup, _W, _ints, random_trees
 from workloads import rng_for
 
@@ -226,3 +227,69 @@ def test_rows_that_contradict_the_table_are_left():
     assert a.tolist() == b.tolist() == [-1] * 4
     assert d.held.tolist() == [16, 8, 7, 10, 0, 0, 0, 16] and torch.equal(d.pages[:7], to_dev(pages)[:7])
     assert d.pages[7].tolist() == [0, 1, 2, 3] and d.refs[:9].tolist() == [2, 2, 2, 2, 1, 1, 1, 0, 1] and int(d.refs[9:].max()) == 0
+
+
+# ---------------------------------------------------------------- groups without values
+
+
+def put_idle(s, g, share=0.15):
+    """Groups of a Setup's pools whose codes become their zero points, in every pool: [pools] of masks like the scales."""
+    masks = []
+    for (codes, sc, z), bits, group in zip((s.pk, s.pv), s.fmt[:2], (s.fmt[2], s.group_v)):
+        m = g.random(sc.shape) < share
+        q = unpack(codes, bits)
+        codes[...] = pack(np.where(np.repeat(m, group, -1), np.repeat(z, group, -1), q).astype(np.uint8), bits)
+        masks.append(m)
+    return masks
+
+
+def to_caches(s):
+    for pool, cache in zip((s.pk, s.pv), s.kv):
+        for t, d in zip(pool, (cache.codes, cache.scales, cache.zeros)):
+            d.copy_(to_dev(t))
+
+
+@pytest.mark.parametrize("dtype,grp,new", [("bf16", 2, 4), ("f32", 3, 5), ("bf16", 3, 8), ("bf16", 4, 40), ("f32", 2, 30), ("bf16", 1, 2)])
+@pytest.mark.parametrize("D,bits,group", [(128, 4, 128), (64, 2, 32), (128, 3, 64), (96, 8, 32), (40, 4, 8), (256, 3, 128), (24, 3, 8),
+                                          (80, 2, 16)])
+def test_attention_groups_without_values_have_no_say(D, bits, group, dtype, grp, new):
+    """A group whose codes all equal its zero point is zeros, whatever its scale: tiny, the 1 that cache_write stores for a row
+    of zeros, or far above all others, the results of trees and chunks have the same bits; one that is a NaN stays one."""
+    for tree in (None, random_trees):
+        s = Setup(f"idle{D}{bits}{group}{dtype}{grp}{new}", [70, 300], [new, new], heads=3, grp=grp, D=D, bits=bits, group=group, dtype=dtype,
+                  tree=tree, had_v=8)
+        masks = put_idle(s, s.g)
+        s.pv[1][...] *= np.float32(2.0**-12)
+        results = []
+        for scale in (2.0**-40, 1.0, -(2.0**60)):
+            for m, pool in zip(masks, (s.pk, s.pv)):
+                pool[1][m] = scale
+            to_caches(s)
+            results.append((host(s.run()), host(s.lse)))
+        for out, lse in results[1:]:
+            assert np.array_equal(out, results[0][0]) and np.array_equal(lse, results[0][1])
+        for m, pool in zip(masks, (s.pk, s.pv)):
+            pool[1][m] = 2.0**-40
+        s.check(to_dev(results[2][0]))  # the bounds of tiny scales hold for the others
+        # a token of the past of sequence 1, which all its rows see (but those that see nothing of a tree see the past too)
+        slot = int(s.table[1, 200 // 16]) * 16 + 200 % 16
+        for pool in (s.pk, s.pv):
+            keep = pool[1].copy()
+            pool[1].reshape(-1, *pool[1].shape[2:])[slot, 1] = np.nan
+            to_caches(s)
+            got = host(s.run())
+            assert np.isnan(got[new:, grp:2 * grp]).any(-1).all() and not np.isnan(got[:new]).any() and not np.isnan(got[:, 2 * grp:]).any()
+            pool[1][...] = keep
+        _W().check_stream_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,bits,group", [(128, 4, 128), (128, 8, 64), (40, 4, 8)])
+def test_attention_of_one_token_with_groups_without_values(D, bits, group, dtype):
+    """The same with the scale 1 that cache_write stores and one token to a sequence: within the bounds."""
+    s = Setup(f"idleone{D}{bits}{group}{dtype}", [70, 300], [1, 1], heads=3, grp=2, D=D, bits=bits, group=group, dtype=dtype)
+    for m, pool in zip(put_idle(s, s.g), (s.pk, s.pv)):
+        pool[1][...] *= np.float32(2.0**-9)
+        pool[1][m] = 1.0
+    to_caches(s)
+    s.check()

@@ -343,9 +343,28 @@ __device__ __forceinline__ void repair(const AttnArgs &a, int b, int block, int 
     if (a.lse && lane == 0) a.lse[row * a.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
+// The scale of a group of a row, without its sign; 0 where it is no number or the group is idle. (Its first byte of codes
+// is loaded beside it: nearly always that one tells.)
+__device__ __forceinline__ float live_scale(const qwha_cache &c, int64_t row, int g, int groups) {
+  const int bytes = c.group / 8 * c.bits;
+  const uint8_t *at = c.codes + row * (c.head_dim / 8 * c.bits) + g * bytes;
+  const float x = fabsf(__ldg(c.scales + row * groups + g));
+  const uint32_t z = __ldg(c.zeros + row * groups + g), first = __ldg(at), mask = (1u << c.bits) - 1u;
+  if (!(x < INFINITY)) return 0.f;
+  if ((first & mask) != z) return x;
+  bool idle;
+  switch (c.bits) {
+    case 2: idle = idle_bytes<2>(at, bytes, z, 0, 1); break;
+    case 3: idle = idle_bytes<3>(at, bytes, z, 0, 1); break;
+    case 4: idle = idle_bytes<4>(at, bytes, z, 0, 1); break;
+    default: idle = idle_bytes<8>(at, bytes, z, 0, 1);
+  }
+  return idle ? 0.f : x;
+}
 // Whether a tile is one of those. A row has at least the largest scale of the tokens that
-// all rows see, of which up to 32 are looked at, or, where there are none, maybe the
-// least of the others alone. The keys' groups count together: a score is their sum.
+// all rows see, of which the newest 32 are looked at (all, where these have none), or, where
+// there are none, maybe the least of the others alone. The keys' groups count together: a
+// score is their sum. Idle groups do not count.
 struct Scales {
   uint32_t top, all, some;  // the largest of tokens that not all rows see; of those that all see; the least of the first
 };
@@ -353,49 +372,55 @@ template <bool TC>
 __device__ __forceinline__ bool needs_repair(const AttnArgs &a, const Seq &s, int b, int block, int tile, Scales (*of)[33]) {
   const int ng = a.v.head_dim / a.v.group, ng_k = a.k.head_dim / a.k.group, head_block = block_of(a, block), length = s.length(a, tile);
   const int safe = a.tree ? s.past : s.past + tile * a.tq + 1;  // every row sees the tokens below
-  if (s.rows == 1 || length <= safe) return false;
+  if (s.rows - tile * a.tq == 1 || a.tq == 1 || length <= safe) return false;  // (one token: its rows see the same)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
   const int per_head = (threads >> 5) / a.hb, hl = warp % a.hb, sub = warp / a.hb, kv = head_block * a.hb + hl;
   __syncthreads();
   for (int i = threadIdx.x; i < a.hb * 33; i += threads) of[i / 33][i % 33] = {0u, 0u, 0x7f800000u};
   __syncthreads();
-  if (sub < per_head && kv < a.k.heads) {
+  auto look = [&](int lo, int hi) {  // the scales of tokens [lo, hi)
+    if (sub >= per_head || kv >= a.k.heads) return;
     const int32_t *table = a.pages + (int64_t)b * a.max_pages;
     auto row_of = [&](int t) -> int64_t {  // of the token's scales; -1: none
       const int pg = page_of(a, t), page = __ldg(table + pg);
       return (uint32_t)page < (uint32_t)a.v.n_pages ? (((int64_t)page * a.v.page_size + t - pg * a.v.page_size) * a.v.heads + kv) : -1;
     };
-    auto put = [&](int g, float top, float all, float some) {
-      const uint32_t top_u = __reduce_max_sync(~0u, __float_as_uint(top)), all_u = __reduce_max_sync(~0u, __float_as_uint(all));
-      const uint32_t some_u = __reduce_min_sync(~0u, __float_as_uint(some));
-      if (lane == 0) atomicMax(&of[hl][g].top, top_u), atomicMax(&of[hl][g].all, all_u), atomicMin(&of[hl][g].some, some_u);
-    };
-    auto finite = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.f; };
-    const int step = 32 * per_head, first = 32 * sub + lane, near = max(safe - 32, 0) + first;
-    for (int g = 0; g < (TC ? ng + 1 : ng); ++g) {  // the last: the keys
-      const bool keys = g == ng;
-      float top = 0.f, all = 0.f, some = INFINITY;
-      for (int t = near; t < length; t += step) {
-        const int64_t row = row_of(t);
-        float x = 0.f;
-        if (row >= 0 && !keys) x = finite(__ldg(a.v.scales + row * ng + g));
-        if (row >= 0 && keys)
-          for (int i = 0; i < ng_k; ++i) x = fmaxf(x, finite(__ldg(a.k.scales + row * ng_k + i)));
-        if (t < safe) all = fmaxf(all, x);
-        else top = fmaxf(top, x), some = x > 0.f ? fminf(some, x) : some;
+    const int step = 32 * per_head;
+    for (int t0 = lo + 32 * sub; t0 < hi; t0 += step) {
+      const int t = t0 + lane;
+      const int64_t row = t < hi ? row_of(t) : -1;
+      auto put = [&](Scales &x, float scale) {
+        const uint32_t bits = __float_as_uint(scale), top = __reduce_max_sync(~0u, t < safe ? 0u : bits);
+        const uint32_t all = __reduce_max_sync(~0u, t < safe ? bits : 0u);
+        const uint32_t some = __reduce_min_sync(~0u, t < safe || !bits ? 0x7f800000u : bits);
+        if (lane == 0) atomicMax(&x.top, top), atomicMax(&x.all, all), atomicMin(&x.some, some);
+      };
+      float keys = 0.f, first = 0.f;  // (asked for together)
+      if (row >= 0) {
+        first = live_scale(a.v, row, 0, ng);
+        if (TC)
+          for (int i = 0; i < ng_k; ++i) keys = fmaxf(keys, live_scale(a.k, row, i, ng_k));
       }
-      put(keys ? 32 : g, top, all, some);
+      put(of[hl][0], first);
+      if (TC) put(of[hl][32], keys);
+      for (int g = 1; g < ng; ++g) put(of[hl][g], row >= 0 ? live_scale(a.v, row, g, ng) : 0.f);
     }
-  }
+  };
+  auto any_of = [&](auto is) {
+    bool any = false;
+    for (int i = threadIdx.x; i < a.hb * 33; i += threads) any |= is(of[i / 33][i % 33]);
+    return __syncthreads_or(any);
+  };
+  const int near = max(safe - 32, 0);
+  look(near, length);
   __syncthreads();
-  bool far = false;
-  for (int i = threadIdx.x; i < a.hb * 33; i += threads) {
-    const int h = i / 33, g = i - h * 33;
-    if (g >= ng && !(TC && g == 32)) continue;
-    const Scales x = of[h][g];
-    far |= __uint_as_float(x.top) > (TC ? kRoomTc : kRoomMma) * __uint_as_float(x.all ? x.all : x.some);
+  if (near > 0 && any_of([](const Scales &x) { return x.top && !x.all; })) {
+    look(0, near);
+    __syncthreads();
   }
-  return __syncthreads_or(far);
+  return any_of([](const Scales &x) {
+    return __uint_as_float(x.top) > (TC ? kRoomTc : kRoomMma) * __uint_as_float(x.all ? x.all : x.some);
+  });
 }
 // CTA (x, y): tiles y, y + gridDim.y, ... of sequences x, x + gridDim.x, ...
 template <bool TC>

@@ -261,6 +261,30 @@ __device__ __forceinline__ uint32_t byte_pair(uint32_t a, uint32_t b, int i, uin
   return d;
 }
 
+// A group whose codes all equal its zero point is zeros whatever its scale (a row of zeros is stored with scale 1): idle.
+// Byte i (word k) of codes that all are z; z above every code is no code.
+template <int BITS>
+__device__ __forceinline__ uint32_t idle_byte(uint32_t z, int i) {
+  if constexpr (BITS == 8) return z;
+  if constexpr (BITS == 4) return z * 0x11u;
+  if constexpr (BITS == 2) return z * 0x55u;
+  return z * 0x249249u >> (8 * (i % 3)) & 0xffu;
+}
+template <int BITS>
+__device__ __forceinline__ uint32_t idle_word(uint32_t z, int k) {
+  if constexpr (BITS == 8) return z * 0x01010101u;
+  if constexpr (BITS == 4) return z * 0x11111111u;
+  if constexpr (BITS == 2) return z * 0x55555555u;
+  return k == 0 ? z * 0x49249249u : k == 1 ? z >> 2 | z * 0x92492492u : z >> 1 | z * 0x24924924u;
+}
+// Of `bytes` codes from `at` on, every `step`-th byte from i on.
+template <int BITS, typename P>
+__device__ __forceinline__ bool idle_bytes(const P *at, int bytes, uint32_t z, int i, int step) {
+  bool same = z < 1u << BITS;
+#pragma unroll 1
+  for (; same && i < bytes; i += step) same = (uint8_t)at[i] == idle_byte<BITS>(z, i);
+  return same;
+}
 // Eight codes of a row in shared memory: two words of which 8 bits use both.
 template <int BITS>
 __device__ __forceinline__ uint2 load_run(const char *row, int chunk, int mis) {
@@ -335,7 +359,11 @@ __device__ __forceinline__ void rotate_lanes(float *v, int had, float unit, int 
   for (int i = 0; i < 8; ++i) v[i] *= unit;
 }
 
-template <int DP, int NT, int PIECES, int GROUPS>
+// IDLE: idle groups have no say in the factor of the scales. Where a row may see less than
+// another of its tile, such a scale (a row of zeros is stored with 1) would take bits
+// from all of them, or have them done again in fp32; with one token to a sequence it
+// is one of those that the row sees, and looking costs 2 to 8%.
+template <int DP, int NT, int PIECES, int GROUPS, bool IDLE>
 __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
     attention_mma_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ MmaShape sh, int per_head, uint32_t one) {
   extern __shared__ __align__(128) char smem[];
@@ -736,6 +764,22 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
             if (masked) s0 = any0 ? s0 : 0.f, s1 = any1 ? s1 : 0.f;
             float c = c_s[warp][gr];
             if (__any_sync(~0u, fabsf(s0) * c > kTop || fabsf(s1) * c > kTop)) {
+              if constexpr (IDLE) {  // four lanes look at a group's codes
+                auto idle = [&](int tk) {
+                  const int back = g - 2 * t + tk;  // v_row, v_zero: of token 2 t
+                  const char *row = st_v + v_row + back * sh.codes[1].pitch + gr * (group_v / 8 * B);
+                  const uint8_t *zero = reinterpret_cast<const uint8_t *>(st_vz) + v_zero + back * sh.zeros[1].pitch + gr;
+                  const uint8_t *o = off + 4 * (g + tk);
+                  if (!sh.codes[1].wide) row += o[3];
+                  if (!sh.zeros[1].wide) zero += o[1];
+                  bool same = idle_bytes<B>(row, group_v / 8 * B, *zero, t, 4);
+                  same &= __shfl_xor_sync(~0u, same, 1);
+                  return same & __shfl_xor_sync(~0u, same, 2);
+                };
+                const bool idle0 = idle(0), idle1 = idle(8);
+                if (idle0 && fabsf(s0) < INFINITY) s0 = 0.f;
+                if (idle1 && fabsf(s1) < INFINITY) s1 = 0.f;
+              }
               // a scale above all before it: twice its power of two. Infinities stay what they are
               const float x0 = fabsf(s0), x1 = fabsf(s1);
               const uint32_t top = __reduce_max_sync(~0u, max(x0 < INFINITY ? __float_as_uint(x0) : 0u, x1 < INFINITY ? __float_as_uint(x1) : 0u));
@@ -980,26 +1024,32 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
   }
 }
 
-template <int DP, int NT, int PIECES, int GROUPS>
+template <int DP, int NT, int PIECES, int GROUPS, bool IDLE>
 cudaError_t launch_mma(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s) {
   static std::atomic<size_t> allowed[64];
-  auto kernel = attention_mma_kernel<DP, NT, PIECES, GROUPS>;
+  auto kernel = attention_mma_kernel<DP, NT, PIECES, GROUPS, IDLE>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), l.smem, allowed);
   if (e != cudaSuccess) return e;
   const MmaShape sh(a.k.head_dim, DP, a.k.bits, a.v.bits, a.k.group, a.v.group, NT, PIECES, a.k.heads, a.hb, l.per_head, l.warps);
   kernel<<<l.ctas, l.warps * 32, l.smem, s>>>(a, sh, l.per_head, 0x64006400u);
   return cudaGetLastError();
 }
-template <int DP, int NT, int PIECES>
+template <int DP, int NT, int PIECES, bool IDLE>
 cudaError_t launch_mma_groups(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s) {
   const bool alike = a.k.group == a.v.group;
-  if (alike && a.k.group == a.k.head_dim) return launch_mma<DP, NT, PIECES, kSingle>(a, l, s);
-  if (alike && a.k.group % 64 == 0) return launch_mma<DP, NT, PIECES, kBlocked>(a, l, s);
-  return launch_mma<DP, NT, PIECES, kMixed>(a, l, s);
+  if (alike && a.k.group == a.k.head_dim) return launch_mma<DP, NT, PIECES, kSingle, IDLE>(a, l, s);
+  if (alike && a.k.group % 64 == 0) return launch_mma<DP, NT, PIECES, kBlocked, IDLE>(a, l, s);
+  return launch_mma<DP, NT, PIECES, kMixed, IDLE>(a, l, s);
+}
+template <int DP, int NT, int PIECES>
+cudaError_t launch_mma_pieces(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s) {
+  // one token to a sequence is the rule only with few rows: no other copies of the kernel
+  if (NT == 1 && a.tq == 1) return launch_mma_groups<DP, NT, PIECES, NT != 1>(a, l, s);
+  return launch_mma_groups<DP, NT, PIECES, true>(a, l, s);
 }
 template <int DP, int NT>
 cudaError_t launch_mma_nt(const AttnArgs &a, const MmaLaunch &l, cudaStream_t s) {
-  return a.f32 ? launch_mma_groups<DP, NT, 2>(a, l, s) : launch_mma_groups<DP, NT, 1>(a, l, s);
+  return a.f32 ? launch_mma_pieces<DP, NT, 2>(a, l, s) : launch_mma_pieces<DP, NT, 1>(a, l, s);
 }
 
 }  // namespace attn

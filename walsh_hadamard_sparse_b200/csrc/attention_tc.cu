@@ -259,10 +259,6 @@ struct Segment {
 // What one unpacking thread fetches of a tile: per round (two) and slab (DP / 64)
 // 32 codes of a token, its scales and zero point.
 template <int BITS>
-struct Raw {
-  uint32_t w[BITS];
-};
-template <int BITS>
 __device__ __forceinline__ void fetch_codes(const uint8_t *p, uint32_t *w) {
   if constexpr (BITS == 2) {
     const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
@@ -328,7 +324,8 @@ struct Unpacker {
 #pragma unroll
     for (int i = 0; i < kSlabs; ++i) {
       const int d = 64 * i + 32 * (threadIdx.x & 1), g = ng > 1 && d < c.head_dim ? d / c.group : 0;
-      scale[r][i] = g == 0 ? all[0] : g == 1 ? all[1] : g == 2 ? all[2] : all[3], zero[r][i] = __ldg(z + g);
+      const float own = g == 0 ? all[0] : g == 1 ? all[1] : g == 2 ? all[2] : all[3];
+      scale[r][i] = d < c.head_dim ? own : 0.f, zero[r][i] = __ldg(z + g);
     }
   }
 
@@ -355,6 +352,14 @@ struct Unpacker {
   }
 
   __device__ __forceinline__ void wait(int bar, uint32_t parity) { ok = ok && wait_for(bars + 8 * bar, parity); }
+
+  // Whether the lane's 32 codes all equal their zero point.
+  __device__ __forceinline__ bool idle(int r, int i) const {
+    bool same = zero[r][i] < 1u << B;
+#pragma unroll
+    for (int k = 0; k < B; ++k) same &= w[r][i][k] == idle_word<B>(zero[r][i], k);
+    return same;
+  }
 
   __device__ __forceinline__ void run(const Segment &g, const Place &at) {
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % (kUnpackWarps / 2), half = lane & 1, D = c.head_dim, ng = D / c.group;
@@ -426,6 +431,18 @@ struct Unpacker {
         uint32_t *top_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount + 16) + (values ? 4 : 0);
         if (threadIdx.x % kUnpackers < 4) top_s[threadIdx.x % kUnpackers] = 0;
         meet();
+        // codes that all equal their zero point have no say, whatever their scale
+#pragma unroll
+        for (int i = 0; i < kSlabs; ++i) {
+          top[i] = 0.f;
+#pragma unroll
+          for (int r = 0; r < kRounds; ++r) {
+            const float x = fabsf(scale[r][i]);
+            if (!(x < INFINITY)) continue;
+            if (x * factor[i] > kTcTop && idle(r, i)) scale[r][i] = 0.f;
+            else top[i] = fmaxf(top[i], x);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < kSlabs; ++i) atomicMax(top_s + (values ? 2 * i + half : 0), __float_as_uint(top[i]));
         meet();
