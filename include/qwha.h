@@ -346,8 +346,9 @@ qwha_status qwha_rotary(qwha_dtype dt, int32_t n_x, const void *const *x, const 
  * largest scale that the row sees in the group by 2^-33 of that), and in bf16 calls of many rows to a cached head the cached
  * values too, by 2^-11; else these are exact.
  * Rows whose tokens' scales are far below those of tokens that only other rows
- * see are done in fp32, more slowly; groups whose codes all equal their zero point
- * (rows of zeros) do not count for that. out must not overlap q. Deterministic.
+ * see (2^8 times, in bf16 calls of many rows 2^16) are done again in fp32, 20 to
+ * 90 times as slowly; groups whose codes all equal their zero point (rows of
+ * zeros) do not count for that. out must not overlap q. Deterministic.
  * ws: qwha_workspace_size(QWHA_OP_ATTENTION, q_heads, head_dim, heads, n, 1 for
  * bf16 or 2 for fp32) bytes. */
 qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_dtype dt, const void *q, int64_t n,

@@ -7,9 +7,9 @@ import numpy as np
 import pytest
 
 import _cache_ops as R
-from _serving import pack, unpack
+from _serving import half_step, pack, unpack
 from _util import host, to_dev
-from test_cache_ops_gpu import Setup, _W, _ints, random_trees
+from test_cache_ops_gpu import Setup, _W, _ints, poison, random_trees
 from workloads import rng_for
 
 pytestmark = pytest.mark.gpu
@@ -293,3 +293,31 @@ def test_attention_of_one_token_with_groups_without_values(D, bits, group, dtype
         pool[1][m] = 1.0
     to_caches(s)
     s.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("past,new,heads,grp,D,bits,group,page_size", [
+    ([700], [64], 2, 4, 128, 4, 128, 16), ([33, 0, 500], [64, 5, 33], 9, 2, 64, 8, 32, 3), ([300, 64], [7, 3], 3, 40, 128, 3, 64, 16),
+    ([100, 31], [9, 40], 2, 3, 256, 4, 128, 16), ([90] * 20, [6] * 20, 5, 1, 40, 4, 8, 16), ([0, 50], [130, 60], 1, 5, 96, 2, 96, 100)])
+def test_attention_of_tiles_done_again(past, new, heads, grp, D, bits, group, page_size, dtype):
+    """Tokens of far larger scales in the middle and at the end of the new ones: rows that do not see them, in every part of a
+    group and block of heads, one sequence to all CTAs and many; what they hold may be no number; the same bits again."""
+    for tree in (None, random_trees)[:1 + (max(new) <= 64)]:
+        s = Setup(f"again{past[0]}{D}{dtype}", past, new, heads=heads, grp=grp, D=D, bits=bits, group=group, page_size=page_size, dtype=dtype,
+                  tree=tree, had_v=8, size=0.5)
+        for b, m in enumerate(new):
+            for u in {m // 2, m - 1}:
+                poison(s, (b, past[b] + u), 2.0**22, (0, 1))
+        got = s.check()
+        for _ in range(2):
+            assert np.array_equal(host(s.run()), got)
+        if tree is None:  # the last token of the first sequence is seen by the last row alone
+            slot = int(s.table[0, (past[0] + new[0] - 1) // page_size]) * page_size + (past[0] + new[0] - 1) % page_size
+            for c in s.kv:
+                c.scales.view(s.kv[0].n_slots, heads, -1)[slot] = float("nan")
+            out = host(s.run())
+            assert np.isnan(out[new[0] - 1]).any(-1).all()
+            # (not the same bits: where the tile is not done again its other rows' weights are rounded to the largest scale met)
+            want, _, tol, _ = s.ref()
+            others = np.arange(len(out)) != new[0] - 1
+            assert np.all((np.abs(out - want) <= tol + half_step(dtype) * np.abs(want))[others])

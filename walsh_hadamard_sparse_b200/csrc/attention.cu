@@ -284,64 +284,133 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const _
 // 325 to 375 us for 304 where four chunks of 1021 tokens are answered behind 2048.)
 constexpr float kRoomMma = 256.f, kRoomTc = 65536.f;
 
-// The rows of a tile again, in fp32, a warp a row and a token at a time. Slow, and
-// right whatever the scales are.
-__device__ __forceinline__ void repair(const AttnArgs &a, int b, int block, int tile) {
-  const Seq s(a, b);
-  const int head_block = block_of(a, block), part = block - head_block * a.parts, each = a.tq * a.gh, length = s.length(a, tile);
-  const int lane = threadIdx.x & 31, D = a.k.head_dim, c0 = 8 * lane;
-  const Rows rows = rows_of(a, s, 0, part, tile);
+// Rows of a tile again, in fp32, right whatever the scales are: of one cached head, up to
+// four rows a warp and 32 cached tokens at a time, which go to shared memory as values.
+// Where every tile is one of those (a later token in eight with values 2^20 times the
+// others'): 4 chunks of 1021 behind 2048 take 7.4 ms for 0.36, 16 trees of 64 behind 4096
+// 8.4 for 0.16, one behind 32768 8.3 for 0.1, 64 trees of 4 3.4 for 0.17; bound by the
+// latency of a step's loads, sums and barriers. (A warp a row and a token at a time: 88,
+// 208 and 101 ms.) 80 registers, so that a CTA starts beside the joining ones: with
+// 128 the ordinary call of 2 trees waited 2 us longer.
+constexpr int kRepairThreads = 256, kRepairWarps = kRepairThreads / 32, kRepairRows = 4, kRepairTokens = 32;
+__host__ __device__ __forceinline__ size_t repair_smem(int D) {
+  return (size_t)(kRepairTokens * (2 * D + 4) + kRepairWarps * kRepairRows * (D + kRepairTokens)) * 4;
+}
+// Rows first, first + 1, ... of the tile's rows of head hl of the block, `each` to a warp; C channels a lane.
+template <int C>
+__device__ __forceinline__ void repair(const AttnArgs &a, const Seq &s, int b, int block, int tile, int hl, int first, int each,
+                                       float *smem, int64_t *slot_s) {
+  const int head_block = block_of(a, block), part = block - head_block * a.parts, kv = head_block * a.hb + hl;
+  const int length = s.length(a, tile), D = a.k.head_dim, pitch = D + 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Rows rows = rows_of(a, s, kv, part, tile);
+  float *k_s = smem, *v_s = k_s + kRepairTokens * pitch;                       // [32][D + 4], [32][D]
+  float *q_s = v_s + kRepairTokens * D + warp * kRepairRows * (D + kRepairTokens);  // of the warp: [4][D], [4][32]
+  float *p_s = q_s + kRepairRows * D;
+  const int r0 = first + warp * each, mine = min(each, rows.n - r0);  // (below 1: none)
+  float m[kRepairRows], l[kRepairRows], acc[kRepairRows][C];
+  int token[kRepairRows];
+  unsigned long long bits[kRepairRows];
+#pragma unroll
+  for (int i = 0; i < kRepairRows; ++i) {
+    m[i] = -INFINITY, l[i] = 0.f, token[i] = 0, bits[i] = 0;
+#pragma unroll
+    for (int k = 0; k < C; ++k) acc[i][k] = 0.f;
+    if (i >= mine) continue;
+    warp_query(a, q_s + i * D, rows.q_row(r0 + i), rows.q_head(r0 + i));
+    token[i] = rows.j0 + rows.token(r0 + i);
+    if (a.tree) bits[i] = (unsigned long long)a.tree[s.row0 + token[i]];
+  }
 #pragma unroll 1
-  for (int rr = threadIdx.x >> 5; rr < a.part_rows; rr += blockDim.x >> 5) {
-    const int hl = rr / each, r = rr - hl * each, kv = head_block * a.hb + hl;
-    if (kv >= a.k.heads || r >= rows.n) continue;
-    const int j = rows.j0 + rows.token(r);
-    const int64_t row = rows.q_row(r), head = rows.q_head(r) + kv * a.grp;
-    const unsigned long long bits = a.tree ? (unsigned long long)a.tree[row] : 0;
-    float q[8], acc[8], m = -INFINITY, l = 0.f;
+  for (int t0 = 0; t0 < length; t0 += kRepairTokens) {
+    __syncthreads();  // the tokens before are used
+    if (threadIdx.x < kRepairTokens) slot_s[threadIdx.x] = t0 + (int)threadIdx.x < length ? slot_of(a, b, t0 + threadIdx.x) : -1;
+    __syncthreads();
+    for (int x = threadIdx.x; x < kRepairTokens * (D / 8); x += kRepairThreads) {
+      const int t = x / (D / 8), c = x - t * (D / 8);
+      float k[8], v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int64_t at = row * a.q_stride + head * D + c0 + k;
-      q[k] = c0 >= D ? 0.f : a.f32 ? static_cast<const float *>(a.q)[at] : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q)[at]);
-      acc[k] = 0.f;
+      for (int e = 0; e < 8; ++e) k[e] = v[e] = 0.f;
+      if (slot_s[t] >= 0) {
+        load_values(a.k, slot_s[t] * a.k.heads + kv, c, k);
+        load_values(a.v, slot_s[t] * a.k.heads + kv, c, v);
+      }
+      float4 *to_k = reinterpret_cast<float4 *>(k_s + t * pitch + c * 8), *to_v = reinterpret_cast<float4 *>(v_s + t * D + c * 8);
+      to_k[0] = make_float4(k[0], k[1], k[2], k[3]), to_k[1] = make_float4(k[4], k[5], k[6], k[7]);
+      to_v[0] = make_float4(v[0], v[1], v[2], v[3]), to_v[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
-    rotate_lanes<32>(q, a.k.had_block, a.unit_k, lane);
+    __syncthreads();
+    if (mine < 1) continue;
+    float x[kRepairRows] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+      const float4 k = *reinterpret_cast<const float4 *>(k_s + lane * pitch + d);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) q[k] *= a.scale2;
+      for (int i = 0; i < kRepairRows; ++i)
+        if (i < mine) {
+          const float4 q = *reinterpret_cast<const float4 *>(q_s + i * D + d);
+          x[i] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, x[i]))));
+        }
+    }
+    const bool there = slot_s[lane] >= 0;
+#pragma unroll
+    for (int i = 0; i < kRepairRows; ++i)
+      if (i < mine) {
+        // a score that is not a number stays one; a masked one counts nothing
+        const bool on = there && s.sees(a, token[i], bits[i], t0 + lane);
+        float top = on ? x[i] : -INFINITY;
+#pragma unroll
+        for (int o = 16; o; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        const float now = fmaxf(m[i], top), base = now == -INFINITY ? 0.f : now, turn = exp2f(m[i] - base);
+        const float p = on ? exp2f(x[i] - base) : 0.f;
+        float sum = p;
+#pragma unroll
+        for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
+        p_s[i * kRepairTokens + lane] = p;
+        m[i] = now, l[i] = l[i] * turn + sum;
+#pragma unroll
+        for (int k = 0; k < C; ++k) acc[i][k] *= turn;
+      }
+    __syncwarp();
 #pragma unroll 1
-    for (int t = 0; t < length; ++t) {
-      if (!s.sees(a, j, bits, t)) continue;
-      const int64_t slot = slot_of(a, b, t);
-      if (slot < 0) continue;
-      float v[8], x = 0.f;
+    for (int t = 0; t < kRepairTokens; t += 4) {
+      float v[4][C];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = 0.f;
-      if (c0 < D) load_values(a.k, slot * a.k.heads + kv, lane, v);
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x = fmaf(q[k], v[k], x);
+        for (int k = 0; k < C; ++k) v[u][k] = lane + 32 * k < D ? v_s[(t + u) * D + lane + 32 * k] : 0.f;
 #pragma unroll
-      for (int o = 16; o; o /= 2) x += __shfl_xor_sync(~0u, x, o);
-      const float now = fmaxf(m, x), base = now == -INFINITY ? 0.f : now, turn = exp2f(m - base), p = exp2f(x - base);
-      m = now, l = l * turn + p;
-      if (c0 < D) load_values(a.v, slot * a.k.heads + kv, lane, v);
+      for (int i = 0; i < kRepairRows; ++i) {
+        if (i >= mine) break;
+        const float4 p = *reinterpret_cast<const float4 *>(p_s + i * kRepairTokens + t);
+        auto add = [&](float w, int u) {
+          if (w != 0.f)  // a masked value may be a NaN
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = p != 0.f ? fmaf(p, v[k], acc[k] * turn) : acc[k] * turn;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] *= inv;
-    rotate_lanes<32>(acc, a.v.had_block, a.unit_v, lane);
-    if (c0 < D) {
-      const int64_t to = (row * a.q_heads + head) * D + c0;
-      if (a.f32) {
-        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(a.out) + to);
-        dst[0] = io<float>::pack(acc), dst[1] = io<float>::pack(acc + 4);
-      } else {
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + to) = io<__nv_bfloat16>::pack(acc);
+            for (int k = 0; k < C; ++k) acc[i][k] = fmaf(w, v[u][k], acc[i][k]);
+        };
+        add(p.x, 0), add(p.y, 1), add(p.z, 2), add(p.w, 3);
       }
     }
-    if (a.lse && lane == 0) a.lse[row * a.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    __syncwarp();
   }
+  for (int i = 0; i < kRepairRows; ++i)
+    if (i < mine) {
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        float y = acc[0][k];
+#pragma unroll
+        for (int j = 1; j < kRepairRows; ++j)
+          if (i == j) y = acc[j][k];
+        if (lane + 32 * k < D) q_s[i * D + lane + 32 * k] = y;
+      }
+      float mm = m[0], ll = l[0];
+#pragma unroll
+      for (int j = 1; j < kRepairRows; ++j)
+        if (i == j) mm = m[j], ll = l[j];
+      __syncwarp();
+      warp_finish(a, q_s + i * D, mm, ll, rows.q_row(r0 + i), rows.q_head(r0 + i));
+      __syncwarp();
+    }
 }
 // The scale of a group of a row, without its sign; 0 where it is no number or the group is idle. (Its first byte of codes
 // is loaded beside it: nearly always that one tells.)
@@ -361,7 +430,7 @@ __device__ __forceinline__ float live_scale(const qwha_cache &c, int64_t row, in
   }
   return idle ? 0.f : x;
 }
-// Whether a tile is one of those. A row has at least the largest scale of the tokens that
+// Which heads of a tile are (bits of the result). A row has at least the largest scale of the tokens that
 // all rows see, of which the newest 32 are looked at (all, where these have none), or, where
 // there are none, maybe the least of the others alone. The keys' groups count together: a
 // score is their sum. Idle groups do not count.
@@ -369,10 +438,10 @@ struct Scales {
   uint32_t top, all, some;  // the largest of tokens that not all rows see; of those that all see; the least of the first
 };
 template <bool TC>
-__device__ __forceinline__ bool needs_repair(const AttnArgs &a, const Seq &s, int b, int block, int tile, Scales (*of)[33]) {
+__device__ __forceinline__ unsigned needs_repair(const AttnArgs &a, const Seq &s, int b, int block, int tile, Scales (*of)[33]) {
   const int ng = a.v.head_dim / a.v.group, ng_k = a.k.head_dim / a.k.group, head_block = block_of(a, block), length = s.length(a, tile);
   const int safe = a.tree ? s.past : s.past + tile * a.tq + 1;  // every row sees the tokens below
-  if (s.rows - tile * a.tq == 1 || a.tq == 1 || length <= safe) return false;  // (one token: its rows see the same)
+  if (s.rows - tile * a.tq == 1 || a.tq == 1 || length <= safe) return 0;  // (one token: its rows see the same)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
   const int per_head = (threads >> 5) / a.hb, hl = warp % a.hb, sub = warp / a.hb, kv = head_block * a.hb + hl;
   __syncthreads();
@@ -418,21 +487,41 @@ __device__ __forceinline__ bool needs_repair(const AttnArgs &a, const Seq &s, in
     look(0, near);
     __syncthreads();
   }
-  return any_of([](const Scales &x) {
-    return __uint_as_float(x.top) > (TC ? kRoomTc : kRoomMma) * __uint_as_float(x.all ? x.all : x.some);
-  });
+  __shared__ unsigned far_s;
+  if (threadIdx.x == 0) far_s = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.hb * 33; i += threads) {
+    const Scales x = of[i / 33][i % 33];
+    if (__uint_as_float(x.top) > (TC ? kRoomTc : kRoomMma) * __uint_as_float(x.all ? x.all : x.some)) atomicOr(&far_s, 1u << (i / 33));
+  }
+  __syncthreads();
+  return far_s;
 }
-// CTA (x, y): tiles y, y + gridDim.y, ... of sequences x, x + gridDim.x, ...
-template <bool TC>
-__global__ void __launch_bounds__(256) attention_repair_kernel(const __grid_constant__ AttnArgs a) {
+// CTA (x, y): of sequences x, x + gridDim.x, ... the tiles y, y + gridDim.y, ..., or, where there are fewer tiles than
+// that, a share of a tile's rows.
+template <bool TC, int C>
+__global__ void __launch_bounds__(kRepairThreads, C <= 4 ? 3 : 2) attention_repair_kernel(const __grid_constant__ AttnArgs a) {
+  extern __shared__ __align__(16) float repair_s[];
   __shared__ Scales of[kMmaWarps][33];
+  __shared__ int64_t slot_s[kRepairTokens];
   for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
     const Seq s(a, b);
-    for (long long i = blockIdx.y; i < (long long)s.tiles * a.blocks; i += gridDim.y) {
+    const long long tiles = (long long)s.tiles * a.blocks;
+    const int share = tiles < gridDim.y && tiles ? (int)(gridDim.y / tiles) : 1, step = (int)(gridDim.y / share);
+    if ((int)blockIdx.y >= step * share) continue;
+    for (long long i = blockIdx.y / share; i < tiles; i += step) {
       const int block = (int)(i / s.tiles), tile = (int)(i - (long long)block * s.tiles);
-      if (!needs_repair<TC>(a, s, b, block, tile, of)) continue;
+      const unsigned heads = needs_repair<TC>(a, s, b, block, tile, of);
+      if (!heads) continue;
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      repair(a, b, block, tile);
+      // pieces of `each` rows a warp, in turn to the CTAs that share the tile
+      const int rows = min(a.tq, s.rows - tile * a.tq) * a.gh;  // (the last part of a group may have fewer)
+      const int each = min(max((rows * __popc(heads) + share * kRepairWarps - 1) / (share * kRepairWarps), 1), kRepairRows);
+      int turn = blockIdx.y % share;
+      for (int hl = 0; hl < a.hb; ++hl)
+        if (heads >> hl & 1)
+          for (int first = 0; first < rows; first += each * kRepairWarps, turn = turn ? turn - 1 : share - 1)
+            if (turn == 0) repair<C>(a, s, b, block, tile, hl, first, each, repair_s, slot_s);
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -586,9 +675,14 @@ cudaError_t launch_attention(AttnArgs a, void *ws, cudaStream_t s) {
   cfg.attrs = attr, cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, D <= 64 ? attention_join_kernel<8> : D <= 128 ? attention_join_kernel<16> : attention_join_kernel<32>, a);
   if (e != cudaSuccess || !repairs(a)) return e;
+  static std::atomic<size_t> repair_allowed[3][64];
+  auto kernel = tc ? attention_repair_kernel<true, 4> : D <= 128 ? attention_repair_kernel<false, 4> : attention_repair_kernel<false, 8>;
+  const size_t smem = repair_smem(D);
+  e = allow_smem(reinterpret_cast<const void *>(kernel), smem, repair_allowed[tc ? 0 : D <= 128 ? 1 : 2]);
+  if (e != cudaSuccess) return e;
   const int ctas = 2 * sm_count(), seqs = std::min(a.n_seqs, ctas);
-  cfg.gridDim = dim3(seqs, ctas / seqs), cfg.blockDim = dim3(256), cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, tc ? attention_repair_kernel<true> : attention_repair_kernel<false>, a);
+  cfg.gridDim = dim3(seqs, ctas / seqs), cfg.blockDim = dim3(kRepairThreads), cfg.dynamicSmemBytes = smem;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace qwha
