@@ -343,12 +343,15 @@ qwha_status qwha_rotary(qwha_dtype dt, int32_t n_x, const void *const *x, const 
  * output. Scores, softmax and sums are fp32. Before the products the rotated
  * query and the softmax weights are rounded, each value by 2^-11 of itself for
  * bf16 and 2^-21 for fp32 at most (a weight times a scale below 2^-24 of the
- * largest scale that the row sees in the group by 2^-33 of that), and in bf16 calls of many rows to a cached head the cached
- * values too, by 2^-11; else these are exact.
- * Rows whose tokens' scales are far below those of tokens that only other rows
- * see (2^8 times, in bf16 calls of many rows 2^16) are done again in fp32, 20 to
- * 90 times as slowly; groups whose codes all equal their zero point (rows of
- * zeros) do not count for that. out must not overlap q. Deterministic.
+ * largest scale that the row sees in the group by 2^-33 of that), and in bf16
+ * calls of many rows to a cached head the cached values too, by 2^-11 + 2^-16 of
+ * each; else these are exact.
+ * Some rows are done again in fp32, 20 to 90 times as slowly: those whose tokens'
+ * scales are far below those of tokens that only other rows see (2^8 times, in
+ * bf16 calls of many rows 2^16), and in the latter calls those that see scales
+ * 2^13 apart (of a head's keys, or of a group of its values). Groups whose codes
+ * all equal their zero point (rows of zeros) do not count for that.
+ * out must not overlap q. Deterministic.
  * ws: qwha_workspace_size(QWHA_OP_ATTENTION, q_heads, head_dim, heads, n, 1 for
  * bf16 or 2 for fp32) bytes. */
 qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_dtype dt, const void *q, int64_t n,

@@ -321,3 +321,45 @@ def test_attention_of_tiles_done_again(past, new, heads, grp, D, bits, group, pa
             want, _, tol, _ = s.ref()
             others = np.arange(len(out)) != new[0] - 1
             assert np.all((np.abs(out - want) <= tol + half_step(dtype) * np.abs(want))[others])
+
+
+def lift(s, b, t, which, factor, channel):
+    """Token t of sequence b: scales of pool `which` times factor, its codes zero points but for one channel."""
+    slot, bits, group = int(s.table[b, t // s.page_size]) * s.page_size + t % s.page_size, s.fmt[which], (s.fmt[2], s.group_v)[which]
+    codes, sc, z = (s.pk, s.pv)[which]
+    codes, sc, z = (x.reshape(-1, *x.shape[2:])[slot] for x in (codes, sc, z))
+    q, zz = unpack(codes, bits), np.repeat(z, group, -1)
+    idle = zz.copy()
+    idle[:, channel] = np.where(q[:, channel] == zz[:, channel], zz[:, channel] ^ 1, q[:, channel])
+    codes[...] = pack(idle.astype(np.uint8), bits)
+    sc *= np.float32(factor)
+    return slot
+
+
+@pytest.mark.parametrize("past,new,grp,heads", [([300, 40], [40, 64], 4, 2), ([2000], [130], 2, 2), ([700, 100], [1, 1], 60, 1)])
+@pytest.mark.parametrize("D,bits,group", [(128, 4, 128), (64, 8, 32), (96, 3, 32), (128, 2, 64)])
+@pytest.mark.parametrize("factor", [2.0**11, 2.0**16, 2.0**20, 2.0**24, 2.0**30])
+def test_attention_of_many_rows_keeps_tokens_beside_one_of_a_far_larger_scale(factor, D, bits, group, past, new, grp, heads):
+    """A token that all rows see, whose key or value is large in one channel alone: the query has nothing there, or the output is
+    looked at in the others. What is left of it there is nothing, and the other tokens keep all their bits."""
+    for which in (0, 1):
+        for at in (0, past[0] - 1):
+            s = Setup(f"beside{D}{bits}{factor}{past[0]}{which}", past, new, heads=heads, grp=grp, D=D, bits=bits, group=group)
+            assert s.cached
+            channel = D - 3
+            slot = lift(s, 0, at, which, factor, channel)
+            to_caches(s)
+            if which == 0:
+                s.qv[..., channel] = 0.0
+                s.q[..., channel] = 0.0
+            got = host(s.run())
+            kd, vd = (R.dense_pool(p, bits, group) for p in (s.pk, s.pv))
+            step = R.largest_steps(s.pv, bits, group)
+            step[slot] = np.abs(vd[slot]) if which else step[slot]
+            want, lse, tol, lse_tol = R.attention(s.qv, kd, vd, step, 0, 0, s.table, 16, s.past, s.new, None, s.scale, 2.0**-11, s.cached)
+            keep = np.arange(D) != channel
+            err = np.abs(got - want)[..., keep] - half_step("bf16") * np.abs(want)[..., keep]
+            assert np.all(err <= tol[..., keep])
+            if which == 0:
+                assert np.all(np.abs(host(s.lse) - lse) <= lse_tol)
+            _W().check_stream_status()

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kAnyThreads) attention_any_kernel(const AttnAr
       }
     }
     if (starts && !ends) begun = make_int4(at.b, at.block, at.tile, 1);
-    if (!starts && first) gone_on = make_int4(at.b, at.block, at.tile, ends ? 3 : 1);
+    if (!starts && first) gone_on = make_int4(at.b, at.block, at.tile, ends ? kPieceThere | kPieceEnds : kPieceThere);
     first = false;
     left -= run;
     at.unit = 0;
@@ -189,15 +189,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const _
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, lane = threadIdx.x & 31;
   const int4 begun = a.part_desc[2 * c + 1];
-  if (!(begun.w & 1)) return;
+  if (!(begun.w & kPieceThere)) return;
   const int part = begun.y - block_of(a, begun.y) * a.parts, kv0 = block_of(a, begun.y) * a.hb, each = a.tq * a.gh;
   if (threadIdx.x < 32) {
     int n = 1;
     if (lane == 0) slots_s[0] = 2 * c + 1;
     for (int p0 = c + 1; p0 < a.ctas; p0 += 32) {
       const int p = p0 + lane, flags = p < a.ctas ? a.part_desc[2 * p].w : 0;  // 0: a CTA without units
-      const unsigned ends = __ballot_sync(~0u, flags & 2), upto = ends ? (ends & -ends) * 2 - 1 : ~0u;
-      const unsigned on = __ballot_sync(~0u, flags & 1) & upto;
+      const unsigned ends = __ballot_sync(~0u, flags & kPieceEnds), upto = ends ? (ends & -ends) * 2 - 1 : ~0u;
+      const unsigned on = __ballot_sync(~0u, flags & kPieceThere) & upto;
       if (on >> lane & 1) slots_s[n + __popc(on & ((1u << lane) - 1))] = 2 * p;
       n += __popc(on);
       if (ends) break;
@@ -283,7 +283,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const _
 // (The same in the kernels themselves took registers and instruction cache from them:
 // 325 to 375 us for 304 where four chunks of 1021 tokens are answered behind 2048.)
 constexpr float kRoomMma = 256.f, kRoomTc = 65536.f;
-
+// On tcgen05 scales in f16 also lose to those of tokens that all rows see, from 2^-13 of
+// the largest on (attention.cuh): where the kernel before has met such, all scales of a
+// tile are looked at.
 // Rows of a tile again, in fp32, right whatever the scales are: of one cached head, up to
 // four rows a warp and 32 cached tokens at a time, which go to shared memory as values.
 // Where every tile is one of those (a later token in eight with values 2^20 times the
@@ -430,7 +432,7 @@ __device__ __forceinline__ float live_scale(const qwha_cache &c, int64_t row, in
   }
   return idle ? 0.f : x;
 }
-// Which heads of a tile are (bits of the result). A row has at least the largest scale of the tokens that
+// Which heads of a tile are (bits of the result). spread: any two tokens' scales are compared. Else: a row has at least the largest scale of the tokens that
 // all rows see, of which the newest 32 are looked at (all, where these have none), or, where
 // there are none, maybe the least of the others alone. The keys' groups count together: a
 // score is their sum. Idle groups do not count.
@@ -438,10 +440,11 @@ struct Scales {
   uint32_t top, all, some;  // the largest of tokens that not all rows see; of those that all see; the least of the first
 };
 template <bool TC>
-__device__ __forceinline__ unsigned needs_repair(const AttnArgs &a, const Seq &s, int b, int block, int tile, Scales (*of)[33]) {
+__device__ __forceinline__ unsigned needs_repair(const AttnArgs &a, const Seq &s, int b, int block, int tile, bool spread,
+                                                 Scales (*of)[33]) {
   const int ng = a.v.head_dim / a.v.group, ng_k = a.k.head_dim / a.k.group, head_block = block_of(a, block), length = s.length(a, tile);
-  const int safe = a.tree ? s.past : s.past + tile * a.tq + 1;  // every row sees the tokens below
-  if (s.rows - tile * a.tq == 1 || a.tq == 1 || length <= safe) return 0;  // (one token: its rows see the same)
+  const int safe = spread ? 0 : a.tree ? s.past : s.past + tile * a.tq + 1;  // every row sees the tokens below
+  if (!spread && (s.rows - tile * a.tq == 1 || a.tq == 1 || length <= safe)) return 0;  // (one token: its rows see the same)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
   const int per_head = (threads >> 5) / a.hb, hl = warp % a.hb, sub = warp / a.hb, kv = head_block * a.hb + hl;
   __syncthreads();
@@ -483,7 +486,7 @@ __device__ __forceinline__ unsigned needs_repair(const AttnArgs &a, const Seq &s
   const int near = max(safe - 32, 0);
   look(near, length);
   __syncthreads();
-  if (near > 0 && any_of([](const Scales &x) { return x.top && !x.all; })) {
+  if (near > 0 && !spread && any_of([](const Scales &x) { return x.top && !x.all; })) {
     look(0, near);
     __syncthreads();
   }
@@ -492,7 +495,8 @@ __device__ __forceinline__ unsigned needs_repair(const AttnArgs &a, const Seq &s
   __syncthreads();
   for (int i = threadIdx.x; i < a.hb * 33; i += threads) {
     const Scales x = of[i / 33][i % 33];
-    if (__uint_as_float(x.top) > (TC ? kRoomTc : kRoomMma) * __uint_as_float(x.all ? x.all : x.some)) atomicOr(&far_s, 1u << (i / 33));
+    const float room = spread ? kSpreadTc : TC ? kRoomTc : kRoomMma;
+    if (__uint_as_float(x.top) > room * __uint_as_float(x.all ? x.all : x.some)) atomicOr(&far_s, 1u << (i / 33));
   }
   __syncthreads();
   return far_s;
@@ -504,27 +508,37 @@ __global__ void __launch_bounds__(kRepairThreads, C <= 4 ? 3 : 2) attention_repa
   extern __shared__ __align__(16) float repair_s[];
   __shared__ Scales of[kMmaWarps][33];
   __shared__ int64_t slot_s[kRepairTokens];
-  for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
-    const Seq s(a, b);
-    const long long tiles = (long long)s.tiles * a.blocks;
-    const int share = tiles < gridDim.y && tiles ? (int)(gridDim.y / tiles) : 1, step = (int)(gridDim.y / share);
-    if ((int)blockIdx.y >= step * share) continue;
-    for (long long i = blockIdx.y / share; i < tiles; i += step) {
-      const int block = (int)(i / s.tiles), tile = (int)(i - (long long)block * s.tiles);
-      const unsigned heads = needs_repair<TC>(a, s, b, block, tile, of);
-      if (!heads) continue;
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      // pieces of `each` rows a warp, in turn to the CTAs that share the tile
-      const int rows = min(a.tq, s.rows - tile * a.tq) * a.gh;  // (the last part of a group may have fewer)
-      const int each = min(max((rows * __popc(heads) + share * kRepairWarps - 1) / (share * kRepairWarps), 1), kRepairRows);
-      int turn = blockIdx.y % share;
-      for (int hl = 0; hl < a.hb; ++hl)
-        if (heads >> hl & 1)
-          for (int first = 0; first < rows; first += each * kRepairWarps, turn = turn ? turn - 1 : share - 1)
-            if (turn == 0) repair<C>(a, s, b, block, tile, hl, first, each, repair_s, slot_s);
+  auto look = [&](bool spread) {
+    for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
+      const Seq s(a, b);
+      const long long tiles = (long long)s.tiles * a.blocks;
+      const int share = tiles < gridDim.y && tiles ? (int)(gridDim.y / tiles) : 1, step = (int)(gridDim.y / share);
+      if ((int)blockIdx.y >= step * share) continue;
+      for (long long i = blockIdx.y / share; i < tiles; i += step) {
+        const int block = (int)(i / s.tiles), tile = (int)(i - (long long)block * s.tiles);
+        const unsigned heads = needs_repair<TC>(a, s, b, block, tile, spread, of);
+        if (!heads) continue;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        // pieces of `each` rows a warp, in turn to the CTAs that share the tile
+        const int rows = min(a.tq, s.rows - tile * a.tq) * a.gh;  // (the last part of a group may have fewer)
+        const int each = min(max((rows * __popc(heads) + share * kRepairWarps - 1) / (share * kRepairWarps), 1), kRepairRows);
+        int turn = blockIdx.y % share;
+        for (int hl = 0; hl < a.hb; ++hl)
+          if (heads >> hl & 1)
+            for (int first = 0; first < rows; first += each * kRepairWarps, turn = turn ? turn - 1 : share - 1)
+              if (turn == 0) repair<C>(a, s, b, block, tile, hl, first, each, repair_s, slot_s);
+      }
     }
+  };
+  // one copy of its code; the second time where some CTA of the kernel before says so
+  for (bool spread = false;; spread = true) {
+    look(spread);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!TC || spread) break;
+    bool coarse = false;
+    for (int i = threadIdx.x; i < a.ctas; i += kRepairThreads) coarse |= a.part_desc[2 * i].w & kPieceCoarse;
+    if (!__syncthreads_or(coarse)) break;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 size_t any_smem(int D) {
@@ -610,8 +624,8 @@ bool tc_takes(const AttnArgs &a) {
   const int64_t rows = cdiv(a.n, a.n_seqs) * a.grp, tokens = (int64_t)a.n_seqs * a.k.heads * a.cap;
   return (rows > kTcAbove || (rows > kTcAboveIfSmall && tokens <= rows << kTcSmallLog2)) && attention_tc_takes(a);
 }
-// Whether rows may have to be done again: not where a tile has one token, whose rows all see the same.
-bool repairs(const AttnArgs &a) { return (tc_takes(a) || mma_takes(a)) && a.n > a.n_seqs; }
+// Whether rows may have to be done again: on mma.sync not where a tile has one token, whose rows all see the same.
+bool repairs(const AttnArgs &a) { return tc_takes(a) || (mma_takes(a) && a.n > a.n_seqs); }
 
 }  // namespace
 

@@ -19,6 +19,10 @@
 namespace qwha {
 namespace attn {
 
+// How far scales may lie apart on tcgen05 (attention_tc.cu): the largest of its group of
+// values, or of a head's keys, is at least 2^4 in f16, so that one within 2^-13 of it has
+// 2^-9, of which the second piece, to 2^-25, keeps all but 2^-16.
+constexpr float kSpreadTc = 8192.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ int clamp_rows(int64_t v, int64_t lo, int64_t hi) { return (int)(v < lo ? lo : v > hi ? hi : v); }
@@ -238,6 +242,8 @@ __device__ __forceinline__ void warp_query(const AttnArgs &a, float *x, int64_t 
 // A piece in the workspace: row r of slot s holds m, l and D values. Slot 2 c is
 // the piece with which CTA c goes on with a tile that another began, slot 2 c + 1
 // the one it began and left.
+// (part_desc: sequence, block, tile and these; 0: none, as of a CTA without units)
+enum { kPieceThere = 1, kPieceEnds = 2, kPieceCoarse = 4 };  // coarse (slot 2 c, there or not): of any of the CTA's tiles
 __device__ __forceinline__ float *piece_stats(const AttnArgs &a, int slot, int r) {
   return a.part_stats + ((int64_t)slot * a.part_rows + r) * 2;
 }

@@ -1012,7 +1012,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, NT == 1 && DP <= 128 ? 2 : 1)
         }
       }
     }
-    if (threadIdx.x == 0 && !(starts && ends)) a.part_desc[slot_out] = make_int4(at.b, at.block, at.tile, ends ? 3 : 1);
+    if (threadIdx.x == 0 && !(starts && ends)) a.part_desc[slot_out] = make_int4(at.b, at.block, at.tile, ends ? kPieceThere | kPieceEnds : kPieceThere);
     left -= run;
     at.unit = 0;
     if (rows.j0 + a.tq >= rows.all) {  // the sequence's last tile

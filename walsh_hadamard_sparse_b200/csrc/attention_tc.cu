@@ -52,6 +52,7 @@ constexpr int kRowsTile = 128, kKeys = 128, kUnpackWarps = 8, kSoftWarps = 8;  /
 constexpr int kUnpackers = kUnpackWarps * 16, kRounds = 128 / kUnpackers * 2, kTcThreads = (kUnpackWarps + kSoftWarps + 1) * 32;
 constexpr int kScaleSlots = 4;      // tiles whose scales are kept: a tile's are read until its weights are made
 constexpr float kTcTop = 64.f;      // of a scale in f16, times 255 of a code below the largest
+constexpr float kTcLeast = 0.001953125f;  // what scales are to be at least: 2^4, where the largest lies, over kSpreadTc
 constexpr float kTcShift = 8.f;     // weights are kept 2^8 times as large: f16 holds them to 2^-33 of the maximum's
 constexpr float kTcSum = 32768.f;   // of the weights of half a tile, before its maximum is taken again
 constexpr uint32_t kTcCols = 512;   // TMEM: S_0, S_1, O_0, O_1
@@ -297,37 +298,33 @@ struct Unpacker {
   uint8_t *smem;
   uint32_t bars, one;
   bool ok = true;
+  bool coarse = false;       // scales far apart were met
   uint32_t it = 0;           // tiles so far
   uint32_t w[kRounds][kSlabs][B];  // raw codes of the next tile's tokens
-  float most[kRounds];       // the largest scale of a token that is a number
   float scale[kRounds][kSlabs];  // of the lane's groups
+  float factor[kSlabs];      // of the scales of the lane's channels (the keys: of all): follows the largest met by any of the warps
   uint8_t zero[kRounds][kSlabs], bad[kRounds];
   bool on[kRounds];
 
   __device__ __forceinline__ Unpacker(const AttnArgs &a_, bool values_, uint8_t *smem_, uint32_t bars_, uint32_t one_)
       : a(a_), c(values_ ? a_.v : a_.k), values(values_), smem(smem_), bars(bars_), one(one_) {}
 
-  // The scales and zero points of the lane's groups, the token's largest scale, which groups are no numbers. Values of
-  // such a group stay out of the products, where they would meet weights of zero; keys go in as they are.
+  // The scales and zero points of the lane's groups, and which of them are no numbers. Values of such a group stay out of
+  // the products, where they would meet weights of zero; keys go in as they are.
   __device__ __forceinline__ void scales(int64_t row, int ng, int r) {
-    const float *s = c.scales + row * ng;
-    const uint8_t *z = c.zeros + row * ng;
-    float all[4], top = 0.f;
     int b = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      all[i] = i < ng ? __ldg(s + i) : 0.f;
-      if (fabsf(all[i]) < INFINITY) top = fmaxf(top, fabsf(all[i]));
-      else if (values) b |= 1 << i, all[i] = 0.f;
-    }
-    most[r] = top, bad[r] = (uint8_t)b;
 #pragma unroll
     for (int i = 0; i < kSlabs; ++i) {
       const int d = 64 * i + 32 * (threadIdx.x & 1), g = ng > 1 && d < c.head_dim ? d / c.group : 0;
-      const float own = g == 0 ? all[0] : g == 1 ? all[1] : g == 2 ? all[2] : all[3];
-      scale[r][i] = d < c.head_dim ? own : 0.f, zero[r][i] = __ldg(z + g);
+      float x = __ldg(c.scales + row * ng + g);
+      zero[r][i] = __ldg(c.zeros + row * ng + g);
+      if (values && !(fabsf(x) < INFINITY)) b |= 1 << g, x = 0.f;
+      scale[r][i] = d < c.head_dim ? x : none(i);
     }
+    bad[r] = (uint8_t)b;
   }
+  // A scale that changes no factor, for what is not there.
+  __device__ __forceinline__ float none(int i) const { return 16.f * inverse2(factor[i]); }
 
   // (code - zero) times the scale, which comes as the sum of two f16 numbers: the product is rounded once.
   __device__ __forceinline__ void write(uint8_t *row, int token, int r, int i, float factor, bool live) {
@@ -388,10 +385,10 @@ struct Unpacker {
 #pragma unroll
       for (int r = 0; r < kRounds; ++r) {
         on[r] = (uint32_t)page[r] < (uint32_t)a.k.n_pages;
-        most[r] = 0.f, bad[r] = 0;
+        bad[r] = 0;
         if (!on[r]) {
 #pragma unroll
-          for (int i = 0; i < kSlabs; ++i) scale[r][i] = 0.f;
+          for (int i = 0; i < kSlabs; ++i) scale[r][i] = none(i);
           if (page[r] != -2) atomicOr(a.err, kErrPage);
           continue;
         }
@@ -404,41 +401,44 @@ struct Unpacker {
         scales(row, ng, r);
       }
     };
+#pragma unroll
+    for (int i = 0; i < kSlabs; ++i) factor[i] = kNoScale;
     ask(true);
     fetch();
     t0 += kKeys;
     ask(g.run > 1);
-    float factor[kSlabs];  // of the scales of the lane's channels (the keys: of all): follows the largest met by any of the warps
-#pragma unroll
-    for (int i = 0; i < kSlabs; ++i) factor[i] = kNoScale;
     uint8_t *tiles = smem + (values ? S::kV : S::kK);
     for (int u = 0; u < g.run; ++u, ++it) {
       const int st = it & 1;
       TileScales &sc = *reinterpret_cast<TileScales *>(smem + S::kScales + (it % kScaleSlots) * sizeof(TileScales));
-      float top[kSlabs], grow[kSlabs];
-      int any_bad = 0, over = 0;
+      float grow[kSlabs];
+      int any_bad = 0;
+      // Scales that times the factor lie outside kTcLeast .. kTcTop: a distance in bits, of which one comparison takes both
+      // ends (0 too), since the factor is a power of two.
+      uint32_t far = 0;
 #pragma unroll
       for (int i = 0; i < kSlabs; ++i) {
-        top[i] = 0.f, grow[i] = 1.f;
+        grow[i] = 1.f;
+        const uint32_t shift = __float_as_uint(factor[i]) - (__float_as_uint(kTcLeast) + __float_as_uint(1.f));
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) top[i] = fmaxf(top[i], values ? fabsf(scale[r][i]) : most[r]);
-        over |= top[i] * factor[i] > kTcTop;
+        for (int r = 0; r < kRounds; ++r) far = max(far, __float_as_uint(fabsf(scale[r][i])) + shift);
       }
 #pragma unroll
       for (int r = 0; r < kRounds; ++r) any_bad |= bad[r];
-      const int grown = any_of(over);
+      const int grown = any_of(far > __float_as_uint(kTcTop) - __float_as_uint(kTcLeast));
       if (grown) {
         uint32_t *top_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount + 16) + (values ? 4 : 0);
         if (threadIdx.x % kUnpackers < 4) top_s[threadIdx.x % kUnpackers] = 0;
         meet();
         // codes that all equal their zero point have no say, whatever their scale
+        float top[kSlabs];
 #pragma unroll
         for (int i = 0; i < kSlabs; ++i) {
           top[i] = 0.f;
 #pragma unroll
           for (int r = 0; r < kRounds; ++r) {
             const float x = fabsf(scale[r][i]);
-            if (!(x < INFINITY)) continue;
+            if (!on[r] || 32 * (2 * i + half) >= D || !(x < INFINITY)) continue;
             if (x * factor[i] > kTcTop && idle(r, i)) scale[r][i] = 0.f;
             else top[i] = fmaxf(top[i], x);
           }
@@ -452,6 +452,9 @@ struct Unpacker {
           e = e < 1 ? 1 : e > 247 ? 247 : e;
           const float now = fminf(factor[i], __uint_as_float((uint32_t)e << 23));
           grow[i] = now * inverse2(factor[i]), factor[i] = now;
+#pragma unroll
+          for (int r = 0; r < kRounds; ++r)
+            coarse |= on[r] && 32 * (2 * i + half) < D && scale[r][i] != 0.f && fabsf(scale[r][i]) * now < kTcLeast;
         }
         meet();
       }
@@ -459,7 +462,7 @@ struct Unpacker {
         any_bad = any_of(any_bad);
 #pragma unroll
         for (int r = 0; r < kRounds; ++r)
-          if (half == 0) sc.groups[mine + 16 * r] = bad[r];
+          if (const int other = __shfl_xor_sync(~0u, bad[r], 1); half == 0) sc.groups[mine + 16 * r] = (uint8_t)(bad[r] | other);
         if (threadIdx.x % kUnpackers < 2) {
 #pragma unroll
           for (int i = 0; i < kSlabs; ++i) sc.values[2 * i + half] = factor[i], sc.grow[2 * i + half] = grow[i];
@@ -510,6 +513,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
   uint8_t *smem = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
   const uint32_t base = saddr(smem), bars = base + S::kBars;
   uint32_t *tmem_s = reinterpret_cast<uint32_t *>(smem + S::kBars + 8 * kBarCount);
+  volatile int *coarse_s = reinterpret_cast<int *>(tmem_s + 1);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kIssue = kUnpackWarps + kSoftWarps;
   if (threadIdx.x == 0) {
@@ -527,7 +531,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     fence_before();
   }
-  if (threadIdx.x == 0) a.part_desc[2 * blockIdx.x] = a.part_desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0) {
+    a.part_desc[2 * blockIdx.x] = a.part_desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+    *coarse_s = 0;
+  }
   Place at;
   long long left = my_share(a, &at);
   __syncthreads();
@@ -550,6 +557,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         g.next(a, &at, &left);
       }
       if (!unpack.ok) atomicOr(a.err, kErrTc);
+      if (unpack.coarse) *coarse_s = kPieceCoarse;
     };
     switch (values ? a.v.bits : a.k.bits) {
       case 2: work(std::integral_constant<int, 2>()); break;
@@ -819,7 +827,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
       }
       slot += g.run;
       if (threadIdx.x == kUnpackWarps * 32 && !(g.starts && g.ends))
-        a.part_desc[out_slot] = make_int4(at.b, at.block, at.tile, g.ends ? 3 : 1);
+        a.part_desc[out_slot] = make_int4(at.b, at.block, at.tile, g.ends ? kPieceThere | kPieceEnds : kPieceThere);
       g.next(a, &at, &left);
     }
     if (!ok) atomicOr(a.err, kErrTc);
@@ -888,6 +896,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
   }
   fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *coarse_s) a.part_desc[2 * blockIdx.x].w |= *coarse_s;
   if (warp == kIssue) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcCols) : "memory");
