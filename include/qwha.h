@@ -345,7 +345,11 @@ qwha_status qwha_rotary(qwha_dtype dt, int32_t n_x, const void *const *x, const 
  * bf16 and 2^-21 for fp32 at most (a weight times a scale below 2^-24 of the
  * largest scale that the row sees in the group by 2^-33 of that), and in bf16
  * calls of many rows to a cached head the cached values too, by 2^-11 + 2^-16 of
- * each; else these are exact.
+ * each; else these are exact. Many rows: more than 44 queries times q_heads / heads
+ * to a sequence on the call's average, or more than 8 where n_seqs * heads *
+ * max_pages * page_size is at most 2^14 times these rows; head_dim and groups whole
+ * 32s, head_dim up to 128. (The average decides for all sequences of a call: a chunk
+ * among many single tokens is better in a call of its own.)
  * Some rows are done again in fp32, 20 to 90 times as slowly: those whose tokens'
  * scales are far below those of tokens that only other rows see (2^8 times, in
  * bf16 calls of many rows 2^16), and in the latter calls those that see scales
@@ -358,6 +362,18 @@ qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_
                                  int32_t q_heads, int64_t q_stride, const int32_t *pages, int32_t max_pages,
                                  const int64_t *q_start, const int64_t *past, int32_t n_seqs, const int64_t *tree,
                                  float scale, void *out, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* The same for a caller who knows that no sequence has more than `longest` tokens,
+ * past and new ones together: with more than 8 and up to 44 rows this stands for
+ * the table's room where the kernel is chosen, which a table made for the longest
+ * context that is allowed does not tell (2 contexts of 1024 in a table for 131072:
+ * 25 us instead of 38 with 12 rows, 27 instead of 55 with 36). It only chooses:
+ * longer sequences are answered all the same. */
+qwha_status qwha_cache_attention_upto(const qwha_cache *k, const qwha_cache *v, qwha_dtype dt, const void *q, int64_t n,
+                                      int32_t q_heads, int64_t q_stride, const int32_t *pages, int32_t max_pages,
+                                      const int64_t *q_start, const int64_t *past, int32_t n_seqs, const int64_t *tree,
+                                      float scale, int64_t longest, void *out, float *lse, void *ws, size_t ws_bytes,
+                                      void *stream);
 
 /* Which pages of a cache (of all caches of a model: every layer's keys and
  * values use the same page numbers) hold the tokens of which sequence. Device

@@ -2,7 +2,7 @@
 
 import ctypes
 
-from test_serving_cpu import BUF, INVALID, MISALIGNED, OK, WORKSPACE, P, _L
+from test_serving_cpu import BUF, INVALID, MISALIGNED, OK, WORKSPACE, P, _cache, _L
 
 
 def test_resize_with_copies_refusals():
@@ -23,3 +23,19 @@ def test_resize_with_copies_refusals():
     assert call(less=1) == WORKSPACE and call(ws=None) != OK
     assert call(n_seqs=0, want=None, origin=None, fresh=None) == OK
     assert h.qwha_pages_resize_copies(None, BUF, BUF, BUF, BUF, 1 << 20, None) == INVALID
+
+
+def test_attention_upto_refusals():
+    """A negative length is refused; all else as without one (the same checks, in the same order)."""
+    L = _L()
+    h, c = L.lib(), _cache(L)
+
+    def call(longest, n=4, q=P(1 << 20), q_heads=4):
+        k = ctypes.byref(c)
+        return h.qwha_cache_attention_upto(k, k, 1, q, n, q_heads, 512, BUF, 2, BUF, BUF, 2, None, ctypes.c_float(0.1), longest, P(1 << 22), None,
+                                           BUF, 1 << 30, None)
+
+    assert call(-1) == INVALID and b"longest" in h.qwha_last_error()
+    for longest in (0, 1, 2**63 - 1):
+        assert call(longest, n=0) == OK and call(longest, n=-1) == INVALID and call(longest, q=None) == INVALID
+        assert call(longest, q_heads=3) == INVALID and b"q_heads" in h.qwha_last_error()

@@ -363,3 +363,23 @@ def test_attention_of_many_rows_keeps_tokens_beside_one_of_a_far_larger_scale(fa
             if which == 0:
                 assert np.all(np.abs(host(s.lse) - lse) <= lse_tol)
             _W().check_stream_status()
+
+
+# ---------------------------------------------------------------- the choice of the kernel
+
+
+@pytest.mark.parametrize("D,bits,group", [(128, 4, 128), (64, 8, 32), (96, 3, 32)])
+@pytest.mark.parametrize("new,grp", [(3, 4), (8, 5), (20, 2)])
+def test_attention_told_of_the_longest_sequence(D, bits, group, new, grp):
+    """A wide table with the longest length is answered as a narrow one is, by the same kernel; a wide one without by the one
+    that keeps cached values exact; whatever is told, the answer is right."""
+    key = dict(heads=2, grp=grp, D=D, bits=bits, group=group, tree=random_trees, had_v=8)
+    narrow = Setup(f"upto{D}{new}", [300, 70, 0], [new] * 3, **key)
+    wide = Setup(f"upto{D}{new}", [300, 70, 0], [new] * 3, room=1 << 20, **key)
+    want = host(narrow.run())
+    assert np.array_equal(host(wide.run(longest=300 + new)), want) and np.array_equal(host(wide.lse), host(narrow.lse))
+    for longest in (0, 5, 1 << 40):
+        wide.check(wide.run(longest=longest))
+    wide.cached = 0.0
+    wide.check()
+    wide.check(wide.run(longest=1 << 20))

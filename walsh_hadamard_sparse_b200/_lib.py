@@ -72,6 +72,8 @@ _SIGNATURES = {
     "qwha_rotary": (ctypes.c_int, [ctypes.c_int, i32, P, P, P, P, P, i32, i64, P, P, i32, ctypes.c_int, f32, i32, P]),
     "qwha_cache_attention": (ctypes.c_int, [ctypes.POINTER(QwhaCache), ctypes.POINTER(QwhaCache), ctypes.c_int, P, i64, i32,
                                             i64, P, i32, P, P, i32, P, f32, P, P, P, sz, P]),
+    "qwha_cache_attention_upto": (ctypes.c_int, [ctypes.POINTER(QwhaCache), ctypes.POINTER(QwhaCache), ctypes.c_int, P, i64,
+                                                 i32, i64, P, i32, P, P, i32, P, f32, i64, P, P, P, sz, P]),
     "qwha_pages_resize": (ctypes.c_int, [ctypes.POINTER(QwhaPageTable), P, P, sz, P]),
     "qwha_pages_resize_copies": (ctypes.c_int, [ctypes.POINTER(QwhaPageTable), P, P, P, P, sz, P]),
     "qwha_pages_fork": (ctypes.c_int, [ctypes.POINTER(QwhaPageTable), P, P, i32, P, P, P, sz, P]),

@@ -432,9 +432,13 @@ def rotary(x, positions: torch.Tensor, freq: torch.Tensor, interleaved: bool = F
     return outs[0] if single else outs
 
 
+_ANY = 2**63 - 1  # nothing known of the lengths
+
+
 def cache_attention(kv, q: torch.Tensor, pages: torch.Tensor, q_start: torch.Tensor, past: torch.Tensor,
                     tree: torch.Tensor | None = None, scale: float | None = None, out: torch.Tensor | None = None,
-                    lse: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+                    lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                    longest: int | None = None) -> torch.Tensor:
     """Attention of queries q [n, q_heads, head_dim] (fp32 or bf16; tokens may lie apart) over the cached keys and values
     kv, read from their codes. Rows q_start[b] .. q_start[b+1] (int64 [n_seqs+1]) are the newest tokens of sequence b,
     cached already behind past[b] (int64 [n_seqs]) earlier ones, token t in page pages[b, t // page_size] (int32
@@ -442,7 +446,8 @@ def cache_attention(kv, q: torch.Tensor, pages: torch.Tensor, q_start: torch.Ten
     [n]) those whose bit is set in its mask (up to 64: a drafted tree's node and its ancestors). q_heads is a multiple of
     the cache's heads; scale defaults to 1/sqrt(head_dim). lse (fp32 [n, q_heads]) receives the log of the softmax sums.
     A row that sees nothing gets zeros (lse -inf); rows from q_start[-1] on are left as they were (without `out` they are
-    not initialised)."""
+    not initialised). longest: the most tokens, past and new, of any sequence, where that is known to be far less than the
+    table has room for; it only helps to choose the kernel."""
     h, dev, dt = lib(), torch.cuda.current_device(), _dt(q)
     k, v = kv
     ck, cv = k.c_struct(dev), v.c_struct(dev)
@@ -453,14 +458,15 @@ def cache_attention(kv, q: torch.Tensor, pages: torch.Tensor, q_start: torch.Ten
         out = q.new_empty((n, q_heads, head_dim))
     if ws is None:
         ws = _new_ws(q, h.qwha_workspace_size(OP_ATTENTION, q_heads, head_dim, ck.heads, n, 2 - dt))
-    check(h.qwha_cache_attention(ck, cv, dt, at, n, q_heads, stride, _fit("pages", pages, torch.int32, (n_seqs, max_pages), dev),
-                                 max_pages, _fit("q_start", q_start, torch.int64, (n_seqs + 1,), dev),
-                                 _fit("past", past, torch.int64, (n_seqs,), dev), n_seqs,
-                                 None if tree is None else _fit("tree", tree, torch.int64, (n,), dev),
-                                 head_dim**-0.5 if scale is None else scale,
-                                 _fit("out", out, q.dtype, (n, q_heads, head_dim), dev),
-                                 None if lse is None else _fit("lse", lse, torch.float32, (n, q_heads), dev),
-                                 *_fit_ws(ws, dev), _raw_stream(dev)), "qwha_cache_attention")
+    check(h.qwha_cache_attention_upto(ck, cv, dt, at, n, q_heads, stride,
+                                      _fit("pages", pages, torch.int32, (n_seqs, max_pages), dev), max_pages,
+                                      _fit("q_start", q_start, torch.int64, (n_seqs + 1,), dev),
+                                      _fit("past", past, torch.int64, (n_seqs,), dev), n_seqs,
+                                      None if tree is None else _fit("tree", tree, torch.int64, (n,), dev),
+                                      head_dim**-0.5 if scale is None else scale, _ANY if longest is None else longest,
+                                      _fit("out", out, q.dtype, (n, q_heads, head_dim), dev),
+                                      None if lse is None else _fit("lse", lse, torch.float32, (n, q_heads), dev),
+                                      *_fit_ws(ws, dev), _raw_stream(dev)), "qwha_cache_attention")
     return out
 
 

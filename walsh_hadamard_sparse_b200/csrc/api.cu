@@ -1106,6 +1106,56 @@ qwha_status resize(const qwha_page_table &t, const int64_t *want, int32_t *from,
   return cuda_status(launch_pages_resize(t, want, from, to, ws, (cudaStream_t)stream), "pages_resize");
 }
 
+qwha_status attend(const qwha_cache *k, const qwha_cache *v, qwha_dtype dt, const void *q, int64_t n,
+                   int32_t q_heads, int64_t q_stride, const int32_t *pages, int32_t max_pages,
+                   const int64_t *q_start, const int64_t *past, int32_t n_seqs, const int64_t *tree, float scale,
+                   int64_t longest, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
+  if (!valid_dtype(dt)) return fail(QWHA_ERR_INVALID_ARG, "dtype %d", (int)dt);
+  if (!k || !v) return fail(QWHA_ERR_INVALID_ARG, "%s is NULL", k ? "v" : "k");
+  qwha_status st = check_cache(k);
+  if (st != QWHA_OK || (st = check_cache(v)) != QWHA_OK) return st;
+  if (k->heads != v->heads || k->head_dim != v->head_dim || k->page_size != v->page_size || k->n_pages != v->n_pages)
+    return fail(QWHA_ERR_INVALID_ARG, "the caches of keys and values differ in heads, head_dim, page_size or n_pages");
+  if (q_heads < 1 || q_heads > 65535 || q_heads % k->heads)
+    return fail(QWHA_ERR_INVALID_ARG, "q_heads %d must be a multiple of the cache's heads %d", q_heads, k->heads);
+  if (n < 0 || n > 2147483647LL) return fail(QWHA_ERR_INVALID_ARG, "n %lld out of range", (long long)n);
+  if (n_seqs < 0 || max_pages < 0) return fail(QWHA_ERR_INVALID_ARG, "n_seqs %d, max_pages %d", n_seqs, max_pages);
+  if (!isfinite(scale)) return fail(QWHA_ERR_INVALID_ARG, "scale is not finite");
+  const int64_t esz = dt == QWHA_F32 ? 4 : 2, row = (int64_t)q_heads * k->head_dim;
+  if (q_stride < row || q_stride > (1LL << 32))
+    return fail(QWHA_ERR_INVALID_ARG, "q_stride %lld of tokens of %lld elements", (long long)q_stride, (long long)row);
+  if (q_stride * esz % 16) return fail(QWHA_ERR_MISALIGNED, "q_stride must be a multiple of 16 bytes");
+  if (n == 0 || n_seqs == 0) return QWHA_OK;
+  QWHA_CHECK_PTR(q, "q");
+  QWHA_CHECK_PTR(out, "out");
+  if (max_pages > 0) QWHA_CHECK_INDEX(pages, "pages");
+  QWHA_CHECK_INDEX(q_start, "q_start");
+  QWHA_CHECK_INDEX(past, "past");
+  if (tree) QWHA_CHECK_INDEX(tree, "tree");
+  if (lse) QWHA_CHECK_PTR(lse, "lse");
+  if ((st = check_ws(ws, ws_bytes, attention_workspace(q_heads, k->head_dim, k->heads, n, dt == QWHA_F32))) != QWHA_OK)
+    return st;
+  const size_t q_bytes = (size_t)(((n - 1) * q_stride + row) * esz), out_bytes = (size_t)(n * row * esz);
+  if ((st = check_apart("q and out", q, q_bytes, out, out_bytes)) != QWHA_OK) return st;
+  if (lse && ((st = check_apart("q and lse", q, q_bytes, lse, (size_t)n * q_heads * 4)) != QWHA_OK ||
+              (st = check_apart("out and lse", out, out_bytes, lse, (size_t)n * q_heads * 4)) != QWHA_OK))
+    return st;
+  AttnArgs a = {};
+  a.k = *k, a.v = *v;
+  a.unit_k = k->had_block ? (float)(1.0 / sqrt((double)k->had_block)) : 1.f;
+  a.unit_v = v->had_block ? (float)(1.0 / sqrt((double)v->had_block)) : 1.f;
+  a.q = q, a.q_stride = q_stride, a.n = n, a.q_heads = q_heads, a.grp = q_heads / k->heads;
+  a.pages = pages, a.max_pages = max_pages;
+  a.cap = (int)std::min<int64_t>((int64_t)max_pages * k->page_size, 1 << 30);
+  a.longest = (int)std::min<int64_t>(a.cap, longest);
+  const int lg = ilog2(k->page_size);  // 2^lg >= page_size: the product of 31 and 32 bits is exact where it counts
+  a.page_shift = 31 + lg, a.page_mul = (unsigned int)(((1ull << a.page_shift) + k->page_size - 1) / k->page_size);
+  a.q_start = q_start, a.past = past, a.n_seqs = n_seqs, a.tree = tree;
+  a.scale2 = (float)(scale * 1.4426950408889634), a.out = out, a.lse = lse, a.f32 = dt == QWHA_F32;
+  StageScope sc(ST_ATTENTION, attention_launches(a), (cudaStream_t)stream);
+  return cuda_status(launch_attention(a, ws, (cudaStream_t)stream), "cache_attention");
+}
+
 CachePair moved_pair(const qwha_cache *caches, int32_t n_caches) {
   CachePair c = {};
   for (int i = 0; i < n_caches; ++i) c.cache[i] = caches[i];
@@ -1171,49 +1221,18 @@ qwha_status qwha_cache_attention(const qwha_cache *k, const qwha_cache *v, qwha_
                                  int32_t q_heads, int64_t q_stride, const int32_t *pages, int32_t max_pages,
                                  const int64_t *q_start, const int64_t *past, int32_t n_seqs, const int64_t *tree,
                                  float scale, void *out, float *lse, void *ws, size_t ws_bytes, void *stream) {
-  if (!valid_dtype(dt)) return fail(QWHA_ERR_INVALID_ARG, "dtype %d", (int)dt);
-  if (!k || !v) return fail(QWHA_ERR_INVALID_ARG, "%s is NULL", k ? "v" : "k");
-  qwha_status st = check_cache(k);
-  if (st != QWHA_OK || (st = check_cache(v)) != QWHA_OK) return st;
-  if (k->heads != v->heads || k->head_dim != v->head_dim || k->page_size != v->page_size || k->n_pages != v->n_pages)
-    return fail(QWHA_ERR_INVALID_ARG, "the caches of keys and values differ in heads, head_dim, page_size or n_pages");
-  if (q_heads < 1 || q_heads > 65535 || q_heads % k->heads)
-    return fail(QWHA_ERR_INVALID_ARG, "q_heads %d must be a multiple of the cache's heads %d", q_heads, k->heads);
-  if (n < 0 || n > 2147483647LL) return fail(QWHA_ERR_INVALID_ARG, "n %lld out of range", (long long)n);
-  if (n_seqs < 0 || max_pages < 0) return fail(QWHA_ERR_INVALID_ARG, "n_seqs %d, max_pages %d", n_seqs, max_pages);
-  if (!isfinite(scale)) return fail(QWHA_ERR_INVALID_ARG, "scale is not finite");
-  const int64_t esz = dt == QWHA_F32 ? 4 : 2, row = (int64_t)q_heads * k->head_dim;
-  if (q_stride < row || q_stride > (1LL << 32))
-    return fail(QWHA_ERR_INVALID_ARG, "q_stride %lld of tokens of %lld elements", (long long)q_stride, (long long)row);
-  if (q_stride * esz % 16) return fail(QWHA_ERR_MISALIGNED, "q_stride must be a multiple of 16 bytes");
-  if (n == 0 || n_seqs == 0) return QWHA_OK;
-  QWHA_CHECK_PTR(q, "q");
-  QWHA_CHECK_PTR(out, "out");
-  if (max_pages > 0) QWHA_CHECK_INDEX(pages, "pages");
-  QWHA_CHECK_INDEX(q_start, "q_start");
-  QWHA_CHECK_INDEX(past, "past");
-  if (tree) QWHA_CHECK_INDEX(tree, "tree");
-  if (lse) QWHA_CHECK_PTR(lse, "lse");
-  if ((st = check_ws(ws, ws_bytes, attention_workspace(q_heads, k->head_dim, k->heads, n, dt == QWHA_F32))) != QWHA_OK)
-    return st;
-  const size_t q_bytes = (size_t)(((n - 1) * q_stride + row) * esz), out_bytes = (size_t)(n * row * esz);
-  if ((st = check_apart("q and out", q, q_bytes, out, out_bytes)) != QWHA_OK) return st;
-  if (lse && ((st = check_apart("q and lse", q, q_bytes, lse, (size_t)n * q_heads * 4)) != QWHA_OK ||
-              (st = check_apart("out and lse", out, out_bytes, lse, (size_t)n * q_heads * 4)) != QWHA_OK))
-    return st;
-  AttnArgs a = {};
-  a.k = *k, a.v = *v;
-  a.unit_k = k->had_block ? (float)(1.0 / sqrt((double)k->had_block)) : 1.f;
-  a.unit_v = v->had_block ? (float)(1.0 / sqrt((double)v->had_block)) : 1.f;
-  a.q = q, a.q_stride = q_stride, a.n = n, a.q_heads = q_heads, a.grp = q_heads / k->heads;
-  a.pages = pages, a.max_pages = max_pages;
-  a.cap = (int)std::min<int64_t>((int64_t)max_pages * k->page_size, 1 << 30);
-  const int lg = ilog2(k->page_size);  // 2^lg >= page_size: the product of 31 and 32 bits is exact where it counts
-  a.page_shift = 31 + lg, a.page_mul = (unsigned int)(((1ull << a.page_shift) + k->page_size - 1) / k->page_size);
-  a.q_start = q_start, a.past = past, a.n_seqs = n_seqs, a.tree = tree;
-  a.scale2 = (float)(scale * 1.4426950408889634), a.out = out, a.lse = lse, a.f32 = dt == QWHA_F32;
-  StageScope sc(ST_ATTENTION, attention_launches(a), (cudaStream_t)stream);
-  return cuda_status(launch_attention(a, ws, (cudaStream_t)stream), "cache_attention");
+  return attend(k, v, dt, q, n, q_heads, q_stride, pages, max_pages, q_start, past, n_seqs, tree, scale, INT64_MAX, out, lse, ws,
+                ws_bytes, stream);
+}
+
+qwha_status qwha_cache_attention_upto(const qwha_cache *k, const qwha_cache *v, qwha_dtype dt, const void *q, int64_t n,
+                                      int32_t q_heads, int64_t q_stride, const int32_t *pages, int32_t max_pages,
+                                      const int64_t *q_start, const int64_t *past, int32_t n_seqs, const int64_t *tree,
+                                      float scale, int64_t longest, void *out, float *lse, void *ws, size_t ws_bytes,
+                                      void *stream) {
+  if (longest < 0) return fail(QWHA_ERR_INVALID_ARG, "longest %lld is negative", (long long)longest);
+  return attend(k, v, dt, q, n, q_heads, q_stride, pages, max_pages, q_start, past, n_seqs, tree, scale, longest, out, lse, ws,
+                ws_bytes, stream);
 }
 
 qwha_status qwha_pages_resize(const qwha_page_table *t, const int64_t *want, void *ws, size_t ws_bytes, void *stream) {

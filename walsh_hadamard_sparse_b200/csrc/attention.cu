@@ -550,13 +550,16 @@ size_t any_smem(int D) {
 namespace {
 
 // Rows of a cached head above which tiles of 128 on tcgen05 are taken instead of 32 on
-// mma.sync, which does as many rows as there are (64 contexts of 4096, 8 heads: 328 us
-// against 163 with 16 rows, 242 with 32, 294 with 40, 327 with 48, 415 with 64); and
-// those above which it is where the call is small: its tiles are a head's, not all
-// heads', and are cut into fewer pieces (2 contexts of 1024: 22 us against 27 with 8
-// rows, 22 against 37 with 16, 25 against 63 with 32). Between the two measurements the
-// times are taken for linear, which puts the border near 2^14 tokens of a cached head
-// for each row; the table's room stands for the tokens, which only the device knows.
+// mma.sync, which does as many rows as there are (64 contexts of 4096, 8 heads, us on
+// tcgen05 and mma.sync: 370 and 206 with 16 rows, 373 and 298 with 28, 376 and 299 with 32;
+// even near 44); and those above which it is where the call is small: its tiles are a
+// head's, not all heads', and are cut into fewer pieces (2 contexts of 1024: 25 and 38
+// with 12 rows, 27 and 55 with 36; 16 of 4096: 101 and 71 with 12, 102 and 111 with 20; 4 of
+// 32768: 169 and 152 with 16, 170 and 178 with 24). Small: up to 2^14 tokens of a cached
+// head for each row, which over 1 to 64 contexts of 256 to 32768 tokens and 2 or 8 heads
+// takes the better or is within 25%, but for one long context (of 32768: 61 and 116 with
+// 16 rows, where it takes the latter). What the caller knows of the longest sequence, or
+// the table's room, stands for the tokens, which only the device knows.
 constexpr int kTcAbove = 44, kTcAboveIfSmall = 8, kTcSmallLog2 = 14;
 
 // Shared memory of an SM, and what a CTA has of it besides the dynamic part: the kernels' arrays (more with more rows)
@@ -621,7 +624,7 @@ bool mma_takes(const AttnArgs &a) {
   return takes_codes(a.k) && takes_codes(a.v) && a.k.n_pages * a.k.page_size < (1LL << 31);
 }
 bool tc_takes(const AttnArgs &a) {
-  const int64_t rows = cdiv(a.n, a.n_seqs) * a.grp, tokens = (int64_t)a.n_seqs * a.k.heads * a.cap;
+  const int64_t rows = cdiv(a.n, a.n_seqs) * a.grp, tokens = (int64_t)a.n_seqs * a.k.heads * a.longest;
   return (rows > kTcAbove || (rows > kTcAboveIfSmall && tokens <= rows << kTcSmallLog2)) && attention_tc_takes(a);
 }
 // Whether rows may have to be done again: on mma.sync not where a tile has one token, whose rows all see the same.

@@ -266,6 +266,7 @@ struct AttnArgs {
   const int32_t *pages;
   int max_pages;
   int cap;  // tokens the page table has room for
+  int longest;  // of a sequence, as far as the host knows: chooses the kernel
   unsigned int page_mul;  // t / page_size = t page_mul >> page_shift for t below 2^31
   int page_shift;
   const int64_t *q_start, *past;
