@@ -383,3 +383,19 @@ def test_attention_told_of_the_longest_sequence(D, bits, group, new, grp):
     wide.cached = 0.0
     wide.check()
     wide.check(wide.run(longest=1 << 20))
+
+
+@pytest.mark.parametrize("D,bits,bits_v,group", [(128, 4, 4, 128), (64, 3, 8, 32), (96, 8, 2, 96), (128, 2, 3, 64), (32, 4, 4, 32)])
+@pytest.mark.parametrize("new,grp", [(3, 3), (4, 4), (11, 4), (22, 2), (44, 1)])
+def test_attention_of_9_to_44_rows_keeps_cached_values_exact(D, bits, bits_v, group, new, grp):
+    """In a table of much room, bounds without a rounding of what is cached: chunks and trees, scales over powers of two."""
+    for tree in (None, random_trees):
+        s = Setup(f"exact{D}{bits}{new}", [150, 33], [new, new], heads=3, grp=grp, D=D, bits=bits, bits_v=bits_v, group=group, tree=tree,
+                  room=1 << 20, had_k=8)
+        assert s.cached
+        s.cached = 0.0
+        s.check()
+        s.pk[1][...] *= (2.0 ** s.g.integers(-6, 1, s.pk[1].shape)).astype(np.float32)
+        s.pv[1][...] *= (2.0 ** s.g.integers(-3, 3, s.pv[1].shape)).astype(np.float32)
+        to_caches(s)
+        s.check()
