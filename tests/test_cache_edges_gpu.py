@@ -399,3 +399,48 @@ def test_attention_of_9_to_44_rows_keeps_cached_values_exact(D, bits, bits_v, gr
         s.pv[1][...] *= (2.0 ** s.g.integers(-3, 3, s.pv[1].shape)).astype(np.float32)
         to_caches(s)
         s.check()
+
+
+# ---------------------------------------------------------------- long moves
+
+
+@pytest.mark.parametrize("heads,D,bits,group,page_size,past,kept", [(2, 128, 4, 128, 64, [20000], [9000]), (1, 24, 3, 8, 7, [3000, 700, 129, 128], [2999, 129, 128, 128]),
+                                                                  (8, 64, 8, 32, 16, [4096, 1, 4095, 0], [257, 1, 4095, 0])])
+def test_compact_of_a_long_context(heads, D, bits, group, page_size, past, kept):
+    """Thousands of kept tokens, in pages that are not in order; sequences that keep all, one or none; a row that breaks off
+    behind the first 128 and one behind the second."""
+    W, g = _W(), rng_for(360, str(heads), str(D))
+    first = np.array([11 if n > 2000 else 0 for n in past], np.int64)
+    table, n_pages = R.shuffled_table(g, [n + int(f) for n, f in zip(past, first)], page_size)
+    pools = [R.random_pool(g, n_pages, page_size, heads, D, b, group) for b in (bits, 4)]
+    caches = tuple(W.QCache(b, group, 0, *(to_dev(t) for t in p)) for b, p in zip((bits, 4), pools))
+    keep = np.full((len(past), max(kept) + 1), -1, np.int32)
+    for b, (n, m) in enumerate(zip(past, kept)):
+        keep[b, :m] = np.sort(g.choice(n, m, replace=False))
+
+    def move(keep):
+        for p in pools:
+            for t in p:
+                flat = t.reshape(-1, *t.shape[2:])
+                old = flat.copy()
+                for b, row in enumerate(keep):
+                    stop = np.flatnonzero(np.diff(row, prepend=-1) <= 0)
+                    u = row[:stop[0] if len(stop) else len(row)].astype(np.int64)
+                    at = [first[b] + u, first[b] + np.arange(len(u))]
+                    src, dst = (table[b, x // page_size] * np.int64(page_size) + x % page_size for x in at)
+                    flat[dst] = old[src]
+
+    W.cache_compact(caches, to_dev(table), to_dev(first), to_dev(keep))
+    W.check_stream_status()
+    move(keep)
+    broken = keep.copy()
+    for b, at in enumerate((128, 129, 127, 256)[:len(past)]):
+        if kept[b] > at:
+            broken[b, at] = broken[b, at - 1]
+    W.cache_compact(caches, to_dev(table), to_dev(first), to_dev(broken))
+    with pytest.raises(W.QwhaError, match="ascend"):
+        W.check_stream_status()
+    move(broken)
+    for p, c in zip(pools, caches):
+        for want, got in zip(p, (c.codes, c.scales, c.zeros)):
+            assert np.array_equal(_ints(got), want)
