@@ -373,8 +373,10 @@ TableWs carve(void *ws, int64_t n_seqs, int64_t n_pages, int64_t m) {
 
 template <typename... K, typename... A>
 cudaError_t launch_table(void (*kernel)(K...), int64_t pages, int64_t rows, cudaStream_t s, A... args) {
-  // one CTA for a small table: a cluster's barriers cost more than they save there
-  const int ctas = pages <= 16384 && rows <= 1024 ? 1 : kMaxCtas;
+  // One CTA for a small table: a cluster's barriers cost more than they save there (a call that grows or cuts all rows, us
+  // with one CTA and with eight: 64 rows, 2048 pages 7.4 and 9.8; 64, 16384 9.0 and 10.3; 64, 65536 12.8 and 10.8; 256, 16384 11.7
+  // and 11.5; 1024, 16384 21.6 and 11.8).
+  const int ctas = pages <= 16384 && rows <= 256 ? 1 : kMaxCtas;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(ctas), c.blockDim = dim3(kTableThreads), c.stream = s;
   cudaLaunchAttribute a[1];
