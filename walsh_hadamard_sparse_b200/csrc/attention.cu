@@ -432,10 +432,11 @@ __device__ __forceinline__ float live_scale(const qwha_cache &c, int64_t row, in
   }
   return idle ? 0.f : x;
 }
-// Which heads of a tile are (bits of the result). spread: any two tokens' scales are compared. Else: a row has at least the largest scale of the tokens that
-// all rows see, of which the newest 32 are looked at (all, where these have none), or, where
-// there are none, maybe the least of the others alone. The keys' groups count together: a
-// score is their sum. Idle groups do not count.
+// Which heads of a tile are (bits of the result). spread: any two tokens' scales are
+// compared. Else: a row has at least the largest scale of the tokens that all rows see, of
+// which the newest 32 are looked at (all, where these have none), or, where there are
+// none, maybe the least of the others alone. The keys' groups count together: a score is
+// their sum. Idle groups do not count.
 struct Scales {
   uint32_t top, all, some;  // the largest of tokens that not all rows see; of those that all see; the least of the first
 };
@@ -447,16 +448,43 @@ __device__ __forceinline__ unsigned needs_repair(const AttnArgs &a, const Seq &s
   if (!spread && (s.rows - tile * a.tq == 1 || a.tq == 1 || length <= safe)) return 0;  // (one token: its rows see the same)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
   const int per_head = (threads >> 5) / a.hb, hl = warp % a.hb, sub = warp / a.hb, kv = head_block * a.hb + hl;
-  __syncthreads();
+  const float room = spread ? kSpreadTc : TC ? kRoomTc : kRoomMma;
+  const int near = max(safe - 32, 0);
+  const bool here = sub < per_head && kv < a.k.heads;
+  const int32_t *table = a.pages + (int64_t)b * a.max_pages;
+  auto row_of = [&](int t) -> int64_t {  // of the token's scales; -1: none
+    const int pg = page_of(a, t), page = __ldg(table + pg);
+    return (uint32_t)page < (uint32_t)a.v.n_pages ? (((int64_t)page * a.v.page_size + t - pg * a.v.page_size) * a.v.heads + kv) : -1;
+  };
+  // First without the codes: hardly any tile has scales so far apart, idle groups and all, as long as the newest token that
+  // all rows see is not idle, whose scale the rows have. (With the codes of all, 5 us more for chunks.)
+  if (!spread) {
+    bool maybe = false;
+    for (int g = sub; here && g < ng + TC; g += per_head) {  // the last: the keys
+      float top = 0.f, least = INFINITY;
+#pragma unroll 4
+      for (int t = near + lane; t < length; t += 32) {
+        const int64_t row = row_of(t);
+        float lo = INFINITY, hi = 0.f;
+        auto take = [&](float x) {
+          x = fabsf(x);
+          if (x > 0.f && x < INFINITY) lo = fminf(lo, x), hi = fmaxf(hi, x);
+        };
+        if (row >= 0 && g < ng) take(__ldg(a.v.scales + row * ng + g));
+        if (row >= 0 && g == ng)
+          for (int i = 0; i < ng_k; ++i) take(__ldg(a.k.scales + row * ng_k + i));
+        if (t == safe - 1) maybe |= row < 0 || live_scale(g < ng ? a.v : a.k, row, g < ng ? g : 0, g < ng ? ng : ng_k) == 0.f;
+        least = fminf(least, lo);
+        if (t >= safe) top = fmaxf(top, hi);
+      }
+      maybe |= __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top))) > room * __uint_as_float(__reduce_min_sync(~0u, __float_as_uint(least)));
+    }
+    if (!__syncthreads_or(maybe)) return 0;
+  }
   for (int i = threadIdx.x; i < a.hb * 33; i += threads) of[i / 33][i % 33] = {0u, 0u, 0x7f800000u};
   __syncthreads();
   auto look = [&](int lo, int hi) {  // the scales of tokens [lo, hi)
-    if (sub >= per_head || kv >= a.k.heads) return;
-    const int32_t *table = a.pages + (int64_t)b * a.max_pages;
-    auto row_of = [&](int t) -> int64_t {  // of the token's scales; -1: none
-      const int pg = page_of(a, t), page = __ldg(table + pg);
-      return (uint32_t)page < (uint32_t)a.v.n_pages ? (((int64_t)page * a.v.page_size + t - pg * a.v.page_size) * a.v.heads + kv) : -1;
-    };
+    if (!here) return;
     const int step = 32 * per_head;
     for (int t0 = lo + 32 * sub; t0 < hi; t0 += step) {
       const int t = t0 + lane;
@@ -483,7 +511,6 @@ __device__ __forceinline__ unsigned needs_repair(const AttnArgs &a, const Seq &s
     for (int i = threadIdx.x; i < a.hb * 33; i += threads) any |= is(of[i / 33][i % 33]);
     return __syncthreads_or(any);
   };
-  const int near = max(safe - 32, 0);
   look(near, length);
   __syncthreads();
   if (near > 0 && !spread && any_of([](const Scales &x) { return x.top && !x.all; })) {
@@ -495,7 +522,6 @@ __device__ __forceinline__ unsigned needs_repair(const AttnArgs &a, const Seq &s
   __syncthreads();
   for (int i = threadIdx.x; i < a.hb * 33; i += threads) {
     const Scales x = of[i / 33][i % 33];
-    const float room = spread ? kSpreadTc : TC ? kRoomTc : kRoomMma;
     if (__uint_as_float(x.top) > room * __uint_as_float(x.all ? x.all : x.some)) atomicOr(&far_s, 1u << (i / 33));
   }
   __syncthreads();
