@@ -350,7 +350,7 @@ qwha_status qwha_rotary(qwha_dtype dt, int32_t n_x, const void *const *x, const 
  * max_pages * page_size is at most 2^14 times these rows; head_dim and groups whole
  * 32s, head_dim up to 128. (The average decides for all sequences of a call: a chunk
  * among many single tokens is better in a call of its own.)
- * Some rows are done again in fp32, 20 to 90 times as slowly: those whose tokens'
+ * Some rows are done again in fp32, 20 to 100 times as slowly: those whose tokens'
  * scales are far below those of tokens that only other rows see (2^8 times, in
  * bf16 calls of many rows 2^16), and in the latter calls those that see scales
  * 2^13 apart (of a head's keys, or of a group of its values). Groups whose codes

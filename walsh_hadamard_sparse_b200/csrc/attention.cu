@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const _
 // steps of 2^-33 of the largest, so that a token costs 2^-25 of a row's own; 2^16 in
 // attention_tc.cu, where 2^-16 of the largest is still a normal number, and for the
 // keys too, whose scales are in f16 there. Caches of values of ordinary spread have none
-// of these; a third launch looks for them while the second runs, which costs 1.3 us.
+// of these; a third launch looks for them while the second runs, which costs 2 us for 2
+// trees behind 1024 and 5 for 16 of 64 or 4 chunks.
 // (The same in the kernels themselves took registers and instruction cache from them:
 // 325 to 375 us for 304 where four chunks of 1021 tokens are answered behind 2048.)
 constexpr float kRoomMma = 256.f, kRoomTc = 65536.f;
@@ -288,11 +289,11 @@ constexpr float kRoomMma = 256.f, kRoomTc = 65536.f;
 // tile are looked at.
 // Rows of a tile again, in fp32, right whatever the scales are: of one cached head, up to
 // four rows a warp and 32 cached tokens at a time, which go to shared memory as values.
-// Where every tile is one of those (a later token in eight with values 2^20 times the
-// others'): 4 chunks of 1021 behind 2048 take 7.4 ms for 0.36, 16 trees of 64 behind 4096
-// 8.4 for 0.16, one behind 32768 8.3 for 0.1, 64 trees of 4 3.4 for 0.17; bound by the
-// latency of a step's loads, sums and barriers. (A warp a row and a token at a time: 88,
-// 208 and 101 ms.) 80 registers, so that a CTA starts beside the joining ones: with
+// With a later token in eight of values 2^20 times the others', which makes nearly every
+// tile one of those, 4 chunks of 1021 behind 2048 take 22.5 ms for 0.36, 16 trees of 64
+// behind 4096 8.4 for 0.16, one behind 32768 8.5 for 0.1, 64 trees of 4 3.4 for 0.17; bound by
+// the latency of a step's loads, sums and barriers. (A warp a row and a token at a time,
+// and a third of the chunks' tiles: 88, 208 and, for the last, 101 ms.) 80 registers, so that a CTA starts beside the joining ones: with
 // 128 the ordinary call of 2 trees waited 2 us longer.
 constexpr int kRepairThreads = 256, kRepairWarps = kRepairThreads / 32, kRepairRows = 4, kRepairTokens = 32;
 __host__ __device__ __forceinline__ size_t repair_smem(int D) {
@@ -542,7 +543,8 @@ __global__ void __launch_bounds__(kRepairThreads, C <= 4 ? 3 : 2) attention_repa
       if ((int)blockIdx.y >= step * share) continue;
       for (long long i = blockIdx.y / share; i < tiles; i += step) {
         const int block = (int)(i / s.tiles), tile = (int)(i - (long long)block * s.tiles);
-        const unsigned heads = needs_repair<TC>(a, s, b, block, tile, spread, of);
+        unsigned heads = needs_repair<TC>(a, s, b, block, tile, spread, of);
+        if (heads && spread) heads &= ~needs_repair<TC>(a, s, b, block, tile, false, of);  // (done the first time)
         if (!heads) continue;
         asm volatile("griddepcontrol.wait;" ::: "memory");
         // pieces of `each` rows a warp, in turn to the CTAs that share the tile
