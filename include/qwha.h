@@ -351,10 +351,10 @@ qwha_status qwha_rotary(qwha_dtype dt, int32_t n_x, const void *const *x, const 
  * 32s, head_dim up to 128. (The average decides for all sequences of a call: a chunk
  * among many single tokens is better in a call of its own.)
  * Some rows are done again in fp32, 20 to 100 times as slowly: those whose tokens'
- * scales are far below those of tokens that only other rows see (2^8 times, in
- * bf16 calls of many rows 2^16), and in the latter calls those that see scales
- * 2^13 apart (of a head's keys, or of a group of its values). Groups whose codes
- * all equal their zero point (rows of zeros) do not count for that.
+ * scales lie 2^8 times below those of tokens that only other rows see, and in bf16
+ * calls of many rows those with scales 2^13 apart, of a head's keys or of a group
+ * of its values. Groups whose codes all equal their zero point (rows of zeros) do
+ * not count for that.
  * out must not overlap q. Deterministic.
  * ws: qwha_workspace_size(QWHA_OP_ATTENTION, q_heads, head_dim, heads, n, 1 for
  * bf16 or 2 for fp32) bytes. */

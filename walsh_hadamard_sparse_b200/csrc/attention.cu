@@ -272,21 +272,21 @@ __global__ void __launch_bounds__(kJoinThreads, 4) attention_join_kernel(const _
 
 // ---------------------------------------------------------------- repairing
 
-// The tensor-core kernels keep scales in f16 relative to the largest that any row of
-// the tile sees. A row that does not see that token has the less room for its own.
-// Tiles where tokens that not all rows see have scales so far above the others' that
-// bits would be lost are done again in fp32: 2^8 in attention_mma.cuh, where p scale has
-// steps of 2^-33 of the largest, so that a token costs 2^-25 of a row's own; 2^16 in
-// attention_tc.cu, where 2^-16 of the largest is still a normal number, and for the
-// keys too, whose scales are in f16 there. Caches of values of ordinary spread have none
-// of these; a third launch looks for them while the second runs, which costs 2 us for 2
-// trees behind 1024 and 5 for 16 of 64 or 4 chunks.
+// The tensor-core kernels keep scales in f16, relative to the largest met.
+// attention_mma.cuh has p scale, of which 2^-33 of the largest is a step. A row that does
+// not see the token of the largest scale has the less room for its own: tiles where
+// tokens that not all rows see have scales 2^8 times the others' are done again in fp32,
+// so that a token costs 2^-25 of a row's own at most.
+// attention_tc.cu has the scales of keys and values themselves, which lose bits from 2^-13
+// of the largest on, whoever sees it. It tells where it met such; tiles with scales that far
+// apart are done again.
+// Caches of values of ordinary spread have none of these. A third launch looks while the
+// second runs (on mma.sync, which cannot tell: 2 us for 2 trees of 2 behind 1024, 4 for 64
+// behind 4096).
 // (The same in the kernels themselves took registers and instruction cache from them:
 // 325 to 375 us for 304 where four chunks of 1021 tokens are answered behind 2048.)
-constexpr float kRoomMma = 256.f, kRoomTc = 65536.f;
-// On tcgen05 scales in f16 also lose to those of tokens that all rows see, from 2^-13 of
-// the largest on (attention.cuh): where the kernel before has met such, all scales of a
-// tile are looked at.
+constexpr float kRoomMma = 256.f;
+
 // Rows of a tile again, in fp32, right whatever the scales are: of one cached head, up to
 // four rows a warp and 32 cached tokens at a time, which go to shared memory as values.
 // With a later token in eight of values 2^20 times the others', which makes nearly every
@@ -433,100 +433,106 @@ __device__ __forceinline__ float live_scale(const qwha_cache &c, int64_t row, in
   }
   return idle ? 0.f : x;
 }
-// Which heads of a tile are (bits of the result). spread: any two tokens' scales are
-// compared. Else: a row has at least the largest scale of the tokens that all rows see, of
-// which the newest 32 are looked at (all, where these have none), or, where there are
-// none, maybe the least of the others alone. The keys' groups count together: a score is
-// their sum. Idle groups do not count.
-struct Scales {
-  uint32_t top, all, some;  // the largest of tokens that not all rows see; of those that all see; the least of the first
-};
-template <bool TC>
-__device__ __forceinline__ unsigned needs_repair(const AttnArgs &a, const Seq &s, int b, int block, int tile, bool spread,
-                                                 Scales (*of)[33]) {
-  const int ng = a.v.head_dim / a.v.group, ng_k = a.k.head_dim / a.k.group, head_block = block_of(a, block), length = s.length(a, tile);
-  const int safe = spread ? 0 : a.tree ? s.past : s.past + tile * a.tq + 1;  // every row sees the tokens below
-  if (!spread && (s.rows - tile * a.tq == 1 || a.tq == 1 || length <= safe)) return 0;  // (one token: its rows see the same)
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
-  const int per_head = (threads >> 5) / a.hb, hl = warp % a.hb, sub = warp / a.hb, kv = head_block * a.hb + hl;
-  const float room = spread ? kSpreadTc : TC ? kRoomTc : kRoomMma;
-  const int near = max(safe - 32, 0);
-  const bool here = sub < per_head && kv < a.k.heads;
-  const int32_t *table = a.pages + (int64_t)b * a.max_pages;
-  auto row_of = [&](int t) -> int64_t {  // of the token's scales; -1: none
-    const int pg = page_of(a, t), page = __ldg(table + pg);
+// Looking at the scales of a tile's tokens: a warp has a cached head of the block, or, where
+// there are fewer heads, a share of it.
+struct Look {
+  const AttnArgs &a;
+  const int b, kv, hl, sub, per_head, lane;
+  __device__ __forceinline__ Look(const AttnArgs &a_, int b_, int head_block)
+      : a(a_), b(b_), kv(head_block * a_.hb + (int)(threadIdx.x >> 5) % a_.hb), hl((int)(threadIdx.x >> 5) % a_.hb),
+        sub((int)(threadIdx.x >> 5) / a_.hb), per_head(kRepairWarps / a_.hb), lane(threadIdx.x & 31) {}
+  __device__ __forceinline__ bool here() const { return sub < per_head && kv < a.k.heads; }
+  __device__ __forceinline__ int64_t row(int t) const {  // of the token's scales; -1: none
+    const int pg = page_of(a, t), page = __ldg(a.pages + (int64_t)b * a.max_pages + pg);
     return (uint32_t)page < (uint32_t)a.v.n_pages ? (((int64_t)page * a.v.page_size + t - pg * a.v.page_size) * a.v.heads + kv) : -1;
-  };
-  // First without the codes: hardly any tile has scales so far apart, idle groups and all, as long as the newest token that
-  // all rows see is not idle, whose scale the rows have. (With the codes of all, 5 us more for chunks.)
-  if (!spread) {
-    bool maybe = false;
-    for (int g = sub; here && g < ng + TC; g += per_head) {  // the last: the keys
-      float top = 0.f, least = INFINITY;
-#pragma unroll 4
-      for (int t = near + lane; t < length; t += 32) {
-        const int64_t row = row_of(t);
-        float lo = INFINITY, hi = 0.f;
-        auto take = [&](float x) {
-          x = fabsf(x);
-          if (x > 0.f && x < INFINITY) lo = fminf(lo, x), hi = fmaxf(hi, x);
-        };
-        if (row >= 0 && g < ng) take(__ldg(a.v.scales + row * ng + g));
-        if (row >= 0 && g == ng)
-          for (int i = 0; i < ng_k; ++i) take(__ldg(a.k.scales + row * ng_k + i));
-        if (t == safe - 1) maybe |= row < 0 || live_scale(g < ng ? a.v : a.k, row, g < ng ? g : 0, g < ng ? ng : ng_k) == 0.f;
-        least = fminf(least, lo);
-        if (t >= safe) top = fmaxf(top, hi);
-      }
-      maybe |= __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top))) > room * __uint_as_float(__reduce_min_sync(~0u, __float_as_uint(least)));
-    }
-    if (!__syncthreads_or(maybe)) return 0;
   }
-  for (int i = threadIdx.x; i < a.hb * 33; i += threads) of[i / 33][i % 33] = {0u, 0u, 0x7f800000u};
+};
+// What is known of a group: bits of fp32, which order like the numbers.
+struct Scales {
+  uint32_t top, all, some;
+};
+constexpr uint32_t kInf = 0x7f800000u;
+__device__ __forceinline__ float as_float(uint32_t x) { return __uint_as_float(x); }
+// Which heads of the block (bits) `is` finds in the table.
+template <typename F>
+__device__ __forceinline__ unsigned heads_where(const AttnArgs &a, Scales (*of)[33], F is) {
+  __shared__ unsigned heads_s;
+  if (threadIdx.x == 0) heads_s = 0;
   __syncthreads();
-  auto look = [&](int lo, int hi) {  // the scales of tokens [lo, hi)
-    if (!here) return;
-    const int step = 32 * per_head;
-    for (int t0 = lo + 32 * sub; t0 < hi; t0 += step) {
-      const int t = t0 + lane;
-      const int64_t row = t < hi ? row_of(t) : -1;
-      auto put = [&](Scales &x, float scale) {
-        const uint32_t bits = __float_as_uint(scale), top = __reduce_max_sync(~0u, t < safe ? 0u : bits);
-        const uint32_t all = __reduce_max_sync(~0u, t < safe ? bits : 0u);
-        const uint32_t some = __reduce_min_sync(~0u, t < safe || !bits ? 0x7f800000u : bits);
-        if (lane == 0) atomicMax(&x.top, top), atomicMax(&x.all, all), atomicMin(&x.some, some);
-      };
-      float keys = 0.f, first = 0.f;  // (asked for together)
-      if (row >= 0) {
-        first = live_scale(a.v, row, 0, ng);
-        if (TC)
-          for (int i = 0; i < ng_k; ++i) keys = fmaxf(keys, live_scale(a.k, row, i, ng_k));
+  for (int i = threadIdx.x; i < a.hb * 33; i += kRepairThreads)
+    if (is(of[i / 33][i % 33])) atomicOr(&heads_s, 1u << (i / 33));
+  __syncthreads();
+  return heads_s;
+}
+__device__ __forceinline__ void clear(const AttnArgs &a, Scales (*of)[33]) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.hb * 33; i += kRepairThreads) of[i / 33][i % 33] = {0u, 0u, kInf};
+  __syncthreads();
+}
+
+// mma.sync: which heads have a group where tokens that not all rows see have scales (top)
+// far above the least that a row may have: the largest of the tokens that all rows see
+// (all), of which the newest 32 are looked at (every one, where these have none), or, where
+// there are none, the least of the others (some). Idle groups do not count.
+__device__ __forceinline__ unsigned far_for_some(const AttnArgs &a, const Seq &s, int b, int block, int tile, Scales (*of)[33]) {
+  const int ng = a.v.head_dim / a.v.group, length = s.length(a, tile);
+  const int safe = a.tree ? s.past : s.past + tile * a.tq + 1, near = max(safe - 32, 0);  // every row sees the tokens below safe
+  if (s.rows - tile * a.tq == 1 || a.tq == 1 || length <= safe) return 0;  // (one token: its rows see the same)
+  const Look l(a, b, block_of(a, block));
+  // First without the codes: hardly any tile has scales so far apart, idle groups and all, as long as the newest token that
+  // all rows see is not idle, whose scale the rows have.
+  bool maybe = false;
+  for (int g = l.sub; l.here() && g < ng; g += l.per_head) {
+    float top = 0.f, least = INFINITY;
+#pragma unroll 4
+    for (int t = near + l.lane; t < length; t += 32) {
+      const int64_t row = l.row(t);
+      const float x = row >= 0 ? fabsf(__ldg(a.v.scales + row * ng + g)) : 0.f;
+      if (t == safe - 1) maybe |= row < 0 || live_scale(a.v, row, g, ng) == 0.f;
+      if (x > 0.f && x < INFINITY) {
+        least = fminf(least, x);
+        if (t >= safe) top = fmaxf(top, x);
       }
-      put(of[hl][0], first);
-      if (TC) put(of[hl][32], keys);
-      for (int g = 1; g < ng; ++g) put(of[hl][g], row >= 0 ? live_scale(a.v, row, g, ng) : 0.f);
     }
-  };
-  auto any_of = [&](auto is) {
-    bool any = false;
-    for (int i = threadIdx.x; i < a.hb * 33; i += threads) any |= is(of[i / 33][i % 33]);
-    return __syncthreads_or(any);
+    maybe |= as_float(__reduce_max_sync(~0u, __float_as_uint(top))) > kRoomMma * as_float(__reduce_min_sync(~0u, __float_as_uint(least)));
+  }
+  if (!__syncthreads_or(maybe)) return 0;
+  clear(a, of);
+  auto look = [&](int lo, int hi) {  // the scales of tokens [lo, hi)
+    for (int t0 = lo + 32 * l.sub; l.here() && t0 < hi; t0 += 32 * l.per_head) {
+      const int t = t0 + l.lane;
+      const int64_t row = t < hi ? l.row(t) : -1;
+      for (int g = 0; g < ng; ++g) {
+        const uint32_t x = row >= 0 ? __float_as_uint(live_scale(a.v, row, g, ng)) : 0u;
+        const uint32_t top = __reduce_max_sync(~0u, t < safe ? 0u : x), all = __reduce_max_sync(~0u, t < safe ? x : 0u);
+        const uint32_t some = __reduce_min_sync(~0u, t < safe || !x ? kInf : x);
+        Scales &y = of[l.hl][g];
+        if (l.lane == 0) atomicMax(&y.top, top), atomicMax(&y.all, all), atomicMin(&y.some, some);
+      }
+    }
+    __syncthreads();
   };
   look(near, length);
-  __syncthreads();
-  if (near > 0 && !spread && any_of([](const Scales &x) { return x.top && !x.all; })) {
-    look(0, near);
-    __syncthreads();
+  if (near > 0 && heads_where(a, of, [](const Scales &x) { return x.top && !x.all; })) look(0, near);
+  return heads_where(a, of, [](const Scales &x) { return as_float(x.top) > kRoomMma * as_float(x.all ? x.all : x.some); });
+}
+// tcgen05: which heads have scales far apart, of the values of a group (top, some) or of the keys (in the last place). Idle
+// groups do not count.
+__device__ __forceinline__ unsigned far_apart(const AttnArgs &a, const Seq &s, int b, int block, int tile, Scales (*of)[33]) {
+  const int ng = a.v.head_dim / a.v.group, ng_k = a.k.head_dim / a.k.group, length = s.length(a, tile);
+  const Look l(a, b, block_of(a, block));
+  clear(a, of);
+  for (int t0 = 32 * l.sub; l.here() && t0 < length; t0 += 32 * l.per_head) {
+    const int64_t row = t0 + l.lane < length ? l.row(t0 + l.lane) : -1;
+    auto put = [&](int at, float scale) {
+      const uint32_t x = __float_as_uint(scale), top = __reduce_max_sync(~0u, x), some = __reduce_min_sync(~0u, x ? x : kInf);
+      if (l.lane == 0) atomicMax(&of[l.hl][at].top, top), atomicMin(&of[l.hl][at].some, some);
+    };
+    for (int g = 0; g < ng; ++g) put(g, row >= 0 ? live_scale(a.v, row, g, ng) : 0.f);
+    for (int g = 0; g < ng_k; ++g) put(32, row >= 0 ? live_scale(a.k, row, g, ng_k) : 0.f);
   }
-  __shared__ unsigned far_s;
-  if (threadIdx.x == 0) far_s = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < a.hb * 33; i += threads) {
-    const Scales x = of[i / 33][i % 33];
-    if (__uint_as_float(x.top) > room * __uint_as_float(x.all ? x.all : x.some)) atomicOr(&far_s, 1u << (i / 33));
-  }
-  __syncthreads();
-  return far_s;
+  return heads_where(a, of, [](const Scales &x) { return as_float(x.top) > kSpreadTc * as_float(x.some); });
 }
 // CTA (x, y): of sequences x, x + gridDim.x, ... the tiles y, y + gridDim.y, ..., or, where there are fewer tiles than
 // that, a share of a tile's rows.
@@ -535,38 +541,33 @@ __global__ void __launch_bounds__(kRepairThreads, C <= 4 ? 3 : 2) attention_repa
   extern __shared__ __align__(16) float repair_s[];
   __shared__ Scales of[kMmaWarps][33];
   __shared__ int64_t slot_s[kRepairTokens];
-  auto look = [&](bool spread) {
-    for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
-      const Seq s(a, b);
-      const long long tiles = (long long)s.tiles * a.blocks;
-      const int share = tiles < gridDim.y && tiles ? (int)(gridDim.y / tiles) : 1, step = (int)(gridDim.y / share);
-      if ((int)blockIdx.y >= step * share) continue;
-      for (long long i = blockIdx.y / share; i < tiles; i += step) {
-        const int block = (int)(i / s.tiles), tile = (int)(i - (long long)block * s.tiles);
-        unsigned heads = needs_repair<TC>(a, s, b, block, tile, spread, of);
-        if (heads && spread) heads &= ~needs_repair<TC>(a, s, b, block, tile, false, of);  // (done the first time)
-        if (!heads) continue;
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        // pieces of `each` rows a warp, in turn to the CTAs that share the tile
-        const int rows = min(a.tq, s.rows - tile * a.tq) * a.gh;  // (the last part of a group may have fewer)
-        const int each = min(max((rows * __popc(heads) + share * kRepairWarps - 1) / (share * kRepairWarps), 1), kRepairRows);
-        int turn = blockIdx.y % share;
-        for (int hl = 0; hl < a.hb; ++hl)
-          if (heads >> hl & 1)
-            for (int first = 0; first < rows; first += each * kRepairWarps, turn = turn ? turn - 1 : share - 1)
-              if (turn == 0) repair<C>(a, s, b, block, tile, hl, first, each, repair_s, slot_s);
-      }
-    }
-  };
-  // one copy of its code; the second time where some CTA of the kernel before says so
-  for (bool spread = false;; spread = true) {
-    look(spread);
+  if (TC) {  // only where some CTA of the kernel before says so
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!TC || spread) break;
     bool coarse = false;
     for (int i = threadIdx.x; i < a.ctas; i += kRepairThreads) coarse |= a.part_desc[2 * i].w & kPieceCoarse;
-    if (!__syncthreads_or(coarse)) break;
+    if (!__syncthreads_or(coarse)) return;
   }
+  for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
+    const Seq s(a, b);
+    const long long tiles = (long long)s.tiles * a.blocks;
+    const int share = tiles < gridDim.y && tiles ? (int)(gridDim.y / tiles) : 1, step = (int)(gridDim.y / share);
+    if ((int)blockIdx.y >= step * share) continue;
+    for (long long i = blockIdx.y / share; i < tiles; i += step) {
+      const int block = (int)(i / s.tiles), tile = (int)(i - (long long)block * s.tiles);
+      const unsigned heads = TC ? far_apart(a, s, b, block, tile, of) : far_for_some(a, s, b, block, tile, of);
+      if (!heads) continue;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      // pieces of `each` rows a warp, in turn to the CTAs that share the tile
+      const int rows = min(a.tq, s.rows - tile * a.tq) * a.gh;  // (the last part of a group may have fewer)
+      const int each = min(max((rows * __popc(heads) + share * kRepairWarps - 1) / (share * kRepairWarps), 1), kRepairRows);
+      int turn = blockIdx.y % share;
+      for (int hl = 0; hl < a.hb; ++hl)
+        if (heads >> hl & 1)
+          for (int first = 0; first < rows; first += each * kRepairWarps, turn = turn ? turn - 1 : share - 1)
+            if (turn == 0) repair<C>(a, s, b, block, tile, hl, first, each, repair_s, slot_s);
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 size_t any_smem(int D) {
