@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kAnyThreads) attention_any_kernel(const AttnAr
 // The tile that CTA blockIdx.x of the kernel before began and left: its piece and
 // those of the CTAs that went on with it, in order. L lanes have a row, eight
 // channels each; they look at L pieces' maxima and sums at once and read the values
-// of four pieces ahead. Bound by the latency of those loads: 15 us of the 350 that 4
+// of four pieces ahead. Bound by the latency of those loads: 15 us of the 343 that 4
 // chunks of 1021 tokens behind 2048 take.
 constexpr int kJoinThreads = 256, kJoinRows = 32, kJoinAhead = 4;
 template <int L>

@@ -26,9 +26,9 @@
 //
 // Bound: instructions, not memory: 2.4 of 4 a clock, the ALU pipe, which unpacks,
 // 47% busy, warps waiting for fixed latencies. 64 contexts of 4096 tokens, 8 heads of
-// 128, 4 bits, one token each of 32 query heads take 97 us, 2.2 TB/s of the 6.5 that
+// 128, 4 bits, one token each of 32 query heads take 98 us, 2.2 TB/s of the 6.5 that
 // a copy moves; 8 contexts of 32768, keys of 4 and values of 2 bits, 120 us; one
-// context of 700, 19 us, of which both launches' latencies are most.
+// context of 700, 18 us, of which both launches' latencies are most.
 #pragma once
 
 #include <cuda_fp16.h>

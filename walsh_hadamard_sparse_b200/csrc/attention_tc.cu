@@ -16,19 +16,22 @@
 // channels of a token: 0.0023 against 0.0019 of error for a tree of 64, 0.0017 of it
 // the output's own rounding.) Scales left to the columns of S and P in fp32 were two
 // multiplications and 16 loads more for 16 scores: 384 us for 4 chunks of 1021 tokens
-// behind 2048, where this takes 350. The query (rotated, its largest value near 2^15)
+// behind 2048, where this took 350. The query (rotated, its largest value near 2^15)
 // and P are rounded to 11 bits as in attention_mma.cuh; the maximum is kept to within
 // what f16 leaves room for: half a tile whose weights sum to more than 2^7 has its
 // maximum taken and is done again, others need none.
 //   8 warps  unpack, four the keys and four the values: a lane's 32 codes of a
-//            token, fetched a tile ahead, to swizzled tiles of f16 (two of each).
+//            token, fetched a tile ahead, to swizzled tiles of f16 (two of each). They
+//            notice scales that lie 2^13 below the largest, which would lose bits in
+//            f16: tiles that have such are done again (attention.cu). By the comparison
+//            that finds growing scales; a minimum kept beside it cost 3%.
 //   8 warps  softmax: four for each tile of rows.
 //   1 warp   issues the products: S_w of the next tile's half behind O_w of this
 //            one's.
 // Bound: the 16384 exponentials and about 80 thousand other operations of a tile of 128
 // rows and tokens, and 1024 clocks of products. 4 chunks of 1021 tokens behind 2048 (32
-// and 8 heads of 128, 8 bits): 350 us, 380 TFLOP/s; trees of 64 tokens on 16 contexts of
-// 4096, 4 bits: 150 us. Of a CTA's clocks in the first the softmax warps spend 38% on
+// and 8 heads of 128, 8 bits): 343 us, 388 TFLOP/s; trees of 64 tokens on 16 contexts of
+// 4096, 4 bits: 149 us. Of a CTA's clocks in the first the softmax warps spend 38% on
 // weights, 14% on writing rows out, 11% on queries, 11% waiting for scores. Every wait is
 // bounded; a thread that gives up sets the error word and goes on without waiting.
 
